@@ -43,6 +43,16 @@ SIGNATURES = {
     "gdn_decay_from_logits": (_i, [_fp, _fp, _fp, _fp, _fp, _fp, _l, _i, _vp]),
     "gdn_chunk_fwd_noalloc": (_i, [_vp, _vp, _vp, _fp, _fp, _ip, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i,
                                    _fp, _fp, _fp, _fp, _fp, _fp, _fp, _f, _vp, _i, _vp]),
+    "gdn_chunk_bwd": (_i, [_vp, _vp, _vp, _fp, _fp, _ip, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _fp, _vp, _i,
+                           _fp, _vp, _vp, _vp, _fp, _fp, _fp, _vp, _sz, _vp]),
+    "gdn_chunk_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "gdn_gate_rmsnorm_silu_bwd": (_i, [_vp, _i, _vp, _i, _fp, _fp, _f, _vp, _fp, _fp, _l, _i, _vp, _sz, _vp]),
+    "gdn_gate_groupnorm_silu": (_i, [_vp, _i, _fp, _fp, _fp, _f, _vp, _i, _l, _i, _i, _vp]),
+    "gdn_gate_groupnorm_silu_bwd": (_i, [_vp, _i, _vp, _i, _fp, _fp, _fp, _f, _vp, _fp, _fp, _fp, _l, _i, _i,
+                                         _vp, _sz, _vp]),
+    "gdn_gate_bwd_workspace_size": (_sz, [_l, _i, _i]),
+    "gdn_decay_from_logits_bwd": (_i, [_fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _l, _i, _vp, _sz, _vp]),
+    "gdn_decay_bwd_workspace_size": (_sz, [_l, _i]),
     "gdn_get_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_int)]),
     "gdn_status_string": (ctypes.c_char_p, [_i]),
     "gdn_selftest_bounded_wait": (_i, [ctypes.c_ulonglong, _vp, _vp]),
@@ -356,6 +366,178 @@ def gdn_decay_from_logits(a, A_log, dt_bias=None, b=None, g_out=None, beta_out=N
               _stream(stream, a))
     _check("gdn_decay_from_logits", rc)
     return (g_out, beta_out) if b is not None else g_out
+
+
+def _workspace(workspace, need, ref):
+    """The caller's workspace, or one of `need` bytes from torch (None when none is needed)."""
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
+    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=0.0, use_qk_l2norm=True,
+                  initial_state=None, dfinal_state=None, output_dinitial_state=None, dq=None, dk=None, dv=None,
+                  dg=None, dbeta=None, dinitial_state=None, workspace=None, stream=None):
+    """Gradients of gdn_chunk_fwd (without gate and convolution, one decay per head): q, k, v, g, beta,
+    cu_seqlens, num_seqs, scale, use_qk_l2norm and initial_state as given to it, dout [total_T, H, d_v]
+    (fp32 or bf16) the gradient of out, dfinal_state [num_seqs, H, d_v, d_k] fp32 that of final_state
+    (None: zeros).  Returns (dq, dk, dv, dg, dbeta, dinitial_state): dq, dk, dv in the inputs' dtype,
+    the others fp32; outputs are allocated unless given.  dinitial_state is None unless it is given,
+    requested, or (output_dinitial_state=None) an initial_state is."""
+    total_T, H_k, d_k = q.shape
+    H, d_v = v.shape[1], v.shape[-1]
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        num_seqs = cu_seqlens.numel() - 1
+    elif num_seqs is None:
+        num_seqs = 1
+    dt = _dt(q)
+    if _dt(k) != dt or _dt(v) != dt:
+        raise TypeError("q, k, v must share one dtype")
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if _dt(dq) != dt or _dt(dk) != dt or _dt(dv) != dt:
+        raise TypeError("dq, dk, dv must have the dtype of q, k, v")
+    if g.dim() != 2:
+        raise ValueError("gdn_chunk_bwd takes one decay per head: g [total_T, H]")
+    dg = torch.empty((total_T, H), dtype=torch.float32, device=q.device) if dg is None else dg
+    dbeta = torch.empty((total_T, H), dtype=torch.float32, device=q.device) if dbeta is None else dbeta
+    if dinitial_state is None and (output_dinitial_state or
+                                   (output_dinitial_state is None and initial_state is not None)):
+        dinitial_state = torch.empty((num_seqs, H, d_v, d_k), dtype=torch.float32, device=q.device)
+    for name, t in (("g", g), ("beta", beta), ("initial_state", initial_state), ("dg", dg), ("dbeta", dbeta),
+                    ("dfinal_state", dfinal_state), ("dinitial_state", dinitial_state)):
+        _f32(t, name)
+    states = num_seqs * H * d_v * d_k
+    _sizes(q, k=(k, total_T * H_k * d_k), v=(v, total_T * H * d_v), g=(g, total_T * H), beta=(beta, total_T * H),
+           cu_seqlens=(cu_seqlens, num_seqs + 1), initial_state=(initial_state, states),
+           dout=(dout, total_T * H * d_v), dfinal_state=(dfinal_state, states), dq=(dq, total_T * H_k * d_k),
+           dk=(dk, total_T * H_k * d_k), dv=(dv, total_T * H * d_v), dg=(dg, total_T * H),
+           dbeta=(dbeta, total_T * H), dinitial_state=(dinitial_state, states), workspace=(workspace, 0))
+    L = lib()
+    workspace, ws_bytes = _workspace(workspace, L.gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v), q)
+    rc = _run(q, L.gdn_chunk_bwd,
+              _p(q), _p(k), _p(v), _p(g), _p(beta), _p(cu_seqlens), num_seqs, total_T, H, H_k, d_k, d_v, dt,
+              GDN_DECAY_PER_HEAD, float(scale), int(bool(use_qk_l2norm)), _p(initial_state), _p(dout), _dt(dout),
+              _p(dfinal_state), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta), _p(dinitial_state), _p(workspace),
+              ws_bytes, _stream(stream, q))
+    _check("gdn_chunk_bwd", rc)
+    return dq, dk, dv, dg, dbeta, dinitial_state
+
+
+def gdn_gate_rmsnorm_silu_bwd(dout, y, z, norm_weight=None, eps=1e-6, dy=None, dz=None, dnorm_weight=None,
+                              workspace=None, stream=None):
+    """Gradients of gdn_gate_rmsnorm_silu: dout (fp32 or bf16), y and z as given to it.  Returns (dy in
+    y's dtype, dz fp32, dnorm_weight fp32); dnorm_weight is None unless it or norm_weight is given."""
+    d_v = y.shape[-1]
+    rows = y.numel() // d_v if d_v else 0
+    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
+    dz = torch.empty(y.shape, dtype=torch.float32, device=y.device) if dz is None else dz
+    if dnorm_weight is None and norm_weight is not None:
+        dnorm_weight = torch.empty((d_v,), dtype=torch.float32, device=y.device)
+    if dy.dtype != y.dtype:
+        raise TypeError("dy must have the dtype of y")
+    for name, t in (("z", z), ("norm_weight", norm_weight), ("dz", dz), ("dnorm_weight", dnorm_weight)):
+        _f32(t, name)
+    _sizes(y, dout=(dout, rows * d_v), z=(z, rows * d_v), norm_weight=(norm_weight, d_v), dy=(dy, rows * d_v),
+           dz=(dz, rows * d_v), dnorm_weight=(dnorm_weight, d_v), workspace=(workspace, 0))
+    L = lib()
+    need = L.gdn_gate_bwd_workspace_size(rows, 1, d_v) if dnorm_weight is not None else 0
+    workspace, ws_bytes = _workspace(workspace, need, y)
+    rc = _run(y, L.gdn_gate_rmsnorm_silu_bwd,
+              _p(dout), _dt(dout), _p(y), _dt(y), _p(z), _p(norm_weight), float(eps), _p(dy), _p(dz),
+              _p(dnorm_weight), rows, d_v, _p(workspace), ws_bytes, _stream(stream, y))
+    _check("gdn_gate_rmsnorm_silu_bwd", rc)
+    return dy, dz, dnorm_weight
+
+
+def _groups(y):
+    if y.dim() < 2:
+        raise ValueError("y must be [..., groups, group_size]")
+    groups, size = y.shape[-2:]
+    return (y.numel() // (groups * size) if groups * size else 0), groups, size
+
+
+def gdn_gate_groupnorm_silu(y, z=None, weight=None, bias=None, eps=1e-6, out=None, out_dtype=None, stream=None):
+    """Group norm over the heads, channels last, with a SiLU: y [..., groups, group_size] (fp32 or bf16),
+    m = weight * (y - mean) / sqrt(var + eps) + bias per group, out = m * silu(z), or silu(m) without z.
+    z like y, fp32; weight, bias [groups, group_size] fp32 or None."""
+    rows, groups, size = _groups(y)
+    odt = _dt(y) if out_dtype is None else _dt(torch.empty(0, dtype=out_dtype))
+    if out is None:
+        out = torch.empty(y.shape, dtype=_torch_dt(odt), device=y.device)
+    else:
+        odt = _dt(out)
+    n, c = rows * groups * size, groups * size
+    for name, t in (("z", z), ("weight", weight), ("bias", bias)):
+        _f32(t, name)
+    _sizes(y, z=(z, n), weight=(weight, c), bias=(bias, c), out=(out, n))
+    rc = _run(y, lib().gdn_gate_groupnorm_silu,
+              _p(y), _dt(y), _p(z), _p(weight), _p(bias), float(eps), _p(out), odt, rows, groups, size,
+              _stream(stream, y))
+    _check("gdn_gate_groupnorm_silu", rc)
+    return out
+
+
+def gdn_gate_groupnorm_silu_bwd(dout, y, z=None, weight=None, bias=None, eps=1e-6, dy=None, dz=None, dweight=None,
+                                dbias=None, workspace=None, stream=None):
+    """Gradients of gdn_gate_groupnorm_silu: dout (fp32 or bf16) and the forward's inputs.  Returns (dy in
+    y's dtype, dz fp32 or None without z, dweight, dbias fp32 [groups, group_size]); dweight (dbias) is
+    None unless it or weight (bias) is given."""
+    rows, groups, size = _groups(y)
+    n, c = rows * groups * size, groups * size
+    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
+    if dy.dtype != y.dtype:
+        raise TypeError("dy must have the dtype of y")
+    if z is not None and dz is None:
+        dz = torch.empty(y.shape, dtype=torch.float32, device=y.device)
+    if weight is not None and dweight is None:
+        dweight = torch.empty((groups, size), dtype=torch.float32, device=y.device)
+    if bias is not None and dbias is None:
+        dbias = torch.empty((groups, size), dtype=torch.float32, device=y.device)
+    for name, t in (("z", z), ("weight", weight), ("bias", bias), ("dz", dz), ("dweight", dweight), ("dbias", dbias)):
+        _f32(t, name)
+    _sizes(y, dout=(dout, n), z=(z, n), weight=(weight, c), bias=(bias, c), dy=(dy, n), dz=(dz, n),
+           dweight=(dweight, c), dbias=(dbias, c), workspace=(workspace, 0))
+    L = lib()
+    need = L.gdn_gate_bwd_workspace_size(rows, groups, size) if dweight is not None or dbias is not None else 0
+    workspace, ws_bytes = _workspace(workspace, need, y)
+    rc = _run(y, L.gdn_gate_groupnorm_silu_bwd,
+              _p(dout), _dt(dout), _p(y), _dt(y), _p(z), _p(weight), _p(bias), float(eps), _p(dy), _p(dz),
+              _p(dweight), _p(dbias), rows, groups, size, _p(workspace), ws_bytes, _stream(stream, y))
+    _check("gdn_gate_groupnorm_silu_bwd", rc)
+    return dy, dz, dweight, dbias
+
+
+def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=None, ddt_bias=None, db=None,
+                              workspace=None, stream=None):
+    """Gradients of gdn_decay_from_logits: a, A_log, dt_bias (or None), b (or None) as given to it, dg
+    [total_T, H] and dbeta [total_T, H] (None exactly when b is) those of its outputs, fp32.  Returns
+    (da, dA_log, ddt_bias, db); ddt_bias is None unless it or dt_bias is given, db is None without b."""
+    total_T, H = a.shape
+    if (b is None) != (dbeta is None):
+        raise ValueError("b and dbeta are given together")
+    da = torch.empty_like(a) if da is None else da
+    dA_log = torch.empty((H,), dtype=torch.float32, device=a.device) if dA_log is None else dA_log
+    if dt_bias is not None and ddt_bias is None:
+        ddt_bias = torch.empty((H,), dtype=torch.float32, device=a.device)
+    if b is not None and db is None:
+        db = torch.empty_like(b)
+    for name, t in (("a", a), ("A_log", A_log), ("dt_bias", dt_bias), ("b", b), ("dg", dg), ("dbeta", dbeta),
+                    ("da", da), ("dA_log", dA_log), ("ddt_bias", ddt_bias), ("db", db)):
+        _f32(t, name)
+    n = total_T * H
+    _sizes(a, A_log=(A_log, H), dt_bias=(dt_bias, H), b=(b, n), dg=(dg, n), dbeta=(dbeta, n), da=(da, n),
+           dA_log=(dA_log, H), ddt_bias=(ddt_bias, H), db=(db, n), workspace=(workspace, 0))
+    L = lib()
+    workspace, ws_bytes = _workspace(workspace, L.gdn_decay_bwd_workspace_size(total_T, H), a)
+    rc = _run(a, L.gdn_decay_from_logits_bwd,
+              _p(a), _p(A_log), _p(dt_bias), _p(b), _p(dg), _p(dbeta), _p(da), _p(dA_log), _p(ddt_bias), _p(db),
+              total_T, H, _p(workspace), ws_bytes, _stream(stream, a))
+    _check("gdn_decay_from_logits_bwd", rc)
+    return da, dA_log, ddt_bias, db
 
 
 def gdn_selftest_bounded_wait(limit_ns, status=None, stream=None):

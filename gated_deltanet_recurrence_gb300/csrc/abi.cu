@@ -169,6 +169,53 @@ int gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* g, c
     return launch_status(e);
 }
 
+static bool chunk_bwd_sizes_ok(int num_seqs, int total_T, int H, int H_k, int d_k, int d_v) {
+    return num_seqs > 0 && total_T >= 0 && heads_ok(H, H_k) && head_size_ok(d_k, d_v) &&
+           ((long long)total_T / 64 + num_seqs) * H <= 0x7fffffffLL &&
+           (long long)total_T * H <= 0x7fffffffLL;
+}
+
+size_t gdn_chunk_bwd_workspace_size(int num_seqs, int total_T, int H, int H_k, int d_k, int d_v) {
+    if (!chunk_bwd_sizes_ok(num_seqs, total_T, H, H_k, d_k, d_v)) return 0;
+    return gdn::chunk_bwd_workspace_bytes(num_seqs, total_T, H, H_k, d_k);
+}
+
+int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                  const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k,
+                  int d_k, int d_v, gdn_dtype qkv_dtype, gdn_decay decay, float scale,
+                  int use_qk_l2norm, const float* initial_state,
+                  const void* dout, gdn_dtype dout_dtype, const float* dfinal_state,
+                  void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dinitial_state,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (!valid_dtype(qkv_dtype) || !valid_dtype(dout_dtype)) return GDN_ERR_DTYPE;
+    if (num_seqs <= 0 || total_T < 0 || !heads_ok(H, H_k) || !valid_decay(decay)) return GDN_ERR_ARG;
+    if (!head_size_ok(d_k, d_v) || decay != GDN_DECAY_PER_HEAD) return GDN_ERR_UNSUPPORTED;
+    if (!chunk_bwd_sizes_ok(num_seqs, total_T, H, H_k, d_k, d_v)) return GDN_ERR_ARG;
+    if (!cu_seqlens && total_T % num_seqs != 0) return GDN_ERR_ARG;
+    if (total_T > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta))
+        return GDN_ERR_ARG;
+    const void* ptrs[] = {q, k, v, g, beta, initial_state, dout, dfinal_state, dq, dk, dv, dg, dbeta,
+                          dinitial_state};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return GDN_ERR_ARG;
+    const size_t need = gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return GDN_ERR_WORKSPACE;
+    if (total_T == 0 && !dinitial_state) return GDN_OK;
+    gdn::ChunkBwdArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
+    a.cu_seqlens = cu_seqlens; a.num_seqs = num_seqs; a.total_T = total_T; a.H = H; a.Hk = H_k;
+    a.d = d_k; a.qkv_dtype = qkv_dtype;
+    a.scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)d_k);
+    a.use_l2 = use_qk_l2norm ? 1 : 0;
+    a.initial_state = initial_state; a.dout = dout; a.dout_dtype = dout_dtype;
+    a.dfinal_state = dfinal_state; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta;
+    a.dinitial_state = dinitial_state; a.workspace = workspace;
+    a.err = device_error_ptr();
+    if (!a.err) return GDN_ERR_CUDA;
+    return launch_status(gdn::launch_chunk_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
 static int decode_entry(const void* q, const void* k, const void* v, const float* g,
                         const float* beta, float* state, int num_slots, const int32_t* idx, int N,
                         int T, int H, int H_k, int d_k, int d_v, gdn_dtype qkv_dtype,
@@ -250,6 +297,106 @@ int gdn_decay_from_logits(const float* a_logits, const float* A_log, const float
     a.a = a_logits; a.A_log = A_log; a.dt_bias = dt_bias; a.b = b;
     a.g = g_out; a.beta = beta_out; a.total_T = total_T; a.H = H;
     return launch_status(gdn::launch_gate_prep(a, static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of the norms' training form: a group of at most 1024 channels, at most 2^20 channels a row,
+// and element counts that leave room for the index arithmetic.
+static bool norm_sizes_ok(long rows, int groups, int size) {
+    return rows >= 0 && groups >= 1 && size >= 1 && size <= 1024 && (long long)groups * size <= (1 << 20) &&
+           rows <= (1L << 42) / ((long)groups * size);
+}
+
+size_t gdn_gate_bwd_workspace_size(long rows, int groups, int group_size) {
+    return norm_sizes_ok(rows, groups, group_size) ? gdn::norm_bwd_workspace_bytes(rows, groups, group_size) : 0;
+}
+
+static int norm_bwd_entry(const gdn::NormArgs& in, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn::NormArgs a = in;
+    const void* ptrs[] = {a.dout, a.y, a.z, a.w, a.b, a.dy, a.dz, a.dw, a.db};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return GDN_ERR_ARG;
+    if (a.dw || a.db) {
+        const size_t need = gdn::norm_bwd_workspace_bytes(a.rows, a.groups, a.size);
+        if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
+        a.partial = static_cast<float*>(workspace);
+    }
+    return launch_status(gdn::launch_norm_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_gate_rmsnorm_silu_bwd(const void* dout, gdn_dtype dout_dtype, const void* y, gdn_dtype y_dtype,
+                              const float* z, const float* norm_weight, float eps, void* dy, float* dz,
+                              float* dnorm_weight, long rows, int d_v, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    if (!valid_dtype(dout_dtype) || !valid_dtype(y_dtype)) return GDN_ERR_DTYPE;
+    if (d_v <= 0 || d_v % 32 != 0 || !norm_sizes_ok(rows, 1, d_v) || !(eps >= 0.0f)) return GDN_ERR_ARG;
+    if (rows == 0 && !dnorm_weight) return GDN_OK;
+    if (rows > 0 && (!dout || !y || !z || !dy || !dz)) return GDN_ERR_ARG;
+    gdn::NormArgs a{};
+    a.y = y; a.y_dtype = y_dtype; a.z = z; a.w = norm_weight; a.eps = eps;
+    a.dout = dout; a.dout_dtype = dout_dtype; a.dy = dy; a.dz = dz; a.dw = dnorm_weight;
+    a.rows = rows; a.groups = 1; a.size = d_v; a.rms = 1;
+    return norm_bwd_entry(a, workspace, workspace_bytes, stream);
+}
+
+int gdn_gate_groupnorm_silu(const void* y, gdn_dtype y_dtype, const float* z, const float* weight,
+                            const float* bias, float eps, void* out, gdn_dtype out_dtype, long rows,
+                            int groups, int group_size, void* stream) {
+    if (!valid_dtype(y_dtype) || !valid_dtype(out_dtype)) return GDN_ERR_DTYPE;
+    if (!norm_sizes_ok(rows, groups, group_size) || !(eps >= 0.0f)) return GDN_ERR_ARG;
+    if (rows == 0) return GDN_OK;
+    if (!y || !out) return GDN_ERR_ARG;
+    const void* ptrs[] = {y, z, weight, bias, out};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return GDN_ERR_ARG;
+    gdn::NormArgs a{};
+    a.y = y; a.y_dtype = y_dtype; a.z = z; a.w = weight; a.b = bias; a.eps = eps;
+    a.out = out; a.out_dtype = out_dtype; a.rows = rows; a.groups = groups; a.size = group_size;
+    return launch_status(gdn::launch_groupnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_gate_groupnorm_silu_bwd(const void* dout, gdn_dtype dout_dtype, const void* y, gdn_dtype y_dtype,
+                                const float* z, const float* weight, const float* bias, float eps,
+                                void* dy, float* dz, float* dweight, float* dbias, long rows,
+                                int groups, int group_size, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (!valid_dtype(dout_dtype) || !valid_dtype(y_dtype)) return GDN_ERR_DTYPE;
+    if (!norm_sizes_ok(rows, groups, group_size) || !(eps >= 0.0f)) return GDN_ERR_ARG;
+    if (rows == 0 && !dweight && !dbias) return GDN_OK;
+    if (rows > 0 && (!dout || !y || !dy || !z != !dz)) return GDN_ERR_ARG;
+    gdn::NormArgs a{};
+    a.y = y; a.y_dtype = y_dtype; a.z = z; a.w = weight; a.b = bias; a.eps = eps;
+    a.dout = dout; a.dout_dtype = dout_dtype; a.dy = dy; a.dz = dz; a.dw = dweight; a.db = dbias;
+    a.rows = rows; a.groups = groups; a.size = group_size;
+    return norm_bwd_entry(a, workspace, workspace_bytes, stream);
+}
+
+static bool decay_bwd_sizes_ok(long total_T, int H) {
+    return total_T >= 0 && H > 0 && H <= (1 << 20) && total_T <= (1L << 42) / H;
+}
+
+size_t gdn_decay_bwd_workspace_size(long total_T, int H) {
+    return decay_bwd_sizes_ok(total_T, H) ? gdn::gate_prep_bwd_workspace_bytes(total_T, H) : 0;
+}
+
+int gdn_decay_from_logits_bwd(const float* a_logits, const float* A_log, const float* dt_bias, const float* b,
+                              const float* dg, const float* dbeta, float* da, float* dA_log,
+                              float* ddt_bias, float* db, long total_T, int H, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    if (!decay_bwd_sizes_ok(total_T, H)) return GDN_ERR_ARG;
+    if (total_T == 0 && !dA_log && !ddt_bias) return GDN_OK;
+    if (!A_log || (total_T > 0 && (!a_logits || !dg || !da || !b != !dbeta || !b != !db))) return GDN_ERR_ARG;
+    const void* ptrs[] = {a_logits, A_log, dt_bias, b, dg, dbeta, da, dA_log, ddt_bias, db};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return GDN_ERR_ARG;
+    gdn::GatePrepBwdArgs a{};
+    if (dA_log || ddt_bias) {
+        const size_t need = gdn::gate_prep_bwd_workspace_bytes(total_T, H);
+        if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
+        a.partial = static_cast<float*>(workspace);
+    }
+    a.a = a_logits; a.A_log = A_log; a.dt_bias = dt_bias; a.b = b; a.dg = dg; a.dbeta = dbeta;
+    a.da = da; a.dA_log = dA_log; a.ddt = ddt_bias; a.db = db; a.total_T = total_T; a.H = H;
+    return launch_status(gdn::launch_gate_prep_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,429 @@
+// gate_bwd.cu -- the training form of the gates: the output norm as a group norm (forward), the
+// gradients of both output norms, and the gradients of the gate preparation.
+//
+// All four are one pass over the data (HBM-bound): a row's statistics are taken from values that
+// stay in registers, every input is read once and every output written once.  Arithmetic and sums
+// are fp32; an output is rounded once, at its store.
+//
+// Norms.  A group of `size` channels is shared by L lanes of a warp (a power of two), each holding
+// NV vectors of VEC consecutive channels: vector i of lane l covers channels (i L + l) VEC ....
+// Lane sets walk the rows with a stride that keeps their group index, so the weight and bias of a
+// set's channels are loaded once, and the sums over rows (dweight, dbias) stay in its registers.
+//
+// The mean of a group is taken twice: what is left of it after the first subtraction (a rounding of
+// the sum, which 1 / sqrt(var + eps) would magnify where a group is nearly constant) is its own mean
+// and is taken off as well.
+//
+// Sums over rows end in a table of partial sums in the workspace, which a second kernel adds up
+// column by column in a fixed order: no atomics, so the same call gives the same bits.
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSMs = 152;
+
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float* p, float* out) {
+    if constexpr (VEC == 4) load_vec<4>(p, out);
+    else out[0] = p[0];
+}
+template <int VEC>
+__device__ __forceinline__ void load_any(const void* base, gdn_dtype dt, long idx, float* out) {
+    if (dt == GDN_BF16) {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + idx;
+        if constexpr (VEC == 4) load_vec<4>(p, out);
+        else out[0] = to_f32(p[0]);
+    } else {
+        load_f32<VEC>(static_cast<const float*>(base) + idx, out);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_any(void* base, gdn_dtype dt, long idx, const float* x) {
+    if constexpr (VEC == 4) {
+        if (dt == GDN_BF16) {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+            uint2 t;
+            t.x = *reinterpret_cast<uint32_t*>(&lo);
+            t.y = *reinterpret_cast<uint32_t*>(&hi);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + idx) = t;
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(base) + idx) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+    } else {
+        store_out(base, idx, dt, x[0]);
+    }
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// How the lane sets cover rows x groups: `stride` sets (a multiple of the groups) work, set s on
+// group s % groups and rows s / groups, s / groups + stride / groups, ...
+struct NormPlan {
+    int L, nv, vec, blocks;
+    long stride;
+};
+
+NormPlan norm_plan(long rows, int groups, int size) {
+    NormPlan p;
+    p.vec = size % 4 == 0 ? 4 : 1;
+    const int vecs = size / p.vec;
+    p.L = 1;
+    while (p.L < 32 && p.L < vecs) p.L *= 2;
+    p.nv = (vecs + p.L - 1) / p.L;
+    const long per_block = kThreads / p.L;
+    const long all = (rows * groups + per_block - 1) / per_block;      // one row a set
+    const long least = (groups + per_block - 1) / per_block;           // every group has a set
+    long b = all < 4 * kSMs ? all : 4 * kSMs;
+    if (b < least) b = least;
+    p.blocks = (int)b;
+    p.stride = b * per_block / groups * groups;
+    return p;
+}
+
+template <int L, int NV, int VEC>
+__global__ void __launch_bounds__(kThreads) groupnorm_kernel(NormArgs a, long stride) {
+    const long set = (long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    const int lane = threadIdx.x % L;
+    const int grp = (int)(set % a.groups);
+    const long rstep = stride / a.groups;
+    const float inv = 1.0f / (float)a.size;
+    float w[NV][VEC], b[NV][VEC];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * L + lane) * VEC;
+        in[i] = c < a.size && set < stride;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) { w[i][j] = 1.f; b[i][j] = 0.f; }
+        if (in[i] && a.w) load_f32<VEC>(a.w + (long)grp * a.size + c, w[i]);
+        if (in[i] && a.b) load_f32<VEC>(a.b + (long)grp * a.size + c, b[i]);
+    }
+    // every lane of a warp runs the same number of passes (the sums below are warp-wide shuffles)
+    const long passes = (a.rows + rstep - 1) / rstep;
+    long row = set / a.groups;
+    for (long p = 0; p < passes; ++p, row += rstep) {
+        const bool live = row < a.rows;
+        const long base = (row * a.groups + grp) * a.size;
+        float y[NV][VEC], z[NV][VEC];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * L + lane) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[i][j] = z[i][j] = 0.f;
+            if (!in[i] || !live) continue;
+            load_any<VEC>(a.y, a.y_dtype, base + c, y[i]);
+            if (a.z) load_f32<VEC>(a.z + base + c, z[i]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum += y[i][j];
+        }
+        const float mean = lanes_sum<L>(sum) / (float)a.size;
+        float rest = 0.f, ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                y[i][j] -= mean;
+                rest += y[i][j];
+                ss += y[i][j] * y[i][j];
+            }
+        }
+        const float off = lanes_sum<L>(rest) * inv;
+        const float r = rsqrtf(fmaxf(lanes_sum<L>(ss) * inv - off * off, 0.f) + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i] || !live) continue;
+            const int c = (i * L + lane) * VEC;
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float m = fmaf(w[i][j], (y[i][j] - off) * r, b[i][j]);
+                o[j] = a.z ? m * (z[i][j] * sigmoidf_(z[i][j])) : m * sigmoidf_(m);
+            }
+            store_any<VEC>(a.out, a.out_dtype, base + c, o);
+        }
+    }
+}
+
+template <int L, int NV, int VEC, bool RMS>
+__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(NormArgs a, long stride) {
+    const long set = (long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    const int lane = threadIdx.x % L;
+    const int grp = (int)(set % a.groups);
+    const long rstep = stride / a.groups;
+    const float inv = 1.0f / (float)a.size;
+    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * L + lane) * VEC;
+        in[i] = c < a.size && set < stride;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) { w[i][j] = 1.f; b[i][j] = 0.f; dw[i][j] = 0.f; db[i][j] = 0.f; }
+        if (in[i] && a.w) load_f32<VEC>(a.w + (long)grp * a.size + c, w[i]);
+        if (!RMS && in[i] && a.b) load_f32<VEC>(a.b + (long)grp * a.size + c, b[i]);
+    }
+    const long passes = (a.rows + rstep - 1) / rstep;
+    long row = set / a.groups;
+    for (long p = 0; p < passes; ++p, row += rstep) {
+        const bool live = row < a.rows;
+        const long base = (row * a.groups + grp) * a.size;
+        float y[NV][VEC], z[NV][VEC], d[NV][VEC];
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * L + lane) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[i][j] = z[i][j] = d[i][j] = 0.f;
+            if (!in[i] || !live) continue;
+            load_any<VEC>(a.y, a.y_dtype, base + c, y[i]);
+            load_any<VEC>(a.dout, a.dout_dtype, base + c, d[i]);
+            if (RMS || a.z) load_f32<VEC>(a.z + base + c, z[i]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum += y[i][j];
+        }
+        const float mean = RMS ? 0.f : lanes_sum<L>(sum) / (float)a.size;
+        float rest = 0.f, ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                y[i][j] -= mean;
+                rest += y[i][j];
+                ss += y[i][j] * y[i][j];
+            }
+        }
+        const float off = RMS ? 0.f : lanes_sum<L>(rest) * inv;
+        const float var = fmaxf(lanes_sum<L>(ss) * inv - off * off, 0.f);
+        const float r = live ? rsqrtf(var + a.eps) : 0.f;  // rows past the end add nothing to dw, db
+        // y becomes n; d becomes dn; z becomes dz
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float n = (y[i][j] - off) * r, g = d[i][j];
+                const float m = RMS ? w[i][j] * n : fmaf(w[i][j], n, b[i][j]);
+                const float t = (RMS || a.z) ? z[i][j] : m;
+                const float sg = sigmoidf_(t), slope = sg * fmaf(t, 1.0f - sg, 1.0f);
+                const float dm = g * ((RMS || a.z) ? t * sg : slope);
+                z[i][j] = g * m * slope;
+                dw[i][j] += dm * n;
+                if (!RMS) db[i][j] += dm;
+                const float dn = dm * w[i][j];
+                y[i][j] = n;
+                d[i][j] = dn;
+                s1 += dn;
+                s2 += dn * n;
+            }
+        }
+        const float m1 = RMS ? 0.f : lanes_sum<L>(s1) * inv;
+        const float m2 = lanes_sum<L>(s2) * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i] || !live) continue;
+            const int c = (i * L + lane) * VEC;
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o[j] = r * (d[i][j] - m1 - y[i][j] * m2);
+            store_any<VEC>(a.dy, a.y_dtype, base + c, o);
+            if (RMS || a.z) store_any<VEC>(a.dz, GDN_F32, base + c, z[i]);
+        }
+    }
+    if (!a.partial || set >= stride) return;
+    const long channels = (long)a.groups * a.size;
+    float* pw = a.partial + (set / a.groups) * channels + (long)grp * a.size;
+    float* pb = pw + rstep * channels;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (!in[i]) continue;
+        const int c = (i * L + lane) * VEC;
+        if (a.dw) store_any<VEC>(pw, GDN_F32, c, dw[i]);
+        if (!RMS && a.db) store_any<VEC>(pb, GDN_F32, c, db[i]);
+    }
+}
+
+// out[c] = sum over r of table[r][c] for both tables (the second may be absent): 32 columns and 8
+// interleaved row ranges per block, each range added in order, the ranges then in order.
+__global__ void __launch_bounds__(kThreads) column_sum_kernel(const float* table, long rows, long cols,
+                                                              float* out0, float* out1) {
+    __shared__ float part[8][32];
+    const long c = (long)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int k = threadIdx.x >> 5;
+    const float* t = table + (blockIdx.y ? rows * cols : 0);
+    float* out = blockIdx.y ? out1 : out0;
+    if (!out) return;
+    float s = 0.f;
+    if (c < cols)
+        for (long r = k; r < rows; r += 8) s += t[r * cols + c];
+    part[k][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+        out[c] = s;
+    }
+}
+
+template <int L, int NV, int VEC>
+void launch_norm_one(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
+    if (!bwd) groupnorm_kernel<L, NV, VEC><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
+    else if (a.rms) norm_bwd_kernel<L, NV, VEC, true><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
+    else norm_bwd_kernel<L, NV, VEC, false><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
+}
+
+template <int VEC>
+void launch_norm_vec(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
+    switch (p.L) {
+        case 1: return launch_norm_one<1, 1, VEC>(a, p, bwd, s);
+        case 2: return launch_norm_one<2, 1, VEC>(a, p, bwd, s);
+        case 4: return launch_norm_one<4, 1, VEC>(a, p, bwd, s);
+        case 8: return launch_norm_one<8, 1, VEC>(a, p, bwd, s);
+        case 16: return launch_norm_one<16, 1, VEC>(a, p, bwd, s);
+        default: break;
+    }
+    if (p.nv == 1) return launch_norm_one<32, 1, VEC>(a, p, bwd, s);
+    if (p.nv == 2) return launch_norm_one<32, 2, VEC>(a, p, bwd, s);
+    if (p.nv <= 4) return launch_norm_one<32, 4, VEC>(a, p, bwd, s);
+    if (p.nv <= 8) return launch_norm_one<32, 8, VEC>(a, p, bwd, s);
+    if constexpr (VEC == 1) return launch_norm_one<32, 32, VEC>(a, p, bwd, s);
+}
+
+cudaError_t launch_norm(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
+    if (p.vec == 4) launch_norm_vec<4>(a, p, bwd, s);
+    else launch_norm_vec<1>(a, p, bwd, s);
+    return cudaGetLastError();
+}
+
+// ---- gate preparation --------------------------------------------------------------------------
+
+// Thread q of the grid works on column vector q % (H / VEC) of rows q / (H / VEC), ..., with a
+// stride that keeps its column, so the column sums stay in registers.
+struct DecayPlan {
+    int vec, blocks;
+    long cols, stride, prows;  // column vectors; working threads; rows of the partial table
+};
+
+DecayPlan decay_plan(long total_T, int H) {
+    DecayPlan p;
+    p.vec = H % 4 == 0 ? 4 : 1;
+    p.cols = H / p.vec;
+    const long all = (total_T * p.cols + kThreads - 1) / kThreads;
+    const long least = (p.cols + kThreads - 1) / kThreads;
+    long b = all < 4 * kSMs ? all : 4 * kSMs;
+    if (b < least) b = least;
+    p.blocks = (int)b;
+    p.stride = b * kThreads / p.cols * p.cols;
+    p.prows = p.cols <= kThreads ? b : p.stride / p.cols;
+    return p;
+}
+
+template <int VEC>
+__global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs a, long cols, long stride,
+                                                                 long prows) {
+    const long q = (long)blockIdx.x * kThreads + threadIdx.x;
+    const long h = (q % cols) * VEC;
+    float A[VEC], bias[VEC], sA[VEC], sd[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        A[j] = expf(a.A_log[h + j]);
+        bias[j] = a.dt_bias ? a.dt_bias[h + j] : 0.f;
+        sA[j] = sd[j] = 0.f;
+    }
+    if (q < stride) {
+        const long n = a.total_T * cols;
+        for (long i = q; i < n; i += stride) {
+            float x[VEC], dg[VEC], o[VEC];
+            load_f32<VEC>(a.a + i * VEC, x);
+            load_f32<VEC>(a.dg + i * VEC, dg);
+            if (a.b) {
+                float b[VEC], dbeta[VEC];
+                load_f32<VEC>(a.b + i * VEC, b);
+                load_f32<VEC>(a.dbeta + i * VEC, dbeta);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float beta = sigmoidf_(b[j]);
+                    b[j] = dbeta[j] * beta * sigmoidf_(-b[j]);
+                }
+                store_any<VEC>(a.db, GDN_F32, i * VEC, b);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float t = x[j] + bias[j];
+                const float sp = t > 20.0f ? t : log1pf(expf(t));
+                o[j] = -dg[j] * A[j] * sigmoidf_(t);
+                sA[j] -= dg[j] * A[j] * sp;
+                sd[j] += o[j];
+            }
+            store_any<VEC>(a.da, GDN_F32, i * VEC, o);
+        }
+    }
+    if (!a.partial) return;
+    // threads of the block that hold the same columns are added in order (cols <= kThreads); idle
+    // threads hold zeros
+    __shared__ float sh[2][kThreads][VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) { sh[0][threadIdx.x][j] = sA[j]; sh[1][threadIdx.x][j] = sd[j]; }
+    __syncthreads();
+    long prow = blockIdx.x;
+    if (cols <= kThreads) {
+        if (threadIdx.x >= cols) return;
+        for (long t = threadIdx.x + cols; t < kThreads; t += cols)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) { sA[j] += sh[0][t][j]; sd[j] += sh[1][t][j]; }
+    } else {
+        if (q >= stride) return;
+        prow = q / cols;
+    }
+    const long H = cols * VEC;
+    store_any<VEC>(a.partial + prow * H, GDN_F32, h, sA);
+    store_any<VEC>(a.partial + (prows + prow) * H, GDN_F32, h, sd);
+}
+
+}  // namespace
+
+size_t norm_bwd_workspace_bytes(long rows, int groups, int size) {
+    const NormPlan p = norm_plan(rows, groups, size);
+    return (size_t)(p.stride / groups) * groups * size * 2 * sizeof(float);
+}
+
+cudaError_t launch_groupnorm(const NormArgs& a, cudaStream_t s) {
+    return launch_norm(a, norm_plan(a.rows, a.groups, a.size), false, s);
+}
+
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s) {
+    const NormPlan p = norm_plan(a.rows, a.groups, a.size);
+    cudaError_t e = launch_norm(a, p, true, s);
+    if (e != cudaSuccess || !a.partial) return e;
+    const long cols = (long)a.groups * a.size;
+    column_sum_kernel<<<dim3((unsigned)((cols + 31) / 32), a.db ? 2 : 1), kThreads, 0, s>>>(
+        a.partial, p.stride / a.groups, cols, a.dw, a.db);
+    return cudaGetLastError();
+}
+
+size_t gate_prep_bwd_workspace_bytes(long total_T, int H) {
+    return (size_t)decay_plan(total_T, H).prows * H * 2 * sizeof(float);
+}
+
+cudaError_t launch_gate_prep_bwd(const GatePrepBwdArgs& a, cudaStream_t s) {
+    const DecayPlan p = decay_plan(a.total_T, a.H);
+    if (p.vec == 4) gate_prep_bwd_kernel<4><<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
+    else gate_prep_bwd_kernel<1><<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.partial) return e;
+    column_sum_kernel<<<dim3((unsigned)((a.H + 31) / 32), a.ddt ? 2 : 1), kThreads, 0, s>>>(
+        a.partial, p.prows, a.H, a.dA_log, a.ddt);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

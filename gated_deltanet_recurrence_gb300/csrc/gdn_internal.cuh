@@ -117,6 +117,37 @@ struct GatePrepArgs {
 };
 cudaError_t launch_gate_prep(const GatePrepArgs& a, cudaStream_t s);
 
+// Gradients of the output norms: RMS norm (rms = 1, groups = 1, bias null) and group norm.
+struct NormArgs {
+    const void* y; gdn_dtype y_dtype; const float* z; const float* w; const float* b; float eps;
+    void* out; gdn_dtype out_dtype;                                       // forward
+    const void* dout; gdn_dtype dout_dtype; void* dy; float* dz; float* dw; float* db;  // backward
+    long rows; int groups, size, rms; float* partial;
+};
+cudaError_t launch_groupnorm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s);
+size_t norm_bwd_workspace_bytes(long rows, int groups, int size);
+
+struct GatePrepBwdArgs {
+    const float* a; const float* A_log; const float* dt_bias; const float* b;
+    const float* dg; const float* dbeta; float* da; float* dA_log; float* ddt; float* db;
+    long total_T; int H; float* partial;
+};
+cudaError_t launch_gate_prep_bwd(const GatePrepBwdArgs& a, cudaStream_t s);
+size_t gate_prep_bwd_workspace_bytes(long total_T, int H);
+
+// Gradients of the chunked form (chunk_bwd.cu).
+struct ChunkBwdArgs {
+    const void* q; const void* k; const void* v; const float* g; const float* beta;
+    const int32_t* cu_seqlens; int num_seqs, total_T, H, Hk, d; gdn_dtype qkv_dtype;
+    float scale; int use_l2; const float* initial_state;
+    const void* dout; gdn_dtype dout_dtype; const float* dfinal_state;
+    void* dq; void* dk; void* dv; float* dg; float* dbeta; float* dinitial_state;
+    void* workspace; int* err;
+};
+size_t chunk_bwd_workspace_bytes(int num_seqs, int total_T, int H, int Hk, int d);
+cudaError_t launch_chunk_bwd(const ChunkBwdArgs& a, cudaStream_t s);
+
 struct PrefillArgs {
     const void* q; const void* k; const void* v; const float* g; const float* beta;
     const int32_t* cu_seqlens; int num_seqs, total_T, H, Hk, d; gdn_dtype qkv_dtype;

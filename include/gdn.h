@@ -125,6 +125,42 @@ size_t gdn_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int d_k, i
                                     gdn_dtype qkv_dtype);
 
 /*
+ * gdn_chunk_bwd -- the gradients of gdn_chunk_fwd without gate and convolution (training form).
+ * The pages say that the chunked form is the one for training ("5. 线性注意力", "Delta Rule 的 Chunk
+ * 实现"; "[LLM Algorithms-2] Gated DeltaNet" section 7) but give no backward pass; it is the adjoint
+ * of the update of "[LLM Algorithms-2] Gated DeltaNet" section 4.  Nothing has to be kept from the
+ * forward call: the states at the chunk starts are recomputed.
+ *
+ *   q, k, v, g, beta, cu_seqlens, num_seqs, total_T, H, H_k, d_k, d_v, qkv_dtype, scale,
+ *   use_qk_l2norm, initial_state   as given to gdn_chunk_fwd; g finite.  decay must be
+ *                 GDN_DECAY_PER_HEAD (GDN_DECAY_PER_KEY_CHANNEL returns GDN_ERR_UNSUPPORTED).
+ *   dout          [total_T, H, d_v] of dout_dtype: the gradient of out.
+ *   dfinal_state  [num_seqs, H, d_v, d_k] fp32, or NULL for zeros: the gradient of final_state.
+ *   dq, dk        [total_T, H_k, d_k] of qkv_dtype (with grouped heads, summed over the value heads
+ *                 that share the query/key head, in a fixed order, and rounded once).
+ *   dv            [total_T, H, d_v] of qkv_dtype.
+ *   dg, dbeta     [total_T, H] fp32.
+ *   dinitial_state [num_seqs, H, d_v, d_k] fp32, or NULL (not written).  For an empty sequence it
+ *                 is dfinal_state.  May alias dfinal_state.
+ *   workspace     at least gdn_chunk_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * No other output may overlap an input.  Rows of tokens behind the last sequence of cu_seqlens are
+ * left as they were.  A malformed cu_seqlens is recorded as GDN_ERR_CU_SEQLENS in the device error
+ * word, and the call then writes nothing.
+ * Arithmetic is that of fp32 for both element types, with one rounding at each output; the same
+ * call gives the same bits.
+ */
+int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                  const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k,
+                  int d_k, int d_v, gdn_dtype qkv_dtype, gdn_decay decay, float scale,
+                  int use_qk_l2norm, const float* initial_state,
+                  const void* dout, gdn_dtype dout_dtype, const float* dfinal_state,
+                  void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dinitial_state,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdn_chunk_bwd needs for these sizes; 0 for sizes it refuses. */
+size_t gdn_chunk_bwd_workspace_size(int num_seqs, int total_T, int H, int H_k, int d_k, int d_v);
+
+/*
  * gdn_recurrent_step -- one decode token for N sequences, state updated in place.
  * Source: "6.6 Gated DeltaNet", 6.6.8 (decode keeps only S); the update of
  * "[LLM Algorithms-2] Gated DeltaNet" section 4.  One read and one write of each state.
@@ -189,6 +225,67 @@ int gdn_gate_rmsnorm_silu(const void* y, gdn_dtype y_dtype, const float* z,
                           long rows, int d_v, void* stream);
 
 /*
+ * gdn_gate_rmsnorm_silu_bwd -- the gradients of gdn_gate_rmsnorm_silu (training form).
+ * The pages give no backward pass; it follows from the forward formula.  With n = y / rms(y),
+ * m = norm_weight * n and out = m * silu(z):
+ *   dm = dout * silu(z),  dz = dout * m * silu'(z),  dnorm_weight = sum over rows of dm * n,
+ *   dn = dm * norm_weight,  dy = (dn - n * mean(dn * n)) / rms(y).
+ *
+ *   dout [rows, d_v] of dout_dtype; y [rows, d_v] of y_dtype; z [rows, d_v] fp32;
+ *   norm_weight [d_v] fp32 or NULL (ones); eps and d_v as in the forward call;
+ *   dy [rows, d_v] of y_dtype (may alias y, or dout when the element types match);
+ *   dz [rows, d_v] fp32 (may alias z); dnorm_weight [d_v] fp32 or NULL (not computed);
+ *   workspace  device scratch of at least gdn_gate_bwd_workspace_size(rows, 1, d_v) bytes, 16-byte
+ *              aligned; may be NULL when dnorm_weight is.
+ * The sum over rows has a fixed order: the same call gives the same bits.
+ */
+int gdn_gate_rmsnorm_silu_bwd(const void* dout, gdn_dtype dout_dtype, const void* y, gdn_dtype y_dtype,
+                              const float* z, const float* norm_weight, float eps, void* dy, float* dz,
+                              float* dnorm_weight, long rows, int d_v, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_gate_groupnorm_silu -- the output norm as a group norm over the heads, channels last.
+ * The output stage of the pages ("5. 线性注意力", "门控 RMSNorm"; "6.6 Gated DeltaNet" 6.6.2) with the
+ * mean taken off as well and an affine map per channel: each token's channels are `groups` groups
+ * (the heads) of `group_size`, and with mean and biased variance over a group's channels,
+ *   n = (y - mean) / sqrt(var + eps),  m = weight * n + bias,
+ *   out = m * silu(z)  with a gate z,   out = silu(m)  without.
+ * Statistics are fp32 over values read once (the variance from the centred values); one rounding,
+ * to out_dtype.
+ *
+ *   y [rows, groups, group_size] of y_dtype; z the same shape fp32, or NULL;
+ *   weight, bias [groups, group_size] fp32 or NULL (ones, zeros);
+ *   out [rows, groups, group_size] of out_dtype (may alias y when the element types match).
+ *   1 <= group_size <= 1024, groups >= 1, groups * group_size <= 2^20.
+ */
+int gdn_gate_groupnorm_silu(const void* y, gdn_dtype y_dtype, const float* z, const float* weight,
+                            const float* bias, float eps, void* out, gdn_dtype out_dtype, long rows,
+                            int groups, int group_size, void* stream);
+
+/*
+ * gdn_gate_groupnorm_silu_bwd -- the gradients of gdn_gate_groupnorm_silu.
+ * With r = 1 / sqrt(var + eps) and dm = dout * silu(z) (gated) or dout * silu'(m) (not gated):
+ *   dz = dout * m * silu'(z),  dweight = sum over rows of dm * n,  dbias = sum over rows of dm,
+ *   dn = dm * weight,  dy = r * (dn - mean(dn) - n * mean(dn * n)).
+ *
+ *   dout of dout_dtype, y of y_dtype, z fp32 or NULL, weight and bias as in the forward call;
+ *   dy of y_dtype (may alias y, or dout when the element types match); dz fp32, given exactly when
+ *   z is (may alias z); dweight, dbias [groups, group_size] fp32, each may be NULL (not computed);
+ *   workspace  at least gdn_gate_bwd_workspace_size(rows, groups, group_size) bytes, 16-byte
+ *              aligned; may be NULL when dweight and dbias are.
+ */
+int gdn_gate_groupnorm_silu_bwd(const void* dout, gdn_dtype dout_dtype, const void* y, gdn_dtype y_dtype,
+                                const float* z, const float* weight, const float* bias, float eps,
+                                void* dy, float* dz, float* dweight, float* dbias, long rows,
+                                int groups, int group_size, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Bytes of workspace the two calls above need for these sizes (RMS norm: groups = 1, group_size =
+ * d_v); 0 for sizes they refuse. */
+size_t gdn_gate_bwd_workspace_size(long rows, int groups, int group_size);
+
+/*
  * gdn_decay_from_logits -- gate preparation.
  * Source: "6.6 Gated DeltaNet" 6.6.3:  alpha = exp(-A softplus(a + dt_bias)) with A = exp(A_log)
  * per head, kept in log space as g = -exp(A_log) softplus(a + dt_bias); beta = sigmoid(b).
@@ -200,6 +297,27 @@ int gdn_gate_rmsnorm_silu(const void* y, gdn_dtype y_dtype, const float* z,
 int gdn_decay_from_logits(const float* a, const float* A_log, const float* dt_bias,
                           const float* b, float* g_out, float* beta_out, long total_T, int H,
                           void* stream);
+
+/*
+ * gdn_decay_from_logits_bwd -- the gradients of gdn_decay_from_logits.
+ * With x = a + dt_bias, g = -exp(A_log) softplus(x) and beta = sigmoid(b):
+ *   da = -dg exp(A_log) sigmoid(x),  dA_log = sum over tokens of dg * g,
+ *   ddt_bias = sum over tokens of da,  db = dbeta * beta * (1 - beta).
+ *
+ *   a, dg, da [total_T, H] fp32; A_log [H]; dt_bias [H] or NULL (zero); b, dbeta, db [total_T, H]
+ *   fp32, all three given or all three NULL; dA_log, ddt_bias [H] fp32, each may be NULL (not
+ *   computed).  da may alias a or dg; db may alias b or dbeta.
+ *   workspace  at least gdn_decay_bwd_workspace_size(total_T, H) bytes, 16-byte aligned; may be
+ *              NULL when dA_log and ddt_bias are.
+ * The sums over tokens have a fixed order: the same call gives the same bits.
+ */
+int gdn_decay_from_logits_bwd(const float* a, const float* A_log, const float* dt_bias, const float* b,
+                              const float* dg, const float* dbeta, float* da, float* dA_log,
+                              float* ddt_bias, float* db, long total_T, int H, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdn_decay_from_logits_bwd needs for these sizes; 0 for sizes it refuses. */
+size_t gdn_decay_bwd_workspace_size(long total_T, int H);
 
 /*
  * gdn_chunk_fwd_noalloc -- gdn_chunk_fwd for callers that cannot allocate device memory.

@@ -1,0 +1,112 @@
+"""Plain fp64 forms of the training operators, for the tests: each is its forward definition written out
+in torch on the CPU, differentiated by autograd."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+F64 = torch.float64
+# A fp32 output: the longest chain of roundings behind one value is a sum of 128 or 64 products at each of
+# some eight products in a row, whose errors add like sqrt(8 * 128) half steps of 2^-24 (2e-6) where
+# nothing cancels; ten times that leaves room for the cancellation in the row dots.
+TOL_F32 = 2e-5
+# A bf16 output is rounded once: at most half a step, 2^-8 of each value, and the fp32 error before it.
+TOL_BF16 = 2.0 ** -8 + TOL_F32
+
+
+def tol_of(t):
+    return TOL_BF16 if t.dtype == torch.bfloat16 else TOL_F32
+
+
+def rel_l2(x, ref):
+    """||x - ref|| / ||ref||, and 0 where both are zero."""
+    x, ref = x.detach().cpu().to(F64), ref.detach().cpu().to(F64)
+    assert x.shape == ref.shape, (x.shape, ref.shape)
+    assert torch.isfinite(x).all()
+    off, norm = float((x - ref).norm()), float(ref.norm())
+    return off / norm if norm else (math.inf if off else 0.0)
+
+
+def delta_forward(q, k, v, g, beta, cu, S0, scale, use_l2):
+    """The recurrence token by token; q, k [T, Hk, d], v [T, H, d], g, beta [T, H], S0 [n, H, d, d]."""
+    H, rep = v.shape[1], v.shape[1] // q.shape[1]
+    if use_l2:
+        q = q / torch.sqrt((q * q).sum(-1, keepdim=True) + 1e-6)
+        k = k / torch.sqrt((k * k).sum(-1, keepdim=True) + 1e-6)
+    q, k = (q * scale).repeat_interleave(rep, 1), k.repeat_interleave(rep, 1)
+    out, final = [], []
+    for n in range(len(cu) - 1):
+        S = S0[n]
+        for t in range(cu[n], cu[n + 1]):
+            S = S * g[t].exp()[:, None, None]
+            u = beta[t][:, None] * (v[t] - (S @ k[t][:, :, None])[..., 0])
+            S = S + u[:, :, None] * k[t][:, None, :]
+            out.append((S @ q[t][:, :, None])[..., 0])
+        final.append(S)
+    y = torch.stack(out) if out else v.new_zeros((0, H, v.shape[-1]))
+    return y, torch.stack(final)
+
+
+def delta_inputs(lengths, H, Hk, d, dtype, seed, a_mean=-1.0, carried=True, lead=0, behind=0):
+    """Seeded inputs of one packed batch, on the CPU; `lead` and `behind` tokens belong to no sequence."""
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    T, n = sum(lengths) + lead + behind, len(lengths)
+    A = torch.exp(torch.rand(H, generator=gen) * math.log(8.0))
+    inp = dict(q=rn(T, Hk, d).to(dtype), k=rn(T, Hk, d).to(dtype), v=rn(T, H, d).to(dtype),
+               g=-A * torch.nn.functional.softplus(rn(T, H) + a_mean), beta=torch.sigmoid(rn(T, H)),
+               dout=rn(T, H, d).to(dtype), initial_state=rn(n, H, d, d) * 0.1 if carried else None,
+               dfinal_state=rn(n, H, d, d) * 0.1 if carried else None)
+    inp["cu"] = [lead + int(x) for x in np.concatenate([[0], np.cumsum(lengths)])]
+    return inp
+
+
+def delta_grads(inp, scale=None, use_l2=True):
+    """fp64 gradients of the inputs of delta_inputs: dq, dk, dv, dg, dbeta, dinitial_state."""
+    d, n, H = inp["q"].shape[-1], len(inp["cu"]) - 1, inp["v"].shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    S0 = inp["initial_state"]
+    S0 = torch.zeros(n, H, d, d) if S0 is None else S0
+    leaves = [x.to(F64).clone().requires_grad_() for x in (inp["q"], inp["k"], inp["v"], inp["g"], inp["beta"], S0)]
+    y, S = delta_forward(*leaves[:5], inp["cu"], leaves[5], scale, use_l2)
+    dS = inp["dfinal_state"]
+    dS = torch.zeros_like(S) if dS is None else dS.to(F64)
+    dy = inp["dout"].to(F64)[inp["cu"][0]:inp["cu"][-1]]
+    got = torch.autograd.grad((y * dy).sum() + (S * dS).sum(), leaves, allow_unused=True)
+    got = [torch.zeros_like(x) if gr is None else gr for gr, x in zip(got, leaves)]
+    return dict(zip(("dq", "dk", "dv", "dg", "dbeta", "dinitial_state"), got))
+
+
+def norm_forward(y, z, w, b, eps, rms):
+    """The output norm over the last dimension of y [rows, groups, size] (w, b broadcast) with its SiLU."""
+    if rms:
+        m = y / torch.sqrt((y * y).mean(-1, keepdim=True) + eps)
+    else:
+        c = y - y.mean(-1, keepdim=True)
+        m = c / torch.sqrt((c * c).mean(-1, keepdim=True) + eps)
+    m = m if w is None else m * w
+    m = m if b is None else m + b
+    t = m if z is None else z
+    return (1.0 if z is None else m) * t * torch.sigmoid(t)
+
+
+def norm_grads(dout, y, z, w, b, eps, rms):
+    """fp64 gradients (dy, dz, dw, db), None where the input is."""
+    leaves = [None if x is None else x.to(F64).clone().requires_grad_() for x in (y, z, w, b)]
+    out = norm_forward(*leaves, eps, rms)
+    got = iter(torch.autograd.grad(out, [x for x in leaves if x is not None], dout.to(F64)))
+    return [None if x is None else next(got) for x in leaves]
+
+
+def decay_grads(a, A_log, dt_bias, b, dg, dbeta):
+    """fp64 gradients (da, dA_log, ddt_bias, db), None where the input is."""
+    leaves = [None if x is None else x.to(F64).clone().requires_grad_() for x in (a, A_log, dt_bias, b)]
+    x = leaves[0] if dt_bias is None else leaves[0] + leaves[2]
+    g = -leaves[1].exp() * (x.clamp(min=0) + torch.log1p(torch.exp(-x.abs())))
+    loss = (g * dg.to(F64)).sum()
+    if b is not None:
+        loss = loss + (torch.sigmoid(leaves[3]) * dbeta.to(F64)).sum()
+    got = iter(torch.autograd.grad(loss, [x for x in leaves if x is not None]))
+    return [None if x is None else next(got) for x in leaves]

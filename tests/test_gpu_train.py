@@ -1,0 +1,261 @@
+"""The training operators on the GPU, against fp64 forms on the same inputs (tests/_train.py)."""
+import pytest
+import torch
+
+import gated_deltanet_recurrence_gb300 as gdn
+from tests import _train
+from tests._train import decay_grads, delta_grads, delta_inputs, norm_grads, rel_l2, tol_of
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dinitial_state")
+
+
+def dev(x):
+    return x.cuda() if isinstance(x, torch.Tensor) else x
+
+
+def chunk_bwd(inp, **kw):
+    cu = torch.tensor(inp["cu"], dtype=torch.int32, device="cuda")
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    got = gdn.gdn_chunk_bwd(*args, cu_seqlens=cu, initial_state=dev(inp["initial_state"]),
+                            dfinal_state=dev(inp["dfinal_state"]), **kw)
+    assert gdn.gdn_get_device_error() == 0
+    return dict(zip(NAMES, got))
+
+
+def check_chunk(inp, got, use_l2=True, scale=None):
+    ref = delta_grads(inp, use_l2=use_l2, scale=scale)
+    lo, hi = inp["cu"][0], inp["cu"][-1]
+    for name in NAMES:
+        if got[name] is None:
+            continue
+        x, r = got[name], ref[name]
+        if name != "dinitial_state":
+            x, r = x[lo:hi], r[lo:hi]
+        assert rel_l2(x, r) <= tol_of(x), (name, rel_l2(x, r))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths,H,Hk,carried", [
+    ([1], 1, 1, False),
+    ([1, 2, 0, 3], 2, 2, True),
+    ([63, 64, 65], 2, 1, True),
+    ([200], 3, 3, False),
+    ([130, 0, 257, 5], 4, 2, True),
+    ([321], 6, 2, False),
+])
+def test_chunk_bwd(lengths, H, Hk, carried, d, dtype):
+    inp = delta_inputs(lengths, H, Hk, d, dtype, seed=sum(lengths) + d, carried=carried)
+    check_chunk(inp, chunk_bwd(inp))
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, F32)])
+@pytest.mark.parametrize("a_mean", [-4.0, 3.0])
+def test_chunk_bwd_slow_and_fast_decay(d, dtype, a_mean):
+    inp = delta_inputs([300, 77], 2, 2, d, dtype, seed=7, a_mean=a_mean)
+    check_chunk(inp, chunk_bwd(inp))
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, F32)])
+def test_chunk_bwd_without_normalisation(d, dtype):
+    inp = delta_inputs([150, 20], 2, 1, d, dtype, seed=9)
+    for x in ("q", "k"):
+        inp[x] = (inp[x].float() * d ** -0.5).to(dtype)
+    check_chunk(inp, chunk_bwd(inp, use_qk_l2norm=False, scale=0.7), use_l2=False, scale=0.7)
+
+
+def test_chunk_bwd_first_token_has_no_decay_gradient():
+    inp = delta_inputs([1, 1], 2, 2, 128, BF16, seed=3, carried=False)
+    assert torch.count_nonzero(chunk_bwd(inp)["dg"]) == 0
+
+
+@pytest.mark.parametrize("Hk", [1, 3])
+def test_chunk_bwd_leaves_rows_outside_the_sequences(Hk):
+    inp = delta_inputs([70, 0, 9], 3, Hk, 64, BF16, seed=5, lead=4, behind=6)
+    T = inp["q"].shape[0]
+    outs = {x: torch.full_like(dev(inp[x[1:]]), 3.5) for x in ("dq", "dk", "dv", "dg", "dbeta")}
+    got = chunk_bwd(inp, **outs)
+    check_chunk(inp, got)
+    for x in outs:
+        assert (got[x][:4] == 3.5).all() and (got[x][T - 6:] == 3.5).all(), x
+
+
+def test_chunk_bwd_fp32_dout_of_bf16_inputs_and_equal_lengths():
+    inp = delta_inputs([96, 96], 2, 2, 128, BF16, seed=6)
+    inp["dout"] = torch.randn(192, 2, 128, generator=torch.Generator().manual_seed(1))
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    got = gdn.gdn_chunk_bwd(*args, num_seqs=2, initial_state=dev(inp["initial_state"]),
+                            dfinal_state=dev(inp["dfinal_state"]))
+    check_chunk(inp, dict(zip(NAMES, got)))
+
+
+def test_chunk_bwd_is_reproducible_and_aliases_the_state_gradient():
+    inp = delta_inputs([200, 33], 4, 2, 128, BF16, seed=8)
+    one, two = chunk_bwd(inp), None
+    dS = dev(inp["dfinal_state"]).clone()
+    cu = torch.tensor(inp["cu"], dtype=torch.int32, device="cuda")
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    two = dict(zip(NAMES, gdn.gdn_chunk_bwd(*args, cu_seqlens=cu, initial_state=dev(inp["initial_state"]),
+                                            dfinal_state=dS, dinitial_state=dS)))
+    for x in NAMES:
+        assert torch.equal(one[x], two[x]), x
+
+
+def test_chunk_bwd_malformed_cu_seqlens_writes_nothing():
+    inp = delta_inputs([64, 64], 2, 1, 64, F32, seed=4)
+    outs = {x: torch.full_like(dev(inp[x[1:]]), 3.5) for x in ("dq", "dk", "dv", "dg", "dbeta")}
+    outs["dinitial_state"] = torch.full_like(dev(inp["initial_state"]), 3.5)
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    for cu in ([0, 100, 64], [0, 64, 129], [-1, 64, 128]):
+        gdn.gdn_chunk_bwd(*args, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                          initial_state=dev(inp["initial_state"]), dfinal_state=dev(inp["dfinal_state"]), **outs)
+        assert gdn.gdn_get_device_error() == -3
+        assert gdn.gdn_get_device_error() == 0
+        assert all((x == 3.5).all() for x in outs.values())
+
+
+def test_chunk_bwd_empty_batch_passes_the_state_gradient_through():
+    inp = delta_inputs([0, 0], 2, 2, 64, F32, seed=2)
+    got = chunk_bwd(inp)
+    assert torch.equal(got["dinitial_state"].cpu(), inp["dfinal_state"])
+    assert got["dq"].numel() == 0
+
+
+# ---- norms -----------------------------------------------------------------------------------------
+
+def _norm_inputs(rows, groups, size, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    return dict(y=(rn(rows, groups, size) * 0.7 + 0.3).to(dtype), z=rn(rows, groups, size) * 2,
+                w=1 + 0.2 * rn(groups, size), b=0.3 * rn(groups, size), dout=rn(rows, groups, size).to(dtype))
+
+
+@pytest.mark.parametrize("rows,heads,d,dtype,weight", [
+    (1, 1, 32, F32, True), (3, 2, 64, BF16, False), (5, 3, 96, BF16, True), (1000, 16, 128, BF16, True),
+    (2500, 1, 1024, F32, True), (7, 5, 128, F32, False), (301, 4, 512, BF16, True)])
+def test_rmsnorm_bwd(rows, heads, d, dtype, weight):
+    x = _norm_inputs(rows, heads, d, dtype, seed=rows + d)
+    w = x["w"][0] if weight else None
+    got = gdn.gdn_gate_rmsnorm_silu_bwd(dev(x["dout"]), dev(x["y"]), dev(x["z"]), dev(w))
+    ref = norm_grads(x["dout"], x["y"], x["z"], w, None, 1e-6, True)
+    for g, r, name in zip(got, ref, ("dy", "dz", "dw")):
+        assert (g is None) == (r is None)
+        if g is not None:
+            assert rel_l2(g, r) <= tol_of(g), (name, rel_l2(g, r))
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("affine", [True, False])
+@pytest.mark.parametrize("rows,groups,size,dtype", [
+    (1, 1, 2, F32), (2, 3, 5, BF16), (4, 16, 64, F32), (1000, 16, 128, BF16), (333, 12, 80, F32),
+    (65, 7, 41, BF16), (50, 2, 1023, F32), (19, 4, 1024, BF16), (3, 700, 4, F32), (9, 1500, 3, BF16)])
+def test_groupnorm(rows, groups, size, dtype, affine, gated):
+    x = _norm_inputs(rows, groups, size, dtype, seed=rows + size)
+    z = x["z"] if gated else None
+    w, b = (x["w"], x["b"]) if affine else (None, None)
+    out = gdn.gdn_gate_groupnorm_silu(dev(x["y"]), dev(z), dev(w), dev(b))
+    f64 = lambda t: None if t is None else t.double()  # noqa: E731
+    ref = _train.norm_forward(*(f64(t) for t in (x["y"], z, w, b)), 1e-6, False)
+    assert rel_l2(out, ref) <= tol_of(out), rel_l2(out, ref)
+    got = gdn.gdn_gate_groupnorm_silu_bwd(dev(x["dout"]), dev(x["y"]), dev(z), dev(w), dev(b))
+    for g, r, name in zip(got, norm_grads(x["dout"], x["y"], z, w, b, 1e-6, False), ("dy", "dz", "dw", "db")):
+        assert (g is None) == (r is None), name
+        if g is not None and not (size == 2 and name == "dy"):   # n = +-1 there: dy is what eps leaves
+            assert rel_l2(g, r) <= tol_of(g), (name, rel_l2(g, r))
+
+
+def test_groupnorm_of_constant_and_single_channel_groups():
+    y = torch.full((6, 3, 40), 1.75)
+    w, b = torch.randn(3, 40), torch.randn(3, 40)
+    out = gdn.gdn_gate_groupnorm_silu(dev(y), None, dev(w), dev(b))
+    assert rel_l2(out, (b * torch.sigmoid(b)).expand_as(y)) <= 2e-6   # n is 0 exactly
+    one = gdn.gdn_gate_groupnorm_silu(dev(torch.randn(4, 9, 1)), None, None, dev(torch.ones(9, 1)))
+    assert rel_l2(one, torch.full((4, 9, 1), 1.0) * torch.sigmoid(torch.tensor(1.0))) <= 2e-6
+
+
+def test_norm_bwd_in_place_and_mixed_types():
+    x = _norm_inputs(77, 4, 64, BF16, seed=1)
+    y, z, dout = dev(x["y"]), dev(x["z"]), dev(x["dout"].float())
+    ref = gdn.gdn_gate_rmsnorm_silu_bwd(dout, y, z)
+    rr = norm_grads(x["dout"], x["y"], x["z"], None, None, 1e-6, True)
+    assert rel_l2(ref[0], rr[0]) <= tol_of(ref[0]) and rel_l2(ref[1], rr[1]) <= tol_of(ref[1])
+    y2, z2 = y.clone(), z.clone()
+    gdn.gdn_gate_rmsnorm_silu_bwd(dout, y2, z2, dy=y2, dz=z2)
+    assert torch.equal(y2, ref[0]) and torch.equal(z2, ref[1])
+    w, b = dev(x["w"]), dev(x["b"])
+    ref = gdn.gdn_gate_groupnorm_silu(y, z, w, b)
+    y2 = y.clone()
+    gdn.gdn_gate_groupnorm_silu(y2, z, w, b, out=y2)
+    assert torch.equal(y2, ref)
+
+
+def test_norm_bwd_of_no_rows_gives_zero_sums():
+    y = torch.empty(0, 3, 32, device="cuda")
+    _, _, dw, db = gdn.gdn_gate_groupnorm_silu_bwd(y, y, y, torch.ones(3, 32, device="cuda"),
+                                                   torch.ones(3, 32, device="cuda"))
+    assert torch.count_nonzero(dw) == 0 and torch.count_nonzero(db) == 0
+
+
+def test_norm_bwd_zero_eps():
+    """Rows past the end take part in no sum even where eps = 0 makes an empty row's factor infinite."""
+    x = _norm_inputs(3, 2, 64, F32, seed=12)
+    got = gdn.gdn_gate_groupnorm_silu_bwd(dev(x["dout"]), dev(x["y"]), dev(x["z"]), dev(x["w"]), dev(x["b"]), eps=0.0)
+    for g, r in zip(got, norm_grads(x["dout"], x["y"], x["z"], x["w"], x["b"], 0.0, False)):
+        assert rel_l2(g, r) <= tol_of(g)
+
+
+# ---- gate preparation --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,H", [(1, 1), (7, 3), (513, 6), (4096, 32), (1000, 33), (20, 300), (3, 2052)])
+@pytest.mark.parametrize("full", [True, False])
+def test_decay_bwd(T, H, full):
+    gen = torch.Generator().manual_seed(T + H)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    a, A_log, dg = rn(T, H) * 8, torch.rand(H, generator=gen) * 2, rn(T, H)
+    dt, b, dbeta = (rn(H), rn(T, H) * 3, rn(T, H)) if full else (None, None, None)
+    got = gdn.gdn_decay_from_logits_bwd(dev(a), dev(A_log), dev(dt), dev(b), dev(dg), dev(dbeta))
+    for g, r, name in zip(got, decay_grads(a, A_log, dt, b, dg, dbeta), ("da", "dA_log", "ddt_bias", "db")):
+        assert (g is None) == (r is None), name
+        if g is not None:
+            assert rel_l2(g, r) <= tol_of(g), (name, rel_l2(g, r))
+
+
+def test_decay_bwd_of_no_tokens_gives_zero_sums():
+    a = torch.empty(0, 5, device="cuda")
+    _, dA, ddt, _ = gdn.gdn_decay_from_logits_bwd(a, torch.ones(5, device="cuda"), torch.ones(5, device="cuda"), a, a, a)
+    assert torch.count_nonzero(dA) == 0 and torch.count_nonzero(ddt) == 0
+
+
+# ---- together ------------------------------------------------------------------------------------------
+
+def test_training_step_together():
+    """Forward and backward of a whole layer core from its logits, as a training step runs it, against
+    fp64 autograd through the same chain."""
+    lengths, H, Hk, d, dtype = [150, 41], 4, 2, 128, BF16
+    inp = delta_inputs(lengths, H, Hk, d, dtype, seed=31, carried=False)
+    gen = torch.Generator().manual_seed(32)
+    T = sum(lengths)
+    a, b, z = (torch.randn(T, *s, generator=gen) for s in ((H,), (H,), (H, d)))
+    A_log, dt, w = torch.rand(H, generator=gen), torch.randn(H, generator=gen) * 0.3, 1 + 0.1 * torch.randn(d, generator=gen)
+    do = torch.randn(T, H, d, generator=gen)
+    cu = torch.tensor(inp["cu"], dtype=torch.int32, device="cuda")
+    q, k, v, A, B, Z, AL, DT, Wt, DO = (dev(x) for x in (inp["q"], inp["k"], inp["v"], a, b, z, A_log, dt, w, do))
+    g, beta = gdn.gdn_decay_from_logits(A, AL, DT, B)
+    y, _ = gdn.gdn_chunk_fwd(q, k, v, g, beta, cu_seqlens=cu, out_dtype=F32)
+    dy, dz, dw = gdn.gdn_gate_rmsnorm_silu_bwd(DO, y, Z, Wt)
+    dq, dk, dv, dg, dbeta, _ = gdn.gdn_chunk_bwd(q, k, v, g, beta, dy, cu_seqlens=cu)
+    da, dAL, ddt, db = gdn.gdn_decay_from_logits_bwd(A, AL, DT, B, dg, dbeta)
+    assert gdn.gdn_get_device_error() == 0
+    names = ("q", "k", "v", "a", "b", "z", "A_log", "dt", "w")
+    leaves = [x.double().clone().requires_grad_() for x in (inp["q"], inp["k"], inp["v"], a, b, z, A_log, dt, w)]
+    lq, lk, lv, la, lb, lz, lA, ldt, lw = leaves
+    yy, _ = _train.delta_forward(lq, lk, lv, -lA.exp() * torch.nn.functional.softplus(la + ldt), torch.sigmoid(lb),
+                                 inp["cu"], torch.zeros(2, H, d, d, dtype=torch.float64), d ** -0.5, True)
+    out = _train.norm_forward(yy, lz, lw, None, 1e-6, True)
+    ref = torch.autograd.grad(out, leaves, do.double())
+    # y comes from the bf16 tensor-core forward, which is within 1e-2 of the exact one; the norm and its
+    # gradient pass that on with a factor of about two
+    for name, x, r in zip(names, (dq, dk, dv, da, db, dz, dAL, ddt, dw), ref):
+        assert rel_l2(x, r) <= 2e-2 + tol_of(x), (name, rel_l2(x, r))
