@@ -7,10 +7,13 @@
 // fp32 where it matters.  A bf16 matrix (8 bits) is exact in the hi plane alone.  A product takes the
 // terms hi hi, hi lo and lo hi (lo lo is below 2^-22 of the result), each an m16n8k16 fp16 tensor-core
 // instruction with fp32 accumulation: three for two split matrices, two where one is exact.  bf16 planes
-// would need three each (six terms) for the same accuracy, tf32 planes run at half the rate.
+// would need three each (six terms) for the same accuracy, tf32 planes run at half the rate (measured
+// here: 600 TFLOP/s for fp16 and bf16, 300 for tf32, 75 for packed fp32 FMA).
 //
 // Planes are row-major with their 16-byte chunks XORed by the row (mod 8), so that the eight rows an
-// ldmatrix phase reads lie in different banks, and so do the pairs an accumulator writes.
+// ldmatrix phase reads lie in different banks, and so do the pairs an accumulator writes.  Planes start
+// at multiples of their row size, so a step along a row is an XOR of the address and a step down an
+// addition.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -23,23 +26,26 @@ namespace planes {
 // Byte offset of element (row, col) in a plane with COLS columns (64 or 128).
 template <int COLS>
 __device__ __forceinline__ uint32_t offset(int row, int col) {
-    return (uint32_t)(row * COLS * 2 + ((((col >> 3) ^ (row & 7)) << 4) | ((col & 7) << 1)));
+    return (uint32_t)(row * COLS * 2 + ((col * 2) ^ ((row & 7) << 4)));
 }
 
-// A matrix of planes in shared memory: shared address of the hi plane, distance to the lo plane.
+// A matrix of P planes of COLS columns in shared memory, LO bytes apart.
+template <int COLS, int P, int LO>
 struct Mat {
-    uint32_t at, lo;
+    uint32_t at;
 };
 
+template <int O>
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4+%5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr), "n"(O));
 }
+template <int O>
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4+%5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr), "n"(O));
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -48,49 +54,70 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The 16 x 16 block of A at rows m0, columns k0: stored [m][k] (T false) or [k][m] (T true).
+// Left operand, 16 x 16 blocks: stored [m][k] (T false) or [k][m] (T true).  lane_a is this lane's
+// address in block (m0, 0); load_a adds k0.
 template <int COLS, bool T>
-__device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t base, int m0, int k0, int lane) {
-    if constexpr (T) ldsm_t(r, base + offset<COLS>(k0 + (lane & 7) + ((lane >> 4) << 3), m0 + (lane & 8)));
-    else ldsm(r, base + offset<COLS>(m0 + (lane & 15), k0 + ((lane >> 4) << 3)));
+__device__ __forceinline__ uint32_t lane_a(uint32_t base, int m0, int lane) {
+    if constexpr (T) return base + offset<COLS>((lane & 7) + ((lane >> 4) << 3), m0 + (lane & 8));
+    else return base + offset<COLS>(m0 + (lane & 15), (lane >> 4) << 3);
 }
-// The 16 x 16 block of B at k0, n0 (r[0], r[1]: columns n0 .. n0 + 7; r[2], r[3]: the next eight):
-// stored [n][k] (T false) or [k][n] (T true).
+template <int COLS, bool T, int O>
+__device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t lane_at, int k0) {
+    if constexpr (T) ldsm_t<O>(r, lane_at + k0 * COLS * 2);
+    else ldsm<O>(r, lane_at ^ (k0 * 2));
+}
+// Right operand, 16 x 16 blocks (r[0], r[1]: columns n0 .. n0 + 7; r[2], r[3]: the next eight): stored
+// [n][k] (T false) or [k][n] (T true).  lane_b is this lane's address in block (0, 0).
 template <int COLS, bool T>
-__device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t base, int n0, int k0, int lane) {
-    if constexpr (T) ldsm_t(r, base + offset<COLS>(k0 + (lane & 15), n0 + ((lane >> 4) << 3)));
-    else ldsm(r, base + offset<COLS>(n0 + (lane & 7) + ((lane >> 4) << 3), k0 + (lane & 8)));
+__device__ __forceinline__ uint32_t lane_b(uint32_t base, int lane) {
+    if constexpr (T) return base + offset<COLS>(lane & 15, (lane >> 4) << 3);
+    else return base + offset<COLS>((lane & 7) + ((lane >> 4) << 3), lane & 8);
+}
+template <int COLS, bool T, int O>
+__device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t lane_at, int n0, int k0) {
+    if constexpr (T) ldsm_t<O>(r, (lane_at ^ (n0 * 2)) + k0 * COLS * 2);
+    else ldsm<O>(r, (lane_at + n0 * COLS * 2) ^ (k0 * 2));
 }
 
 // Which 16-blocks of A's inner dimension can be non-zero: all, j <= i (A lower triangular), or j >= i.
 enum Fill { kFull, kLower, kUpper };
 
-// acc += A B for this warp's row tiles m[] and the columns n0 .. n0 + 8 NT.  CA, CB: columns of the
-// stored matrices; TA, TB: stored transposed (see load_a, load_b); PA, PB: planes; K: inner dimension.
-template <int MT, int NT, int K, int CA, bool TA, int PA, int CB, bool TB, int PB, Fill F = kFull>
-__device__ __forceinline__ void product(float (&acc)[MT][NT][4], Mat A, const int (&m)[MT], Mat B, int n0, int lane) {
+// acc += A B for this warp's row tiles m[] and the columns n0 .. n0 + 8 NT; TA, TB: stored transposed
+// (see lane_a, lane_b); K: inner dimension.
+template <int K, bool TA, bool TB, Fill F = kFull, int MT, int NT, int CA, int PA, int LA, int CB, int PB, int LB>
+__device__ __forceinline__ void product(float (&acc)[MT][NT][4], Mat<CA, PA, LA> A, const int (&m)[MT],
+                                        Mat<CB, PB, LB> B, int n0, int lane) {
+    uint32_t la[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) la[i] = lane_a<CA, TA>(A.at, m[i], lane);
+    const uint32_t lb = lane_b<CB, TB>(B.at, lane);
 #pragma unroll
     for (int k = 0; k < K; k += 16) {
         uint32_t a[PA][MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             if ((F == kLower && k > m[i]) || (F == kUpper && k < m[i])) continue;
-#pragma unroll
-            for (int p = 0; p < PA; ++p) load_a<CA, TA>(a[p][i], A.at + p * A.lo, m[i], k, lane);
+            load_a<CA, TA, 0>(a[0][i], la[i], k);
+            if constexpr (PA == 2) load_a<CA, TA, LA>(a[1][i], la[i], k);
         }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
+            if (F != kFull && MT == 1 && ((F == kLower && k > m[0]) || (F == kUpper && k < m[0]))) continue;
             uint32_t b[PB][4];
-#pragma unroll
-            for (int p = 0; p < PB; ++p) load_b<CB, TB>(b[p], B.at + p * B.lo, n0 + 8 * j, k, lane);
+            load_b<CB, TB, 0>(b[0], lb, n0 + 8 * j, k);
+            if constexpr (PB == 2) load_b<CB, TB, LB>(b[1], lb, n0 + 8 * j, k);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 if ((F == kLower && k > m[i]) || (F == kUpper && k < m[i])) continue;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mma(acc[i][j + h], a[0][i], b[0][2 * h], b[0][2 * h + 1]);
-                    if constexpr (PB == 2) mma(acc[i][j + h], a[0][i], b[1][2 * h], b[1][2 * h + 1]);
-                    if constexpr (PA == 2) mma(acc[i][j + h], a[1][i], b[0][2 * h], b[0][2 * h + 1]);
+                for (int h = 0; h < 2; ++h) mma(acc[i][j + h], a[0][i], b[0][2 * h], b[0][2 * h + 1]);
+                if constexpr (PB == 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma(acc[i][j + h], a[0][i], b[1][2 * h], b[1][2 * h + 1]);
+                }
+                if constexpr (PA == 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma(acc[i][j + h], a[1][i], b[0][2 * h], b[0][2 * h + 1]);
                 }
             }
         }
@@ -107,16 +134,16 @@ __device__ __forceinline__ void clear(float (&acc)[MT][NT][4]) {
             for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 }
 
-// Calls f(value, row, column) for every accumulator element of this warp.
+// Calls f(i, j, h, row, column) for every pair acc[i][j][2 h], acc[i][j][2 h + 1] of this warp.
 template <int MT, int NT, class Fn>
-__device__ __forceinline__ void each(float (&acc)[MT][NT][4], const int (&m)[MT], int n0, int lane, Fn f) {
+__device__ __forceinline__ void pairs(const int (&m)[MT], int n0, int lane, Fn f) {
     const int g = lane >> 2, t = (lane & 3) * 2;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f(acc[i][j][e], m[i] + g + (e >> 1) * 8, n0 + 8 * j + t + (e & 1));
+            for (int j = 0; j < NT; ++j) f(i, j, h, m[i] + g + 8 * h, n0 + 8 * j + t);
 }
 
 // The scale of a set whose largest magnitude has the given fp32 bits: mul = 2^(9 - e), back = 1 / mul.
@@ -148,6 +175,10 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* x) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t x;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
@@ -158,32 +189,34 @@ __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& x, uint32_t& y) {
 }
 __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-// Writes this warp's accumulators, times mul, into planes of COLS columns.
-template <int COLS, int MT, int NT>
-__device__ __forceinline__ void write(Mat dst, const float (&acc)[MT][NT][4], const int (&m)[MT], int n0, int lane,
-                                      float mul) {
-    const int g = lane >> 2, t = (lane & 3) * 2;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t hi, lo;
-                split(acc[i][j][2 * h] * mul, acc[i][j][2 * h + 1] * mul, hi, lo);
-                const uint32_t at = dst.at + offset<COLS>(m[i] + g + 8 * h, n0 + 8 * j + t);
-                sts32(at, hi);
-                sts32(at + dst.lo, lo);
-            }
+// Address of the pair (i, j, h) of pairs() in a plane: n0 is a multiple of 8 NT.
+template <int COLS, int NT>
+__device__ __forceinline__ uint32_t pair_at(uint32_t base, int m, int n0, int j, int h, int lane) {
+    const int g = lane >> 2;
+    const uint32_t first = base + (m + g) * COLS * 2 + ((n0 * 2) ^ (g << 4)) + (lane & 3) * 4;
+    return (first ^ (16 * j)) + 8 * h * COLS * 2;
 }
 
-// The pair of elements (row, col), (row, col + 1) of a matrix of P planes, without its scale.
-template <int COLS, int P>
-__device__ __forceinline__ float2 read(Mat a, int row, int col) {
-    const uint32_t at = a.at + offset<COLS>(row, col);
+// Writes this warp's accumulators, times mul, into two planes.
+template <int COLS, int LO, int MT, int NT>
+__device__ __forceinline__ void write(Mat<COLS, 2, LO> dst, const float (&acc)[MT][NT][4], const int (&m)[MT], int n0,
+                                      int lane, float mul) {
+    pairs<MT, NT>(m, n0, lane, [&](int i, int j, int h, int, int) {
+        uint32_t hi, lo;
+        split(acc[i][j][2 * h] * mul, acc[i][j][2 * h + 1] * mul, hi, lo);
+        const uint32_t at = pair_at<COLS, NT>(dst.at, m[i], n0, j, h, lane);
+        sts32(at, hi);
+        sts32(at + LO, lo);
+    });
+}
+
+// The pair (i, j, h) of a matrix, without its scale.
+template <int NT, int COLS, int P, int LO>
+__device__ __forceinline__ float2 read(Mat<COLS, P, LO> a, int m, int n0, int j, int h, int lane) {
+    const uint32_t at = pair_at<COLS, NT>(a.at, m, n0, j, h, lane);
     float2 x = halves(lds32(at));
     if constexpr (P == 2) {
-        const float2 y = halves(lds32(at + a.lo));
+        const float2 y = halves(lds32(at + LO));
         x.x += y.x;
         x.y += y.y;
     }
@@ -200,6 +233,12 @@ __device__ __forceinline__ uint32_t max_bits(const float (&acc)[MT][NT][4]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) m = max(m, abs_bits(acc[i][j][e]));
     return __reduce_max_sync(0xffffffffu, m);
+}
+
+// The largest of W warps' maxima (W a power of two up to 32; a barrier lies between their writes and this).
+template <int W>
+__device__ __forceinline__ uint32_t top_of(const uint32_t* red, int lane) {
+    return __reduce_max_sync(0xffffffffu, red[lane & (W - 1)]);
 }
 
 }  // namespace planes
