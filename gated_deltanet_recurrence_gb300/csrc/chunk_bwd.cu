@@ -115,7 +115,7 @@ __device__ bool find_span(const ChunkBwdArgs& a, long slot, Span& s) {
 // Per (slot, head):
 //   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
 //   T      planes of T
-//   U      T diag(beta) V, then U (fp32 [64, d])        E   fp32 [64, d]
+//   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
 //   S      S0 (fp32 [d, d])                             dS  X, then dS1 (fp32 [d, d])
 //   meta   scales and maxima
 struct LinkTail {
@@ -125,7 +125,7 @@ struct LinkTail {
 static_assert(sizeof(LinkTail) == 512, "");
 
 struct Meta {
-    uint32_t s_max[8], ds_max[8], u_max[8];  // bits of the largest magnitude in 16 rows (of U: columns)
+    uint32_t s_max[8], ds_max[8], u_max[8];  // bits of the largest magnitude in 16 rows (of U^T too)
     float t_scale, pad[7];
 };
 static_assert(sizeof(Meta) == 128, "");
@@ -213,98 +213,150 @@ __device__ __forceinline__ void load4(const void* src, gdn_dtype dt, long i, flo
     else load_vec<4>(static_cast<const float*>(src) + i, x);
 }
 
-// A chunk of a token tensor [T, heads, D] as planes (one plane takes bf16 only, which it holds exactly),
-// each row with a power of two of its own; zeros past the sequence's end.  factor[r] takes row r of the
-// planes to x (norm false), or to scale * x / |x| (norm and use_l2) and scale * x (norm, not use_l2);
-// inv[r], if given, receives 1 / |x| (1 without).  Factors that a later product folds into the other
-// operand of a contraction must not differ much between rows: with use_l2 the norm sets their size;
-// without it all rows share the largest row's power of two (the block then synchronises on *top, which
-// must be zero).  NW warps take part, the calling thread's index is warp and lane.
-template <int NW, int D, int P, int LO>
-__device__ void load_rows(Mat<D, P, LO> dst, const void* src, gdn_dtype dt, long t0, int len, int heads, int h,
-                          float* factor, float* inv, bool norm, bool use_l2, float scale, uint32_t* top, int warp,
-                          int lane) {
-    constexpr int LPR = D / 4, RPP = 32 / LPR, N = kC / NW / RPP;  // lanes a row, rows a pass, passes
-    const int l = lane % LPR;
-    float x[N][4];
-    uint32_t big[N];
-    float ss[N];
+// A chunk of a token tensor [T, heads, D], four elements a lane and row: raw in registers between fetch
+// (which only loads) and put, so that the loads of several tensors are under way together.  With P = 1 the
+// tensor is bf16.  NW warps take part.
+template <int NW, int D, int P>
+struct Rows {
+    static constexpr int LPR = D / 4, RPP = 32 / LPR, N = kC / NW / RPP;  // lanes a row, rows a pass, passes
+    uint2 raw[P == 1 ? N : 1];
+    float x[P == 2 ? N : 1][4];
+
+    static __device__ __forceinline__ int row(int p, int warp, int lane) { return (p * NW + warp) * RPP + lane / LPR; }
+
+    __device__ __forceinline__ void fetch(const void* src, gdn_dtype dt, long t0, int len, int heads, int h, int warp,
+                                          int lane) {
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-        const int r = (p * NW + warp) * RPP + lane / LPR;
+        for (int p = 0; p < N; ++p) {
+            const int r = row(p, warp, lane);
+            const long at = ((t0 + r) * heads + h) * D + 4 * (lane % LPR);
+            if constexpr (P == 1) {
+                raw[p] = make_uint2(0u, 0u);
+                if (r < len) raw[p] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src) + at);
+            } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[p][e] = 0.f;
-        if (r < len) load4(src, dt, ((t0 + r) * heads + h) * D + 4 * l, x[p]);
+                for (int e = 0; e < 4; ++e) x[p][e] = 0.f;
+                if (r < len) load4(src, dt, at, x[p]);
+            }
+        }
     }
-    uint32_t all = 0;
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-        ss[p] = 0.f;
-        big[p] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            ss[p] = fmaf(x[p][e], x[p][e], ss[p]);
-            big[p] = max(big[p], planes::abs_bits(x[p][e]));
-        }
-        if (norm) {
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss[p] += __shfl_xor_sync(0xffffffffu, ss[p], o);
-        }
-        if constexpr (LPR == 32) {
-            big[p] = __reduce_max_sync(0xffffffffu, big[p]);
+
+    __device__ __forceinline__ void get(int p, float (&y)[4], uint32_t& top) const {
+        if constexpr (P == 1) {
+            y[0] = __uint_as_float(raw[p].x << 16);
+            y[1] = __uint_as_float(raw[p].x & 0xffff0000u);
+            y[2] = __uint_as_float(raw[p].y << 16);
+            y[3] = __uint_as_float(raw[p].y & 0xffff0000u);
+            const uint32_t u = raw[p].x & 0x7fff7fffu, v = raw[p].y & 0x7fff7fffu;
+            const __nv_bfloat162 m =
+                __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&v));
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+            top = max(w & 0xffff0000u, w << 16);
         } else {
+            top = 0;
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) big[p] = max(big[p], __shfl_xor_sync(0xffffffffu, big[p], o));
-        }
-        all = max(all, big[p]);
-    }
-    const bool common = norm && !use_l2;
-    if (common) {
-        atomicMax(top, all);
-        __syncthreads();
-        all = *top;
-    }
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-        const int r = (p * NW + warp) * RPP + lane / LPR;
-        const Scale s = planes::scale_of(common ? all : big[p]);
-        uint32_t hi[2], lo[2];
-        planes::split(x[p][0] * s.mul, x[p][1] * s.mul, hi[0], lo[0]);
-        planes::split(x[p][2] * s.mul, x[p][3] * s.mul, hi[1], lo[1]);
-        const uint32_t at = dst.at + planes::offset<D>(r, 4 * l);
-        planes::sts64(at, hi[0], hi[1]);
-        if constexpr (P == 2) planes::sts64(at + LO, lo[0], lo[1]);
-        if (l == 0) {
-            const float f = norm && use_l2 ? rsqrtf(ss[p] + kL2Eps) : 1.f;
-            factor[r] = (norm ? f * scale : 1.f) * s.back;
-            if (inv) inv[r] = f;
+            for (int e = 0; e < 4; ++e) {
+                y[e] = x[p][e];
+                top = max(top, planes::abs_bits(y[e]));
+            }
         }
     }
+
+    // As planes, each row with a power of two of its own (one plane holds bf16 exactly).  factor[r] takes
+    // row r of the planes to x (NORM false), or to scale * x / |x| (NORM, use_l2) and scale * x (NORM, not
+    // use_l2); inv[r], if given, receives 1 / |x| (1 without).  Factors that a later product folds into
+    // the other operand of a contraction must not differ much between rows: with use_l2 the norm sets
+    // their size; without it all rows share the largest row's power of two (the block then synchronises
+    // on *shared_top, which must be zero).
+    template <bool NORM, int LO>
+    __device__ __forceinline__ void put(Mat<D, P, LO> dst, float* factor, float* inv, bool use_l2, float scale,
+                                        uint32_t* shared_top, int warp, int lane) const {
+        uint32_t all = 0;
+        const bool common = NORM && !use_l2;
+        if (common) {
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                float y[4];
+                uint32_t top;
+                get(p, y, top);
+                all = max(all, top);
+            }
+            atomicMax(shared_top, all);
+            __syncthreads();
+            all = *shared_top;
+        }
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            const int r = row(p, warp, lane);
+            float y[4], ss = 0.f;
+            uint32_t top;
+            get(p, y, top);
+            if constexpr (NORM) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            }
+            if constexpr (LPR == 32) {
+                top = __reduce_max_sync(0xffffffffu, top);
+            } else {
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            const Scale s = planes::scale_of(common ? all : top);
+            const uint32_t at = dst.at + planes::offset<D>(r, 4 * (lane % LPR));
+            if constexpr (P == 1) {
+                const __half2 u = __floats2half2_rn(y[0] * s.mul, y[1] * s.mul);
+                const __half2 v = __floats2half2_rn(y[2] * s.mul, y[3] * s.mul);
+                planes::sts64(at, *reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+            } else {
+                uint32_t hi[2], lo[2];
+                planes::split(y[0] * s.mul, y[1] * s.mul, hi[0], lo[0]);
+                planes::split(y[2] * s.mul, y[3] * s.mul, hi[1], lo[1]);
+                planes::sts64(at, hi[0], hi[1]);
+                planes::sts64(at + LO, lo[0], lo[1]);
+            }
+            if (lane % LPR == 0) {
+                const float f = NORM && use_l2 ? rsqrtf(ss + kL2Eps) : 1.f;
+                factor[r] = (NORM ? f * scale : 1.f) * s.back;
+                if (inv) inv[r] = f;
+            }
+        }
+    }
+};
+
+// Asks for a stretch of global memory (a multiple of 16 bytes) to be brought into L2.
+__device__ __forceinline__ void prefetch(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // ---- prep ----------------------------------------------------------------------------------------
 
 constexpr int kPrepThreads = 256;
 
-// Index of (i, j) in a 64 x 64 fp32 matrix whose columns are XORed by the row: rows and columns are
-// both read without bank conflicts.
-__device__ __forceinline__ int at64(int i, int j) { return i * kC + (j ^ (i & 31)); }
+constexpr int kLd = kC + 4;  // row of a 64 x 64 fp32 matrix in shared memory (16-byte aligned rows)
 
-// X = (I + A)^-1 for strictly lower triangular A (both at64; X's upper triangle is scratch): the four
-// 16 x 16 diagonal blocks by substitution, a warp each and a column a lane, then twice the block below
-// two inverted neighbours, X21 = -X22 (A21 X11).
+// X = (I + A)^-1 for strictly lower triangular A (X's upper triangle is scratch): the four 16 x 16
+// diagonal blocks by substitution, a warp each and a column a lane, then twice the block below two
+// inverted neighbours, X21 = -X22 (A21 X11).
 __device__ void unit_lower_inverse(const float* A, float* X) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp < 4 && lane < 16) {
-        const int o = 16 * warp;
+    auto row4 = [](const float* p, int i, int j) { return *reinterpret_cast<const float4*>(p + i * kLd + j); };
+    if (warp < 4) {
+        const int o = 16 * warp, c = lane & 15;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float acc[2] = {i == lane ? 1.f : 0.f, 0.f};
+            float acc[2] = {i == c ? 1.f : 0.f, 0.f};
 #pragma unroll
-            for (int m = 0; m < i; ++m) acc[m & 1] = fmaf(-A[at64(o + i, o + m)], x[m], acc[m & 1]);
+            for (int m = 0; m < i; m += 4) {
+                const float4 v = row4(A, o + i, o + m);
+                const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4 && m + k < i; ++k) acc[k & 1] = fmaf(-r[k], x[m + k], acc[k & 1]);
+            }
             x[i] = acc[0] + acc[1];
-            if (i >= lane) X[at64(o + i, o + lane)] = x[i];
+            if (lane < 16) X[(o + i) * kLd + o + c] = x[i];  // zero above the diagonal
         }
     }
     __syncthreads();
@@ -313,11 +365,12 @@ __device__ void unit_lower_inverse(const float* A, float* X) {
         const int o = (e >> 8) * 32, r = (e >> 4) & 15, c = e & 15;
         float acc = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            const float x = X[at64(o + m, o + c)];
-            acc = fmaf(A[at64(o + 16 + r, o + m)], m >= c ? x : 0.f, acc);
+        for (int m = 0; m < 16; m += 4) {
+            const float4 v = row4(A, o + 16 + r, o + m);
+            const float* x = X + (o + m) * kLd + o + c;
+            acc = fmaf(v.x, x[0], fmaf(v.y, x[kLd], fmaf(v.z, x[2 * kLd], fmaf(v.w, x[3 * kLd], acc))));
         }
-        X[at64(o + r, o + 16 + c)] = acc;
+        X[(o + r) * kLd + o + 16 + c] = acc;
     }
     __syncthreads();
 #pragma unroll
@@ -325,40 +378,48 @@ __device__ void unit_lower_inverse(const float* A, float* X) {
         const int o = (e >> 8) * 32, r = (e >> 4) & 15, c = e & 15;
         float acc = 0.f;
 #pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            const float x = X[at64(o + 16 + r, o + 16 + m)];
-            acc = fmaf(m <= r ? -x : 0.f, X[at64(o + m, o + 16 + c)], acc);
+        for (int m = 0; m < 16; m += 4) {
+            const float4 v = row4(X, o + 16 + r, o + 16 + m);
+            const float* y = X + (o + m) * kLd + o + 16 + c;
+            acc = fmaf(v.x, y[0], fmaf(v.y, y[kLd], fmaf(v.z, y[2 * kLd], fmaf(v.w, y[3 * kLd], acc))));
         }
-        X[at64(o + 16 + r, o + c)] = acc;
+        X[(o + 16 + r) * kLd + o + c] = -acc;
     }
     __syncthreads();
-    {  // the pair of 32-blocks: a warp four rows, a lane a column
-        const int c = lane, r0 = 4 * warp;
-        float acc[4] = {};
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-            const float x = m >= c ? X[at64(m, c)] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = fmaf(A[at64(32 + r0 + i, m)], x, acc[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) X[at64(r0 + i, 32 + c)] = acc[i];
-    }
-    __syncthreads();
+    // the pair of 32-blocks: a warp four rows, a lane a column; scratch above X11's diagonal blocks is skipped
+    const int c = lane, r0 = 4 * warp;
     {
-        const int c = lane, r0 = 4 * warp;
         float acc[4] = {};
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-            const float y = X[at64(m, 32 + c)];
+#pragma unroll
+        for (int m = 0; m < 32; m += 4) {
+            const float* p = X + m * kLd + c;
+            const bool in = m >= 16 || c < 16;
+            const float x[4] = {in ? p[0] : 0.f, in ? p[kLd] : 0.f, in ? p[2 * kLd] : 0.f, in ? p[3 * kLd] : 0.f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = X[at64(32 + r0 + i, 32 + m)];
-                acc[i] = fmaf(m <= r0 + i ? -x : 0.f, y, acc[i]);
+                const float4 v = row4(A, 32 + r0 + i, m);
+                acc[i] = fmaf(v.x, x[0], fmaf(v.y, x[1], fmaf(v.z, x[2], fmaf(v.w, x[3], acc[i]))));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) X[at64(32 + r0 + i, c)] = acc[i];
+        for (int i = 0; i < 4; ++i) X[(r0 + i) * kLd + 32 + c] = acc[i];
+    }
+    __syncthreads();
+    {
+        float acc[4] = {};
+#pragma unroll
+        for (int m = 0; m < 32; m += 4) {
+            if (m >= 16 && r0 < 16) break;  // X22's scratch block
+            const float* p = X + m * kLd + 32 + c;
+            const float y[4] = {p[0], p[kLd], p[2 * kLd], p[3 * kLd]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = row4(X, 32 + r0 + i, 32 + m);
+                acc[i] = fmaf(v.x, y[0], fmaf(v.y, y[1], fmaf(v.z, y[2], fmaf(v.w, y[3], acc[i]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) X[(32 + r0 + i) * kLd + c] = -acc[i];
     }
     __syncthreads();
 }
@@ -394,11 +455,11 @@ __device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char
 }
 
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
-// factors, then P) and a 64 x d buffer (A and T in fp32, then W, then dY).  d = 128 in bf16 takes 96 KB,
+// factors, then P) and a 64 x d buffer (W, then dY); before them, over both, A and T in fp32.  d = 128 in bf16 takes 96 KB,
 // so two blocks share an SM and one works while the other waits at a barrier.
 template <int D, int P>
 struct PrepSmem {
-    static constexpr int plane = kC * D * 2, square = kC * kC * 2, fp32 = 2 * kC * kC * 4;
+    static constexpr int plane = kC * D * 2, square = kC * kC * 2, fp32 = 2 * kC * kLd * 4 - 2 * square;
     static constexpr int K = 0, V = P * plane, Q = 2 * P * plane, TX = 3 * P * plane, W = TX + 2 * square;
     static constexpr int bytes = W + (2 * plane > fp32 ? 2 * plane : fp32);
 };
@@ -421,7 +482,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     const Mat<D, P, PL> K{base + L::K}, V{base + L::V}, Q{base + L::Q}, Y{base + L::W};
     const Mat<D, 2, PL> Qp{base + L::V}, W{base + L::W};
     const Mat<kC, 2, SQ> TX{base + L::TX};
-    float *Af = reinterpret_cast<float*>(sm + L::W), *Tf = Af + kC * kC;
+    float *Af = reinterpret_cast<float*>(sm + L::TX), *Tf = Af + kC * kLd;
     unsigned char* link = w.link + unit * link_bytes(D, P);
     LinkTail& tail = *reinterpret_cast<LinkTail*>(link + (2 + P) * PL);
 
@@ -429,10 +490,19 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         if (tid < 2) tops[tid] = 0;
         __syncthreads();
     }
-    if (warp == 0) load_gates(a, t, t0, len, h, lane);
-    load_rows<NW>(K, a.k, a.qkv_dtype, t0, len, a.Hk, hk, fK, nullptr, true, a.use_l2, 1.f, &tops[0], warp, lane);
-    load_rows<NW>(Q, a.q, a.qkv_dtype, t0, len, a.Hk, hk, fQ, nullptr, true, a.use_l2, a.scale, &tops[1], warp, lane);
-    load_rows<NW>(V, a.v, a.qkv_dtype, t0, len, a.H, h, fV, nullptr, false, false, 1.f, nullptr, warp, lane);
+    {
+        Rows<NW, D, P> k, v, q;
+        k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
+        q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
+        v.fetch(a.v, a.qkv_dtype, t0, len, a.H, h, warp, lane);
+        if (lane < len - 8 * warp && lane < 8)
+            prefetch(static_cast<const char*>(a.dout) + ((t0 + 8 * warp + lane) * a.H + h) * D * (P == 1 || a.dout_dtype == GDN_BF16 ? 2 : 4),
+                     D * (P == 1 || a.dout_dtype == GDN_BF16 ? 2 : 4));
+        if (warp == NW - 1) load_gates(a, t, t0, len, h, lane);
+        k.template put<true>(K, fK, nullptr, a.use_l2, 1.f, &tops[0], warp, lane);
+        q.template put<true>(Q, fQ, nullptr, a.use_l2, a.scale, &tops[1], warp, lane);
+        v.template put<false>(V, fV, nullptr, false, 1.f, nullptr, warp, lane);
+    }
     __syncthreads();
 
     // Warps 2 x 4 over a 64-row result.  A warp's two row tiles are mw and 3 - mw, which gives both rows
@@ -448,8 +518,9 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         planes::pairs<2, 2>(m, nc, lane, [&](int i, int j, int hh, int r, int c) {
             const float f = t.beta[r] * fK[r];
             const float2 gr = t.G[r];
-            Af[at64(r, c)] = c < r ? kk[i][j][2 * hh] * (f * fK[c]) * decay(gr, t.G[c]) : 0.f;
-            Af[at64(r, c + 1)] = c + 1 < r ? kk[i][j][2 * hh + 1] * (f * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f;
+            *reinterpret_cast<float2*>(Af + r * kLd + c) =
+                make_float2(c < r ? kk[i][j][2 * hh] * (f * fK[c]) * decay(gr, t.G[c]) : 0.f,
+                            c + 1 < r ? kk[i][j][2 * hh + 1] * (f * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f);
         });
     }
     if (tid < kC) tail.c[tid] = decay(t.G[kC - 1], t.G[tid]) * fK[tid];
@@ -464,9 +535,11 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     {
         uint32_t m0 = 0, m1 = 0, m2 = 0;
 #pragma unroll
+        for (int i = 0; i < 16; i += 4) load_vec<4>(Tf + rr * kLd + rc + i, tr + i);
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int j = rc + i;
-            tr[i] = j <= rr ? Tf[at64(rr, j)] : 0.f;
+            tr[i] = j <= rr ? tr[i] : 0.f;
             const float x = tr[i] * t.beta[j];
             m0 = max(m0, planes::abs_bits(tr[i]));
             m1 = max(m1, planes::abs_bits(x * fV[j]));
@@ -495,8 +568,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     planes::clear(acc);
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, V, nd, lane);
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-        *reinterpret_cast<float2*>(w.U + (unit * kC + r) * D + c) =
-            make_float2(acc[i][j][2 * hh] * su.back, acc[i][j][2 * hh + 1] * su.back);
+        w.U[(unit * D + c) * kC + r] = acc[i][j][2 * hh] * su.back;
+        w.U[(unit * D + c + 1) * kC + r] = acc[i][j][2 * hh + 1] * su.back;
     });
     __syncthreads();
     {
@@ -547,7 +620,11 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         w.meta[unit].t_scale = st.back;
     }
     __syncthreads();  // W, V and Q have been read
-    load_rows<NW>(Y, a.dout, a.dout_dtype, t0, len, a.H, h, fY, nullptr, false, false, 1.f, nullptr, warp, lane);
+    {
+        Rows<NW, D, P> y;
+        y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
+        y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
+    }
     __syncthreads();
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
         acc[i][j][2 * hh] *= fY[r];
@@ -592,13 +669,25 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // N[j] += rows (16 x 16 KT, in the accumulator layout) times B from column n0: the rows' planes are made
-// here, scaled by mul (one power of two for each of this thread's two rows).
+// here, scaled by mul (one power of two for each of this thread's two rows).  One warp has an SM
+// sub-partition to itself: the blocks of B for the next step are loaded before this step's products, and
+// the terms of one accumulator lie NT products apart.
 template <bool TB, int KT, int NT, int CB, int PB, int LB>
 __device__ __forceinline__ void row_product(float (&N)[NT][4], const float (&rows)[2 * KT][4], const float (&mul)[2],
                                             Mat<CB, PB, LB> B, int n0, int lane) {
     const uint32_t lb = planes::lane_b<CB, TB>(B.at, lane);
+    uint32_t b[2][PB][NT / 2][4];
+    auto load = [&](uint32_t (&x)[PB][NT / 2][4], int k) {
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+            planes::load_b<CB, TB, 0>(x[0][j], lb, n0 + 16 * j, 16 * k);
+            if constexpr (PB == 2) planes::load_b<CB, TB, LB>(x[1][j], lb, n0 + 16 * j, 16 * k);
+        }
+    };
+    load(b[0], 0);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
+        if (k + 1 < KT) load(b[(k + 1) & 1], k + 1);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -606,18 +695,13 @@ __device__ __forceinline__ void row_product(float (&N)[NT][4], const float (&row
             planes::split(rows[2 * k + e][2] * mul[1], rows[2 * k + e][3] * mul[1], hi[2 * e + 1], lo[2 * e + 1]);
         }
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-            uint32_t b[PB][4];
-            planes::load_b<CB, TB, 0>(b[0], lb, n0 + 8 * j, 16 * k);
-            if constexpr (PB == 2) planes::load_b<CB, TB, LB>(b[1], lb, n0 + 8 * j, 16 * k);
+        for (int j = 0; j < NT; ++j) planes::mma(N[j], hi, b[k & 1][0][j / 2][2 * (j & 1)], b[k & 1][0][j / 2][2 * (j & 1) + 1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) planes::mma(N[j + h], hi, b[0][2 * h], b[0][2 * h + 1]);
+        for (int j = 0; j < NT; ++j) planes::mma(N[j], lo, b[k & 1][0][j / 2][2 * (j & 1)], b[k & 1][0][j / 2][2 * (j & 1) + 1]);
+        if constexpr (PB == 2) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) planes::mma(N[j + h], lo, b[0][2 * h], b[0][2 * h + 1]);
-            if constexpr (PB == 2) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) planes::mma(N[j + h], hi, b[1][2 * h], b[1][2 * h + 1]);
-            }
+            for (int j = 0; j < NT; ++j)
+                planes::mma(N[j], hi, b[k & 1][1][j / 2][2 * (j & 1)], b[k & 1][1][j / 2][2 * (j & 1) + 1]);
         }
     }
 }
@@ -671,13 +755,13 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
     for (int i = 0; i < s.chunks; ++i) {
         const long unit = unit_of(i);
         float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + col;
-        float* side = (BACK ? w.E : w.U) + (unit * kC + col) * D + row;  // [j][row]
+        float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + col;
         float z0[ZT][4];
         if constexpr (!BACK) {
 #pragma unroll
             for (int j = 0; j < ZT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z0[j][e] = side[(8 * j + (e & 1)) * D + 8 * (e >> 1)];
+                for (int hh = 0; hh < 2; ++hh) load_vec<2>(side + 8 * j + hh * 8 * kC, z0[j] + 2 * hh);
         }
         copy_wait<1>();
         __syncthreads();  // stage i is here, and every warp has left stage i - 1
@@ -702,20 +786,22 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
 #pragma unroll
         for (int j = 0; j < ZT; ++j) {
             const float2 c = *reinterpret_cast<const float2*>(tail.c + 8 * j + col);
+            float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float f = rs[e >> 1].back, cj = e & 1 ? c.y : c.x;
-                float x;
                 if constexpr (BACK) {
-                    x = Z[j][e] * f * cj;
-                    Z[j][e] = -x;
+                    x[e] = Z[j][e] * f * cj;
+                    Z[j][e] = -x[e];
                 } else {
-                    x = z0[j][e] - Z[j][e] * (f * w_scale);
-                    Z[j][e] = x * cj;
-                    u_top = max(u_top, planes::abs_bits(x));
+                    x[e] = z0[j][e] - Z[j][e] * (f * w_scale);
+                    Z[j][e] = x[e] * cj;
+                    u_top = max(u_top, planes::abs_bits(x[e]));
                 }
-                side[(8 * j + (e & 1)) * D + 8 * (e >> 1)] = x;
             }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+                *reinterpret_cast<float2*>(side + 8 * j + hh * 8 * kC) = make_float2(x[2 * hh], x[2 * hh + 1]);
         }
         if constexpr (!BACK) {
             u_top = __reduce_max_sync(0xffffffffu, u_top);
@@ -792,37 +878,45 @@ struct GradSmem {
     static constexpr int WM = D / 32, threads = WM * 128;
 };
 
-// An fp32 matrix of ROWS x D as planes with the given scale.  DOT: returns also this thread's part of
-// the dot product with what the planes held before, without its scale.
-template <int T, int ROWS, int D, bool DOT, int LO>
-__device__ float load_planes(Mat<D, 2, LO> dst, const float* src, float mul) {
-    constexpr int N = ROWS * D / 4 / T;
-    float dot = 0.f, x[N][4];
+// An fp32 matrix of ROWS x COLS, raw in registers between fetch and put.  put writes its planes with the
+// given scale; with DOT it returns this thread's part of the dot product with what the planes held before,
+// without its scale.
+template <int T, int ROWS, int COLS>
+struct Flat {
+    static constexpr int N = ROWS * COLS / 4 / T;
+    float x[N][4];
+
+    __device__ __forceinline__ void fetch(const float* src) {
 #pragma unroll
-    for (int p = 0; p < N; ++p) load_vec<4>(src + (p * T + threadIdx.x) * 4, x[p]);
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-        const int e = (p * T + threadIdx.x) * 4;
-        const uint32_t at = dst.at + planes::offset<D>(e / D, e % D);
-        if constexpr (DOT) {
-            uint32_t u[2], v[2];
-            planes::lds64(at, u[0], u[1]);
-            planes::lds64(at + LO, v[0], v[1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 hi = planes::halves(u[i]), lo = planes::halves(v[i]);
-                dot = fmaf(hi.x + lo.x, x[p][2 * i], dot);
-                dot = fmaf(hi.y + lo.y, x[p][2 * i + 1], dot);
-            }
-        }
-        uint32_t hi[2], lo[2];
-        planes::split(x[p][0] * mul, x[p][1] * mul, hi[0], lo[0]);
-        planes::split(x[p][2] * mul, x[p][3] * mul, hi[1], lo[1]);
-        planes::sts64(at, hi[0], hi[1]);
-        planes::sts64(at + LO, lo[0], lo[1]);
+        for (int p = 0; p < N; ++p) load_vec<4>(src + (p * T + threadIdx.x) * 4, x[p]);
     }
-    return dot;
-}
+    template <bool DOT, int LO>
+    __device__ __forceinline__ float put(Mat<COLS, 2, LO> dst, float mul) const {
+        float dot = 0.f;
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            const int e = (p * T + threadIdx.x) * 4;
+            const uint32_t at = dst.at + planes::offset<COLS>(e / COLS, e % COLS);
+            if constexpr (DOT) {
+                uint32_t u[2], v[2];
+                planes::lds64(at, u[0], u[1]);
+                planes::lds64(at + LO, v[0], v[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 hi = planes::halves(u[i]), lo = planes::halves(v[i]);
+                    dot = fmaf(hi.x + lo.x, x[p][2 * i], dot);
+                    dot = fmaf(hi.y + lo.y, x[p][2 * i + 1], dot);
+                }
+            }
+            uint32_t hi[2], lo[2];
+            planes::split(x[p][0] * mul, x[p][1] * mul, hi[0], lo[0]);
+            planes::split(x[p][2] * mul, x[p][3] * mul, hi[1], lo[1]);
+            planes::sts64(at, hi[0], hi[1]);
+            planes::sts64(at + LO, lo[0], lo[1]);
+        }
+        return dot;
+    }
+};
 
 // A pair of elements of a q/k/v-like tensor.
 __device__ __forceinline__ float2 load2(const void* src, gdn_dtype dt, long i) {
@@ -858,6 +952,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const Mat<D, 2, L::state> ST{base + L::ST};
     const Mat<kC, 2, SQ> Pm{base + L::Pm}, Tm{base + L::Tm}, Sq1{base + L::B1}, Sq2{base + L::B2};
     const Mat<D, 2, PL> B1{base + L::B1}, B2{base + L::B2};
+    const Mat<kC, 2, PL> UT{base + L::B1};  // U^T
     // Warps WM x 4.  With two row tiles a warp's are mw and 3 - mw; with one, the four warps of an SM
     // sub-partition (warp mod 4) are the four row tiles of a column block: either way the shares of a
     // triangular product are even.
@@ -868,39 +963,55 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     constexpr int NT = D / 32;
     const int nd = nw * (D / 4), nc = nw * 16;
     const Meta& meta = w.meta[unit];
-
-    Scale ss, sds, su;
-    {
-        const int i = lane & (D / 16 - 1);
-        ss = planes::scale_of(__reduce_max_sync(0xffffffffu, meta.s_max[i]));
-        sds = planes::scale_of(__reduce_max_sync(0xffffffffu, meta.ds_max[i]));
-        su = planes::scale_of(__reduce_max_sync(0xffffffffu, meta.u_max[i]));
+    const float* S0 = w.S + unit * D * D;
+    const float* dS1 = w.dS + unit * D * D;
+    if (tid == 0) {
+        prefetch(S0, D * D * 4);
+        prefetch(w.E + unit * kC * D, kC * D * 4);
+        prefetch(w.U + unit * kC * D, kC * D * 4);
+        prefetch(dS1, D * D * 4);
     }
-    const float t_back = meta.t_scale;
+    Flat<T, D, D> state;
+    Scale ss, sds, su;
     if (!a.use_l2) {
         if (tid < 2) tops[tid] = 0;
         __syncthreads();
     }
-    if (warp == 0) load_gates(a, t, t0, len, h, lane);
-    load_rows<NW>(K, a.k, a.qkv_dtype, t0, len, a.Hk, hk, fK, kinv, true, a.use_l2, 1.f, &tops[0], warp, lane);
-    load_rows<NW>(Q, a.q, a.qkv_dtype, t0, len, a.Hk, hk, fQ, qinv, true, a.use_l2, a.scale, &tops[1], warp, lane);
-    if constexpr (!L::share)
-        load_rows<NW>(Y, a.dout, a.dout_dtype, t0, len, a.H, h, fY, nullptr, false, false, 1.f, nullptr, warp, lane);
     {
+        Rows<NW, D, P> k, q, y;
+        uint4 tt[kTBytes / 16 / T];
+        k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
+        q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
+        if constexpr (!L::share) y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
         const uint4* src = reinterpret_cast<const uint4*>(w.T + unit * kTBytes);
+#pragma unroll
+        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) tt[i] = src[i * T + tid];
+        const int i16 = lane & (D / 16 - 1);
+        const uint32_t top[3] = {meta.s_max[i16], meta.ds_max[i16], meta.u_max[i16]};
+        if (warp == NW - 1) load_gates(a, t, t0, len, h, lane);
+        k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
+        q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
+        if constexpr (!L::share) y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
         uint4* dst = reinterpret_cast<uint4*>(sm + L::Tm);
 #pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) dst[i * T + tid] = src[i * T + tid];
+        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) dst[i * T + tid] = tt[i];
+        ss = planes::scale_of(__reduce_max_sync(0xffffffffu, top[0]));
+        sds = planes::scale_of(__reduce_max_sync(0xffffffffu, top[1]));
+        su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
+    const float t_back = meta.t_scale;
     __syncthreads();
 
     {
         float qk[MT][2][4];  // P, with the rows' factors of dY for P^T dY
+        if constexpr (!L::share) state.fetch(S0);
         planes::clear(qk);
         planes::product<D, false, false>(qk, Q, m, K, nc, lane);
         if constexpr (L::share) {
+            Rows<NW, D, P> y;
+            y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
             __syncthreads();
-            load_rows<NW>(Y, a.dout, a.dout_dtype, t0, len, a.H, h, fY, nullptr, false, false, 1.f, nullptr, warp, lane);
+            y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
             __syncthreads();
         }
         planes::pairs<MT, 2>(m, nc, lane, [&](int i, int j, int hh, int r, int c) {
@@ -918,11 +1029,13 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         __syncthreads();
         const Scale sp = planes::scale_of(planes::top_of<NW>(red[0], lane));
         planes::write(Pm, qk, m, nc, lane, sp.mul);
+        if constexpr (L::share) state.fetch(S0);
         float2 e0[MT][NT][2];
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-            e0[i][j][hh] = *reinterpret_cast<const float2*>(w.E + (unit * kC + r) * D + c);
+            const float* e = w.E + (unit * D + c) * kC + r;
+            e0[i][j][hh] = make_float2(e[0], e[kC]);
         });
-        load_planes<T, D, D, false>(ST, w.S + unit * D * D, ss.mul);
+        state.template put<false>(ST, ss.mul);
         __syncthreads();
         float acc[MT][NT][4];  // P^T dY + E
         planes::clear(acc);
@@ -945,6 +1058,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
             v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
         });
+        Flat<T, D, kC> u;
+        u.fetch(w.U + unit * kC * D);
         float dR[MT][NT][4];
         planes::clear(dR);
         planes::product<kC, true, true, planes::kUpper>(dR, Tm, m, B1, nd, lane);
@@ -960,7 +1075,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         __syncthreads();  // also: B1 has been read
         sr = planes::scale_of(planes::top_of<NW>(red[0], lane));
         planes::write(B2, dR, m, nd, lane, sr.mul);
-        load_planes<T, kC, D, false>(B1, w.U + unit * kC * D, su.mul);
+        u.template put<false>(UT, su.mul);
     }
     __syncthreads();
 
@@ -977,10 +1092,11 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             F[i][j][e] *= ff;
         }
     });
+    state.fetch(dS1);
     planes::clear(dP);
-    planes::product<D, false, false>(dP, Y, m, B1, nc, lane);
+    planes::product<D, false, true>(dP, Y, m, UT, nc, lane);
     planes::clear(Z);
-    planes::product<D, false, false>(Z, B2, m, B1, nc, lane);
+    planes::product<D, false, true>(Z, B2, m, UT, nc, lane);
     // dP and Z are wanted twice: with the factors of K's rows on the columns (for the products with K)
     // and with the factors of the left rows (for the transposed products)
     uint32_t tp[4] = {0, 0, 0, 0};
@@ -1004,7 +1120,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         }
     });
     __syncthreads();  // B2, ST, P, T and dY have been read (B1 not yet by H)
-    const float state_dot = load_planes<T, D, D, true>(ST, w.dS + unit * D * D, sds.mul);  // and <S0, dS1>
+    const float state_dot = state.template put<true>(ST, sds.mul);  // and <S0, dS1>
     // dP and Z's planes go where P and T were, and the warps' four maxima and state dots where dY's row
     // factors and the maxima of dR were
     static_assert(4 * NW <= kC, "");
@@ -1019,8 +1135,11 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         const float x = warp_sum(state_dot);
         if (lane == 0) dots[warp] = x;
     }
-    if constexpr (L::share)
-        load_rows<NW>(Q, a.q, a.qkv_dtype, t0, len, a.Hk, hk, fQ, qinv, true, a.use_l2, a.scale, &tops[1], warp, lane);
+    if constexpr (L::share) {
+        Rows<NW, D, P> q;
+        q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
+        q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
+    }
     __syncthreads();
     Scale sc[4];
 #pragma unroll
@@ -1042,7 +1161,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     put(Sq2, dP, sc[1].mul, false, fQ, nullptr);
     float H[MT][NT][4];
     planes::clear(H);
-    planes::product<D, false, true>(H, B1, m, ST, nd, lane);
+    planes::product<D, true, true>(H, UT, m, ST, nd, lane);
     planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
         const float f = decay(t.G[kC - 1], t.G[r]) * su.back * sds.back;
         H[i][j][2 * hh] *= f;
