@@ -125,10 +125,10 @@ struct LinkTail {
 static_assert(sizeof(LinkTail) == 512, "");
 
 struct Meta {
-    uint32_t s_max[8], ds_max[8], u_max[8];  // bits of the largest magnitude in 16 rows (of U^T too)
-    float t_scale, pad[7];
+    uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
+    float t_scale, pad[15];
 };
-static_assert(sizeof(Meta) == 128, "");
+static_assert(sizeof(Meta) == 256, "");
 
 constexpr size_t kTBytes = 2 * kC * kC * sizeof(__half);
 __host__ __device__ constexpr size_t link_bytes(int d, int p) {
@@ -651,13 +651,19 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 }
 
 // ---- scan ----------------------------------------------------------------------------------------
-// A warp keeps 16 rows of the state in its accumulators for the whole sequence: an accumulator's layout
-// is the left operand's layout of the next product, so the rows never pass through shared memory, and
-// rows do not depend on one another.  Per chunk, forwards: U^T = (T diag(beta) V)^T - S W^T, then
-// S <- b_C S + U^T Kd; backwards: E^T = dS Kd^T, then dS <- b_C dS + X - E^T W.  The chunks' links arrive
-// by asynchronous copies, three stages.
+// Two warps keep 16 rows of the state in their accumulators for the whole sequence, half the columns each:
+// an accumulator's layout is the left operand's layout of the next product, so the state never passes
+// through shared memory, and rows do not depend on one another.  Per chunk, forwards:
+// U^T = (T diag(beta) V)^T - S W^T, then S <- b_C S + U^T Kd; backwards: E^T = dS Kd^T, then
+// dS <- b_C dS + X - E^T W.  The first product is split over the inner dimension, each warp taking its own
+// columns of the state, and the two parts meet through shared memory; both warps then hold the whole of
+// U^T or E^T (16 x 64) and take the second product for their own columns.  The chunks' links arrive by
+// asynchronous copies.  (One warp for 16 rows: 6.8k cycles a chunk at d = 128, at four cycles an
+// instruction of the only warp of an SM sub-partition.)
 
-constexpr int kScanThreads = 128, kStages = 3;
+constexpr int kScanThreads = 256;
+constexpr int scan_stages(int d, int p) { return d == 128 && p == 2 ? 2 : 3; }
+constexpr int scan_bytes(int d, int p) { return scan_stages(d, p) * (int)link_bytes(d, p) + 8 * 16 * kC * 4; }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -668,20 +674,20 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// N[j] += rows (16 x 16 KT, in the accumulator layout) times B from column n0: the rows' planes are made
-// here, scaled by mul (one power of two for each of this thread's two rows).  One warp has an SM
-// sub-partition to itself: the blocks of B for the next step are loaded before this step's products, and
-// the terms of one accumulator lie NT products apart.
+// N[j] += rows (16 x 16 KT, in the accumulator layout) times B from column n0 and inner index k0: the
+// rows' planes are made here, scaled by mul (one power of two for each of this thread's two rows).  An SM
+// sub-partition has two warps only: the blocks of B for the next step are loaded before this step's
+// products, and the terms of one accumulator lie NT products apart.
 template <bool TB, int KT, int NT, int CB, int PB, int LB>
 __device__ __forceinline__ void row_product(float (&N)[NT][4], const float (&rows)[2 * KT][4], const float (&mul)[2],
-                                            Mat<CB, PB, LB> B, int n0, int lane) {
+                                            Mat<CB, PB, LB> B, int n0, int k0, int lane) {
     const uint32_t lb = planes::lane_b<CB, TB>(B.at, lane);
     uint32_t b[2][PB][NT / 2][4];
     auto load = [&](uint32_t (&x)[PB][NT / 2][4], int k) {
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
-            planes::load_b<CB, TB, 0>(x[0][j], lb, n0 + 16 * j, 16 * k);
-            if constexpr (PB == 2) planes::load_b<CB, TB, LB>(x[1][j], lb, n0 + 16 * j, 16 * k);
+            planes::load_b<CB, TB, 0>(x[0][j], lb, n0 + 16 * j, k0 + 16 * k);
+            if constexpr (PB == 2) planes::load_b<CB, TB, LB>(x[1][j], lb, n0 + 16 * j, k0 + 16 * k);
         }
     };
     load(b[0], 0);
@@ -725,128 +731,143 @@ __device__ __forceinline__ uint32_t row_scales(const float (&x)[NT][4], Scale (&
 }
 
 template <int D, int P, bool BACK>
-__device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const Span& s, int h, int r0,
+__device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const Span& s, int h, int slice,
                                      unsigned char* sm) {
-    constexpr int NT = D / 8, ZT = kC / 8, PL = kC * D * 2, LINK = (int)link_bytes(D, P);
-    const int lane = threadIdx.x & 31, row = r0 + (lane >> 2), col = (lane & 3) * 2;
+    constexpr int NT = D / 16, ZT = kC / 8, PL = kC * D * 2, LINK = (int)link_bytes(D, P), ST = scan_stages(D, P);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp & 3, half = warp >> 2;
+    const int block = slice * 4 + pair, row = block * 16 + (lane >> 2), c2 = (lane & 3) * 2, n0 = half * (D / 2);
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
-    const long state = ((long)s.n * a.H + h) * D * D + row * D + col;
+    float4* mine = reinterpret_cast<float4*>(sm + ST * LINK) + (warp * ZT) * 32 + lane;  // part of Z, [ZT][32]
+    const float4* other = reinterpret_cast<const float4*>(sm + ST * LINK) + ((warp ^ 4) * ZT) * 32 + lane;
+    const long state = ((long)s.n * a.H + h) * D * D + row * D + n0 + c2;
     const float* from = BACK ? a.dfinal_state : a.initial_state;
     auto unit_of = [&](int i) { return (s.base + (BACK ? s.chunks - 1 - i : i)) * a.H + h; };
     auto fetch = [&](int i) {
         if (i < s.chunks) {
             const unsigned char* src = w.link + unit_of(i) * LINK;
-            const uint32_t dst = smem + (i % kStages) * LINK;
+            const uint32_t dst = smem + (i % ST) * LINK;
             for (int o = threadIdx.x * 16; o < LINK; o += kScanThreads * 16) copy16(dst + o, src + o);
         }
         copy_commit();
     };
-    fetch(0);
-    fetch(1);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(i);
     float S[NT][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const float2 x = from ? *reinterpret_cast<const float2*>(from + state + 8 * j) : make_float2(0.f, 0.f);
-        const float2 y = from ? *reinterpret_cast<const float2*>(from + state + 8 * D + 8 * j) : make_float2(0.f, 0.f);
-        S[j][0] = x.x; S[j][1] = x.y; S[j][2] = y.x; S[j][3] = y.y;
-    }
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const float2 x = from ? *reinterpret_cast<const float2*>(from + state + hh * 8 * D + 8 * j) : make_float2(0.f, 0.f);
+            S[j][2 * hh] = x.x;
+            S[j][2 * hh + 1] = x.y;
+        }
     // what follows the last chunk is wanted only as the gradient of the initial state
     const int steps = BACK && a.dinitial_state ? s.chunks : s.chunks - 1;
+    // X of a chunk (backwards), or (T diag(beta) V)^T (forwards): loaded while the chunk before is worked on
+    float x[BACK ? NT : ZT][4];
+    auto load_x = [&](int i) {
+        if (i >= s.chunks) return;
+        const float* p = BACK ? w.dS + unit_of(i) * D * D + row * D + n0 + c2 : w.U + (unit_of(i) * D + row) * kC + c2;
+#pragma unroll
+        for (int j = 0; j < (BACK ? NT : ZT); ++j)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) load_vec<2>(p + hh * 8 * (BACK ? D : kC) + 8 * j, x[j] + 2 * hh);
+    };
+    load_x(0);
     for (int i = 0; i < s.chunks; ++i) {
         const long unit = unit_of(i);
-        float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + col;
-        float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + col;
-        float z0[ZT][4];
-        if constexpr (!BACK) {
-#pragma unroll
-            for (int j = 0; j < ZT; ++j)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) load_vec<2>(side + 8 * j + hh * 8 * kC, z0[j] + 2 * hh);
-        }
-        copy_wait<1>();
+        float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + n0 + c2;
+        float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + c2;
+        copy_wait<ST - 2>();
         __syncthreads();  // stage i is here, and every warp has left stage i - 1
-        fetch(i + 2);
-        const uint32_t at = smem + (i % kStages) * LINK;
-        const LinkTail& tail = *reinterpret_cast<const LinkTail*>(sm + (i % kStages) * LINK + (2 + P) * PL);
+        fetch(i + ST - 1);
+        const uint32_t at = smem + (i % ST) * LINK;
+        const LinkTail& tail = *reinterpret_cast<const LinkTail*>(sm + (i % ST) * LINK + (2 + P) * PL);
         const Mat<D, 2, PL> W{at};
         const Mat<D, P, PL> K{at + 2 * PL};
-        const float w_scale = tail.w_scale, b_last = tail.b_last;
         Scale rs[2], zs[2];
         const uint32_t top = row_scales(S, rs);
-        if (lane == 0) (BACK ? w.meta[unit].ds_max : w.meta[unit].s_max)[r0 / 16] = top;
+        if (lane == 0) (BACK ? w.meta[unit].ds_max : w.meta[unit].s_max)[block * 2 + half] = top;
         const float mul[2] = {rs[0].mul, rs[1].mul};
         float Z[ZT][4];
 #pragma unroll
         for (int j = 0; j < ZT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) Z[j][e] = 0.f;
-        if constexpr (BACK) row_product<false, NT / 2>(Z, S, mul, K, 0, lane);
-        else row_product<false, NT / 2>(Z, S, mul, W, 0, lane);
+        if constexpr (BACK) row_product<false, NT / 2>(Z, S, mul, K, 0, n0, lane);
+        else row_product<false, NT / 2>(Z, S, mul, W, 0, n0, lane);
+        const float zf = BACK ? 1.f : tail.w_scale, f[2] = {rs[0].back * zf, rs[1].back * zf};
+#pragma unroll
+        for (int j = 0; j < ZT; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Z[j][e] *= f[e >> 1];
+            mine[j * 32] = make_float4(Z[j][0], Z[j][1], Z[j][2], Z[j][3]);
+        }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
         uint32_t u_top = 0;
 #pragma unroll
         for (int j = 0; j < ZT; ++j) {
-            const float2 c = *reinterpret_cast<const float2*>(tail.c + 8 * j + col);
-            float x[4];
+            const float4 o = other[j * 32];
+            const float2 c = *reinterpret_cast<const float2*>(tail.c + 8 * j + c2);
+            const float y[4] = {o.x, o.y, o.z, o.w};
+            float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float f = rs[e >> 1].back, cj = e & 1 ? c.y : c.x;
+                const float cj = e & 1 ? c.y : c.x;
                 if constexpr (BACK) {
-                    x[e] = Z[j][e] * f * cj;
-                    Z[j][e] = -x[e];
+                    v[e] = (Z[j][e] + y[e]) * cj;
+                    Z[j][e] = -v[e];
                 } else {
-                    x[e] = z0[j][e] - Z[j][e] * (f * w_scale);
-                    Z[j][e] = x[e] * cj;
-                    u_top = max(u_top, planes::abs_bits(x[e]));
+                    v[e] = x[j][e] - (Z[j][e] + y[e]);
+                    Z[j][e] = v[e] * cj;
+                    u_top = max(u_top, planes::abs_bits(v[e]));
                 }
             }
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-                *reinterpret_cast<float2*>(side + 8 * j + hh * 8 * kC) = make_float2(x[2 * hh], x[2 * hh + 1]);
-        }
-        if constexpr (!BACK) {
-            u_top = __reduce_max_sync(0xffffffffu, u_top);
-            if (lane == 0) w.meta[unit].u_max[r0 / 16] = u_top;
-        }
-        row_scales(Z, zs);
-        const float zmul[2] = {zs[0].mul, zs[1].mul};
-        const float zb[2] = {zs[0].back * (BACK ? w_scale : 1.f), zs[1].back * (BACK ? w_scale : 1.f)};
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-            float N[8][4], x[8][4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const float2 y = BACK ? *reinterpret_cast<const float2*>(kept + 64 * half + 8 * j + hh * 8 * D)
-                                          : make_float2(0.f, 0.f);
-                    x[j][2 * hh] = y.x;
-                    x[j][2 * hh + 1] = y.y;
-                    N[j][2 * hh] = N[j][2 * hh + 1] = 0.f;
-                }
-            if (i < steps) {
-                if constexpr (BACK) row_product<true, 4>(N, Z, zmul, W, 64 * half, lane);
-                else row_product<true, 4>(N, Z, zmul, K, 64 * half, lane);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float* S4 = S[8 * half + j];
+            if ((j < ZT / 2) == (half == 0)) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
-                    *reinterpret_cast<float2*>(kept + 64 * half + 8 * j + hh * 8 * D) =
-                        make_float2(S4[2 * hh], S4[2 * hh + 1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S4[e] = fmaf(N[j][e], zb[e >> 1], fmaf(b_last, S4[e], x[j][e]));
+                    *reinterpret_cast<float2*>(side + hh * 8 * kC + 8 * j) = make_float2(v[2 * hh], v[2 * hh + 1]);
             }
         }
+        if constexpr (!BACK) {
+            load_x(i + 1);
+            u_top = __reduce_max_sync(0xffffffffu, u_top);
+            if (lane == 0) w.meta[unit].u_max[block * 2 + half] = u_top;
+        }
+        float N[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) N[j][e] = 0.f;
+        float zb[2] = {0.f, 0.f};
+        if (i < steps) {
+            row_scales(Z, zs);
+            const float zmul[2] = {zs[0].mul, zs[1].mul}, nf = BACK ? tail.w_scale : 1.f;
+            zb[0] = zs[0].back * nf;
+            zb[1] = zs[1].back * nf;
+            if constexpr (BACK) row_product<true, ZT / 2>(N, Z, zmul, W, n0, 0, lane);
+            else row_product<true, ZT / 2>(N, Z, zmul, K, n0, 0, lane);
+        }
+        const float b_last = tail.b_last;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+                *reinterpret_cast<float2*>(kept + hh * 8 * D + 8 * j) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[j][e] = fmaf(N[j][e], zb[e >> 1], BACK ? fmaf(b_last, S[j][e], x[j][e]) : b_last * S[j][e]);
+        }
+        if constexpr (BACK) load_x(i + 1);
     }
     copy_wait<0>();
     if (BACK && a.dinitial_state) {
-        float* out = a.dinitial_state + state;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            *reinterpret_cast<float2*>(out + 8 * j) = make_float2(S[j][0], S[j][1]);
-            *reinterpret_cast<float2*>(out + 8 * D + 8 * j) = make_float2(S[j][2], S[j][3]);
-        }
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+                *reinterpret_cast<float2*>(a.dinitial_state + state + hh * 8 * D + 8 * j) =
+                    make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
     }
 }
 
@@ -856,11 +877,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
     constexpr int slices = D / 64;
     Span s;
     if (!find_span(a, -1, s)) return;
-    const int pair = blockIdx.x / slices;
-    s = seq_span(a, pair / a.H);
-    const int r0 = (blockIdx.x % slices) * 64 + (threadIdx.x >> 5) * 16;
-    if (blockIdx.y) scan<D, P, true>(a, w, s, pair % a.H, r0, sm);
-    else scan<D, P, false>(a, w, s, pair % a.H, r0, sm);
+    const int unit = blockIdx.x / slices, slice = blockIdx.x % slices;
+    s = seq_span(a, unit / a.H);
+    if (blockIdx.y) scan<D, P, true>(a, w, s, unit % a.H, slice, sm);
+    else scan<D, P, false>(a, w, s, unit % a.H, slice, sm);
 }
 
 // ---- grad ----------------------------------------------------------------------------------------
@@ -986,8 +1006,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         const uint4* src = reinterpret_cast<const uint4*>(w.T + unit * kTBytes);
 #pragma unroll
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) tt[i] = src[i * T + tid];
-        const int i16 = lane & (D / 16 - 1);
-        const uint32_t top[3] = {meta.s_max[i16], meta.ds_max[i16], meta.u_max[i16]};
+        const int part = lane & (D / 8 - 1);  // one of the scan's warps
+        const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
         if (warp == NW - 1) load_gates(a, t, t0, len, h, lane);
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
@@ -1313,7 +1333,7 @@ template <int D, int P>
 cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
     const size_t units = (size_t)slot_count(a.num_seqs, a.total_T) * a.H;
     const Work w = work_of(a.workspace, units, (size_t)a.total_T * a.H, D, P);
-    const int prep = PrepSmem<D, P>::bytes, grad = GradSmem<D, P>::bytes, scan = kStages * (int)link_bytes(D, P);
+    const int prep = PrepSmem<D, P>::bytes, grad = GradSmem<D, P>::bytes, scan = scan_bytes(D, P);
     auto allow = [](const void* f, int bytes) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         return e != cudaSuccess ? e : cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
