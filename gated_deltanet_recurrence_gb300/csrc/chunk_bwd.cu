@@ -32,6 +32,7 @@
 // between the products is fp32.
 #include "gdn_internal.cuh"
 #include "mma_planes.cuh"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -72,43 +73,52 @@ __device__ __forceinline__ Span seq_span(const ChunkBwdArgs& a, int n) {
     return s;
 }
 
-// Whether cu_seqlens is monotone and inside [0, total_T]; with a slot (>= 0) also finds its span, whose
-// n is -1 for an unused slot.  All threads take part; contains a block barrier.
-__device__ bool find_span(const ChunkBwdArgs& a, long slot, Span& s) {
-    __shared__ int found;
+// Whether cu_seqlens is monotone and inside [0, total_T]; finds the spans of N slots, whose n is -1 for an
+// unused slot.  All threads take part; contains block barriers.
+template <int N>
+__device__ bool find_spans(const ChunkBwdArgs& a, const long (&slot)[N], Span (&s)[N]) {
+    __shared__ int found[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k].n = -1;
     if (!a.cu_seqlens) {
-        if (slot >= 0) {
-            const long per = ((long)(a.total_T / a.num_seqs) + kC - 1) / kC;
-            const long n = per > 0 ? slot / per : a.num_seqs;
-            s.n = -1;
-            if (n < a.num_seqs) {
-                s = seq_span(a, (int)n);
-                s.c = (int)(slot - s.base);
+        const long per = ((long)(a.total_T / a.num_seqs) + kC - 1) / kC;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (slot[k] >= 0 && per > 0 && slot[k] < per * a.num_seqs) {
+                s[k] = seq_span(a, (int)(slot[k] / per));
+                s[k].c = (int)(slot[k] - s[k].base);
             }
-        }
         return true;
     }
-    if (threadIdx.x == 0) found = -1;
+    if (threadIdx.x < N) found[threadIdx.x] = -1;
     __syncthreads();
     bool bad = false;
     for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x) {
         const int lo = a.cu_seqlens[i], hi = a.cu_seqlens[i + 1];
         bad |= lo < 0 || hi < lo || hi > a.total_T;
-        const long c = slot - (lo / kC + i);
-        if (c >= 0 && c * kC < (long)hi - lo) found = i;  // at most one i where no entry is bad
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const long c = slot[k] - (lo / kC + i);
+            if (c >= 0 && c * kC < (long)hi - lo) found[k] = i;  // at most one i where no entry is bad
+        }
     }
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) record_error(a.err, GDN_ERR_CU_SEQLENS);
         return false;
     }
-    if (slot >= 0) {
-        s.n = -1;
-        if (found >= 0) {
-            s = seq_span(a, found);
-            s.c = (int)(slot - s.base);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (found[k] >= 0) {
+            s[k] = seq_span(a, found[k]);
+            s[k].c = (int)(slot[k] - s[k].base);
         }
-    }
     return true;
+}
+
+__device__ bool cu_valid(const ChunkBwdArgs& a) {
+    const long none[1] = {-1};
+    Span s[1];
+    return find_spans<1>(a, none, s);
 }
 
 // ---- workspace ---------------------------------------------------------------------------------
@@ -178,32 +188,48 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp
 }
 __device__ __forceinline__ float decay(float2 gi, float2 gj) { return exp2_approx((gi.x - gj.x) + (gi.y - gj.y)); }
 
-// By one warp.
-__device__ void load_gates(const ChunkBwdArgs& a, Gates& t, long t0, int len, int h, int lane) {
-    const int i0 = 2 * lane;
-    float g[2], beta[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const bool in = i0 + e < len;
-        g[e] = in ? a.g[(t0 + i0 + e) * a.H + h] : 0.f;
-        beta[e] = in ? a.beta[(t0 + i0 + e) * a.H + h] : 0.f;
-    }
-    double s = (double)g[0] + (double)g[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += x;
-    }
-    const double G[2] = {s - (double)g[1], s};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const double x = G[e] * 1.4426950408889634;
-        const float hi = (float)x;
-        t.G[i0 + e] = make_float2(hi, (float)(x - (double)hi));
-        t.b[i0 + e] = expf((float)G[e]);
-        t.beta[i0 + e] = beta[e];
-    }
+// (x + y) + (u + v) as a pair whose second part is the rounding of the first.
+__device__ __forceinline__ float2 add2(float2 p, float2 q) {
+    const float s = p.x + q.x, d = s - p.x;
+    const float e = ((p.x - (s - d)) + (q.x - d)) + (p.y + q.y);
+    const float x = s + e;
+    return make_float2(x, e - (x - s));
 }
+
+// By one warp, two tokens a lane: raw between fetch and put, as for Rows.
+struct GateRows {
+    float g[2], beta[2];
+
+    __device__ __forceinline__ void fetch(const ChunkBwdArgs& a, long t0, int len, int h, int lane) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool in = 2 * lane + e < len;
+            g[e] = in ? a.g[(t0 + 2 * lane + e) * a.H + h] : 0.f;
+            beta[e] = in ? a.beta[(t0 + 2 * lane + e) * a.H + h] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void put(Gates& t, int lane) const {
+        const float2 first = make_float2(g[0], 0.f);
+        float2 s = add2(first, make_float2(g[1], 0.f));  // inclusive sums over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float2 x = make_float2(__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o));
+            if (lane >= o) s = add2(x, s);
+        }
+        float2 before = make_float2(__shfl_up_sync(0xffffffffu, s.x, 1), __shfl_up_sync(0xffffffffu, s.y, 1));
+        if (lane == 0) before = make_float2(0.f, 0.f);
+        const float2 G[2] = {add2(before, first), s};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // times log2(e) = hi + lo
+            const float hi = 1.44269502f, lo = 1.92596299e-8f, x = G[e].x * hi;
+            const float y = fmaf(G[e].x, hi, -x) + fmaf(G[e].x, lo, G[e].y * hi);
+            t.G[2 * lane + e] = make_float2(x, y);
+            t.b[2 * lane + e] = expf(G[e].x) * (1.f + G[e].y);
+            t.beta[2 * lane + e] = beta[e];
+        }
+    }
+};
 
 // ---- loads -------------------------------------------------------------------------------------
 
@@ -213,53 +239,44 @@ __device__ __forceinline__ void load4(const void* src, gdn_dtype dt, long i, flo
     else load_vec<4>(static_cast<const float*>(src) + i, x);
 }
 
-// A chunk of a token tensor [T, heads, D], four elements a lane and row: raw in registers between fetch
-// (which only loads) and put, so that the loads of several tensors are under way together.  With P = 1 the
-// tensor is bf16.  NW warps take part.
+// A chunk of a token tensor [T, heads, D]: raw in registers between fetch (which only loads) and put, so
+// that the loads of several tensors are under way together.  With P = 1 the tensor is bf16.  NW warps take
+// part, LPR lanes a row and every row at once, so that a row's norm and maximum are a few shuffles and its
+// factors are worked out by its own lanes.  (A warp's 32 lanes on one row after another took 5.4k cycles
+// for a 64 x 128 tile, most of them waiting for shuffles.)
 template <int NW, int D, int P>
 struct Rows {
-    static constexpr int LPR = D / 4, RPP = 32 / LPR, N = kC / NW / RPP;  // lanes a row, rows a pass, passes
-    uint2 raw[P == 1 ? N : 1];
+    static constexpr int LPR = NW / 2, V = P == 1 ? 8 : 4, N = D / LPR / V;  // lanes a row; elements, vectors a lane
+    uint4 raw[P == 1 ? N : 1];
     float x[P == 2 ? N : 1][4];
 
-    static __device__ __forceinline__ int row(int p, int warp, int lane) { return (p * NW + warp) * RPP + lane / LPR; }
+    static __device__ __forceinline__ int row(int warp, int lane) { return warp * (kC / NW) + lane / LPR; }
+    // Column of a lane's vector i; odd rows of four lanes take the vectors in another order, so that the
+    // eight lanes of a store phase lie in different banks.
+    static __device__ __forceinline__ int col(int i, int lane) {
+        const int k = LPR == 4 ? i ^ ((lane / LPR) & 1) : i;
+        return V * (lane % LPR + LPR * k);
+    }
 
     __device__ __forceinline__ void fetch(const void* src, gdn_dtype dt, long t0, int len, int heads, int h, int warp,
                                           int lane) {
+        const int r = row(warp, lane);
+        const long at = ((t0 + r) * heads + h) * D;
 #pragma unroll
-        for (int p = 0; p < N; ++p) {
-            const int r = row(p, warp, lane);
-            const long at = ((t0 + r) * heads + h) * D + 4 * (lane % LPR);
+        for (int i = 0; i < N; ++i) {
             if constexpr (P == 1) {
-                raw[p] = make_uint2(0u, 0u);
-                if (r < len) raw[p] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src) + at);
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < len) raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + at + col(i, lane));
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[p][e] = 0.f;
-                if (r < len) load4(src, dt, at, x[p]);
+                for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+                if (r < len) load4(src, dt, at + col(i, lane), x[i]);
             }
         }
     }
 
-    __device__ __forceinline__ void get(int p, float (&y)[4], uint32_t& top) const {
-        if constexpr (P == 1) {
-            y[0] = __uint_as_float(raw[p].x << 16);
-            y[1] = __uint_as_float(raw[p].x & 0xffff0000u);
-            y[2] = __uint_as_float(raw[p].y << 16);
-            y[3] = __uint_as_float(raw[p].y & 0xffff0000u);
-            const uint32_t u = raw[p].x & 0x7fff7fffu, v = raw[p].y & 0x7fff7fffu;
-            const __nv_bfloat162 m =
-                __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&v));
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
-            top = max(w & 0xffff0000u, w << 16);
-        } else {
-            top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = x[p][e];
-                top = max(top, planes::abs_bits(y[e]));
-            }
-        }
+    static __device__ __forceinline__ float2 wide(uint32_t u) {
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
 
     // As planes, each row with a power of two of its own (one plane holds bf16 exactly).  factor[r] takes
@@ -271,56 +288,71 @@ struct Rows {
     template <bool NORM, int LO>
     __device__ __forceinline__ void put(Mat<D, P, LO> dst, float* factor, float* inv, bool use_l2, float scale,
                                         uint32_t* shared_top, int warp, int lane) const {
-        uint32_t all = 0;
-        const bool common = NORM && !use_l2;
-        if (common) {
+        const int r = row(warp, lane);
+        float ss = 0.f;
+        uint32_t top = 0;
+        if constexpr (P == 1) {
+            __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-            for (int p = 0; p < N; ++p) {
-                float y[4];
-                uint32_t top;
-                get(p, y, top);
-                all = max(all, top);
+            for (int i = 0; i < N; ++i) {
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v = u[e] & 0x7fff7fffu;
+                    m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v));
+                    if constexpr (NORM) {
+                        const float2 y = wide(u[e]);
+                        ss = fmaf(y.x, y.x, fmaf(y.y, y.y, ss));
+                    }
+                }
             }
-            atomicMax(shared_top, all);
-            __syncthreads();
-            all = *shared_top;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+            top = max(w & 0xffff0000u, w << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    top = max(top, planes::abs_bits(x[i][e]));
+                    if constexpr (NORM) ss = fmaf(x[i][e], x[i][e], ss);
+                }
         }
 #pragma unroll
-        for (int p = 0; p < N; ++p) {
-            const int r = row(p, warp, lane);
-            float y[4], ss = 0.f;
-            uint32_t top;
-            get(p, y, top);
-            if constexpr (NORM) {
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if constexpr (NORM) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        if (NORM && !use_l2) {
+            atomicMax(shared_top, top);
+            __syncthreads();
+            top = *shared_top;
+        }
+        const Scale s = planes::scale_of(top);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            }
-            if constexpr (LPR == 32) {
-                top = __reduce_max_sync(0xffffffffu, top);
-            } else {
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            }
-            const Scale s = planes::scale_of(common ? all : top);
-            const uint32_t at = dst.at + planes::offset<D>(r, 4 * (lane % LPR));
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = dst.at + planes::offset<D>(r, col(i, lane));
             if constexpr (P == 1) {
-                const __half2 u = __floats2half2_rn(y[0] * s.mul, y[1] * s.mul);
-                const __half2 v = __floats2half2_rn(y[2] * s.mul, y[3] * s.mul);
-                planes::sts64(at, *reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = wide(u[e]);
+                    const __half2 z = __floats2half2_rn(y.x * s.mul, y.y * s.mul);
+                    h[e] = *reinterpret_cast<const uint32_t*>(&z);
+                }
+                planes::sts128(at, h);
             } else {
                 uint32_t hi[2], lo[2];
-                planes::split(y[0] * s.mul, y[1] * s.mul, hi[0], lo[0]);
-                planes::split(y[2] * s.mul, y[3] * s.mul, hi[1], lo[1]);
+                planes::split(x[i][0] * s.mul, x[i][1] * s.mul, hi[0], lo[0]);
+                planes::split(x[i][2] * s.mul, x[i][3] * s.mul, hi[1], lo[1]);
                 planes::sts64(at, hi[0], hi[1]);
                 planes::sts64(at + LO, lo[0], lo[1]);
             }
-            if (lane % LPR == 0) {
-                const float f = NORM && use_l2 ? rsqrtf(ss + kL2Eps) : 1.f;
-                factor[r] = (NORM ? f * scale : 1.f) * s.back;
-                if (inv) inv[r] = f;
-            }
+        }
+        if (lane % LPR == 0) {
+            const float f = NORM && use_l2 ? rsqrtf(ss + kL2Eps) : 1.f;
+            factor[r] = (NORM ? f * scale : 1.f) * s.back;
+            if (inv) inv[r] = f;
         }
     }
 };
@@ -329,6 +361,23 @@ struct Rows {
 __device__ __forceinline__ void prefetch(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
+
+// Asks for the rows of a chunk of one token tensor that a later block will read; all T threads.
+template <int T, int D>
+__device__ __forceinline__ void prefetch_rows(const void* src, gdn_dtype dt, const Span& s, int heads, int h) {
+    const int lines = dt == GDN_BF16 ? D / 64 : D / 32;  // of 128 bytes, a row
+    const long t0 = s.bos + (long)s.c * kC;
+    for (int i = threadIdx.x; i < kC * lines; i += T) {
+        const int r = i / lines;
+        if (t0 + r < s.eos)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(src) +
+                                                           (((t0 + r) * heads + h) * lines + i % lines) * 128));
+    }
+}
+
+// Blocks of one chunk each run for tens of microseconds with few loads of their own under way, so each
+// asks for the inputs of the block that will follow it on its SM (about kSMs x blocks an SM later).
+constexpr int kSMs = 152;
 
 // ---- prep ----------------------------------------------------------------------------------------
 
@@ -472,9 +521,11 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
     __shared__ uint32_t red[7][NW], tops[2];
-    const long slot = blockIdx.x / a.H;
-    Span s;
-    if (!find_span(a, slot, s) || s.n < 0) return;
+    const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
+    const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
+    Span spans[2];
+    if (!find_spans<2>(a, slots, spans) || spans[0].n < 0) return;
+    const Span& s = spans[0];
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
@@ -491,14 +542,13 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         __syncthreads();
     }
     {
+        GateRows gates;
+        if (warp == NW - 1) gates.fetch(a, t0, len, h, lane);
         Rows<NW, D, P> k, v, q;
         k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         v.fetch(a.v, a.qkv_dtype, t0, len, a.H, h, warp, lane);
-        if (lane < len - 8 * warp && lane < 8)
-            prefetch(static_cast<const char*>(a.dout) + ((t0 + 8 * warp + lane) * a.H + h) * D * (P == 1 || a.dout_dtype == GDN_BF16 ? 2 : 4),
-                     D * (P == 1 || a.dout_dtype == GDN_BF16 ? 2 : 4));
-        if (warp == NW - 1) load_gates(a, t, t0, len, h, lane);
+        if (warp == NW - 1) gates.put(t, lane);
         k.template put<true>(K, fK, nullptr, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true>(Q, fQ, nullptr, a.use_l2, a.scale, &tops[1], warp, lane);
         v.template put<false>(V, fV, nullptr, false, 1.f, nullptr, warp, lane);
@@ -522,6 +572,13 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
                 make_float2(c < r ? kk[i][j][2 * hh] * (f * fK[c]) * decay(gr, t.G[c]) : 0.f,
                             c + 1 < r ? kk[i][j][2 * hh + 1] * (f * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f);
         });
+    }
+    if (spans[1].n >= 0) {
+        const int h2 = next % a.H, hk2 = h2 / (a.H / a.Hk);
+        prefetch_rows<kPrepThreads, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
+        prefetch_rows<kPrepThreads, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
+        prefetch_rows<kPrepThreads, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
+        prefetch_rows<kPrepThreads, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
     }
     if (tid < kC) tail.c[tid] = decay(t.G[kC - 1], t.G[tid]) * fK[tid];
     copy_out<P * PL / 16>(link + 2 * PL, sm + L::K);
@@ -658,21 +715,13 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 // dS <- b_C dS + X - E^T W.  The first product is split over the inner dimension, each warp taking its own
 // columns of the state, and the two parts meet through shared memory; both warps then hold the whole of
 // U^T or E^T (16 x 64) and take the second product for their own columns.  The chunks' links arrive by
-// asynchronous copies.  (One warp for 16 rows: 6.8k cycles a chunk at d = 128, at four cycles an
-// instruction of the only warp of an SM sub-partition.)
+// bulk copies; each pair of warps waits for a link and gives it back by itself, so that pairs drift apart
+// and one sub-partition's two warps (of two pairs) are not in the same phase.
 
 constexpr int kScanThreads = 256;
 constexpr int scan_stages(int d, int p) { return d == 128 && p == 2 ? 2 : 3; }
-constexpr int scan_bytes(int d, int p) { return scan_stages(d, p) * (int)link_bytes(d, p) + 8 * 16 * kC * 4; }
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+constexpr int scan_bytes(int d, int p) { return scan_stages(d, p) * (int)link_bytes(d, p) + 8 * 16 * kC * 4 + 64; }
+constexpr uint64_t kWaitNs = 2000000000ull;  // bound on one barrier wait
 
 // N[j] += rows (16 x 16 KT, in the accumulator layout) times B from column n0 and inner index k0: the
 // rows' planes are made here, scaled by mul (one power of two for each of this thread's two rows).  An SM
@@ -734,24 +783,40 @@ template <int D, int P, bool BACK>
 __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const Span& s, int h, int slice,
                                      unsigned char* sm) {
     constexpr int NT = D / 16, ZT = kC / 8, PL = kC * D * 2, LINK = (int)link_bytes(D, P), ST = scan_stages(D, P);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp & 3, half = warp >> 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
     const int block = slice * 4 + pair, row = block * 16 + (lane >> 2), c2 = (lane & 3) * 2, n0 = half * (D / 2);
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
     float4* mine = reinterpret_cast<float4*>(sm + ST * LINK) + (warp * ZT) * 32 + lane;  // part of Z, [ZT][32]
-    const float4* other = reinterpret_cast<const float4*>(sm + ST * LINK) + ((warp ^ 4) * ZT) * 32 + lane;
+    const float4* other = reinterpret_cast<const float4*>(sm + ST * LINK) + ((warp ^ 1) * ZT) * 32 + lane;
     const long state = ((long)s.n * a.H + h) * D * D + row * D + n0 + c2;
     const float* from = BACK ? a.dfinal_state : a.initial_state;
     auto unit_of = [&](int i) { return (s.base + (BACK ? s.chunks - 1 - i : i)) * a.H + h; };
-    auto fetch = [&](int i) {
-        if (i < s.chunks) {
-            const unsigned char* src = w.link + unit_of(i) * LINK;
-            const uint32_t dst = smem + (i % ST) * LINK;
-            for (int o = threadIdx.x * 16; o < LINK; o += kScanThreads * 16) copy16(dst + o, src + o);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + ST * LINK + 8 * 16 * kC * 4);
+    uint64_t* empty = full + ST;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], kScanThreads / 32);
         }
-        copy_commit();
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    // A wait that gives up is recorded, and this thread waits no more: what it computes from then on is
+    // meaningless but stays in its own places, and the kernel ends.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int use) {
+        if (ok && !ptx::mbar_wait(bar, use & 1, kWaitNs)) {
+            ok = false;
+            record_error(a.err, GDN_ERR_TIMEOUT);
+        }
     };
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) fetch(i);
+    auto fetch = [&](int i) {  // one thread: the link of chunk i, once chunk i - ST has given its place back
+        if (i >= s.chunks) return;
+        if (i >= ST) wait(&empty[i % ST], i / ST - 1);
+        ptx::mbar_arrive_expect_tx(&full[i % ST], LINK);
+        ptx::bulk_load(sm + (i % ST) * LINK, w.link + unit_of(i) * LINK, LINK, &full[i % ST]);
+    };
+    if (threadIdx.x == 0) fetch(0);
     float S[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -778,9 +843,9 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
         const long unit = unit_of(i);
         float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + n0 + c2;
         float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + c2;
-        copy_wait<ST - 2>();
-        __syncthreads();  // stage i is here, and every warp has left stage i - 1
-        fetch(i + ST - 1);
+        if (threadIdx.x == 0) fetch(i + 1);
+        __syncwarp();
+        wait(&full[i % ST], i / ST);
         const uint32_t at = smem + (i % ST) * LINK;
         const LinkTail& tail = *reinterpret_cast<const LinkTail*>(sm + (i % ST) * LINK + (2 + P) * PL);
         const Mat<D, 2, PL> W{at};
@@ -849,6 +914,8 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
             else row_product<true, ZT / 2>(N, Z, zmul, K, n0, 0, lane);
         }
         const float b_last = tail.b_last;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[i % ST]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -860,7 +927,8 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
         }
         if constexpr (BACK) load_x(i + 1);
     }
-    copy_wait<0>();
+    if (threadIdx.x == 0 && !ok)  // no copy may still be on its way when the block ends
+        for (int i = s.chunks > ST ? s.chunks - ST : 0; i < s.chunks; ++i) ptx::mbar_wait(&full[i % ST], (i / ST) & 1, kWaitNs);
     if (BACK && a.dinitial_state) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -875,10 +943,9 @@ template <int D, int P>
 __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBwdArgs a, Work w) {
     extern __shared__ __align__(256) unsigned char sm[];
     constexpr int slices = D / 64;
-    Span s;
-    if (!find_span(a, -1, s)) return;
+    if (!cu_valid(a)) return;
     const int unit = blockIdx.x / slices, slice = blockIdx.x % slices;
-    s = seq_span(a, unit / a.H);
+    const Span s = seq_span(a, unit / a.H);
     if (blockIdx.y) scan<D, P, true>(a, w, s, unit % a.H, slice, sm);
     else scan<D, P, false>(a, w, s, unit % a.H, slice, sm);
 }
@@ -961,9 +1028,11 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
     __shared__ uint32_t red[2][NW], tops[2];
-    const long slot = blockIdx.x / a.H;
-    Span s;
-    if (!find_span(a, slot, s) || s.n < 0) return;
+    const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
+    const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
+    Span spans[2];
+    if (!find_spans<2>(a, slots, spans) || spans[0].n < 0) return;
+    const Span& s = spans[0];
     const int h = blockIdx.x % a.H, rep = a.H / a.Hk, hk = h / rep, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
@@ -985,12 +1054,13 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const Meta& meta = w.meta[unit];
     const float* S0 = w.S + unit * D * D;
     const float* dS1 = w.dS + unit * D * D;
-    if (tid == 0) {
-        prefetch(S0, D * D * 4);
-        prefetch(w.E + unit * kC * D, kC * D * 4);
-        prefetch(w.U + unit * kC * D, kC * D * 4);
-        prefetch(dS1, D * D * 4);
-    }
+    auto prefetch_states = [&](long u) {
+        prefetch(w.S + u * D * D, D * D * 4);
+        prefetch(w.E + u * kC * D, kC * D * 4);
+        prefetch(w.U + u * kC * D, kC * D * 4);
+        prefetch(w.dS + u * D * D, D * D * 4);
+    };
+    if (tid == 0 && blockIdx.x < kSMs) prefetch_states(unit);
     Flat<T, D, D> state;
     Scale ss, sds, su;
     if (!a.use_l2) {
@@ -998,6 +1068,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         __syncthreads();
     }
     {
+        GateRows gates;
+        if (warp == NW - 1) gates.fetch(a, t0, len, h, lane);
         Rows<NW, D, P> k, q, y;
         uint4 tt[kTBytes / 16 / T];
         k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
@@ -1008,7 +1080,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) tt[i] = src[i * T + tid];
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
         const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
-        if (warp == NW - 1) load_gates(a, t, t0, len, h, lane);
+        if (warp == NW - 1) gates.put(t, lane);
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
         if constexpr (!L::share) y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
@@ -1021,7 +1093,20 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     }
     const float t_back = meta.t_scale;
     __syncthreads();
+    if (spans[1].n >= 0) {
+        const int h2 = next % a.H, hk2 = h2 / rep;
+        prefetch_rows<T, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
+        prefetch_rows<T, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
+        prefetch_rows<T, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
+        prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
+        if (tid == 0) {
+            prefetch(w.T + next * kTBytes, kTBytes);
+            prefetch_states(next);
+        }
+    }
 
+    float2 v[MT][NT][2];
+    Flat<T, D, kC> u;
     {
         float qk[MT][2][4];  // P, with the rows' factors of dY for P^T dY
         if constexpr (!L::share) state.fetch(S0);
@@ -1057,6 +1142,9 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         });
         state.template put<false>(ST, ss.mul);
         __syncthreads();
+        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
+            v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
+        });
         float acc[MT][NT][4];  // P^T dY + E
         planes::clear(acc);
         planes::product<kC, true, true, planes::kUpper>(acc, Pm, m, Y, nd, lane);
@@ -1074,11 +1162,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     Scale sr;
     {
         const float back = t_back * planes::scale_of(planes::top_of<NW>(red[1], lane)).back;
-        float2 v[MT][NT][2];
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-            v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
-        });
-        Flat<T, D, kC> u;
         u.fetch(w.U + unit * kC * D);
         float dR[MT][NT][4];
         planes::clear(dR);
@@ -1309,8 +1392,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
 // dq, dk of grouped heads: the sum over the group's value heads, in order.  Tokens outside every
 // sequence are left as they were.
 __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdArgs a, Work w) {
-    Span s;
-    if (!find_span(a, -1, s)) return;
+    if (!cu_valid(a)) return;
     const int rep = a.H / a.Hk;
     const long first = a.cu_seqlens ? a.cu_seqlens[0] : 0;
     const long end = a.cu_seqlens ? a.cu_seqlens[a.num_seqs] : a.total_T;
