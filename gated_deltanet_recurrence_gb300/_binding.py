@@ -117,10 +117,12 @@ def _sizes(ref, **tensors):
     """The library sees only pointers, so the binding refuses, before the call, a tensor on another
     device than `ref` or holding fewer elements than the call reads or writes through it.
     Each keyword is name=(tensor or None, elements the call touches)."""
+    dev, cuda = ref.get_device(), ref.is_cuda
     for name, (t, numel) in tensors.items():
         if t is None:
             continue
-        if t.device != ref.device:
+        # the index alone tells CUDA tensors apart; on the host the devices themselves are compared
+        if t.get_device() != dev or (not cuda and t.device != ref.device) or t.is_cuda != cuda:
             raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
         if t.numel() < numel:
             raise ValueError(f"{name} holds {t.numel()} elements; the call touches {numel}")
@@ -128,6 +130,8 @@ def _sizes(ref, **tensors):
 
 def _stream(stream, ref=None):
     if stream is None:
+        if ref is not None and ref.is_cuda:  # the raw handle: a Stream object takes some microseconds more
+            return torch._C._cuda_getCurrentRawStream(ref.get_device())
         return torch.cuda.current_stream(ref.device if ref is not None else None).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -138,7 +142,7 @@ def _run(ref, fn, *args):
     """Call library function `fn` with the device of `ref` current: the library launches its
     kernels on the calling thread's current device."""
     dev = ref.get_device()
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)

@@ -944,6 +944,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
     extern __shared__ __align__(256) unsigned char sm[];
     constexpr int slices = D / 64;
     if (!cu_valid(a)) return;
+    dependency_wait();
     const int unit = blockIdx.x / slices, slice = blockIdx.x % slices;
     const Span s = seq_span(a, unit / a.H);
     if (blockIdx.y) scan<D, P, true>(a, w, s, unit % a.H, slice, sm);
@@ -1032,6 +1033,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
     Span spans[2];
     if (!find_spans<2>(a, slots, spans) || spans[0].n < 0) return;
+    dependency_wait();
     const Span& s = spans[0];
     const int h = blockIdx.x % a.H, rep = a.H / a.Hk, hk = h / rep, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
@@ -1393,6 +1395,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
 // sequence are left as they were.
 __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdArgs a, Work w) {
     if (!cu_valid(a)) return;
+    dependency_wait();
     const int rep = a.H / a.Hk;
     const long first = a.cu_seqlens ? a.cu_seqlens[0] : 0;
     const long end = a.cu_seqlens ? a.cu_seqlens[a.num_seqs] : a.total_T;
@@ -1428,12 +1431,12 @@ cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
         chunk_bwd_prep_kernel<D, P><<<(unsigned)units, kPrepThreads, prep, s>>>(a, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    chunk_bwd_scan_kernel<D, P><<<dim3((unsigned)(a.num_seqs * a.H * (D / 64)), 2), kScanThreads, scan, s>>>(a, w);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.total_T == 0) return e;
-    chunk_bwd_grad_kernel<D, P><<<(unsigned)units, GradSmem<D, P>::threads, grad, s>>>(a, w);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.H == a.Hk) return e;
-    chunk_bwd_heads_kernel<<<152 * 8, kPrepThreads, 0, s>>>(a, w);
-    return cudaGetLastError();
+    const dim3 chains((unsigned)(a.num_seqs * a.H * (D / 64)), 2);
+    e = launch_after(chunk_bwd_scan_kernel<D, P>, chains, kScanThreads, scan, s, a, w);
+    if (e != cudaSuccess || a.total_T == 0) return e;
+    e = launch_after(chunk_bwd_grad_kernel<D, P>, dim3((unsigned)units), GradSmem<D, P>::threads, grad, s, a, w);
+    if (e != cudaSuccess || a.H == a.Hk) return e;
+    return launch_after(chunk_bwd_heads_kernel, dim3(kSMs * 8), kPrepThreads, 0, s, a, w);
 }
 
 }  // namespace

@@ -85,6 +85,24 @@ __device__ __forceinline__ void record_error(int* err, int status) {
 int prefill_fused_form();
 int decode_blocks_form();
 
+// Launches a kernel that begins with dependency_wait() behind the kernel before it on the stream: its
+// launch overlaps that kernel's end, and what that kernel wrote is seen after the wait.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- launchers (one translation unit each; called from abi.cu after argument checks) --------
 
 // The fused short convolution ("因果卷积"): weight [dim, 4]; states [rows, dim, 3], oldest first.
