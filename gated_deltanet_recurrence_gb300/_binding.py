@@ -9,6 +9,7 @@ fallback: if libgdn.so is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -126,6 +127,29 @@ def _sizes(ref, **tensors):
             raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
         if t.numel() < numel:
             raise ValueError(f"{name} holds {t.numel()} elements; the call touches {numel}")
+
+
+def _pointers(ref, *tensors):
+    """The checks of _f32, _sizes and _p in one pass, for calls whose host side is their time: each of
+    `tensors` is (name, tensor or None, elements the call touches, fp32 only).  Returns the pointers."""
+    dev, dense, out = ref.get_device(), True, []
+    for name, t, numel, f32 in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if f32 and t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be float32")
+        if t.get_device() != dev or (dev < 0 and t.device != ref.device):
+            raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
+        if t.numel() < numel:
+            raise ValueError(f"{name} holds {t.numel()} elements; the call touches {numel}")
+        dense = dense and t.is_contiguous()
+        out.append(t.data_ptr())
+    if not ref.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    if not dense:
+        raise ValueError("all tensors must be contiguous")
+    return out
 
 
 def _stream(stream, ref=None):
@@ -373,15 +397,36 @@ def gdn_decay_from_logits(a, A_log, dt_bias=None, b=None, g_out=None, beta_out=N
 
 
 def _workspace(workspace, need, ref):
-    """The caller's workspace, or one of `need` bytes from torch (None when none is needed)."""
-    if workspace is None and need:
+    """The caller's workspace, or one of `need` bytes from torch (None when none is needed), with its
+    pointer and size."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
-    return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
+        return workspace, workspace.data_ptr(), need
+    ptr, = _pointers(ref, ("workspace", workspace, 0, False))
+    return workspace, ptr, workspace.numel() * workspace.element_size()
 
 
+def _on_stream(call):
+    """With stream=..., runs the call with that stream current, so that what it allocates belongs to the
+    stream that uses it (memory taken on one stream may still be read by that stream's pending work)."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            first = next(t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor))
+            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
+
+
+@_on_stream
 def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=0.0, use_qk_l2norm=True,
                   initial_state=None, dfinal_state=None, output_dinitial_state=None, dq=None, dk=None, dv=None,
-                  dg=None, dbeta=None, dinitial_state=None, workspace=None, stream=None):
+                  dg=None, dbeta=None, dinitial_state=None, workspace=None):
     """Gradients of gdn_chunk_fwd (without gate and convolution, one decay per head): q, k, v, g, beta,
     cu_seqlens, num_seqs, scale, use_qk_l2norm and initial_state as given to it, dout [total_T, H, d_v]
     (fp32 or bf16) the gradient of out, dfinal_state [num_seqs, H, d_v, d_k] fp32 that of final_state
@@ -411,48 +456,43 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=
     if dinitial_state is None and (output_dinitial_state or
                                    (output_dinitial_state is None and initial_state is not None)):
         dinitial_state = torch.empty((num_seqs, H, d_v, d_k), dtype=torch.float32, device=q.device)
-    for name, t in (("g", g), ("beta", beta), ("initial_state", initial_state), ("dg", dg), ("dbeta", dbeta),
-                    ("dfinal_state", dfinal_state), ("dinitial_state", dinitial_state)):
-        _f32(t, name)
-    states = num_seqs * H * d_v * d_k
-    _sizes(q, k=(k, total_T * H_k * d_k), v=(v, total_T * H * d_v), g=(g, total_T * H), beta=(beta, total_T * H),
-           cu_seqlens=(cu_seqlens, num_seqs + 1), initial_state=(initial_state, states),
-           dout=(dout, total_T * H * d_v), dfinal_state=(dfinal_state, states), dq=(dq, total_T * H_k * d_k),
-           dk=(dk, total_T * H_k * d_k), dv=(dv, total_T * H * d_v), dg=(dg, total_T * H),
-           dbeta=(dbeta, total_T * H), dinitial_state=(dinitial_state, states), workspace=(workspace, 0))
+    states, nk, nv, nh = num_seqs * H * d_v * d_k, total_T * H_k * d_k, total_T * H * d_v, total_T * H
     L = lib()
-    workspace, ws_bytes = _workspace(workspace, L.gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v), q)
-    rc = _run(q, L.gdn_chunk_bwd,
-              _p(q), _p(k), _p(v), _p(g), _p(beta), _p(cu_seqlens), num_seqs, total_T, H, H_k, d_k, d_v, dt,
-              GDN_DECAY_PER_HEAD, float(scale), int(bool(use_qk_l2norm)), _p(initial_state), _p(dout), _dt(dout),
-              _p(dfinal_state), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta), _p(dinitial_state), _p(workspace),
-              ws_bytes, _stream(stream, q))
+    p = _pointers(q, ("q", q, nk, False), ("k", k, nk, False), ("v", v, nv, False), ("g", g, nh, True),
+                  ("beta", beta, nh, True), ("cu_seqlens", cu_seqlens, num_seqs + 1, False),
+                  ("initial_state", initial_state, states, True), ("dout", dout, nv, False),
+                  ("dfinal_state", dfinal_state, states, True), ("dq", dq, nk, False), ("dk", dk, nk, False),
+                  ("dv", dv, nv, False), ("dg", dg, nh, True), ("dbeta", dbeta, nh, True),
+                  ("dinitial_state", dinitial_state, states, True))
+    need = L.gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v)
+    workspace, ws, ws_bytes = _workspace(workspace, need, q)
+    rc = _run(q, L.gdn_chunk_bwd, *p[:6], num_seqs, total_T, H, H_k, d_k, d_v, dt, GDN_DECAY_PER_HEAD, float(scale),
+              int(bool(use_qk_l2norm)), p[6], p[7], _dt(dout), *p[8:], ws, ws_bytes, _stream(None, q))
     _check("gdn_chunk_bwd", rc)
     return dq, dk, dv, dg, dbeta, dinitial_state
 
 
+@_on_stream
 def gdn_gate_rmsnorm_silu_bwd(dout, y, z, norm_weight=None, eps=1e-6, dy=None, dz=None, dnorm_weight=None,
-                              workspace=None, stream=None):
+                              workspace=None):
     """Gradients of gdn_gate_rmsnorm_silu: dout (fp32 or bf16), y and z as given to it.  Returns (dy in
     y's dtype, dz fp32, dnorm_weight fp32); dnorm_weight is None unless it or norm_weight is given."""
     d_v = y.shape[-1]
     rows = y.numel() // d_v if d_v else 0
-    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
-    dz = torch.empty(y.shape, dtype=torch.float32, device=y.device) if dz is None else dz
+    dy = torch.empty_like(y) if dy is None else dy
+    dz = torch.empty_like(y, dtype=torch.float32) if dz is None else dz
     if dnorm_weight is None and norm_weight is not None:
-        dnorm_weight = torch.empty((d_v,), dtype=torch.float32, device=y.device)
+        dnorm_weight = torch.empty_like(norm_weight)
     if dy.dtype != y.dtype:
         raise TypeError("dy must have the dtype of y")
-    for name, t in (("z", z), ("norm_weight", norm_weight), ("dz", dz), ("dnorm_weight", dnorm_weight)):
-        _f32(t, name)
-    _sizes(y, dout=(dout, rows * d_v), z=(z, rows * d_v), norm_weight=(norm_weight, d_v), dy=(dy, rows * d_v),
-           dz=(dz, rows * d_v), dnorm_weight=(dnorm_weight, d_v), workspace=(workspace, 0))
-    L = lib()
+    n, L = rows * d_v, lib()
+    p = _pointers(y, ("dout", dout, n, False), ("y", y, n, False), ("z", z, n, True),
+                  ("norm_weight", norm_weight, d_v, True), ("dy", dy, n, False), ("dz", dz, n, True),
+                  ("dnorm_weight", dnorm_weight, d_v, True))
     need = L.gdn_gate_bwd_workspace_size(rows, 1, d_v) if dnorm_weight is not None else 0
-    workspace, ws_bytes = _workspace(workspace, need, y)
-    rc = _run(y, L.gdn_gate_rmsnorm_silu_bwd,
-              _p(dout), _dt(dout), _p(y), _dt(y), _p(z), _p(norm_weight), float(eps), _p(dy), _p(dz),
-              _p(dnorm_weight), rows, d_v, _p(workspace), ws_bytes, _stream(stream, y))
+    workspace, ws, ws_bytes = _workspace(workspace, need, y)
+    rc = _run(y, L.gdn_gate_rmsnorm_silu_bwd, p[0], _dt(dout), p[1], _dt(y), p[2], p[3], float(eps), p[4], p[5], p[6],
+              rows, d_v, ws, ws_bytes, _stream(None, y))
     _check("gdn_gate_rmsnorm_silu_bwd", rc)
     return dy, dz, dnorm_weight
 
@@ -464,59 +504,55 @@ def _groups(y):
     return (y.numel() // (groups * size) if groups * size else 0), groups, size
 
 
-def gdn_gate_groupnorm_silu(y, z=None, weight=None, bias=None, eps=1e-6, out=None, out_dtype=None, stream=None):
+@_on_stream
+def gdn_gate_groupnorm_silu(y, z=None, weight=None, bias=None, eps=1e-6, out=None, out_dtype=None):
     """Group norm over the heads, channels last, with a SiLU: y [..., groups, group_size] (fp32 or bf16),
     m = weight * (y - mean) / sqrt(var + eps) + bias per group, out = m * silu(z), or silu(m) without z.
     z like y, fp32; weight, bias [groups, group_size] fp32 or None."""
     rows, groups, size = _groups(y)
-    odt = _dt(y) if out_dtype is None else _dt(torch.empty(0, dtype=out_dtype))
     if out is None:
-        out = torch.empty(y.shape, dtype=_torch_dt(odt), device=y.device)
-    else:
-        odt = _dt(out)
+        out = torch.empty_like(y, dtype=out_dtype)
     n, c = rows * groups * size, groups * size
-    for name, t in (("z", z), ("weight", weight), ("bias", bias)):
-        _f32(t, name)
-    _sizes(y, z=(z, n), weight=(weight, c), bias=(bias, c), out=(out, n))
-    rc = _run(y, lib().gdn_gate_groupnorm_silu,
-              _p(y), _dt(y), _p(z), _p(weight), _p(bias), float(eps), _p(out), odt, rows, groups, size,
-              _stream(stream, y))
+    p = _pointers(y, ("y", y, n, False), ("z", z, n, True), ("weight", weight, c, True), ("bias", bias, c, True),
+                  ("out", out, n, False))
+    rc = _run(y, lib().gdn_gate_groupnorm_silu, p[0], _dt(y), p[1], p[2], p[3], float(eps), p[4], _dt(out), rows,
+              groups, size, _stream(None, y))
     _check("gdn_gate_groupnorm_silu", rc)
     return out
 
 
+@_on_stream
 def gdn_gate_groupnorm_silu_bwd(dout, y, z=None, weight=None, bias=None, eps=1e-6, dy=None, dz=None, dweight=None,
-                                dbias=None, workspace=None, stream=None):
+                                dbias=None, workspace=None):
     """Gradients of gdn_gate_groupnorm_silu: dout (fp32 or bf16) and the forward's inputs.  Returns (dy in
     y's dtype, dz fp32 or None without z, dweight, dbias fp32 [groups, group_size]); dweight (dbias) is
     None unless it or weight (bias) is given."""
     rows, groups, size = _groups(y)
     n, c = rows * groups * size, groups * size
-    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device) if dy is None else dy
+    dy = torch.empty_like(y) if dy is None else dy
     if dy.dtype != y.dtype:
         raise TypeError("dy must have the dtype of y")
     if z is not None and dz is None:
-        dz = torch.empty(y.shape, dtype=torch.float32, device=y.device)
+        dz = torch.empty_like(z)
     if weight is not None and dweight is None:
-        dweight = torch.empty((groups, size), dtype=torch.float32, device=y.device)
+        dweight = torch.empty_like(weight)
     if bias is not None and dbias is None:
-        dbias = torch.empty((groups, size), dtype=torch.float32, device=y.device)
-    for name, t in (("z", z), ("weight", weight), ("bias", bias), ("dz", dz), ("dweight", dweight), ("dbias", dbias)):
-        _f32(t, name)
-    _sizes(y, dout=(dout, n), z=(z, n), weight=(weight, c), bias=(bias, c), dy=(dy, n), dz=(dz, n),
-           dweight=(dweight, c), dbias=(dbias, c), workspace=(workspace, 0))
+        dbias = torch.empty_like(bias)
     L = lib()
+    p = _pointers(y, ("dout", dout, n, False), ("y", y, n, False), ("z", z, n, True), ("weight", weight, c, True),
+                  ("bias", bias, c, True), ("dy", dy, n, False), ("dz", dz, n, True), ("dweight", dweight, c, True),
+                  ("dbias", dbias, c, True))
     need = L.gdn_gate_bwd_workspace_size(rows, groups, size) if dweight is not None or dbias is not None else 0
-    workspace, ws_bytes = _workspace(workspace, need, y)
-    rc = _run(y, L.gdn_gate_groupnorm_silu_bwd,
-              _p(dout), _dt(dout), _p(y), _dt(y), _p(z), _p(weight), _p(bias), float(eps), _p(dy), _p(dz),
-              _p(dweight), _p(dbias), rows, groups, size, _p(workspace), ws_bytes, _stream(stream, y))
+    workspace, ws, ws_bytes = _workspace(workspace, need, y)
+    rc = _run(y, L.gdn_gate_groupnorm_silu_bwd, p[0], _dt(dout), p[1], _dt(y), p[2], p[3], p[4], float(eps), p[5],
+              p[6], p[7], p[8], rows, groups, size, ws, ws_bytes, _stream(None, y))
     _check("gdn_gate_groupnorm_silu_bwd", rc)
     return dy, dz, dweight, dbias
 
 
+@_on_stream
 def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=None, ddt_bias=None, db=None,
-                              workspace=None, stream=None):
+                              workspace=None):
     """Gradients of gdn_decay_from_logits: a, A_log, dt_bias (or None), b (or None) as given to it, dg
     [total_T, H] and dbeta [total_T, H] (None exactly when b is) those of its outputs, fp32.  Returns
     (da, dA_log, ddt_bias, db); ddt_bias is None unless it or dt_bias is given, db is None without b."""
@@ -524,22 +560,17 @@ def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=N
     if (b is None) != (dbeta is None):
         raise ValueError("b and dbeta are given together")
     da = torch.empty_like(a) if da is None else da
-    dA_log = torch.empty((H,), dtype=torch.float32, device=a.device) if dA_log is None else dA_log
+    dA_log = torch.empty_like(A_log) if dA_log is None else dA_log
     if dt_bias is not None and ddt_bias is None:
-        ddt_bias = torch.empty((H,), dtype=torch.float32, device=a.device)
+        ddt_bias = torch.empty_like(dt_bias)
     if b is not None and db is None:
         db = torch.empty_like(b)
-    for name, t in (("a", a), ("A_log", A_log), ("dt_bias", dt_bias), ("b", b), ("dg", dg), ("dbeta", dbeta),
-                    ("da", da), ("dA_log", dA_log), ("ddt_bias", ddt_bias), ("db", db)):
-        _f32(t, name)
-    n = total_T * H
-    _sizes(a, A_log=(A_log, H), dt_bias=(dt_bias, H), b=(b, n), dg=(dg, n), dbeta=(dbeta, n), da=(da, n),
-           dA_log=(dA_log, H), ddt_bias=(ddt_bias, H), db=(db, n), workspace=(workspace, 0))
-    L = lib()
-    workspace, ws_bytes = _workspace(workspace, L.gdn_decay_bwd_workspace_size(total_T, H), a)
-    rc = _run(a, L.gdn_decay_from_logits_bwd,
-              _p(a), _p(A_log), _p(dt_bias), _p(b), _p(dg), _p(dbeta), _p(da), _p(dA_log), _p(ddt_bias), _p(db),
-              total_T, H, _p(workspace), ws_bytes, _stream(stream, a))
+    n, L = total_T * H, lib()
+    p = _pointers(a, ("a", a, n, True), ("A_log", A_log, H, True), ("dt_bias", dt_bias, H, True), ("b", b, n, True),
+                  ("dg", dg, n, True), ("dbeta", dbeta, n, True), ("da", da, n, True), ("dA_log", dA_log, H, True),
+                  ("ddt_bias", ddt_bias, H, True), ("db", db, n, True))
+    workspace, ws, ws_bytes = _workspace(workspace, L.gdn_decay_bwd_workspace_size(total_T, H), a)
+    rc = _run(a, L.gdn_decay_from_logits_bwd, *p[:10], total_T, H, ws, ws_bytes, _stream(None, a))
     _check("gdn_decay_from_logits_bwd", rc)
     return da, dA_log, ddt_bias, db
 
