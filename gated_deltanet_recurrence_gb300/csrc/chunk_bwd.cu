@@ -131,7 +131,7 @@ __device__ bool cu_valid(const ChunkBwdArgs& a) {
 struct LinkTail {
     float c[kC];  // takes row j of K's planes to Kd: tail_j and the row's factor
     float w_scale, b_last, pad[62];
-};
+};  // 512 bytes, so that a link's planes, at any of its places, start at a multiple of 512
 static_assert(sizeof(LinkTail) == 512, "");
 
 struct Meta {
@@ -285,8 +285,8 @@ struct Rows {
     // the other operand of a contraction must not differ much between rows: with use_l2 the norm sets
     // their size; without it all rows share the largest row's power of two (the block then synchronises
     // on *shared_top, which must be zero).
-    template <bool NORM, int LO>
-    __device__ __forceinline__ void put(Mat<D, P, LO> dst, float* factor, float* inv, bool use_l2, float scale,
+    template <bool NORM, int LO, int HS>
+    __device__ __forceinline__ void put(Mat<D, P, LO, HS> dst, float* factor, float* inv, bool use_l2, float scale,
                                         uint32_t* shared_top, int warp, int lane) const {
         const int r = row(warp, lane);
         float ss = 0.f;
@@ -330,7 +330,7 @@ struct Rows {
         const Scale s = planes::scale_of(top);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint32_t at = dst.at + planes::offset<D>(r, col(i, lane));
+            const uint32_t at = dst(r, col(i, lane));
             if constexpr (P == 1) {
                 const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                 uint32_t h[4];
@@ -481,7 +481,7 @@ __device__ __forceinline__ void put16(uint32_t dst, unsigned char* image, int r,
     for (int i = 0; i < 8; ++i) planes::split(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t o = planes::offset<kC>(r, c + 8 * i);
+        const uint32_t o = planes::offset<kC, 0>(r, c + 8 * i);
         if (image) {
             *reinterpret_cast<uint4*>(image + o) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
             *reinterpret_cast<uint4*>(image + kTBytes / 2 + o) =
@@ -516,8 +516,8 @@ struct PrepSmem {
 template <int D, int P>
 __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_kernel(ChunkBwdArgs a, Work w) {
     using L = PrepSmem<D, P>;
-    constexpr int NW = kPrepThreads / 32, PL = L::plane, SQ = L::square;
-    extern __shared__ __align__(256) unsigned char sm[];
+    constexpr int NW = kPrepThreads / 32, PL = L::plane, SQ = L::square, HS = kC * 128;
+    extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
     __shared__ uint32_t red[7][NW], tops[2];
@@ -530,9 +530,9 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
-    const Mat<D, P, PL> K{base + L::K}, V{base + L::V}, Q{base + L::Q}, Y{base + L::W};
-    const Mat<D, 2, PL> Qp{base + L::V}, W{base + L::W};
-    const Mat<kC, 2, SQ> TX{base + L::TX};
+    const Mat<D, P, PL, HS> K{base + L::K}, V{base + L::V}, Q{base + L::Q}, Y{base + L::W};
+    const Mat<D, 2, PL, HS> Qp{base + L::V}, W{base + L::W};
+    const Mat<kC, 2, SQ, 0> TX{base + L::TX};
     float *Af = reinterpret_cast<float*>(sm + L::TX), *Tf = Af + kC * kLd;
     unsigned char* link = w.link + unit * link_bytes(D, P);
     LinkTail& tail = *reinterpret_cast<LinkTail*>(link + (2 + P) * PL);
@@ -727,16 +727,16 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // bound on one barrier wait
 // rows' planes are made here, scaled by mul (one power of two for each of this thread's two rows).  An SM
 // sub-partition has two warps only: the blocks of B for the next step are loaded before this step's
 // products, and the terms of one accumulator lie NT products apart.
-template <bool TB, int KT, int NT, int CB, int PB, int LB>
+template <bool TB, int KT, int NT, int CB, int PB, int LB, int HB>
 __device__ __forceinline__ void row_product(float (&N)[NT][4], const float (&rows)[2 * KT][4], const float (&mul)[2],
-                                            Mat<CB, PB, LB> B, int n0, int k0, int lane) {
-    const uint32_t lb = planes::lane_b<CB, TB>(B.at, lane);
+                                            Mat<CB, PB, LB, HB> B, int n0, int k0, int lane) {
+    const uint32_t lb = planes::lane_b<TB>(B, lane);
     uint32_t b[2][PB][NT / 2][4];
     auto load = [&](uint32_t (&x)[PB][NT / 2][4], int k) {
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
-            planes::load_b<CB, TB, 0>(x[0][j], lb, n0 + 16 * j, k0 + 16 * k);
-            if constexpr (PB == 2) planes::load_b<CB, TB, LB>(x[1][j], lb, n0 + 16 * j, k0 + 16 * k);
+            planes::load_b<TB, 0, HB>(x[0][j], lb, n0 + 16 * j, k0 + 16 * k);
+            if constexpr (PB == 2) planes::load_b<TB, LB, HB>(x[1][j], lb, n0 + 16 * j, k0 + 16 * k);
         }
     };
     load(b[0], 0);
@@ -848,8 +848,8 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
         wait(&full[i % ST], i / ST);
         const uint32_t at = smem + (i % ST) * LINK;
         const LinkTail& tail = *reinterpret_cast<const LinkTail*>(sm + (i % ST) * LINK + (2 + P) * PL);
-        const Mat<D, 2, PL> W{at};
-        const Mat<D, P, PL> K{at + 2 * PL};
+        const Mat<D, 2, PL, kC * 128> W{at};
+        const Mat<D, P, PL, kC * 128> K{at + 2 * PL};
         Scale rs[2], zs[2];
         const uint32_t top = row_scales(S, rs);
         if (lane == 0) (BACK ? w.meta[unit].ds_max : w.meta[unit].s_max)[block * 2 + half] = top;
@@ -941,7 +941,7 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
 
 template <int D, int P>
 __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBwdArgs a, Work w) {
-    extern __shared__ __align__(256) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     constexpr int slices = D / 64;
     if (!cu_valid(a)) return;
     dependency_wait();
@@ -952,18 +952,35 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
 }
 
 // ---- grad ----------------------------------------------------------------------------------------
+// The small products up to dR run on warp-level MMAs; those with the states, with U and with K and Q on
+// tcgen05, whose accumulators (TMEM) leave the registers, and whose operands are read from shared memory
+// once per block instead of once per warp.  They are stacked so that M = 128 is full:
+//   D1 = [dY; dR] S0            rows 0 .. 63: dQ's, rows 64 .. 127: F's part from the state
+//   NZ = [dY; dR] U^T           dP and Z before their decays
+//   D2 = [dP; Z] K              with K's row factors folded into dP's and Z's columns
+//   D3 = dP^T Q + (diag(beta) Z)^T K,  HH = U dS1:  the hi plane of the left side in rows 0 .. 63, its lo
+//        plane in rows 64 .. 127, to be added up
+// A thread then has one token's row: of dQ (TMEM lanes 0 .. 63) or of F and dK (lanes 64 .. 127), and 32
+// columns of it.
 
-// Shared memory: K, Q, dY (P planes each; with two planes Q and dY share one place, in turn), a state (S0,
-// then dS1), P then dP, T then Z, and two 64 x d buffers.
+constexpr uint64_t kMmaWaitNs = 2000000000ull;
+
+// Shared memory.  YR holds dY (rows 0 .. 63) above dR (rows 64 .. 127), two planes; later dP^T's and Z^T's
+// left sides go where dR was, and with `share` Q comes and goes in dY's place.  ST holds S0, then dS1, then
+// the rows that pass from one half of the lanes to the other.  SQ holds P above T, then dP above Z.  B1
+// holds P^T dY + E, then U^T, then the row sums.
 template <int D, int P>
 struct GradSmem {
-    static constexpr bool share = P == 2;
-    static constexpr int plane = kC * D * 2, square = kC * kC * 2, state = D * D * 2;
-    static constexpr int K = 0, Q = P * plane, Y = share ? Q : 2 * P * plane;
-    static constexpr int ST = Y + P * plane, Pm = ST + 2 * state, Tm = Pm + 2 * square;
-    static constexpr int B1 = Tm + 2 * square, B2 = B1 + 2 * plane, bytes = B2 + 2 * plane;
-    // d = 128: 16 warps of one block, d = 64: 8 warps, and two blocks on an SM where they fit
+    // d = 64: two blocks share an SM, which takes Q out; d = 128 in fp32 needs the room as well
+    static constexpr bool share = P == 2 || D == 64;
+    // room for diag(beta) Z beside dP^T's left side, or only after U has been used
+    static constexpr bool late = D == 64;
+    static constexpr int H2 = D / 64, half = kC * 128, plane = half * H2, yr = 2 * plane, st = D * 128 * H2;
+    static constexpr int K = 0, Q = P * plane, YR = share ? Q : 2 * P * plane;
+    static constexpr int ST = YR + 2 * yr, SQ = ST + 2 * st, B1 = SQ + 4 * half, bytes = B1 + 2 * plane;
     static constexpr int WM = D / 32, threads = WM * 128;
+    // TMEM columns: D1, D2, D3, then NZ and HH in turn
+    static constexpr int tD1 = 0, tD2 = D, tD3 = 2 * D, tNZ = 3 * D, tmem = 4 * D;
 };
 
 // An fp32 matrix of ROWS x COLS, raw in registers between fetch and put.  put writes its planes with the
@@ -978,13 +995,13 @@ struct Flat {
 #pragma unroll
         for (int p = 0; p < N; ++p) load_vec<4>(src + (p * T + threadIdx.x) * 4, x[p]);
     }
-    template <bool DOT, int LO>
-    __device__ __forceinline__ float put(Mat<COLS, 2, LO> dst, float mul) const {
+    template <bool DOT, int LO, int HS>
+    __device__ __forceinline__ float put(Mat<COLS, 2, LO, HS> dst, float mul) const {
         float dot = 0.f;
 #pragma unroll
         for (int p = 0; p < N; ++p) {
             const int e = (p * T + threadIdx.x) * 4;
-            const uint32_t at = dst.at + planes::offset<COLS>(e / COLS, e % COLS);
+            const uint32_t at = dst(e / COLS, e % COLS);
             if constexpr (DOT) {
                 uint32_t u[2], v[2];
                 planes::lds64(at, u[0], u[1]);
@@ -1019,16 +1036,48 @@ __device__ __forceinline__ void store2(void* dst, gdn_dtype dt, long i, float x,
     else
         *reinterpret_cast<float2*>(static_cast<float*>(dst) + i) = make_float2(x, y);
 }
+// Eight consecutive elements.
+__device__ __forceinline__ void store8(void* dst, gdn_dtype dt, long i, const float (&x)[8]) {
+    if (dt == GDN_BF16) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+            u[j] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+        float* p = static_cast<float*>(dst) + i;
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// One pass of tcgen05 MMAs over an inner dimension of 16 STEPS, by one thread: D (+)= A B.  A and B are
+// shared addresses of 128-byte-swizzled tiles; MN: stored [inner][outer], blocks of 64 outer elements
+// `block` bytes apart; otherwise stored [outer][inner], blocks of 64 inner elements `block` bytes apart.
+template <int STEPS, int N, bool AMN, bool BMN>
+__device__ __forceinline__ void issue(uint32_t d, uint32_t A, int a_block, uint32_t B, int b_block, bool accumulate) {
+    constexpr uint32_t id = ptx::idesc_f16(128, N, AMN, BMN);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const uint32_t ao = AMN ? k * 2048 : (k >> 2) * a_block + (k & 3) * 32;
+        const uint32_t bo = BMN ? k * 2048 : (k >> 2) * b_block + (k & 3) * 32;
+        ptx::mma_bf16_ss(d, ptx::sdesc_sw128(A + ao, AMN ? a_block : 16, 1024),
+                         ptx::sdesc_sw128(B + bo, BMN ? b_block : 16, 1024), id, accumulate || k > 0);
+    }
+}
 
 template <int D, int P>
 __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2 : 1)
     chunk_bwd_grad_kernel(ChunkBwdArgs a, Work w) {
     using L = GradSmem<D, P>;
-    constexpr int T = L::threads, NW = T / 32, WM = L::WM, MT = 4 / WM, PL = L::plane, SQ = L::square;
-    extern __shared__ __align__(256) unsigned char sm[];
+    constexpr int T = L::threads, NW = T / 32, WM = L::WM, MT = 4 / WM, HF = L::half, PL = L::plane, CG = NW / 4;
+    extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
-    __shared__ uint32_t red[2][NW], tops[2];
+    __shared__ uint32_t red[2][NW], tops[2], tmem_at;
+    __shared__ uint64_t bars[3];
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
     Span spans[2];
@@ -1039,11 +1088,19 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
-    const Mat<D, P, PL> K{base + L::K}, Q{base + L::Q}, Y{base + L::Y};
-    const Mat<D, 2, L::state> ST{base + L::ST};
-    const Mat<kC, 2, SQ> Pm{base + L::Pm}, Tm{base + L::Tm}, Sq1{base + L::B1}, Sq2{base + L::B2};
-    const Mat<D, 2, PL> B1{base + L::B1}, B2{base + L::B2};
-    const Mat<kC, 2, PL> UT{base + L::B1};  // U^T
+    constexpr int QHS = L::share ? 2 * HF : HF, QLO = L::share ? L::yr : PL;
+    const Mat<D, P, PL, HF> K{base + L::K};
+    const Mat<D, P, QLO, QHS> Q{base + L::Q};
+    const Mat<D, P, L::yr, 2 * HF> Y{base + L::YR};
+    const Mat<D, 2, L::yr, 2 * HF> R{base + L::YR + HF};
+    const Mat<D, 2, L::st, D * 128> ST{base + L::ST};
+    const Mat<kC, 2, 2 * HF, 0> Pm{base + L::SQ}, Tm{base + L::SQ + HF};
+    const Mat<D, 2, PL, HF> B1{base + L::B1};
+    const Mat<kC, 2, PL, 0> UT{base + L::B1};  // U^T
+    // the left sides of D3: planes two blocks apart in dR's place; diag(beta) Z in dY's place or, later, in U's
+    const Mat<kC, 2, 2 * HF, 0> Pt{base + L::YR + HF};
+    constexpr int ZLO = L::late ? HF : 2 * HF;
+    const Mat<kC, 2, ZLO, 0> Zt{base + (L::late ? L::B1 : L::YR + 5 * HF)};
     // Warps WM x 4.  With two row tiles a warp's are mw and 3 - mw; with one, the four warps of an SM
     // sub-partition (warp mod 4) are the four row tiles of a column block: either way the shares of a
     // triangular product are even.
@@ -1062,8 +1119,17 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         prefetch(w.U + u * kC * D, kC * D * 4);
         prefetch(w.dS + u * D * D, D * D * 4);
     };
-    if (tid == 0 && blockIdx.x < kSMs) prefetch_states(unit);
+    if (tid == 0) {
+        if (blockIdx.x < kSMs) prefetch_states(unit);
+        for (int i = 0; i < 3; ++i) ptx::mbar_init(&bars[i], 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc(&tmem_at, L::tmem);
+        ptx::tmem_relinquish();
+    }
     Flat<T, D, D> state;
+    Flat<T, D, kC> u;
     Scale ss, sds, su;
     if (!a.use_l2) {
         if (tid < 2) tops[tid] = 0;
@@ -1086,15 +1152,28 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
         if constexpr (!L::share) y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
-        uint4* dst = reinterpret_cast<uint4*>(sm + L::Tm);
+        // T's planes, each where SQ has T's: 512 vectors a plane
 #pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) dst[i * T + tid] = tt[i];
+        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
+            const int e = i * T + tid;
+            *reinterpret_cast<uint4*>(sm + L::SQ + HF + (e >> 9) * 2 * HF + (e & 511) * 16) = tt[i];
+        }
+        if constexpr (P == 1) {  // dY's lo plane is zero (below dR's, rows of 8 KB)
+#pragma unroll
+            for (int i = 0; i < PL / 16 / T; ++i) {
+                const int e = i * T + tid;
+                *reinterpret_cast<uint4*>(sm + L::YR + L::yr + (e >> 9) * 2 * HF + (e & 511) * 16) = make_uint4(0, 0, 0, 0);
+            }
+        }
         ss = planes::scale_of(__reduce_max_sync(0xffffffffu, top[0]));
         sds = planes::scale_of(__reduce_max_sync(0xffffffffu, top[1]));
         su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
     const float t_back = meta.t_scale;
+    ptx::tc_fence_before();
     __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tm = tmem_at;
     if (spans[1].n >= 0) {
         const int h2 = next % a.H, hk2 = h2 / rep;
         prefetch_rows<T, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
@@ -1108,7 +1187,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     }
 
     float2 v[MT][NT][2];
-    Flat<T, D, kC> u;
     {
         float qk[MT][2][4];  // P, with the rows' factors of dY for P^T dY
         if constexpr (!L::share) state.fetch(S0);
@@ -1177,68 +1255,79 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         });
         const uint32_t top = planes::max_bits(dR);
         if (lane == 0) red[0][warp] = top;
-        __syncthreads();  // also: B1 has been read
+        __syncthreads();  // also: B1, P and T have been read
         sr = planes::scale_of(planes::top_of<NW>(red[0], lane));
-        planes::write(B2, dR, m, nd, lane, sr.mul);
+        planes::write(R, dR, m, nd, lane, sr.mul);
         u.template put<false>(UT, su.mul);
     }
+    // D1 and NZ
+    ptx::fence_async_smem();
     __syncthreads();
-
-    float dQ[MT][NT][4], F[MT][NT][4], dP[MT][2][4], Z[MT][2][4];
-    planes::clear(dQ);
-    planes::product<D, false, true>(dQ, Y, m, ST, nd, lane);
-    planes::clear(F);
-    planes::product<D, false, true>(F, B2, m, ST, nd, lane);
-    planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
-        const float b = t.b[r] * ss.back, fq = b * fY[r], ff = -b * sr.back;
-#pragma unroll
-        for (int e = 2 * hh; e < 2 * hh + 2; ++e) {
-            dQ[i][j][e] *= fq;
-            F[i][j][e] *= ff;
-        }
-    });
-    state.fetch(dS1);
-    planes::clear(dP);
-    planes::product<D, false, true>(dP, Y, m, UT, nc, lane);
-    planes::clear(Z);
-    planes::product<D, false, true>(Z, B2, m, UT, nc, lane);
-    // dP and Z are wanted twice: with the factors of K's rows on the columns (for the products with K)
-    // and with the factors of the left rows (for the transposed products)
-    uint32_t tp[4] = {0, 0, 0, 0};
-    planes::pairs<MT, 2>(m, nc, lane, [&](int i, int j, int hh, int r, int c) {
-        const float2 gr = t.G[r];
-        const float fp = fY[r] * su.back, fz = -sr.back * su.back, fq = fQ[r], fz2 = t.beta[r] * fK[r];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float &x = dP[i][j][2 * hh + e], &z = Z[i][j][2 * hh + e];
-            const float dec = decay(gr, t.G[c + e]), y = x * fp * dec, fk = fK[c + e];
-            if (c + e == r) {
-                dpp[r] = y;
-                diag[r] *= y;  // by the thread that wrote q_r . k_r
-            }
-            x = c + e < r ? y : 0.f;
-            z = c + e < r ? z * fz * dec : 0.f;
-            tp[0] = max(tp[0], planes::abs_bits(x * fk));
-            tp[1] = max(tp[1], planes::abs_bits(x * fq));
-            tp[2] = max(tp[2], planes::abs_bits(z * fk));
-            tp[3] = max(tp[3], planes::abs_bits(z * fz2));
-        }
-    });
-    __syncthreads();  // B2, ST, P, T and dY have been read (B1 not yet by H)
-    const float state_dot = state.template put<true>(ST, sds.mul);  // and <S0, dS1>
-    // dP and Z's planes go where P and T were, and the warps' four maxima and state dots where dY's row
-    // factors and the maxima of dR were
-    static_assert(4 * NW <= kC, "");
-    uint32_t(*tops4)[NW] = reinterpret_cast<uint32_t(*)[NW]>(fY);
-    float* dots = reinterpret_cast<float*>(red[0]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, tp[i]);
-        if (lane == 0) tops4[i][warp] = top;
+    if (tid == 0) {
+        ptx::tc_fence_after();
+        constexpr int KS = D / 16;
+        const uint32_t yr = base + L::YR, ut = base + L::B1, st = base + L::ST;
+        issue<KS, 64, false, true>(tm + L::tNZ, yr, 2 * HF, ut, 16, false);
+        issue<KS, 64, false, true>(tm + L::tNZ, yr, 2 * HF, ut + PL, 16, true);
+        issue<KS, 64, false, true>(tm + L::tNZ, yr + L::yr, 2 * HF, ut, 16, true);
+        ptx::mma_commit(&bars[0]);
+        issue<KS, D, false, true>(tm + L::tD1, yr, 2 * HF, st, D * 128, false);
+        issue<KS, D, false, true>(tm + L::tD1, yr, 2 * HF, st + L::st, D * 128, true);
+        issue<KS, D, false, true>(tm + L::tD1, yr + L::yr, 2 * HF, st, D * 128, true);
+        ptx::mma_commit(&bars[1]);
     }
+    state.fetch(dS1);
+    // A wait that gives up is recorded; what follows is then meaningless, but ends.
+    bool ok = true;
+    auto wait = [&](int i, int use) {
+        if (ok && !ptx::mbar_wait(&bars[i], use, kMmaWaitNs)) {
+            ok = false;
+            record_error(a.err, GDN_ERR_TIMEOUT);
+        }
+        ptx::tc_fence_after();
+    };
+    // This thread's token, which half of the lanes, and its columns of a 64-wide and of a d-wide result
+    const int part = (warp & 3) >> 1, row = (warp & 1) * 32 + lane, cg = warp >> 2;
+    const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    constexpr int NC = kC / CG;
+    float x[NC];
+    uint32_t top1 = 0, top2 = 0;
+    wait(0, 0);
     {
-        const float x = warp_sum(state_dot);
-        if (lane == 0) dots[warp] = x;
+        uint32_t raw[NC];
+        if constexpr (NC == 16) ptx::tmem_ld16(lanes + L::tNZ + cg * NC, raw);
+        else ptx::tmem_ld32(lanes + L::tNZ + cg * NC, raw);
+        ptx::tmem_wait_ld();
+        const float2 gr = t.G[row];
+        const float f = part ? -sr.back * su.back : fY[row] * su.back, f2 = part ? t.beta[row] * fK[row] : fQ[row];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = cg * NC + i;
+            const float y = __uint_as_float(raw[i]) * f * decay(gr, t.G[c]);
+            if (c == row && part == 0) {
+                dpp[row] = y;
+                diag[row] *= y;
+            }
+            x[i] = c < row ? y : 0.f;
+            top1 = max(top1, planes::abs_bits(x[i] * fK[c]));
+            top2 = max(top2, planes::abs_bits(x[i] * f2));
+        }
+    }
+    top1 = __reduce_max_sync(0xffffffffu, top1);
+    top2 = __reduce_max_sync(0xffffffffu, top2);
+    wait(1, 0);  // S0's planes, dY and dR have been read
+    const float state_dot = warp_sum(state.template put<true>(ST, sds.mul));  // and <S0, dS1>
+    // the maxima and the parts of the dot product go where dR's maxima and dY's row factors were
+    static_assert(2 * NW <= kC, "");
+    const float f1 = part ? -t.b[row] * sr.back * ss.back : t.b[row] * fY[row] * ss.back;
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    uint32_t* tops2 = reinterpret_cast<uint32_t*>(fY);
+    if (lane == 0) {
+        tops2[warp] = top1;
+        tops2[NW + warp] = top2;
+        reinterpret_cast<float*>(red[0])[warp] = state_dot;
     }
     if constexpr (L::share) {
         Rows<NW, D, P> q;
@@ -1246,141 +1335,181 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
     }
     __syncthreads();
-    Scale sc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[i] = planes::scale_of(planes::top_of<NW>(tops4[i], lane));
-    // a square's planes with row factors (rf) or column factors (cf)
-    auto put = [&](Mat<kC, 2, SQ> dst, const float (&x)[MT][2][4], float mul, bool cols, const float* rf, const float* rf2) {
-        planes::pairs<MT, 2>(m, nc, lane, [&](int i, int j, int hh, int r, int c) {
-            const float f = cols ? mul * fK[c] : mul * rf[r] * (rf2 ? rf2[r] : 1.f);
-            const float f2 = cols ? mul * fK[c + 1] : f;
-            uint32_t hi, lo;
-            planes::split(x[i][j][2 * hh] * f, x[i][j][2 * hh + 1] * f2, hi, lo);
-            const uint32_t at = planes::pair_at<kC, 2>(dst.at, m[i], nc, j, hh, lane);
-            planes::sts32(at, hi);
-            planes::sts32(at + SQ, lo);
-        });
-    };
-    put(Pm, dP, sc[0].mul, true, nullptr, nullptr);
-    put(Tm, Z, sc[2].mul, true, nullptr, nullptr);
-    put(Sq2, dP, sc[1].mul, false, fQ, nullptr);
-    float H[MT][NT][4];
-    planes::clear(H);
-    planes::product<D, true, true>(H, UT, m, ST, nd, lane);
-    planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
-        const float f = decay(t.G[kC - 1], t.G[r]) * su.back * sds.back;
-        H[i][j][2 * hh] *= f;
-        H[i][j][2 * hh + 1] *= f;
-    });
-    __syncthreads();  // B1 and ST have been read
-    put(Sq1, Z, sc[3].mul, false, t.beta, fK);
-    __syncthreads();
-
-    float* sums = reinterpret_cast<float*>(sm + L::ST);  // [5][4][64]: parts of row sums, where dS1 was
+    // scales: dP's and Z's own for D2 (their rows are apart), one for D3 (their products are added)
+    Scale sk, sq;
     {
-        float acc[MT][NT][4], qdot[MT][2] = {}, kpos[MT][2] = {}, kneg[MT][2] = {}, hdot[MT][2] = {};
-        planes::clear(acc);
-        planes::product<kC, false, true, planes::kLower>(acc, Pm, m, K, nd, lane);
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            const float2 q = planes::read<NT>(Q, m[i], nd, j, hh, lane);
-            float &x = dQ[i][j][2 * hh], &y = dQ[i][j][2 * hh + 1];
-            x = fmaf(acc[i][j][2 * hh], sc[0].back, x);
-            y = fmaf(acc[i][j][2 * hh + 1], sc[0].back, y);
-            qdot[i][hh] = fmaf(x, q.x, fmaf(y, q.y, qdot[i][hh]));
-        });
-        planes::clear(acc);
-        planes::product<kC, false, true, planes::kLower>(acc, Tm, m, K, nd, lane);
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            float &x = F[i][j][2 * hh], &y = F[i][j][2 * hh + 1];
-            x = fmaf(acc[i][j][2 * hh], sc[2].back, x);
-            y = fmaf(acc[i][j][2 * hh + 1], sc[2].back, y);
-        });
-        planes::clear(acc);
-        planes::product<kC, true, true, planes::kUpper>(acc, Sq2, m, Q, nd, lane);
-        const float ratio = sc[1].back;
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            acc[i][j][2 * hh] *= ratio;
-            acc[i][j][2 * hh + 1] *= ratio;
-        });
-        float x[MT][NT][4];
-        planes::clear(x);
-        planes::product<kC, true, true, planes::kUpper>(x, Sq1, m, K, nd, lane);
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            const float2 k = planes::read<NT>(K, m[i], nd, j, hh, lane);
-            const float x0 = fmaf(x[i][j][2 * hh], sc[3].back, acc[i][j][2 * hh]);
-            const float x1 = fmaf(x[i][j][2 * hh + 1], sc[3].back, acc[i][j][2 * hh + 1]);
-            float &h0 = H[i][j][2 * hh], &h1 = H[i][j][2 * hh + 1];
-            kpos[i][hh] = fmaf(F[i][j][2 * hh], k.x, fmaf(F[i][j][2 * hh + 1], k.y, kpos[i][hh]));
-            hdot[i][hh] = fmaf(h0, k.x, fmaf(h1, k.y, hdot[i][hh]));
-            kneg[i][hh] = fmaf(x0, k.x, fmaf(x1, k.y, kneg[i][hh]));
-            h0 += x0;  // dK- without P's diagonal
-            h1 += x1;
-        });
-        // each warp's part of the row sums
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float y[5] = {qdot[i][hh], kpos[i][hh], kneg[i][hh], hdot[i][hh], vdot[i][hh]};
-                const int r = m[i] + (lane >> 2) + 8 * hh;
-#pragma unroll
-                for (int k = 0; k < 5; ++k) {
-                    y[k] += __shfl_xor_sync(0xffffffffu, y[k], 1);
-                    y[k] += __shfl_xor_sync(0xffffffffu, y[k], 2);
-                    if ((lane & 3) == 0) sums[(k * 4 + nw) * kC + r] = y[k];
-                }
-            }
+        const uint32_t y = tops2[lane & (NW - 1)], z = tops2[NW + (lane & (NW - 1))];
+        sk = planes::scale_of(__reduce_max_sync(0xffffffffu, ((lane >> 1) & 1) == part ? y : 0u));
+        sq = planes::scale_of(__reduce_max_sync(0xffffffffu, z));
     }
-    __syncthreads();
-    auto sum_of = [&](int k, int r) {
-        const float* x = sums + k * 4 * kC + r;
-        return (x[0] + x[kC]) + (x[2 * kC] + x[3 * kC]);
+    auto put_row = [&](auto dst, auto&& value) {
+#pragma unroll
+        for (int i = 0; i < NC; i += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) planes::split(value(i + 2 * j), value(i + 2 * j + 1), hi[j], lo[j]);
+            const uint32_t at = dst(row, cg * NC + i);
+            planes::sts128(at, hi);
+            planes::sts128(at + decltype(dst)::lo, lo);
+        }
     };
-    // through the normalisation: with xh = scale * x * inv and n = x * inv, dx = scale * inv * (d - n (n . d))
-    const long q_row = rep > 1 ? a.H : a.Hk;
-    const int q_head = rep > 1 ? h : hk;
-    void* dq = rep > 1 ? w.dq : a.dq;
-    void* dk = rep > 1 ? w.dk : a.dk;
-    const gdn_dtype qk_type = rep > 1 ? GDN_F32 : a.qkv_dtype;
+    put_row(part ? Tm : Pm, [&](int i) { return x[i] * (fK[cg * NC + i] * sk.mul); });
+    const float fq = (part ? t.beta[row] * fK[row] : fQ[row]) * sq.mul;
+    if (part == 0) put_row(Pt, [&](int i) { return x[i] * fq; });
+    else if (!L::late) put_row(Zt, [&](int i) { return x[i] * fq; });
+    ptx::fence_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+        ptx::tc_fence_after();
+        constexpr int KS = D / 16;
+        const uint32_t ut = base + L::B1, st = base + L::ST, sq_at = base + L::SQ;
+        issue<KS, D, true, true>(tm + L::tNZ, ut, PL, st, D * 128, false);          // HH
+        issue<KS, D, true, true>(tm + L::tNZ, ut, PL, st + L::st, D * 128, true);
+        if constexpr (L::late) ptx::mma_commit(&bars[0]);
+        issue<4, D, false, true>(tm + L::tD2, sq_at, 0, K.at, HF, false);
+        issue<4, D, false, true>(tm + L::tD2, sq_at + 2 * HF, 0, K.at, HF, true);
+        issue<4, D, true, true>(tm + L::tD3, Pt.at, 2 * HF, Q.at, QHS, false);
+        if constexpr (P == 2) {
+            issue<4, D, false, true>(tm + L::tD2, sq_at, 0, K.at + PL, HF, true);
+            issue<4, D, true, true>(tm + L::tD3, Pt.at, 2 * HF, Q.at + QLO, QHS, true);
+        }
+    }
+    if constexpr (L::late) {
+        wait(0, 1);  // U has been read
+        if (part) put_row(Zt, [&](int i) { return x[i] * fq; });
+        ptx::fence_async_smem();
+        ptx::tc_fence_before();
+        __syncthreads();
+    }
+    if (tid == 0) {
+        ptx::tc_fence_after();
+        issue<4, D, true, true>(tm + L::tD3, Zt.at, ZLO, K.at, HF, true);
+        if constexpr (P == 2) issue<4, D, true, true>(tm + L::tD3, Zt.at, ZLO, K.at + PL, HF, true);
+        ptx::mma_commit(&bars[2]);
+    }
+    wait(2, 0);
+
+    // 32 columns of this token's row: dQ or F in y; dK- + H (this half's planes) in z
+    const int c0 = cg * 32;
+    float y[32], z[32];
+    float dot0 = 0.f, dot1 = 0.f, dot2 = 0.f;  // dQ . q or F . k; H . k; (dK- - H) . k
+    {
+        const float fh = decay(t.G[kC - 1], t.G[row]) * su.back * sds.back;
+        uint32_t r1[32], r2[32];
+        ptx::tmem_ld32(lanes + L::tD1 + c0, r1);
+        ptx::tmem_ld32(lanes + L::tD2 + c0, r2);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(r2[i]), sk.back, __uint_as_float(r1[i]) * f1);
+        ptx::tmem_ld32(lanes + L::tD3 + c0, r1);
+        ptx::tmem_ld32(lanes + L::tNZ + c0, r2);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            float k[8], q[8];
+            planes::read8(K, row, c0 + i, k);
+            if (part == 0) planes::read8(Q, row, c0 + i, q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float hx = __uint_as_float(r2[i + j]) * fh, dx = __uint_as_float(r1[i + j]) * sq.back;
+                dot0 = fmaf(y[i + j], part ? k[j] : q[j], dot0);
+                dot1 = fmaf(hx, k[j], dot1);
+                dot2 = fmaf(dx, k[j], dot2);
+                z[i + j] = hx + dx;
+            }
+        }
+    }
+    // row sums, each by column group: [0] dQ . q, [1] F . k, [2, 3] H . k, [4, 5] (dK- - H) . k of the two
+    // halves, [6] dR . v of the four columns of warps
+    float(*sums)[4][kC] = reinterpret_cast<float(*)[4][kC]>(sm + L::B1);
+    sums[part][cg][row] = dot0;
+    sums[2 + part][cg][row] = dot1;
+    sums[4 + part][cg][row] = dot2;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-            const int r = m[i] + (lane >> 2) + 8 * hh;
-            if (r >= len) continue;
-            const float qd = a.use_l2 ? fmaf(sum_of(0, r), fQ[r], diag[r]) / (a.scale * a.scale) : 0.f;
-            const float kd = a.use_l2 ? fmaf(t.beta[r] * sum_of(1, r) + sum_of(2, r) + sum_of(3, r), fK[r], diag[r]) : 0.f;
-            const float oq = a.scale * qinv[r], ok = kinv[r], dp = dpp[r], beta = t.beta[r];
+            float e = vdot[i][hh];
+            e += __shfl_xor_sync(0xffffffffu, e, 1);
+            e += __shfl_xor_sync(0xffffffffu, e, 2);
+            if ((lane & 3) == 0) sums[6][nw][m[i] + (lane >> 2) + 8 * hh] = e;
+        }
+    // the first half of the lanes hands its part of dK's rows over
+    auto pass = [&](int c) {
+        return reinterpret_cast<float4*>(sm + L::ST + row * D * 4 + (((c >> 2) ^ (row & 7)) << 4));
+    };
+    if (part == 0) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float2 q = planes::read<NT>(Q, m[i], nd, j, hh, lane), k = planes::read<NT>(K, m[i], nd, j, hh, lane);
-                const float q0 = q.x * fQ[r], q1 = q.y * fQ[r], k0 = k.x * fK[r], k1 = k.y * fK[r];
-                const long at = ((t0 + r) * q_row + q_head) * D + nd + 8 * j + (lane & 3) * 2;
-                store2(dq, qk_type, at, oq * (fmaf(dp, k0, dQ[i][j][2 * hh]) - q0 * qd),
-                       oq * (fmaf(dp, k1, dQ[i][j][2 * hh + 1]) - q1 * qd));
-                const float d0 = fmaf(beta, F[i][j][2 * hh], fmaf(dp, q0, H[i][j][2 * hh]));
-                const float d1 = fmaf(beta, F[i][j][2 * hh + 1], fmaf(dp, q1, H[i][j][2 * hh + 1]));
-                store2(dk, qk_type, at, ok * (d0 - k0 * kd), ok * (d1 - k1 * kd));
+        for (int i = 0; i < 32; i += 4) *pass(c0 + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tm, L::tmem);
+    }
+    auto sum_of = [&](int k, int r, int n) {
+        float e = sums[k][0][r] + sums[k][1][r];
+        if (n == 4) e += sums[k][2][r] + sums[k][3][r];
+        return e;
+    };
+    // through the normalisation: with xh = scale * x * inv and n = x * inv, dx = scale * inv * (d - n (n . d))
+    if (row < len) {
+        const gdn_dtype type = rep > 1 ? GDN_F32 : a.qkv_dtype;
+        const long at = ((t0 + row) * (rep > 1 ? a.H : a.Hk) + (rep > 1 ? h : hk)) * D + c0;
+        const float dp = dpp[row], fq_row = fQ[row], fk_row = fK[row];
+        if (part == 0) {
+            const float qd = a.use_l2 ? fmaf(sum_of(0, row, CG), fq_row, diag[row]) / (a.scale * a.scale) * fq_row : 0.f;
+            const float o = a.scale * qinv[row], dk_row = dp * fk_row;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                float k[8], q[8], out[8];
+                planes::read8(K, row, c0 + i, k);
+                planes::read8(Q, row, c0 + i, q);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[j] = o * (fmaf(dk_row, k[j], y[i + j]) - q[j] * qd);
+                store8(rep > 1 ? w.dq : a.dq, type, at + i, out);
+            }
+        } else {
+            const float beta = t.beta[row], o = kinv[row], dq_row = dp * fq_row;
+            const float other = sum_of(2, row, CG) + sum_of(3, row, CG) + sum_of(4, row, CG) + sum_of(5, row, CG);
+            const float kd = a.use_l2 ? fmaf(beta * sum_of(1, row, CG) + other, fk_row, diag[row]) * fk_row : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                float k[8], q[8], out[8];
+                planes::read8(K, row, c0 + i, k);
+                planes::read8(Q, row, c0 + i, q);
+                const float4 z0 = *pass(c0 + i), z1 = *pass(c0 + i + 4);
+                const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float d = fmaf(beta, y[i + j], fmaf(dq_row, q[j], z[i + j] + zz[j]));
+                    out[j] = o * (d - k[j] * kd);
+                }
+                store8(rep > 1 ? w.dk : a.dk, type, at + i, out);
             }
         }
+    }
     // dbeta; dg by a scan from the chunk's end and one from its start, two rows a lane
-    if (warp == 0) {
+    if (warp == NW - 1) {
         float d[2], hd[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 2 * lane + e;
-            const float kp = sum_of(1, r) * fK[r];
-            if (r < len) a.dbeta[(t0 + r) * a.H + h] = sum_of(4, r) + kp;
-            d[e] = sum_of(0, r) * fQ[r] + t.beta[r] * kp - sum_of(2, r) * fK[r];
-            hd[e] = sum_of(3, r) * fK[r];
+            const float kp = sum_of(1, r, CG) * fK[r];
+            if (r < len) a.dbeta[(t0 + r) * a.H + h] = sum_of(6, r, 4) + kp;
+            d[e] = sum_of(0, r, CG) * fQ[r] + t.beta[r] * kp - (sum_of(4, r, CG) + sum_of(5, r, CG)) * fK[r];
+            hd[e] = (sum_of(2, r, CG) + sum_of(3, r, CG)) * fK[r];
         }
+        const float* dots = reinterpret_cast<const float*>(red[0]);
         const float carried = t.b[kC - 1] * ss.back * warp_sum(lane < NW ? dots[lane] : 0.f);
         float after = d[0] + d[1], before = hd[0] + hd[1];  // inclusive sums over the later, the earlier lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_down_sync(0xffffffffu, after, o), z = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane + o < 32) after += y;
-            if (lane >= o) before += z;
+            const float p = __shfl_down_sync(0xffffffffu, after, o), q = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane + o < 32) after += p;
+            if (lane >= o) before += q;
         }
         float later = __shfl_down_sync(0xffffffffu, after, 1), earlier = __shfl_up_sync(0xffffffffu, before, 1);
         if (lane == 31) later = 0.f;

@@ -10,10 +10,10 @@
 // would need three each (six terms) for the same accuracy, tf32 planes run at half the rate (measured
 // here: 600 TFLOP/s for fp16 and bf16, 300 for tf32, 75 for packed fp32 FMA).
 //
-// Planes are row-major with their 16-byte chunks XORed by the row (mod 8), so that the eight rows an
-// ldmatrix phase reads lie in different banks, and so do the pairs an accumulator writes.  Planes start
-// at multiples of their row size, so a step along a row is an XOR of the address and a step down an
-// addition.
+// Planes are laid out in blocks of 64 columns: rows of 128 bytes whose 16-byte chunks are XORed by the row
+// (mod 8), so that the eight rows an ldmatrix phase reads lie in different banks, and so do the pairs an
+// accumulator writes.  It is the 128-byte swizzle of tcgen05 operands too (blocks start at multiples of
+// 1024 bytes), so one tile serves both.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -23,16 +23,19 @@
 namespace gdn {
 namespace planes {
 
-// Byte offset of element (row, col) in a plane with COLS columns (64 or 128).
-template <int COLS>
+// Byte offset of element (row, col) in a plane with COLS columns (64 or 128), blocks of 64 columns HS apart.
+template <int COLS, int HS>
 __device__ __forceinline__ uint32_t offset(int row, int col) {
-    return (uint32_t)(row * COLS * 2 + ((col * 2) ^ ((row & 7) << 4)));
+    if constexpr (COLS == 64) return (uint32_t)(row * 128 + ((col * 2) ^ ((row & 7) << 4)));
+    else return (uint32_t)((col >> 6) * HS + row * 128 + (((col & 63) * 2) ^ ((row & 7) << 4)));
 }
 
-// A matrix of P planes of COLS columns in shared memory, LO bytes apart.
-template <int COLS, int P, int LO>
+// A matrix of P planes of COLS columns in shared memory: planes LO bytes apart, blocks of 64 columns HS.
+template <int COLS, int P, int LO, int HS>
 struct Mat {
+    static constexpr int lo = LO;
     uint32_t at;
+    __device__ __forceinline__ uint32_t operator()(int row, int col) const { return at + offset<COLS, HS>(row, col); }
 };
 
 template <int O>
@@ -56,27 +59,27 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 
 // Left operand, 16 x 16 blocks: stored [m][k] (T false) or [k][m] (T true).  lane_a is this lane's
 // address in block (m0, 0); load_a adds k0.
-template <int COLS, bool T>
-__device__ __forceinline__ uint32_t lane_a(uint32_t base, int m0, int lane) {
-    if constexpr (T) return base + offset<COLS>((lane & 7) + ((lane >> 4) << 3), m0 + (lane & 8));
-    else return base + offset<COLS>(m0 + (lane & 15), (lane >> 4) << 3);
+template <bool T, int COLS, int P, int LO, int HS>
+__device__ __forceinline__ uint32_t lane_a(Mat<COLS, P, LO, HS> A, int m0, int lane) {
+    if constexpr (T) return A((lane & 7) + ((lane >> 4) << 3), m0 + (lane & 8));
+    else return A(m0 + (lane & 15), (lane >> 4) << 3);
 }
-template <int COLS, bool T, int O>
+template <bool T, int O, int HS>
 __device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t lane_at, int k0) {
-    if constexpr (T) ldsm_t<O>(r, lane_at + k0 * COLS * 2);
-    else ldsm<O>(r, lane_at ^ (k0 * 2));
+    if constexpr (T) ldsm_t<O>(r, lane_at + k0 * 128);
+    else ldsm<O>(r, (lane_at ^ ((k0 & 63) * 2)) + (k0 >> 6) * HS);
 }
 // Right operand, 16 x 16 blocks (r[0], r[1]: columns n0 .. n0 + 7; r[2], r[3]: the next eight): stored
 // [n][k] (T false) or [k][n] (T true).  lane_b is this lane's address in block (0, 0).
-template <int COLS, bool T>
-__device__ __forceinline__ uint32_t lane_b(uint32_t base, int lane) {
-    if constexpr (T) return base + offset<COLS>(lane & 15, (lane >> 4) << 3);
-    else return base + offset<COLS>((lane & 7) + ((lane >> 4) << 3), lane & 8);
+template <bool T, int COLS, int P, int LO, int HS>
+__device__ __forceinline__ uint32_t lane_b(Mat<COLS, P, LO, HS> B, int lane) {
+    if constexpr (T) return B(lane & 15, (lane >> 4) << 3);
+    else return B((lane & 7) + ((lane >> 4) << 3), lane & 8);
 }
-template <int COLS, bool T, int O>
+template <bool T, int O, int HS>
 __device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t lane_at, int n0, int k0) {
-    if constexpr (T) ldsm_t<O>(r, (lane_at ^ (n0 * 2)) + k0 * COLS * 2);
-    else ldsm<O>(r, (lane_at + n0 * COLS * 2) ^ (k0 * 2));
+    if constexpr (T) ldsm_t<O>(r, (lane_at ^ ((n0 & 63) * 2)) + (n0 >> 6) * HS + k0 * 128);
+    else ldsm<O>(r, ((lane_at + n0 * 128) ^ ((k0 & 63) * 2)) + (k0 >> 6) * HS);
 }
 
 // Which 16-blocks of A's inner dimension can be non-zero: all, j <= i (A lower triangular), or j >= i.
@@ -84,28 +87,29 @@ enum Fill { kFull, kLower, kUpper };
 
 // acc += A B for this warp's row tiles m[] and the columns n0 .. n0 + 8 NT; TA, TB: stored transposed
 // (see lane_a, lane_b); K: inner dimension.
-template <int K, bool TA, bool TB, Fill F = kFull, int MT, int NT, int CA, int PA, int LA, int CB, int PB, int LB>
-__device__ __forceinline__ void product(float (&acc)[MT][NT][4], Mat<CA, PA, LA> A, const int (&m)[MT],
-                                        Mat<CB, PB, LB> B, int n0, int lane) {
+template <int K, bool TA, bool TB, Fill F = kFull, int MT, int NT, int CA, int PA, int LA, int HA, int CB, int PB, int LB,
+          int HB>
+__device__ __forceinline__ void product(float (&acc)[MT][NT][4], Mat<CA, PA, LA, HA> A, const int (&m)[MT],
+                                        Mat<CB, PB, LB, HB> B, int n0, int lane) {
     uint32_t la[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) la[i] = lane_a<CA, TA>(A.at, m[i], lane);
-    const uint32_t lb = lane_b<CB, TB>(B.at, lane);
+    for (int i = 0; i < MT; ++i) la[i] = lane_a<TA>(A, m[i], lane);
+    const uint32_t lb = lane_b<TB>(B, lane);
 #pragma unroll
     for (int k = 0; k < K; k += 16) {
         uint32_t a[PA][MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             if ((F == kLower && k > m[i]) || (F == kUpper && k < m[i])) continue;
-            load_a<CA, TA, 0>(a[0][i], la[i], k);
-            if constexpr (PA == 2) load_a<CA, TA, LA>(a[1][i], la[i], k);
+            load_a<TA, 0, HA>(a[0][i], la[i], k);
+            if constexpr (PA == 2) load_a<TA, LA, HA>(a[1][i], la[i], k);
         }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
             if (F != kFull && MT == 1 && ((F == kLower && k > m[0]) || (F == kUpper && k < m[0]))) continue;
             uint32_t b[PB][4];
-            load_b<CB, TB, 0>(b[0], lb, n0 + 8 * j, k);
-            if constexpr (PB == 2) load_b<CB, TB, LB>(b[1], lb, n0 + 8 * j, k);
+            load_b<TB, 0, HB>(b[0], lb, n0 + 8 * j, k);
+            if constexpr (PB == 2) load_b<TB, LB, HB>(b[1], lb, n0 + 8 * j, k);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 if ((F == kLower && k > m[i]) || (F == kUpper && k < m[i])) continue;
@@ -187,33 +191,39 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& x, uint32_t& y) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&x)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-// Address of the pair (i, j, h) of pairs() in a plane: n0 is a multiple of 8 NT.
-template <int COLS, int NT>
-__device__ __forceinline__ uint32_t pair_at(uint32_t base, int m, int n0, int j, int h, int lane) {
+// Address of the pair (i, j, h) of pairs() in a plane: n0 is a multiple of 8 NT, which divides 64.
+template <int NT, int COLS, int P, int LO, int HS>
+__device__ __forceinline__ uint32_t pair_at(Mat<COLS, P, LO, HS> a, int m, int n0, int j, int h, int lane) {
     const int g = lane >> 2;
-    const uint32_t first = base + (m + g) * COLS * 2 + ((n0 * 2) ^ (g << 4)) + (lane & 3) * 4;
-    return (first ^ (16 * j)) + 8 * h * COLS * 2;
+    const uint32_t first = a.at + (n0 >> 6) * HS + (m + g) * 128 + (((n0 & 63) * 2) ^ (g << 4)) + (lane & 3) * 4;
+    return (first ^ (16 * j)) + 8 * h * 128;
 }
 
 // Writes this warp's accumulators, times mul, into two planes.
-template <int COLS, int LO, int MT, int NT>
-__device__ __forceinline__ void write(Mat<COLS, 2, LO> dst, const float (&acc)[MT][NT][4], const int (&m)[MT], int n0,
+template <int COLS, int LO, int HS, int MT, int NT>
+__device__ __forceinline__ void write(Mat<COLS, 2, LO, HS> dst, const float (&acc)[MT][NT][4], const int (&m)[MT], int n0,
                                       int lane, float mul) {
     pairs<MT, NT>(m, n0, lane, [&](int i, int j, int h, int, int) {
         uint32_t hi, lo;
         split(acc[i][j][2 * h] * mul, acc[i][j][2 * h + 1] * mul, hi, lo);
-        const uint32_t at = pair_at<COLS, NT>(dst.at, m[i], n0, j, h, lane);
+        const uint32_t at = pair_at<NT>(dst, m[i], n0, j, h, lane);
         sts32(at, hi);
         sts32(at + LO, lo);
     });
 }
 
 // The pair (i, j, h) of a matrix, without its scale.
-template <int NT, int COLS, int P, int LO>
-__device__ __forceinline__ float2 read(Mat<COLS, P, LO> a, int m, int n0, int j, int h, int lane) {
-    const uint32_t at = pair_at<COLS, NT>(a.at, m, n0, j, h, lane);
+template <int NT, int COLS, int P, int LO, int HS>
+__device__ __forceinline__ float2 read(Mat<COLS, P, LO, HS> a, int m, int n0, int j, int h, int lane) {
+    const uint32_t at = pair_at<NT>(a, m, n0, j, h, lane);
     float2 x = halves(lds32(at));
     if constexpr (P == 2) {
         const float2 y = halves(lds32(at + LO));
@@ -221,6 +231,23 @@ __device__ __forceinline__ float2 read(Mat<COLS, P, LO> a, int m, int n0, int j,
         x.y += y.y;
     }
     return x;
+}
+
+// Eight consecutive elements of a row, from column col (a multiple of eight).
+template <int COLS, int P, int LO, int HS>
+__device__ __forceinline__ void read8(Mat<COLS, P, LO, HS> a, int row, int col, float (&x)[8]) {
+    const uint32_t at = a(row, col);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        uint32_t u[4];
+        lds128(at + p * LO, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = halves(u[i]);
+            x[2 * i] = p ? x[2 * i] + y.x : y.x;
+            x[2 * i + 1] = p ? x[2 * i + 1] + y.y : y.y;
+        }
+    }
 }
 
 template <int MT, int NT>
