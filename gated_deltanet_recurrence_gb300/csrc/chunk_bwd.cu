@@ -81,12 +81,18 @@ __device__ bool find_spans(const ChunkBwdArgs& a, const long (&slot)[N], Span (&
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k].n = -1;
     if (!a.cu_seqlens) {
-        const long per = ((long)(a.total_T / a.num_seqs) + kC - 1) / kC;
+        const int len = a.total_T / a.num_seqs, per = (len + kC - 1) / kC;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (slot[k] >= 0 && per > 0 && slot[k] < per * a.num_seqs) {
-                s[k] = seq_span(a, (int)(slot[k] / per));
-                s[k].c = (int)(slot[k] - s[k].base);
+            if (slot[k] >= 0 && per > 0) {
+                const int n = (int)slot[k] / per;
+                if (n >= a.num_seqs) continue;
+                s[k].n = n;
+                s[k].bos = (long)n * len;
+                s[k].eos = s[k].bos + len;
+                s[k].base = (long)n * per;
+                s[k].chunks = per;
+                s[k].c = (int)slot[k] - n * per;
             }
         return true;
     }
@@ -124,7 +130,7 @@ __device__ bool cu_valid(const ChunkBwdArgs& a) {
 // ---- workspace ---------------------------------------------------------------------------------
 // Per (slot, head):
 //   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
-//   T      planes of T
+//   T, P   planes of T and of P
 //   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
 //   S      S0 (fp32 [d, d])                             dS  X, then dS1 (fp32 [d, d])
 //   meta   scales and maxima
@@ -136,9 +142,10 @@ static_assert(sizeof(LinkTail) == 512, "");
 
 struct Meta {
     uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
-    float t_scale, pad[15];
+    float t_scale, p_scale, pad[14];
+    float p_diag[kC];  // P's diagonal, q_i . k_i
 };
-static_assert(sizeof(Meta) == 256, "");
+static_assert(sizeof(Meta) == 512, "");
 
 constexpr size_t kTBytes = 2 * kC * kC * sizeof(__half);
 __host__ __device__ constexpr size_t link_bytes(int d, int p) {
@@ -146,7 +153,7 @@ __host__ __device__ constexpr size_t link_bytes(int d, int p) {
 }
 
 struct Work {
-    unsigned char *link, *T;
+    unsigned char *link, *T, *P;
     float *U, *E, *S, *dS;
     Meta* meta;
     float *dq, *dk;  // [total_T, H, d] each, grouped heads only
@@ -161,7 +168,8 @@ __host__ __forceinline__ Work work_of(void* ws, size_t units, size_t tokens, int
     Work w;
     w.link = static_cast<unsigned char*>(ws);
     w.T = w.link + units * link_bytes(d, p);
-    w.U = reinterpret_cast<float*>(w.T + units * kTBytes);
+    w.P = w.T + units * kTBytes;
+    w.U = reinterpret_cast<float*>(w.P + units * kTBytes);
     w.E = w.U + units * kC * d;
     w.S = w.E + units * kC * d;
     w.dS = w.S + units * d * d;
@@ -285,7 +293,8 @@ struct Rows {
     // the other operand of a contraction must not differ much between rows: with use_l2 the norm sets
     // their size; without it all rows share the largest row's power of two (the block then synchronises
     // on *shared_top, which must be zero).
-    template <bool NORM, int LO, int HS>
+    // STORE false: the factors only.
+    template <bool NORM, bool STORE = true, int LO, int HS>
     __device__ __forceinline__ void put(Mat<D, P, LO, HS> dst, float* factor, float* inv, bool use_l2, float scale,
                                         uint32_t* shared_top, int warp, int lane) const {
         const int r = row(warp, lane);
@@ -329,7 +338,7 @@ struct Rows {
         }
         const Scale s = planes::scale_of(top);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; STORE && i < N; ++i) {
             const uint32_t at = dst(r, col(i, lane));
             if constexpr (P == 1) {
                 const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -362,17 +371,22 @@ __device__ __forceinline__ void prefetch(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// Asks for the rows of a chunk of one token tensor that a later block will read; all T threads.
+// Asks for the rows of a chunk of one token tensor that a later block will read, LINES of 128 bytes each;
+// all T threads.
+template <int T, int LINES>
+__device__ __forceinline__ void prefetch_lines(const char* src, const Span& s, int heads, int h) {
+    const long t0 = s.bos + (long)s.c * kC;
+    const int rows = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
+    const char* first = src + (t0 * heads + h) * (LINES * 128);
+#pragma unroll
+    for (int i = threadIdx.x; i < kC * LINES; i += T)
+        if (i / LINES < rows)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(first + (long)(i / LINES) * heads * (LINES * 128) + i % LINES * 128));
+}
 template <int T, int D>
 __device__ __forceinline__ void prefetch_rows(const void* src, gdn_dtype dt, const Span& s, int heads, int h) {
-    const int lines = dt == GDN_BF16 ? D / 64 : D / 32;  // of 128 bytes, a row
-    const long t0 = s.bos + (long)s.c * kC;
-    for (int i = threadIdx.x; i < kC * lines; i += T) {
-        const int r = i / lines;
-        if (t0 + r < s.eos)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(src) +
-                                                           (((t0 + r) * heads + h) * lines + i % lines) * 128));
-    }
+    if (dt == GDN_BF16) prefetch_lines<T, D / 64>(static_cast<const char*>(src), s, heads, h);
+    else prefetch_lines<T, D / 32>(static_cast<const char*>(src), s, heads, h);
 }
 
 // Blocks of one chunk each run for tens of microseconds with few loads of their own under way, so each
@@ -650,6 +664,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         float &x = qk[i][j][2 * hh], &y = qk[i][j][2 * hh + 1];
         x = c <= r ? x * (fQ[r] * fK[c]) * decay(gr, t.G[c]) : 0.f;
         y = c + 1 <= r ? y * (fQ[r] * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f;
+        if (c == r) w.meta[unit].p_diag[r] = x;
+        if (c + 1 == r) w.meta[unit].p_diag[r] = y;
     });
     {
         const uint32_t top = planes::max_bits(qk);
@@ -671,7 +687,9 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         acc[i][j][2 * hh + 1] = f * q.y - p * acc[i][j][2 * hh + 1];
     });
     copy_out<2 * PL / 16>(link, sm + L::W);
+    copy_out<(int)kTBytes / 16>(w.P + unit * kTBytes, sm + L::TX);
     if (tid == 0) {
+        w.meta[unit].p_scale = sp.back;
         tail.w_scale = w_scale;
         tail.b_last = t.b[kC - 1];
         w.meta[unit].t_scale = st.back;
@@ -952,7 +970,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
 }
 
 // ---- grad ----------------------------------------------------------------------------------------
-// The small products up to dR run on warp-level MMAs; those with the states, with U and with K and Q on
+// P comes from the preparation.  The small products up to dR run on warp-level MMAs; those with the states, with U and with K and Q on
 // tcgen05, whose accumulators (TMEM) leave the registers, and whose operands are read from shared memory
 // once per block instead of once per warp.  They are stacked so that M = 128 is full:
 //   D1 = [dY; dR] S0            rows 0 .. 63: dQ's, rows 64 .. 127: F's part from the state
@@ -1109,7 +1127,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     m[0] = 16 * mw;
     if constexpr (MT == 2) m[1] = 16 * (3 - mw);
     constexpr int NT = D / 32;
-    const int nd = nw * (D / 4), nc = nw * 16;
+    const int nd = nw * (D / 4);
     const Meta& meta = w.meta[unit];
     const float* S0 = w.S + unit * D * D;
     const float* dS1 = w.dS + unit * D * D;
@@ -1142,16 +1160,17 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         uint4 tt[kTBytes / 16 / T];
         k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
-        if constexpr (!L::share) y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
+        y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
         const uint4* src = reinterpret_cast<const uint4*>(w.T + unit * kTBytes);
 #pragma unroll
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) tt[i] = src[i * T + tid];
+        if (tid < kC) diag[tid] = meta.p_diag[tid];
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
         const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
         if (warp == NW - 1) gates.put(t, lane);
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
-        q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
-        if constexpr (!L::share) y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
+        q.template put<true, !L::share>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
+        y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
         // T's planes, each where SQ has T's: 512 vectors a plane
 #pragma unroll
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
@@ -1169,7 +1188,14 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         sds = planes::scale_of(__reduce_max_sync(0xffffffffu, top[1]));
         su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
-    const float t_back = meta.t_scale;
+    const float t_back = meta.t_scale, p_back = meta.p_scale;
+    uint4 pp[kTBytes / 16 / T];
+    {
+        const uint4* src = reinterpret_cast<const uint4*>(w.P + unit * kTBytes);
+#pragma unroll
+        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) pp[i] = src[i * T + tid];
+    }
+    state.fetch(S0);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -1182,55 +1208,43 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
         if (tid == 0) {
             prefetch(w.T + next * kTBytes, kTBytes);
+            prefetch(w.P + next * kTBytes, kTBytes);
             prefetch_states(next);
         }
     }
 
     float2 v[MT][NT][2];
     {
-        float qk[MT][2][4];  // P, with the rows' factors of dY for P^T dY
-        if constexpr (!L::share) state.fetch(S0);
-        planes::clear(qk);
-        planes::product<D, false, false>(qk, Q, m, K, nc, lane);
-        if constexpr (L::share) {
-            Rows<NW, D, P> y;
-            y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
-            __syncthreads();
-            y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
-            __syncthreads();
-        }
-        planes::pairs<MT, 2>(m, nc, lane, [&](int i, int j, int hh, int r, int c) {
-            const float2 gr = t.G[r];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float& x = qk[i][j][2 * hh + e];
-                const float p = c + e <= r ? x * (fQ[r] * fK[c + e]) * decay(gr, t.G[c + e]) : 0.f;
-                if (c + e == r) diag[r] = p;  // q_r . k_r for now
-                x = p * fY[r];
-            }
-        });
-        const uint32_t top = planes::max_bits(qk);
-        if (lane == 0) red[0][warp] = top;
-        __syncthreads();
-        const Scale sp = planes::scale_of(planes::top_of<NW>(red[0], lane));
-        planes::write(Pm, qk, m, nc, lane, sp.mul);
-        if constexpr (L::share) state.fetch(S0);
         float2 e0[MT][NT][2];
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
             const float* e = w.E + (unit * D + c) * kC + r;
             e0[i][j][hh] = make_float2(e[0], e[kC]);
         });
-        state.template put<false>(ST, ss.mul);
-        __syncthreads();
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
             v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
         });
+        // P with the rows' factors of dY, powers of two, which P^T dY contracts over
+        float fY_top = fmaxf(fY[lane], fY[lane + 32]);
+        fY_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fY_top)));
+        const float fY_inv = 1.f / fY_top;
+#pragma unroll
+        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
+            const int e = i * T + tid;
+            const __half2 f = __float2half2_rn(fY[(e & 511) >> 3] * fY_inv);
+            __half2* x = reinterpret_cast<__half2*>(&pp[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = __hmul2(x[j], f);
+            *reinterpret_cast<uint4*>(sm + L::SQ + (e >> 9) * 2 * HF + (e & 511) * 16) = pp[i];
+        }
+        const float pu = p_back * fY_top;
+        state.template put<false>(ST, ss.mul);
+        __syncthreads();
         float acc[MT][NT][4];  // P^T dY + E
         planes::clear(acc);
         planes::product<kC, true, true, planes::kUpper>(acc, Pm, m, Y, nd, lane);
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], sp.back, e0[i][j][hh].x);
-            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], sp.back, e0[i][j][hh].y);
+            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], pu, e0[i][j][hh].x);
+            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], pu, e0[i][j][hh].y);
         });
         const uint32_t top2 = planes::max_bits(acc);
         if (lane == 0) red[1][warp] = top2;
@@ -1306,7 +1320,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             const float y = __uint_as_float(raw[i]) * f * decay(gr, t.G[c]);
             if (c == row && part == 0) {
                 dpp[row] = y;
-                diag[row] *= y;
+                diag[row] *= y;  // dP_ii q_i . k_i
             }
             x[i] = c < row ? y : 0.f;
             top1 = max(top1, planes::abs_bits(x[i] * fK[c]));
@@ -1572,7 +1586,7 @@ cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
 
 size_t chunk_bwd_workspace_bytes(int num_seqs, int total_T, int H, int Hk, int d) {
     const size_t units = (size_t)slot_count(num_seqs, total_T) * H;
-    const size_t unit = link_bytes(d, 2) + kTBytes + sizeof(float) * (2 * kC * d + 2 * d * d) + sizeof(Meta);
+    const size_t unit = link_bytes(d, 2) + 2 * kTBytes + sizeof(float) * (2 * kC * d + 2 * d * d) + sizeof(Meta);
     return units * unit + (H > Hk ? 2 * sizeof(float) * total_T * H * d : 0);
 }
 
