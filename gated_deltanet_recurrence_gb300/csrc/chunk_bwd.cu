@@ -73,10 +73,36 @@ __device__ __forceinline__ Span seq_span(const ChunkBwdArgs& a, int n) {
     return s;
 }
 
+// Above this many sequences a kernel of its own looks cu_seqlens over and writes down each slot's sequence;
+// up to it every block does so for itself, which saves the launch (four loads a thread at most).
+constexpr int kScanSeqs = 1024;
+
+// index[0]: whether cu_seqlens is well formed; index[1 + slot]: the slot's sequence, or -1.  One block.
+__global__ void __launch_bounds__(1024) chunk_bwd_index_kernel(ChunkBwdArgs a, int* index, int slots) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < a.num_seqs; i += 1024) {
+        const int lo = a.cu_seqlens[i], hi = a.cu_seqlens[i + 1];
+        bad |= lo < 0 || hi < lo || hi > a.total_T;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+        index[0] = !bad;
+        if (bad) record_error(a.err, GDN_ERR_CU_SEQLENS);
+    }
+    if (bad) return;
+    for (int i = threadIdx.x; i < slots; i += 1024) index[1 + i] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.num_seqs; i += 1024) {
+        const int lo = a.cu_seqlens[i], hi = a.cu_seqlens[i + 1];
+        for (int c = 0; c * kC < hi - lo; ++c) index[1 + lo / kC + i + c] = i;
+    }
+}
+
 // Whether cu_seqlens is monotone and inside [0, total_T]; finds the spans of N slots, whose n is -1 for an
-// unused slot.  All threads take part; contains block barriers.
+// unused slot.  All threads take part; contains block barriers.  `index` is null or what
+// chunk_bwd_index_kernel wrote.
 template <int N>
-__device__ bool find_spans(const ChunkBwdArgs& a, const long (&slot)[N], Span (&s)[N]) {
+__device__ bool find_spans(const ChunkBwdArgs& a, const int* index, const long (&slot)[N], Span (&s)[N]) {
     __shared__ int found[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k].n = -1;
@@ -96,35 +122,44 @@ __device__ bool find_spans(const ChunkBwdArgs& a, const long (&slot)[N], Span (&
             }
         return true;
     }
-    if (threadIdx.x < N) found[threadIdx.x] = -1;
-    __syncthreads();
-    bool bad = false;
-    for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x) {
-        const int lo = a.cu_seqlens[i], hi = a.cu_seqlens[i + 1];
-        bad |= lo < 0 || hi < lo || hi > a.total_T;
+    int n[N];
+    if (index) {
+        if (!index[0]) return false;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const long c = slot[k] - (lo / kC + i);
-            if (c >= 0 && c * kC < (long)hi - lo) found[k] = i;  // at most one i where no entry is bad
+        for (int k = 0; k < N; ++k) n[k] = slot[k] >= 0 ? index[1 + slot[k]] : -1;
+    } else {
+        if (threadIdx.x < N) found[threadIdx.x] = -1;
+        __syncthreads();
+        bool bad = false;
+        for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x) {
+            const int lo = a.cu_seqlens[i], hi = a.cu_seqlens[i + 1];
+            bad |= lo < 0 || hi < lo || hi > a.total_T;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const long c = slot[k] - (lo / kC + i);
+                if (slot[k] >= 0 && c >= 0 && c * kC < (long)hi - lo) found[k] = i;  // one i at most, where none is bad
+            }
         }
-    }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) record_error(a.err, GDN_ERR_CU_SEQLENS);
-        return false;
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0) record_error(a.err, GDN_ERR_CU_SEQLENS);
+            return false;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) n[k] = found[k];
     }
 #pragma unroll
     for (int k = 0; k < N; ++k)
-        if (found[k] >= 0) {
-            s[k] = seq_span(a, found[k]);
+        if (n[k] >= 0) {
+            s[k] = seq_span(a, n[k]);
             s[k].c = (int)(slot[k] - s[k].base);
         }
     return true;
 }
 
-__device__ bool cu_valid(const ChunkBwdArgs& a) {
+__device__ bool cu_valid(const ChunkBwdArgs& a, const int* index) {
     const long none[1] = {-1};
     Span s[1];
-    return find_spans<1>(a, none, s);
+    return find_spans<1>(a, index, none, s);
 }
 
 // ---- workspace ---------------------------------------------------------------------------------
@@ -157,6 +192,7 @@ struct Work {
     float *U, *E, *S, *dS;
     Meta* meta;
     float *dq, *dk;  // [total_T, H, d] each, grouped heads only
+    int* index;      // 1 + slots, many sequences only (else null)
 };
 
 // K's planes in the link: one where the inputs are bf16 throughout (it holds them exactly), else two.
@@ -164,9 +200,12 @@ __host__ __forceinline__ int input_planes(gdn_dtype qkv, gdn_dtype dout) {
     return qkv == GDN_BF16 && dout == GDN_BF16 ? 1 : 2;
 }
 
-__host__ __forceinline__ Work work_of(void* ws, size_t units, size_t tokens, int d, int p) {
+__host__ __forceinline__ size_t index_bytes(size_t slots) { return ((1 + slots) * sizeof(int) + 255) / 256 * 256; }
+
+__host__ __forceinline__ Work work_of(void* ws, size_t slots, size_t units, size_t tokens, int d, int p, bool index) {
     Work w;
-    w.link = static_cast<unsigned char*>(ws);
+    w.index = index ? static_cast<int*>(ws) : nullptr;
+    w.link = static_cast<unsigned char*>(ws) + index_bytes(slots);
     w.T = w.link + units * link_bytes(d, p);
     w.P = w.T + units * kTBytes;
     w.U = reinterpret_cast<float*>(w.P + units * kTBytes);
@@ -208,11 +247,14 @@ __device__ __forceinline__ float2 add2(float2 p, float2 q) {
 struct GateRows {
     float g[2], beta[2];
 
+    // A log-decay below -128 is taken as -128: e^-128 is zero in fp32 either way, and the sums keep their
+    // precision for the tokens behind one that forgets everything (g = -inf included).
     __device__ __forceinline__ void fetch(const ChunkBwdArgs& a, long t0, int len, int h, int lane) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const bool in = 2 * lane + e < len;
             g[e] = in ? a.g[(t0 + 2 * lane + e) * a.H + h] : 0.f;
+            g[e] = g[e] < -128.f ? -128.f : g[e];
             beta[e] = in ? a.beta[(t0 + 2 * lane + e) * a.H + h] : 0.f;
         }
     }
@@ -538,7 +580,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
     Span spans[2];
-    if (!find_spans<2>(a, slots, spans) || spans[0].n < 0) return;
+    if (!find_spans<2>(a, w.index, slots, spans) || spans[0].n < 0) return;
     const Span& s = spans[0];
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
@@ -961,7 +1003,7 @@ template <int D, int P>
 __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBwdArgs a, Work w) {
     extern __shared__ __align__(1024) unsigned char sm[];
     constexpr int slices = D / 64;
-    if (!cu_valid(a)) return;
+    if (!cu_valid(a, w.index)) return;
     dependency_wait();
     const int unit = blockIdx.x / slices, slice = blockIdx.x % slices;
     const Span s = seq_span(a, unit / a.H);
@@ -1099,7 +1141,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
     Span spans[2];
-    if (!find_spans<2>(a, slots, spans) || spans[0].n < 0) return;
+    if (!find_spans<2>(a, w.index, slots, spans) || spans[0].n < 0) return;
     dependency_wait();
     const Span& s = spans[0];
     const int h = blockIdx.x % a.H, rep = a.H / a.Hk, hk = h / rep, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1529,15 +1571,20 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         if (lane == 31) later = 0.f;
         if (lane == 0) earlier = 0.f;
         const int r = 2 * lane;
-        if (r < len) a.dg[(t0 + r) * a.H + h] = (later + d[1] + d[0]) + earlier + carried;
-        if (r + 1 < len) a.dg[(t0 + r + 1) * a.H + h] = (later + d[1]) + (earlier + hd[0]) + carried;
+        const float dg[2] = {(later + d[1] + d[0]) + earlier + carried, (later + d[1]) + (earlier + hd[0]) + carried};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (r + e < len) {  // nothing passes a decay to zero: no gradient, where the sums leave a rounding
+                const long at = (t0 + r + e) * a.H + h;
+                a.dg[at] = a.g[at] < -128.f ? 0.f : dg[e];
+            }
     }
 }
 
 // dq, dk of grouped heads: the sum over the group's value heads, in order.  Tokens outside every
 // sequence are left as they were.
 __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdArgs a, Work w) {
-    if (!cu_valid(a)) return;
+    if (!cu_valid(a, w.index)) return;
     dependency_wait();
     const int rep = a.H / a.Hk;
     const long first = a.cu_seqlens ? a.cu_seqlens[0] : 0;
@@ -1559,8 +1606,9 @@ __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdA
 
 template <int D, int P>
 cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
-    const size_t units = (size_t)slot_count(a.num_seqs, a.total_T) * a.H;
-    const Work w = work_of(a.workspace, units, (size_t)a.total_T * a.H, D, P);
+    const size_t slots = (size_t)slot_count(a.num_seqs, a.total_T), units = slots * a.H;
+    const bool index = a.cu_seqlens && a.num_seqs > kScanSeqs;
+    const Work w = work_of(a.workspace, slots, units, (size_t)a.total_T * a.H, D, P, index);
     const int prep = PrepSmem<D, P>::bytes, grad = GradSmem<D, P>::bytes, scan = scan_bytes(D, P);
     auto allow = [](const void* f, int bytes) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1570,13 +1618,21 @@ cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = allow(reinterpret_cast<const void*>(chunk_bwd_scan_kernel<D, P>), scan);
     if (e == cudaSuccess) e = allow(reinterpret_cast<const void*>(chunk_bwd_grad_kernel<D, P>), grad);
     if (e != cudaSuccess) return e;
-    if (a.total_T > 0) {
-        chunk_bwd_prep_kernel<D, P><<<(unsigned)units, kPrepThreads, prep, s>>>(a, w);
+    if (index) {
+        chunk_bwd_index_kernel<<<1, 1024, 0, s>>>(a, w.index, (int)slots);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
+    // The first kernel is launched plainly: what it reads may come from the kernel before it.  Those behind
+    // it may read the inputs and the index (both complete before it) ahead of dependency_wait(), but nothing else.
     const dim3 chains((unsigned)(a.num_seqs * a.H * (D / 64)), 2);
+    if (a.total_T == 0) {
+        chunk_bwd_scan_kernel<D, P><<<chains, kScanThreads, scan, s>>>(a, w);
+        return cudaGetLastError();
+    }
+    chunk_bwd_prep_kernel<D, P><<<(unsigned)units, kPrepThreads, prep, s>>>(a, w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_after(chunk_bwd_scan_kernel<D, P>, chains, kScanThreads, scan, s, a, w);
-    if (e != cudaSuccess || a.total_T == 0) return e;
+    if (e != cudaSuccess) return e;
     e = launch_after(chunk_bwd_grad_kernel<D, P>, dim3((unsigned)units), GradSmem<D, P>::threads, grad, s, a, w);
     if (e != cudaSuccess || a.H == a.Hk) return e;
     return launch_after(chunk_bwd_heads_kernel, dim3(kSMs * 8), kPrepThreads, 0, s, a, w);
@@ -1585,9 +1641,9 @@ cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t chunk_bwd_workspace_bytes(int num_seqs, int total_T, int H, int Hk, int d) {
-    const size_t units = (size_t)slot_count(num_seqs, total_T) * H;
+    const size_t slots = (size_t)slot_count(num_seqs, total_T), units = slots * H;
     const size_t unit = link_bytes(d, 2) + 2 * kTBytes + sizeof(float) * (2 * kC * d + 2 * d * d) + sizeof(Meta);
-    return units * unit + (H > Hk ? 2 * sizeof(float) * total_T * H * d : 0);
+    return index_bytes(slots) + units * unit + (H > Hk ? 2 * sizeof(float) * total_T * H * d : 0);
 }
 
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs& a, cudaStream_t s) {

@@ -132,8 +132,9 @@ size_t gdn_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int d_k, i
  * forward call: the states at the chunk starts are recomputed.
  *
  *   q, k, v, g, beta, cu_seqlens, num_seqs, total_T, H, H_k, d_k, d_v, qkv_dtype, scale,
- *   use_qk_l2norm, initial_state   as given to gdn_chunk_fwd; g finite.  decay must be
- *                 GDN_DECAY_PER_HEAD (GDN_DECAY_PER_KEY_CHANNEL returns GDN_ERR_UNSUPPORTED).
+ *   use_qk_l2norm, initial_state   as given to gdn_chunk_fwd (g <= 0; a g below -128, -inf
+ *                 included, is a decay to zero).  decay must be GDN_DECAY_PER_HEAD
+ *                 (GDN_DECAY_PER_KEY_CHANNEL returns GDN_ERR_UNSUPPORTED).
  *   dout          [total_T, H, d_v] of dout_dtype: the gradient of out.
  *   dfinal_state  [num_seqs, H, d_v, d_k] fp32, or NULL for zeros: the gradient of final_state.
  *   dq, dk        [total_T, H_k, d_k] of qkv_dtype (with grouped heads, summed over the value heads

@@ -21,8 +21,10 @@ def tol_of(t):
 
 
 def rel_l2(x, ref):
-    """||x - ref|| / ||ref||, and 0 where both are zero."""
+    """||x - ref|| / ||ref||, and 0 where both are zero.  A reference below 2^-150 counts as zero: half the
+    smallest fp32 (and bf16) magnitude, 2^-149 (2^-133), is its nearest representable neighbour's border."""
     x, ref = x.detach().cpu().to(F64), ref.detach().cpu().to(F64)
+    ref = torch.where(ref.abs() < 2.0 ** -150, torch.zeros_like(ref), ref)
     assert x.shape == ref.shape, (x.shape, ref.shape)
     assert torch.isfinite(x).all()
     off, norm = float((x - ref).norm()), float(ref.norm())

@@ -123,6 +123,101 @@ def test_chunk_bwd_empty_batch_passes_the_state_gradient_through():
     assert got["dq"].numel() == 0
 
 
+@pytest.mark.parametrize("reset", [-float("inf"), -3e38, -200.0])
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, F32)])
+def test_chunk_bwd_decay_to_zero(d, dtype, reset):
+    """Tokens that forget everything (documents packed into one sequence): nothing passes them, and the
+    tokens behind them keep their own decays."""
+    inp = delta_inputs([180], 2, 2, d, dtype, seed=17)
+    for t in (0, 30, 31, 64, 130):
+        inp["g"][t] = reset
+    got = chunk_bwd(inp)
+    check_chunk(inp, got)
+    assert torch.count_nonzero(got["dinitial_state"]) == 0
+    assert torch.count_nonzero(got["dg"][[0, 30, 31, 64, 130]]) == 0
+
+
+def test_chunk_bwd_many_sequences():
+    """More sequences than a block looks over by itself."""
+    gen = torch.Generator().manual_seed(2)
+    lengths = torch.randint(0, 3, (1500,), generator=gen).tolist()
+    lengths[700] = 130
+    inp = delta_inputs(lengths, 2, 1, 64, F32, seed=3)
+    check_chunk(inp, chunk_bwd(inp))
+    inp["cu"][900] += 5
+    inp["cu"][901] = inp["cu"][900] - 1
+    outs = {x: torch.full_like(dev(inp[x[1:]]), 3.5) for x in ("dq", "dk", "dv", "dg", "dbeta")}
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    gdn.gdn_chunk_bwd(*args, cu_seqlens=torch.tensor(inp["cu"], dtype=torch.int32, device="cuda"), **outs)
+    assert gdn.gdn_get_device_error() == -3
+    assert all((x == 3.5).all() for x in outs.values())
+
+
+def test_chunk_bwd_degenerate_values():
+    """Zero queries and keys, no update (beta = 0), full overwrite without decay."""
+    for mode in ("zero", "beta0", "full"):
+        inp = delta_inputs([100, 30], 2, 2, 128, BF16, seed=21)
+        if mode == "zero":
+            inp["q"][::5] = 0
+            inp["k"][::7] = 0
+            inp["dout"][::3] = 0
+        elif mode == "beta0":
+            inp["beta"].zero_()
+        else:
+            inp["beta"].fill_(1.0)
+            inp["g"].zero_()
+        check_chunk(inp, chunk_bwd(inp))
+
+
+@pytest.mark.parametrize("big,small", [(2.0 ** 60, 2.0 ** -70), (2.0 ** -50, 2.0 ** 40)])
+def test_chunk_bwd_scales_with_its_inputs(big, small):
+    """Values (and the output's gradient) far from one: v and the states times a power of two, dout and
+    dfinal_state times another, scale every output by exact powers of two."""
+    inp = delta_inputs([150, 7], 2, 1, 128, BF16, seed=23)
+    one = chunk_bwd(inp)
+    far = dict(inp, v=inp["v"] * big, initial_state=inp["initial_state"] * big, dout=inp["dout"] * small,
+               dfinal_state=inp["dfinal_state"] * small)
+    got = chunk_bwd(far)
+    for name, f in (("dq", big * small), ("dk", big * small), ("dg", big * small), ("dbeta", big * small),
+                    ("dv", small), ("dinitial_state", small)):
+        assert torch.equal(got[name], one[name] * f), name
+
+
+def _streams_and_graph(call):
+    """The call's result eagerly, on a side stream beside another call, and from a replayed graph."""
+    eager = [x for x in call() if x is not None]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = call(stream=side)
+    b = call()
+    c = call(stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = call()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for other in (a, b, c, g):
+        for x, y in zip(eager, [x for x in other if x is not None]):
+            assert torch.equal(x, y)
+
+
+def test_calls_on_streams_and_in_graphs():
+    inp = delta_inputs([200, 0, 70, 33], 4, 2, 128, BF16, seed=41)
+    cu = torch.tensor(inp["cu"], dtype=torch.int32, device="cuda")
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    S0, dS = dev(inp["initial_state"]), dev(inp["dfinal_state"])
+    _streams_and_graph(lambda **kw: gdn.gdn_chunk_bwd(*args, cu_seqlens=cu, initial_state=S0, dfinal_state=dS, **kw))
+    x = _norm_inputs(300, 4, 64, BF16, seed=2)
+    y, z, w, b, do = (dev(x[k]) for k in ("y", "z", "w", "b", "dout"))
+    _streams_and_graph(lambda **kw: gdn.gdn_gate_groupnorm_silu_bwd(do, y, z, w, b, **kw))
+    _streams_and_graph(lambda **kw: gdn.gdn_gate_rmsnorm_silu_bwd(do, y, z, w[0].contiguous(), **kw))
+    _streams_and_graph(lambda **kw: (gdn.gdn_gate_groupnorm_silu(y, z, w, b, **kw),))
+    a = torch.randn(777, 8, device="cuda")
+    _streams_and_graph(lambda **kw: gdn.gdn_decay_from_logits_bwd(a, a[0].contiguous(), a[1].contiguous(), a, a, a, **kw))
+
+
 # ---- norms -----------------------------------------------------------------------------------------
 
 def _norm_inputs(rows, groups, size, dtype, seed):
@@ -226,6 +321,16 @@ def test_decay_bwd_of_no_tokens_gives_zero_sums():
     a = torch.empty(0, 5, device="cuda")
     _, dA, ddt, _ = gdn.gdn_decay_from_logits_bwd(a, torch.ones(5, device="cuda"), torch.ones(5, device="cuda"), a, a, a)
     assert torch.count_nonzero(dA) == 0 and torch.count_nonzero(ddt) == 0
+
+
+def test_decay_bwd_in_place():
+    a, dg, b, dbeta = (torch.randn(100, 7, device="cuda") for _ in range(4))
+    A = torch.rand(7, device="cuda")
+    ref = gdn.gdn_decay_from_logits_bwd(a, A, None, b, dg, dbeta)
+    a2, b2 = a.clone(), b.clone()
+    got = gdn.gdn_decay_from_logits_bwd(a2, A, None, b2, dg, dbeta, da=a2, db=b2)
+    for x, y in zip(ref, got):
+        assert (x is None and y is None) or torch.equal(x, y)
 
 
 # ---- together ------------------------------------------------------------------------------------------
