@@ -333,6 +333,65 @@ def test_decay_bwd_in_place():
         assert (x is None and y is None) or torch.equal(x, y)
 
 
+# ---- guard bands -----------------------------------------------------------------------------------------
+
+GUARD = 64
+
+
+def _guarded(shape, dtype):
+    """A tensor of `shape` between two bands of GUARD sentinel elements; returns (tensor, whole buffer)."""
+    n = 1
+    for x in shape:
+        n *= x
+    buf = torch.full((GUARD + n + GUARD,), 7.0 if dtype != torch.uint8 else 7, dtype=dtype, device="cuda")
+    return buf[GUARD:GUARD + n].view(shape), buf
+
+
+def _intact(bufs):
+    torch.cuda.synchronize()
+    return all(bool((b[:GUARD] == 7).all()) and bool((b[-GUARD:] == 7).all()) for b in bufs)
+
+
+def _workspace(need):
+    """`need` bytes, 256-byte aligned, between two bands."""
+    buf = torch.full((256 + need + GUARD,), 7, dtype=torch.uint8, device="cuda")
+    return buf[256:256 + need], buf[256 - GUARD:]
+
+
+@pytest.mark.parametrize("d,dtype,Hk", [(128, BF16, 2), (128, F32, 1), (64, BF16, 1), (64, F32, 2)])
+def test_chunk_bwd_stays_inside_its_outputs(d, dtype, Hk):
+    inp = delta_inputs([1, 0, 130, 64, 63], 2, Hk, d, dtype, seed=50)
+    bufs, outs = [], {}
+    for x in ("dq", "dk", "dv", "dg", "dbeta"):
+        outs[x], b = _guarded(tuple(inp[x[1:]].shape), inp[x[1:]].dtype)
+        bufs.append(b)
+    outs["dinitial_state"], b = _guarded(tuple(inp["initial_state"].shape), F32)
+    bufs.append(b)
+    T = inp["q"].shape[0]
+    ws, b = _workspace(gdn.lib().gdn_chunk_bwd_workspace_size(5, T, 2, Hk, d, d))
+    bufs.append(b)
+    check_chunk(inp, chunk_bwd(inp, workspace=ws, **outs))
+    assert _intact(bufs)
+
+
+@pytest.mark.parametrize("rows,groups,size,dtype", [(7, 3, 41, BF16), (1, 2, 64, F32), (300, 5, 128, BF16), (3, 400, 8, F32)])
+def test_norms_and_gates_stay_inside_their_outputs(rows, groups, size, dtype):
+    x = _norm_inputs(rows, groups, size, dtype, seed=4)
+    y, z, w, b, do = (dev(x[k]) for k in ("y", "z", "w", "b", "dout"))
+    shapes = dict(dy=(y.shape, dtype), dz=(y.shape, F32), dweight=(w.shape, F32), dbias=(w.shape, F32))
+    outs = {k: _guarded(tuple(s), t) for k, (s, t) in shapes.items()}
+    ws, band = _workspace(gdn.lib().gdn_gate_bwd_workspace_size(rows, groups, size))
+    gdn.gdn_gate_groupnorm_silu_bwd(do, y, z, w, b, workspace=ws, **{k: v[0] for k, v in outs.items()})
+    out, out_buf = _guarded(tuple(y.shape), dtype)
+    gdn.gdn_gate_groupnorm_silu(y, z, w, b, out=out)
+    H = groups * size
+    a = torch.randn(rows, H, device="cuda")
+    dec = [_guarded((rows, H), F32), _guarded((H,), F32), _guarded((H,), F32), _guarded((rows, H), F32)]
+    ws2, band2 = _workspace(gdn.lib().gdn_decay_bwd_workspace_size(rows, H))
+    gdn.gdn_decay_from_logits_bwd(a, a[0].contiguous(), a[0].contiguous(), a, a, a, *[t for t, _ in dec], workspace=ws2)
+    assert _intact([v[1] for v in outs.values()] + [band, out_buf, band2] + [v for _, v in dec])
+
+
 # ---- together ------------------------------------------------------------------------------------------
 
 def test_training_step_together():
