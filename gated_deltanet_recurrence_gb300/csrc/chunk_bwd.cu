@@ -1119,12 +1119,20 @@ __device__ __forceinline__ void store8(void* dst, gdn_dtype dt, long i, const fl
 template <int STEPS, int N, bool AMN, bool BMN>
 __device__ __forceinline__ void issue(uint32_t d, uint32_t A, int a_block, uint32_t B, int b_block, bool accumulate) {
     constexpr uint32_t id = ptx::idesc_f16(128, N, AMN, BMN);
+    // a step adds to the descriptors' start addresses (in units of 16 bytes), which never carry out
+    const uint64_t da = ptx::sdesc_sw128(A, AMN ? a_block : 16, 1024), db = ptx::sdesc_sw128(B, BMN ? b_block : 16, 1024);
+    const uint32_t a_hi = (uint32_t)(da >> 32), b_hi = (uint32_t)(db >> 32), a_lo = (uint32_t)da, b_lo = (uint32_t)db;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
         const uint32_t ao = AMN ? k * 2048 : (k >> 2) * a_block + (k & 3) * 32;
         const uint32_t bo = BMN ? k * 2048 : (k >> 2) * b_block + (k & 3) * 32;
-        ptx::mma_bf16_ss(d, ptx::sdesc_sw128(A + ao, AMN ? a_block : 16, 1024),
-                         ptx::sdesc_sw128(B + bo, BMN ? b_block : 16, 1024), id, accumulate || k > 0);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+            "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a_lo + (ao >> 4)), "r"(a_hi),
+            "r"(b_lo + (bo >> 4)), "r"(b_hi), "r"(id), "r"((uint32_t)(accumulate || k > 0))
+            : "memory");
     }
 }
 
