@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "gdn_internal.cuh"
+#include "train_internal.cuh"
 
 namespace {
 

@@ -30,9 +30,9 @@
 //
 // Every product is taken on the tensor cores from fp16 planes at fp32 accuracy (mma_planes.cuh); what is
 // between the products is fp32.
-#include "gdn_internal.cuh"
 #include "mma_planes.cuh"
 #include "sm100_ptx.cuh"
+#include "train_internal.cuh"
 
 namespace gdn {
 namespace {
@@ -1113,12 +1113,28 @@ __device__ __forceinline__ void store8(void* dst, gdn_dtype dt, long i, const fl
     }
 }
 
+// f16 x f16 -> f32, dense; a_mn / b_mn select MN-major operands
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 16 consecutive 32-bit TMEM columns of this thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 // One pass of tcgen05 MMAs over an inner dimension of 16 STEPS, by one thread: D (+)= A B.  A and B are
 // shared addresses of 128-byte-swizzled tiles; MN: stored [inner][outer], blocks of 64 outer elements
 // `block` bytes apart; otherwise stored [outer][inner], blocks of 64 inner elements `block` bytes apart.
 template <int STEPS, int N, bool AMN, bool BMN>
 __device__ __forceinline__ void issue(uint32_t d, uint32_t A, int a_block, uint32_t B, int b_block, bool accumulate) {
-    constexpr uint32_t id = ptx::idesc_f16(128, N, AMN, BMN);
+    constexpr uint32_t id = idesc_f16(128, N, AMN, BMN);
     // a step adds to the descriptors' start addresses (in units of 16 bytes), which never carry out
     const uint64_t da = ptx::sdesc_sw128(A, AMN ? a_block : 16, 1024), db = ptx::sdesc_sw128(B, BMN ? b_block : 16, 1024);
     const uint32_t a_hi = (uint32_t)(da >> 32), b_hi = (uint32_t)(db >> 32), a_lo = (uint32_t)da, b_lo = (uint32_t)db;
@@ -1359,7 +1375,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     wait(0, 0);
     {
         uint32_t raw[NC];
-        if constexpr (NC == 16) ptx::tmem_ld16(lanes + L::tNZ + cg * NC, raw);
+        if constexpr (NC == 16) tmem_ld16(lanes + L::tNZ + cg * NC, raw);
         else ptx::tmem_ld32(lanes + L::tNZ + cg * NC, raw);
         ptx::tmem_wait_ld();
         const float2 gr = t.G[row];

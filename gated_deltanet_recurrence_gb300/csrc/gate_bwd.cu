@@ -16,7 +16,7 @@
 //
 // Sums over rows end in a table of partial sums in the workspace, which a second kernel adds up
 // column by column in a fixed order: no atomics, so the same call gives the same bits.
-#include "gdn_internal.cuh"
+#include "train_internal.cuh"
 
 namespace gdn {
 namespace {
