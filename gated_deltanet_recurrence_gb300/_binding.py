@@ -70,6 +70,8 @@ class GdnError(RuntimeError):
 def lib():
     """Load libgdn.so (building it first if it is missing or older than its sources)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             from . import build as _build
@@ -129,21 +131,23 @@ def _sizes(ref, **tensors):
             raise ValueError(f"{name} holds {t.numel()} elements; the call touches {numel}")
 
 
-def _pointers(ref, *tensors):
-    """The checks of _f32, _sizes and _p in one pass, for calls whose host side is their time: each of
-    `tensors` is (name, tensor or None, elements the call touches, fp32 only).  Returns the pointers."""
-    dev, dense, out = ref.get_device(), True, []
-    for name, t, numel, f32 in tensors:
+def _pointers(ref, names, tensors, sizes, fp32):
+    """The checks of _f32, _sizes and _p in one pass, for calls whose host side is their time: for each of
+    `tensors` (None where not given) its name, the elements the call touches, and whether it must be fp32.
+    Returns the pointers."""
+    dev, dense, out, f32 = ref.get_device(), True, [], torch.float32
+    for name, t, numel, only32 in zip(names, tensors, sizes, fp32):
         if t is None:
             out.append(None)
             continue
-        if f32 and t.dtype is not torch.float32:
+        if only32 and t.dtype is not f32:
             raise TypeError(f"{name} must be float32")
         if t.get_device() != dev or (dev < 0 and t.device != ref.device):
             raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
         if t.numel() < numel:
             raise ValueError(f"{name} holds {t.numel()} elements; the call touches {numel}")
-        dense = dense and t.is_contiguous()
+        if not t.is_contiguous():
+            dense = False
         out.append(t.data_ptr())
     if not ref.is_cuda:
         raise ValueError("all tensors must be CUDA tensors")
@@ -404,7 +408,7 @@ def _workspace(workspace, need, ref):
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=ref.device)
         return workspace, workspace.data_ptr(), need
-    ptr, = _pointers(ref, ("workspace", workspace, 0, False))
+    ptr, = _pointers(ref, ("workspace",), (workspace,), (0,), (False,))
     return workspace, ptr, workspace.numel() * workspace.element_size()
 
 
@@ -421,6 +425,22 @@ def _on_stream(call):
         with torch.cuda.stream(stream):
             return call(*args, **kw)
     return wrapped
+
+
+# The tensors of the training calls, in the order of their pointers, and which of them are fp32 only.
+_CHUNK_BWD_NAMES = ("q", "k", "v", "g", "beta", "cu_seqlens", "initial_state", "dout", "dfinal_state", "dq", "dk",
+                  "dv", "dg", "dbeta", "dinitial_state")
+_CHUNK_BWD_FP32 = tuple(n in ("g", "beta", "initial_state", "dfinal_state", "dg", "dbeta", "dinitial_state") for n
+                  in _CHUNK_BWD_NAMES)
+_RMSNORM_BWD_NAMES = ("dout", "y", "z", "norm_weight", "dy", "dz", "dnorm_weight")
+_RMSNORM_BWD_FP32 = tuple(n in ("z", "norm_weight", "dz", "dnorm_weight") for n in _RMSNORM_BWD_NAMES)
+_GROUPNORM_NAMES = ("y", "z", "weight", "bias", "out")
+_GROUPNORM_FP32 = tuple(n in ("z", "weight", "bias") for n in _GROUPNORM_NAMES)
+_GROUPNORM_BWD_NAMES = ("dout", "y", "z", "weight", "bias", "dy", "dz", "dweight", "dbias")
+_GROUPNORM_BWD_FP32 = tuple(n in ("z", "weight", "bias", "dz", "dweight", "dbias") for n in _GROUPNORM_BWD_NAMES)
+_DECAY_BWD_NAMES = ("a", "A_log", "dt_bias", "b", "dg", "dbeta", "da", "dA_log", "ddt_bias", "db")
+_DECAY_BWD_FP32 = tuple(n in ("a", "A_log", "dt_bias", "b", "dg", "dbeta", "da", "dA_log", "ddt_bias", "db") for n
+                  in _DECAY_BWD_NAMES)
 
 
 @_on_stream
@@ -458,12 +478,11 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=
         dinitial_state = torch.empty((num_seqs, H, d_v, d_k), dtype=torch.float32, device=q.device)
     states, nk, nv, nh = num_seqs * H * d_v * d_k, total_T * H_k * d_k, total_T * H * d_v, total_T * H
     L = lib()
-    p = _pointers(q, ("q", q, nk, False), ("k", k, nk, False), ("v", v, nv, False), ("g", g, nh, True),
-                  ("beta", beta, nh, True), ("cu_seqlens", cu_seqlens, num_seqs + 1, False),
-                  ("initial_state", initial_state, states, True), ("dout", dout, nv, False),
-                  ("dfinal_state", dfinal_state, states, True), ("dq", dq, nk, False), ("dk", dk, nk, False),
-                  ("dv", dv, nv, False), ("dg", dg, nh, True), ("dbeta", dbeta, nh, True),
-                  ("dinitial_state", dinitial_state, states, True))
+    p = _pointers(q, _CHUNK_BWD_NAMES,
+                  (q, k, v, g, beta, cu_seqlens, initial_state, dout, dfinal_state, dq, dk, dv, dg, dbeta,
+                   dinitial_state),
+                  (nk, nk, nv, nh, nh, num_seqs + 1, states, nv, states, nk, nk, nv, nh, nh, states),
+                  _CHUNK_BWD_FP32)
     need = L.gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v)
     workspace, ws, ws_bytes = _workspace(workspace, need, q)
     rc = _run(q, L.gdn_chunk_bwd, *p[:6], num_seqs, total_T, H, H_k, d_k, d_v, dt, GDN_DECAY_PER_HEAD, float(scale),
@@ -486,9 +505,10 @@ def gdn_gate_rmsnorm_silu_bwd(dout, y, z, norm_weight=None, eps=1e-6, dy=None, d
     if dy.dtype != y.dtype:
         raise TypeError("dy must have the dtype of y")
     n, L = rows * d_v, lib()
-    p = _pointers(y, ("dout", dout, n, False), ("y", y, n, False), ("z", z, n, True),
-                  ("norm_weight", norm_weight, d_v, True), ("dy", dy, n, False), ("dz", dz, n, True),
-                  ("dnorm_weight", dnorm_weight, d_v, True))
+    p = _pointers(y, _RMSNORM_BWD_NAMES,
+                  (dout, y, z, norm_weight, dy, dz, dnorm_weight),
+                  (n, n, n, d_v, n, n, d_v),
+                  _RMSNORM_BWD_FP32)
     need = L.gdn_gate_bwd_workspace_size(rows, 1, d_v) if dnorm_weight is not None else 0
     workspace, ws, ws_bytes = _workspace(workspace, need, y)
     rc = _run(y, L.gdn_gate_rmsnorm_silu_bwd, p[0], _dt(dout), p[1], _dt(y), p[2], p[3], float(eps), p[4], p[5], p[6],
@@ -513,8 +533,10 @@ def gdn_gate_groupnorm_silu(y, z=None, weight=None, bias=None, eps=1e-6, out=Non
     if out is None:
         out = torch.empty_like(y, dtype=out_dtype)
     n, c = rows * groups * size, groups * size
-    p = _pointers(y, ("y", y, n, False), ("z", z, n, True), ("weight", weight, c, True), ("bias", bias, c, True),
-                  ("out", out, n, False))
+    p = _pointers(y, _GROUPNORM_NAMES,
+                  (y, z, weight, bias, out),
+                  (n, n, c, c, n),
+                  _GROUPNORM_FP32)
     rc = _run(y, lib().gdn_gate_groupnorm_silu, p[0], _dt(y), p[1], p[2], p[3], float(eps), p[4], _dt(out), rows,
               groups, size, _stream(None, y))
     _check("gdn_gate_groupnorm_silu", rc)
@@ -539,9 +561,10 @@ def gdn_gate_groupnorm_silu_bwd(dout, y, z=None, weight=None, bias=None, eps=1e-
     if bias is not None and dbias is None:
         dbias = torch.empty_like(bias)
     L = lib()
-    p = _pointers(y, ("dout", dout, n, False), ("y", y, n, False), ("z", z, n, True), ("weight", weight, c, True),
-                  ("bias", bias, c, True), ("dy", dy, n, False), ("dz", dz, n, True), ("dweight", dweight, c, True),
-                  ("dbias", dbias, c, True))
+    p = _pointers(y, _GROUPNORM_BWD_NAMES,
+                  (dout, y, z, weight, bias, dy, dz, dweight, dbias),
+                  (n, n, n, c, c, n, n, c, c),
+                  _GROUPNORM_BWD_FP32)
     need = L.gdn_gate_bwd_workspace_size(rows, groups, size) if dweight is not None or dbias is not None else 0
     workspace, ws, ws_bytes = _workspace(workspace, need, y)
     rc = _run(y, L.gdn_gate_groupnorm_silu_bwd, p[0], _dt(dout), p[1], _dt(y), p[2], p[3], p[4], float(eps), p[5],
@@ -566,9 +589,10 @@ def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=N
     if b is not None and db is None:
         db = torch.empty_like(b)
     n, L = total_T * H, lib()
-    p = _pointers(a, ("a", a, n, True), ("A_log", A_log, H, True), ("dt_bias", dt_bias, H, True), ("b", b, n, True),
-                  ("dg", dg, n, True), ("dbeta", dbeta, n, True), ("da", da, n, True), ("dA_log", dA_log, H, True),
-                  ("ddt_bias", ddt_bias, H, True), ("db", db, n, True))
+    p = _pointers(a, _DECAY_BWD_NAMES,
+                  (a, A_log, dt_bias, b, dg, dbeta, da, dA_log, ddt_bias, db),
+                  (n, H, H, n, n, n, n, H, H, n),
+                  _DECAY_BWD_FP32)
     workspace, ws, ws_bytes = _workspace(workspace, L.gdn_decay_bwd_workspace_size(total_T, H), a)
     rc = _run(a, L.gdn_decay_from_logits_bwd, *p[:10], total_T, H, ws, ws_bytes, _stream(None, a))
     _check("gdn_decay_from_logits_bwd", rc)
