@@ -15,7 +15,11 @@
 // and is taken off as well.
 //
 // Sums over rows end in a table of partial sums in the workspace, which a second kernel adds up
-// column by column in a fixed order: no atomics, so the same call gives the same bits.
+// column by column in a fixed order: no atomics, so the same call gives the same bits.  A small call's
+// blocks are one cluster instead and add their sums up through distributed shared memory, without
+// the table and the second launch.
+#include <cooperative_groups.h>
+
 #include "train_internal.cuh"
 
 namespace gdn {
@@ -23,6 +27,51 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSMs = 152;
+constexpr int kCluster = 8;  // blocks of a small call's cluster
+// A call that wants sums over rows is small up to this many blocks of one vector a lane.  us a call, one
+// cluster against a grid and column_sum_kernel, as a replayed graph and called from the binding:
+//   blocks                             4                8               16               32               64
+//   RMS norm, d = 64           4.2/29  5.1/33   4.2/28  5.1/31   5.1/28  5.5/32   6.6/27  5.6/31   9.7/30  5.9/31
+//   gate preparation, H = 6    3.0/31  3.9/33   3.1/31  4.1/32   3.4/30  4.1/34   4.1/30  4.6/33   5.4/31  4.5/35
+// and the RMS norm of d = 1024 (four vectors a lane) 8.0/30 against 9.2/31 at 8 blocks, 11.8/32 against 9.2/32
+// at 16.
+constexpr int kNormClusterBlocks = 16, kDecayClusterBlocks = 32;
+constexpr int kClusterChannels = 4096;  // whose two sums fit beside the kernel's shared memory
+
+// Launches one cluster of `blocks` blocks.
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), int blocks, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// out[c] = the sum over the cluster's blocks, in order, of element at(c) of each block's `table`; the
+// blocks share the columns.  Every thread of the cluster takes part, and tables may be reused after it.
+template <class At, class Out>
+__device__ __forceinline__ void cluster_sum(float* table, int cols, At at, Out out) {
+    const auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    const int n = gridDim.x;
+    for (int c = blockIdx.x * kThreads + threadIdx.x; c < cols; c += n * kThreads) {
+        float x[kCluster], sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) x[r] = r < n ? cluster.map_shared_rank(table, r)[at(c)] : 0.f;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) sum += x[r];
+        out(c, sum);
+    }
+    cluster.sync();
+}
 
 template <int VEC>
 __device__ __forceinline__ void load_f32(const float* p, float* out) {
@@ -95,10 +144,12 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f,
 // group s % groups and rows s / groups, s / groups + stride / groups, ...
 struct NormPlan {
     int L, nv, vec, blocks;
+    bool cluster;        // the blocks are one cluster, which adds the sums over rows up itself
     long stride, prows;  // prows: rows of the table of partial sums
 };
 
-NormPlan norm_plan(long rows, int groups, int size, bool bwd) {
+// sums: sums over rows are wanted.
+NormPlan norm_plan(long rows, int groups, int size, bool bwd, bool sums) {
     NormPlan p;
     p.vec = size % 8 == 0 ? 8 : size % 4 == 0 ? 4 : 1;
     const int vecs = size / p.vec;
@@ -113,6 +164,8 @@ NormPlan norm_plan(long rows, int groups, int size, bool bwd) {
     const long most = (bwd ? 2 : 3) * kSMs;
     long b = all < most ? all : most;
     if (b < least) b = least;
+    p.cluster = sums && all * p.nv <= kNormClusterBlocks && groups <= per_block && groups * size <= kClusterChannels;
+    if (p.cluster && b > kCluster) b = kCluster;
     p.blocks = (int)b;
     p.stride = b * per_block / groups * groups;
     // a block whose sets cover every group adds its own sets up first
@@ -199,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 3 : 1) groupno
     }
 }
 
-template <int L, int NV, int VEC, bool RMS>
+// prows: rows of the table of partial sums.  ONE: the grid is one cluster and writes dw and db itself.
+template <int L, int NV, int VEC, bool RMS, bool ONE>
 __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 2 : 1) norm_bwd_kernel(NormArgs a, long stride, long prows) {
     const long set = (long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const int lane = threadIdx.x % L;
@@ -293,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 2 : 1) norm_bw
             if (gated) store_f32<VEC>(a.dz + base + c, z[i]);
         }
     }
-    if (!a.partial) return;
+    if (!ONE && !a.partial) return;
     const long channels = (long)a.groups * a.size;
     constexpr int PER = kThreads / L;
-    if (a.groups > PER) {
+    if (!ONE && a.groups > PER) {
         if (set >= stride) return;
         float* pw = a.partial + (set / a.groups) * channels + (long)grp * a.size;
 #pragma unroll
@@ -310,8 +364,9 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 2 : 1) norm_bw
     }
     // the block's sets of one group are added in order (idle sets hold zeros)
     __shared__ float sh[kThreads * VEC];
+    extern __shared__ __align__(16) float sums[];  // [2, channels], in a cluster
     const int k = threadIdx.x / L;
-    float* pw = a.partial + blockIdx.x * channels + (long)grp * a.size;
+    float* pw = (ONE ? sums : a.partial + blockIdx.x * channels) + (long)grp * a.size;
 #pragma unroll
     for (int part = 0; part < (RMS ? 1 : 2); ++part) {
         if (!(part ? a.db : a.dw)) continue;
@@ -327,9 +382,16 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 2 : 1) norm_bw
                 for (int q = k + a.groups; q < PER; q += a.groups)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) x[j] += sh[j * kThreads + q * L + lane];
-                store_f32<VEC>(pw + part * prows * channels + c, x);
+                store_f32<VEC>(pw + part * (ONE ? 1 : prows) * channels + c, x);
             }
         }
+    }
+    if constexpr (ONE) {
+        const int n = (int)channels;
+        cluster_sum(sums, a.db ? 2 * n : n, [](int c) { return c; }, [&](int c, float x) {
+            if (c >= n) a.db[c - n] = x;
+            else if (a.dw) a.dw[c] = x;
+        });
     }
 }
 
@@ -364,9 +426,17 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float* ta
 
 template <int L, int NV, int VEC>
 void launch_norm_one(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
-    if (!bwd) groupnorm_kernel<L, NV, VEC><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
-    else if (a.rms) norm_bwd_kernel<L, NV, VEC, true><<<p.blocks, kThreads, 0, s>>>(a, p.stride, p.prows);
-    else norm_bwd_kernel<L, NV, VEC, false><<<p.blocks, kThreads, 0, s>>>(a, p.stride, p.prows);
+    if (!bwd) {
+        groupnorm_kernel<L, NV, VEC><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
+        return;
+    }
+    if (p.cluster) {
+        const auto kernel = a.rms ? norm_bwd_kernel<L, NV, VEC, true, true> : norm_bwd_kernel<L, NV, VEC, false, true>;
+        launch_cluster(kernel, p.blocks, 2 * sizeof(float) * a.groups * a.size, s, a, p.stride, 0);
+    } else {
+        const auto kernel = a.rms ? norm_bwd_kernel<L, NV, VEC, true, false> : norm_bwd_kernel<L, NV, VEC, false, false>;
+        kernel<<<p.blocks, kThreads, 0, s>>>(a, p.stride, p.prows);
+    }
 }
 
 template <int VEC>
@@ -401,10 +471,11 @@ cudaError_t launch_norm(const NormArgs& a, const NormPlan& p, bool bwd, cudaStre
 // stride that keeps its column, so the column sums stay in registers.
 struct DecayPlan {
     int vec, blocks;
+    bool cluster;  // as in NormPlan
     long cols, stride, prows;  // column vectors; working threads; rows of the partial table
 };
 
-DecayPlan decay_plan(long total_T, int H) {
+DecayPlan decay_plan(long total_T, int H, bool sums) {
     DecayPlan p;
     p.vec = H % 4 == 0 ? 4 : 1;
     p.cols = H / p.vec;
@@ -412,6 +483,8 @@ DecayPlan decay_plan(long total_T, int H) {
     const long least = (p.cols + kThreads - 1) / kThreads;
     long b = all < 4 * kSMs ? all : 4 * kSMs;
     if (b < least) b = least;
+    p.cluster = sums && all <= kDecayClusterBlocks && p.cols <= kThreads;
+    if (p.cluster && b > kCluster) b = kCluster;
     p.blocks = (int)b;
     p.stride = b * kThreads / p.cols * p.cols;
     p.prows = p.cols <= kThreads ? b : p.stride / p.cols;
@@ -459,24 +532,36 @@ __global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs
             store_f32<VEC>(a.da + i * VEC, o);
         }
     }
-    if (!a.partial) return;
+    if (!a.dA_log && !a.ddt) return;
     // threads of the block that hold the same columns are added in order (cols <= kThreads); idle
     // threads hold zeros
     __shared__ float sh[2][kThreads][VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) { sh[0][threadIdx.x][j] = sA[j]; sh[1][threadIdx.x][j] = sd[j]; }
     __syncthreads();
-    long prow = blockIdx.x;
-    if (cols <= kThreads) {
-        if (threadIdx.x >= cols) return;
+    const long H = cols * VEC;
+    if (threadIdx.x < cols)
         for (long t = threadIdx.x + cols; t < kThreads; t += cols)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) { sA[j] += sh[0][t][j]; sd[j] += sh[1][t][j]; }
+    if (!prows) {
+        if (threadIdx.x < cols)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) { sh[0][q % cols][j] = sA[j]; sh[1][q % cols][j] = sd[j]; }  // read by no thread above
+        const int n = (int)H;
+        cluster_sum(&sh[0][0][0], 2 * n, [&](int c) { return c < n ? c : c - n + kThreads * VEC; }, [&](int c, float x) {
+            float* out = c < n ? a.dA_log : a.ddt;
+            if (out) out[c < n ? c : c - n] = x;
+        });
+        return;
+    }
+    long prow = blockIdx.x;
+    if (cols <= kThreads) {
+        if (threadIdx.x >= cols) return;
     } else {
         if (q >= stride) return;
         prow = q / cols;
     }
-    const long H = cols * VEC;
     store_f32<VEC>(a.partial + prow * H + h, sA);
     store_f32<VEC>(a.partial + (prows + prow) * H + h, sd);
 }
@@ -484,33 +569,36 @@ __global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(long rows, int groups, int size) {
-    const NormPlan p = norm_plan(rows, groups, size, true);
+    const NormPlan p = norm_plan(rows, groups, size, true, false);  // small calls do not use it
     return (size_t)p.prows * groups * size * 2 * sizeof(float);
 }
 
 cudaError_t launch_groupnorm(const NormArgs& a, cudaStream_t s) {
-    return launch_norm(a, norm_plan(a.rows, a.groups, a.size, false), false, s);
+    return launch_norm(a, norm_plan(a.rows, a.groups, a.size, false, false), false, s);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s) {
-    const NormPlan p = norm_plan(a.rows, a.groups, a.size, true);
+    const bool sums = a.dw || a.db;
+    const NormPlan p = norm_plan(a.rows, a.groups, a.size, true, sums);
     cudaError_t e = launch_norm(a, p, true, s);
-    if (e != cudaSuccess || !a.partial) return e;
+    if (e != cudaSuccess || !sums || p.cluster) return e;
     const long cols = (long)a.groups * a.size;
     return launch_after(column_sum_kernel, dim3((unsigned)((cols + 31) / 32), a.db ? 2 : 1), kSumThreads, 0, s,
                         a.partial, p.prows, cols, a.dw, a.db);
 }
 
 size_t gate_prep_bwd_workspace_bytes(long total_T, int H) {
-    return (size_t)decay_plan(total_T, H).prows * H * 2 * sizeof(float);
+    return (size_t)decay_plan(total_T, H, false).prows * H * 2 * sizeof(float);
 }
 
 cudaError_t launch_gate_prep_bwd(const GatePrepBwdArgs& a, cudaStream_t s) {
-    const DecayPlan p = decay_plan(a.total_T, a.H);
-    if (p.vec == 4) gate_prep_bwd_kernel<4><<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
-    else gate_prep_bwd_kernel<1><<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
+    const bool sums = a.dA_log || a.ddt;
+    const DecayPlan p = decay_plan(a.total_T, a.H, sums);
+    const auto kernel = p.vec == 4 ? gate_prep_bwd_kernel<4> : gate_prep_bwd_kernel<1>;
+    if (p.cluster) return launch_cluster(kernel, p.blocks, 0, s, a, p.cols, p.stride, 0);
+    kernel<<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.partial) return e;
+    if (e != cudaSuccess || !sums) return e;
     return launch_after(column_sum_kernel, dim3((unsigned)((a.H + 31) / 32), a.ddt ? 2 : 1), kSumThreads, 0, s,
                         a.partial, p.prows, a.H, a.dA_log, a.ddt);
 }
