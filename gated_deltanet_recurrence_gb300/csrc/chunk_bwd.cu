@@ -726,6 +726,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     const Scale sp = planes::scale_of(planes::top_of<NW>(red[4], lane));
     planes::write(W, acc, m, nd, lane, sw.mul);
     planes::write(TX, qk, m, nc, lane, sp.mul);
+    Rows<NW, D, P> y;
+    y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
     __syncthreads();
     planes::clear(acc);  // Q' = diag(b) Q - P W
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, W, nd, lane);
@@ -745,11 +747,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         w.meta[unit].t_scale = st.back;
     }
     __syncthreads();  // W, V and Q have been read
-    {
-        Rows<NW, D, P> y;
-        y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
-        y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
-    }
+    y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
     __syncthreads();
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
         acc[i][j][2 * hh] *= fY[r];
@@ -1278,6 +1276,14 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) pp[i] = src[i * T + tid];
     }
     state.fetch(S0);
+    float2 v[MT][NT][2], e0[MT][NT][2];
+    planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
+        const float* e = w.E + (unit * D + c) * kC + r;
+        e0[i][j][hh] = make_float2(e[0], e[kC]);
+    });
+    planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
+        v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
+    });
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -1295,16 +1301,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         }
     }
 
-    float2 v[MT][NT][2];
     {
-        float2 e0[MT][NT][2];
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-            const float* e = w.E + (unit * D + c) * kC + r;
-            e0[i][j][hh] = make_float2(e[0], e[kC]);
-        });
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-            v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
-        });
         // P with the rows' factors of dY, powers of two, which P^T dY contracts over
         float fY_top = fmaxf(fY[lane], fY[lane + 32]);
         fY_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fY_top)));
