@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
     __shared__ uint32_t red[2][NW], tops[2], tmem_at;
-    __shared__ uint64_t bars[3];
+    __shared__ uint64_t bars[5];  // of the MMAs; of the copies of T, P and E; of S0's
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
     Span spans[2];
@@ -1209,7 +1209,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     constexpr int NT = D / 32;
     const int nd = nw * (D / 4);
     const Meta& meta = w.meta[unit];
-    const float* S0 = w.S + unit * D * D;
     const float* dS1 = w.dS + unit * D * D;
     auto prefetch_states = [&](long u) {
         prefetch(w.S + u * D * D, D * D * 4);
@@ -1219,9 +1218,27 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     };
     if (tid == 0) {
         if (blockIdx.x < kSMs) prefetch_states(unit);
-        for (int i = 0; i < 3; ++i) ptx::mbar_init(&bars[i], 1);
+        for (int i = 0; i < 5; ++i) ptx::mbar_init(&bars[i], 1);
         ptx::fence_mbar_init();
+        // T goes where it stays; P, E and S0 go, as they are, to the places of what is made of them
+        ptx::mbar_arrive_expect_tx(&bars[3], 2 * (uint32_t)kTBytes + kC * D * 4);
+        for (int i = 0; i < 2; ++i) {
+            ptx::bulk_load(sm + L::SQ + 2 * i * HF, w.P + unit * kTBytes + i * HF, HF, &bars[3]);
+            ptx::bulk_load(sm + L::SQ + (2 * i + 1) * HF, w.T + unit * kTBytes + i * HF, HF, &bars[3]);
+        }
+        ptx::bulk_load(sm + L::B1, w.E + unit * kC * D, kC * D * 4, &bars[3]);
+        ptx::mbar_arrive_expect_tx(&bars[4], D * D * 4);
+        ptx::bulk_load(sm + L::ST, w.S + unit * D * D, D * D * 4, &bars[4]);
     }
+    // A wait that gives up is recorded; what follows is then meaningless, but ends.
+    bool ok = true;
+    auto wait = [&](int i, int use) {
+        if (ok && !ptx::mbar_wait(&bars[i], use, kMmaWaitNs)) {
+            ok = false;
+            record_error(a.err, GDN_ERR_TIMEOUT);
+        }
+        ptx::tc_fence_after();
+    };
     if (warp == 0) {
         ptx::tmem_alloc(&tmem_at, L::tmem);
         ptx::tmem_relinquish();
@@ -1237,13 +1254,9 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         GateRows gates;
         if (warp == NW - 1) gates.fetch(a, t0, len, h, lane);
         Rows<NW, D, P> k, q, y;
-        uint4 tt[kTBytes / 16 / T];
         k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
-        const uint4* src = reinterpret_cast<const uint4*>(w.T + unit * kTBytes);
-#pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) tt[i] = src[i * T + tid];
         if (tid < kC) diag[tid] = meta.p_diag[tid];
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
         const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
@@ -1251,12 +1264,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true, !L::share>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
         y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
-        // T's planes, each where SQ has T's: 512 vectors a plane
-#pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
-            const int e = i * T + tid;
-            *reinterpret_cast<uint4*>(sm + L::SQ + HF + (e >> 9) * 2 * HF + (e & 511) * 16) = tt[i];
-        }
         if constexpr (P == 1) {  // dY's lo plane is zero (below dR's, rows of 8 KB)
 #pragma unroll
             for (int i = 0; i < PL / 16 / T; ++i) {
@@ -1269,18 +1276,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
     const float t_back = meta.t_scale, p_back = meta.p_scale;
-    uint4 pp[kTBytes / 16 / T];
-    {
-        const uint4* src = reinterpret_cast<const uint4*>(w.P + unit * kTBytes);
-#pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) pp[i] = src[i * T + tid];
-    }
-    state.fetch(S0);
-    float2 v[MT][NT][2], e0[MT][NT][2];
-    planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-        const float* e = w.E + (unit * D + c) * kC + r;
-        e0[i][j][hh] = make_float2(e[0], e[kC]);
-    });
+    float2 v[MT][NT][2];
     planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
         v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
     });
@@ -1303,6 +1299,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
 
     {
         // P with the rows' factors of dY, powers of two, which P^T dY contracts over
+        wait(3, 0);
         float fY_top = fmaxf(fY[lane], fY[lane + 32]);
         fY_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fY_top)));
         const float fY_inv = 1.f / fY_top;
@@ -1310,20 +1307,25 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
             const int e = i * T + tid;
             const __half2 f = __float2half2_rn(fY[(e & 511) >> 3] * fY_inv);
-            __half2* x = reinterpret_cast<__half2*>(&pp[i]);
+            uint4* at = reinterpret_cast<uint4*>(sm + L::SQ + (e >> 9) * 2 * HF + (e & 511) * 16);
+            uint4 pp = *at;
+            __half2* x = reinterpret_cast<__half2*>(&pp);
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[j] = __hmul2(x[j], f);
-            *reinterpret_cast<uint4*>(sm + L::SQ + (e >> 9) * 2 * HF + (e & 511) * 16) = pp[i];
+            *at = pp;
         }
         const float pu = p_back * fY_top;
-        state.template put<false>(ST, ss.mul);
+        wait(4, 0);
+        state.fetch(reinterpret_cast<const float*>(sm + L::ST));
         __syncthreads();
+        state.template put<false>(ST, ss.mul);
         float acc[MT][NT][4];  // P^T dY + E
         planes::clear(acc);
         planes::product<kC, true, true, planes::kUpper>(acc, Pm, m, Y, nd, lane);
-        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int, int) {
-            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], pu, e0[i][j][hh].x);
-            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], pu, e0[i][j][hh].y);
+        const float* E = reinterpret_cast<const float*>(sm + L::B1);
+        planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
+            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], pu, E[c * kC + r]);
+            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], pu, E[(c + 1) * kC + r]);
         });
         const uint32_t top2 = planes::max_bits(acc);
         if (lane == 0) red[1][warp] = top2;
@@ -1370,15 +1372,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         ptx::mma_commit(&bars[1]);
     }
     state.fetch(dS1);
-    // A wait that gives up is recorded; what follows is then meaningless, but ends.
-    bool ok = true;
-    auto wait = [&](int i, int use) {
-        if (ok && !ptx::mbar_wait(&bars[i], use, kMmaWaitNs)) {
-            ok = false;
-            record_error(a.err, GDN_ERR_TIMEOUT);
-        }
-        ptx::tc_fence_after();
-    };
     // This thread's token, which half of the lanes, and its columns of a 64-wide and of a d-wide result
     const int part = (warp & 3) >> 1, row = (warp & 1) * 32 + lane, cg = warp >> 2;
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1616,6 +1609,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
                 a.dg[at] = a.g[at] < -128.f ? 0.f : dg[e];
             }
     }
+    if (tid == 0 && !ok)  // no copy may still be on its way when the block ends
+        for (int i = 3; i < 5; ++i) ptx::mbar_wait(&bars[i], 0, kMmaWaitNs);
 }
 
 // dq, dk of grouped heads: the sum over the group's value heads, in order.  Tokens outside every
