@@ -47,6 +47,20 @@ using planes::Scale;
 
 constexpr int kC = 64;
 
+// Division of numbers below 2^31 by a divisor that the host knows, as a product with its scaled reciprocal
+// (Granlund and Montgomery, "Division by Invariant Integers using Multiplication", 1994): with
+// 2^(l - 1) < d <= 2^l and mul = floor(2^(31 + l) / d) + 1, n / d = floor(n mul / 2^(31 + l)).  (The half
+// dozen divisions a block begins with were 2.5k cycles before its first load.)
+struct Divisor {
+    uint32_t mul, shift;
+    static __host__ Divisor of(uint32_t d) {
+        uint32_t l = 0;
+        while ((1ull << l) < d) ++l;
+        return {(uint32_t)((1ull << (31 + l)) / d + 1), 31 + l};
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
+};
+
 // ---- the chunk slots ---------------------------------------------------------------------------
 // Chunk c of sequence n has slot base(n) + c.  With lengths from cu_seqlens base(n) = cu[n] / 64 + n
 // leaves every sequence at least as many slots as it has chunks; unused slots do nothing.  With equal
@@ -103,32 +117,88 @@ __global__ void __launch_bounds__(1024) chunk_bwd_index_kernel(ChunkBwdArgs a, i
     }
 }
 
+// ---- workspace ---------------------------------------------------------------------------------
+// Per (slot, head):
+//   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
+//   T, P   planes of T and of P
+//   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
+//   S      S0 (fp32 [d, d])                             dS  X, then dS1 (fp32 [d, d])
+//   meta   scales and maxima
+struct LinkTail {
+    float c[kC];  // takes row j of K's planes to Kd: tail_j and the row's factor
+    float w_scale, b_last, pad[62];
+};  // 512 bytes, so that a link's planes, at any of its places, start at a multiple of 512
+static_assert(sizeof(LinkTail) == 512, "");
+
+struct Meta {
+    uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
+    float t_scale, p_scale, pad[14];
+    float p_diag[kC];  // P's diagonal, q_i . k_i
+};
+static_assert(sizeof(Meta) == 512, "");
+
+constexpr size_t kTBytes = 2 * kC * kC * sizeof(__half);
+__host__ __device__ constexpr size_t link_bytes(int d, int p) {
+    return (2 + (size_t)p) * kC * d * sizeof(__half) + sizeof(LinkTail);
+}
+
+struct Work {
+    unsigned char *link, *T, *P;
+    float *U, *E, *S, *dS;
+    Meta* meta;
+    float *dq, *dk;  // [total_T, H, d] each, grouped heads only
+    int* index;      // 1 + slots, many sequences only (else null)
+    Divisor heads, rep, chunks;  // H, H / Hk, and with equal lengths the chunks of a sequence
+    int len, per;                // with equal lengths: a sequence's tokens and chunks (0: no tokens)
+};
+
+// K's planes in the link: one where the inputs are bf16 throughout (it holds them exactly), else two.
+__host__ __forceinline__ int input_planes(gdn_dtype qkv, gdn_dtype dout) {
+    return qkv == GDN_BF16 && dout == GDN_BF16 ? 1 : 2;
+}
+
+__host__ __forceinline__ size_t index_bytes(size_t slots) { return ((1 + slots) * sizeof(int) + 255) / 256 * 256; }
+
+__host__ __forceinline__ Work work_of(void* ws, size_t slots, size_t units, size_t tokens, int d, int p, bool index) {
+    Work w;
+    w.index = index ? static_cast<int*>(ws) : nullptr;
+    w.link = static_cast<unsigned char*>(ws) + index_bytes(slots);
+    w.T = w.link + units * link_bytes(d, p);
+    w.P = w.T + units * kTBytes;
+    w.U = reinterpret_cast<float*>(w.P + units * kTBytes);
+    w.E = w.U + units * kC * d;
+    w.S = w.E + units * kC * d;
+    w.dS = w.S + units * d * d;
+    w.meta = reinterpret_cast<Meta*>(w.dS + units * d * d);
+    w.dq = reinterpret_cast<float*>(w.meta + units);
+    w.dk = w.dq + tokens * d;
+    return w;
+}
+
 // Whether cu_seqlens is monotone and inside [0, total_T]; finds the spans of N slots, whose n is -1 for an
-// unused slot.  All threads take part; contains block barriers.  `index` is null or what
-// chunk_bwd_index_kernel wrote.
+// unused slot.  All threads take part; contains block barriers.
 template <int N>
-__device__ bool find_spans(const ChunkBwdArgs& a, const int* index, const long (&slot)[N], Span (&s)[N]) {
+__device__ bool find_spans(const ChunkBwdArgs& a, const Work& w, const int (&slot)[N], Span (&s)[N]) {
     __shared__ int found[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) s[k].n = -1;
     if (!a.cu_seqlens) {
-        const int len = a.total_T / a.num_seqs, per = (len + kC - 1) / kC;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (slot[k] >= 0 && per > 0) {
-                const int n = (int)slot[k] / per;
+            if (slot[k] >= 0 && w.per > 0) {
+                const int n = w.chunks(slot[k]);
                 if (n >= a.num_seqs) continue;
                 s[k].n = n;
-                s[k].bos = (long)n * len;
-                s[k].eos = s[k].bos + len;
-                s[k].base = (long)n * per;
-                s[k].chunks = per;
-                s[k].c = (int)slot[k] - n * per;
+                s[k].bos = (long)n * w.len;
+                s[k].eos = s[k].bos + w.len;
+                s[k].base = (long)n * w.per;
+                s[k].chunks = w.per;
+                s[k].c = slot[k] - n * w.per;
             }
         return true;
     }
     int n[N];
-    if (index) {
+    if (const int* index = w.index) {
         if (!index[0]) return false;
 #pragma unroll
         for (int k = 0; k < N; ++k) n[k] = slot[k] >= 0 ? index[1 + slot[k]] : -1;
@@ -161,66 +231,10 @@ __device__ bool find_spans(const ChunkBwdArgs& a, const int* index, const long (
     return true;
 }
 
-__device__ bool cu_valid(const ChunkBwdArgs& a, const int* index) {
-    const long none[1] = {-1};
+__device__ bool cu_valid(const ChunkBwdArgs& a, const Work& w) {
+    const int none[1] = {-1};
     Span s[1];
-    return find_spans<1>(a, index, none, s);
-}
-
-// ---- workspace ---------------------------------------------------------------------------------
-// Per (slot, head):
-//   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
-//   T, P   planes of T and of P
-//   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
-//   S      S0 (fp32 [d, d])                             dS  X, then dS1 (fp32 [d, d])
-//   meta   scales and maxima
-struct LinkTail {
-    float c[kC];  // takes row j of K's planes to Kd: tail_j and the row's factor
-    float w_scale, b_last, pad[62];
-};  // 512 bytes, so that a link's planes, at any of its places, start at a multiple of 512
-static_assert(sizeof(LinkTail) == 512, "");
-
-struct Meta {
-    uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
-    float t_scale, p_scale, pad[14];
-    float p_diag[kC];  // P's diagonal, q_i . k_i
-};
-static_assert(sizeof(Meta) == 512, "");
-
-constexpr size_t kTBytes = 2 * kC * kC * sizeof(__half);
-__host__ __device__ constexpr size_t link_bytes(int d, int p) {
-    return (2 + (size_t)p) * kC * d * sizeof(__half) + sizeof(LinkTail);
-}
-
-struct Work {
-    unsigned char *link, *T, *P;
-    float *U, *E, *S, *dS;
-    Meta* meta;
-    float *dq, *dk;  // [total_T, H, d] each, grouped heads only
-    int* index;      // 1 + slots, many sequences only (else null)
-};
-
-// K's planes in the link: one where the inputs are bf16 throughout (it holds them exactly), else two.
-__host__ __forceinline__ int input_planes(gdn_dtype qkv, gdn_dtype dout) {
-    return qkv == GDN_BF16 && dout == GDN_BF16 ? 1 : 2;
-}
-
-__host__ __forceinline__ size_t index_bytes(size_t slots) { return ((1 + slots) * sizeof(int) + 255) / 256 * 256; }
-
-__host__ __forceinline__ Work work_of(void* ws, size_t slots, size_t units, size_t tokens, int d, int p, bool index) {
-    Work w;
-    w.index = index ? static_cast<int*>(ws) : nullptr;
-    w.link = static_cast<unsigned char*>(ws) + index_bytes(slots);
-    w.T = w.link + units * link_bytes(d, p);
-    w.P = w.T + units * kTBytes;
-    w.U = reinterpret_cast<float*>(w.P + units * kTBytes);
-    w.E = w.U + units * kC * d;
-    w.S = w.E + units * kC * d;
-    w.dS = w.S + units * d * d;
-    w.meta = reinterpret_cast<Meta*>(w.dS + units * d * d);
-    w.dq = reinterpret_cast<float*>(w.meta + units);
-    w.dk = w.dq + tokens * d;
-    return w;
+    return find_spans<1>(a, w, none, s);
 }
 
 // ---- decays ------------------------------------------------------------------------------------
@@ -436,6 +450,15 @@ __device__ __forceinline__ void prefetch_rows(const void* src, gdn_dtype dt, con
     else prefetch_lines<T, D / 32>(static_cast<const char*>(src), s, heads, h);
 }
 
+// The same of its g and beta, a token a thread.
+__device__ __forceinline__ void prefetch_gates(const ChunkBwdArgs& a, const Span& s, int h) {
+    const long t = s.bos + (long)s.c * kC + threadIdx.x;
+    if (threadIdx.x < kC && t < s.eos) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.g + t * a.H + h));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.beta + t * a.H + h));
+    }
+}
+
 // Blocks of one chunk each run for tens of microseconds with few loads of their own under way, so each
 // asks for the inputs of the block that will follow it on its SM (about kSMs x blocks an SM later).
 constexpr int kSMs = 152;
@@ -586,11 +609,12 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
     __shared__ uint32_t red[7][NW], tops[2];
     const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
-    const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
+    const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
+    const long slot = slots[0];
     Span spans[2];
-    if (!find_spans<2>(a, w.index, slots, spans) || spans[0].n < 0) return;
+    if (!find_spans<2>(a, w, slots, spans) || spans[0].n < 0) return;
     const Span& s = spans[0];
-    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hk), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x - slots[0] * a.H, hk = w.rep(h), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
@@ -638,11 +662,12 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         });
     }
     if (spans[1].n >= 0) {
-        const int h2 = next % a.H, hk2 = h2 / (a.H / a.Hk);
+        const int h2 = next - slots[1] * a.H, hk2 = w.rep(h2);
         prefetch_rows<kPrepThreads, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
         prefetch_rows<kPrepThreads, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
         prefetch_rows<kPrepThreads, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
         prefetch_rows<kPrepThreads, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
+        prefetch_gates(a, spans[1], h2);
     }
     if (tid < kC) tail.c[tid] = decay(t.G[kC - 1], t.G[tid]) * fK[tid];
     copy_out<P * PL / 16>(link + 2 * PL, sm + L::K);
@@ -1013,7 +1038,7 @@ template <int D, int P>
 __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBwdArgs a, Work w) {
     extern __shared__ __align__(1024) unsigned char sm[];
     constexpr int slices = D / 64;
-    if (!cu_valid(a, w.index)) return;
+    if (!cu_valid(a, w)) return;
     dependency_wait();
     const int unit = blockIdx.x / slices, slice = blockIdx.x % slices;
     const Span s = seq_span(a, unit / a.H);
@@ -1097,13 +1122,29 @@ struct Flat {
     }
 };
 
-// A pair of elements of a q/k/v-like tensor.
-__device__ __forceinline__ float2 load2(const void* src, gdn_dtype dt, long i) {
+// A pair of elements of a q/k/v-like tensor, kept as it is in memory until it is wanted (with P = 1 the tensor
+// is bf16): a conversion behind the load would wait for it.
+template <int P>
+struct Pair {
+    uint32_t raw;
+    __device__ __forceinline__ void load(const void* src, gdn_dtype, long i, bool in) {
+        raw = in ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(src) + i) : 0u;
+    }
+    __device__ __forceinline__ float2 value() const {
+        return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
+    }
+};
+template <>
+struct Pair<2> {
     float x[2];
-    if (dt == GDN_BF16) load_vec<2>(static_cast<const __nv_bfloat16*>(src) + i, x);
-    else load_vec<2>(static_cast<const float*>(src) + i, x);
-    return make_float2(x[0], x[1]);
-}
+    __device__ __forceinline__ void load(const void* src, gdn_dtype dt, long i, bool in) {
+        x[0] = x[1] = 0.f;
+        if (!in) return;
+        if (dt == GDN_BF16) load_vec<2>(static_cast<const __nv_bfloat16*>(src) + i, x);
+        else load_vec<2>(static_cast<const float*>(src) + i, x);
+    }
+    __device__ __forceinline__ float2 value() const { return make_float2(x[0], x[1]); }
+};
 __device__ __forceinline__ void store2(void* dst, gdn_dtype dt, long i, float x, float y) {
     if (dt == GDN_BF16)
         *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(dst) + i) = __floats2bfloat162_rn(x, y);
@@ -1177,12 +1218,13 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     __shared__ uint32_t red[2][NW], tops[2], tmem_at;
     __shared__ uint64_t bars[5];  // of the MMAs; of the copies of T, P and E; of S0's
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
-    const long slots[2] = {(int)blockIdx.x / a.H, next < 0 ? -1 : next / a.H}, slot = slots[0];
+    const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
+    const long slot = slots[0];
     Span spans[2];
-    if (!find_spans<2>(a, w.index, slots, spans) || spans[0].n < 0) return;
+    if (!find_spans<2>(a, w, slots, spans) || spans[0].n < 0) return;
     dependency_wait();
     const Span& s = spans[0];
-    const int h = blockIdx.x % a.H, rep = a.H / a.Hk, hk = h / rep, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x - slots[0] * a.H, hk = w.rep(h), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long t0 = s.bos + (long)s.c * kC, unit = slot * a.H + h;
     const int len = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
@@ -1239,10 +1281,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         }
         ptx::tc_fence_after();
     };
-    if (warp == 0) {
-        ptx::tmem_alloc(&tmem_at, L::tmem);
-        ptx::tmem_relinquish();
-    }
     Flat<T, D, D> state;
     Flat<T, D, kC> u;
     Scale ss, sds, su;
@@ -1257,6 +1295,10 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         k.fetch(a.k, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
+        if (warp == 1) {  // takes thousands of cycles, while the loads are under way
+            ptx::tmem_alloc(&tmem_at, L::tmem);
+            ptx::tmem_relinquish();
+        }
         if (tid < kC) diag[tid] = meta.p_diag[tid];
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
         const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
@@ -1276,23 +1318,25 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
     const float t_back = meta.t_scale, p_back = meta.p_scale;
-    float2 v[MT][NT][2];
+    Pair<P> v[MT][NT][2];
     planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-        v[i][j][hh] = r < len ? load2(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c) : make_float2(0.f, 0.f);
+        v[i][j][hh].load(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c, r < len);
     });
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tm = tmem_at;
     if (spans[1].n >= 0) {
-        const int h2 = next % a.H, hk2 = h2 / rep;
+        const int h2 = next - slots[1] * a.H, hk2 = w.rep(h2);
         prefetch_rows<T, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
         prefetch_rows<T, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
         prefetch_rows<T, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
         prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
+        prefetch_gates(a, spans[1], h2);
         if (tid == 0) {
             prefetch(w.T + next * kTBytes, kTBytes);
             prefetch(w.P + next * kTBytes, kTBytes);
+            prefetch(w.meta + next, sizeof(Meta));
             prefetch_states(next);
         }
     }
@@ -1345,7 +1389,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             float &x = dR[i][j][2 * hh], &y = dR[i][j][2 * hh + 1];
             x *= back;
             y *= back;
-            vdot[i][hh] = fmaf(x, v[i][j][hh].x, fmaf(y, v[i][j][hh].y, vdot[i][hh]));
+            const float2 vv = v[i][j][hh].value();
+            vdot[i][hh] = fmaf(x, vv.x, fmaf(y, vv.y, vdot[i][hh]));
             if (r < len) store2(a.dv, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c, t.beta[r] * x, t.beta[r] * y);
         });
         const uint32_t top = planes::max_bits(dR);
@@ -1541,9 +1586,10 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         return e;
     };
     // through the normalisation: with xh = scale * x * inv and n = x * inv, dx = scale * inv * (d - n (n . d))
+    const bool grouped = a.H > a.Hk;
     if (row < len) {
-        const gdn_dtype type = rep > 1 ? GDN_F32 : a.qkv_dtype;
-        const long at = ((t0 + row) * (rep > 1 ? a.H : a.Hk) + (rep > 1 ? h : hk)) * D + c0;
+        const gdn_dtype type = grouped ? GDN_F32 : a.qkv_dtype;
+        const long at = ((t0 + row) * (grouped ? a.H : a.Hk) + (grouped ? h : hk)) * D + c0;
         const float dp = dpp[row], fq_row = fQ[row], fk_row = fK[row];
         if (part == 0) {
             const float qd = a.use_l2 ? fmaf(sum_of(0, row, CG), fq_row, diag[row]) / (a.scale * a.scale) * fq_row : 0.f;
@@ -1555,7 +1601,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
                 planes::read8(Q, row, c0 + i, q);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) out[j] = o * (fmaf(dk_row, k[j], y[i + j]) - q[j] * qd);
-                store8(rep > 1 ? w.dq : a.dq, type, at + i, out);
+                store8(grouped ? w.dq : a.dq, type, at + i, out);
             }
         } else {
             const float beta = t.beta[row], o = kinv[row], dq_row = dp * fq_row;
@@ -1573,7 +1619,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
                     const float d = fmaf(beta, y[i + j], fmaf(dq_row, q[j], z[i + j] + zz[j]));
                     out[j] = o * (d - k[j] * kd);
                 }
-                store8(rep > 1 ? w.dk : a.dk, type, at + i, out);
+                store8(grouped ? w.dk : a.dk, type, at + i, out);
             }
         }
     }
@@ -1616,7 +1662,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
 // dq, dk of grouped heads: the sum over the group's value heads, in order.  Tokens outside every
 // sequence are left as they were.
 __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdArgs a, Work w) {
-    if (!cu_valid(a, w.index)) return;
+    if (!cu_valid(a, w)) return;
     dependency_wait();
     const int rep = a.H / a.Hk;
     const long first = a.cu_seqlens ? a.cu_seqlens[0] : 0;
@@ -1640,7 +1686,12 @@ template <int D, int P>
 cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
     const size_t slots = (size_t)slot_count(a.num_seqs, a.total_T), units = slots * a.H;
     const bool index = a.cu_seqlens && a.num_seqs > kScanSeqs;
-    const Work w = work_of(a.workspace, slots, units, (size_t)a.total_T * a.H, D, P, index);
+    Work w = work_of(a.workspace, slots, units, (size_t)a.total_T * a.H, D, P, index);
+    w.heads = Divisor::of(a.H);
+    w.rep = Divisor::of(a.H / a.Hk);
+    w.len = a.cu_seqlens ? 0 : a.total_T / a.num_seqs;
+    w.per = (w.len + kC - 1) / kC;
+    w.chunks = Divisor::of(w.per > 0 ? w.per : 1);
     const int prep = PrepSmem<D, P>::bytes, grad = GradSmem<D, P>::bytes, scan = scan_bytes(D, P);
     auto allow = [](const void* f, int bytes) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
