@@ -933,8 +933,19 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) load_vec<2>(p + hh * 8 * (BACK ? D : kC) + 8 * j, x[j] + 2 * hh);
     };
+    // this block's rows of them, and its half or whole of a link, in L2 some steps before
+    constexpr int AHEAD = 4;
+    auto ask = [&](int i) {
+        if (i >= s.chunks) return;
+        if (BACK) prefetch(w.dS + (unit_of(i) * D + slice * 64) * D, 64 * D * 4);
+        else prefetch(w.U + (unit_of(i) * D + slice * 64) * kC, 64 * kC * 4);
+        prefetch(w.link + unit_of(i) * LINK + slice * (LINK / (D / 64) / 16 * 16), LINK / (D / 64) / 16 * 16);
+    };
+    if (threadIdx.x == 32)
+        for (int i = 1; i < AHEAD; ++i) ask(i);
     load_x(0);
     for (int i = 0; i < s.chunks; ++i) {
+        if (threadIdx.x == 32) ask(i + AHEAD);
         const long unit = unit_of(i);
         float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + n0 + c2;
         float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + c2;
