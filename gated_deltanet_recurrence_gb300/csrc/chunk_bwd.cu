@@ -33,8 +33,8 @@
 //
 // The chain over the chunks is the only serial part, so it is kept to what the state meets, and the rest
 // runs over all chunks at once; the price is what the kernels hand over, 295 KB a chunk and head at d = 128.
-// Measured on 2 x 4096 tokens, 16 heads, d = 128, bf16: 0.73 ms in all (inputs and outputs alone would take
-// 35 us at the copy rate), prep 198, scan 213, grad 322 us; 16384 tokens, 32 heads: 2.74 ms.
+// Measured on 2 x 4096 tokens, 16 heads, d = 128, bf16: 0.68 ms in all (inputs and outputs alone would take
+// 35 us at the copy rate), prep 189, scan 212, grad 284 us; 16384 tokens, 32 heads: 2.55 ms.
 #include "mma_planes.cuh"
 #include "sm100_ptx.cuh"
 #include "train_internal.cuh"
@@ -590,8 +590,8 @@ __device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
 // factors, then P) and a 64 x d buffer (W, then dY); before them, over both, A and T in fp32.  d = 128 in
 // bf16 takes 96 KB, so two blocks share an SM and one works while the other waits at a barrier.
-// No pipe is full (198 us at the sizes above: tensor pipe 25%, shared memory 48%, issue slots 36%, DRAM
-// 2.5 TB/s): what is left is the latency of a chunk's dependent steps.  Blocks that stay on their SM took
+// No pipe is full (189 us at the sizes above: tensor pipe 26%, shared memory 51%, issue slots 37%, DRAM
+// 2.6 TB/s): what is left is the latency of a chunk's dependent steps.  Blocks that stay on their SM took
 // 210 us (what the loop keeps in registers spills).
 template <int D, int P>
 struct PrepSmem {
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 // U^T or E^T (16 x 64) and take the second product for their own columns.  The chunks' links arrive by
 // bulk copies; each pair of warps waits for a link and gives it back by itself, so that pairs drift apart
 // and one sub-partition's two warps (of two pairs) are not in the same phase.
-// At the sizes above 128 blocks take 64 steps of 3.3 us (6.2k cycles); MMAs fill 41% of it, the rest is the
+// At the sizes above 128 blocks take 64 steps of 3.3 us (6.2k cycles); MMAs fill 42% of it, the rest is the
 // splitting of S and Z into planes and the wait for the other half.  With the links copied by all warps
 // between block barriers it took 252 us; with the transposed state on tcgen05, 250 us: its products have
 // N = 64 and are bound by reading the left side from shared memory (56 cycles each).
@@ -1068,10 +1068,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
 //        plane in rows 64 .. 127, to be added up
 // A thread then has one token's row: of dQ (TMEM lanes 0 .. 63) or of F and dK (lanes 64 .. 127), and 32
 // columns of it.
-// 322 us at the sizes above (398 with all products on warp-level MMAs): about 36k cycles a chunk, a third
-// of them loading and splitting its first tiles, and 6k from block to block; tensor pipe 13%, issue slots 35%, DRAM
-// 2.5 TB/s.  Blocks that stay on their SM took 382 us with the chunk in the loop (spills) and 447 us as a
-// function of its own.
+// 284 us at the sizes above: some 36k cycles a chunk, 10k of them until its first tiles are in place; tensor
+// pipe 15%, issue slots 38%, DRAM 2.6 TB/s.  What brought it there, from 398 us: the products on tcgen05 (351),
+// P from the preparation (320), E's and v's loads a phase earlier (314), T, P, E and S0 by bulk copies instead
+// of through registers (302), no divisions, and no wait for TMEM or v, at a block's start (289).  Blocks that
+// stay on their SM took 382 against 320 us with the chunk in the loop (spills) and 447 as a function of its own.
 
 constexpr uint64_t kMmaWaitNs = 2000000000ull;
 

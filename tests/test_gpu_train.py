@@ -91,6 +91,22 @@ def test_chunk_bwd_fp32_dout_of_bf16_inputs_and_equal_lengths():
     check_chunk(inp, dict(zip(NAMES, got)))
 
 
+@pytest.mark.parametrize("num,length,H,Hk,d,dtype", [
+    (7, 100, 15, 5, 64, BF16), (3, 129, 14, 2, 128, BF16), (5, 64, 11, 11, 64, F32), (9, 1, 7, 1, 128, F32), (2, 700, 13, 1, 128, BF16)])
+def test_chunk_bwd_equal_lengths_of_odd_counts(num, length, H, Hk, d, dtype):
+    """Blocks find their head, group and sequence by division: counts that are no powers of two, and more
+    blocks than fit the device at once."""
+    inp = delta_inputs([length] * num, H, Hk, d, dtype, seed=num + H)
+    args = [dev(inp[x]) for x in ("q", "k", "v", "g", "beta", "dout")]
+    got = gdn.gdn_chunk_bwd(*args, num_seqs=num, initial_state=dev(inp["initial_state"]),
+                            dfinal_state=dev(inp["dfinal_state"]))
+    assert gdn.gdn_get_device_error() == 0
+    check_chunk(inp, dict(zip(NAMES, got)))
+    packed = chunk_bwd(inp)
+    for x, y in zip(NAMES, got):
+        assert torch.equal(packed[x], y), x
+
+
 def test_chunk_bwd_is_reproducible_and_aliases_the_state_gradient():
     inp = delta_inputs([200, 33], 4, 2, 128, BF16, seed=8)
     one, two = chunk_bwd(inp), None
