@@ -435,25 +435,25 @@ __device__ __forceinline__ void prefetch(const void* p, uint32_t bytes) {
 // Asks for the rows of a chunk of one token tensor that a later block will read, LINES of 128 bytes each;
 // all T threads.
 template <int T, int LINES>
-__device__ __forceinline__ void prefetch_lines(const char* src, const Span& s, int heads, int h) {
+__device__ __forceinline__ void prefetch_lines(const char* src, const Span& s, int heads, int h, int tid) {
     const long t0 = s.bos + (long)s.c * kC;
     const int rows = s.eos - t0 < kC ? (int)(s.eos - t0) : kC;
     const char* first = src + (t0 * heads + h) * (LINES * 128);
 #pragma unroll
-    for (int i = threadIdx.x; i < kC * LINES; i += T)
+    for (int i = tid; i < kC * LINES; i += T)
         if (i / LINES < rows)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(first + (long)(i / LINES) * heads * (LINES * 128) + i % LINES * 128));
 }
 template <int T, int D>
-__device__ __forceinline__ void prefetch_rows(const void* src, gdn_dtype dt, const Span& s, int heads, int h) {
-    if (dt == GDN_BF16) prefetch_lines<T, D / 64>(static_cast<const char*>(src), s, heads, h);
-    else prefetch_lines<T, D / 32>(static_cast<const char*>(src), s, heads, h);
+__device__ __forceinline__ void prefetch_rows(const void* src, gdn_dtype dt, const Span& s, int heads, int h, int tid) {
+    if (dt == GDN_BF16) prefetch_lines<T, D / 64>(static_cast<const char*>(src), s, heads, h, tid);
+    else prefetch_lines<T, D / 32>(static_cast<const char*>(src), s, heads, h, tid);
 }
 
 // The same of its g and beta, a token a thread.
-__device__ __forceinline__ void prefetch_gates(const ChunkBwdArgs& a, const Span& s, int h) {
-    const long t = s.bos + (long)s.c * kC + threadIdx.x;
-    if (threadIdx.x < kC && t < s.eos) {
+__device__ __forceinline__ void prefetch_gates(const ChunkBwdArgs& a, const Span& s, int h, int tid) {
+    const long t = s.bos + (long)s.c * kC + tid;
+    if (tid < kC && t < s.eos) {
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.g + t * a.H + h));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.beta + t * a.H + h));
     }
@@ -471,8 +471,9 @@ constexpr int kLd = kC + 4;  // row of a 64 x 64 fp32 matrix in shared memory (1
 
 // X = (I + A)^-1 for strictly lower triangular A (X's upper triangle is scratch): the four 16 x 16
 // diagonal blocks by substitution, a warp each and a column a lane, then twice the block below two
-// inverted neighbours, X21 = -X22 (A21 X11).
-__device__ void unit_lower_inverse(const float* A, float* X) {
+// inverted neighbours, X21 = -X22 (A21 X11).  Warps 4 .. 7, idle during the substitution, call `meanwhile`.
+template <class Fn>
+__device__ __forceinline__ void unit_lower_inverse(const float* A, float* X, Fn meanwhile) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto row4 = [](const float* p, int i, int j) { return *reinterpret_cast<const float4*>(p + i * kLd + j); };
     if (warp < 4) {
@@ -491,6 +492,8 @@ __device__ void unit_lower_inverse(const float* A, float* X) {
             x[i] = acc[0] + acc[1];
             if (lane < 16) X[(o + i) * kLd + o + c] = x[i];  // zero above the diagonal
         }
+    } else {
+        meanwhile();
     }
     __syncthreads();
 #pragma unroll
@@ -577,14 +580,13 @@ __device__ __forceinline__ void put16(uint32_t dst, unsigned char* image, int r,
     }
 }
 
-// Copies N * 16 bytes from shared to global memory, all threads.
-template <int N>
-__device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char* src) {
-    static_assert(N % kPrepThreads == 0, "");
+// Copies N * 16 bytes from shared to global memory, T threads.
+template <int N, int T>
+__device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char* src, int tid) {
+    static_assert(N % T == 0, "");
 #pragma unroll
-    for (int i = 0; i < N / kPrepThreads; ++i)
-        reinterpret_cast<uint4*>(dst)[i * kPrepThreads + threadIdx.x] =
-            reinterpret_cast<const uint4*>(src)[i * kPrepThreads + threadIdx.x];
+    for (int i = 0; i < N / T; ++i)
+        reinterpret_cast<uint4*>(dst)[i * T + tid] = reinterpret_cast<const uint4*>(src)[i * T + tid];
 }
 
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
@@ -661,18 +663,20 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
                             c + 1 < r ? kk[i][j][2 * hh + 1] * (f * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f);
         });
     }
-    if (spans[1].n >= 0) {
-        const int h2 = next - slots[1] * a.H, hk2 = w.rep(h2);
-        prefetch_rows<kPrepThreads, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
-        prefetch_rows<kPrepThreads, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
-        prefetch_rows<kPrepThreads, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
-        prefetch_rows<kPrepThreads, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
-        prefetch_gates(a, spans[1], h2);
-    }
-    if (tid < kC) tail.c[tid] = decay(t.G[kC - 1], t.G[tid]) * fK[tid];
-    copy_out<P * PL / 16>(link + 2 * PL, sm + L::K);
     __syncthreads();
-    unit_lower_inverse(Af, Tf);
+    unit_lower_inverse(Af, Tf, [&] {
+        constexpr int half = kPrepThreads / 2;
+        const int th = tid - half;
+        copy_out<P * PL / 16, half>(link + 2 * PL, sm + L::K, th);
+        if (th < kC) tail.c[th] = decay(t.G[kC - 1], t.G[th]) * fK[th];
+        if (spans[1].n < 0) return;
+        const int h2 = next - slots[1] * a.H, hk2 = w.rep(h2);
+        prefetch_rows<half, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2, th);
+        prefetch_rows<half, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2, th);
+        prefetch_rows<half, D>(a.v, a.qkv_dtype, spans[1], a.H, h2, th);
+        prefetch_rows<half, D>(a.dout, a.dout_dtype, spans[1], a.H, h2, th);
+        prefetch_gates(a, spans[1], h2, th);
+    });
 
     // T's planes to the workspace; T diag(beta) and T diag(beta b) (with the rows' factors of V and K) as
     // the left sides of U and W
@@ -763,8 +767,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         acc[i][j][2 * hh] = f * q.x - p * acc[i][j][2 * hh];
         acc[i][j][2 * hh + 1] = f * q.y - p * acc[i][j][2 * hh + 1];
     });
-    copy_out<2 * PL / 16>(link, sm + L::W);
-    copy_out<(int)kTBytes / 16>(w.P + unit * kTBytes, sm + L::TX);
+    copy_out<2 * PL / 16, kPrepThreads>(link, sm + L::W, tid);
+    copy_out<(int)kTBytes / 16, kPrepThreads>(w.P + unit * kTBytes, sm + L::TX, tid);
     if (tid == 0) {
         w.meta[unit].p_scale = sp.back;
         tail.w_scale = w_scale;
@@ -1340,11 +1344,11 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const uint32_t tm = tmem_at;
     if (spans[1].n >= 0) {
         const int h2 = next - slots[1] * a.H, hk2 = w.rep(h2);
-        prefetch_rows<T, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2);
-        prefetch_rows<T, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2);
-        prefetch_rows<T, D>(a.v, a.qkv_dtype, spans[1], a.H, h2);
-        prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2);
-        prefetch_gates(a, spans[1], h2);
+        prefetch_rows<T, D>(a.k, a.qkv_dtype, spans[1], a.Hk, hk2, tid);
+        prefetch_rows<T, D>(a.q, a.qkv_dtype, spans[1], a.Hk, hk2, tid);
+        prefetch_rows<T, D>(a.v, a.qkv_dtype, spans[1], a.H, h2, tid);
+        prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2, tid);
+        prefetch_gates(a, spans[1], h2, tid);
         if (tid == 0) {
             prefetch(w.T + next * kTBytes, kTBytes);
             prefetch(w.P + next * kTBytes, kTBytes);
