@@ -34,7 +34,7 @@
 // The chain over the chunks is the only serial part, so it is kept to what the state meets, and the rest
 // runs over all chunks at once; the price is what the kernels hand over, 295 KB a chunk and head at d = 128.
 // Measured on 2 x 4096 tokens, 16 heads, d = 128, bf16: 0.68 ms in all (inputs and outputs alone would take
-// 35 us at the copy rate), prep 189, scan 212, grad 284 us; 16384 tokens, 32 heads: 2.55 ms.
+// 35 us at the copy rate), prep 184, scan 212, grad 284 - 290 us; 16384 tokens, 32 heads: 2.53 ms.
 #include "mma_planes.cuh"
 #include "sm100_ptx.cuh"
 #include "train_internal.cuh"
@@ -592,7 +592,7 @@ __device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
 // factors, then P) and a 64 x d buffer (W, then dY); before them, over both, A and T in fp32.  d = 128 in
 // bf16 takes 96 KB, so two blocks share an SM and one works while the other waits at a barrier.
-// No pipe is full (189 us at the sizes above: tensor pipe 26%, shared memory 51%, issue slots 37%, DRAM
+// No pipe is full (184 us at the sizes above: tensor pipe 26%, shared memory 52%, issue slots 37%, DRAM
 // 2.6 TB/s): what is left is the latency of a chunk's dependent steps.  Blocks that stay on their SM took
 // 210 us (what the loop keeps in registers spills).
 template <int D, int P>
@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
 //        plane in rows 64 .. 127, to be added up
 // A thread then has one token's row: of dQ (TMEM lanes 0 .. 63) or of F and dK (lanes 64 .. 127), and 32
 // columns of it.
-// 284 us at the sizes above: some 36k cycles a chunk, 10k of them until its first tiles are in place; tensor
+// 284 - 290 us at the sizes above: some 36k cycles a chunk, 10k of them until its first tiles are in place; tensor
 // pipe 15%, issue slots 38%, DRAM 2.6 TB/s.  What brought it there, from 398 us: the products on tcgen05 (351),
 // P from the preparation (320), E's and v's loads a phase earlier (314), T, P, E and S0 by bulk copies instead
 // of through registers (302), no divisions, and no wait for TMEM or v, at a block's start (289).  Blocks that
