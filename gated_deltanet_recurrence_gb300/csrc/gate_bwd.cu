@@ -495,7 +495,7 @@ DecayPlan decay_plan(long total_T, int H, bool sums) {
     return p;
 }
 
-// 131072 x 32: 21 us as a replayed graph (plain form 181 us; 15 us at the copy rate), 27 - 30 us called from the
+// 131072 x 32: 21 us as a replayed graph (plain form 181 us; 15 us at the copy rate), 27 - 34 us called from the
 // binding, whose checks and allocations take that long.
 template <int VEC>
 __global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs a, long cols, long stride,
