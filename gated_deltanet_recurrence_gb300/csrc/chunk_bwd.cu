@@ -809,9 +809,11 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 // U^T = (T diag(beta) V)^T - S W^T, then S <- b_C S + U^T Kd; backwards: E^T = dS Kd^T, then
 // dS <- b_C dS + X - E^T W.  The first product is split over the inner dimension, each warp taking its own
 // columns of the state, and the two parts meet through shared memory; both warps then hold the whole of
-// U^T or E^T (16 x 64) and take the second product for their own columns.  The chunks' links arrive by
-// bulk copies; each pair of warps waits for a link and gives it back by itself, so that pairs drift apart
-// and one sub-partition's two warps (of two pairs) are not in the same phase.
+// U^T or E^T (16 x 64) and take the second product for their own columns.  A pair has one barrier a step,
+// between its writes of the parts and their reads, and two places for the parts, used in turn: a warp that
+// writes a place again has met the next step's barrier, which its partner reaches only after reading it.
+// The chunks' links arrive by bulk copies; each pair of warps waits for a link and gives it back by itself, so
+// that pairs drift apart and one sub-partition's two warps (of two pairs) are not in the same phase.
 // At the sizes above 128 blocks take 64 steps of 3.3 us (6.2k cycles); MMAs fill 42% of it, the rest is the
 // splitting of S and Z into planes and the wait for the other half.  With the links copied by all warps
 // between block barriers it took 252 us; with the transposed state on tcgen05, 250 us: its products have
@@ -819,7 +821,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 
 constexpr int kScanThreads = 256;
 constexpr int scan_stages(int d, int p) { return d == 128 && p == 2 ? 2 : 3; }
-constexpr int scan_bytes(int d, int p) { return scan_stages(d, p) * (int)link_bytes(d, p) + 8 * 16 * kC * 4 + 64; }
+constexpr int kParts = 8 * 16 * kC * 4;  // one part of Z of each warp
+constexpr int scan_bytes(int d, int p) { return scan_stages(d, p) * (int)link_bytes(d, p) + 2 * kParts + 64; }
 constexpr uint64_t kWaitNs = 2000000000ull;  // bound on one barrier wait
 
 // N[j] += rows (16 x 16 KT, in the accumulator layout) times B from column n0 and inner index k0: the
@@ -885,12 +888,13 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pair = warp >> 1, half = warp & 1;
     const int block = slice * 4 + pair, row = block * 16 + (lane >> 2), c2 = (lane & 3) * 2, n0 = half * (D / 2);
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
-    float4* mine = reinterpret_cast<float4*>(sm + ST * LINK) + (warp * ZT) * 32 + lane;  // part of Z, [ZT][32]
-    const float4* other = reinterpret_cast<const float4*>(sm + ST * LINK) + ((warp ^ 1) * ZT) * 32 + lane;
+    // parts of Z, [2][warps][ZT][32]: even steps, odd steps
+    float4* parts = reinterpret_cast<float4*>(sm + ST * LINK) + (warp * ZT) * 32 + lane;
+    const int to_other = (warp & 1 ? -1 : 1) * ZT * 32;
     const long state = ((long)s.n * a.H + h) * D * D + row * D + n0 + c2;
     const float* from = BACK ? a.dfinal_state : a.initial_state;
     auto unit_of = [&](int i) { return (s.base + (BACK ? s.chunks - 1 - i : i)) * a.H + h; };
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + ST * LINK + 8 * 16 * kC * 4);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + ST * LINK + 2 * kParts);
     uint64_t* empty = full + ST;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -951,6 +955,8 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
     for (int i = 0; i < s.chunks; ++i) {
         if (threadIdx.x == 32) ask(i + AHEAD);
         const long unit = unit_of(i);
+        float4* mine = parts + (i & 1) * (kParts / 16);
+        const float4* other = mine + to_other;
         float* kept = (BACK ? w.dS : w.S) + unit * D * D + row * D + n0 + c2;
         float* side = (BACK ? w.E : w.U) + (unit * D + row) * kC + c2;
         if (threadIdx.x == 0) fetch(i + 1);

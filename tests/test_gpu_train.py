@@ -107,6 +107,19 @@ def test_chunk_bwd_equal_lengths_of_odd_counts(num, length, H, Hk, d, dtype):
         assert torch.equal(packed[x], y), x
 
 
+@pytest.mark.parametrize("lengths,H,Hk,d,dtype", [([2300], 1, 1, 128, BF16), ([1500, 40], 2, 1, 64, F32),
+                                                  ([1300], 1, 1, 128, F32)])
+def test_chunk_bwd_long_chains(lengths, H, Hk, d, dtype):
+    """Tens of chunks in a row: the scan's warps run far ahead of one another, and every chunk's states, U and E
+    still come from that chunk.  The same call gives the same bits."""
+    inp = delta_inputs(lengths, H, Hk, d, dtype, seed=sum(lengths), a_mean=-4.0)
+    got = chunk_bwd(inp)
+    check_chunk(inp, got)
+    for _ in range(20):
+        again = chunk_bwd(inp)
+        assert all(torch.equal(got[x], again[x]) for x in NAMES)
+
+
 def test_chunk_bwd_is_reproducible_and_aliases_the_state_gradient():
     inp = delta_inputs([200, 33], 4, 2, 128, BF16, seed=8)
     one, two = chunk_bwd(inp), None
