@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(1024) chunk_bwd_index_kernel(ChunkBwdArgs a, i
 // ---- workspace ---------------------------------------------------------------------------------
 // Per (slot, head):
 //   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
-//   T, P   planes of T and of P
+//   T, P   T^T and P^T (fp32 [64, 64], on and above the diagonal): the gradient kernel's planes of them carry
+//          factors of dY's and of other rows, which have to go in before the rounding
 //   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
 //   S      S0 (fp32 [d, d])                             dS  X, then dS1 (fp32 [d, d])
 //   meta   scales and maxima
@@ -132,19 +133,19 @@ static_assert(sizeof(LinkTail) == 512, "");
 
 struct Meta {
     uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
-    float t_scale, p_scale, pad[14];
+    float pad[16];
     float p_diag[kC];  // P's diagonal, q_i . k_i
 };
 static_assert(sizeof(Meta) == 512, "");
 
-constexpr size_t kTBytes = 2 * kC * kC * sizeof(__half);
+constexpr size_t kTBytes = kC * kC * sizeof(float);
 __host__ __device__ constexpr size_t link_bytes(int d, int p) {
     return (2 + (size_t)p) * kC * d * sizeof(__half) + sizeof(LinkTail);
 }
 
 struct Work {
-    unsigned char *link, *T, *P;
-    float *U, *E, *S, *dS;
+    unsigned char* link;
+    float *T, *P, *U, *E, *S, *dS;
     Meta* meta;
     float *dq, *dk;  // [total_T, H, d] each, grouped heads only
     int* index;      // 1 + slots, many sequences only (else null)
@@ -163,9 +164,9 @@ __host__ __forceinline__ Work work_of(void* ws, size_t slots, size_t units, size
     Work w;
     w.index = index ? static_cast<int*>(ws) : nullptr;
     w.link = static_cast<unsigned char*>(ws) + index_bytes(slots);
-    w.T = w.link + units * link_bytes(d, p);
-    w.P = w.T + units * kTBytes;
-    w.U = reinterpret_cast<float*>(w.P + units * kTBytes);
+    w.T = reinterpret_cast<float*>(w.link + units * link_bytes(d, p));
+    w.P = w.T + units * kC * kC;
+    w.U = w.P + units * kC * kC;
     w.E = w.U + units * kC * d;
     w.S = w.E + units * kC * d;
     w.dS = w.S + units * d * d;
@@ -560,23 +561,16 @@ __device__ __forceinline__ void unit_lower_inverse(const float* A, float* X, Fn 
     __syncthreads();
 }
 
-// Sixteen scaled elements of row r from column c into the planes of a 64 x 64 matrix, in shared memory
-// (dst) or as their image in global memory (image).
-__device__ __forceinline__ void put16(uint32_t dst, unsigned char* image, int r, int c, const float (&x)[16]) {
-    uint32_t hi[8], lo[8];
+// N scaled elements of row r from column c (both multiples of eight) into the planes of a 64 x 64 matrix.
+template <int N, int LO>
+__device__ __forceinline__ void put_part(Mat<kC, 2, LO, 0> dst, int r, int c, const float (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) planes::split(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+    for (int i = 0; i < N; i += 8) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t o = planes::offset<kC, 0>(r, c + 8 * i);
-        if (image) {
-            *reinterpret_cast<uint4*>(image + o) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            *reinterpret_cast<uint4*>(image + kTBytes / 2 + o) =
-                make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-        } else {
-            planes::sts128(dst + o, hi + 4 * i);
-            planes::sts128(dst + kTBytes / 2 + o, lo + 4 * i);
-        }
+        for (int j = 0; j < 4; ++j) planes::split(x[i + 2 * j], x[i + 2 * j + 1], hi[j], lo[j]);
+        planes::sts128(dst(r, c + i), hi);
+        planes::sts128(dst(r, c + i) + LO, lo);
     }
 }
 
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
-    __shared__ uint32_t red[7][NW], tops[2];
+    __shared__ uint32_t red[5][NW], tops[2];
     const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
     const long slot = slots[0];
@@ -678,40 +672,35 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         prefetch_gates(a, spans[1], h2, th);
     });
 
-    // T's planes to the workspace; T diag(beta) and T diag(beta b) (with the rows' factors of V and K) as
-    // the left sides of U and W
+    // T to the workspace; T diag(beta) and T diag(beta b) (with the rows' factors of V and K) as the left
+    // sides of U and W
     float tr[16];
     const int rr = tid >> 2, rc = (tid & 3) * 16;
     {
-        uint32_t m0 = 0, m1 = 0, m2 = 0;
+        uint32_t m1 = 0, m2 = 0;
 #pragma unroll
         for (int i = 0; i < 16; i += 4) load_vec<4>(Tf + rr * kLd + rc + i, tr + i);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int j = rc + i;
             tr[i] = j <= rr ? tr[i] : 0.f;
+            if (j <= rr) w.T[(unit * kC + j) * kC + rr] = tr[i];
             const float x = tr[i] * t.beta[j];
-            m0 = max(m0, planes::abs_bits(tr[i]));
             m1 = max(m1, planes::abs_bits(x * fV[j]));
             m2 = max(m2, planes::abs_bits(x * (t.b[j] * fK[j])));
         }
-        m0 = __reduce_max_sync(0xffffffffu, m0);
         m1 = __reduce_max_sync(0xffffffffu, m1);
         m2 = __reduce_max_sync(0xffffffffu, m2);
-        if (lane == 0) { red[0][warp] = m0; red[1][warp] = m1; red[2][warp] = m2; }
+        if (lane == 0) { red[0][warp] = m1; red[1][warp] = m2; }
     }
     __syncthreads();
-    const Scale st = planes::scale_of(planes::top_of<NW>(red[0], lane));
-    const Scale su = planes::scale_of(planes::top_of<NW>(red[1], lane));
-    const Scale sk = planes::scale_of(planes::top_of<NW>(red[2], lane));
+    const Scale su = planes::scale_of(planes::top_of<NW>(red[0], lane));
+    const Scale sk = planes::scale_of(planes::top_of<NW>(red[1], lane));
     {
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = tr[i] * st.mul;
-        put16(0, w.T + unit * kTBytes, rr, rc, x);
-#pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = tr[i] * t.beta[rc + i] * fV[rc + i] * su.mul;
-        put16(TX.at, nullptr, rr, rc, x);
+        put_part(TX, rr, rc, x);
     }
     __syncthreads();
     float acc[2][NT][4];
@@ -726,14 +715,14 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = tr[i] * t.beta[rc + i] * (t.b[rc + i] * fK[rc + i]) * sk.mul;
-        put16(TX.at, nullptr, rr, rc, x);
+        put_part(TX, rr, rc, x);
     }
     __syncthreads();
     planes::clear(acc);
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, K, nd, lane);
     {
         const uint32_t top = planes::max_bits(acc);
-        if (lane == 0) red[3][warp] = top;
+        if (lane == 0) red[2][warp] = top;
     }
     float qk[2][2][4];  // P
     planes::clear(qk);
@@ -745,14 +734,16 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         y = c + 1 <= r ? y * (fQ[r] * fK[c + 1]) * decay(gr, t.G[c + 1]) : 0.f;
         if (c == r) w.meta[unit].p_diag[r] = x;
         if (c + 1 == r) w.meta[unit].p_diag[r] = y;
+        if (c <= r) w.P[(unit * kC + c) * kC + r] = x;
+        if (c + 1 <= r) w.P[(unit * kC + c + 1) * kC + r] = y;
     });
     {
         const uint32_t top = planes::max_bits(qk);
-        if (lane == 0) red[4][warp] = top;
+        if (lane == 0) red[3][warp] = top;
     }
     __syncthreads();
-    const Scale sw = planes::scale_of(planes::top_of<NW>(red[3], lane));  // of acc: W = acc * sk.back
-    const Scale sp = planes::scale_of(planes::top_of<NW>(red[4], lane));
+    const Scale sw = planes::scale_of(planes::top_of<NW>(red[2], lane));  // of acc: W = acc * sk.back
+    const Scale sp = planes::scale_of(planes::top_of<NW>(red[3], lane));
     planes::write(W, acc, m, nd, lane, sw.mul);
     planes::write(TX, qk, m, nc, lane, sp.mul);
     Rows<NW, D, P> y;
@@ -768,12 +759,9 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         acc[i][j][2 * hh + 1] = f * q.y - p * acc[i][j][2 * hh + 1];
     });
     copy_out<2 * PL / 16, kPrepThreads>(link, sm + L::W, tid);
-    copy_out<(int)kTBytes / 16, kPrepThreads>(w.P + unit * kTBytes, sm + L::TX, tid);
     if (tid == 0) {
-        w.meta[unit].p_scale = sp.back;
         tail.w_scale = w_scale;
         tail.b_last = t.b[kC - 1];
-        w.meta[unit].t_scale = st.back;
     }
     __syncthreads();  // W, V and Q have been read
     y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
@@ -784,10 +772,10 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     });
     {
         const uint32_t top = planes::max_bits(acc);
-        if (lane == 0) red[5][warp] = top;
+        if (lane == 0) red[4][warp] = top;
     }
     __syncthreads();
-    const Scale sq = planes::scale_of(planes::top_of<NW>(red[5], lane));
+    const Scale sq = planes::scale_of(planes::top_of<NW>(red[4], lane));
     planes::write(Qp, acc, m, nd, lane, sq.mul);
     __syncthreads();
 #pragma unroll
@@ -1088,8 +1076,14 @@ constexpr uint64_t kMmaWaitNs = 2000000000ull;
 
 // Shared memory.  YR holds dY (rows 0 .. 63) above dR (rows 64 .. 127), two planes; later dP^T's and Z^T's
 // left sides go where dR was, and with `share` Q comes and goes in dY's place.  ST holds S0, then dS1, then
-// the rows that pass from one half of the lanes to the other.  SQ holds P above T, then dP above Z.  B1
-// holds P^T dY + E, then U^T, then the row sums.
+// the rows that pass from one half of the lanes to the other.  SQ holds P^T's planes, then T^T's, beside T^T
+// in fp32 (P^T comes in fp32 to dR's place), then maxima and scales (at SQ + TMP), then dP above Z.  B1 holds
+// E, then P^T dY + E, then U^T, then the row sums.
+//
+// A token's results have to hold beside those of any other token of the chunk, whose dY may be larger by any
+// factor: what has a row a token gets a power of two a row.  dY_i, dR_i and (P^T dY + E)_i carry theirs where
+// they are right sides too: there the other side's column i is multiplied by it in fp32, before its own rows
+// are scaled and split (tri_planes; dP^T Q and Z^T K have their scales by columns for the same reason).
 template <int D, int P>
 struct GradSmem {
     // d = 64: two blocks share an SM, which takes Q out; d = 128 in fp32 needs the room as well
@@ -1099,6 +1093,9 @@ struct GradSmem {
     static constexpr int H2 = D / 64, half = kC * 128, plane = half * H2, yr = 2 * plane, st = D * 128 * H2;
     static constexpr int K = 0, Q = P * plane, YR = share ? Q : 2 * P * plane;
     static constexpr int ST = YR + 2 * yr, SQ = ST + 2 * st, B1 = SQ + 4 * half, bytes = B1 + 2 * plane;
+    // at TMP: maxima of dR's rows [4][64], dR's scales [64], maxima of dP's and Z's rows [column group][128] and
+    // columns [4][64]
+    static constexpr int TMP = 2 * half, tRows = TMP, tScale = TMP + 1024, tPZ = TMP + 2048, tCols = TMP + 4096;
     static constexpr int WM = D / 32, threads = WM * 128;
     // TMEM columns: D1, D2, D3, then NZ and HH in turn
     static constexpr int tD1 = 0, tD2 = D, tD3 = 2 * D, tNZ = 3 * D, tmem = 4 * D;
@@ -1229,6 +1226,53 @@ __device__ __forceinline__ void issue(uint32_t d, uint32_t A, int a_block, uint3
     }
 }
 
+// The planes of X diag(f) for an upper triangular X (rows of fp32 at x), each row with a power of two of its
+// own: T threads, N elements each (a row's lanes are neighbours), f of this thread's columns.  back[r] takes
+// row r of the planes to X diag(f).
+template <int T, int LO, int N>
+__device__ __forceinline__ void tri_planes(Mat<kC, 2, LO, 0> dst, const float* x, const float (&f)[N], float* back) {
+    static_assert(N == kC * kC / T, "");
+    constexpr int LPR = kC / N;
+    const int r = threadIdx.x / LPR, c = (threadIdx.x % LPR) * N;
+    float y[N];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) load_vec<4>(x + i, y + i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        y[i] = c + i >= r ? y[i] * f[i] : 0.f;  // below the diagonal nothing was written
+        top = max(top, planes::abs_bits(y[i]));
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const Scale s = planes::scale_of(top);
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] *= s.mul;
+    put_part(dst, r, c, y);
+    if (c == 0) back[r] = s.back;
+}
+
+// The largest magnitudes of a warp's part of its rows into tops[column of warps][row].
+template <int MT, int NT>
+__device__ __forceinline__ void row_tops(uint32_t* tops, const float (&acc)[MT][NT][4], const int (&m)[MT], int nw, int lane) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) top = max(top, planes::abs_bits(acc[i][j][2 * h + e]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if ((lane & 3) == 0) tops[nw * kC + m[i] + (lane >> 2) + 8 * h] = top;
+        }
+}
+__device__ __forceinline__ Scale row_scale(const uint32_t* tops, int r) {
+    return planes::scale_of(max(max(tops[r], tops[kC + r]), max(tops[2 * kC + r], tops[3 * kC + r])));
+}
+
 template <int D, int P>
 __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2 : 1)
     chunk_bwd_grad_kernel(ChunkBwdArgs a, Work w) {
@@ -1236,8 +1280,10 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     constexpr int T = L::threads, NW = T / 32, WM = L::WM, MT = 4 / WM, HF = L::half, PL = L::plane, CG = NW / 4;
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ Gates t;
-    __shared__ float fK[kC], fQ[kC], fY[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
-    __shared__ uint32_t red[2][NW], tops[2], tmem_at;
+    __shared__ __align__(16) float fY[kC];
+    __shared__ float fK[kC], fQ[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
+    __shared__ uint32_t tops[2], tmem_at;
+    __shared__ float dots[NW];
     __shared__ uint64_t bars[5];  // of the MMAs; of the copies of T, P and E; of S0's
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
@@ -1256,7 +1302,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const Mat<D, P, L::yr, 2 * HF> Y{base + L::YR};
     const Mat<D, 2, L::yr, 2 * HF> R{base + L::YR + HF};
     const Mat<D, 2, L::st, D * 128> ST{base + L::ST};
-    const Mat<kC, 2, 2 * HF, 0> Pm{base + L::SQ}, Tm{base + L::SQ + HF};
+    const Mat<kC, 2, HF, 0> Tri{base + L::SQ};                              // of P^T, then of T^T
+    const Mat<kC, 2, 2 * HF, 0> dP{base + L::SQ}, Zm{base + L::SQ + HF};
     const Mat<D, 2, PL, HF> B1{base + L::B1};
     const Mat<kC, 2, PL, 0> UT{base + L::B1};  // U^T
     // the left sides of D3: planes two blocks apart in dR's place; diag(beta) Z in dY's place or, later, in U's
@@ -1284,12 +1331,10 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         if (blockIdx.x < kSMs) prefetch_states(unit);
         for (int i = 0; i < 5; ++i) ptx::mbar_init(&bars[i], 1);
         ptx::fence_mbar_init();
-        // T goes where it stays; P, E and S0 go, as they are, to the places of what is made of them
         ptx::mbar_arrive_expect_tx(&bars[3], 2 * (uint32_t)kTBytes + kC * D * 4);
-        for (int i = 0; i < 2; ++i) {
-            ptx::bulk_load(sm + L::SQ + 2 * i * HF, w.P + unit * kTBytes + i * HF, HF, &bars[3]);
-            ptx::bulk_load(sm + L::SQ + (2 * i + 1) * HF, w.T + unit * kTBytes + i * HF, HF, &bars[3]);
-        }
+        for (int i = 0; i < 2; ++i)
+            ptx::bulk_load(sm + L::YR + (2 * i + 1) * HF, w.P + unit * kC * kC + i * (HF / 4), HF, &bars[3]);
+        ptx::bulk_load(sm + L::SQ + 2 * HF, w.T + unit * kC * kC, (uint32_t)kTBytes, &bars[3]);
         ptx::bulk_load(sm + L::B1, w.E + unit * kC * D, kC * D * 4, &bars[3]);
         ptx::mbar_arrive_expect_tx(&bars[4], D * D * 4);
         ptx::bulk_load(sm + L::ST, w.S + unit * D * D, D * D * 4, &bars[4]);
@@ -1339,7 +1384,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         sds = planes::scale_of(__reduce_max_sync(0xffffffffu, top[1]));
         su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
-    const float t_back = meta.t_scale, p_back = meta.p_scale;
     Pair<P> v[MT][NT][2];
     planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
         v[i][j][hh].load(a.v, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c, r < len);
@@ -1356,70 +1400,79 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         prefetch_rows<T, D>(a.dout, a.dout_dtype, spans[1], a.H, h2, tid);
         prefetch_gates(a, spans[1], h2, tid);
         if (tid == 0) {
-            prefetch(w.T + next * kTBytes, kTBytes);
-            prefetch(w.P + next * kTBytes, kTBytes);
+            prefetch(w.T + (long)next * kC * kC, kTBytes);
+            prefetch(w.P + (long)next * kC * kC, kTBytes);
             prefetch(w.meta + next, sizeof(Meta));
             prefetch_states(next);
         }
     }
 
+    constexpr int EL = kC * kC / T, LPR = kC / EL;  // a thread's elements of a 64 x 64 matrix, lanes a row
+    const int er = tid / LPR, ec = (tid % LPR) * EL;
+    uint32_t* b1_tops = reinterpret_cast<uint32_t*>(sm + L::YR + HF);  // once P^T has been read
     {
-        // P with the rows' factors of dY, powers of two, which P^T dY contracts over
         wait(3, 0);
-        float fY_top = fmaxf(fY[lane], fY[lane + 32]);
-        fY_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fY_top)));
-        const float fY_inv = 1.f / fY_top;
+        float f[EL];
 #pragma unroll
-        for (int i = 0; i < (int)kTBytes / 16 / T; ++i) {
-            const int e = i * T + tid;
-            const __half2 f = __float2half2_rn(fY[(e & 511) >> 3] * fY_inv);
-            uint4* at = reinterpret_cast<uint4*>(sm + L::SQ + (e >> 9) * 2 * HF + (e & 511) * 16);
-            uint4 pp = *at;
-            __half2* x = reinterpret_cast<__half2*>(&pp);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = __hmul2(x[j], f);
-            *at = pp;
-        }
-        const float pu = p_back * fY_top;
+        for (int i = 0; i < EL; i += 4) load_vec<4>(fY + ec + i, f + i);
+        tri_planes<T>(Tri, reinterpret_cast<const float*>(sm + L::YR + HF + (er >> 5) * 2 * HF) + (er & 31) * kC + ec, f, dpp);
         wait(4, 0);
         state.fetch(reinterpret_cast<const float*>(sm + L::ST));
         __syncthreads();
         state.template put<false>(ST, ss.mul);
         float acc[MT][NT][4];  // P^T dY + E
         planes::clear(acc);
-        planes::product<kC, true, true, planes::kUpper>(acc, Pm, m, Y, nd, lane);
+        planes::product<kC, false, true, planes::kUpper>(acc, Tri, m, Y, nd, lane);
         const float* E = reinterpret_cast<const float*>(sm + L::B1);
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], pu, E[c * kC + r]);
-            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], pu, E[(c + 1) * kC + r]);
+            acc[i][j][2 * hh] = fmaf(acc[i][j][2 * hh], dpp[r], E[c * kC + r]);
+            acc[i][j][2 * hh + 1] = fmaf(acc[i][j][2 * hh + 1], dpp[r], E[(c + 1) * kC + r]);
         });
-        const uint32_t top2 = planes::max_bits(acc);
-        if (lane == 0) red[1][warp] = top2;
+        row_tops(b1_tops, acc, m, nw, lane);
         __syncthreads();
-        planes::write(B1, acc, m, nd, lane, planes::scale_of(planes::top_of<NW>(red[1], lane)).mul);
+        float mul[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) mul[i][hh] = row_scale(b1_tops, m[i] + (lane >> 2) + 8 * hh).mul;
+        planes::write(B1, acc, m, nd, lane, mul);
+    }
+    {
+        float f[EL];  // T^T takes the scales of B1's rows
+#pragma unroll
+        for (int i = 0; i < EL; ++i) f[i] = row_scale(b1_tops, ec + i).back;
+        tri_planes<T>(Tri, reinterpret_cast<const float*>(sm + L::SQ + 2 * HF) + er * kC + ec, f, dpp);
     }
     __syncthreads();
     float vdot[MT][2] = {};
-    Scale sr;
+    float* fR = reinterpret_cast<float*>(sm + L::SQ + L::tScale);  // takes a row of R to dR
     {
-        const float back = t_back * planes::scale_of(planes::top_of<NW>(red[1], lane)).back;
+        uint32_t* dr_tops = reinterpret_cast<uint32_t*>(sm + L::SQ + L::tRows);
         u.fetch(w.U + unit * kC * D);
         float dR[MT][NT][4];
         planes::clear(dR);
-        planes::product<kC, true, true, planes::kUpper>(dR, Tm, m, B1, nd, lane);
+        planes::product<kC, false, true, planes::kUpper>(dR, Tri, m, B1, nd, lane);
         planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
             float &x = dR[i][j][2 * hh], &y = dR[i][j][2 * hh + 1];
-            x *= back;
-            y *= back;
+            x *= dpp[r];
+            y *= dpp[r];
             const float2 vv = v[i][j][hh].value();
             vdot[i][hh] = fmaf(x, vv.x, fmaf(y, vv.y, vdot[i][hh]));
             if (r < len) store2(a.dv, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c, t.beta[r] * x, t.beta[r] * y);
         });
-        const uint32_t top = planes::max_bits(dR);
-        if (lane == 0) red[0][warp] = top;
-        __syncthreads();  // also: B1, P and T have been read
-        sr = planes::scale_of(planes::top_of<NW>(red[0], lane));
-        planes::write(R, dR, m, nd, lane, sr.mul);
+        row_tops(dr_tops, dR, m, nw, lane);
+        __syncthreads();  // also: B1, P^T and T^T have been read
+        float mul[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int r = m[i] + (lane >> 2) + 8 * hh;
+                const Scale sr = row_scale(dr_tops, r);
+                mul[i][hh] = sr.mul;
+                if (nw == 0 && (lane & 3) == 0) fR[r] = sr.back;
+            }
+        planes::write(R, dR, m, nd, lane, mul);
         u.template put<false>(UT, su.mul);
     }
     // D1 and NZ
@@ -1444,7 +1497,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     constexpr int NC = kC / CG;
     float x[NC];
-    uint32_t top1 = 0, top2 = 0;
     wait(0, 0);
     {
         uint32_t raw[NC];
@@ -1452,7 +1504,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         else ptx::tmem_ld32(lanes + L::tNZ + cg * NC, raw);
         ptx::tmem_wait_ld();
         const float2 gr = t.G[row];
-        const float f = part ? -sr.back * su.back : fY[row] * su.back, f2 = part ? t.beta[row] * fK[row] : fQ[row];
+        const float f = (part ? -fR[row] : fY[row]) * su.back, f2 = part ? t.beta[row] * fK[row] : fQ[row];
+        uint32_t top = 0, mine = 0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = cg * NC + i;
@@ -1462,25 +1515,30 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
                 diag[row] *= y;  // dP_ii q_i . k_i
             }
             x[i] = c < row ? y : 0.f;
-            top1 = max(top1, planes::abs_bits(x[i] * fK[c]));
-            top2 = max(top2, planes::abs_bits(x[i] * f2));
+            top = max(top, planes::abs_bits(x[i] * fK[c]));
+            const uint32_t col = __reduce_max_sync(0xffffffffu, planes::abs_bits(x[i] * f2));
+            if (lane == i) mine = col;
         }
+        reinterpret_cast<uint32_t*>(sm + L::SQ + L::tPZ)[cg * 128 + part * kC + row] = top;
+        if (lane < NC) reinterpret_cast<uint32_t*>(sm + L::SQ + L::tCols)[(warp & 3) * kC + cg * NC + lane] = mine;
     }
-    top1 = __reduce_max_sync(0xffffffffu, top1);
-    top2 = __reduce_max_sync(0xffffffffu, top2);
     wait(1, 0);  // S0's planes, dY and dR have been read
     const float state_dot = warp_sum(state.template put<true>(ST, sds.mul));  // and <S0, dS1>
-    // the maxima and the parts of the dot product go where dR's maxima and dY's row factors were
-    static_assert(2 * NW <= kC, "");
-    const float f1 = part ? -t.b[row] * sr.back * ss.back : t.b[row] * fY[row] * ss.back;
+    const float f1 = (part ? -t.b[row] * fR[row] : t.b[row] * fY[row]) * ss.back;
+    if (lane == 0) dots[warp] = state_dot;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    uint32_t* tops2 = reinterpret_cast<uint32_t*>(fY);
-    if (lane == 0) {
-        tops2[warp] = top1;
-        tops2[NW + warp] = top2;
-        reinterpret_cast<float*>(red[0])[warp] = state_dot;
+    // scales: dP's and Z's rows their own for D2; one for a column of both for D3, where they are added: it
+    // goes where dY's row factors were
+    float* fC = fY;
+    if (tid < kC) fC[tid] = row_scale(reinterpret_cast<const uint32_t*>(sm + L::SQ + L::tCols), tid).mul;
+    Scale sk;
+    {
+        const uint32_t* tops_pz = reinterpret_cast<const uint32_t*>(sm + L::SQ + L::tPZ) + part * kC + row;
+        uint32_t top = max(tops_pz[0], tops_pz[128]);
+        if constexpr (CG == 4) top = max(top, max(tops_pz[256], tops_pz[384]));
+        sk = planes::scale_of(top);
     }
     if constexpr (L::share) {
         Rows<NW, D, P> q;
@@ -1488,13 +1546,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
     }
     __syncthreads();
-    // scales: dP's and Z's own for D2 (their rows are apart), one for D3 (their products are added)
-    Scale sk, sq;
-    {
-        const uint32_t y = tops2[lane & (NW - 1)], z = tops2[NW + (lane & (NW - 1))];
-        sk = planes::scale_of(__reduce_max_sync(0xffffffffu, ((lane >> 1) & 1) == part ? y : 0u));
-        sq = planes::scale_of(__reduce_max_sync(0xffffffffu, z));
-    }
     auto put_row = [&](auto dst, auto&& value) {
 #pragma unroll
         for (int i = 0; i < NC; i += 8) {
@@ -1506,10 +1557,10 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             planes::sts128(at + decltype(dst)::lo, lo);
         }
     };
-    put_row(part ? Tm : Pm, [&](int i) { return x[i] * (fK[cg * NC + i] * sk.mul); });
-    const float fq = (part ? t.beta[row] * fK[row] : fQ[row]) * sq.mul;
-    if (part == 0) put_row(Pt, [&](int i) { return x[i] * fq; });
-    else if (!L::late) put_row(Zt, [&](int i) { return x[i] * fq; });
+    put_row(part ? Zm : dP, [&](int i) { return x[i] * fK[cg * NC + i] * sk.mul; });
+    const float fq = part ? t.beta[row] * fK[row] : fQ[row];
+    if (part == 0) put_row(Pt, [&](int i) { return x[i] * fq * fC[cg * NC + i]; });
+    else if (!L::late) put_row(Zt, [&](int i) { return x[i] * fq * fC[cg * NC + i]; });
     ptx::fence_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
@@ -1530,7 +1581,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     }
     if constexpr (L::late) {
         wait(0, 1);  // U has been read
-        if (part) put_row(Zt, [&](int i) { return x[i] * fq; });
+        if (part) put_row(Zt, [&](int i) { return x[i] * fq * fC[cg * NC + i]; });
         ptx::fence_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
@@ -1549,6 +1600,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     float dot0 = 0.f, dot1 = 0.f, dot2 = 0.f;  // dQ . q or F . k; H . k; (dK- - H) . k
     {
         const float fh = decay(t.G[kC - 1], t.G[row]) * su.back * sds.back;
+        const float fd = __uint_as_float((254u << 23) - __float_as_uint(fC[row]));  // 1 / fC, a power of two
         uint32_t r1[32], r2[32];
         ptx::tmem_ld32(lanes + L::tD1 + c0, r1);
         ptx::tmem_ld32(lanes + L::tD2 + c0, r2);
@@ -1565,7 +1617,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             if (part == 0) planes::read8(Q, row, c0 + i, q);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float hx = __uint_as_float(r2[i + j]) * fh, dx = __uint_as_float(r1[i + j]) * sq.back;
+                const float hx = __uint_as_float(r2[i + j]) * fh, dx = __uint_as_float(r1[i + j]) * fd;
                 dot0 = fmaf(y[i + j], part ? k[j] : q[j], dot0);
                 dot1 = fmaf(hx, k[j], dot1);
                 dot2 = fmaf(dx, k[j], dot2);
@@ -1656,7 +1708,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             d[e] = sum_of(0, r, CG) * fQ[r] + t.beta[r] * kp - (sum_of(4, r, CG) + sum_of(5, r, CG)) * fK[r];
             hd[e] = (sum_of(2, r, CG) + sum_of(3, r, CG)) * fK[r];
         }
-        const float* dots = reinterpret_cast<const float*>(red[0]);
         const float carried = t.b[kC - 1] * ss.back * warp_sum(lane < NW ? dots[lane] : 0.f);
         float after = d[0] + d[1], before = hd[0] + hd[1];  // inclusive sums over the later, the earlier lanes
 #pragma unroll

@@ -220,6 +220,19 @@ __device__ __forceinline__ void write(Mat<COLS, 2, LO, HS> dst, const float (&ac
     });
 }
 
+// The same with a factor for each row.
+template <int COLS, int LO, int HS, int MT, int NT>
+__device__ __forceinline__ void write(Mat<COLS, 2, LO, HS> dst, const float (&acc)[MT][NT][4], const int (&m)[MT], int n0,
+                                      int lane, const float (&mul)[MT][2]) {
+    pairs<MT, NT>(m, n0, lane, [&](int i, int j, int h, int, int) {
+        uint32_t hi, lo;
+        split(acc[i][j][2 * h] * mul[i][h], acc[i][j][2 * h + 1] * mul[i][h], hi, lo);
+        const uint32_t at = pair_at<NT>(dst, m[i], n0, j, h, lane);
+        sts32(at, hi);
+        sts32(at + LO, lo);
+    });
+}
+
 // The pair (i, j, h) of a matrix, without its scale.
 template <int NT, int COLS, int P, int LO, int HS>
 __device__ __forceinline__ float2 read(Mat<COLS, P, LO, HS> a, int m, int n0, int j, int h, int lane) {

@@ -81,6 +81,71 @@ def delta_grads(inp, scale=None, use_l2=True):
     return dict(zip(("dq", "dk", "dv", "dg", "dbeta", "dinitial_state"), got))
 
 
+# Half a step of an operand of a product that is kept in 22 bits.
+EPS = 2.0 ** -23
+
+
+def delta_errors(inp, scale=None, use_l2=True):
+    """Standard deviations, in units of EPS, of the gradients of delta_grads token by token when every operand and
+    every term of the chunk form is rounded once to within EPS (decays to 2 EPS): first-order propagation of variances in fp64
+    (M below is a matrix's values, its variance var_M; a product's is var_A B^2 + A^2 var_B + 2 A^2 B^2).  dq, dk
+    [T, Hk] and dv [T, H] (a vector's 2-norm), dg and dbeta [T, H].  A token's gradient may be far smaller than
+    the terms that it is the sum of, and its error goes by them."""
+    (T, Hk, d), H, cu = inp["q"].shape, inp["v"].shape[1], inp["cu"]
+    scale = d ** -0.5 if scale is None else scale
+    q, k, v, g, beta, dy = (inp[x].to(F64) for x in ("q", "k", "v", "g", "beta", "dout"))
+    rep = lambda x: x.repeat_interleave(H // Hk, 1)  # noqa: E731
+    rq, rk = (rep(torch.rsqrt((x * x).sum(-1) + 1e-6) if use_l2 else torch.ones(T, Hk, dtype=F64)) for x in (q, k))
+    q, k = rep(q) * rq[..., None] * scale, rep(k) * rk[..., None]
+    out = {x: torch.zeros(T, H, dtype=F64) for x in ("dq", "dk", "dv", "dg", "dbeta")}
+
+    def mul(A, B):  # (values, variances) of a product of two such pairs
+        (a, va), (b, vb) = A, B
+        return a @ b, va @ b ** 2 + a ** 2 @ vb + 2 * a ** 2 @ b ** 2
+
+    exact = lambda x: (x, torch.zeros_like(x))  # noqa: E731
+    add = lambda A, B, s=1.0: (A[0] + s * B[0], A[1] + B[1])  # noqa: E731
+    by = lambda f, A: (f * A[0], f ** 2 * A[1])  # noqa: E731
+    fade = lambda f, A: (f * A[0], f ** 2 * (A[1] + 4 * A[0] ** 2))  # noqa: E731  by a decay, 2 EPS off
+    t = lambda A: (A[0].T, A[1].T)  # noqa: E731
+    dot = lambda A, B: (A[0] * B[0], A[1] * B[0] ** 2 + A[0] ** 2 * (B[1] + 2 * B[0] ** 2))  # noqa: E731
+    for n in range(len(cu) - 1):
+        for h in range(H):
+            S = exact(torch.zeros(d, d, dtype=F64) if inp["initial_state"] is None else inp["initial_state"][n, h].to(F64))
+            chunks = []
+            for c in range(cu[n], cu[n + 1], 64):
+                i = slice(c, min(c + 64, cu[n + 1]))
+                K, Q, V, Y, be, G = exact(k[i, h]), exact(q[i, h]), exact(v[i, h]), exact(dy[i, h]), beta[i, h], g[i, h]
+                G = G.clamp(min=-128).cumsum(0)
+                D, b, tail = torch.exp(G[:, None] - G[None]).tril(), G.exp()[:, None], torch.exp(G[-1] - G)[:, None]
+                A = fade((be[:, None] * D).tril(-1), mul(K, t(K)))
+                X = torch.linalg.solve_triangular(torch.eye(len(be), dtype=F64) + A[0], torch.eye(len(be), dtype=F64), upper=False)
+                X = X, X ** 2 @ (A[1] + A[0] ** 2) @ X ** 2 + X ** 2
+                W, Pm = mul(X, fade(be[:, None] * b, K)), fade(D, mul(Q, t(K)))
+                U = add(mul(X, by(be[:, None], V)), mul(W, t(S)), -1.0)
+                chunks.append((i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S))
+                S = add(fade(b[-1], S), mul(t(fade(tail, U)), K))
+            dS = exact(torch.zeros(d, d, dtype=F64) if inp["dfinal_state"] is None else inp["dfinal_state"][n, h].to(F64))
+            for i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S in reversed(chunks):
+                E = fade(tail, mul(K, t(dS)))
+                dR = mul(t(X), add(mul(t(Pm), Y), E))
+                dP, Z = fade(D, mul(Y, t(U))), fade(-D.tril(-1), mul(dR, t(U)))
+                dQ, F = add(fade(b, mul(Y, S)), mul(dP, K)), add(mul(Z, K), fade(b, mul(dR, S)), -1.0)
+                Hd, rest = fade(tail, mul(U, dS)), add(mul(t(dP), Q), mul(t(Z), by(be[:, None], K)))
+                dK = add(by(be[:, None], F), add(Hd, rest))
+                later = add(add(dot(dQ, Q), dot(by(be[:, None], F), K)), dot(rest, K))[1].sum(-1)
+                out["dq"][i, h] = (scale * rq[i, h]) ** 2 * dQ[1].sum(-1)
+                out["dk"][i, h] = rk[i, h] ** 2 * dK[1].sum(-1)
+                out["dv"][i, h] = be ** 2 * dR[1].sum(-1)
+                out["dbeta"][i, h] = (dot(dR, V)[1] + dot(F, K)[1]).sum(-1)
+                hk = dot(Hd, K)[1].sum(-1)
+                out["dg"][i, h] = later.flip(0).cumsum(0).flip(0) + hk.cumsum(0) - hk + b[-1] ** 2 * dot(S, dS)[1].sum()
+                dS = add(add(fade(b[-1], dS), mul(t(Y), add(fade(b, Q), mul(Pm, W), -1.0))), mul(t(E), W), -1.0)
+    for x in ("dq", "dk"):
+        out[x] = out[x].reshape(T, Hk, H // Hk).sum(-1)
+    return {x: y.sqrt() for x, y in out.items()}
+
+
 def norm_forward(y, z, w, b, eps, rms):
     """The output norm over the last dimension of y [rows, groups, size] (w, b broadcast) with its SiLU."""
     if rms:

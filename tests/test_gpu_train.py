@@ -66,6 +66,49 @@ def test_chunk_bwd_without_normalisation(d, dtype):
     check_chunk(inp, chunk_bwd(inp, use_qk_l2norm=False, scale=0.7), use_l2=False, scale=0.7)
 
 
+def _exponents(pattern, lengths):
+    """Powers of two of a batch's tokens, spread over 2^30 in every chunk of 64."""
+    gen = torch.Generator().manual_seed(len(pattern))
+    out = []
+    for n in lengths:
+        t = torch.arange(n) % 64
+        out.append({"first": torch.where(t == 0, 30, 0), "falling": 15 - t // 2, "rising": t // 2 - 15,
+                    "mixed": torch.randint(-15, 16, (n,), generator=gen)}[pattern])
+    return torch.cat(out).double()
+
+
+def check_tokens(inp, got, **kw):
+    """Each token's and head's gradients by themselves: off by their own rounding and at most ten standard
+    deviations of what the roundings of their terms leave.  (Against the gradient itself no such bound holds, in
+    fp32 neither: with a_mean = 1 and "mixed" below, token 147 of head 0 has dR = 0.0012 from terms of 0.12,
+    0.054, 0.041, 0.024, ..., and half a step of 22 bits of the first alone is 0.12 * 2^-23 / 0.0012 = 1.2e-5.)"""
+    ref, size = delta_grads(inp, **kw), _train.delta_errors(inp, **kw)
+    lo, hi = inp["cu"][0], inp["cu"][-1]
+    for name, sigma in size.items():
+        x, r = (y.detach().cpu().double()[lo:hi] for y in (got[name], ref[name]))
+        assert torch.isfinite(x).all(), name
+        half = 2.0 ** -8 if got[name].dtype == BF16 else 2.0 ** -24
+        off, most = (x - r).abs(), r.abs() * half
+        if x.dim() == 3:
+            off, most = off.norm(dim=-1), most.norm(dim=-1)
+        most = most + 10 * _train.EPS * sigma[lo:hi]
+        assert (off <= most).all(), (name, float((off / most).max()), int((off / most).argmax()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("a_mean", [-4.0, 1.0])
+@pytest.mark.parametrize("pattern", ["first", "falling", "rising", "mixed"])
+def test_chunk_bwd_tokens_whose_gradients_are_far_apart(d, dtype, a_mean, pattern):
+    """The output's gradient 2^30 apart between tokens of a chunk: a token's results keep their accuracy beside
+    the others' (those behind a token with a large one depend on the small ones alone)."""
+    lengths = [64, 100]
+    inp = delta_inputs(lengths, 4, 2, d, dtype, seed=61, a_mean=a_mean, carried=False)
+    e = _exponents(pattern, lengths)
+    inp["dout"] = (inp["dout"].double() * 2.0 ** e[:, None, None]).to(dtype)
+    check_tokens(inp, chunk_bwd(inp))
+
+
 def test_chunk_bwd_first_token_has_no_decay_gradient():
     inp = delta_inputs([1, 1], 2, 2, 128, BF16, seed=3, carried=False)
     assert torch.count_nonzero(chunk_bwd(inp)["dg"]) == 0
