@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(1024) chunk_bwd_index_kernel(ChunkBwdArgs a, i
 
 // ---- workspace ---------------------------------------------------------------------------------
 // Per (slot, head):
-//   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w_scale, b_last
+//   link   what the scan needs of a chunk: planes of W (two) and K (one or two), then c, w, b_last
 //   T, P   T^T and P^T (fp32 [64, 64], on and above the diagonal): the gradient kernel's planes of them carry
 //          factors of dY's and of other rows, which have to go in before the rounding
 //   U      (T diag(beta) V)^T, then U^T (fp32 [d, 64])  E   E^T (fp32 [d, 64])
@@ -127,13 +127,14 @@ __global__ void __launch_bounds__(1024) chunk_bwd_index_kernel(ChunkBwdArgs a, i
 //   meta   scales and maxima
 struct LinkTail {
     float c[kC];  // takes row j of K's planes to Kd: tail_j and the row's factor
-    float w_scale, b_last, pad[62];
-};  // 512 bytes, so that a link's planes, at any of its places, start at a multiple of 512
-static_assert(sizeof(LinkTail) == 512, "");
+    float w[kC];  // takes row j of W's planes to W
+    float b_last, pad[63];
+};  // 768 bytes, so that a link's planes, at any of its places, start at a multiple of 256
+static_assert(sizeof(LinkTail) == 768, "");
 
 struct Meta {
-    uint32_t s_max[16], ds_max[16], u_max[16];  // bits of the largest magnitudes of parts of S0, dS1, U
-    float pad[16];
+    uint32_t s_max[16], ds_max[16];  // bits of the largest magnitudes of parts of S0, dS1
+    float pad[32];
     float p_diag[kC];  // P's diagonal, q_i . k_i
 };
 static_assert(sizeof(Meta) == 512, "");
@@ -583,6 +584,27 @@ __device__ __forceinline__ void copy_out(unsigned char* dst, const unsigned char
         reinterpret_cast<uint4*>(dst)[i * T + tid] = reinterpret_cast<const uint4*>(src)[i * T + tid];
 }
 
+// The largest magnitudes of a warp's part of its rows into tops[column of warps][row].
+template <int MT, int NT>
+__device__ __forceinline__ void row_tops(uint32_t* tops, const float (&acc)[MT][NT][4], const int (&m)[MT], int nw, int lane) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) top = max(top, planes::abs_bits(acc[i][j][2 * h + e]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if ((lane & 3) == 0) tops[nw * kC + m[i] + (lane >> 2) + 8 * h] = top;
+        }
+}
+__device__ __forceinline__ Scale row_scale(const uint32_t* tops, int r) {
+    return planes::scale_of(max(max(tops[r], tops[kC + r]), max(tops[2 * kC + r], tops[3 * kC + r])));
+}
+
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
 // factors, then P) and a 64 x d buffer (W, then dY); before them, over both, A and T in fp32.  d = 128 in
 // bf16 takes 96 KB, so two blocks share an SM and one works while the other waits at a barrier.
@@ -603,7 +625,8 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
-    __shared__ uint32_t red[5][NW], tops[2];
+    __shared__ float back_u[kC], back_w[kC];
+    __shared__ uint32_t red[2][NW], tops[2], w_tops[4 * kC];
     const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
     const long slot = slots[0];
@@ -673,9 +696,11 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     });
 
     // T to the workspace; T diag(beta) and T diag(beta b) (with the rows' factors of V and K) as the left
-    // sides of U and W
+    // sides of U and W, each row with a power of two of its own: a row contracts over its own and earlier
+    // tokens, and keeps its accuracy beside later ones whose v is larger
     float tr[16];
     const int rr = tid >> 2, rc = (tid & 3) * 16;
+    float mul_u, mul_w;
     {
         uint32_t m1 = 0, m2 = 0;
 #pragma unroll
@@ -685,21 +710,28 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
             const int j = rc + i;
             tr[i] = j <= rr ? tr[i] : 0.f;
             if (j <= rr) w.T[(unit * kC + j) * kC + rr] = tr[i];
-            const float x = tr[i] * t.beta[j];
-            m1 = max(m1, planes::abs_bits(x * fV[j]));
-            m2 = max(m2, planes::abs_bits(x * (t.b[j] * fK[j])));
+            tr[i] *= t.beta[j];
+            m1 = max(m1, planes::abs_bits(tr[i] * fV[j]));
+            m2 = max(m2, planes::abs_bits(tr[i] * (t.b[j] * fK[j])));
         }
-        m1 = __reduce_max_sync(0xffffffffu, m1);
-        m2 = __reduce_max_sync(0xffffffffu, m2);
-        if (lane == 0) { red[0][warp] = m1; red[1][warp] = m2; }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {  // a row's four lanes
+            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+        }
+        const Scale su = planes::scale_of(m1), sk = planes::scale_of(m2);
+        mul_u = su.mul;
+        mul_w = sk.mul;
+        if (rc == 0) {
+            back_u[rr] = su.back;
+            back_w[rr] = sk.back;
+        }
     }
     __syncthreads();
-    const Scale su = planes::scale_of(planes::top_of<NW>(red[0], lane));
-    const Scale sk = planes::scale_of(planes::top_of<NW>(red[1], lane));
     {
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = tr[i] * t.beta[rc + i] * fV[rc + i] * su.mul;
+        for (int i = 0; i < 16; ++i) x[i] = tr[i] * fV[rc + i] * mul_u;
         put_part(TX, rr, rc, x);
     }
     __syncthreads();
@@ -707,23 +739,24 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     planes::clear(acc);
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, V, nd, lane);
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
-        w.U[(unit * D + c) * kC + r] = acc[i][j][2 * hh] * su.back;
-        w.U[(unit * D + c + 1) * kC + r] = acc[i][j][2 * hh + 1] * su.back;
+        w.U[(unit * D + c) * kC + r] = acc[i][j][2 * hh] * back_u[r];
+        w.U[(unit * D + c + 1) * kC + r] = acc[i][j][2 * hh + 1] * back_u[r];
     });
     __syncthreads();
     {
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = tr[i] * t.beta[rc + i] * (t.b[rc + i] * fK[rc + i]) * sk.mul;
+        for (int i = 0; i < 16; ++i) x[i] = tr[i] * (t.b[rc + i] * fK[rc + i]) * mul_w;
         put_part(TX, rr, rc, x);
     }
     __syncthreads();
     planes::clear(acc);
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, K, nd, lane);
-    {
-        const uint32_t top = planes::max_bits(acc);
-        if (lane == 0) red[2][warp] = top;
-    }
+    planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
+        acc[i][j][2 * hh] *= back_w[r];
+        acc[i][j][2 * hh + 1] *= back_w[r];
+    });
+    row_tops(w_tops, acc, m, nw, lane);
     float qk[2][2][4];  // P
     planes::clear(qk);
     planes::product<D, false, false>(qk, Q, m, K, nc, lane);
@@ -739,28 +772,52 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     });
     {
         const uint32_t top = planes::max_bits(qk);
-        if (lane == 0) red[3][warp] = top;
+        if (lane == 0) red[0][warp] = top;
     }
     __syncthreads();
-    const Scale sw = planes::scale_of(planes::top_of<NW>(red[2], lane));  // of acc: W = acc * sk.back
-    const Scale sp = planes::scale_of(planes::top_of<NW>(red[3], lane));
-    planes::write(W, acc, m, nd, lane, sw.mul);
-    planes::write(TX, qk, m, nc, lane, sp.mul);
+    const Scale sp = planes::scale_of(planes::top_of<NW>(red[0], lane));
+    // W's rows have powers of two of their own: beside the first rows' the later ones' decays may be anything.
+    // P W contracts over them, so they go into P's columns (as shares of the largest).
+    const float w0 = row_scale(w_tops, lane).back, w1 = row_scale(w_tops, lane + 32).back;
+    const float w_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(w0, w1))));
+    {
+        float mul[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) mul[i][hh] = row_scale(w_tops, m[i] + (lane >> 2) + 8 * hh).mul;
+        planes::write(W, acc, m, nd, lane, mul);
+        if (warp == 0) {
+            tail.w[lane] = w0;
+            tail.w[lane + 32] = w1;
+        }
+        const float share = (nw < 2 ? w0 : w1) * (1.f / w_top);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = __shfl_sync(0xffffffffu, share, (nc + 8 * j + (lane & 3) * 2 + e) & 31) * sp.mul;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    qk[i][j][e] *= f;
+                    qk[i][j][2 + e] *= f;
+                }
+            }
+        planes::write(TX, qk, m, nc, lane, 1.f);
+    }
     Rows<NW, D, P> y;
     y.fetch(a.dout, a.dout_dtype, t0, len, a.H, h, warp, lane);
     __syncthreads();
     planes::clear(acc);  // Q' = diag(b) Q - P W
     planes::product<kC, false, true, planes::kLower>(acc, TX, m, W, nd, lane);
-    const float w_scale = sw.back * sk.back;
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
         const float2 q = planes::read<NT>(Q, m[i], nd, j, hh, lane);
-        const float f = t.b[r] * fQ[r], p = w_scale * sp.back;
+        const float f = t.b[r] * fQ[r], p = w_top * sp.back;
         acc[i][j][2 * hh] = f * q.x - p * acc[i][j][2 * hh];
         acc[i][j][2 * hh + 1] = f * q.y - p * acc[i][j][2 * hh + 1];
     });
     copy_out<2 * PL / 16, kPrepThreads>(link, sm + L::W, tid);
     if (tid == 0) {
-        tail.w_scale = w_scale;
         tail.b_last = t.b[kC - 1];
     }
     __syncthreads();  // W, V and Q have been read
@@ -772,10 +829,10 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     });
     {
         const uint32_t top = planes::max_bits(acc);
-        if (lane == 0) red[4][warp] = top;
+        if (lane == 0) red[1][warp] = top;
     }
     __syncthreads();
-    const Scale sq = planes::scale_of(planes::top_of<NW>(red[4], lane));
+    const Scale sq = planes::scale_of(planes::top_of<NW>(red[1], lane));
     planes::write(Qp, acc, m, nd, lane, sq.mul);
     __syncthreads();
 #pragma unroll
@@ -965,7 +1022,7 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
             for (int e = 0; e < 4; ++e) Z[j][e] = 0.f;
         if constexpr (BACK) row_product<false, NT / 2>(Z, S, mul, K, 0, n0, lane);
         else row_product<false, NT / 2>(Z, S, mul, W, 0, n0, lane);
-        const float zf = BACK ? 1.f : tail.w_scale, f[2] = {rs[0].back * zf, rs[1].back * zf};
+        const float f[2] = {rs[0].back, rs[1].back};
 #pragma unroll
         for (int j = 0; j < ZT; ++j) {
 #pragma unroll
@@ -973,23 +1030,22 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
             mine[j * 32] = make_float4(Z[j][0], Z[j][1], Z[j][2], Z[j][3]);
         }
         asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
-        uint32_t u_top = 0;
 #pragma unroll
         for (int j = 0; j < ZT; ++j) {
             const float4 o = other[j * 32];
             const float2 c = *reinterpret_cast<const float2*>(tail.c + 8 * j + c2);
+            const float2 wf = *reinterpret_cast<const float2*>(tail.w + 8 * j + c2);
             const float y[4] = {o.x, o.y, o.z, o.w};
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float cj = e & 1 ? c.y : c.x;
+                const float cj = e & 1 ? c.y : c.x, wj = e & 1 ? wf.y : wf.x;
                 if constexpr (BACK) {
                     v[e] = (Z[j][e] + y[e]) * cj;
-                    Z[j][e] = -v[e];
+                    Z[j][e] = -v[e] * wj;
                 } else {
-                    v[e] = x[j][e] - (Z[j][e] + y[e]);
+                    v[e] = fmaf(Z[j][e] + y[e], -wj, x[j][e]);
                     Z[j][e] = v[e] * cj;
-                    u_top = max(u_top, planes::abs_bits(v[e]));
                 }
             }
             if ((j < ZT / 2) == (half == 0)) {
@@ -998,11 +1054,7 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
                     *reinterpret_cast<float2*>(side + hh * 8 * kC + 8 * j) = make_float2(v[2 * hh], v[2 * hh + 1]);
             }
         }
-        if constexpr (!BACK) {
-            load_x(i + 1);
-            u_top = __reduce_max_sync(0xffffffffu, u_top);
-            if (lane == 0) w.meta[unit].u_max[block * 2 + half] = u_top;
-        }
+        if constexpr (!BACK) load_x(i + 1);
         float N[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1011,9 +1063,9 @@ __device__ __forceinline__ void scan(const ChunkBwdArgs& a, const Work& w, const
         float zb[2] = {0.f, 0.f};
         if (i < steps) {
             row_scales(Z, zs);
-            const float zmul[2] = {zs[0].mul, zs[1].mul}, nf = BACK ? tail.w_scale : 1.f;
-            zb[0] = zs[0].back * nf;
-            zb[1] = zs[1].back * nf;
+            const float zmul[2] = {zs[0].mul, zs[1].mul};
+            zb[0] = zs[0].back;
+            zb[1] = zs[1].back;
             if constexpr (BACK) row_product<true, ZT / 2>(N, Z, zmul, W, n0, 0, lane);
             else row_product<true, ZT / 2>(N, Z, zmul, K, n0, 0, lane);
         }
@@ -1081,9 +1133,10 @@ constexpr uint64_t kMmaWaitNs = 2000000000ull;
 // E, then P^T dY + E, then U^T, then the row sums.
 //
 // A token's results have to hold beside those of any other token of the chunk, whose dY may be larger by any
-// factor: what has a row a token gets a power of two a row.  dY_i, dR_i and (P^T dY + E)_i carry theirs where
-// they are right sides too: there the other side's column i is multiplied by it in fp32, before its own rows
-// are scaled and split (tri_planes; dP^T Q and Z^T K have their scales by columns for the same reason).
+// factor, and so may v (and U): what has a row a token gets a power of two a row.  dY_i, dR_i and
+// (P^T dY + E)_i carry theirs where they are right sides too: there the other side's column i is multiplied by
+// it in fp32, before its own rows are scaled and split (tri_planes; dP^T Q and Z^T K have their scales by
+// columns for the same reason).
 template <int D, int P>
 struct GradSmem {
     // d = 64: two blocks share an SM, which takes Q out; d = 128 in fp32 needs the room as well
@@ -1093,8 +1146,8 @@ struct GradSmem {
     static constexpr int H2 = D / 64, half = kC * 128, plane = half * H2, yr = 2 * plane, st = D * 128 * H2;
     static constexpr int K = 0, Q = P * plane, YR = share ? Q : 2 * P * plane;
     static constexpr int ST = YR + 2 * yr, SQ = ST + 2 * st, B1 = SQ + 4 * half, bytes = B1 + 2 * plane;
-    // at TMP: maxima of dR's rows [4][64], dR's scales [64], maxima of dP's and Z's rows [column group][128] and
-    // columns [4][64]
+    // at TMP: maxima of dR's rows [4][64], scales of dR and of U [2][64], maxima of dP's and Z's rows [column
+    // group][128] and columns [4][64]
     static constexpr int TMP = 2 * half, tRows = TMP, tScale = TMP + 1024, tPZ = TMP + 2048, tCols = TMP + 4096;
     static constexpr int WM = D / 32, threads = WM * 128;
     // TMEM columns: D1, D2, D3, then NZ and HH in turn
@@ -1115,6 +1168,12 @@ struct Flat {
     }
     template <bool DOT, int LO, int HS>
     __device__ __forceinline__ float put(Mat<COLS, 2, LO, HS> dst, float mul) const {
+        const float by[4] = {mul, mul, mul, mul};
+        return put<DOT>(dst, by);
+    }
+    template <bool DOT, int LO, int HS>  // a scale for each of this thread's four columns (the same in every row)
+    __device__ __forceinline__ float put(Mat<COLS, 2, LO, HS> dst, const float (&mul)[4]) const {
+        static_assert(T * 4 % COLS == 0, "");
         float dot = 0.f;
 #pragma unroll
         for (int p = 0; p < N; ++p) {
@@ -1132,8 +1191,8 @@ struct Flat {
                 }
             }
             uint32_t hi[2], lo[2];
-            planes::split(x[p][0] * mul, x[p][1] * mul, hi[0], lo[0]);
-            planes::split(x[p][2] * mul, x[p][3] * mul, hi[1], lo[1]);
+            planes::split(x[p][0] * mul[0], x[p][1] * mul[1], hi[0], lo[0]);
+            planes::split(x[p][2] * mul[2], x[p][3] * mul[3], hi[1], lo[1]);
             planes::sts64(at, hi[0], hi[1]);
             planes::sts64(at + LO, lo[0], lo[1]);
         }
@@ -1252,27 +1311,6 @@ __device__ __forceinline__ void tri_planes(Mat<kC, 2, LO, 0> dst, const float* x
     if (c == 0) back[r] = s.back;
 }
 
-// The largest magnitudes of a warp's part of its rows into tops[column of warps][row].
-template <int MT, int NT>
-__device__ __forceinline__ void row_tops(uint32_t* tops, const float (&acc)[MT][NT][4], const int (&m)[MT], int nw, int lane) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) top = max(top, planes::abs_bits(acc[i][j][2 * h + e]));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if ((lane & 3) == 0) tops[nw * kC + m[i] + (lane >> 2) + 8 * h] = top;
-        }
-}
-__device__ __forceinline__ Scale row_scale(const uint32_t* tops, int r) {
-    return planes::scale_of(max(max(tops[r], tops[kC + r]), max(tops[2 * kC + r], tops[3 * kC + r])));
-}
-
 template <int D, int P>
 __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2 : 1)
     chunk_bwd_grad_kernel(ChunkBwdArgs a, Work w) {
@@ -1282,6 +1320,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     __shared__ Gates t;
     __shared__ __align__(16) float fY[kC];
     __shared__ float fK[kC], fQ[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
+    uint32_t* u_tops = reinterpret_cast<uint32_t*>(diag);  // of U's tokens, before diag is written
     __shared__ uint32_t tops[2], tmem_at;
     __shared__ float dots[NW];
     __shared__ uint64_t bars[5];  // of the MMAs; of the copies of T, P and E; of S0's
@@ -1350,7 +1389,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     };
     Flat<T, D, D> state;
     Flat<T, D, kC> u;
-    Scale ss, sds, su;
+    Scale ss, sds;
     if (!a.use_l2) {
         if (tid < 2) tops[tid] = 0;
         __syncthreads();
@@ -1366,9 +1405,9 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             ptx::tmem_alloc(&tmem_at, L::tmem);
             ptx::tmem_relinquish();
         }
-        if (tid < kC) diag[tid] = meta.p_diag[tid];
+        if (tid < kC) u_tops[tid] = 0;
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
-        const uint32_t top[3] = {meta.s_max[part], meta.ds_max[part], meta.u_max[part]};
+        const uint32_t top[2] = {meta.s_max[part], meta.ds_max[part]};
         if (warp == NW - 1) gates.put(t, lane);
         k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
         q.template put<true, !L::share>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
@@ -1382,7 +1421,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         }
         ss = planes::scale_of(__reduce_max_sync(0xffffffffu, top[0]));
         sds = planes::scale_of(__reduce_max_sync(0xffffffffu, top[1]));
-        su = planes::scale_of(__reduce_max_sync(0xffffffffu, top[2]));
     }
     Pair<P> v[MT][NT][2];
     planes::pairs<MT, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int c) {
@@ -1445,7 +1483,8 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     }
     __syncthreads();
     float vdot[MT][2] = {};
-    float* fR = reinterpret_cast<float*>(sm + L::SQ + L::tScale);  // takes a row of R to dR
+    float* fR = reinterpret_cast<float*>(sm + L::SQ + L::tScale);  // takes a row of R to dR,
+    float* fU = fR + kC;                                           // a column of U^T's planes to U^T
     {
         uint32_t* dr_tops = reinterpret_cast<uint32_t*>(sm + L::SQ + L::tRows);
         u.fetch(w.U + unit * kC * D);
@@ -1461,6 +1500,14 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
             if (r < len) store2(a.dv, a.qkv_dtype, ((t0 + r) * a.H + h) * D + c, t.beta[r] * x, t.beta[r] * y);
         });
         row_tops(dr_tops, dR, m, nw, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // a thread's four tokens of U; lanes 16 apart have the same
+            uint32_t top = 0;
+#pragma unroll
+            for (int p = 0; p < u.N; ++p) top = max(top, planes::abs_bits(u.x[p][e]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (lane < 16) atomicMax(&u_tops[4 * lane + e], top);
+        }
         __syncthreads();  // also: B1, P^T and T^T have been read
         float mul[MT][2];
 #pragma unroll
@@ -1473,7 +1520,14 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
                 if (nw == 0 && (lane & 3) == 0) fR[r] = sr.back;
             }
         planes::write(R, dR, m, nd, lane, mul);
-        u.template put<false>(UT, su.mul);
+        float mul_u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const Scale su = planes::scale_of(u_tops[4 * (lane & 15) + e]);
+            mul_u[e] = su.mul;
+            if (tid < 16) fU[4 * lane + e] = su.back;
+        }
+        u.template put<false>(UT, mul_u);
     }
     // D1 and NZ
     ptx::fence_async_smem();
@@ -1494,6 +1548,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     state.fetch(dS1);
     // This thread's token, which half of the lanes, and its columns of a 64-wide and of a d-wide result
     const int part = (warp & 3) >> 1, row = (warp & 1) * 32 + lane, cg = warp >> 2;
+    const float p_diag = meta.p_diag[row];
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     constexpr int NC = kC / CG;
     float x[NC];
@@ -1504,15 +1559,15 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         else ptx::tmem_ld32(lanes + L::tNZ + cg * NC, raw);
         ptx::tmem_wait_ld();
         const float2 gr = t.G[row];
-        const float f = (part ? -fR[row] : fY[row]) * su.back, f2 = part ? t.beta[row] * fK[row] : fQ[row];
+        const float f = part ? -fR[row] : fY[row], f2 = part ? t.beta[row] * fK[row] : fQ[row];
         uint32_t top = 0, mine = 0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = cg * NC + i;
-            const float y = __uint_as_float(raw[i]) * f * decay(gr, t.G[c]);
+            const float y = __uint_as_float(raw[i]) * f * (decay(gr, t.G[c]) * fU[c]);
             if (c == row && part == 0) {
                 dpp[row] = y;
-                diag[row] *= y;  // dP_ii q_i . k_i
+                diag[row] = p_diag * y;  // dP_ii q_i . k_i
             }
             x[i] = c < row ? y : 0.f;
             top = max(top, planes::abs_bits(x[i] * fK[c]));
@@ -1525,6 +1580,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     wait(1, 0);  // S0's planes, dY and dR have been read
     const float state_dot = warp_sum(state.template put<true>(ST, sds.mul));  // and <S0, dS1>
     const float f1 = (part ? -t.b[row] * fR[row] : t.b[row] * fY[row]) * ss.back;
+    const float fh = decay(t.G[kC - 1], t.G[row]) * fU[row] * sds.back;
     if (lane == 0) dots[warp] = state_dot;
     ptx::tc_fence_before();
     __syncthreads();
@@ -1599,7 +1655,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     float y[32], z[32];
     float dot0 = 0.f, dot1 = 0.f, dot2 = 0.f;  // dQ . q or F . k; H . k; (dK- - H) . k
     {
-        const float fh = decay(t.G[kC - 1], t.G[row]) * su.back * sds.back;
         const float fd = __uint_as_float((254u << 23) - __float_as_uint(fC[row]));  // 1 / fC, a power of two
         uint32_t r1[32], r2[32];
         ptx::tmem_ld32(lanes + L::tD1 + c0, r1);

@@ -147,8 +147,9 @@ size_t gdn_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int d_k, i
  * No other output may overlap an input.  Rows of tokens behind the last sequence of cu_seqlens are
  * left as they were.  A malformed cu_seqlens is recorded as GDN_ERR_CU_SEQLENS in the device error
  * word, and the call then writes nothing.
- * Arithmetic is that of fp32 for both element types, with one rounding at each output; the same
- * call gives the same bits.
+ * Arithmetic is that of fp32 for both element types, with one rounding at each output, but that the
+ * operands of products hold 22 bits.  A token's gradients keep that accuracy beside tokens of the
+ * same chunk whose dout or v is larger by any factor.  The same call gives the same bits.
  */
 int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                   const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k,

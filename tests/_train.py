@@ -86,11 +86,14 @@ EPS = 2.0 ** -23
 
 
 def delta_errors(inp, scale=None, use_l2=True):
-    """Standard deviations, in units of EPS, of the gradients of delta_grads token by token when every operand and
-    every term of the chunk form is rounded once to within EPS (decays to 2 EPS): first-order propagation of variances in fp64
-    (M below is a matrix's values, its variance var_M; a product's is var_A B^2 + A^2 var_B + 2 A^2 B^2).  dq, dk
-    [T, Hk] and dv [T, H] (a vector's 2-norm), dg and dbeta [T, H].  A token's gradient may be far smaller than
-    the terms that it is the sum of, and its error goes by them."""
+    """Standard deviations, in units of EPS, of the gradients of delta_grads token by token, from the chunk form
+    with its roundings: first-order propagation of variances in fp64.  dq, dk [T, Hk] and dv [T, H] (a vector's
+    2-norm), dg and dbeta [T, H].  A token's gradient may be far smaller than the terms that it is the sum of, and
+    its error goes by them.  What is rounded:
+      a product's operands, to EPS of each element;
+      its accumulator, cut off at each of 3 inner / 16 steps (the terms hi hi, hi lo, lo hi of 16 products), by
+      half an EPS on average of a partial sum that grows to the product: together 3 inner / 64 of it;
+      a decay e^-x, by 2 EPS in the exponential and by x / 2 EPS in its argument (x 2^-24)."""
     (T, Hk, d), H, cu = inp["q"].shape, inp["v"].shape[1], inp["cu"]
     scale = d ** -0.5 if scale is None else scale
     q, k, v, g, beta, dy = (inp[x].to(F64) for x in ("q", "k", "v", "g", "beta", "dout"))
@@ -101,12 +104,14 @@ def delta_errors(inp, scale=None, use_l2=True):
 
     def mul(A, B):  # (values, variances) of a product of two such pairs
         (a, va), (b, vb) = A, B
-        return a @ b, va @ b ** 2 + a ** 2 @ vb + 2 * a ** 2 @ b ** 2
+        c = a @ b
+        return c, va @ b ** 2 + a ** 2 @ vb + 2 * a ** 2 @ b ** 2 + (3 * a.shape[1] / 64 * c) ** 2
 
     exact = lambda x: (x, torch.zeros_like(x))  # noqa: E731
     add = lambda A, B, s=1.0: (A[0] + s * B[0], A[1] + B[1])  # noqa: E731
     by = lambda f, A: (f * A[0], f ** 2 * A[1])  # noqa: E731
-    fade = lambda f, A: (f * A[0], f ** 2 * (A[1] + 4 * A[0] ** 2))  # noqa: E731  by a decay, 2 EPS off
+    # by a decay
+    fade = lambda f, A, x: (f * A[0], f ** 2 * (A[1] + (4 + x ** 2 / 4) * A[0] ** 2))  # noqa: E731
     t = lambda A: (A[0].T, A[1].T)  # noqa: E731
     dot = lambda A, B: (A[0] * B[0], A[1] * B[0] ** 2 + A[0] ** 2 * (B[1] + 2 * B[0] ** 2))  # noqa: E731
     for n in range(len(cu) - 1):
@@ -117,21 +122,22 @@ def delta_errors(inp, scale=None, use_l2=True):
                 i = slice(c, min(c + 64, cu[n + 1]))
                 K, Q, V, Y, be, G = exact(k[i, h]), exact(q[i, h]), exact(v[i, h]), exact(dy[i, h]), beta[i, h], g[i, h]
                 G = G.clamp(min=-128).cumsum(0)
-                D, b, tail = torch.exp(G[:, None] - G[None]).tril(), G.exp()[:, None], torch.exp(G[-1] - G)[:, None]
-                A = fade((be[:, None] * D).tril(-1), mul(K, t(K)))
+                far, x, to_end = G[:, None] - G[None], G[:, None], (G[-1] - G)[:, None]
+                D, b, tail = far.exp().tril(), x.exp(), to_end.exp()
+                A = fade((be[:, None] * D).tril(-1), mul(K, t(K)), far)
                 X = torch.linalg.solve_triangular(torch.eye(len(be), dtype=F64) + A[0], torch.eye(len(be), dtype=F64), upper=False)
                 X = X, X ** 2 @ (A[1] + A[0] ** 2) @ X ** 2 + X ** 2
-                W, Pm = mul(X, fade(be[:, None] * b, K)), fade(D, mul(Q, t(K)))
+                W, Pm = mul(X, fade(be[:, None] * b, K, x)), fade(D, mul(Q, t(K)), far)
                 U = add(mul(X, by(be[:, None], V)), mul(W, t(S)), -1.0)
-                chunks.append((i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S))
-                S = add(fade(b[-1], S), mul(t(fade(tail, U)), K))
+                chunks.append((i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S, far, x, to_end))
+                S = add(fade(b[-1], S, x[-1]), mul(t(fade(tail, U, to_end)), K))
             dS = exact(torch.zeros(d, d, dtype=F64) if inp["dfinal_state"] is None else inp["dfinal_state"][n, h].to(F64))
-            for i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S in reversed(chunks):
-                E = fade(tail, mul(K, t(dS)))
+            for i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S, far, x, to_end in reversed(chunks):
+                E = fade(tail, mul(K, t(dS)), to_end)
                 dR = mul(t(X), add(mul(t(Pm), Y), E))
-                dP, Z = fade(D, mul(Y, t(U))), fade(-D.tril(-1), mul(dR, t(U)))
-                dQ, F = add(fade(b, mul(Y, S)), mul(dP, K)), add(mul(Z, K), fade(b, mul(dR, S)), -1.0)
-                Hd, rest = fade(tail, mul(U, dS)), add(mul(t(dP), Q), mul(t(Z), by(be[:, None], K)))
+                dP, Z = fade(D, mul(Y, t(U)), far), fade(-D.tril(-1), mul(dR, t(U)), far)
+                dQ, F = add(fade(b, mul(Y, S), x), mul(dP, K)), add(mul(Z, K), fade(b, mul(dR, S), x), -1.0)
+                Hd, rest = fade(tail, mul(U, dS), to_end), add(mul(t(dP), Q), mul(t(Z), by(be[:, None], K)))
                 dK = add(by(be[:, None], F), add(Hd, rest))
                 later = add(add(dot(dQ, Q), dot(by(be[:, None], F), K)), dot(rest, K))[1].sum(-1)
                 out["dq"][i, h] = (scale * rq[i, h]) ** 2 * dQ[1].sum(-1)
@@ -140,7 +146,7 @@ def delta_errors(inp, scale=None, use_l2=True):
                 out["dbeta"][i, h] = (dot(dR, V)[1] + dot(F, K)[1]).sum(-1)
                 hk = dot(Hd, K)[1].sum(-1)
                 out["dg"][i, h] = later.flip(0).cumsum(0).flip(0) + hk.cumsum(0) - hk + b[-1] ** 2 * dot(S, dS)[1].sum()
-                dS = add(add(fade(b[-1], dS), mul(t(Y), add(fade(b, Q), mul(Pm, W), -1.0))), mul(t(E), W), -1.0)
+                dS = add(add(fade(b[-1], dS, x[-1]), mul(t(Y), add(fade(b, Q, x), mul(Pm, W), -1.0))), mul(t(E), W), -1.0)
     for x in ("dq", "dk"):
         out[x] = out[x].reshape(T, Hk, H // Hk).sum(-1)
     return {x: y.sqrt() for x, y in out.items()}

@@ -109,6 +109,20 @@ def test_chunk_bwd_tokens_whose_gradients_are_far_apart(d, dtype, a_mean, patter
     check_tokens(inp, chunk_bwd(inp))
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F32), (64, BF16), (128, F32), (128, BF16)])
+@pytest.mark.parametrize("a_mean", [-4.0, 1.0])
+@pytest.mark.parametrize("pattern", ["rising", "mixed"])
+def test_chunk_bwd_tokens_whose_values_are_far_apart(d, dtype, a_mean, pattern):
+    """v 2^30 apart: a token's results depend on its own and earlier tokens' v and keep their accuracy beside
+    later ones."""
+    lengths = [64, 100]
+    inp = delta_inputs(lengths, 4, 2, d, dtype, seed=63, a_mean=a_mean)
+    e = _exponents(pattern, lengths)
+    inp["v"] = (inp["v"].double() * 2.0 ** e[:, None, None]).to(dtype)
+    inp["initial_state"] *= 2.0 ** -15
+    check_tokens(inp, chunk_bwd(inp))
+
+
 def test_chunk_bwd_first_token_has_no_decay_gradient():
     inp = delta_inputs([1, 1], 2, 2, 128, BF16, seed=3, carried=False)
     assert torch.count_nonzero(chunk_bwd(inp)["dg"]) == 0
