@@ -350,16 +350,13 @@ struct Rows {
         return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
 
-    // As planes, each row with a power of two of its own (one plane holds bf16 exactly).  factor[r] takes
-    // row r of the planes to x (NORM false), or to scale * x / |x| (NORM, use_l2) and scale * x (NORM, not
-    // use_l2); inv[r], if given, receives 1 / |x| (1 without).  Factors that a later product folds into
-    // the other operand of a contraction must not differ much between rows: with use_l2 the norm sets
-    // their size; without it all rows share the largest row's power of two (the block then synchronises
-    // on *shared_top, which must be zero).
+    // As planes, each row with a power of two of its own (one plane holds bf16 exactly, down to 2^-26 of the
+    // row's largest).  factor[r] takes row r of the planes to x (NORM false), or to scale * x / |x| (NORM,
+    // use_l2) and scale * x (NORM, not use_l2); inv[r], if given, receives 1 / |x| (1 without).
     // STORE false: the factors only.
     template <bool NORM, bool STORE = true, int LO, int HS>
     __device__ __forceinline__ void put(Mat<D, P, LO, HS> dst, float* factor, float* inv, bool use_l2, float scale,
-                                        uint32_t* shared_top, int warp, int lane) const {
+                                        int warp, int lane) const {
         const int r = row(warp, lane);
         float ss = 0.f;
         uint32_t top = 0;
@@ -393,11 +390,6 @@ struct Rows {
         for (int o = LPR / 2; o > 0; o >>= 1) {
             top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             if constexpr (NORM) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        }
-        if (NORM && !use_l2) {
-            atomicMax(shared_top, top);
-            __syncthreads();
-            top = *shared_top;
         }
         const Scale s = planes::scale_of(top);
 #pragma unroll
@@ -626,7 +618,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     __shared__ Gates t;
     __shared__ float fK[kC], fQ[kC], fY[kC], fV[kC];
     __shared__ float back_u[kC], back_w[kC];
-    __shared__ uint32_t red[2][NW], tops[2], w_tops[4 * kC];
+    __shared__ uint32_t red[2][NW], w_tops[4 * kC];
     const int ahead = blockIdx.x + 2 * kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
     const int slots[2] = {w.heads(blockIdx.x), next < 0 ? -1 : w.heads(next)};
     const long slot = slots[0];
@@ -644,10 +636,6 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
     unsigned char* link = w.link + unit * link_bytes(D, P);
     LinkTail& tail = *reinterpret_cast<LinkTail*>(link + (2 + P) * PL);
 
-    if (!a.use_l2) {
-        if (tid < 2) tops[tid] = 0;
-        __syncthreads();
-    }
     {
         GateRows gates;
         if (warp == NW - 1) gates.fetch(a, t0, len, h, lane);
@@ -656,9 +644,9 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
         v.fetch(a.v, a.qkv_dtype, t0, len, a.H, h, warp, lane);
         if (warp == NW - 1) gates.put(t, lane);
-        k.template put<true>(K, fK, nullptr, a.use_l2, 1.f, &tops[0], warp, lane);
-        q.template put<true>(Q, fQ, nullptr, a.use_l2, a.scale, &tops[1], warp, lane);
-        v.template put<false>(V, fV, nullptr, false, 1.f, nullptr, warp, lane);
+        k.template put<true>(K, fK, nullptr, a.use_l2, 1.f, warp, lane);
+        q.template put<true>(Q, fQ, nullptr, a.use_l2, a.scale, warp, lane);
+        v.template put<false>(V, fV, nullptr, false, 1.f, warp, lane);
     }
     __syncthreads();
 
@@ -821,7 +809,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
         tail.b_last = t.b[kC - 1];
     }
     __syncthreads();  // W, V and Q have been read
-    y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
+    y.template put<false>(Y, fY, nullptr, false, 1.f, warp, lane);
     __syncthreads();
     planes::pairs<2, NT>(m, nd, lane, [&](int i, int j, int hh, int r, int) {
         acc[i][j][2 * hh] *= fY[r];
@@ -1321,7 +1309,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     __shared__ __align__(16) float fY[kC];
     __shared__ float fK[kC], fQ[kC], kinv[kC], qinv[kC], dpp[kC], diag[kC];
     uint32_t* u_tops = reinterpret_cast<uint32_t*>(diag);  // of U's tokens, before diag is written
-    __shared__ uint32_t tops[2], tmem_at;
+    __shared__ uint32_t tmem_at;
     __shared__ float dots[NW];
     __shared__ uint64_t bars[5];  // of the MMAs; of the copies of T, P and E; of S0's
     const int ahead = blockIdx.x + kSMs, next = ahead < (int)gridDim.x ? ahead : -1;
@@ -1390,10 +1378,6 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     Flat<T, D, D> state;
     Flat<T, D, kC> u;
     Scale ss, sds;
-    if (!a.use_l2) {
-        if (tid < 2) tops[tid] = 0;
-        __syncthreads();
-    }
     {
         GateRows gates;
         if (warp == NW - 1) gates.fetch(a, t0, len, h, lane);
@@ -1409,9 +1393,9 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
         const int part = lane & (D / 8 - 1);  // one of the scan's warps
         const uint32_t top[2] = {meta.s_max[part], meta.ds_max[part]};
         if (warp == NW - 1) gates.put(t, lane);
-        k.template put<true>(K, fK, kinv, a.use_l2, 1.f, &tops[0], warp, lane);
-        q.template put<true, !L::share>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
-        y.template put<false>(Y, fY, nullptr, false, 1.f, nullptr, warp, lane);
+        k.template put<true>(K, fK, kinv, a.use_l2, 1.f, warp, lane);
+        q.template put<true, !L::share>(Q, fQ, qinv, a.use_l2, a.scale, warp, lane);
+        y.template put<false>(Y, fY, nullptr, false, 1.f, warp, lane);
         if constexpr (P == 1) {  // dY's lo plane is zero (below dR's, rows of 8 KB)
 #pragma unroll
             for (int i = 0; i < PL / 16 / T; ++i) {
@@ -1599,7 +1583,7 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     if constexpr (L::share) {
         Rows<NW, D, P> q;
         q.fetch(a.q, a.qkv_dtype, t0, len, a.Hk, hk, warp, lane);
-        q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, &tops[1], warp, lane);
+        q.template put<true>(Q, fQ, qinv, a.use_l2, a.scale, warp, lane);
     }
     __syncthreads();
     auto put_row = [&](auto dst, auto&& value) {

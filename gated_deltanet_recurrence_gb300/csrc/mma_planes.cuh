@@ -4,7 +4,8 @@
 //   x = s * (hi + lo),  hi = fp16(x / s),  lo = fp16(x / s - hi).
 // s puts the largest magnitude of the scaled set (a tile, or a row) into [2^9, 2^10), so hi + lo holds
 // 22 bits of every element down to 2^-13 of that maximum and an absolute 2^-35 of it below: the step of
-// fp32 where it matters.  A bf16 matrix (8 bits) is exact in the hi plane alone.  A product takes the
+// fp32 where it matters.  A bf16 set (8 bits) is exact in the hi plane alone down to 2^-26 of its maximum, with
+// an absolute 2^-34 of it below.  Maxima below 2^-100 count as 2^-100.  A product takes the
 // terms hi hi, hi lo and lo hi (lo lo is below 2^-22 of the result), each an m16n8k16 fp16 tensor-core
 // instruction with fp32 accumulation: three for two split matrices, two where one is exact.  bf16 planes
 // would need three each (six terms) for the same accuracy, tf32 planes run at half the rate (measured

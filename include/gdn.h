@@ -149,7 +149,8 @@ size_t gdn_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int d_k, i
  * word, and the call then writes nothing.
  * Arithmetic is that of fp32 for both element types, with one rounding at each output, but that the
  * operands of products hold 22 bits.  A token's gradients keep that accuracy beside tokens of the
- * same chunk whose dout or v is larger by any factor.  The same call gives the same bits.
+ * same chunk whose dout, v or (without normalisation) q or k is larger by any factor; rows of
+ * magnitudes below 2^-100 lose bits.  The same call gives the same bits.
  */
 int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                   const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k,

@@ -85,71 +85,84 @@ def delta_grads(inp, scale=None, use_l2=True):
 EPS = 2.0 ** -23
 
 
-def delta_errors(inp, scale=None, use_l2=True):
-    """Standard deviations, in units of EPS, of the gradients of delta_grads token by token, from the chunk form
-    with its roundings: first-order propagation of variances in fp64.  dq, dk [T, Hk] and dv [T, H] (a vector's
-    2-norm), dg and dbeta [T, H].  A token's gradient may be far smaller than the terms that it is the sum of, and
-    its error goes by them.  What is rounded:
-      a product's operands, to EPS of each element;
-      its accumulator, cut off at each of 3 inner / 16 steps (the terms hi hi, hi lo, lo hi of 16 products), by
-      half an EPS on average of a partial sum that grows to the product: together 3 inner / 64 of it;
-      a decay e^-x, by 2 EPS in the exponential and by x / 2 EPS in its argument (x 2^-24)."""
+def _delta_chunks(q, k, v, g, beta, dy, S, dS, scale, rounded):
+    """Gradients of one sequence in the chunk form, in fp64 and by heads: q (scaled), k [H, T, d] and v, dy
+    alike, g, beta [H, T], S, dS [H, d, d].  Returns those of q, k (as they are here), v, g and beta; rounded(x, s)
+    is x with a relative error of s EPS."""
+    C, T = 64, q.shape[1]
+
+    def mul(A, B):
+        # the operands' roundings, and the accumulator's: it is cut off at each of 3 inner / 16 steps (the terms
+        # hi hi, hi lo and lo hi of 16 products), by half an EPS on average of a partial sum that grows to the
+        # product, together 3 inner / 64 of it
+        return rounded(rounded(A, 1.0) @ rounded(B, 1.0), 3 * A.shape[-1] / 64)
+
+    def fade(x, far, low=None):
+        # by e^far: 2 EPS in the exponential, |far| / 2 EPS in its argument (|far| 2^-24)
+        f = far.exp() if low is None else far.masked_fill(~low, 0.0).exp() * low
+        return x * rounded(f, torch.sqrt(4 + far ** 2 / 4))
+
+    def dot(A, B):
+        return rounded(A * B, 1.0).sum(-1)
+
+    chunks, res = [], [torch.zeros_like(x) for x in (q, k, v, g, beta)]
+    for c in range(0, T, C):
+        i = slice(c, min(c + C, T))
+        K, Q, V, Y, be, G = k[:, i], q[:, i], v[:, i], dy[:, i], beta[:, i, None], g[:, i].clamp(min=-128).cumsum(1)
+        n = G.shape[1]
+        low = torch.ones(n, n, dtype=torch.bool, device=q.device).tril()
+        far, to_end, G = G[:, :, None] - G[:, None], (G[:, -1:] - G)[..., None], G[..., None]
+        A = be * fade(mul(K, K.mT), far, low.tril(-1))
+        eye = torch.eye(n, dtype=F64, device=q.device).expand_as(A)
+        X = rounded(torch.linalg.solve_triangular(eye + rounded(A, 1.0), eye, upper=False), 1.0)
+        W, P = mul(X, be * fade(K, G)), fade(mul(Q, K.mT), far, low)
+        U = mul(X, be * V) - mul(W, S.mT)
+        chunks.append((i, K, Q, V, Y, be, G, far, to_end, low, X, W, P, U, S))
+        S = fade(S, G[:, -1:]) + mul(fade(U, to_end).mT, K)
+    for i, K, Q, V, Y, be, G, far, to_end, low, X, W, P, U, S in reversed(chunks):
+        E = fade(mul(K, dS.mT), to_end)
+        dR = mul(X.mT, mul(P.mT, Y) + E)
+        dP, Z = fade(mul(Y, U.mT), far, low), -fade(mul(dR, U.mT), far, low.tril(-1))
+        dQ, F = fade(mul(Y, S), G) + mul(dP, K), mul(Z, K) - fade(mul(dR, S), G)
+        Hd, rest = fade(mul(U, dS), to_end), mul(dP.mT, Q) + mul(Z.mT, be * K)
+        later, hk = dot(dQ, Q) + be[..., 0] * dot(F, K) - dot(rest, K), dot(Hd, K)
+        carried = fade(dot(S, dS).sum(-1)[:, None], G[:, -1])
+        dg = later.flip(1).cumsum(1).flip(1) + hk.cumsum(1) - hk + carried
+        for x, y in zip(res, (dQ, be * F + Hd + rest, be * dR, dg, dot(dR, V) + dot(F, K))):
+            x[:, i] = y
+        dS = fade(dS, G[:, -1:]) + mul(Y.mT, fade(Q, G) - mul(P, W)) - mul(E.mT, W)
+    return res
+
+
+def delta_errors(inp, scale=None, use_l2=True, samples=32, device="cpu"):
+    """Standard deviations of the errors of delta_grads' gradients token by token when the chunk form is rounded as
+    _delta_chunks says, from random roundings of that size (in fp64; cancellations and errors that many terms
+    share are then counted as they are): dq, dk [T, Hk] and dv [T, H] (a vector's 2-norm), dg and dbeta [T, H]."""
     (T, Hk, d), H, cu = inp["q"].shape, inp["v"].shape[1], inp["cu"]
     scale = d ** -0.5 if scale is None else scale
-    q, k, v, g, beta, dy = (inp[x].to(F64) for x in ("q", "k", "v", "g", "beta", "dout"))
+    q, k, v, g, beta, dy = (inp[x].to(device, F64) for x in ("q", "k", "v", "g", "beta", "dout"))
     rep = lambda x: x.repeat_interleave(H // Hk, 1)  # noqa: E731
-    rq, rk = (rep(torch.rsqrt((x * x).sum(-1) + 1e-6) if use_l2 else torch.ones(T, Hk, dtype=F64)) for x in (q, k))
-    q, k = rep(q) * rq[..., None] * scale, rep(k) * rk[..., None]
-    out = {x: torch.zeros(T, H, dtype=F64) for x in ("dq", "dk", "dv", "dg", "dbeta")}
-
-    def mul(A, B):  # (values, variances) of a product of two such pairs
-        (a, va), (b, vb) = A, B
-        c = a @ b
-        return c, va @ b ** 2 + a ** 2 @ vb + 2 * a ** 2 @ b ** 2 + (3 * a.shape[1] / 64 * c) ** 2
-
-    exact = lambda x: (x, torch.zeros_like(x))  # noqa: E731
-    add = lambda A, B, s=1.0: (A[0] + s * B[0], A[1] + B[1])  # noqa: E731
-    by = lambda f, A: (f * A[0], f ** 2 * A[1])  # noqa: E731
-    # by a decay
-    fade = lambda f, A, x: (f * A[0], f ** 2 * (A[1] + (4 + x ** 2 / 4) * A[0] ** 2))  # noqa: E731
-    t = lambda A: (A[0].T, A[1].T)  # noqa: E731
-    dot = lambda A, B: (A[0] * B[0], A[1] * B[0] ** 2 + A[0] ** 2 * (B[1] + 2 * B[0] ** 2))  # noqa: E731
+    rq, rk = (torch.rsqrt((x * x).sum(-1, keepdim=True) + 1e-6) if use_l2 else torch.ones_like(x[..., :1]) for x in (q, k))
+    heads = [x.transpose(0, 1) for x in (rep(q * rq) * scale, rep(k * rk), v, g, beta, dy)]
+    gen = torch.Generator(device=device).manual_seed(0)
+    noisy = lambda x, s: x * (1 + s * EPS * torch.randn(x.shape, generator=gen, dtype=F64, device=device))  # noqa: E731
+    out = {x: torch.zeros(T, Hk if x in ("dq", "dk") else H, dtype=F64) for x in ("dq", "dk", "dv", "dg", "dbeta")}
     for n in range(len(cu) - 1):
-        for h in range(H):
-            S = exact(torch.zeros(d, d, dtype=F64) if inp["initial_state"] is None else inp["initial_state"][n, h].to(F64))
-            chunks = []
-            for c in range(cu[n], cu[n + 1], 64):
-                i = slice(c, min(c + 64, cu[n + 1]))
-                K, Q, V, Y, be, G = exact(k[i, h]), exact(q[i, h]), exact(v[i, h]), exact(dy[i, h]), beta[i, h], g[i, h]
-                G = G.clamp(min=-128).cumsum(0)
-                far, x, to_end = G[:, None] - G[None], G[:, None], (G[-1] - G)[:, None]
-                D, b, tail = far.exp().tril(), x.exp(), to_end.exp()
-                A = fade((be[:, None] * D).tril(-1), mul(K, t(K)), far)
-                X = torch.linalg.solve_triangular(torch.eye(len(be), dtype=F64) + A[0], torch.eye(len(be), dtype=F64), upper=False)
-                X = X, X ** 2 @ (A[1] + A[0] ** 2) @ X ** 2 + X ** 2
-                W, Pm = mul(X, fade(be[:, None] * b, K, x)), fade(D, mul(Q, t(K)), far)
-                U = add(mul(X, by(be[:, None], V)), mul(W, t(S)), -1.0)
-                chunks.append((i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S, far, x, to_end))
-                S = add(fade(b[-1], S, x[-1]), mul(t(fade(tail, U, to_end)), K))
-            dS = exact(torch.zeros(d, d, dtype=F64) if inp["dfinal_state"] is None else inp["dfinal_state"][n, h].to(F64))
-            for i, K, Q, V, Y, be, D, b, tail, X, W, Pm, U, S, far, x, to_end in reversed(chunks):
-                E = fade(tail, mul(K, t(dS)), to_end)
-                dR = mul(t(X), add(mul(t(Pm), Y), E))
-                dP, Z = fade(D, mul(Y, t(U)), far), fade(-D.tril(-1), mul(dR, t(U)), far)
-                dQ, F = add(fade(b, mul(Y, S), x), mul(dP, K)), add(mul(Z, K), fade(b, mul(dR, S), x), -1.0)
-                Hd, rest = fade(tail, mul(U, dS), to_end), add(mul(t(dP), Q), mul(t(Z), by(be[:, None], K)))
-                dK = add(by(be[:, None], F), add(Hd, rest))
-                later = add(add(dot(dQ, Q), dot(by(be[:, None], F), K)), dot(rest, K))[1].sum(-1)
-                out["dq"][i, h] = (scale * rq[i, h]) ** 2 * dQ[1].sum(-1)
-                out["dk"][i, h] = rk[i, h] ** 2 * dK[1].sum(-1)
-                out["dv"][i, h] = be ** 2 * dR[1].sum(-1)
-                out["dbeta"][i, h] = (dot(dR, V)[1] + dot(F, K)[1]).sum(-1)
-                hk = dot(Hd, K)[1].sum(-1)
-                out["dg"][i, h] = later.flip(0).cumsum(0).flip(0) + hk.cumsum(0) - hk + b[-1] ** 2 * dot(S, dS)[1].sum()
-                dS = add(add(fade(b[-1], dS, x[-1]), mul(t(Y), add(fade(b, Q, x), mul(Pm, W), -1.0))), mul(t(E), W), -1.0)
-    for x in ("dq", "dk"):
-        out[x] = out[x].reshape(T, Hk, H // Hk).sum(-1)
-    return {x: y.sqrt() for x, y in out.items()}
+        i = slice(cu[n], cu[n + 1])
+        states = [torch.zeros(H, d, d, dtype=F64, device=device) if inp[x] is None else inp[x][n].to(device, F64)
+                  for x in ("initial_state", "dfinal_state")]
+
+        def grads(count, rounded):  # [count, heads, tokens, ...]
+            many = [x.repeat(count, *[1] * (x.dim() - 1)) for x in [x[:, i] for x in heads] + states]
+            got = [x.reshape(count, H, *x.shape[1:]) for x in _delta_chunks(*many, scale, rounded)]
+            for x, r in ((0, scale * rq), (1, rk)):
+                got[x] = got[x].reshape(count, Hk, H // Hk, -1, d).sum(2) * r[i].transpose(0, 1)
+            return got
+
+        for x, many, one in zip(out, grads(samples, noisy), grads(1, lambda x, s: x)):
+            square = ((many - one) ** 2).mean(0)
+            out[x][i] = (square.sum(-1) if square.dim() == 3 else square).sqrt().transpose(0, 1).cpu()
+    return out
 
 
 def norm_forward(y, z, w, b, eps, rms):

@@ -82,7 +82,7 @@ def check_tokens(inp, got, **kw):
     deviations of what the roundings of their terms leave.  (Against the gradient itself no such bound holds, in
     fp32 neither: with a_mean = 1 and "mixed" below, token 147 of head 0 has dR = 0.0012 from terms of 0.12,
     0.054, 0.041, 0.024, ..., and half a step of 22 bits of the first alone is 0.12 * 2^-23 / 0.0012 = 1.2e-5.)"""
-    ref, size = delta_grads(inp, **kw), _train.delta_errors(inp, **kw)
+    ref, size = delta_grads(inp, **kw), _train.delta_errors(inp, device="cuda", **kw)
     lo, hi = inp["cu"][0], inp["cu"][-1]
     for name, sigma in size.items():
         x, r = (y.detach().cpu().double()[lo:hi] for y in (got[name], ref[name]))
@@ -91,7 +91,7 @@ def check_tokens(inp, got, **kw):
         off, most = (x - r).abs(), r.abs() * half
         if x.dim() == 3:
             off, most = off.norm(dim=-1), most.norm(dim=-1)
-        most = most + 10 * _train.EPS * sigma[lo:hi]
+        most = most + 10 * sigma[lo:hi]
         assert (off <= most).all(), (name, float((off / most).max()), int((off / most).argmax()))
 
 
@@ -107,6 +107,19 @@ def test_chunk_bwd_tokens_whose_gradients_are_far_apart(d, dtype, a_mean, patter
     e = _exponents(pattern, lengths)
     inp["dout"] = (inp["dout"].double() * 2.0 ** e[:, None, None]).to(dtype)
     check_tokens(inp, chunk_bwd(inp))
+
+
+@pytest.mark.parametrize("d,dtype", [(64, F32), (64, BF16), (128, F32), (128, BF16)])
+@pytest.mark.parametrize("a_mean", [-4.0, 1.0])
+@pytest.mark.parametrize("pattern", ["first", "falling", "mixed"])
+def test_chunk_bwd_queries_and_keys_far_apart_without_normalisation(d, dtype, a_mean, pattern):
+    """Rows of q and of k 2^30 apart where no norm takes their sizes off: small ones keep their accuracy."""
+    lengths = [64, 100]
+    inp = delta_inputs(lengths, 4, 2, d, dtype, seed=65, a_mean=a_mean)
+    e = _exponents(pattern, lengths)
+    for x, most in (("q", 0.0), ("k", float(e.max()))):  # keys of length one at most
+        inp[x] = (inp[x].double() * d ** -0.5 * 2.0 ** (e - most)[:, None, None]).to(dtype)
+    check_tokens(inp, chunk_bwd(inp, use_qk_l2norm=False, scale=0.5), use_l2=False, scale=0.5)
 
 
 @pytest.mark.parametrize("d,dtype", [(64, F32), (64, BF16), (128, F32), (128, BF16)])

@@ -175,6 +175,25 @@ def test_plain_delta_gradients_match_differences(use_l2):
         assert abs(num - ana) <= 1e-6 * max(1.0, abs(ana)), (x, num, ana)
 
 
+@pytest.mark.parametrize("use_l2", [True, False])
+def test_plain_chunk_form_gives_the_gradients_of_the_recurrence(use_l2):
+    """The form whose roundings give the token-wise tolerances; its normalised q's and k's gradients go through
+    the norm here."""
+    inp = _train.delta_inputs([150], 2, 2, 64, torch.float64, seed=5)
+    if not use_l2:
+        inp["q"], inp["k"] = inp["q"] / 8, inp["k"] / 8
+    ref = _train.delta_grads(inp, use_l2=use_l2, scale=0.3)
+    leaves = [inp[x].double().clone().requires_grad_() for x in ("q", "k")]
+    q, k = (x / torch.sqrt((x * x).sum(-1, keepdim=True) + 1e-6) if use_l2 else x for x in leaves)
+    v, g, beta, dy = (inp[x].double().transpose(0, 1) for x in ("v", "g", "beta", "dout"))
+    got = _train._delta_chunks((0.3 * q).detach().transpose(0, 1), k.detach().transpose(0, 1), v, g, beta, dy,
+                               inp["initial_state"][0].double(), inp["dfinal_state"][0].double(), 0.3, lambda x, s: x)
+    dq, dk, dv, dg, dbeta = (x.transpose(0, 1) for x in got)
+    dq, dk = torch.autograd.grad((0.3 * q, k), leaves, (dq, dk))
+    for name, x in zip(("dq", "dk", "dv", "dg", "dbeta"), (dq, dk, dv, dg, dbeta)):
+        assert _train.rel_l2(x, ref[name]) <= 1e-10, (name, _train.rel_l2(x, ref[name]))
+
+
 @pytest.mark.parametrize("rms,gated", [(True, True), (False, True), (False, False)])
 def test_plain_norm_gradients_match_differences(rms, gated):
     gen = torch.Generator().manual_seed(5)
