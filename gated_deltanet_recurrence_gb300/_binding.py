@@ -46,6 +46,7 @@ SIGNATURES = {
                                    _fp, _fp, _fp, _fp, _fp, _fp, _fp, _f, _vp, _i, _vp]),
     "gdn_chunk_bwd": (_i, [_vp, _vp, _vp, _fp, _fp, _ip, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _fp, _vp, _i,
                            _fp, _vp, _vp, _vp, _fp, _fp, _fp, _vp, _sz, _vp]),
+    "gdn_chunk_bwd_zero_outside": (_i, [_ip, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _fp, _fp, _vp]),
     "gdn_chunk_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "gdn_gate_rmsnorm_silu_bwd": (_i, [_vp, _i, _vp, _i, _fp, _fp, _f, _vp, _fp, _fp, _l, _i, _vp, _sz, _vp]),
     "gdn_gate_groupnorm_silu": (_i, [_vp, _i, _fp, _fp, _fp, _f, _vp, _i, _l, _i, _i, _vp]),
@@ -451,7 +452,8 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=
     cu_seqlens, num_seqs, scale, use_qk_l2norm and initial_state as given to it, dout [total_T, H, d_v]
     (fp32 or bf16) the gradient of out, dfinal_state [num_seqs, H, d_v, d_k] fp32 that of final_state
     (None: zeros).  Returns (dq, dk, dv, dg, dbeta, dinitial_state): dq, dk, dv in the inputs' dtype,
-    the others fp32; outputs are allocated unless given.  dinitial_state is None unless it is given,
+    the others fp32; outputs are allocated unless given.  Rows of tokens outside the sequences of cu_seqlens are
+    zeros in the outputs allocated here and left as they were in those given.  dinitial_state is None unless it is given,
     requested, or (output_dinitial_state=None) an initial_state is."""
     total_T, H_k, d_k = q.shape
     H, d_v = v.shape[1], v.shape[-1]
@@ -464,6 +466,7 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=
     dt = _dt(q)
     if _dt(k) != dt or _dt(v) != dt:
         raise TypeError("q, k, v must share one dtype")
+    own = [x is None for x in (dq, dk, dv, dg, dbeta)]
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -485,6 +488,10 @@ def gdn_chunk_bwd(q, k, v, g, beta, dout, cu_seqlens=None, num_seqs=None, scale=
                   _CHUNK_BWD_FP32)
     need = L.gdn_chunk_bwd_workspace_size(num_seqs, total_T, H, H_k, d_k, d_v)
     workspace, ws, ws_bytes = _workspace(workspace, need, q)
+    if cu_seqlens is not None and any(own):
+        _check("gdn_chunk_bwd_zero_outside",
+               _run(q, L.gdn_chunk_bwd_zero_outside, p[5], num_seqs, total_T, H, H_k, d_k, d_v, dt,
+                    *(x if o else None for x, o in zip(p[9:14], own)), _stream(None, q)))
     rc = _run(q, L.gdn_chunk_bwd, *p[:6], num_seqs, total_T, H, H_k, d_k, d_v, dt, GDN_DECAY_PER_HEAD, float(scale),
               int(bool(use_qk_l2norm)), p[6], p[7], _dt(dout), *p[8:], ws, ws_bytes, _stream(None, q))
     _check("gdn_chunk_bwd", rc)

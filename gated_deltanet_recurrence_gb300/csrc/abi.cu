@@ -217,6 +217,27 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
     return launch_status(gdn::launch_chunk_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
+int gdn_chunk_bwd_zero_outside(const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k, int d_k,
+                               int d_v, gdn_dtype qkv_dtype, void* dq, void* dk, void* dv, float* dg,
+                               float* dbeta, void* stream) {
+    if (!valid_dtype(qkv_dtype)) return GDN_ERR_DTYPE;
+    if (num_seqs <= 0 || total_T < 0 || !heads_ok(H, H_k)) return GDN_ERR_ARG;
+    if (!head_size_ok(d_k, d_v)) return GDN_ERR_UNSUPPORTED;
+    if (!chunk_bwd_sizes_ok(num_seqs, total_T, H, H_k, d_k, d_v)) return GDN_ERR_ARG;
+    const void* ptrs[] = {dq, dk, dv, dg, dbeta};
+    bool any = false;
+    for (const void* p : ptrs) {
+        if (p && !aligned16(p)) return GDN_ERR_ARG;
+        any |= p != nullptr;
+    }
+    if (!cu_seqlens || total_T == 0 || !any) return GDN_OK;
+    gdn::ChunkBwdArgs a{};
+    a.cu_seqlens = cu_seqlens; a.num_seqs = num_seqs; a.total_T = total_T; a.H = H; a.Hk = H_k;
+    a.d = d_k; a.qkv_dtype = qkv_dtype;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta;
+    return launch_status(gdn::launch_chunk_bwd_zero_outside(a, static_cast<cudaStream_t>(stream)));
+}
+
 static int decode_entry(const void* q, const void* k, const void* v, const float* g,
                         const float* beta, float* state, int num_slots, const int32_t* idx, int N,
                         int T, int H, int H_k, int d_k, int d_v, gdn_dtype qkv_dtype,

@@ -1794,6 +1794,20 @@ __global__ void __launch_bounds__(kPrepThreads) chunk_bwd_heads_kernel(ChunkBwdA
     }
 }
 
+// Zeros to the rows of tokens before the first and behind the last sequence, of those gradients that are given:
+// blockIdx.y is the gradient, a word of four bytes a thread (a row of every one is a multiple of them).
+__global__ void __launch_bounds__(kPrepThreads) chunk_bwd_zero_outside_kernel(ChunkBwdArgs a) {
+    const int first = a.cu_seqlens[0], end = a.cu_seqlens[a.num_seqs];
+    if (first < 0 || end < first || end > a.total_T) return;  // gdn_chunk_bwd records it
+    void* const outs[5] = {a.dq, a.dk, a.dv, a.dg, a.dbeta};
+    uint32_t* out = static_cast<uint32_t*>(outs[blockIdx.y]);
+    if (!out) return;
+    const long words = blockIdx.y > 2 ? a.H : (long)(blockIdx.y == 2 ? a.H : a.Hk) * a.d / (a.qkv_dtype == GDN_BF16 ? 2 : 1);
+    const long before = first * words, skip = (end - first) * words, all = a.total_T * words - skip;
+    for (long i = (long)blockIdx.x * kPrepThreads + threadIdx.x; i < all; i += (long)gridDim.x * kPrepThreads)
+        out[i < before ? i : i + skip] = 0u;
+}
+
 template <int D, int P>
 cudaError_t launch(const ChunkBwdArgs& a, cudaStream_t s) {
     const size_t slots = (size_t)slot_count(a.num_seqs, a.total_T), units = slots * a.H;
@@ -1839,6 +1853,11 @@ size_t chunk_bwd_workspace_bytes(int num_seqs, int total_T, int H, int Hk, int d
     const size_t slots = (size_t)slot_count(num_seqs, total_T), units = slots * H;
     const size_t unit = link_bytes(d, 2) + 2 * kTBytes + sizeof(float) * (2 * kC * d + 2 * d * d) + sizeof(Meta);
     return index_bytes(slots) + units * unit + (H > Hk ? 2 * sizeof(float) * total_T * H * d : 0);
+}
+
+cudaError_t launch_chunk_bwd_zero_outside(const ChunkBwdArgs& a, cudaStream_t s) {
+    chunk_bwd_zero_outside_kernel<<<dim3(kSMs / 4, 5), kPrepThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs& a, cudaStream_t s) {

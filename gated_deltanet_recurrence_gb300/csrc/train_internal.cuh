@@ -55,5 +55,6 @@ struct ChunkBwdArgs {
 };
 size_t chunk_bwd_workspace_bytes(int num_seqs, int total_T, int H, int Hk, int d);
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_bwd_zero_outside(const ChunkBwdArgs& a, cudaStream_t s);
 
 }  // namespace gdn

@@ -144,8 +144,9 @@ size_t gdn_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int d_k, i
  *   dinitial_state [num_seqs, H, d_v, d_k] fp32, or NULL (not written).  For an empty sequence it
  *                 is dfinal_state.  May alias dfinal_state.
  *   workspace     at least gdn_chunk_bwd_workspace_size(...) bytes, 256-byte aligned.
- * No other output may overlap an input.  Rows of tokens behind the last sequence of cu_seqlens are
- * left as they were.  A malformed cu_seqlens is recorded as GDN_ERR_CU_SEQLENS in the device error
+ * No other output may overlap an input.  Rows of tokens before the first and behind the last
+ * sequence of cu_seqlens are left as they were (gdn_chunk_bwd_zero_outside writes the zeros that
+ * their gradients are).  A malformed cu_seqlens is recorded as GDN_ERR_CU_SEQLENS in the device error
  * word, and the call then writes nothing.
  * Arithmetic is that of fp32 for both element types, with one rounding at each output, but that the
  * operands of products hold 22 bits.  A token's gradients keep that accuracy beside tokens of the
@@ -162,6 +163,17 @@ int gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* g, c
 
 /* Bytes of workspace gdn_chunk_bwd needs for these sizes; 0 for sizes it refuses. */
 size_t gdn_chunk_bwd_workspace_size(int num_seqs, int total_T, int H, int H_k, int d_k, int d_v);
+
+/*
+ * gdn_chunk_bwd_zero_outside -- zeros to the rows that gdn_chunk_bwd leaves as they were: those of
+ * tokens before cu_seqlens[0] and from cu_seqlens[num_seqs] on, whose gradients are zero.
+ *   sizes and cu_seqlens as in gdn_chunk_bwd (without cu_seqlens every token is covered and nothing is
+ *   written); dq, dk, dv of qkv_dtype, dg, dbeta fp32: each may be NULL.  An interval outside
+ *   [0, total_T] writes nothing (gdn_chunk_bwd records it).
+ */
+int gdn_chunk_bwd_zero_outside(const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int H_k, int d_k,
+                               int d_v, gdn_dtype qkv_dtype, void* dq, void* dk, void* dv, float* dg,
+                               float* dbeta, void* stream);
 
 /*
  * gdn_recurrent_step -- one decode token for N sequences, state updated in place.

@@ -152,6 +152,39 @@ def test_chunk_bwd_leaves_rows_outside_the_sequences(Hk):
         assert (got[x][:4] == 3.5).all() and (got[x][T - 6:] == 3.5).all(), x
 
 
+@pytest.mark.parametrize("dtype,d,Hk", [(BF16, 64, 1), (F32, 128, 3)])
+def test_chunk_bwd_allocated_rows_outside_the_sequences_are_zero(dtype, d, Hk):
+    """Tokens of no sequence (a padded batch) have zero gradients in what the binding allocates, also where the
+    memory held something else before, and on another stream; given outputs keep their rows."""
+    inp = delta_inputs([70, 0, 9], 3, Hk, d, dtype, seed=5, lead=4, behind=60)
+    T = inp["q"].shape[0]
+    shapes = [tuple(inp[x].shape) for x in ("q", "k", "v", "g", "beta")]
+    for stream in (None, torch.cuda.Stream()):
+        with torch.cuda.stream(stream):  # None: as it is
+            before = [torch.full(s, float("nan"), dtype=t, device="cuda") for s, t in zip(shapes, (dtype,) * 3 + (F32,) * 2)]
+            torch.cuda.synchronize()
+            del before
+        dv = torch.full(shapes[2], 3.5, dtype=dtype, device="cuda")
+        torch.cuda.synchronize()
+        got = chunk_bwd(inp, stream=stream, dv=dv)
+        torch.cuda.synchronize()
+        check_chunk(inp, got)
+        for x in ("dq", "dk", "dg", "dbeta"):
+            assert (got[x][:4] == 0).all() and (got[x][T - 60:] == 0).all(), x
+        assert (dv[:4] == 3.5).all() and (dv[T - 60:] == 3.5).all()
+
+
+def test_chunk_bwd_without_any_token_in_a_sequence():
+    inp = delta_inputs([0, 0], 2, 1, 64, F32, seed=5, lead=3, behind=2)
+    del inp["cu"][:]
+    inp["cu"] += [3, 3, 3]
+    nan = [torch.full((5, 2, 64), float("nan"), device="cuda") for _ in range(8)]
+    del nan
+    got = chunk_bwd(inp)
+    assert all(torch.count_nonzero(got[x]) == 0 for x in NAMES[:5])
+    assert torch.equal(got["dinitial_state"].cpu(), inp["dfinal_state"])
+
+
 def test_chunk_bwd_fp32_dout_of_bf16_inputs_and_equal_lengths():
     inp = delta_inputs([96, 96], 2, 2, 128, BF16, seed=6)
     inp["dout"] = torch.randn(192, 2, 128, generator=torch.Generator().manual_seed(1))

@@ -57,6 +57,16 @@ def test_chunk_bwd_workspace_size():
 
 
 @pytest.mark.parametrize("status,kw", [
+    (DTYPE, dict(dt=2)), (ARG, dict(num_seqs=0)), (ARG, dict(total_T=-1)), (ARG, dict(H=3)), (UNSUPPORTED, dict(dk=96, dv=96)),
+    (ARG, dict(dv_=Q4)), (ARG, dict(dg=Q4)), (ARG, dict(total_T=1 << 30, H=4, Hk=4)), (0, dict(cu=NUL)), (0, dict(total_T=0)),
+    (0, dict(dq=NUL, dk_=NUL, dv_=NUL, dg=NUL, dbeta=NUL))])
+def test_zero_outside_refusals(status, kw):
+    args = dict(cu=P, num_seqs=1, total_T=64, H=2, Hk=2, dk=128, dv=128, dt=0, dq=P, dk_=P, dv_=P, dg=P, dbeta=P, stream=NUL)
+    assert set(kw) <= set(args)
+    assert gdn.lib().gdn_chunk_bwd_zero_outside(*{**args, **kw}.values()) == status
+
+
+@pytest.mark.parametrize("status,kw", [
     (DTYPE, dict(odt=3)), (DTYPE, dict(dt=-1)), (ARG, dict(d=100)), (ARG, dict(d=2048)), (ARG, dict(d=0)),
     (ARG, dict(rows=-1)), (ARG, dict(eps=-1.0)), (ARG, dict(eps=float("nan"))), (ARG, dict(z=NUL)), (ARG, dict(dz=NUL)),
     (ARG, dict(y=NUL)), (ARG, dict(dout=Q4)), (WORKSPACE, dict(dw=P)), (WORKSPACE, dict(dw=P, ws=P, wsb=8)),
