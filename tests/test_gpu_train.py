@@ -418,6 +418,40 @@ def test_norm_bwd_in_place_and_mixed_types():
     assert torch.equal(y2, ref)
 
 
+def _off(x, ref, most):
+    """The largest error of an element beside what it may be, `most` times its value."""
+    ref = ref.double()
+    return float(((x.detach().cpu().double() - ref).abs() / (ref.abs() * most)).max())
+
+
+def test_small_gates_keep_their_relative_accuracy():
+    """Gates far from zero: silu(z) and its slope are tiny on the negative side and each element is right by
+    itself.  Per element: the exponential (2 + 1.16 |z|) 2^-23, 1 + e 2^-24, the division 2^-22, the norm's rsqrt
+    and sum of squares 2^-22 each, and eight products and sums 2^-24 each."""
+    x = _norm_inputs(64, 2, 128, F32, seed=15)
+    gen = torch.Generator().manual_seed(16)
+    z = (2 + 78 * torch.rand(64, 2, 128, generator=gen)) * torch.where(torch.rand(64, 2, 128, generator=gen) < 0.8, -1, 1)
+    tol = 3 * 2.0 ** -22 + 9 * 2.0 ** -24 + (2 + 1.16 * z.double().abs()) * 2.0 ** -23
+    y = torch.rand(64, 2, 128, generator=gen) + 0.5
+    _, dz, _ = gdn.gdn_gate_rmsnorm_silu_bwd(dev(x["dout"]), dev(y), dev(z))
+    assert _off(dz, norm_grads(x["dout"], y, z, None, None, 1e-6, True)[1], tol) <= 1
+    one = torch.full((64, 2, 1), 1.0)  # a group of one channel: n = 0, m = bias
+    out = gdn.gdn_gate_groupnorm_silu(dev(one), dev(z[..., :1].contiguous()), None, dev(torch.ones(2, 1)))
+    assert _off(out, z[..., :1].double() * torch.sigmoid(z[..., :1].double()), tol[..., :1]) <= 1
+    a, b, dg = (t.contiguous() for t in (z[:, 0], z[:, 1], x["dout"][:, 0]))
+    A_log = torch.rand(128, generator=gen)
+    got = gdn.gdn_decay_from_logits_bwd(dev(a), dev(A_log), None, dev(b), dev(dg), dev(dg))
+    assert _off(got[0], decay_grads(a, A_log, None, b, dg, dg)[0], tol[:, 0]) <= 1
+    bb = b.double()  # sigma(b) sigma(-b): 1 - sigma(80) is zero in 64 bits
+    assert _off(got[3], dg.double() * torch.sigmoid(bb) * torch.sigmoid(-bb), tol[:, 1]) <= 1
+    for v in (float("inf"), 1000.0):  # what the formulas give at the ends
+        ends = torch.tensor([[v, -v]], device="cuda")
+        da, _, _, db = gdn.gdn_decay_from_logits_bwd(ends, torch.zeros(2, device="cuda"), None, ends, *[torch.ones(1, 2, device="cuda")] * 2)
+        assert da.tolist() == [[-1.0, 0.0]] and db.tolist() == [[0.0, 0.0]]
+        out = gdn.gdn_gate_groupnorm_silu(dev(one[:1]), ends[..., None], None, dev(torch.ones(2, 1)))
+        assert out[0, 0, 0] == v and (out[0, 1, 0].isnan() if v == float("inf") else out[0, 1, 0] == 0)
+
+
 def test_norm_bwd_of_no_rows_gives_zero_sums():
     y = torch.empty(0, 3, 32, device="cuda")
     _, _, dw, db = gdn.gdn_gate_groupnorm_silu_bwd(y, y, y, torch.ones(3, 32, device="cuda"),
