@@ -413,6 +413,13 @@ def _workspace(workspace, need, ref):
     return workspace, ptr, workspace.numel() * workspace.element_size()
 
 
+def _same_device(stream, ref):
+    """Refuses a stream of another device than the call's: made current, it would leave the call on its own
+    device's current stream instead, unordered with the given one."""
+    if ref.is_cuda and stream.device != ref.device:
+        raise ValueError(f"the stream is on {stream.device}, the call runs on {ref.device}")
+
+
 def _on_stream(call):
     """With stream=..., runs the call with that stream current, so that what it allocates belongs to the
     stream that uses it (memory taken on one stream may still be read by that stream's pending work)."""
@@ -420,9 +427,10 @@ def _on_stream(call):
     def wrapped(*args, stream=None, **kw):
         if stream is None:
             return call(*args, **kw)
+        first = next(t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor))
         if not isinstance(stream, torch.cuda.Stream):
-            first = next(t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor))
             stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        _same_device(stream, first)
         with torch.cuda.stream(stream):
             return call(*args, **kw)
     return wrapped

@@ -156,6 +156,32 @@ def test_undersized_and_mistyped_tensors_are_refused_by_name():
         gdn.gdn_decay_from_logits_bwd(a, a[0], None, a, a, None)
 
 
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """With stand-ins for a stream and for a tensor on the GPU: made current, such a stream would leave the call on
+    its own device's current stream, unordered with the given one."""
+    from contextlib import nullcontext
+
+    from gated_deltanet_recurrence_gb300 import _binding
+
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    class OnGpu(torch.Tensor):
+        is_cuda, device = True, torch.device("cuda", 0)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: nullcontext())
+    ran = []
+    call = _binding._on_stream(lambda t: ran.append(t))
+    t = torch.zeros(1).as_subclass(OnGpu)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        call(t, stream=Stream(1))
+    assert not ran
+    call(t, stream=Stream(0))
+    assert len(ran) == 1
+
+
 # ---- the yardstick against differences ---------------------------------------------------------------
 
 def _difference(f, x, direction, h=1e-6):
