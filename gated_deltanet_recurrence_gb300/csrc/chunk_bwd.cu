@@ -1538,25 +1538,33 @@ __global__ void __launch_bounds__(GradSmem<D, P>::threads, D == 64 && P == 1 ? 2
     float x[NC];
     wait(0, 0);
     {
-        uint32_t raw[NC];
-        if constexpr (NC == 16) tmem_ld16(lanes + L::tNZ + cg * NC, raw);
-        else ptx::tmem_ld32(lanes + L::tNZ + cg * NC, raw);
-        ptx::tmem_wait_ld();
         const float2 gr = t.G[row];
         const float f = part ? -fR[row] : fY[row], f2 = part ? t.beta[row] * fK[row] : fQ[row];
         uint32_t top = 0, mine = 0;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = cg * NC + i;
-            const float y = __uint_as_float(raw[i]) * f * (decay(gr, t.G[c]) * fU[c]);
-            if (c == row && part == 0) {
-                dpp[row] = y;
-                diag[row] = p_diag * y;  // dP_ii q_i . k_i
+        for (int p = 0; p < NC; p += 16) {
+            const int c0 = cg * NC + p;
+            if (c0 > (row | 31)) {  // above the diagonal in every row of this warp
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[p + i] = 0.f;
+                continue;
             }
-            x[i] = c < row ? y : 0.f;
-            top = max(top, planes::abs_bits(x[i] * fK[c]));
-            const uint32_t col = __reduce_max_sync(0xffffffffu, planes::abs_bits(x[i] * f2));
-            if (lane == i) mine = col;
+            uint32_t raw[16];
+            tmem_ld16(lanes + L::tNZ + c0, raw);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int c = c0 + i;
+                const float y = __uint_as_float(raw[i]) * f * (decay(gr, t.G[c]) * fU[c]);
+                if (c == row && part == 0) {
+                    dpp[row] = y;
+                    diag[row] = p_diag * y;  // dP_ii q_i . k_i
+                }
+                x[p + i] = c < row ? y : 0.f;
+                top = max(top, planes::abs_bits(x[p + i] * fK[c]));
+                const uint32_t col = __reduce_max_sync(0xffffffffu, planes::abs_bits(x[p + i] * f2));
+                if (lane == p + i) mine = col;
+            }
         }
         reinterpret_cast<uint32_t*>(sm + L::SQ + L::tPZ)[cg * 128 + part * kC + row] = top;
         if (lane < NC) reinterpret_cast<uint32_t*>(sm + L::SQ + L::tCols)[(warp & 3) * kC + cg * NC + lane] = mine;
