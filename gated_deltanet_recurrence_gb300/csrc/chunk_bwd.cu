@@ -29,12 +29,15 @@
 // adds the heads of a group in order.
 //
 // Every product is taken on the tensor cores from fp16 planes at fp32 accuracy (mma_planes.cuh); what is
-// between the products is fp32.
+// between the products is fp32.  What has a row a token is scaled row by row, so that a token's gradients keep
+// that accuracy beside tokens of the chunk whose q, k, v or dY are larger by any factor; the states and X have one
+// scale a matrix (or, in the scan, one a row of theirs).
 //
 // The chain over the chunks is the only serial part, so it is kept to what the state meets, and the rest
-// runs over all chunks at once; the price is what the kernels hand over, 295 KB a chunk and head at d = 128.
-// Measured on 2 x 4096 tokens, 16 heads, d = 128, bf16: 0.68 ms in all (inputs and outputs alone would take
-// 35 us at the copy rate), prep 184, scan 212, grad 284 - 290 us; 16384 tokens, 32 heads: 2.53 ms.
+// runs over all chunks at once; the price is what the kernels hand over, 296 KB a chunk and head at d = 128.
+// Measured on 2 x 4096 tokens, 16 heads, d = 128, bf16: 0.70 ms in all (inputs and outputs alone would take
+// 35 us at the copy rate), prep 185, scan 217 - 220, grad 304 us; 16384 tokens, 32 heads: 2.62 ms.  (With one scale
+// a chunk where there is one a row now: 0.68 ms and 2.52 ms.)
 #include "mma_planes.cuh"
 #include "sm100_ptx.cuh"
 #include "train_internal.cuh"
@@ -600,8 +603,8 @@ __device__ __forceinline__ Scale row_scale(const uint32_t* tops, int r) {
 // Shared memory: K, V, Q (P planes each; the two planes of Q' go over V and Q), a 64 x 64 matrix (T with
 // factors, then P) and a 64 x d buffer (W, then dY); before them, over both, A and T in fp32.  d = 128 in
 // bf16 takes 96 KB, so two blocks share an SM and one works while the other waits at a barrier.
-// No pipe is full (184 us at the sizes above: tensor pipe 26%, shared memory 52%, issue slots 37%, DRAM
-// 2.6 TB/s): what is left is the latency of a chunk's dependent steps.  Blocks that stay on their SM took
+// No pipe is full (185 us at the sizes above: tensor pipe 26%, shared memory 50%, issue slots 38%, DRAM
+// 2.5 TB/s): what is left is the latency of a chunk's dependent steps.  Blocks that stay on their SM took
 // 210 us (what the loop keeps in registers spills).
 template <int D, int P>
 struct PrepSmem {
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(kPrepThreads, P == 1 ? 2 : 1) chunk_bwd_prep_k
 // writes a place again has met the next step's barrier, which its partner reaches only after reading it.
 // The chunks' links arrive by bulk copies; each pair of warps waits for a link and gives it back by itself, so
 // that pairs drift apart and one sub-partition's two warps (of two pairs) are not in the same phase.
-// At the sizes above 128 blocks take 64 steps of 3.3 us (6.2k cycles); MMAs fill 42% of it, the rest is the
+// At the sizes above 128 blocks take 64 steps of 3.4 us (6.4k cycles); MMAs fill 41% of it, the rest is the
 // splitting of S and Z into planes and the wait for the other half.  With the links copied by all warps
 // between block barriers it took 252 us; with the transposed state on tcgen05, 250 us: its products have
 // N = 64 and are bound by reading the left side from shared memory (56 cycles each).
@@ -1106,10 +1109,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) chunk_bwd_scan_kernel(ChunkBw
 //        plane in rows 64 .. 127, to be added up
 // A thread then has one token's row: of dQ (TMEM lanes 0 .. 63) or of F and dK (lanes 64 .. 127), and 32
 // columns of it.
-// 284 - 290 us at the sizes above: some 36k cycles a chunk, 10k of them until its first tiles are in place; tensor
-// pipe 15%, issue slots 38%, DRAM 2.6 TB/s.  What brought it there, from 398 us: the products on tcgen05 (351),
+// 304 us at the sizes above: some 38k cycles a chunk, 10k of them until its first tiles are in place; tensor
+// pipe 14%, issue slots 39%, DRAM 2.5 TB/s.  What brought it there, from 398 us: the products on tcgen05 (351),
 // P from the preparation (320), E's and v's loads a phase earlier (314), T, P, E and S0 by bulk copies instead
-// of through registers (302), no divisions, and no wait for TMEM or v, at a block's start (289).  Blocks that
+// of through registers (302), no divisions, and no wait for TMEM or v, at a block's start (289);
+// scales by rows and columns instead of one a tile took it to 304.  Blocks that
 // stay on their SM took 382 against 320 us with the chunk in the loop (spills) and 447 as a function of its own.
 
 constexpr uint64_t kMmaWaitNs = 2000000000ull;
