@@ -52,7 +52,7 @@ cudaError_t launch_cluster(void (*kernel)(P...), int blocks, size_t smem, cudaSt
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    return launch_config(cfg, kernel, args...);
 }
 
 // out[c] = the sum over the cluster's blocks, in order, of element at(c) of each block's `table`; the
@@ -432,22 +432,21 @@ __global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float* ta
 }
 
 template <int L, int NV, int VEC>
-void launch_norm_one(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
+cudaError_t launch_norm_one(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
     if (!bwd) {
         groupnorm_kernel<L, NV, VEC><<<p.blocks, kThreads, 0, s>>>(a, p.stride);
-        return;
-    }
-    if (p.cluster) {
+    } else if (p.cluster) {
         const auto kernel = a.rms ? norm_bwd_kernel<L, NV, VEC, true, true> : norm_bwd_kernel<L, NV, VEC, false, true>;
-        launch_cluster(kernel, p.blocks, 2 * sizeof(float) * a.groups * a.size, s, a, p.stride, 0);
+        return launch_cluster(kernel, p.blocks, 2 * sizeof(float) * a.groups * a.size, s, a, p.stride, 0);
     } else {
         const auto kernel = a.rms ? norm_bwd_kernel<L, NV, VEC, true, false> : norm_bwd_kernel<L, NV, VEC, false, false>;
         kernel<<<p.blocks, kThreads, 0, s>>>(a, p.stride, p.prows);
     }
+    return cudaGetLastError();
 }
 
 template <int VEC>
-void launch_norm_vec(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
+cudaError_t launch_norm_vec(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
     switch (p.L) {
         case 1: return launch_norm_one<1, 1, VEC>(a, p, bwd, s);
         case 2: return launch_norm_one<2, 1, VEC>(a, p, bwd, s);
@@ -463,13 +462,13 @@ void launch_norm_vec(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_
         if (p.nv <= 8) return launch_norm_one<32, 8, VEC>(a, p, bwd, s);
     }
     if constexpr (VEC == 1) return launch_norm_one<32, 32, VEC>(a, p, bwd, s);
+    return cudaErrorInvalidValue;  // groups of more than 1024 channels are refused before
 }
 
 cudaError_t launch_norm(const NormArgs& a, const NormPlan& p, bool bwd, cudaStream_t s) {
-    if (p.vec == 8) launch_norm_vec<8>(a, p, bwd, s);
-    else if (p.vec == 4) launch_norm_vec<4>(a, p, bwd, s);
-    else launch_norm_vec<1>(a, p, bwd, s);
-    return cudaGetLastError();
+    if (p.vec == 8) return launch_norm_vec<8>(a, p, bwd, s);
+    if (p.vec == 4) return launch_norm_vec<4>(a, p, bwd, s);
+    return launch_norm_vec<1>(a, p, bwd, s);
 }
 
 // ---- gate preparation --------------------------------------------------------------------------

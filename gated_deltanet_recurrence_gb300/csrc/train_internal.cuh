@@ -5,6 +5,15 @@
 
 namespace gdn {
 
+// Launches a kernel.  A failure is returned and not left in the runtime, where the launch check of the next call
+// would take it for its own.
+template <class... P, class... A>
+cudaError_t launch_config(const cudaLaunchConfig_t& cfg, void (*kernel)(P...), A... args) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 // Launches a kernel that begins with dependency_wait() behind the kernel before it on the stream: its
 // launch overlaps that kernel's end, and what that kernel wrote is seen after the wait.
 template <class... P, class... A>
@@ -19,7 +28,7 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    return launch_config(cfg, kernel, args...);
 }
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -1,4 +1,6 @@
 """The training operators on the GPU, against fp64 forms on the same inputs (tests/_train.py)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -633,6 +635,42 @@ def test_decay_sums_on_either_side_of_a_cluster(T, H, which):
             assert bool((g == 5).all())
         else:
             assert rel_l2(g, r) <= tol_of(g), (i, rel_l2(g, r))
+
+
+@pytest.mark.parametrize("which", ["decay", "norm", "chunk"])
+def test_a_launch_that_fails_leaves_no_error_to_the_next_call(which):
+    """A launch into a stream whose capture has been broken off fails on the host; the call says so, and the next
+    call on another stream is not told of it."""
+    rt = next(r for r in (_cudart(n) for n in ("libcudart.so.13", "libcudart.so")) if r is not None)
+    L, s = gdn.lib(), torch.cuda.Stream()
+    x = torch.randn(40, 2, 64, device="cuda")
+    c, st = torch.ones(2, 64, device="cuda"), torch.zeros(1, 2, 64, 64, device="cuda")
+    outs, sums, ws = [torch.empty_like(x) for _ in range(6)], torch.empty(4, 128, device="cuda"), torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(ctypes.c_void_p(s.cuda_stream), 2) == 0
+    assert rt.cudaStreamSynchronize(ctypes.c_void_p(s.cuda_stream)) != 0  # not allowed: the capture is broken off
+    if which == "decay":
+        rc = L.gdn_decay_from_logits_bwd(p(x), p(c), None, None, p(x), None, p(outs[0]), p(sums), None, None, 40, 128,
+                                         p(ws), ws.numel(), s.cuda_stream)
+    elif which == "norm":
+        rc = L.gdn_gate_groupnorm_silu_bwd(p(x), 0, p(x), 0, None, p(c), None, 1e-6, p(outs[0]), None, p(sums), None, 40, 2,
+                                           64, p(ws), ws.numel(), s.cuda_stream)
+    else:
+        rc = L.gdn_chunk_bwd(p(x), p(x), p(x), p(x), p(x), None, 1, 40, 2, 2, 64, 64, 0, 0, 0.0, 1, None, p(x), 0, None,
+                             *(p(t) for t in outs[:5]), None, p(ws), ws.numel(), s.cuda_stream)
+    graph = ctypes.c_void_p()
+    assert rt.cudaStreamEndCapture(ctypes.c_void_p(s.cuda_stream), ctypes.byref(graph)) != 0
+    rt.cudaGetLastError()
+    assert rc == -5
+    assert torch.isfinite(gdn.gdn_gate_groupnorm_silu(x)).all()
+
+
+def _cudart(name):
+    try:
+        return ctypes.CDLL(name)
+    except OSError:
+        return None
 
 
 def test_small_calls_on_two_streams_at_once():
