@@ -22,6 +22,7 @@ GDN_F32, GDN_BF16 = 0, 1
 GDN_DECAY_PER_HEAD, GDN_DECAY_PER_KEY_CHANNEL = 0, 1
 GDN_CONV_KERNEL = 4
 GDN_FORM_AUTO, GDN_FORM_OFF, GDN_FORM_ON = 0, 1, 2
+GDN_NORM_RMS, GDN_NORM_L2 = 0, 1
 STATUS = {0: "GDN_OK", -1: "GDN_ERR_ARG", -2: "GDN_ERR_DTYPE", -3: "GDN_ERR_CU_SEQLENS",
           -4: "GDN_ERR_WORKSPACE", -5: "GDN_ERR_LAUNCH", -6: "GDN_ERR_TIMEOUT",
           -7: "GDN_ERR_UNSUPPORTED", -8: "GDN_ERR_CUDA"}
@@ -55,6 +56,24 @@ SIGNATURES = {
     "gdn_gate_bwd_workspace_size": (_sz, [_l, _i, _i]),
     "gdn_decay_from_logits_bwd": (_i, [_fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _l, _i, _vp, _sz, _vp]),
     "gdn_decay_bwd_workspace_size": (_sz, [_l, _i]),
+    "gdn_short_conv_fwd": (_i, [_vp, _l, _fp, _fp, _ip, _i, _i, _i, _i, _i, _fp, _fp, _vp, _vp]),
+    "gdn_short_conv_step": (_i, [_vp, _l, _fp, _fp, _fp, _i, _ip, _i, _i, _i, _i, _i, _vp, _vp]),
+    "gdn_short_conv_bwd": (_i, [_vp, _vp, _l, _fp, _fp, _ip, _i, _i, _i, _i, _i, _fp, _fp, _vp, _fp, _fp, _fp, _i,
+                                _vp, _sz, _vp]),
+    "gdn_short_conv_bwd_workspace_size": (_sz, [_i, _i, _i]),
+    "gdn_ssm_chunk_fwd": (_i, [_vp, _l, _vp, _l, _vp, _l, _fp, _fp, _fp, _fp, _ip, _i, _i, _i, _i, _i, _i, _i, _fp,
+                               _fp, _vp, _vp, _sz, _vp]),
+    "gdn_ssm_chunk_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "gdn_ssm_step": (_i, [_vp, _l, _vp, _l, _vp, _l, _fp, _fp, _fp, _fp, _fp, _i, _ip, _i, _i, _i, _i, _i, _i, _i,
+                          _vp, _vp]),
+    "gdn_ssm_chunk_bwd": (_i, [_vp, _vp, _l, _vp, _l, _vp, _l, _fp, _fp, _fp, _fp, _ip, _i, _i, _i, _i, _i, _i, _i,
+                               _fp, _fp, _vp, _vp, _vp, _fp, _fp, _fp, _fp, _fp, _i, _vp, _sz, _vp]),
+    "gdn_ssm_chunk_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "gdn_qk_norm_rope": (_i, [_vp, _l, _vp, _l, _fp, _ip, _l, _fp, _fp, _i, _f, _i, _i, _i, _i, _i, _i, _i, _vp, _l,
+                              _vp, _l, _vp]),
+    "gdn_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _l, _vp, _l, _fp, _ip, _l, _fp, _fp, _i, _f, _i, _i, _i, _i, _i, _i,
+                                  _i, _vp, _l, _vp, _l, _fp, _fp, _vp, _sz, _vp]),
+    "gdn_qk_norm_rope_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
     "gdn_get_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_int)]),
     "gdn_status_string": (ctypes.c_char_p, [_i]),
     "gdn_selftest_bounded_wait": (_i, [ctypes.c_ulonglong, _vp, _vp]),
@@ -612,6 +631,313 @@ def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=N
     rc = _run(a, L.gdn_decay_from_logits_bwd, *p[:10], total_T, H, ws, ws_bytes, _stream(None, a))
     _check("gdn_decay_from_logits_bwd", rc)
     return da, dA_log, ddt_bias, db
+
+
+def _rows(ref, name, t, shape, lead=1):
+    """Pointer and stride of a token tensor that may be a slice of a wider one: `shape` (its first `lead` dimensions
+    the tokens), each token's row contiguous, tokens one stride apart."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {tuple(shape)}")
+    if t.get_device() != ref.get_device() or (not ref.is_cuda and t.device != ref.device):
+        raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
+    width, strides = 1, t.stride()
+    for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
+        if n != 1 and st != width:
+            raise ValueError(f"{name}: the rows of a token must be contiguous")
+        width *= n
+    stride = strides[lead - 1]
+    if lead == 2:
+        if shape[1] == 1:
+            stride = strides[0]
+        elif shape[0] > 1 and strides[0] != shape[1] * stride:
+            raise ValueError(f"{name}: tokens must be one stride apart over all sequences")
+    tokens = 1
+    for n in shape[:lead]:
+        tokens *= n
+    if tokens <= 1:  # one row has no stride
+        stride = -(-width // 8) * 8
+    return t.data_ptr(), stride
+
+
+def _seqs(cu_seqlens, num_seqs):
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        return cu_seqlens.numel() - 1
+    return 1 if num_seqs is None else num_seqs
+
+
+def _same_dtype(dt, **tensors):
+    for name, t in tensors.items():
+        if t is not None and _dt(t) != dt:
+            raise TypeError(f"{name} must have the dtype of the inputs")
+
+
+def _tokens(t, dims, name):
+    """A step call's tensor with its token dimension: [N, T, ...] as given, or [N, ...] as one token."""
+    if t.dim() == dims:
+        return t
+    if t.dim() == dims - 1:
+        return t.unsqueeze(1)
+    raise ValueError(f"{name} must have {dims - 1} or {dims} dimensions")
+
+
+_CONV_NAMES = ("weight", "bias", "cu_seqlens", "conv_state", "conv_state_out", "out")
+_CONV_FP32 = (True, True, False, True, True, False)
+_CONV_STEP_NAMES = ("weight", "bias", "conv_state", "state_indices", "out")
+_CONV_STEP_FP32 = (True, True, True, False, False)
+_CONV_BWD_NAMES = ("dout", "weight", "bias", "cu_seqlens", "conv_state", "dconv_state_out", "dx", "dweight", "dbias",
+                   "dconv_state")
+_CONV_BWD_FP32 = (False, True, True, False, True, True, False, True, True, True)
+_SSM_NAMES = ("a", "A_log", "dt_bias", "D", "cu_seqlens", "initial_state", "final_state", "out")
+_SSM_FP32 = (True, True, True, True, False, True, True, False)
+_SSM_STEP_NAMES = ("a", "A_log", "dt_bias", "D", "state", "state_indices", "out")
+_SSM_STEP_FP32 = (True, True, True, True, True, False, False)
+_SSM_BWD_NAMES = ("dout", "a", "A_log", "dt_bias", "D", "cu_seqlens", "initial_state", "dfinal_state", "dx", "dB", "dC",
+                  "da", "dA_log", "ddt_bias", "dD", "dinitial_state")
+_SSM_BWD_FP32 = (False, True, True, True, True, False, True, True, False, False, False, True, True, True, True, True)
+_QK_NAMES = ("cos_sin", "positions", "q_weight", "k_weight", "dq_weight", "dk_weight")
+_QK_FP32 = (True, False, True, True, True, True)
+
+
+@_on_stream
+def gdn_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, num_seqs=None, conv_state=None, conv_state_out=None,
+                       output_final_state=True, silu=True, out=None):
+    """The causal short convolution (four taps, SiLU) over packed sequences: x [total_T, dim] (fp32 or bf16; may be a
+    slice of a wider tensor, rows one stride apart), weight [dim, 4], bias [dim] or None, conv_state
+    [num_seqs, dim, 3] the carried inputs (None: zeros).  Returns (out [total_T, dim], conv_state_out), which is
+    allocated unless given (it may be conv_state itself) or not requested."""
+    total_T, dim = x.shape
+    num_seqs, dt = _seqs(cu_seqlens, num_seqs), _dt(x)
+    px, stride = _rows(x, "x", x, (total_T, dim))
+    if out is None:
+        out = torch.empty((total_T, dim), dtype=x.dtype, device=x.device)
+    _same_dtype(dt, out=out)
+    if conv_state_out is None and output_final_state:
+        conv_state_out = torch.empty((num_seqs, dim, 3), dtype=torch.float32, device=x.device)
+    st = num_seqs * dim * 3
+    p = _pointers(x, _CONV_NAMES, (weight, bias, cu_seqlens, conv_state, conv_state_out, out),
+                  (dim * GDN_CONV_KERNEL, dim, num_seqs + 1, st, st, total_T * dim), _CONV_FP32)
+    _check("gdn_short_conv_fwd",
+           _run(x, lib().gdn_short_conv_fwd, px, stride, p[0], p[1], p[2], num_seqs, total_T, dim, dt,
+                int(bool(silu)), p[3], p[4], p[5], _stream(None, x)))
+    return out, conv_state_out
+
+
+@_on_stream
+def gdn_short_conv_step(x, weight, conv_state, bias=None, state_indices=None, silu=True, out=None):
+    """The convolution of T more tokens of N sequences: x [N, T, dim] or [N, dim] (a slice of a wider tensor is
+    taken as it is), conv_state [slots, dim, 3] fp32 updated in place, state_indices int32 [N] (negative = skip) or None.
+    Returns out like x."""
+    x3 = _tokens(x, 3, "x")
+    N, T, dim = x3.shape
+    dt = _dt(x)
+    px, stride = _rows(x, "x", x3, (N, T, dim), lead=2)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _same_dtype(dt, out=out)
+    if state_indices is not None and state_indices.dtype != torch.int32:
+        raise TypeError("state_indices must be int32")
+    slots = conv_state.shape[0]
+    p = _pointers(x, _CONV_STEP_NAMES, (weight, bias, conv_state, state_indices, out),
+                  (dim * GDN_CONV_KERNEL, dim, slots * dim * 3, N, N * T * dim), _CONV_STEP_FP32)
+    _check("gdn_short_conv_step",
+           _run(x, lib().gdn_short_conv_step, px, stride, p[0], p[1], p[2], slots, p[3], N, T, dim, dt,
+                int(bool(silu)), p[4], _stream(None, x)))
+    return out
+
+
+@_on_stream
+def gdn_short_conv_bwd(dout, x, weight, bias=None, cu_seqlens=None, num_seqs=None, conv_state=None,
+                       dconv_state_out=None, silu=True, dx=None, dweight=None, dbias=None, dconv_state=None,
+                       workspace=None):
+    """Gradients of gdn_short_conv_fwd: dout [total_T, dim] in x's dtype, the forward's inputs, dconv_state_out the
+    gradient of its final history (None: zeros).  Returns (dx, dweight, dbias, dconv_state): dx in x's dtype, the
+    others fp32; dbias is None unless it or bias is given, dconv_state unless it or conv_state is.  Rows of tokens
+    outside the sequences of cu_seqlens are zeros in a dx allocated here and left as they were in one given."""
+    total_T, dim = x.shape
+    num_seqs, dt = _seqs(cu_seqlens, num_seqs), _dt(x)
+    px, stride = _rows(x, "x", x, (total_T, dim))
+    zeros = dx is None
+    if dx is None:
+        dx = torch.empty((total_T, dim), dtype=x.dtype, device=x.device)
+    _same_dtype(dt, dout=dout, dx=dx)
+    if dweight is None:
+        dweight = torch.empty((dim, GDN_CONV_KERNEL), dtype=torch.float32, device=x.device)
+    if dbias is None and bias is not None:
+        dbias = torch.empty((dim,), dtype=torch.float32, device=x.device)
+    if dconv_state is None and conv_state is not None:
+        dconv_state = torch.empty((num_seqs, dim, 3), dtype=torch.float32, device=x.device)
+    st, n, L = num_seqs * dim * 3, total_T * dim, lib()
+    p = _pointers(x, _CONV_BWD_NAMES,
+                  (dout, weight, bias, cu_seqlens, conv_state, dconv_state_out, dx, dweight, dbias, dconv_state),
+                  (n, dim * GDN_CONV_KERNEL, dim, num_seqs + 1, st, st, n, dim * GDN_CONV_KERNEL, dim, st),
+                  _CONV_BWD_FP32)
+    workspace, ws, ws_bytes = _workspace(workspace, L.gdn_short_conv_bwd_workspace_size(num_seqs, total_T, dim), x)
+    _check("gdn_short_conv_bwd",
+           _run(x, L.gdn_short_conv_bwd, p[0], px, stride, p[1], p[2], p[3], num_seqs, total_T, dim, dt,
+                int(bool(silu)), p[4], p[5], p[6], p[7], p[8], p[9], int(zeros), ws, ws_bytes, _stream(None, x)))
+    return dx, dweight, dbias, dconv_state
+
+
+def _ssm_inputs(x, B, C, lead):
+    """Sizes, dtype and the pointers with strides of x [..., H, P], B and C [..., G, N]."""
+    H, P = x.shape[lead:]
+    G, N = B.shape[lead:]
+    dt = _dt(x)
+    _same_dtype(dt, B=B, C=C)
+    tok = tuple(x.shape[:lead])
+    rows = (*_rows(x, "x", x, tok + (H, P), lead), *_rows(x, "B", B, tok + (G, N), lead),
+            *_rows(x, "C", C, tok + (G, N), lead))
+    return H, P, G, N, dt, rows
+
+
+@_on_stream
+def gdn_ssm_chunk_fwd(x, B, C, a, A_log, dt_bias=None, D=None, cu_seqlens=None, num_seqs=None, initial_state=None,
+                      final_state=None, output_final_state=True, out=None, workspace=None):
+    """The selective state space scan over packed prompts: S_t = exp(-exp(A_log) dt_t) S_{t-1} + dt_t x_t B_t^T,
+    y_t = S_t C_t + D x_t, dt = softplus(a + dt_bias).  x [total_T, H, P], B, C [total_T, G, N] (fp32 or bf16; slices of
+    a wider tensor are taken as they are), a [total_T, H], A_log, dt_bias, D [H] fp32, states [num_seqs, H, P, N] fp32.
+    Returns (out [total_T, H, P], final_state), which is allocated unless given or not requested."""
+    total_T = x.shape[0]
+    H, P, G, N, dt, rows = _ssm_inputs(x, B, C, 1)
+    num_seqs = _seqs(cu_seqlens, num_seqs)
+    if out is None:
+        out = torch.empty((total_T, H, P), dtype=x.dtype, device=x.device)
+    _same_dtype(dt, out=out)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((num_seqs, H, P, N), dtype=torch.float32, device=x.device)
+    st, L = num_seqs * H * P * N, lib()
+    p = _pointers(x, _SSM_NAMES, (a, A_log, dt_bias, D, cu_seqlens, initial_state, final_state, out),
+                  (total_T * H, H, H, H, num_seqs + 1, st, st, total_T * H * P), _SSM_FP32)
+    need = L.gdn_ssm_chunk_fwd_workspace_size(num_seqs, total_T, H, G, P, N, dt)
+    workspace, ws, ws_bytes = _workspace(workspace, need, x)
+    _check("gdn_ssm_chunk_fwd",
+           _run(x, L.gdn_ssm_chunk_fwd, *rows, *p[:5], num_seqs, total_T, H, G, P, N, dt, *p[5:], ws, ws_bytes,
+                _stream(None, x)))
+    return out, final_state
+
+
+@_on_stream
+def gdn_ssm_step(x, B, C, a, A_log, state, dt_bias=None, D=None, state_indices=None, out=None):
+    """T tokens of the scan for N sequences: x [N, T, H, P], B, C [N, T, G, N_state], a [N, T, H] (or without T, for one
+    token), state [slots, H, P, N_state] fp32 updated in place, state_indices int32 [N] (negative = skip) or None.
+    Returns out like x."""
+    x4, a3 = _tokens(x, 4, "x"), _tokens(a, 3, "a")
+    n_seq, T = x4.shape[:2]
+    H, P, G, N, dt, rows = _ssm_inputs(x4, _tokens(B, 4, "B"), _tokens(C, 4, "C"), 2)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _same_dtype(dt, out=out)
+    if state_indices is not None and state_indices.dtype != torch.int32:
+        raise TypeError("state_indices must be int32")
+    slots = state.shape[0]
+    p = _pointers(x, _SSM_STEP_NAMES, (a3, A_log, dt_bias, D, state, state_indices, out),
+                  (n_seq * T * H, H, H, H, slots * H * P * N, n_seq, n_seq * T * H * P), _SSM_STEP_FP32)
+    _check("gdn_ssm_step",
+           _run(x, lib().gdn_ssm_step, *rows, *p[:5], slots, p[5], n_seq, T, H, G, P, N, dt, p[6], _stream(None, x)))
+    return out
+
+
+@_on_stream
+def gdn_ssm_chunk_bwd(dout, x, B, C, a, A_log, dt_bias=None, D=None, cu_seqlens=None, num_seqs=None,
+                      initial_state=None, dfinal_state=None, output_dinitial_state=None, dx=None, dB=None, dC=None,
+                      da=None, dA_log=None, ddt_bias=None, dD=None, dinitial_state=None, workspace=None):
+    """Gradients of gdn_ssm_chunk_fwd: dout [total_T, H, P] in x's dtype, the forward's inputs, dfinal_state the
+    gradient of final_state (None: zeros).  Returns (dx, dB, dC, da, dA_log, ddt_bias, dD, dinitial_state): the first
+    three in x's dtype, the others fp32; ddt_bias (dD) is None unless it or dt_bias (D) is given, dinitial_state unless
+    it is given, requested, or (output_dinitial_state=None) an initial_state is.  Rows of tokens outside the sequences
+    of cu_seqlens are zeros when dx, dB, dC and da are all allocated here, and left as they were otherwise."""
+    total_T = x.shape[0]
+    H, P, G, N, dt, rows = _ssm_inputs(x, B, C, 1)
+    num_seqs = _seqs(cu_seqlens, num_seqs)
+    zeros = dx is None and dB is None and dC is None and da is None
+
+    def new(t, shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device=x.device) if t is None else t
+
+    dx, da = new(dx, (total_T, H, P), x.dtype), new(da, (total_T, H))
+    dB, dC = new(dB, (total_T, G, N), x.dtype), new(dC, (total_T, G, N), x.dtype)
+    _same_dtype(dt, dout=dout, dx=dx, dB=dB, dC=dC)
+    dA_log = new(dA_log, (H,))
+    if dt_bias is not None:
+        ddt_bias = new(ddt_bias, (H,))
+    if D is not None:
+        dD = new(dD, (H,))
+    if output_dinitial_state or (output_dinitial_state is None and initial_state is not None):
+        dinitial_state = new(dinitial_state, (num_seqs, H, P, N))
+    st, nx, nb, L = num_seqs * H * P * N, total_T * H * P, total_T * G * N, lib()
+    p = _pointers(x, _SSM_BWD_NAMES,
+                  (dout, a, A_log, dt_bias, D, cu_seqlens, initial_state, dfinal_state, dx, dB, dC, da, dA_log,
+                   ddt_bias, dD, dinitial_state),
+                  (nx, total_T * H, H, H, H, num_seqs + 1, st, st, nx, nb, nb, total_T * H, H, H, H, st),
+                  _SSM_BWD_FP32)
+    need = L.gdn_ssm_chunk_bwd_workspace_size(num_seqs, total_T, H, G, P, N, dt)
+    workspace, ws, ws_bytes = _workspace(workspace, need, x)
+    _check("gdn_ssm_chunk_bwd",
+           _run(x, L.gdn_ssm_chunk_bwd, p[0], *rows, *p[1:6], num_seqs, total_T, H, G, P, N, dt, *p[6:],
+                int(zeros), ws, ws_bytes, _stream(None, x)))
+    return dx, dB, dC, da, dA_log, ddt_bias, dD, dinitial_state
+
+
+def _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight, dq_weight=None, dk_weight=None):
+    T, H, d = q.shape
+    H_k, dt = (0 if k is None else k.shape[1]), _dt(q)
+    _same_dtype(dt, k=k)
+    max_positions, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if positions is not None and positions.dtype != torch.int32:
+        raise TypeError("positions must be int32")
+    p = _pointers(q, _QK_NAMES, (cos_sin, positions, q_weight, k_weight, dq_weight, dk_weight),
+                  (max_positions * rot, T, d, d, d, d), _QK_FP32)
+    rows = (*_rows(q, "q", q, (T, H, d)), *((None, 0) if k is None else _rows(q, "k", k, (T, H_k, d))))
+    return T, H, H_k, d, rot, dt, max_positions, p, rows
+
+
+@_on_stream
+def gdn_qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, norm=GDN_NORM_RMS, eps=1e-6,
+                     interleaved=False, q_out=None, k_out=None):
+    """Queries and keys normalised per head (GDN_NORM_RMS, or GDN_NORM_L2: to length one) and rotated by their
+    position: q [T, H, d], k [T, H_k, d] or None (fp32 or bf16; slices of a wider tensor are taken as they are), cos_sin
+    [max_positions, d_rot] fp32 (the cosines of a position's d_rot / 2 angles, then the sines; None: no rotation),
+    positions int32 [T] or None (row t has position t), weights [d] fp32 or None.  Pairs are channels i and
+    d_rot / 2 + i, or neighbours when interleaved.  Returns (q_out, k_out), allocated unless given (they may be q and k)."""
+    T, H, H_k, d, rot, dt, most, p, rows = _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight)
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty((T, H_k, d), dtype=q.dtype, device=q.device)
+    _same_dtype(dt, q_out=q_out, k_out=k_out)
+    outs = (*_rows(q, "q_out", q_out, (T, H, d)), *((None, 0) if k is None else _rows(q, "k_out", k_out, (T, H_k, d))))
+    _check("gdn_qk_norm_rope",
+           _run(q, lib().gdn_qk_norm_rope, *rows, p[0], p[1], most, p[2], p[3], int(norm), float(eps),
+                int(bool(interleaved)), T, H, H_k, d, rot, dt, *outs, _stream(None, q)))
+    return q_out, k_out
+
+
+@_on_stream
+def gdn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin, positions=None, q_weight=None, k_weight=None, norm=GDN_NORM_RMS,
+                         eps=1e-6, interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None):
+    """Gradients of gdn_qk_norm_rope: dq_out, dk_out (contiguous, in q's dtype) and the forward's inputs.  Returns
+    (dq, dk in q's dtype, dq_weight, dk_weight fp32); a weight's gradient is None unless it or the weight is given."""
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty_like(q_weight)
+    if k_weight is not None and dk_weight is None and k is not None:
+        dk_weight = torch.empty_like(k_weight)
+    T, H, H_k, d, rot, dt, most, p, rows = _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight, dq_weight, dk_weight)
+    if dq is None:
+        dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    if dk is None and k is not None:
+        dk = torch.empty((T, H_k, d), dtype=q.dtype, device=q.device)
+    _same_dtype(dt, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
+    g = _pointers(q, ("dq_out", "dk_out"), (dq_out, dk_out), (T * H * d, T * H_k * d), (False, False))
+    outs = (*_rows(q, "dq", dq, (T, H, d)), *((None, 0) if k is None else _rows(q, "dk", dk, (T, H_k, d))))
+    L = lib()
+    need = L.gdn_qk_norm_rope_bwd_workspace_size(T, H, H_k, d) if dq_weight is not None or dk_weight is not None else 0
+    workspace, ws, ws_bytes = _workspace(workspace, need, q)
+    _check("gdn_qk_norm_rope_bwd",
+           _run(q, L.gdn_qk_norm_rope_bwd, *g, *rows, p[0], p[1], most, p[2], p[3], int(norm), float(eps),
+                int(bool(interleaved)), T, H, H_k, d, rot, dt, *outs, p[4], p[5], ws, ws_bytes, _stream(None, q)))
+    return dq, dk, dq_weight, dk_weight
 
 
 def gdn_selftest_bounded_wait(limit_ns, status=None, stream=None):

@@ -5,7 +5,7 @@
 #include <mutex>
 
 #include "gdn_internal.cuh"
-#include "train_internal.cuh"
+#include "ssm_internal.cuh"
 
 namespace {
 
@@ -63,6 +63,7 @@ bool valid_form(int f) { return f == GDN_FORM_AUTO || f == GDN_FORM_OFF || f == 
 namespace gdn {
 int prefill_fused_form() { return g_prefill_fused_form.load(std::memory_order_relaxed); }
 int decode_blocks_form() { return g_decode_blocks_form.load(std::memory_order_relaxed); }
+int* device_error_word() { return device_error_ptr(); }
 }  // namespace gdn
 
 extern "C" {

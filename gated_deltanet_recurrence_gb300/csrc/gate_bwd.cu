@@ -20,7 +20,7 @@
 // the table and the second launch.
 #include <cooperative_groups.h>
 
-#include "train_internal.cuh"
+#include "ssm_internal.cuh"
 
 namespace gdn {
 namespace {
@@ -576,6 +576,11 @@ __global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs
 
 }  // namespace
 
+cudaError_t launch_column_sum(const float* table, long rows, long cols, float* out0, float* out1, cudaStream_t s) {
+    return launch_after(column_sum_kernel, dim3((unsigned)((cols + 31) / 32), out1 ? 2 : 1), kSumThreads, 0, s, table,
+                        rows, cols, out0, out1);
+}
+
 size_t norm_bwd_workspace_bytes(long rows, int groups, int size) {
     const NormPlan p = norm_plan(rows, groups, size, true, false);  // small calls do not use it
     return (size_t)p.prows * groups * size * 2 * sizeof(float);
@@ -591,8 +596,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t s) {
     cudaError_t e = launch_norm(a, p, true, s);
     if (e != cudaSuccess || !sums || p.cluster) return e;
     const long cols = (long)a.groups * a.size;
-    return launch_after(column_sum_kernel, dim3((unsigned)((cols + 31) / 32), a.db ? 2 : 1), kSumThreads, 0, s,
-                        a.partial, p.prows, cols, a.dw, a.db);
+    return launch_column_sum(a.partial, p.prows, cols, a.dw, a.db, s);
 }
 
 size_t gate_prep_bwd_workspace_bytes(long total_T, int H) {

@@ -1,0 +1,389 @@
+// short_conv.cu -- the causal short convolution as a call of its own: prompts, tokens and gradients.
+//
+// "5. 线性注意力", "因果卷积(Causal Conv1d)": four taps per channel and a SiLU,
+//   c_t = bias + sum_j w_j x_{t-3+j},   out_t = silu(c_t),
+// with the three inputs before a sequence's first token in its history.  Gradients: dc = dout silu'(c),
+//   dx_t = sum_j w_j dc_{t+3-j},  dw_j = sum_t dc_t x_{t-3+j},  dbias = sum_t dc_t.
+//
+// All are bound by memory: every input is read once and every output written once but for the three rows in
+// front of (and, for gradients, behind) the run of tokens that a thread walks along with the window of four
+// inputs in registers.  Arithmetic and sums are fp32; an output is rounded once, at its store.
+#include "ssm_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTaps = GDN_CONV_KERNEL;
+constexpr int kVec = 8;     // channels of a thread, forward
+constexpr int kVecB = 4;    // and in the backward pass, whose sums take 20 registers a channel quarter
+constexpr int kSMs = 152;
+
+__device__ __forceinline__ float silu_or(float c, int silu) { return silu ? c * sigmoidf_(c) : c; }
+
+// The input at position p (token index t0 + p of the batch) of a sequence whose first token is t0: its history
+// for p < 0, zeros without one.
+template <typename T, int VEC>
+__device__ __forceinline__ void input_at(const ShortConvArgs& a, int n, int bos, int p, int c0, float (&x)[VEC]) {
+    if (p >= 0) {
+        load_row<VEC>(static_cast<const T*>(a.x) + (long)(bos + p) * a.x_stride + c0, x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            x[j] = a.state_in ? a.state_in[((long)n * a.dim + c0 + j) * 3 + 3 + p] : 0.f;
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c0, float (&w)[VEC][kTaps], float (&b)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        load_vec<4>(a.w + (long)(c0 + j) * kTaps, w[j]);
+        b[j] = a.bias ? a.bias[c0 + j] : 0.f;
+    }
+}
+
+// The last three inputs of sequence n, for one vector of channels.
+template <typename T, int VEC>
+__device__ void final_history(const ShortConvArgs& a, int n, int bos, int len, int c0) {
+    float h[3][VEC];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) input_at<T, VEC>(a, n, bos, len - 3 + j, c0, h[j]);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) a.state_out[((long)n * a.dim + c0 + j) * 3 + k] = h[k][j];
+}
+
+// Blocks [0, runs * cols): one run of `run` tokens of kThreads channel vectors each; the blocks behind them write
+// the final histories (num_seqs * vectors threads).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ShortConvArgs a, int run, int cols, int runs) {
+    const int vecs = a.dim / kVec;
+    if (blockIdx.x >= (unsigned)(runs * cols)) {
+        if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+        const long q = (long)(blockIdx.x - runs * cols) * kThreads + threadIdx.x;
+        if (q >= (long)a.seqs.num_seqs * vecs) return;
+        const int n = (int)(q / vecs), bos = a.seqs.bos(n);
+        final_history<T, kVec>(a, n, bos, a.seqs.bos(n + 1) - bos, (int)(q % vecs) * kVec);
+        return;
+    }
+    const int col = blockIdx.x % cols;
+    // `cols` blocks cover the channel vectors, or, with few channels, one block covers several runs
+    const int per = cols > 1 ? 1 : kThreads / vecs;
+    const int v = cols > 1 ? col * kThreads + (int)threadIdx.x : (int)threadIdx.x % vecs;
+    const int first = (int)(blockIdx.x / cols) * per * run;
+    int n = packed_find(a.seqs, first, 1, 0, a.err);
+    if (n == -2) return;
+    int t = first + (cols > 1 ? 0 : (int)threadIdx.x / vecs * run);
+    if (v >= vecs || (cols == 1 && (int)threadIdx.x / vecs >= per)) return;
+    const int end = min(t + run, a.seqs.total_T), N = a.seqs.num_seqs;
+    if (n < 0) {  // tokens before the first sequence stay as they are
+        n = 0;
+        t = max(t, a.seqs.bos(0));
+    }
+    if (t >= end) return;
+    const int c0 = v * kVec;
+    float w[kVec][kTaps], b[kVec], h[3][kVec], x[kVec];
+    load_taps<kVec>(a, c0, w, b);
+    T* out = static_cast<T*>(a.out);
+    while (n < N && t < end) {
+        const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1);
+        if (t >= eos) { ++n; continue; }
+#pragma unroll
+        for (int j = 0; j < 3; ++j) input_at<T, kVec>(a, n, bos, t - bos - 3 + j, c0, h[j]);
+        const int stop = min(end, eos);
+        const T* src = static_cast<const T*>(a.x) + c0;
+#pragma unroll 4
+        for (; t < stop; ++t) {
+            load_row<kVec>(src + (long)t * a.x_stride, x);
+            float o[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[2][j], fmaf(w[j][1], h[1][j], fmaf(w[j][0], h[0][j], b[j]))));
+                o[j] = silu_or(c, a.silu);
+                h[0][j] = h[1][j];
+                h[1][j] = h[2][j];
+                h[2][j] = x[j];
+            }
+            store_row<kVec>(out + (long)t * a.dim + c0, o);
+        }
+    }
+}
+
+// One thread: four channels of one sequence, its history read, moved on by T tokens and written back.
+template <typename T>
+__global__ void __launch_bounds__(128) conv_step_kernel(ShortConvArgs a) {
+    const int vecs = a.dim / 4;
+    const long q = (long)blockIdx.x * 128 + threadIdx.x;
+    if (q >= (long)a.N * vecs) return;
+    const int n = (int)(q / vecs), c0 = (int)(q % vecs) * 4;
+    const int slot = a.idx ? a.idx[n] : n;
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        record_error(a.err, GDN_ERR_ARG);
+        return;
+    }
+    float4* st = reinterpret_cast<float4*>(a.pool + ((long)slot * a.dim + c0) * 3);
+    const T* src = static_cast<const T*>(a.x) + (long)n * a.T * a.x_stride + c0;
+    T* out = static_cast<T*>(a.out) + (long)n * a.T * a.dim + c0;
+    float w[4][kTaps], b[4], x[4], h[12];  // h: channel by channel, oldest first
+    load_row<4>(src, x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const float4 f = st[i];
+        h[4 * i] = f.x; h[4 * i + 1] = f.y; h[4 * i + 2] = f.z; h[4 * i + 3] = f.w;
+    }
+    load_taps<4>(a, c0, w, b);
+    for (int t = 0; t < a.T; ++t) {
+        float o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[3 * j + 2], fmaf(w[j][1], h[3 * j + 1], fmaf(w[j][0], h[3 * j], b[j]))));
+            o[j] = silu_or(c, a.silu);
+            h[3 * j] = h[3 * j + 1];
+            h[3 * j + 1] = h[3 * j + 2];
+            h[3 * j + 2] = x[j];
+        }
+        store_row<4>(out + (long)t * a.dim, o);
+        if (t + 1 < a.T) load_row<4>(src + (long)(t + 1) * a.x_stride, x);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) st[i] = make_float4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+}
+
+// dc of one token: the slope of the SiLU at c, times dout.
+__device__ __forceinline__ float dc_of(float c, float d, int silu) {
+    if (!silu) return d;
+    const float sg = sigmoidf_(c);
+    return d * sg * fmaf(c, 1.0f - sg, 1.0f);
+}
+
+// A block is 32 channel vectors (of four) x 8 runs of tokens; the sums over its runs are added in order and go to
+// row blockIdx.x of the table of partial sums [rows][dim * 4], with the biases' [rows][dim] behind it.  The blocks
+// with blockIdx.x = rows give the gradients of the carried histories, one thread per (sequence, vector).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int run, int rows) {
+    const int vecs = a.dim / kVecB;
+    const int v = blockIdx.y * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+    const int c0 = v * kVecB, N = a.seqs.num_seqs;
+    const bool on = v < vecs;
+    const T* src = static_cast<const T*>(a.x) + c0;
+    const T* dout = static_cast<const T*>(a.dout) + c0;
+    T* dx = static_cast<T*>(a.dx) + c0;
+    const bool state_block = (int)blockIdx.x == rows;
+    const int first = state_block ? 0 : (int)blockIdx.x * 8 * run;
+    int n = packed_find(a.seqs, first, 1, 0, a.err);
+    float w[kVecB][kTaps], b[kVecB];
+    float dw[kVecB][kTaps], db[kVecB];
+#pragma unroll
+    for (int j = 0; j < kVecB; ++j) {
+        db[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kTaps; ++i) dw[j][i] = 0.f;
+    }
+    if (on) load_taps<kVecB>(a, c0, w, b);
+    if (state_block) {
+        if (n == -2 || !on) return;
+        for (int m = k; m < N; m += 8) {
+            const int bos = a.seqs.bos(m), len = a.seqs.bos(m + 1) - bos;
+            float x[6][kVecB], g[3][kVecB];
+#pragma unroll
+            for (int p = 0; p < 6; ++p) {
+                if (p - 3 < len) input_at<T, kVecB>(a, m, bos, p - 3, c0, x[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {  // dc of the first three tokens
+#pragma unroll
+                for (int j = 0; j < kVecB; ++j) g[p][j] = 0.f;
+                if (p >= len) continue;
+                float d[kVecB];
+                load_row<kVecB>(dout + (long)(bos + p) * a.dim, d);
+#pragma unroll
+                for (int j = 0; j < kVecB; ++j) {
+                    const float c = fmaf(w[j][3], x[p + 3][j], fmaf(w[j][2], x[p + 2][j], fmaf(w[j][1], x[p + 1][j], fmaf(w[j][0], x[p][j], b[j]))));
+                    g[p][j] = dc_of(c, d[j], a.silu);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j) {
+                const long at = ((long)m * a.dim + c0 + j) * 3;
+                float o[3];
+                // position p - 3 meets token q through tap p - q (of the taps 0 .. 2)
+                o[0] = w[j][0] * g[0][j];
+                o[1] = fmaf(w[j][0], g[1][j], w[j][1] * g[0][j]);
+                o[2] = fmaf(w[j][0], g[2][j], fmaf(w[j][1], g[1][j], w[j][2] * g[0][j]));
+                float s[3] = {0.f, 0.f, 0.f};
+                if (a.dstate_out) {
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) s[p] = a.dstate_out[at + p];
+                }
+                // entry p of the final history is position len - 3 + p: a carried one where that is negative
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const int e = p - len;  // entry of the final history at position p - 3
+                    if (e >= 0) o[p] += e == 0 ? s[0] : (e == 1 ? s[1] : s[2]);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) a.dstate_in[at + p] = o[p];
+            }
+        }
+        return;
+    }
+    const bool sound = n != -2;  // without sound offsets nothing is written but zeros to the sums
+    int t = first + k * run;
+    const int end = min(t + run, a.seqs.total_T);
+    if (n < 0) n = sound ? 0 : N;
+    const int head = sound ? a.seqs.bos(0) : 0, tail = sound ? a.seqs.bos(N) : 0;
+    if (on && sound && a.zero_outside) {
+        const float zero[kVecB] = {};
+        for (int u = t; u < min(end, head); ++u) store_row<kVecB>(dx + (long)u * a.dim, zero);
+        for (int u = max(t, tail); u < end; ++u) store_row<kVecB>(dx + (long)u * a.dim, zero);
+    }
+    t = max(t, head);
+    while (on && n < N && t < end) {
+        const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1);
+        if (t >= eos) { ++n; continue; }
+        const int stop = min(end, eos);
+        float h[3][kVecB], g[3][kVecB];  // the inputs and the dc of the three tokens before
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            input_at<T, kVecB>(a, n, bos, t - bos - 3 + j, c0, h[j]);
+#pragma unroll
+            for (int i = 0; i < kVecB; ++i) g[j][i] = 0.f;
+        }
+        const int from = t;
+        // the three tokens behind the run give their dc to the run's last tokens
+#pragma unroll 2
+        for (; t < stop + 3; ++t) {
+            float x[kVecB], d[kVecB], o[kVecB];
+            const bool live = t < eos, mine = t < stop;
+            if (live) {
+                load_row<kVecB>(src + (long)t * a.x_stride, x);
+                load_row<kVecB>(dout + (long)t * a.dim, d);
+            }
+            const int u = t - 3;  // the token whose gradient is complete now
+            float s[kVecB];
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j) s[j] = 0.f;
+            if (a.dstate_out && u >= eos - 3 && u < eos) {
+#pragma unroll
+                for (int j = 0; j < kVecB; ++j) s[j] = a.dstate_out[((long)n * a.dim + c0 + j) * 3 + u - (eos - 3)];
+            }
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j) {
+                float gc = 0.f;
+                if (live) {
+                    const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[2][j], fmaf(w[j][1], h[1][j], fmaf(w[j][0], h[0][j], b[j]))));
+                    gc = dc_of(c, d[j], a.silu);
+                    if (mine) {
+                        dw[j][0] = fmaf(gc, h[0][j], dw[j][0]);
+                        dw[j][1] = fmaf(gc, h[1][j], dw[j][1]);
+                        dw[j][2] = fmaf(gc, h[2][j], dw[j][2]);
+                        dw[j][3] = fmaf(gc, x[j], dw[j][3]);
+                        db[j] += gc;
+                    }
+                }
+                o[j] = fmaf(w[j][0], gc, fmaf(w[j][1], g[2][j], fmaf(w[j][2], g[1][j], fmaf(w[j][3], g[0][j], s[j]))));
+                g[0][j] = g[1][j];
+                g[1][j] = g[2][j];
+                g[2][j] = gc;
+                h[0][j] = h[1][j];
+                h[1][j] = h[2][j];
+                h[2][j] = live ? x[j] : 0.f;
+            }
+            if (u >= from) store_row<kVecB>(dx + (long)u * a.dim, o);
+        }
+        t = stop;
+    }
+    if (!a.partial) return;
+    __shared__ float sh[8][32][kVecB * 5 + 1];
+#pragma unroll
+    for (int j = 0; j < kVecB; ++j) {
+#pragma unroll
+        for (int i = 0; i < kTaps; ++i) sh[k][threadIdx.x & 31][j * kTaps + i] = dw[j][i];
+        sh[k][threadIdx.x & 31][kVecB * kTaps + j] = db[j];
+    }
+    __syncthreads();
+    float* pw = a.partial + (long)blockIdx.x * a.dim * kTaps;
+    float* pb = a.partial + (long)rows * a.dim * kTaps + (long)blockIdx.x * a.dim;
+    for (int i = threadIdx.x; i < 32 * kVecB * 5; i += kThreads) {
+        const int l = i / (kVecB * 5), e = i % (kVecB * 5), vv = blockIdx.y * 32 + l;
+        if (vv >= vecs) break;
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s += sh[r][l][e];
+        if (e < kVecB * kTaps) pw[(long)vv * kVecB * kTaps + e] = s;
+        else pb[(long)vv * kVecB + e - kVecB * kTaps] = s;
+    }
+}
+
+// Tokens a thread walks: long runs re-read few rows, short ones give enough threads to a small call.
+int run_length(long total_T, long vecs, int least, int most) {
+    long run = total_T * vecs / (kSMs * 4L * kThreads);
+    run = run < least ? least : (run > most ? most : run);
+    return (int)run;
+}
+
+}  // namespace
+
+cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
+    const int vecs = a.dim / kVec;
+    const int cols = vecs > kThreads ? (vecs + kThreads - 1) / kThreads : 1;
+    const int per = cols > 1 ? 1 : kThreads / vecs;
+    const int run = run_length(a.seqs.total_T, vecs, 4, 16);
+    const int runs = (int)(((long)a.seqs.total_T + (long)per * run - 1) / ((long)per * run));
+    const long tail = a.state_out ? ((long)a.seqs.num_seqs * vecs + kThreads - 1) / kThreads : 0;
+    const auto kernel = a.dtype == GDN_BF16 ? conv_fwd_kernel<__nv_bfloat16> : conv_fwd_kernel<float>;
+    // histories that are carried in place are written behind everything that reads them
+    const bool apart = a.state_out && a.state_out == a.state_in;
+    if ((long)runs * cols + tail > 0x7fffffffL) return cudaErrorInvalidValue;
+    if (runs > 0 || (tail > 0 && !apart)) {
+        kernel<<<(unsigned)((long)runs * cols + (apart ? 0 : tail)), kThreads, 0, s>>>(a, run, cols, runs);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (apart) {
+        kernel<<<(unsigned)tail, kThreads, 0, s>>>(a, run, cols, 0);
+        return cudaGetLastError();
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_short_conv_step(const ShortConvArgs& a, cudaStream_t s) {
+    const long blocks = ((long)a.N * (a.dim / 4) + 127) / 128;
+    if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
+    if (a.dtype == GDN_BF16) conv_step_kernel<__nv_bfloat16><<<(unsigned)blocks, 128, 0, s>>>(a);
+    else conv_step_kernel<float><<<(unsigned)blocks, 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+static void bwd_plan(int total_T, int dim, int& run, int& rows) {
+    run = run_length(total_T, dim / kVecB, 8, 32);
+    rows = (int)(((long)total_T + 8L * run - 1) / (8L * run));
+}
+
+size_t short_conv_bwd_workspace_bytes(int total_T, int dim) {
+    int run, rows;
+    bwd_plan(total_T, dim, run, rows);
+    return (size_t)rows * dim * 5 * sizeof(float);
+}
+
+cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s) {
+    int run, rows;
+    bwd_plan(a.seqs.total_T, a.dim, run, rows);
+    const dim3 grid((unsigned)(rows + (a.dstate_in ? 1 : 0)), (unsigned)((a.dim / kVecB + 31) / 32));
+    if (grid.x > 0) {
+        if (a.dtype == GDN_BF16) conv_bwd_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a, run, rows);
+        else conv_bwd_kernel<float><<<grid, kThreads, 0, s>>>(a, run, rows);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = cudaSuccess;
+    if (a.dw) e = launch_column_sum(a.partial, rows, (long)a.dim * kTaps, a.dw, nullptr, s);
+    if (e == cudaSuccess && a.dbias)
+        e = launch_column_sum(a.partial + (long)rows * a.dim * kTaps, rows, a.dim, a.dbias, nullptr, s);
+    return e;
+}
+
+}  // namespace gdn

@@ -1,0 +1,438 @@
+// ssm_bwd.cu -- the gradients of the selective state space scan.
+//
+// Inside a chunk, with v = dt x, b_i = e^{G_i}, r_j = e^{G_last - G_j}, S_0 the state at its start and dS_1 the
+// gradient of the state at its end, and for j <= i
+//   M_ij = e^{G_i - G_j} C_i . B_j,   E_ij = e^{G_i - G_j} dy_i . v_j,   T_ij = M_ij dy_i . v_j:
+//   dv_j = sum_i M_ij dy_i + r_j dS_1 B_j,
+//   dC_i = sum_j E_ij B_j + b_i S_0^T dy_i,        dB_j = sum_i E_ij C_i + r_j dS_1^T v_j,
+//   dS_0 = b_last dS_1 + sum_i b_i dy_i C_i^T,
+//   dG_i = sum_{j < i} T_ij - sum_{m > i} T_mi + b_i dy_i . S_0 C_i - r_i v_i . dS_1 B_i,
+//   dg_t = sum_{i >= t} dG_i + b_last <dS_1, S_0> + sum_j r_j v_j . dS_1 B_j
+// (the diagonal of T leaves dG), and with z = a + dt_bias, rate = exp(A_log):
+//   ddt = dv . x - rate dg,  da = ddt sigmoid(z),  dx = dt dv + D dy,
+//   dA_log = sum dg g,  ddt_bias = sum da,  dD = sum dy . x.
+// The states and their gradients come from the scan kernels of the forward pass, run in both directions.  The
+// gradient kernel's block takes one chunk and a subset of the heads of one group, so that C B^T is formed once and
+// dB, dC of the group's heads are summed before they are written.
+#include "ssm_chunk.cuh"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+// 16 warps: warp w holds rows 16 (w % 4) .. and a quarter of the columns.
+template <typename T, int N>
+struct Smem {
+    static constexpr int PX = bfp::kPlanes<T>;
+    static constexpr int k = 0, c = k + bfp::kTileBytes<kC, N, PX>, x = c + bfp::kTileBytes<kC, N, PX>,
+                         y = x + bfp::kTileBytes<kC, 64, PX>, s = y + bfp::kTileBytes<kC, 64, PX>,
+                         m = s + bfp::kTileBytes<64, N, 3>, bytes = m + bfp::kTileBytes<kC, 64, 3>;
+};
+
+// Sums over the four lanes that share a row of an accumulator.
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
+    using L = Smem<T, N>;
+    constexpr int PX = L::PX, NT = N / 32;  // NT: 8-column tiles of a warp in a 64 x N result
+    constexpr int KV = kC * N / 8 / kThreads;  // vectors of a 64 x N tile a thread loads
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const bfp::Tile<kC, N, PX> Kt{base + L::k}, Ct{base + L::c};
+    const bfp::Tile<kC, 64, PX> Xt{base + L::x}, Yt{base + L::y};
+    const bfp::Tile<64, N, 3> St{base + L::s};
+    const bfp::Tile<kC, 64, 3> Mt{base + L::m};
+    __shared__ float gate[kGateRows][kC];
+    __shared__ float rowT[4][kC], colT[4][kC], in1[4][kC], in2[4][kC], ddt4[4][kC];  // by column (row) of warps
+    __shared__ float part[2][kWarps];  // <dS, S0>, dD
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = blockIdx.y % a.G, subset = blockIdx.y / a.G, per = a.H / a.G;
+    const int lo = per * subset / w.subsets, hi = per * (subset + 1) / w.subsets;
+    Chunk c;
+    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) {
+        const long all = (long)gridDim.x * a.H;
+        for (int i = tid; i < hi - lo; i += kThreads) {
+            const long at = (long)blockIdx.x * a.H + g * per + lo + i;
+            w.sums[at] = w.sums[all + at] = w.sums[2 * all + at] = 0.f;
+        }
+        return;
+    }
+    const int m = (warp & 3) * 16, cw = warp >> 2, n0 = cw * (N / 4), p0 = cw * 16;
+    {
+        const T* B = static_cast<const T*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
+        const T* C = static_cast<const T*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
+#pragma unroll
+        for (int i = 0; i < KV; ++i) {
+            const int v = i * kThreads + tid, r = v / (N / 8), col = v % (N / 8) * 8;
+            bfp::Raw8<T> k, q;
+            k.load(B + (long)r * a.B_stride + col, r < c.len);
+            q.load(C + (long)r * a.C_stride + col, r < c.len);
+            k.put(Kt, r, col);
+            q.put(Ct, r, col);
+        }
+    }
+    __syncthreads();
+    float CK[2][4], Es[2][4], dB[NT][4], dC[NT][4];
+    bfp::clear(CK);
+    bfp::clear(Es);
+    bfp::clear(dB);
+    bfp::clear(dC);
+    bfp::product<N, false, false>(CK, Ct, m, Kt, p0, lane);
+    const int slices = a.P / 64;
+    for (int h = g * per + lo; h < g * per + hi; ++h) {
+        const long sh = (long)blockIdx.x * a.H + h;
+        const float D = a.D ? a.D[h] : 0.f;
+        float E[2][4];
+        bfp::clear(E);
+        float ss = 0.f, sd = 0.f;
+        for (int s = 0; s < slices; ++s) {
+            __syncthreads();  // what was in the tiles and sums has been read
+            if (s == 0) {
+                for (int i = tid; i < kGateRows * kC; i += kThreads)
+                    (&gate[0][0])[i] = w.gates[sh * (kGateRows * kC) + i];
+            }
+            {
+                const int r = tid / 8, col = tid % 8 * 8;
+                const long ch = (long)h * a.P + s * 64 + col;
+                bfp::Raw8<T> x, y;
+                x.load(static_cast<const T*>(a.x) + (long)(c.t0 + r) * a.x_stride + ch, r < c.len);
+                y.load(static_cast<const T*>(a.dout) + (long)(c.t0 + r) * a.H * a.P + ch, r < c.len);
+                x.put(Xt, r, col);
+                y.put(Yt, r, col);
+            }
+            const float* S0 = w.states + (sh * a.P + s * 64) * N;
+            const float* S1 = w.dstates + (sh * a.P + s * 64) * N;
+#pragma unroll
+            for (int i = 0; i < KV; ++i) {
+                const int v = i * kThreads + tid, r = v / (N / 8), col = v % (N / 8) * 8;
+                float x[8], z[8];
+                load_row<8>(S1 + (long)r * N + col, x);
+                load_row<8>(S0 + (long)r * N + col, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], z[e], ss);
+                bfp::put8(St, r, col, x);
+            }
+            __syncthreads();
+            if (s == 0) {
+                bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int t) {
+                    float v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float d = (gate[1][i] - gate[1][t + e]) + (gate[2][i] - gate[2][t + e]);
+                        v[e] = t + e <= i ? CK[j][2 * hh + e] * expf(d) : 0.f;
+                    }
+                    bfp::put2(Mt, i, t, v[0], v[1]);
+                });
+            }
+            bfp::product<64, false, false>(E, Yt, m, Xt, p0, lane);
+            // dB: rows r_j dt_j times x dS
+            {
+                float acc[NT][4];
+                bfp::clear(acc);
+                bfp::product<64, false, true>(acc, Xt, m, St, n0, lane);
+                bfp::pairs<NT>(m, n0, lane, [&](int j, int hh, int i, int) {
+                    const float f = gate[0][i] * gate[4][i];
+                    dB[j][2 * hh] = fmaf(f, acc[j][2 * hh], dB[j][2 * hh]);
+                    dB[j][2 * hh + 1] = fmaf(f, acc[j][2 * hh + 1], dB[j][2 * hh + 1]);
+                });
+            }
+            __syncthreads();  // M is in place
+            // dv: B dS^T and M^T dy
+            {
+                float acc[2][4], q2[2] = {0.f, 0.f}, qd[2] = {0.f, 0.f};
+                bfp::clear(acc);
+                bfp::product<N, false, false>(acc, Kt, m, St, p0, lane);
+                bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int p) {
+                    const float2 x = bfp::get2(Xt, i, p);
+                    acc[j][2 * hh] *= gate[4][i];
+                    acc[j][2 * hh + 1] *= gate[4][i];
+                    q2[hh] = fmaf(acc[j][2 * hh], x.x, fmaf(acc[j][2 * hh + 1], x.y, q2[hh]));
+                });
+                bfp::product<kC, true, true, bfp::kUpper>(acc, Mt, m, Yt, p0, lane);
+                T* dx = static_cast<T*>(a.dx) + ((long)c.t0 * a.H + h) * a.P + s * 64;
+                bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int p) {
+                    const float2 x = bfp::get2(Xt, i, p), y = bfp::get2(Yt, i, p);
+                    const float v0 = acc[j][2 * hh], v1 = acc[j][2 * hh + 1];
+                    qd[hh] = fmaf(v0, x.x, fmaf(v1, x.y, qd[hh]));
+                    sd = fmaf(y.x, x.x, fmaf(y.y, x.y, sd));
+                    const float o0 = fmaf(gate[0][i], v0, D * y.x), o1 = fmaf(gate[0][i], v1, D * y.y);
+                    if (i < c.len) {
+                        T* o = dx + (long)i * a.H * a.P + p;
+                        if constexpr (PX == 1) *reinterpret_cast<uint32_t*>(o) = pack_bf16(o0, o1);
+                        else *reinterpret_cast<float2*>(o) = make_float2(o0, o1);
+                    }
+                });
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float u = quad_sum(q2[hh]), v = quad_sum(qd[hh]);
+                    const int i = m + (lane >> 2) + 8 * hh;
+                    if ((lane & 3) == 0) {  // one warp a row and quarter: plain read and write
+                        in2[cw][i] = (s ? in2[cw][i] : 0.f) + gate[0][i] * u;
+                        ddt4[cw][i] = (s ? ddt4[cw][i] : 0.f) + v;
+                    }
+                }
+            }
+            __syncthreads();  // dS has been read: S0 takes its place
+#pragma unroll
+            for (int i = 0; i < KV; ++i) {
+                const int v = i * kThreads + tid, r = v / (N / 8), col = v % (N / 8) * 8;
+                float z[8];
+                load_row<8>(S0 + (long)r * N + col, z);
+                bfp::put8(St, r, col, z);
+            }
+            __syncthreads();
+            {
+                float acc[NT][4], q1[2] = {0.f, 0.f};
+                bfp::clear(acc);
+                bfp::product<64, false, true>(acc, Yt, m, St, n0, lane);
+                bfp::pairs<NT>(m, n0, lane, [&](int j, int hh, int i, int n) {
+                    const float2 q = bfp::get2(Ct, i, n);
+                    const float u = gate[3][i] * acc[j][2 * hh], v = gate[3][i] * acc[j][2 * hh + 1];
+                    q1[hh] = fmaf(u, q.x, fmaf(v, q.y, q1[hh]));
+                    dC[j][2 * hh] += u;
+                    dC[j][2 * hh + 1] += v;
+                });
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const float u = quad_sum(q1[hh]);
+                    const int i = m + (lane >> 2) + 8 * hh;
+                    if ((lane & 3) == 0) in1[cw][i] = (s ? in1[cw][i] : 0.f) + u;
+                }
+            }
+        }
+        // E, T and the sums of T's rows and columns below the diagonal
+        {
+            float rows[2] = {0.f, 0.f}, cols[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+            bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int t) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float d = (gate[1][i] - gate[1][t + e]) + (gate[2][i] - gate[2][t + e]);
+                    const float v = t + e <= i ? E[j][2 * hh + e] * (gate[0][t + e] * expf(d)) : 0.f;
+                    Es[j][2 * hh + e] += v;
+                    const float q = t + e < i ? v * CK[j][2 * hh + e] : 0.f;
+                    rows[hh] += q;
+                    cols[j][e] += q;
+                }
+            });
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const float u = quad_sum(rows[hh]);
+                if ((lane & 3) == 0) rowT[cw][m + (lane >> 2) + 8 * hh] = u;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float u = cols[j][e];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+                    if (lane < 4) colT[warp & 3][p0 + 8 * j + 2 * lane + e] = u;
+                }
+            ss = warp_sum(ss);
+            sd = warp_sum(sd);
+            if (lane == 0) {
+                part[0][warp] = ss;
+                part[1][warp] = sd;
+            }
+        }
+        __syncthreads();
+        // warp 0: the chunk's tokens, two a lane
+        if (warp == 0) {
+            float dot = lane < kWarps ? part[0][lane] : 0.f, dD = lane < kWarps ? part[1][lane] : 0.f;
+            dot = warp_sum(dot) * gate[3][kC - 1];
+            dD = warp_sum(dD);
+            float own[2], ddt[2], tot2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                float r = 0.f, q = 0.f, u1 = 0.f, u2 = 0.f;
+                ddt[e] = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    r += rowT[x][i];
+                    q += colT[x][i];
+                    u1 += in1[x][i];
+                    u2 += in2[x][i];
+                    ddt[e] += ddt4[x][i];
+                }
+                own[e] = (r - q) + (u1 - u2);
+                tot2 += u2;
+            }
+            dot += warp_sum(tot2);
+            float suf = own[0] + own[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float down = __shfl_down_sync(0xffffffffu, suf, o);
+                if (lane + o < 32) suf += down;
+            }
+            float behind = __shfl_down_sync(0xffffffffu, suf, 1);
+            if (lane == 31) behind = 0.f;
+            const float dg[2] = {suf + dot, behind + own[1] + dot};
+            const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+            float sA = 0.f, sb = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                if (i >= c.len) continue;
+                const long at = (long)(c.t0 + i) * a.H + h;
+                const float gi = -rate * gate[0][i];
+                const float da = fmaf(-rate, dg[e], ddt[e]) * sigmoidf_(a.a[at] + bias);
+                a.da[at] = da;
+                sA = fmaf(dg[e], gi, sA);
+                sb += da;
+            }
+            sA = warp_sum(sA);
+            sb = warp_sum(sb);
+            if (lane == 0) {
+                const long all = (long)gridDim.x * a.H;
+                w.sums[sh] = sA;
+                w.sums[all + sh] = sb;
+                w.sums[2 * all + sh] = dD;
+            }
+        }
+    }
+    __syncthreads();
+    bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int t) { bfp::put2(Mt, i, t, Es[j][2 * hh], Es[j][2 * hh + 1]); });
+    __syncthreads();
+    bfp::product<kC, false, true, bfp::kLower>(dC, Mt, m, Kt, n0, lane);
+    bfp::product<kC, true, true, bfp::kUpper>(dB, Mt, m, Ct, n0, lane);
+    bfp::pairs<NT>(m, n0, lane, [&](int j, int hh, int i, int n) {
+        if (i >= c.len) return;
+        const long at = ((long)(c.t0 + i) * a.G + g) * N + n;
+        const float2 vb = make_float2(dB[j][2 * hh], dB[j][2 * hh + 1]), vc = make_float2(dC[j][2 * hh], dC[j][2 * hh + 1]);
+        if (w.subsets > 1) {
+            const long all = (long)a.seqs.total_T * a.G * N;
+            *reinterpret_cast<float2*>(w.parts + subset * all + at) = vb;
+            *reinterpret_cast<float2*>(w.parts + (w.subsets + subset) * all + at) = vc;
+        } else if constexpr (PX == 1) {
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.dB) + at) = pack_bf16(vb.x, vb.y);
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.dC) + at) = pack_bf16(vc.x, vc.y);
+        } else {
+            *reinterpret_cast<float2*>(static_cast<T*>(a.dB) + at) = vb;
+            *reinterpret_cast<float2*>(static_cast<T*>(a.dC) + at) = vc;
+        }
+    });
+}
+
+// What is left: the subsets' dB and dC added up in order, zeros for tokens outside every sequence where they are
+// asked for.  One thread: eight elements of dB or dC (y = 0, 1), or of dx and da (y = 2).
+template <typename T>
+__global__ void __launch_bounds__(256) ssm_finish_kernel(SsmArgs a, Work w, long elems) {
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    const long first = a.seqs.cu ? a.seqs.bos(0) : 0, end = a.seqs.cu ? a.seqs.bos(a.seqs.num_seqs) : a.seqs.total_T;
+    const long at = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
+    const float zero[8] = {};
+    if (blockIdx.y < 2) {
+        if (at >= elems) return;
+        T* out = static_cast<T*>(blockIdx.y ? a.dC : a.dB) + at;
+        const long t = at / ((long)a.G * a.N);
+        if (t < first || t >= end) {
+            if (a.zero_outside) store_row<8>(out, zero);
+            return;
+        }
+        if (w.subsets == 1) return;
+        const float* p = w.parts + (blockIdx.y ? w.subsets * elems : 0) + at;
+        float x[8] = {};
+        for (int s = 0; s < w.subsets; ++s) {
+            float y[8];
+            load_row<8>(p + s * elems, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += y[e];
+        }
+        store_row<8>(out, x);
+        return;
+    }
+    if (!a.zero_outside) return;
+    // dx, da: few rows as a rule, walked by all threads
+    const long rows = first + (a.seqs.total_T - end), width = (long)a.H * a.P / 8;
+    const long stride = (long)gridDim.x * 256, q0 = (long)blockIdx.x * 256 + threadIdx.x;
+    for (long q = q0; q < rows * width; q += stride) {
+        const long r = q / width, t = r < first ? r : end + (r - first);
+        store_row<8>(static_cast<T*>(a.dx) + (t * width + q % width) * 8, zero);
+    }
+    for (long q = q0; q < rows * a.H; q += stride) {
+        const long r = q / a.H, t = r < first ? r : end + (r - first);
+        a.da[t * a.H + q % a.H] = 0.f;
+    }
+}
+
+template <typename T, int N>
+cudaError_t grad_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
+    const auto kernel = ssm_grad_kernel<T, N>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<T, N>::bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)(a.G * w.subsets));
+    kernel<<<grid, kThreads, Smem<T, N>::bytes, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+// Subsets of a group's heads: as many blocks as the SMs take in a few rounds, at least two heads a block where the
+// group has them (each subset writes its dB and dC in fp32 for another kernel to add).
+int subsets_of(int num_seqs, int total_T, int H, int G) {
+    const long blocks = slots_of(num_seqs, total_T) * G, per = H / G;
+    long n = (3 * 152 + blocks - 1) / blocks;
+    const long most = per > 1 ? per / 2 : 1;
+    n = n > most ? most : n;
+    return (int)(n < 1 ? 1 : n);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, unsigned char* at) {
+    const size_t slots = (size_t)slots_of(num_seqs, total_T);
+    const size_t gates = align256(slots * H * kGateRows * kC * sizeof(float));
+    const size_t states = align256(slots * H * P * N * sizeof(float)), sums = align256(slots * H * 3 * sizeof(float));
+    const int subsets = subsets_of(num_seqs, total_T, H, G);
+    const size_t parts = subsets > 1 ? (size_t)subsets * 2 * total_T * G * N * sizeof(float) : 0;
+    if (w) {
+        w->gates = reinterpret_cast<float*>(at);
+        w->states = reinterpret_cast<float*>(at + gates);
+        w->dstates = reinterpret_cast<float*>(at + gates + states);
+        w->sums = reinterpret_cast<float*>(at + gates + 2 * states);
+        w->parts = reinterpret_cast<float*>(at + gates + 2 * states + sums);
+        w->subsets = subsets;
+    }
+    return gates + 2 * states + sums + parts;
+}
+
+}  // namespace
+}  // namespace ssm
+
+size_t ssm_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype) {
+    return ssm::layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
+}
+
+cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
+    ssm::Work w{};
+    ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
+    cudaError_t e = ssm::launch_gates(a, w, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
+    if (e != cudaSuccess) return e;
+    const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
+    if (a.dtype == GDN_BF16) e = a.N == 128 ? ssm::grad_one<__nv_bfloat16, 128>(a, w, s) : ssm::grad_one<__nv_bfloat16, 64>(a, w, s);
+    else e = a.N == 128 ? ssm::grad_one<float, 128>(a, w, s) : ssm::grad_one<float, 64>(a, w, s);
+    if (e != cudaSuccess) return e;
+    const bool zeros = a.zero_outside && a.seqs.cu;
+    if (a.seqs.total_T > 0 && (w.subsets > 1 || zeros)) {
+        const long elems = (long)a.seqs.total_T * a.G * a.N;
+        const dim3 grid((unsigned)((elems / 8 + 255) / 256), zeros ? 3 : 2);
+        if (a.dtype == GDN_BF16) ssm::ssm_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, w, elems);
+        else ssm::ssm_finish_kernel<float><<<grid, 256, 0, s>>>(a, w, elems);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const long all = slots * a.H;
+    if (a.dA_log || a.ddt_bias) e = launch_column_sum(w.sums, slots, a.H, a.dA_log, a.ddt_bias, s);
+    if (e == cudaSuccess && a.dD) e = launch_column_sum(w.sums + 2 * all, slots, a.H, a.dD, nullptr, s);
+    return e;
+}
+
+}  // namespace gdn

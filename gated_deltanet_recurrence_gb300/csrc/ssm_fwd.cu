@@ -1,0 +1,318 @@
+// ssm_fwd.cu -- the selective state space scan over packed prompts, in chunks of 64 tokens.
+//
+// Per head, with v_t = dt_t x_t and G the running sums of the log decays g_t = -exp(A_log) dt_t inside a chunk,
+//   y_i = e^{G_i} S_0 C_i + sum_{j <= i} e^{G_i - G_j} (B_j . C_i) v_j + D x_i,
+//   S_1 = e^{G_last} S_0 + sum_j e^{G_last - G_j} v_j B_j^T.
+// Three kernels: the gates of all chunks; the states at the chunk starts, one block per (sequence, head, 64 rows)
+// that walks along its chunks with the state in registers; the outputs, one block per (chunk, head, 64 rows).
+#include "ssm_chunk.cuh"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+// ---- gates ---------------------------------------------------------------------------------------
+
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+    const float s = a.h + b.h, z = s - a.h;
+    const float e = (a.h - (s - z)) + (b.h - z) + (a.l + b.l);
+    Two r;
+    r.h = s + e;
+    r.l = e - (r.h - s);
+    return r;
+}
+
+// One warp per (slot, head): lane l holds tokens 2 l and 2 l + 1.
+constexpr int kGateWarps = 8;
+__global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, float* gates) {
+    Chunk c;
+    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) return;
+    const int lane = threadIdx.x & 31;
+    const int h = blockIdx.y * kGateWarps + (threadIdx.x >> 5);
+    if (h >= a.H) return;
+    const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    float dt[2], g[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        dt[i] = t < c.len ? ssm_softplus(a.a[(long)(c.t0 + t) * a.H + h] + bias) : 0.f;
+        g[i] = t < c.len ? fmaxf(-rate * dt[i], kMinLog) : 0.f;
+    }
+    Two pair = two_add(Two{g[0], 0.f}, Two{g[1], 0.f}), sum = pair;
+    float suf = g[0] + g[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Two up{__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+        if (lane >= o) sum = two_add(up, sum);
+        const float down = __shfl_down_sync(0xffffffffu, suf, o);
+        if (lane + o < 32) suf += down;
+    }
+    // sums before this lane's tokens, and behind them
+    Two before{__shfl_up_sync(0xffffffffu, sum.h, 1), __shfl_up_sync(0xffffffffu, sum.l, 1)};
+    if (lane == 0) before = Two{0.f, 0.f};
+    float behind = __shfl_down_sync(0xffffffffu, suf, 1);
+    if (lane == 31) behind = 0.f;
+    const Two G0 = two_add(before, Two{g[0], 0.f});
+    float* out = gates + ((long)blockIdx.x * a.H + h) * (kGateRows * kC) + 2 * lane;
+    *reinterpret_cast<float2*>(out) = make_float2(dt[0], dt[1]);
+    *reinterpret_cast<float2*>(out + kC) = make_float2(G0.h, sum.h);
+    *reinterpret_cast<float2*>(out + 2 * kC) = make_float2(G0.l, sum.l);
+    *reinterpret_cast<float2*>(out + 3 * kC) = make_float2(expf(G0.h) * (1.f + G0.l), expf(sum.h) * (1.f + sum.l));
+    *reinterpret_cast<float2*>(out + 4 * kC) = make_float2(expf(behind + g[1]), expf(behind));
+}
+
+// ---- states --------------------------------------------------------------------------------------
+
+// Block: 8 warps; warp w holds rows 16 (w % 4) .. of the 64 and half of the N columns.  REV: the states' gradients,
+// from the last chunk to the first.
+constexpr int kScanThreads = 256;
+template <typename T, int N, bool REV>
+__global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work w) {
+    constexpr int PX = bfp::kPlanes<T>, NT = N / 16, KV = N / 32;  // KV: vectors of B a thread loads
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const bfp::Tile<kC, N, PX> Kt{base};
+    const bfp::Tile<kC, 64, 3> Vt{base + bfp::kTileBytes<kC, N, PX>};
+    __shared__ float fac[kC];
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
+    const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kC - 1) / kC;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m0 = (warp & 3) * 16, n0 = (warp >> 2) * (N / 2);
+    const int g = h / (a.H / a.G);
+    const T* K = static_cast<const T*>(REV ? a.C : a.B) + (long)g * N;
+    const long k_stride = REV ? a.C_stride : a.B_stride;
+    const T* X = static_cast<const T*>(REV ? a.dout : a.x) + (long)h * a.P + s * 64;
+    const long x_stride = REV ? (long)a.H * a.P : a.x_stride;
+    const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
+    const float* init = REV ? a.dfinal_state : a.initial_state;
+    float* last = REV ? a.dinitial_state : a.final_state;
+    float* keep = REV ? w.dstates : w.states;
+
+    float S[NT][4];
+    bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
+        const float2 v = init ? *reinterpret_cast<const float2*>(init + row0 + (long)p * N + c) : make_float2(0.f, 0.f);
+        S[j][2 * hh] = v.x;
+        S[j][2 * hh + 1] = v.y;
+    });
+    bfp::Raw8<T> kr[KV], xr[2];
+    float gd = 0.f, gb = 0.f, gl = 0.f;  // this thread's token: dt, the chunk factor; the whole chunk's decay
+    const auto fetch = [&](int k) {
+        const int t0 = bos + k * kC, len = min(eos - t0, kC);
+#pragma unroll
+        for (int i = 0; i < KV; ++i) {
+            const int v = i * kScanThreads + tid, r = v / (N / 8), c = v % (N / 8) * 8;
+            kr[i].load(K + (long)(t0 + r) * k_stride + c, r < len);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = i * kScanThreads + tid, r = v / 8, c = v % 8 * 8;
+            xr[i].load(X + (long)(t0 + r) * x_stride + c, r < len);
+        }
+        const float* gt = w.gates + ((long)(bos / kC + n + k) * a.H + h) * (kGateRows * kC);
+        if (tid < kC) {
+            gd = REV ? 1.f : gt[tid];
+            gb = gt[(REV ? 3 : 4) * kC + tid];
+        }
+        gl = gt[3 * kC + kC - 1];
+    };
+    if (chunks > 0) fetch(REV ? chunks - 1 : 0);
+    for (int q = 0; q < chunks; ++q) {
+        const int k = REV ? chunks - 1 - q : q;
+        const float decay = gl;
+        if (tid < kC) fac[tid] = gd * gb;
+#pragma unroll
+        for (int i = 0; i < KV; ++i) {
+            const int v = i * kScanThreads + tid;
+            kr[i].put(Kt, v / (N / 8), v % (N / 8) * 8);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = i * kScanThreads + tid, r = v / 8;
+            float x[8];
+            xr[i].get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= fac[r];
+            bfp::put8(Vt, r, v % 8 * 8, x);
+        }
+        float* to = keep + (((long)(bos / kC + n + k) * a.H + h) * a.P + s * 64) * N;
+        bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
+            *reinterpret_cast<float2*>(to + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
+            S[j][2 * hh] *= decay;
+            S[j][2 * hh + 1] *= decay;
+        });
+        if (q + 1 < chunks) fetch(REV ? k - 1 : k + 1);
+        __syncthreads();
+        bfp::product<kC, true, true>(S, Vt, m0, Kt, n0, lane);
+        __syncthreads();
+    }
+    if (last)
+        bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
+            *reinterpret_cast<float2*>(last + row0 + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
+        });
+}
+
+template <typename T, int N, bool REV>
+cudaError_t scan_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
+    constexpr int smem = bfp::kTileBytes<kC, N, bfp::kPlanes<T>> + bfp::kTileBytes<kC, 64, 3>;
+    const auto kernel = ssm_scan_kernel<T, N, REV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), kScanThreads, smem, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+// ---- outputs -------------------------------------------------------------------------------------
+
+// Block: 4 warps of 16 tokens each.  PS: planes of the state and of the masked products (the output's accuracy).
+constexpr int kOutThreads = 128;
+template <typename T, int N>
+constexpr int kOutSmem = 2 * bfp::kTileBytes<kC, N, bfp::kPlanes<T>> + bfp::kTileBytes<kC, 64, bfp::kPlanes<T>> +
+                         bfp::kTileBytes<64, N, (bfp::kPlanes<T> == 1 ? 2 : 3)>;
+template <typename T, int N>
+__global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w) {
+    constexpr int PX = bfp::kPlanes<T>, PS = PX == 1 ? 2 : 3;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const bfp::Tile<kC, N, PX> Kt{base}, Ct{base + bfp::kTileBytes<kC, N, PX>};
+    const bfp::Tile<kC, 64, PX> Xt{base + 2 * bfp::kTileBytes<kC, N, PX>};
+    const bfp::Tile<64, N, PS> St{base + 2 * bfp::kTileBytes<kC, N, PX> + bfp::kTileBytes<kC, 64, PX>};
+    __shared__ float gate[kGateRows][kC];
+    Chunk c;
+    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) return;
+    const int slices = a.P / 64, s = blockIdx.y % slices, h = blockIdx.y / slices, g = h / (a.H / a.G);
+    const int tid = threadIdx.x, lane = tid & 31, m = (tid >> 5) * 16;
+    const T* X = static_cast<const T*>(a.x) + (long)c.t0 * a.x_stride + (long)h * a.P + s * 64;
+    const T* B = static_cast<const T*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
+    const T* C = static_cast<const T*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
+    const float* S0 = w.states + (((long)blockIdx.x * a.H + h) * a.P + s * 64) * N;
+    const float* gt = w.gates + ((long)blockIdx.x * a.H + h) * (kGateRows * kC);
+    for (int i = tid; i < kGateRows * kC; i += kOutThreads) (&gate[0][0])[i] = gt[i];
+#pragma unroll 4
+    for (int v = tid; v < kC * N / 8; v += kOutThreads) {
+        const int r = v / (N / 8), col = v % (N / 8) * 8;
+        bfp::Raw8<T> k, q;
+        k.load(B + (long)r * a.B_stride + col, r < c.len);
+        q.load(C + (long)r * a.C_stride + col, r < c.len);
+        k.put(Kt, r, col);
+        q.put(Ct, r, col);
+    }
+#pragma unroll 4
+    for (int v = tid; v < kC * 8; v += kOutThreads) {
+        bfp::Raw8<T> x;
+        x.load(X + (long)(v / 8) * a.x_stride + v % 8 * 8, v / 8 < c.len);
+        x.put(Xt, v / 8, v % 8 * 8);
+    }
+#pragma unroll 4
+    for (int v = tid; v < 64 * N / 8; v += kOutThreads) {
+        const int r = v / (N / 8), col = v % (N / 8) * 8;
+        float x[8];
+        load_row<8>(S0 + (long)r * N + col, x);
+        bfp::put8(St, r, col, x);
+    }
+    __syncthreads();
+    float M[8][4], Y[8][4];
+    bfp::clear(M);
+    bfp::clear(Y);
+    bfp::product<N, false, false>(M, Ct, m, Kt, 0, lane);
+    bfp::product<N, false, false>(Y, Ct, m, St, 0, lane);
+    bfp::pairs<8>(m, 0, lane, [&](int j, int hh, int i, int col) {
+        Y[j][2 * hh] *= gate[3][i];
+        Y[j][2 * hh + 1] *= gate[3][i];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = col + e;
+            const float d = (gate[1][i] - gate[1][t]) + (gate[2][i] - gate[2][t]);
+            M[j][2 * hh + e] = t <= i ? M[j][2 * hh + e] * gate[0][t] * expf(d) : 0.f;
+        }
+    });
+    // the masked products are the left operand of the product with x, from the registers they are in
+    const uint32_t lb = bfp::lane_b<true>(Xt, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (16 * k > m) continue;
+        uint32_t f[PS][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t u[PS];
+            bfp::split<PS>(M[2 * k + (e >> 1)][2 * (e & 1)], M[2 * k + (e >> 1)][2 * (e & 1) + 1], u);
+#pragma unroll
+            for (int p = 0; p < PS; ++p) f[p][e] = u[p];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t b[PX][4];
+            bfp::load_b<true, 0, kC * 128>(b[0], lb, 8 * j, 16 * k);
+            if constexpr (PX > 1) {
+                bfp::load_b<true, kC * 128, kC * 128>(b[1], lb, 8 * j, 16 * k);
+                bfp::load_b<true, 2 * kC * 128, kC * 128>(b[2], lb, 8 * j, 16 * k);
+            }
+            bfp::terms<PS, PX>(Y[j], f, b, 0);
+            bfp::terms<PS, PX>(Y[j + 1], f, b, 1);
+        }
+    }
+    const float D = a.D ? a.D[h] : 0.f;
+    T* out = static_cast<T*>(a.out) + ((long)c.t0 * a.H + h) * a.P + s * 64;
+    bfp::pairs<8>(m, 0, lane, [&](int j, int hh, int i, int col) {
+        if (i >= c.len) return;
+        const float2 x = bfp::get2(Xt, i, col);
+        const float y0 = fmaf(D, x.x, Y[j][2 * hh]), y1 = fmaf(D, x.y, Y[j][2 * hh + 1]);
+        T* o = out + (long)i * a.H * a.P + col;
+        if constexpr (PX == 1) *reinterpret_cast<uint32_t*>(o) = pack_bf16(y0, y1);
+        else *reinterpret_cast<float2*>(o) = make_float2(y0, y1);
+    });
+}
+
+template <typename T, int N>
+cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
+    const auto kernel = ssm_out_kernel<T, N>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem<T, N>);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)(a.H * (a.P / 64)));
+    kernel<<<grid, kOutThreads, kOutSmem<T, N>, s>>>(a, w);
+    return cudaGetLastError();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
+    const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)((a.H + kGateWarps - 1) / kGateWarps));
+    ssm_gates_kernel<<<grid, kGateWarps * 32, 0, s>>>(a, w.gates);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool reverse, cudaStream_t s) {
+    if (a.dtype == GDN_BF16) {
+        if (a.N == 128) return reverse ? scan_one<__nv_bfloat16, 128, true>(a, w, s) : scan_one<__nv_bfloat16, 128, false>(a, w, s);
+        return reverse ? scan_one<__nv_bfloat16, 64, true>(a, w, s) : scan_one<__nv_bfloat16, 64, false>(a, w, s);
+    }
+    if (a.N == 128) return reverse ? scan_one<float, 128, true>(a, w, s) : scan_one<float, 128, false>(a, w, s);
+    return reverse ? scan_one<float, 64, true>(a, w, s) : scan_one<float, 64, false>(a, w, s);
+}
+
+}  // namespace ssm
+
+size_t ssm_fwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
+    const size_t slots = (size_t)ssm::slots_of(num_seqs, total_T);
+    return ssm::align256(slots * H * ssm::kGateRows * ssm::kC * sizeof(float)) + slots * H * P * N * sizeof(float);
+}
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
+    ssm::Work w{};
+    const size_t slots = (size_t)ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
+    w.gates = static_cast<float*>(a.workspace);
+    w.states = w.gates + ssm::align256(slots * a.H * ssm::kGateRows * ssm::kC * sizeof(float)) / sizeof(float);
+    cudaError_t e = ssm::launch_gates(a, w, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
+    if (e != cudaSuccess || a.seqs.total_T == 0) return e;
+    if (a.dtype == GDN_BF16) return a.N == 128 ? ssm::out_one<__nv_bfloat16, 128>(a, w, s) : ssm::out_one<__nv_bfloat16, 64>(a, w, s);
+    return a.N == 128 ? ssm::out_one<float, 128>(a, w, s) : ssm::out_one<float, 64>(a, w, s);
+}
+
+}  // namespace gdn

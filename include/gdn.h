@@ -334,6 +334,154 @@ int gdn_decay_from_logits_bwd(const float* a, const float* A_log, const float* d
 /* Bytes of workspace gdn_decay_from_logits_bwd needs for these sizes; 0 for sizes it refuses. */
 size_t gdn_decay_bwd_workspace_size(long total_T, int H);
 
+/* ---- the state space layer, and what prepares the inputs of a recurrence ---------------------------
+ *
+ * The other recurrence with a matrix state and one decay per head that the pages name beside the delta rule
+ * ("5. 线性注意力" compares the two): the same states [sequences, H, head size, state size] fp32, the same log decay
+ * g = -exp(A_log) softplus(a + dt_bias), the same packed batches and pools, without the prediction S k.  Further
+ * conventions of these calls:
+ *   - Token tensors whose row length comes with a stride (in elements, between tokens) may be slices of a wider
+ *     tensor, as a layer's projection or convolution leaves them: a row is contiguous, starts on a 16-byte
+ *     boundary, and the stride is a multiple of 8 and at least the row's length.  The others are contiguous.
+ *   - Element type: dtype for the token tensors, fp32 for weights, logits and states.  Arithmetic and sums are
+ *     fp32; an output is rounded once.  The same call gives the same bits.
+ *   - Rows of tokens before the first and behind the last sequence of cu_seqlens are left as they were (calls with
+ *     zero_outside: their gradients become zeros when it is not 0).  A malformed cu_seqlens is recorded as
+ *     GDN_ERR_CU_SEQLENS and the call then writes nothing, but for sums over tokens, which have no meaning then.
+ *   - Outputs overlap no input unless stated.
+ */
+
+/*
+ * gdn_short_conv_fwd -- the causal short convolution over packed sequences, as a call of its own.
+ * Source: "5. 线性注意力", "因果卷积(Causal Conv1d)" (which gdn_chunk_fwd fuses for its own q, k, v).
+ *   c_t = bias + sum_j weight[c][j] x_{t - 3 + j},  out_t = silu(c_t), or c_t with silu = 0.
+ *
+ *   x       [total_T, dim] of dtype, rows x_stride apart; weight [dim, GDN_CONV_KERNEL]; bias [dim] or NULL.
+ *   conv_state_in, conv_state_out  [num_seqs, dim, 3]: the three inputs before each sequence's first token, oldest
+ *           first (NULL: zeros), and the last three of it (NULL: not written).  They may be the same array.
+ *   out     [total_T, dim] of dtype.
+ *   dim     a multiple of 8 (GDN_ERR_UNSUPPORTED otherwise), at most 2^20.
+ */
+int gdn_short_conv_fwd(const void* x, long x_stride, const float* weight, const float* bias,
+                       const int32_t* cu_seqlens, int num_seqs, int total_T, int dim, gdn_dtype dtype, int silu,
+                       const float* conv_state_in, float* conv_state_out, void* out, void* stream);
+
+/*
+ * gdn_short_conv_step -- T tokens of N sequences whose histories live in a pool.
+ *   x [N, T, dim], rows x_stride apart (sequences T x_stride); out [N, T, dim];
+ *   conv_state_pool [num_slots, dim, 3], updated in place; state_indices as in gdn_recurrent_multi_step.
+ */
+int gdn_short_conv_step(const void* x, long x_stride, const float* weight, const float* bias, float* conv_state_pool,
+                        int num_slots, const int32_t* state_indices, int N, int T, int dim, gdn_dtype dtype, int silu,
+                        void* out, void* stream);
+
+/*
+ * gdn_short_conv_bwd -- the gradients of gdn_short_conv_fwd.  With dc = dout * silu'(c):
+ *   dx_t = sum_j weight[c][j] dc_{t + 3 - j},  dweight[c][j] = sum_t dc_t x_{t - 3 + j},  dbias = sum_t dc_t.
+ *
+ *   dout [total_T, dim] of dtype; the forward's inputs; dconv_state_out [num_seqs, dim, 3] the gradient of
+ *   conv_state_out, or NULL for zeros; dx [total_T, dim] of dtype; dweight, dbias, dconv_state_in fp32, each may be
+ *   NULL (not computed).
+ *   workspace  gdn_short_conv_bwd_workspace_size(...) bytes, 16-byte aligned; may be NULL when dweight and dbias are.
+ */
+int gdn_short_conv_bwd(const void* dout, const void* x, long x_stride, const float* weight, const float* bias,
+                       const int32_t* cu_seqlens, int num_seqs, int total_T, int dim, gdn_dtype dtype, int silu,
+                       const float* conv_state_in, const float* dconv_state_out, void* dx, float* dweight,
+                       float* dbias, float* dconv_state_in, int zero_outside, void* workspace,
+                       size_t workspace_bytes, void* stream);
+size_t gdn_short_conv_bwd_workspace_size(int num_seqs, int total_T, int dim);
+
+/*
+ * gdn_ssm_chunk_fwd -- the selective state space scan over packed prompts, in chunks of 64 tokens.
+ * Per head h, with dt_t = softplus(a_t + dt_bias) and a state S [d_head, d_state]:
+ *   S_t = exp(-exp(A_log) dt_t) S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D x_t.
+ *
+ *   x    [total_T, H, d_head], B, C [total_T, G, d_state] of dtype, rows x_stride, B_stride, C_stride apart; head h
+ *        uses B and C of group h / (H / G); G divides H.
+ *   a    [total_T, H]; A_log [H]; dt_bias, D [H] or NULL (zeros).  A log decay below -128 is a decay to zero.
+ *   initial_state, final_state  [num_seqs, H, d_head, d_state] or NULL (zeros; not written); may be the same array.
+ *   out  [total_T, H, d_head] of dtype.
+ *   d_head, d_state  each 64 or 128 (GDN_ERR_UNSUPPORTED otherwise); H at most 16384.
+ *   workspace  gdn_ssm_chunk_fwd_workspace_size(...) bytes, 256-byte aligned; may be NULL when that is 0.
+ * A NaN or an infinity in a token's inputs reaches the outputs of its chunk (64 tokens of its sequence) and of every
+ * later token, and no other sequence.
+ */
+int gdn_ssm_chunk_fwd(const void* x, long x_stride, const void* B, long B_stride, const void* C, long C_stride,
+                      const float* a, const float* A_log, const float* dt_bias, const float* D,
+                      const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int G, int d_head, int d_state,
+                      gdn_dtype dtype, const float* initial_state, float* final_state, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+size_t gdn_ssm_chunk_fwd_workspace_size(int num_seqs, int total_T, int H, int G, int d_head, int d_state,
+                                        gdn_dtype dtype);
+
+/*
+ * gdn_ssm_step -- T tokens of N sequences on states in a pool: each state is read once and written once.
+ *   x [N, T, H, d_head], B, C [N, T, G, d_state] (rows by their strides, sequences T rows apart), a [N, T, H],
+ *   out [N, T, H, d_head]; state_pool [num_slots, H, d_head, d_state], updated in place; state_indices as in
+ *   gdn_recurrent_multi_step.  The rest as in gdn_ssm_chunk_fwd.
+ */
+int gdn_ssm_step(const void* x, long x_stride, const void* B, long B_stride, const void* C, long C_stride,
+                 const float* a, const float* A_log, const float* dt_bias, const float* D, float* state_pool,
+                 int num_slots, const int32_t* state_indices, int N, int T, int H, int G, int d_head, int d_state,
+                 gdn_dtype dtype, void* out, void* stream);
+
+/*
+ * gdn_ssm_chunk_bwd -- the gradients of gdn_ssm_chunk_fwd.  Nothing is kept from the forward call: the states at
+ * the chunk starts are recomputed.
+ *   dout [total_T, H, d_head] of dtype; dfinal_state like final_state, or NULL for zeros; the forward's inputs.
+ *   dx [total_T, H, d_head], dB, dC [total_T, G, d_state] of dtype (sums over a group's heads in a fixed order,
+ *   rounded once); da [total_T, H] fp32; dA_log, ddt_bias, dD [H] fp32 and dinitial_state, each may be NULL (not
+ *   computed).  dinitial_state may be dfinal_state.
+ *   workspace  gdn_ssm_chunk_bwd_workspace_size(...) bytes, 256-byte aligned.
+ */
+int gdn_ssm_chunk_bwd(const void* dout, const void* x, long x_stride, const void* B, long B_stride, const void* C,
+                      long C_stride, const float* a, const float* A_log, const float* dt_bias, const float* D,
+                      const int32_t* cu_seqlens, int num_seqs, int total_T, int H, int G, int d_head, int d_state,
+                      gdn_dtype dtype, const float* initial_state, const float* dfinal_state, void* dx, void* dB,
+                      void* dC, float* da, float* dA_log, float* ddt_bias, float* dD, float* dinitial_state,
+                      int zero_outside, void* workspace, size_t workspace_bytes, void* stream);
+size_t gdn_ssm_chunk_bwd_workspace_size(int num_seqs, int total_T, int H, int G, int d_head, int d_state,
+                                        gdn_dtype dtype);
+
+/* The normalisation of gdn_qk_norm_rope: x / sqrt(mean x^2 + eps) or x / sqrt(sum x^2 + eps). */
+typedef enum { GDN_NORM_RMS = 0, GDN_NORM_L2 = 1 } gdn_norm;
+
+/*
+ * gdn_qk_norm_rope -- queries and keys normalised per head and rotated by their position, in one pass: for
+ * gdn_chunk_fwd with use_qk_l2norm = 0 (the normalisation of "6.6 Gated DeltaNet", 6.6.4, is GDN_NORM_L2 with
+ * eps = 1e-6), or for C and B of gdn_ssm_chunk_fwd.
+ *   n = the normalised head, m = weight * n; pair i < d_rot / 2 of the first d_rot channels, (u, v), becomes
+ *   (u cos_i - v sin_i, v cos_i + u sin_i); the other channels pass.  Pair i is channels i and d_rot / 2 + i, or
+ *   2 i and 2 i + 1 when interleaved is not 0.
+ *
+ *   q [T, H, d], k [T, H_k, d] of dtype, rows by their strides (H_k = 0: no k); q_weight, k_weight [d] or NULL (ones);
+ *   cos_sin [max_positions, d_rot]: the cosines of a position's d_rot / 2 angles, then the sines;
+ *   positions int32 [T] (4-byte aligned), or NULL: row t has position t.  A position outside the table is recorded as
+ *   GDN_ERR_ARG in the device error word and its row is left as it was.
+ *   q_out, k_out  like q and k, rows by their own strides; may be q and k themselves.
+ *   d a multiple of 8, at most 256 (GDN_ERR_UNSUPPORTED otherwise); d_rot even, 0 <= d_rot <= d.
+ */
+int gdn_qk_norm_rope(const void* q, long q_stride, const void* k, long k_stride, const float* cos_sin,
+                     const int32_t* positions, long max_positions, const float* q_weight, const float* k_weight,
+                     gdn_norm norm, float eps, int interleaved, int T, int H, int H_k, int d, int d_rot,
+                     gdn_dtype dtype, void* q_out, long q_out_stride, void* k_out, long k_out_stride, void* stream);
+
+/*
+ * gdn_qk_norm_rope_bwd -- its gradients: the rotation backwards gives dm; dweight = sum over rows of dm * n,
+ * dn = dm * weight, dx = r (dn - n mean(dn n)) with r the row's factor (GDN_NORM_L2: the sum in place of the mean).
+ *   dq_out [T, H, d], dk_out [T, H_k, d] of dtype, contiguous; dq, dk of dtype, rows by their strides (may be dq_out and
+ *   dk_out, or q and k); dq_weight, dk_weight [d] fp32, each may be NULL (not computed); rows of a position outside the
+ *   table add nothing and are left as they were;
+ *   workspace  gdn_qk_norm_rope_bwd_workspace_size(...) bytes, 16-byte aligned; may be NULL when both weights' are.
+ */
+int gdn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, long q_stride, const void* k,
+                         long k_stride, const float* cos_sin, const int32_t* positions, long max_positions,
+                         const float* q_weight, const float* k_weight, gdn_norm norm, float eps, int interleaved,
+                         int T, int H, int H_k, int d, int d_rot, gdn_dtype dtype, void* dq, long dq_stride,
+                         void* dk, long dk_stride, float* dq_weight, float* dk_weight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t gdn_qk_norm_rope_bwd_workspace_size(int T, int H, int H_k, int d);
+
 /*
  * gdn_chunk_fwd_noalloc -- gdn_chunk_fwd for callers that cannot allocate device memory.
  * The pages have no counterpart of this call; it exists for callers that have no allocator at hand
