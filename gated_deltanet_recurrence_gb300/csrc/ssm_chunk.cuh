@@ -15,6 +15,27 @@ constexpr int kC = 64;          // tokens of a chunk
 constexpr int kGateRows = 5;    // dt, G hi, G lo, b, r
 constexpr float kMinLog = -128.f;  // a log decay below it is a decay to zero
 
+// A sum in two floats, h + l.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+    const float s = a.h + b.h, z = s - a.h;
+    const float e = (a.h - (s - z)) + (b.h - z) + (a.l + b.l);
+    Two r;
+    r.h = s + e;
+    r.l = e - (r.h - s);
+    return r;
+}
+__device__ __forceinline__ void two_add(Two& a, float x) {
+    const float s = a.h + x, z = s - a.h;
+    a.l += (a.h - (s - z)) + (x - z);
+    a.h = s;
+}
+__device__ __forceinline__ Two two_shfl(Two a, int mask) {
+    return Two{__shfl_xor_sync(0xffffffffu, a.h, mask), __shfl_xor_sync(0xffffffffu, a.l, mask)};
+}
+
 struct Chunk {
     int n, k, bos, eos, t0, len;  // sequence, chunk of it, its tokens, the chunk's first token, tokens in it
 };

@@ -13,18 +13,6 @@ namespace {
 
 // ---- gates ---------------------------------------------------------------------------------------
 
-struct Two {
-    float h, l;
-};
-__device__ __forceinline__ Two two_add(Two a, Two b) {
-    const float s = a.h + b.h, z = s - a.h;
-    const float e = (a.h - (s - z)) + (b.h - z) + (a.l + b.l);
-    Two r;
-    r.h = s + e;
-    r.l = e - (r.h - s);
-    return r;
-}
-
 // One warp per (slot, head): lane l holds tokens 2 l and 2 l + 1.
 constexpr int kGateWarps = 8;
 __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, float* gates) {
