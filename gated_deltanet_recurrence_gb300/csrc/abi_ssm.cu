@@ -16,6 +16,14 @@ bool aligned(P... p) {
         if (q && (reinterpret_cast<uintptr_t>(q) & 15u) != 0) return false;
     return true;
 }
+// What is read and written one number at a time: logits, the vectors over heads, and their gradients.
+template <class... P>
+bool aligned4(P... p) {
+    const void* ptrs[] = {p...};
+    for (const void* q : ptrs)
+        if (q && (reinterpret_cast<uintptr_t>(q) & 3u) != 0) return false;
+    return true;
+}
 // Rows of `width` elements, `stride` apart: none overlap, each starts on a 16-byte boundary.
 bool rows_ok(long stride, long width) { return stride >= width && stride % 8 == 0 && stride <= (1L << 31); }
 int status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
@@ -164,7 +172,7 @@ int gdn_ssm_chunk_fwd(const void* x, long x_stride, const void* B, long B_stride
     if (!ssm_strides(a)) return GDN_ERR_ARG;
     if (total_T == 0 && !final_state) return GDN_OK;
     if (!A_log || (total_T > 0 && (!x || !B || !C || !a_logits || !out))) return GDN_ERR_ARG;
-    if (!aligned(x, B, C, a_logits, A_log, dt_bias, D, initial_state, final_state, out)) return GDN_ERR_ARG;
+    if (!aligned(x, B, C, initial_state, final_state, out) || !aligned4(a_logits, A_log, dt_bias, D)) return GDN_ERR_ARG;
     const size_t need = gdn::ssm_fwd_workspace_bytes(num_seqs, total_T, H, G, d_head, d_state, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
         return GDN_ERR_WORKSPACE;
@@ -191,7 +199,7 @@ int gdn_ssm_step(const void* x, long x_stride, const void* B, long B_stride, con
     if (!ssm_strides(a)) return GDN_ERR_ARG;
     if (N == 0) return GDN_OK;
     if (!x || !B || !C || !a_logits || !A_log || !state_pool || !out) return GDN_ERR_ARG;
-    if (!aligned(x, B, C, a_logits, A_log, dt_bias, D, state_pool, out)) return GDN_ERR_ARG;
+    if (!aligned(x, B, C, state_pool, out) || !aligned4(a_logits, A_log, dt_bias, D)) return GDN_ERR_ARG;
     a.pool = state_pool; a.num_slots = num_slots; a.idx = state_indices; a.n_seq = N; a.T = T; a.out = out;
     a.err = gdn::device_error_word();
     if (!a.err) return GDN_ERR_CUDA;
@@ -221,8 +229,8 @@ int gdn_ssm_chunk_bwd(const void* dout, const void* x, long x_stride, const void
     a.seqs = gdn::Packed{cu_seqlens, num_seqs, total_T}; a.H = H; a.G = G; a.P = d_head; a.N = d_state; a.dtype = dtype;
     if (!ssm_strides(a)) return GDN_ERR_ARG;
     if (!A_log || (total_T > 0 && (!dout || !x || !B || !C || !a_logits || !dx || !dB || !dC || !da))) return GDN_ERR_ARG;
-    if (!aligned(dout, x, B, C, a_logits, A_log, dt_bias, D, initial_state, dfinal_state, dx, dB, dC, da, dA_log, ddt_bias,
-                 dD, dinitial_state))
+    if (!aligned(dout, x, B, C, initial_state, dfinal_state, dx, dB, dC, dinitial_state) ||
+        !aligned4(a_logits, A_log, dt_bias, D, da, dA_log, ddt_bias, dD))
         return GDN_ERR_ARG;
     const size_t need = gdn::ssm_bwd_workspace_bytes(num_seqs, total_T, H, G, d_head, d_state, dtype);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GDN_ERR_WORKSPACE;

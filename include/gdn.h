@@ -343,6 +343,7 @@ size_t gdn_decay_bwd_workspace_size(long total_T, int H);
  *   - Token tensors whose row length comes with a stride (in elements, between tokens) may be slices of a wider
  *     tensor, as a layer's projection or convolution leaves them: a row is contiguous, starts on a 16-byte
  *     boundary, and the stride is a multiple of 8 and at least the row's length.  The others are contiguous.
+ *   - Logits, A_log, dt_bias, D and their gradients are read and written one by one: 4-byte alignment is enough.
  *   - Element type: dtype for the token tensors, fp32 for weights, logits and states.  Arithmetic and sums are
  *     fp32; an output is rounded once.  The same call gives the same bits.
  *   - Rows of tokens before the first and behind the last sequence of cu_seqlens are left as they were (calls with
