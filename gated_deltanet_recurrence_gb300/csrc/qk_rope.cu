@@ -43,119 +43,183 @@ __device__ __forceinline__ float set_sum(float x) {
     return x;
 }
 
-// The rotation of one lane's eight channels; `sign` is -1 for the rotation backwards.  cs, sn: this lane's cosines and
-// sines by channel (1 and 0 past d_rot), where sn has the sign with which the partner's value enters.
-template <int L, Pairs PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[kV], const float (&cs)[kV], const float (&sn)[kV], int lane, int d, int m,
-                                       float* row) {
-    float y[kV];
+// One lane's eight channels x and their partners y, as they lie in memory (so that bf16 pairs move in one exchange).
+template <typename T, int L, Pairs PAIRS>
+__device__ __forceinline__ void partners(const RawRow<T, kV>& r, const float (&x)[kV], float (&y)[kV], int lane, int from, int m,
+                                         float* row) {
     if constexpr (PAIRS == kNeighbours) {
 #pragma unroll
         for (int j = 0; j < kV; ++j) y[j] = x[j ^ 1];
     } else if constexpr (PAIRS == kLanes) {
-        const int off = m / kV;
-        const int from = lane < off ? lane + off : lane - off;  // lanes past d_rot get a value they do not use
+        RawRow<T, kV> p;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], from & (L - 1), L);
+        for (int j = 0; j < RawRow<T, kV>::W; ++j) p.u[j] = __shfl_sync(0xffffffffu, r.u[j], from, L);
+        p.get(y);
     } else {
         __syncwarp();
-        if (lane * kV < d) {
 #pragma unroll
-            for (int j = 0; j < kV; ++j) row[lane * kV + j] = x[j];
-        }
+        for (int j = 0; j < kV; ++j) row[lane * kV + j] = x[j];
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = lane * kV + j;
-            y[j] = c < m ? row[c + m] : (c < 2 * m ? row[c - m] : 0.f);
+            y[j] = row[c < m ? c + m : (c < 2 * m ? c - m : c)];
         }
     }
-#pragma unroll
-    for (int j = 0; j < kV; ++j) x[j] = sn[j] == 0.f ? x[j] * cs[j] : fmaf(y[j], sn[j], x[j] * cs[j]);
 }
 
-// One block: kThreads / L sets; a set: one token, `per` heads of the q and k heads taken together.
+// One block: kThreads / L sets; a set: one token, `per` heads of the q and k heads taken together.  Sets are numbered
+// part by part, each part's tokens rounded up to whole warps, so that all sets of a warp have the same heads.
 template <typename T, int L, Pairs PAIRS, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_kernel(QkArgs a, int per, int parts, long sets) {
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int per, long tokens, long sets) {
+    constexpr int U = BWD ? 2 : 4, kGroups = 2;  // rows worked on together; groups of them on their way
+    using Rows = Ring<T, kV, U * kGroups, kThreads>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Rows rx(smem), rg(smem + (BWD ? Rows::kSmem : 0));
     __shared__ float stage[PAIRS == kShared ? kThreads * kV : 1];
     const int lane = threadIdx.x % L;
     const int c0 = lane * kV, d = a.d, m = a.rot / 2;
     const bool in = c0 < d;
     const float inv = a.l2 ? 1.0f : 1.0f / (float)d;
     float* row = stage + (PAIRS == kShared ? threadIdx.x / L * L * kV : 0);
-    float w[2][kV], dw[2][kV];
+    const int off = m / kV, from = lane >= 2 * off ? lane : (lane < off ? lane + off : lane - off);
+    float dw[2][kV];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) { w[i][j] = 1.f; dw[i][j] = 0.f; }
-        if (in && a.w[i]) load_row<kV>(a.w[i] + c0, w[i]);
-    }
-    // every set of a block makes the same number of passes: the shuffles and barriers of a warp stay together
+    for (int j = 0; j < kV; ++j) dw[0][j] = dw[1][j] = 0.f;
     const long stride = (long)gridDim.x * (kThreads / L);
     for (long base = (long)blockIdx.x * (kThreads / L); base < sets; base += stride) {
         const long set = base + threadIdx.x / L;
-        const int t = (int)(set / parts), part = (int)(set % parts);
-        bool live = set < sets;
+        const long t = set % tokens;
+        const int part = (int)(set / tokens);
+        bool live = set < sets && t < a.T;
         float cs[kV], sn[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) { cs[j] = 1.f; sn[j] = 0.f; }
         if (live) {
-            const long pos = a.positions ? (long)a.positions[t] : (long)t;
+            const long pos = a.positions ? (long)a.positions[t] : t;
             if (pos < 0 || pos >= a.max_positions) {
-                live = false;
                 if (lane == 0) record_error(a.err, GDN_ERR_ARG);
+                live = false;
             } else {
                 const float* tab = a.cos_sin + pos * a.rot;
+                if (PAIRS == kLanes) {
+                    if (c0 < 2 * m) {
+                        load_row<kV>(tab + (c0 < m ? c0 : c0 - m), cs);
+                        load_row<kV>(tab + (c0 < m ? c0 + m : c0), sn);
+                        if ((c0 >= m) == BWD) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    const int c = c0 + j;
-                    if (c >= 2 * m) continue;
-                    const int i = PAIRS == kNeighbours ? c >> 1 : (c < m ? c : c - m);
-                    const bool second = PAIRS == kNeighbours ? c & 1 : c >= m;
-                    cs[j] = tab[i];
-                    sn[j] = second != BWD ? tab[m + i] : -tab[m + i];
+                            for (int j = 0; j < kV; ++j) sn[j] = -sn[j];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) {
+                        const int c = c0 + j;
+                        if (c >= 2 * m) continue;
+                        const int i = PAIRS == kNeighbours ? c >> 1 : (c < m ? c : c - m);
+                        const bool second = PAIRS == kNeighbours ? c & 1 : c >= m;
+                        cs[j] = tab[i];
+                        sn[j] = second != BWD ? tab[m + i] : -tab[m + i];
+                    }
                 }
             }
         }
-        const int h1 = min(a.heads[0] + a.heads[1], (part + 1) * per);
-#pragma unroll 2
-        for (int p = 0; p < per; ++p) {
-            const int hh = part * per + p, i = hh >= a.heads[0], h = i ? hh - a.heads[0] : hh;
-            const bool on = live && in && hh < h1;
-            float x[kV], g[kV];
-#pragma unroll
-            for (int j = 0; j < kV; ++j) x[j] = g[j] = 0.f;
-            if (on) {
-                load_row<kV>(static_cast<const T*>(i ? a.x[1] : a.x[0]) + (long)t * (i ? a.x_stride[1] : a.x_stride[0]) + (long)h * d + c0, x);
-                if (BWD) load_row<kV>(static_cast<const T*>(i ? a.dout[1] : a.dout[0]) + ((long)t * (i ? a.heads[1] : a.heads[0]) + h) * d + c0, g);
+        const bool on = live && in;
+        if (!on) {  // a set without a row reads zeros, whatever an earlier one has left
+            for (int i = 0; i < U * kGroups; ++i) {
+                rx.clear(i);
+                if (BWD) rg.clear(i);
             }
-            float ss = 0.f;
+        }
+        // this set's heads of q, then of k
+        const int lo = part * per, hi = min(a.heads[0] + a.heads[1], lo + per);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) ss = fmaf(x[j], x[j], ss);
-            const float r = rsqrtf(set_sum<L>(ss) * inv + a.eps);
-            T* out = static_cast<T*>(i ? a.out[1] : a.out[0]) + (long)t * (i ? a.out_stride[1] : a.out_stride[0]) + (long)h * d + c0;
-            if constexpr (!BWD) {
+        for (int i = 0; i < 2; ++i) {
+            const int h0 = i ? max(lo - a.heads[0], 0) : lo, h1 = i ? hi - a.heads[0] : min(hi, a.heads[0]);
+            if (h0 >= h1) continue;
+            // forward: the weights go into the rotation's factors, w of the channel and of its partner
+            float w[kV], wc[kV], ws[kV];
+            {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) x[j] *= r * (i ? w[1][j] : w[0][j]);
-                rotate<L, PAIRS>(x, cs, sn, lane, d, m, row);
-                if (on) store_row<kV>(out, x);
-            } else {
-                rotate<L, PAIRS>(g, cs, sn, lane, d, m, row);
-                float dot = 0.f;
+                for (int j = 0; j < kV; ++j) w[j] = 1.f;
+                if (in && a.w[i]) load_row<kV>(a.w[i] + c0, w);
+                if constexpr (!BWD) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    x[j] *= r;
-                    const float gn = on ? g[j] * x[j] : 0.f;
-                    dw[0][j] += i ? 0.f : gn;
-                    dw[1][j] += i ? gn : 0.f;
-                    g[j] *= i ? w[1][j] : w[0][j];
-                    dot = fmaf(g[j], x[j], dot);
+                    for (int j = 0; j < kV; ++j) {
+                        const int c = c0 + j;
+                        const int other = PAIRS == kNeighbours ? c ^ 1 : (c < m ? c + m : (c < 2 * m ? c - m : c));
+                        wc[j] = w[j] * cs[j];
+                        ws[j] = in && a.w[i] ? a.w[i][other] * sn[j] : sn[j];
+                    }
                 }
-                dot = set_sum<L>(dot) * inv;
-#pragma unroll
-                for (int j = 0; j < kV; ++j) g[j] = r * (g[j] - x[j] * dot);
-                if (on) store_row<kV>(out, g);
             }
+            const T* src = static_cast<const T*>(a.x[i]) + t * a.x_stride[i] + h0 * d + c0;
+            const T* grad = BWD ? static_cast<const T*>(a.dout[i]) + (t * a.heads[i] + h0) * d + c0 : nullptr;
+            T* out = static_cast<T*>(a.out[i]) + t * a.out_stride[i] + h0 * d + c0;
+            int asked = h0;
+            const auto ask = [&](int q) {
+                if (on) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (asked + u < h1) {
+                            rx.ask(U * q + u, src + u * d);
+                            if (BWD) rg.ask(U * q + u, grad + u * d);
+                        }
+                }
+                ring_commit();
+                asked += U;
+                src += U * d;
+                if (BWD) grad += U * d;
+            };
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) ask(q);
+            int group = 0;
+            for (int h = h0; h < h1; h += U) {
+                RawRow<T, kV> xr[U], gr[BWD ? U : 1];
+                ring_wait<kGroups - 1>();
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rx.read(U * group + u, xr[u]);
+                    if constexpr (BWD) rg.read(U * group + u, gr[u]);
+                }
+                ask(group);
+                group ^= 1;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (h + u >= h1) break;
+                    float x[kV], y[kV];
+                    xr[u].get(x);
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) ss = fmaf(x[j], x[j], ss);
+                    const float r = rsqrtf(set_sum<L>(ss) * inv + a.eps);
+                    if constexpr (!BWD) {
+                        partners<T, L, PAIRS>(xr[u], x, y, lane, from, m, row);
+#pragma unroll
+                        for (int j = 0; j < kV; ++j) x[j] = r * fmaf(y[j], ws[j], x[j] * wc[j]);
+                        if (on) store_row<kV>(out + u * d, x);
+                    } else {
+                        float g[kV];
+                        gr[u].get(g);
+                        partners<T, L, PAIRS>(gr[u], g, y, lane, from, m, row);
+                        float dot = 0.f;
+#pragma unroll
+                        for (int j = 0; j < kV; ++j) {
+                            g[j] = fmaf(y[j], sn[j], g[j] * cs[j]);
+                            x[j] *= r;
+                            dw[i][j] = fmaf(g[j], x[j], dw[i][j]);
+                            g[j] *= w[j];
+                            dot = fmaf(g[j], x[j], dot);
+                        }
+                        dot = set_sum<L>(dot) * inv;
+#pragma unroll
+                        for (int j = 0; j < kV; ++j) g[j] = r * fmaf(-x[j], dot, g[j]);
+                        if (on) store_row<kV>(out + u * d, g);
+                    }
+                }
+                out += U * d;
+            }
+            ring_wait<0>();
         }
     }
     if constexpr (BWD) {
@@ -177,15 +241,16 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(QkArgs a, int per, int par
 }
 
 struct Plan {
-    int L, per, parts;
-    long sets, blocks;
+    int L, per;
+    long tokens, sets, blocks;
 };
 Plan plan(int T, int H, int H_k, int d, bool bwd) {
     Plan p;
     p.L = lanes_of(d);
     p.per = heads_per_set(T, H + H_k, p.L);
-    p.parts = (H + H_k + p.per - 1) / p.per;
-    p.sets = (long)T * p.parts;
+    const int warp = 32 / p.L;
+    p.tokens = ((long)T + warp - 1) / warp * warp;
+    p.sets = p.tokens * ((H + H_k + p.per - 1) / p.per);
     p.blocks = (p.sets + kThreads / p.L - 1) / (kThreads / p.L);
     // the sums over rows go into one row of a table per block: the blocks stay and walk on
     if (bwd && p.blocks > 4 * kSMs) p.blocks = 4 * kSMs;
@@ -197,7 +262,10 @@ cudaError_t launch_pairs(const QkArgs& a, const Plan& p, cudaStream_t s) {
     const auto kernel = a.interleaved ? qk_kernel<T, L, kNeighbours, BWD>
                         : (a.rot / 2) % kV == 0 ? qk_kernel<T, L, kLanes, BWD>
                                                 : qk_kernel<T, L, kShared, BWD>;
-    kernel<<<(unsigned)p.blocks, kThreads, 0, s>>>(a, p.per, p.parts, p.sets);
+    constexpr int smem = 8 * kV * (int)sizeof(T) * kThreads;  // the rings
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)p.blocks, kThreads, smem, s>>>(a, p.per, p.tokens, p.sets);
     return cudaGetLastError();
 }
 

@@ -15,11 +15,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTaps = GDN_CONV_KERNEL;
-constexpr int kVec = 8;     // channels of a thread, forward
-constexpr int kVecB = 4;    // and in the backward pass, whose sums take 20 registers a channel quarter
+constexpr int kVec = 4;     // channels of a thread, forward
+constexpr int kVecB = 2;    // and in the backward pass, whose taps, windows and sums take 30 registers a channel
 constexpr int kSMs = 152;
+constexpr int kGroups = 4;  // groups of four rows that a thread has on their way
 
-__device__ __forceinline__ float silu_or(float c, int silu) { return silu ? c * sigmoidf_(c) : c; }
+template <bool SILU>
+__device__ __forceinline__ float silu_or(float c) {
+    return SILU ? c * sigmoid_hw(c) : c;
+}
 
 // The input at position p (token index t0 + p of the batch) of a sequence whose first token is t0: its history
 // for p < 0, zeros without one.
@@ -57,8 +61,10 @@ __device__ void final_history(const ShortConvArgs& a, int n, int bos, int len, i
 
 // Blocks [0, runs * cols): one run of `run` tokens of kThreads channel vectors each; the blocks behind them write
 // the final histories (num_seqs * vectors threads).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ShortConvArgs a, int run, int cols, int runs) {
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ShortConvArgs a, int run, int cols, int runs) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    Ring<T, kVec, 4 * kGroups, kThreads> ring(smem);
     const int vecs = a.dim / kVec;
     if (blockIdx.x >= (unsigned)(runs * cols)) {
         if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
@@ -73,6 +79,9 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ShortConvArgs a, int
     const int per = cols > 1 ? 1 : kThreads / vecs;
     const int v = cols > 1 ? col * kThreads + (int)threadIdx.x : (int)threadIdx.x % vecs;
     const int first = (int)(blockIdx.x / cols) * per * run;
+    const int c0 = v * kVec;
+    float w[kVec][kTaps], b[kVec], h[3][kVec];
+    if (v < vecs) load_taps<kVec>(a, c0, w, b);
     int n = packed_find(a.seqs, first, 1, 0, a.err);
     if (n == -2) return;
     int t = first + (cols > 1 ? 0 : (int)threadIdx.x / vecs * run);
@@ -83,36 +92,64 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ShortConvArgs a, int
         t = max(t, a.seqs.bos(0));
     }
     if (t >= end) return;
-    const int c0 = v * kVec;
-    float w[kVec][kTaps], b[kVec], h[3][kVec], x[kVec];
-    load_taps<kVec>(a, c0, w, b);
     T* out = static_cast<T*>(a.out);
     while (n < N && t < end) {
         const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1);
         if (t >= eos) { ++n; continue; }
-#pragma unroll
-        for (int j = 0; j < 3; ++j) input_at<T, kVec>(a, n, bos, t - bos - 3 + j, c0, h[j]);
         const int stop = min(end, eos);
-        const T* src = static_cast<const T*>(a.x) + c0;
-#pragma unroll 4
-        for (; t < stop; ++t) {
-            load_row<kVec>(src + (long)t * a.x_stride, x);
+        const long xs = a.x_stride, os = a.dim;
+        const T* src = static_cast<const T*>(a.x) + (long)t * xs + c0;
+        T* dst = out + (long)t * os + c0;
+        const auto one = [&](const float (&x)[kVec], const float (&h2)[kVec], const float (&h1)[kVec], const float (&h0)[kVec], T* to) {
             float o[kVec];
 #pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                o[j] = silu_or<SILU>(fmaf(w[j][3], x[j], fmaf(w[j][2], h2[j], fmaf(w[j][1], h1[j], fmaf(w[j][0], h0[j], b[j])))));
+            store_row<kVec>(to, o);
+        };
+        // four rows at a time; the rows of the groups behind them are on their way
+        int asked = t;
+        const T* next = src;
+        const auto ask = [&](int group) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (asked + i < stop) ring.ask(4 * group + i, next + i * xs);
+            ring_commit();
+            asked += 4;
+            next += 4 * xs;
+        };
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) ask(q);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) input_at<T, kVec>(a, n, bos, t - bos - 3 + j, c0, h[j]);
+        int group = 0;
+        for (; t < stop; t += 4) {
+            float x[4][kVec];
+            ring_wait<kGroups - 1>();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + i < stop) ring.read(4 * group + i, x[i]);
+            one(x[0], h[2], h[1], h[0], dst);
+            if (t + 1 < stop) one(x[1], x[0], h[2], h[1], dst + os);
+            if (t + 2 < stop) one(x[2], x[1], x[0], h[2], dst + 2 * os);
+            if (t + 3 < stop) one(x[3], x[2], x[1], x[0], dst + 3 * os);
+            ask(group);
+            group = group + 1 == kGroups ? 0 : group + 1;
+            dst += 4 * os;
+#pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[2][j], fmaf(w[j][1], h[1][j], fmaf(w[j][0], h[0][j], b[j]))));
-                o[j] = silu_or(c, a.silu);
-                h[0][j] = h[1][j];
-                h[1][j] = h[2][j];
-                h[2][j] = x[j];
+                h[0][j] = x[1][j];
+                h[1][j] = x[2][j];
+                h[2][j] = x[3][j];
             }
-            store_row<kVec>(out + (long)t * a.dim + c0, o);
         }
+        ring_wait<0>();
+        t = stop;
     }
 }
 
 // One thread: four channels of one sequence, its history read, moved on by T tokens and written back.
-template <typename T>
+template <typename T, bool SILU>
 __global__ void __launch_bounds__(128) conv_step_kernel(ShortConvArgs a) {
     const int vecs = a.dim / 4;
     const long q = (long)blockIdx.x * 128 + threadIdx.x;
@@ -140,7 +177,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ShortConvArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[3 * j + 2], fmaf(w[j][1], h[3 * j + 1], fmaf(w[j][0], h[3 * j], b[j]))));
-            o[j] = silu_or(c, a.silu);
+            o[j] = silu_or<SILU>(c);
             h[3 * j] = h[3 * j + 1];
             h[3 * j + 1] = h[3 * j + 2];
             h[3 * j + 2] = x[j];
@@ -153,17 +190,20 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ShortConvArgs a) {
 }
 
 // dc of one token: the slope of the SiLU at c, times dout.
-__device__ __forceinline__ float dc_of(float c, float d, int silu) {
-    if (!silu) return d;
-    const float sg = sigmoidf_(c);
+template <bool SILU>
+__device__ __forceinline__ float dc_of(float c, float d) {
+    if (!SILU) return d;
+    const float sg = sigmoid_hw(c);
     return d * sg * fmaf(c, 1.0f - sg, 1.0f);
 }
 
-// A block is 32 channel vectors (of four) x 8 runs of tokens; the sums over its runs are added in order and go to
+// A block is 32 channel vectors (of two) x 8 runs of tokens; the sums over its runs are added in order and go to
 // row blockIdx.x of the table of partial sums [rows][dim * 4], with the biases' [rows][dim] behind it.  The blocks
 // with blockIdx.x = rows give the gradients of the carried histories, one thread per (sequence, vector).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int run, int rows) {
+template <typename T, bool SILU>
+__global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, int run, int rows) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    Ring<T, kVecB, 4 * kGroups, kThreads> rx(smem), rd(smem + Ring<T, kVecB, 4 * kGroups, kThreads>::kSmem);
     const int vecs = a.dim / kVecB;
     const int v = blockIdx.y * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
     const int c0 = v * kVecB, N = a.seqs.num_seqs;
@@ -173,7 +213,6 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int
     T* dx = static_cast<T*>(a.dx) + c0;
     const bool state_block = (int)blockIdx.x == rows;
     const int first = state_block ? 0 : (int)blockIdx.x * 8 * run;
-    int n = packed_find(a.seqs, first, 1, 0, a.err);
     float w[kVecB][kTaps], b[kVecB];
     float dw[kVecB][kTaps], db[kVecB];
 #pragma unroll
@@ -183,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int
         for (int i = 0; i < kTaps; ++i) dw[j][i] = 0.f;
     }
     if (on) load_taps<kVecB>(a, c0, w, b);
+    int n = packed_find(a.seqs, first, 1, 0, a.err);
     if (state_block) {
         if (n == -2 || !on) return;
         for (int m = k; m < N; m += 8) {
@@ -202,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int
 #pragma unroll
                 for (int j = 0; j < kVecB; ++j) {
                     const float c = fmaf(w[j][3], x[p + 3][j], fmaf(w[j][2], x[p + 2][j], fmaf(w[j][1], x[p + 1][j], fmaf(w[j][0], x[p][j], b[j]))));
-                    g[p][j] = dc_of(c, d[j], a.silu);
+                    g[p][j] = dc_of<SILU>(c, d[j]);
                 }
             }
 #pragma unroll
@@ -246,53 +286,110 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ShortConvArgs a, int
         if (t >= eos) { ++n; continue; }
         const int stop = min(end, eos);
         float h[3][kVecB], g[3][kVecB];  // the inputs and the dc of the three tokens before
+        const int from = t;
+        const long xs = a.x_stride, os = a.dim;
+        const T* px = src + (long)t * xs;
+        const T* pd = dout + (long)t * os;
+        T* po = dx + (long)(t - 3) * os;
+        // dc of a token of the run (its sums too, where `sums`), from its input and the three before it
+        const auto dc = [&](const float (&x)[kVecB], const float (&h2)[kVecB], const float (&h1)[kVecB], const float (&h0)[kVecB],
+                            const float (&d)[kVecB], bool sums, float (&gc)[kVecB]) {
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j) {
+                const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h2[j], fmaf(w[j][1], h1[j], fmaf(w[j][0], h0[j], b[j]))));
+                gc[j] = dc_of<SILU>(c, d[j]);
+                if (sums) {
+                    dw[j][0] = fmaf(gc[j], h0[j], dw[j][0]);
+                    dw[j][1] = fmaf(gc[j], h1[j], dw[j][1]);
+                    dw[j][2] = fmaf(gc[j], h2[j], dw[j][2]);
+                    dw[j][3] = fmaf(gc[j], x[j], dw[j][3]);
+                    db[j] += gc[j];
+                }
+            }
+        };
+        // the gradient that is complete with g3, the dc of three tokens later
+        const auto gradient = [&](const float (&g3)[kVecB], const float (&g2)[kVecB], const float (&g1)[kVecB], const float (&g0)[kVecB],
+                                  const float (&more)[kVecB], T* to) {
+            float o[kVecB];
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j)
+                o[j] = fmaf(w[j][0], g3[j], fmaf(w[j][1], g2[j], fmaf(w[j][2], g1[j], fmaf(w[j][3], g0[j], more[j]))));
+            store_row<kVecB>(to, o);
+        };
+        const float none[kVecB] = {};
+        const int last = min(stop + 3, eos);
+        int asked = t, group = 0;
+        const auto ask = [&](int q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (asked + i < last) {
+                    rx.ask(4 * q + i, px + i * xs);
+                    rd.ask(4 * q + i, pd + i * os);
+                }
+            ring_commit();
+            asked += 4;
+            px += 4 * xs;
+            pd += 4 * os;
+        };
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) ask(q);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             input_at<T, kVecB>(a, n, bos, t - bos - 3 + j, c0, h[j]);
 #pragma unroll
             for (int i = 0; i < kVecB; ++i) g[j][i] = 0.f;
         }
-        const int from = t;
-        // the three tokens behind the run give their dc to the run's last tokens
-#pragma unroll 2
-        for (; t < stop + 3; ++t) {
-            float x[kVecB], d[kVecB], o[kVecB];
-            const bool live = t < eos, mine = t < stop;
-            if (live) {
-                load_row<kVecB>(src + (long)t * a.x_stride, x);
-                load_row<kVecB>(dout + (long)t * a.dim, d);
-            }
-            const int u = t - 3;  // the token whose gradient is complete now
-            float s[kVecB];
+        for (; t + 4 <= stop; t += 4) {
+            float x[4][kVecB], d[4][kVecB], n4[4][kVecB];
+            ring_wait<kGroups - 1>();
 #pragma unroll
-            for (int j = 0; j < kVecB; ++j) s[j] = 0.f;
-            if (a.dstate_out && u >= eos - 3 && u < eos) {
-#pragma unroll
-                for (int j = 0; j < kVecB; ++j) s[j] = a.dstate_out[((long)n * a.dim + c0 + j) * 3 + u - (eos - 3)];
+            for (int i = 0; i < 4; ++i) {
+                rx.read(4 * group + i, x[i]);
+                rd.read(4 * group + i, d[i]);
             }
+            ask(group);
+            group = group + 1 == kGroups ? 0 : group + 1;
+            dc(x[0], h[2], h[1], h[0], d[0], true, n4[0]);
+            dc(x[1], x[0], h[2], h[1], d[1], true, n4[1]);
+            dc(x[2], x[1], x[0], h[2], d[2], true, n4[2]);
+            dc(x[3], x[2], x[1], x[0], d[3], true, n4[3]);
+            if (t != from) {  // the three tokens before the run are another thread's
+                gradient(n4[0], g[2], g[1], g[0], none, po);
+                gradient(n4[1], n4[0], g[2], g[1], none, po + os);
+                gradient(n4[2], n4[1], n4[0], g[2], none, po + 2 * os);
+            }
+            gradient(n4[3], n4[2], n4[1], n4[0], none, po + 3 * os);
+            po += 4 * os;
 #pragma unroll
             for (int j = 0; j < kVecB; ++j) {
-                float gc = 0.f;
-                if (live) {
-                    const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h[2][j], fmaf(w[j][1], h[1][j], fmaf(w[j][0], h[0][j], b[j]))));
-                    gc = dc_of(c, d[j], a.silu);
-                    if (mine) {
-                        dw[j][0] = fmaf(gc, h[0][j], dw[j][0]);
-                        dw[j][1] = fmaf(gc, h[1][j], dw[j][1]);
-                        dw[j][2] = fmaf(gc, h[2][j], dw[j][2]);
-                        dw[j][3] = fmaf(gc, x[j], dw[j][3]);
-                        db[j] += gc;
-                    }
-                }
-                o[j] = fmaf(w[j][0], gc, fmaf(w[j][1], g[2][j], fmaf(w[j][2], g[1][j], fmaf(w[j][3], g[0][j], s[j]))));
-                g[0][j] = g[1][j];
-                g[1][j] = g[2][j];
-                g[2][j] = gc;
-                h[0][j] = h[1][j];
-                h[1][j] = h[2][j];
-                h[2][j] = live ? x[j] : 0.f;
+                h[0][j] = x[1][j]; h[1][j] = x[2][j]; h[2][j] = x[3][j];
+                g[0][j] = n4[1][j]; g[1][j] = n4[2][j]; g[2][j] = n4[3][j];
             }
-            if (u >= from) store_row<kVecB>(dx + (long)u * a.dim, o);
+        }
+        // what is left of the run, and the three tokens behind it, which give their dc to its last tokens
+        const int rest = stop + 3 - t, live = eos - t;
+        ring_wait<0>();
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            if (i >= rest) break;
+            const int u = t + i - 3;
+            float x[kVecB] = {}, d[kVecB], gc[kVecB] = {}, more[kVecB] = {};
+            if (i < live) {
+                const int slot = 4 * (i < 4 ? group : (group + 1 == kGroups ? 0 : group + 1)) + (i & 3);
+                rx.read(slot, x);
+                rd.read(slot, d);
+                dc(x, h[2], h[1], h[0], d, t + i < stop, gc);
+            }
+            if (a.dstate_out && u >= eos - 3 && u < eos) {
+#pragma unroll
+                for (int j = 0; j < kVecB; ++j) more[j] = a.dstate_out[((long)n * a.dim + c0 + j) * 3 + u - (eos - 3)];
+            }
+            if (u >= from) gradient(gc, g[2], g[1], g[0], more, dx + (long)u * os);
+#pragma unroll
+            for (int j = 0; j < kVecB; ++j) {
+                h[0][j] = h[1][j]; h[1][j] = h[2][j]; h[2][j] = x[j];
+                g[0][j] = g[1][j]; g[1][j] = g[2][j]; g[2][j] = gc[j];
+            }
         }
         t = stop;
     }
@@ -331,20 +428,25 @@ cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
     const int vecs = a.dim / kVec;
     const int cols = vecs > kThreads ? (vecs + kThreads - 1) / kThreads : 1;
     const int per = cols > 1 ? 1 : kThreads / vecs;
-    const int run = run_length(a.seqs.total_T, vecs, 4, 16);
+    const int run = run_length(a.seqs.total_T, vecs, 4, 32);
     const int runs = (int)(((long)a.seqs.total_T + (long)per * run - 1) / ((long)per * run));
     const long tail = a.state_out ? ((long)a.seqs.num_seqs * vecs + kThreads - 1) / kThreads : 0;
-    const auto kernel = a.dtype == GDN_BF16 ? conv_fwd_kernel<__nv_bfloat16> : conv_fwd_kernel<float>;
+    using B = __nv_bfloat16;
+    const auto kernel = a.dtype == GDN_BF16 ? (a.silu ? conv_fwd_kernel<B, true> : conv_fwd_kernel<B, false>)
+                                            : (a.silu ? conv_fwd_kernel<float, true> : conv_fwd_kernel<float, false>);
+    const int smem = a.dtype == GDN_BF16 ? Ring<__nv_bfloat16, kVec, 4 * kGroups, kThreads>::kSmem : Ring<float, kVec, 4 * kGroups, kThreads>::kSmem;
+    cudaError_t set = allow_smem(kernel, smem);
+    if (set != cudaSuccess) return set;
     // histories that are carried in place are written behind everything that reads them
     const bool apart = a.state_out && a.state_out == a.state_in;
     if ((long)runs * cols + tail > 0x7fffffffL) return cudaErrorInvalidValue;
     if (runs > 0 || (tail > 0 && !apart)) {
-        kernel<<<(unsigned)((long)runs * cols + (apart ? 0 : tail)), kThreads, 0, s>>>(a, run, cols, runs);
+        kernel<<<(unsigned)((long)runs * cols + (apart ? 0 : tail)), kThreads, smem, s>>>(a, run, cols, runs);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (apart) {
-        kernel<<<(unsigned)tail, kThreads, 0, s>>>(a, run, cols, 0);
+        kernel<<<(unsigned)tail, kThreads, smem, s>>>(a, run, cols, 0);
         return cudaGetLastError();
     }
     return cudaSuccess;
@@ -353,8 +455,10 @@ cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
 cudaError_t launch_short_conv_step(const ShortConvArgs& a, cudaStream_t s) {
     const long blocks = ((long)a.N * (a.dim / 4) + 127) / 128;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidValue;
-    if (a.dtype == GDN_BF16) conv_step_kernel<__nv_bfloat16><<<(unsigned)blocks, 128, 0, s>>>(a);
-    else conv_step_kernel<float><<<(unsigned)blocks, 128, 0, s>>>(a);
+    using B = __nv_bfloat16;
+    const auto kernel = a.dtype == GDN_BF16 ? (a.silu ? conv_step_kernel<B, true> : conv_step_kernel<B, false>)
+                                            : (a.silu ? conv_step_kernel<float, true> : conv_step_kernel<float, false>);
+    kernel<<<(unsigned)blocks, 128, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -374,9 +478,15 @@ cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s) {
     bwd_plan(a.seqs.total_T, a.dim, run, rows);
     const dim3 grid((unsigned)(rows + (a.dstate_in ? 1 : 0)), (unsigned)((a.dim / kVecB + 31) / 32));
     if (grid.x > 0) {
-        if (a.dtype == GDN_BF16) conv_bwd_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a, run, rows);
-        else conv_bwd_kernel<float><<<grid, kThreads, 0, s>>>(a, run, rows);
-        const cudaError_t e = cudaGetLastError();
+        const bool bf = a.dtype == GDN_BF16;
+        using B = __nv_bfloat16;
+        const auto kernel = bf ? (a.silu ? conv_bwd_kernel<B, true> : conv_bwd_kernel<B, false>)
+                               : (a.silu ? conv_bwd_kernel<float, true> : conv_bwd_kernel<float, false>);
+        const int smem = 2 * (bf ? Ring<__nv_bfloat16, kVecB, 4 * kGroups, kThreads>::kSmem : Ring<float, kVecB, 4 * kGroups, kThreads>::kSmem);
+        cudaError_t e = allow_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, kThreads, smem, s>>>(a, run, rows);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = cudaSuccess;

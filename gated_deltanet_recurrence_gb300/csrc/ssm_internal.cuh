@@ -48,8 +48,10 @@ __device__ __forceinline__ int packed_find(const Packed& s, int at, int unit, in
 
 template <int VEC>
 __device__ __forceinline__ void load_row(const float* p, float (&out)[VEC]) {
+    if constexpr (VEC == 2) load_vec<2>(p, out);
+    else
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) load_vec<4>(p + i, out + i);
+        for (int i = 0; i < VEC; i += 4) load_vec<4>(p + i, out + i);
 }
 template <int VEC>
 __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&out)[VEC]) {
@@ -62,11 +64,13 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&out)[VE
             out[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
     } else {
-        load_vec<4>(p, out);
+        load_vec<VEC>(p, out);
     }
 }
 template <int VEC>
 __device__ __forceinline__ void store_row(float* p, const float (&x)[VEC]) {
+    if constexpr (VEC == 2) *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+    else
 #pragma unroll
     for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
 }
@@ -80,11 +84,120 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[VEC
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) u[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     if constexpr (VEC == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-    else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    else *reinterpret_cast<uint32_t*>(p) = u[0];
+}
+
+// VEC consecutive elements as they lie in memory, fetched ahead of their use.
+template <typename T, int VEC>
+struct RawRow {
+    static constexpr int W = VEC * (int)sizeof(T) / 4;
+    uint32_t u[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (W == 1) {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (W == 2) {
+            const uint2 t = *reinterpret_cast<const uint2*>(p);
+            u[0] = t.x; u[1] = t.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const uint4 t = reinterpret_cast<const uint4*>(p)[i / 4];
+                u[i] = t.x; u[i + 1] = t.y; u[i + 2] = t.z; u[i + 3] = t.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) u[i] = 0;
+    }
+    __device__ __forceinline__ void get(float (&x)[VEC]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[i] = __uint_as_float(u[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+// A thread's own ring of rows on their way from global memory: SLOTS rows of VEC elements, each asked for by the
+// thread itself and read by it alone, so that no barrier is needed and a row in flight takes no registers.  Slots of
+// the block's threads lie side by side.  Rows are asked for in groups; wait<P>() returns when all groups but the
+// last P are there.
+template <typename T, int VEC, int SLOTS, int THREADS>
+struct Ring {
+    static constexpr int BYTES = VEC * (int)sizeof(T);
+    static constexpr int kSmem = SLOTS * BYTES * THREADS;
+    uint32_t at;
+    __device__ __forceinline__ explicit Ring(void* smem)
+        : at(static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * (BYTES < 16 ? BYTES : 16)) {}
+    __device__ __forceinline__ void ask(int slot, const T* p) {
+        const uint32_t to = at + slot * (BYTES * THREADS);
+        if constexpr (BYTES == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p) : "memory");
+        else if constexpr (BYTES == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
+        else
+#pragma unroll
+            for (int i = 0; i < BYTES; i += 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * THREADS),
+                             "l"(reinterpret_cast<const char*>(p) + i)
+                             : "memory");
+    }
+    __device__ __forceinline__ void clear(int slot) const {
+        const uint32_t to = at + slot * (BYTES * THREADS);
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (i / 4) * 16 * THREADS + (i % 4) * 4), "r"(0) : "memory");
+    }
+    __device__ __forceinline__ void read(int slot, float (&x)[VEC]) const {
+        RawRow<T, VEC> r;
+        read(slot, r);
+        r.get(x);
+    }
+    __device__ __forceinline__ void read(int slot, RawRow<T, VEC>& r) const {
+        const uint32_t from = at + slot * (BYTES * THREADS);
+        if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.u[0]) : "r"(from) : "memory");
+        else if constexpr (BYTES == 8)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.u[0]), "=r"(r.u[1]) : "r"(from) : "memory");
+        else
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r.u[4 * i]), "=r"(r.u[4 * i + 1]), "=r"(r.u[4 * i + 2]), "=r"(r.u[4 * i + 3])
+                             : "r"(from + i * 16 * THREADS)
+                             : "memory");
+    }
+};
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int P>
+__device__ __forceinline__ void ring_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(P) : "memory"); }
+
+__device__ __forceinline__ float exp2_hw(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + e^-x) from the hardware exponential and reciprocal (six instructions with its product): an absolute 1e-7, and
+// relative (4 + 1.16 max(-x, 0)) 2^-23.  Where e^-x overflows the reciprocal is 0, as it should be.
+__device__ __forceinline__ float sigmoid_hw(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp2_hw(x * -1.4426950408889634f)));
+    return y;
 }
 
 // The step and the log decay of one token: dt = softplus(a + bias), g = -rate dt with rate = exp(A_log).
 __device__ __forceinline__ float ssm_softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
+
+// Lets a kernel have `smem` bytes of dynamic shared memory, where that is more than any kernel may have unasked.
+template <class K>
+cudaError_t allow_smem(K kernel, int smem) {
+    if (smem <= 20 * 1024) return cudaSuccess;  // beside 28 KB of static arrays at most
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
 
 // ---- launchers (called from abi_ssm.cu after argument checks) -------------------------------------
 
