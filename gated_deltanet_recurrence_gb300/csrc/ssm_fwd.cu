@@ -287,11 +287,13 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool reverse, cudaStrea
 }  // namespace ssm
 
 size_t ssm_fwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
+    if (dtype == GDN_BF16) return 0;
     const size_t slots = (size_t)ssm::slots_of(num_seqs, total_T);
     return ssm::align256(slots * H * ssm::kGateRows * ssm::kC * sizeof(float)) + slots * H * P * N * sizeof(float);
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
+    if (a.dtype == GDN_BF16 && a.seqs.total_T > 0) return ssm::launch_tc(a, s);
     ssm::Work w{};
     const size_t slots = (size_t)ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
     w.gates = static_cast<float*>(a.workspace);

@@ -1,0 +1,529 @@
+// ssm_tc.cu -- the selective state space scan over packed bf16 prompts on the tensor cores (tcgen05), in one kernel.
+//
+// The chunked form (see ssm_fwd.cu) with chunks of 128 tokens.  A block takes one (sequence, head, 64 rows of the
+// state) and walks along its chunks; nothing but inputs, outputs and the states at both ends touches memory.  Per
+// chunk four products, accumulated in TMEM:
+//   CB = C B^T                         [128 tokens x 128 tokens], exact inputs
+//   CS = C [S hi | S mid]              [128 tokens x 64 | 64], the state at the chunk's start in two bf16 planes
+//   U  = B^T [V hi | V mid | V lo]     [N x 64 | 64 | 64], V_j = e^{G_last - G_j} dt_j x_j in three planes
+//   MX = (CB o decays dt) X            [128 tokens x 64], its left side in two planes, from TMEM
+// The planes of a factor lie side by side, so that the other one is read once for all of them (an instruction with
+// N = 64 is bound by reading the left operand); their results are added in registers.  The state itself, in fp32,
+// is the registers of four warps, 64 a thread: S <- e^{G_last} S + U with rounded additions (the tensor cores cut
+// sums off, which a state carried through many chunks would keep).
+//
+// Warps: 0 - 3 tokens (a thread is a token: masked decays, outputs), 4 - 7 state (a thread is a state column
+// [the N side], and a token where V is formed), 8 issues the MMAs, 9 the loads, 10 forms the gates.  Decays of pairs
+// of tokens in different runs of 32 are products of two factors that are at most 1; inside a run they are exponentials
+// of differences of sums in two floats.
+//
+// Every mbarrier wait is bounded; when one runs out the kernel records GDN_ERR_TIMEOUT, every role leaves its loop,
+// copies and MMAs in flight are waited for (bounded), TMEM is freed.
+#include <cudaTypedefs.h>
+
+#include "sm100_ptx.cuh"
+#include "ssm_chunk.cuh"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+using namespace ptx;
+
+constexpr int kT = 128;                    // tokens of a chunk
+constexpr int kBlock = kT * 128;           // bytes of a tile of 128 rows and 64 columns
+constexpr uint64_t kLimit = 2000000000ull;  // ns, bound on any wait
+constexpr int kThreads = 11 * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Bar { FB0, FB1, EB0, EB1, FC, EC, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
+
+template <int N>
+struct Lay {
+    static constexpr int nb = N / 64;  // tiles of B and of C
+    static constexpr int b = 0, c = b + 2 * nb * kBlock, x = c + nb * kBlock, v = x + 2 * kBlock, s = v + 3 * kBlock,
+                         gates = s + 2 * kBlock, gate_rows = 6, gate_bytes = (gate_rows * kT + 8) * 4,
+                         bars = gates + 2 * gate_bytes, bytes = bars + kBars * 8 + 16;
+};
+// rows of the gates of a chunk: sums from the start of the token's run of 32 in two floats (log2), e^{sums to the run's
+// end} dt, dt, e^{sums to the chunk's end} dt, e^{sums from the chunk's start}; then e^{total} of the runs and of the chunk
+enum Gate { kPh, kPl, kQ, kDt, kW, kB };
+
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+// 16-byte chunk c of row r of a tile
+__device__ __forceinline__ uint32_t at16(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mC,
+              SsmArgs a) {
+    using L = Lay<N>;
+    constexpr int NB = L::nb;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sm = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint32_t* tbase = reinterpret_cast<uint32_t*>(smem + L::bars + kBars * 8);
+    volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kBars * 8 + 4);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
+    const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kT - 1) / kT;
+    const int g = h / (a.H / a.G);
+    const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
+
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i) {
+            const bool all = i == VR || i == SR || i == MR || i == YE || i == EX0 || i == EX1;
+            mbar_init(&bars[i], all ? 128 : (i == GE0 || i == GE1 ? 256 : (i == GF0 || i == GF1 ? 32 : 1)));
+        }
+        *dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(tbase, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = *tbase;
+    const uint32_t tU = tm, tCS = tm + 192, tMX = tm + 320, tCB = tm + 384;
+
+    // false once the wait has run out or another role has given up
+    const auto wait = [&](int bar, int index) -> bool {
+        if (mbar_try_wait(&bars[bar], index & 1, 100000u)) return true;
+        const long long limit = static_cast<long long>(kLimit) * 21 / 10, t0 = clock64();
+        while (!mbar_try_wait(&bars[bar], index & 1, 100000u)) {
+            if (*dead) return false;
+            if (clock64() - t0 > limit) {
+                record_error(a.err, GDN_ERR_TIMEOUT);
+                *dead = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    // a whole warp's wait: all lanes go on or none
+    const auto warp_wait = [&](int bar, int index) -> bool { return __all_sync(0xffffffffu, wait(bar, index)); };
+    const auto gates_of = [&](int c) { return reinterpret_cast<float*>(smem + L::gates + (c & 1) * L::gate_bytes); };
+
+    if (warp < 4) {
+        // ================= tokens =================
+        const int i = tid;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const float D = a.D ? a.D[h] : 0.f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long)bos * a.H + h) * a.P + s * 64;
+        const long out_stride = (long)a.H * a.P;
+        for (int c = 0; c < chunks; ++c) {
+            const float* gt = gates_of(c);
+            if (!warp_wait(GF0 + (c & 1), c >> 1)) break;
+            const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i], bi = gt[kB * kT + i];
+            // e^{sums from the end of run u to this token}, for the runs before this token's
+            float rf[3];
+            {
+                const float* et = gt + L::gate_rows * kT;
+                float f = exp2_hw(ph + pl);
+#pragma unroll
+                for (int u = 2; u >= 0; --u) {
+                    rf[u] = f;  // read for u < warp only
+                    if (u < warp) f *= et[u];
+                }
+                // rf[u] for u < warp: the factors of the runs between u and warp
+            }
+            if (!warp_wait(CBD, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t r[32], o[32];
+                if (u > warp) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0;
+                } else {
+                    tmem_ld32(tCB + lanes + 32 * u, r);
+                    tmem_wait_ld();
+                    float m[32];
+                    if (u < warp) {
+                        const float f = u == 0 ? rf[0] : (u == 1 ? rf[1] : rf[2]);
+                        const float4* q = reinterpret_cast<const float4*>(gt + kQ * kT + 32 * u);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 t = q[j];
+                            m[4 * j] = __uint_as_float(r[4 * j]) * t.x * f;
+                            m[4 * j + 1] = __uint_as_float(r[4 * j + 1]) * t.y * f;
+                            m[4 * j + 2] = __uint_as_float(r[4 * j + 2]) * t.z * f;
+                            m[4 * j + 3] = __uint_as_float(r[4 * j + 3]) * t.w * f;
+                        }
+                    } else {
+                        const float4* qh = reinterpret_cast<const float4*>(gt + kPh * kT + 32 * u);
+                        const float4* ql = reinterpret_cast<const float4*>(gt + kPl * kT + 32 * u);
+                        const float4* qd = reinterpret_cast<const float4*>(gt + kDt * kT + 32 * u);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 th = qh[j], tl = ql[j], td = qd[j];
+                            const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int t = 4 * j + e;
+                                m[t] = t <= lane ? __uint_as_float(r[t]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])) : 0.f;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float x = m[2 * j], y = m[2 * j + 1];
+                        o[j] = bfp::peel(x, y);
+                        o[16 + j] = pack_bf16(x, y);
+                    }
+                }
+                tmem_st32(tCB + lanes + 32 * u, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars[MR]);
+            if (!warp_wait(YD, c)) break;
+            tc_fence_after();
+            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t hi[32], mid[32], mx[32];
+                tmem_ld32(tCS + lanes + 32 * half, hi);
+                tmem_ld32(tCS + lanes + 64 + 32 * half, mid);
+                tmem_ld32(tMX + lanes + 32 * half, mx);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t at = at16(xt, i, half * 4 + k);
+                    uint32_t u[4];
+                    planes::lds128(at, u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 8 * k + 2 * e;
+                        const float y0 = fmaf(bi, __uint_as_float(hi[j]) + __uint_as_float(mid[j]), __uint_as_float(mx[j]));
+                        const float y1 = fmaf(bi, __uint_as_float(hi[j + 1]) + __uint_as_float(mid[j + 1]), __uint_as_float(mx[j + 1]));
+                        u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
+                    }
+                    planes::sts128(at, u);  // y takes x's place
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[YE]);
+            mbar_arrive(&bars[GE0 + (c & 1)]);
+            __syncwarp();
+            const int len = min(eos - bos - c * kT, kT);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = warp * 32 + 4 * k + (lane >> 3), col = lane & 7;
+                if (r < len) {
+                    uint32_t u[4];
+                    planes::lds128(at16(xt, r, col), u);
+                    *reinterpret_cast<uint4*>(out + ((long)c * kT + r) * out_stride + col * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[EX0 + (c & 1)]);
+        }
+    } else if (warp < 8) {
+        // ================= state =================
+        const int r = tid - 128;
+        const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+        const bool holds = r < N;
+        float S[64];
+#pragma unroll
+        for (int p = 0; p < 64; ++p) S[p] = holds && a.initial_state ? a.initial_state[row0 + (long)p * N + r] : 0.f;
+        float decay = 0.f;
+        bool ok = true;
+        const auto add_update = [&]() {
+            tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t hi[32], mid[32], lo[32];
+                tmem_ld32(tU + lanes + 32 * half, hi);
+                tmem_ld32(tU + lanes + 64 + 32 * half, mid);
+                tmem_ld32(tU + lanes + 128 + 32 * half, lo);
+                tmem_wait_ld();
+#pragma unroll
+                for (int p = 0; p < 32; ++p)
+                    S[32 * half + p] = fmaf(decay, S[32 * half + p], __uint_as_float(hi[p]) + (__uint_as_float(mid[p]) + __uint_as_float(lo[p])));
+            }
+            tc_fence_before();
+        };
+        for (int c = 0; c < chunks; ++c) {
+            if (c > 0) {
+                if (!(ok = warp_wait(UD, c - 1))) break;
+                add_update();
+                if (!(ok = warp_wait(CSD, c - 1))) break;
+            }
+            if (holds) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t hi[4], mid[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = S[8 * k + 2 * e], y = S[8 * k + 2 * e + 1];
+                        hi[e] = bfp::peel(x, y);
+                        mid[e] = pack_bf16(x, y);
+                    }
+                    planes::sts128(at16(sm + L::s, r, k), hi);
+                    planes::sts128(at16(sm + L::s + kBlock, r, k), mid);
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[SR]);
+            // V of token r; rows past the sequence's end become zeros wherever they are summed over
+            if (!(ok = warp_wait(GF0 + (c & 1), c >> 1))) break;
+            const float* gt = gates_of(c);
+            const float w = gt[kW * kT + r];
+            decay = gt[L::gate_rows * kT + 4];
+            mbar_arrive(&bars[GE0 + (c & 1)]);
+            if (!(ok = warp_wait(FX0 + (c & 1), c >> 1))) break;
+            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
+            if (r < eos - bos - c * kT) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t u[4], v[3][4];
+                    planes::lds128(at16(xt, r, k), u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t t[3];
+                        bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
+                        v[0][e] = t[0];
+                        v[1][e] = t[1];
+                        v[2][e] = t[2];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) planes::sts128(at16(sm + L::v + q * kBlock, r, k), v[q]);
+                }
+            }
+            if (c + 1 == chunks) {
+                if (!(ok = warp_wait(FB0 + (c & 1), c >> 1))) break;
+                if (r >= eos - bos - c * kT) {
+                    const uint32_t zero[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        planes::sts128(at16(xt, r, k), zero);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) planes::sts128(at16(sm + L::v + q * kBlock, r, k), zero);
+#pragma unroll
+                        for (int q = 0; q < NB; ++q) planes::sts128(at16(sm + L::b + ((c & 1) * NB + q) * kBlock, r, k), zero);
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[VR]);
+        }
+        if (ok && chunks > 0) {
+            ok = warp_wait(UD, chunks - 1);
+            if (ok) add_update();
+        }
+        if (ok && holds && a.final_state) {
+#pragma unroll
+            for (int p = 0; p < 64; ++p) a.final_state[row0 + (long)p * N + r] = S[p];
+        }
+    } else if (warp == 8) {
+        // ================= MMAs =================
+        if (lane == 0) {
+            constexpr uint32_t idCB = idesc_bf16(128, 128, 0, 0), idCS = idesc_bf16(128, 128, 0, 1), idU = idesc_bf16(128, 192, 1, 1),
+                               idMX = idesc_bf16(128, 64, 0, 1);
+            const uint64_t dCk = sdesc_sw128(sm + L::c, 16, 1024), dS = sdesc_sw128(sm + L::s, kBlock, 1024),
+                           dV = sdesc_sw128(sm + L::v, kBlock, 1024);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1;
+                const uint32_t bt = sm + L::b + st * NB * kBlock;
+                const uint64_t dBk = sdesc_sw128(bt, 16, 1024), dBm = sdesc_sw128(bt, kBlock, 1024),
+                               dX = sdesc_sw128(sm + L::x + st * kBlock, kBlock, 1024);
+                if (!wait(FB0 + st, c >> 1) || !wait(FC, c)) break;
+                if (c > 0 && !wait(YD, c - 1)) break;  // MX has read the masked products that CB overwrites
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < N / 16; ++k) {
+                    const uint64_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                    mma_bf16_ss(tCB, dCk + off, dBk + off, idCB, k > 0);
+                }
+                mma_commit(&bars[CBD]);
+                if (!wait(SR, c)) break;
+                if (c > 0 && !wait(YE, c - 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < N / 16; ++k)
+                    mma_bf16_ss(tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
+                mma_commit(&bars[CSD]);
+                mma_commit(&bars[EC]);
+                if (!wait(VR, c)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kT / 16; ++k) mma_bf16_ss(tU, dBm + k * 128, dV + k * 128, idU, k > 0);
+                mma_commit(&bars[UD]);
+                mma_commit(&bars[EB0 + st]);
+                if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 1; q >= 0; --q)
+#pragma unroll
+                    for (int k = 0; k < kT / 16; ++k)
+                        mma_bf16_ts(tMX, tCB + 32 * (k >> 1) + 16 * q + 8 * (k & 1), dX + k * 128, idMX, q == 0 || k > 0);
+                mma_commit(&bars[YD]);
+            }
+            if (chunks > 0) {  // MMAs in flight, after a wait that ran out, end before TMEM is freed
+                mma_commit(&bars[DR]);
+                mbar_wait(&bars[DR], 0, kLimit);
+            }
+        }
+    } else if (warp == 9) {
+        // ================= loads =================
+        if (lane == 0) {
+            int nb = 0, nc = 0, nx = 0;  // loads issued
+            const int xc = h * a.P + s * 64, gc = g * N;
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c & 1, t0 = bos + c * kT;
+                if (c >= 2 && !wait(EB0 + st, (c >> 1) - 1)) break;
+                mbar_arrive_expect_tx(&bars[FB0 + st], NB * kBlock);
+                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::b + (st * NB + q) * kBlock, &mB, &bars[FB0 + st], gc + 64 * q, t0);
+                ++nb;
+                if (c >= 2 && !wait(EX0 + st, (c >> 1) - 1)) break;
+                mbar_arrive_expect_tx(&bars[FX0 + st], kBlock);
+                tma_load_2d(smem + L::x + st * kBlock, &mX, &bars[FX0 + st], xc, t0);
+                ++nx;
+                if (c >= 1 && !wait(EC, c - 1)) break;
+                mbar_arrive_expect_tx(&bars[FC], NB * kBlock);
+                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::c + q * kBlock, &mC, &bars[FC], gc + 64 * q, t0);
+                ++nc;
+                if (c + 1 < chunks)
+                    for (int q = 0; q < NB; ++q) prefetch_2d(&mC, gc + 64 * q, t0 + kT);
+            }
+            // the last loads have landed before the block may leave
+            for (int k = max(0, nb - 2); k < nb; ++k) mbar_wait(&bars[FB0 + (k & 1)], (k >> 1) & 1, kLimit);
+            for (int k = max(0, nx - 2); k < nx; ++k) mbar_wait(&bars[FX0 + (k & 1)], (k >> 1) & 1, kLimit);
+            if (nc > 0) mbar_wait(&bars[FC], (nc - 1) & 1, kLimit);
+        }
+    } else {
+        // ================= gates =================
+        const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        float z[4];
+        const auto fetch = [&](int c) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = bos + c * kT + 4 * lane + e;
+                z[e] = t < eos ? a.a[(long)t * a.H + h] : 0.f;
+            }
+        };
+        if (chunks > 0) fetch(0);
+        for (int c = 0; c < chunks; ++c) {
+            const int left = eos - bos - c * kT - 4 * lane;  // this lane's tokens inside the sequence
+            float dt[4], gl[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dt[e] = e < left ? ssm_softplus(z[e] + bias) : 0.f;
+                gl[e] = e < left ? fmaxf(-rate * dt[e], kMinLog) : 0.f;
+            }
+            if (c + 1 < chunks) fetch(c + 1);
+            // sums inside the run of 32 (eight lanes): from its start, in two floats, and to its end
+            Two pre[4];
+            pre[0] = Two{gl[0], 0.f};
+#pragma unroll
+            for (int e = 1; e < 4; ++e) pre[e] = two_add(pre[e - 1], Two{gl[e], 0.f});
+            Two run = pre[3];
+            float suf = (gl[0] + gl[1]) + (gl[2] + gl[3]);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const Two up{__shfl_up_sync(0xffffffffu, run.h, o, 8), __shfl_up_sync(0xffffffffu, run.l, o, 8)};
+                const float down = __shfl_down_sync(0xffffffffu, suf, o, 8);
+                if ((lane & 7) >= o) run = two_add(up, run);
+                if ((lane & 7) + o < 8) suf += down;
+            }
+            Two before{__shfl_up_sync(0xffffffffu, run.h, 1, 8), __shfl_up_sync(0xffffffffu, run.l, 1, 8)};
+            if ((lane & 7) == 0) before = Two{0.f, 0.f};
+            float behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+            if ((lane & 7) == 7) behind = 0.f;
+            float tot[4], head = 0.f, tail = 0.f, all = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                tot[u] = __shfl_sync(0xffffffffu, run.h, 8 * u + 7);
+                if (u < lane >> 3) head += tot[u];
+                if (u > lane >> 3) tail += tot[u];
+                all += tot[u];
+            }
+            if (c >= 2 && !warp_wait(GE0 + (c & 1), (c >> 1) - 1)) break;
+            float* gt = gates_of(c);
+            float ph[4], pl[4], q[4], w[4], b[4];
+#pragma unroll
+            for (int e = 3; e >= 0; --e) {
+                const Two p = two_add(before, pre[e]);
+                ph[e] = p.h * kLog2e;
+                // the product's rounding, and the low part
+                pl[e] = fmaf(p.h, kLog2e, -ph[e]) + p.l * kLog2e + p.h * 1.9259629911266175e-8f;
+                q[e] = expf(behind) * dt[e];
+                w[e] = expf(behind + tail) * dt[e];
+                b[e] = expf(head + p.h);
+                behind += gl[e];
+            }
+            const auto put = [&](int row, const float (&x)[4]) {
+                *reinterpret_cast<float4*>(gt + row * kT + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+            };
+            put(kPh, ph);
+            put(kPl, pl);
+            put(kQ, q);
+            put(kDt, dt);
+            put(kW, w);
+            put(kB, b);
+            if (lane < 4) gt[L::gate_rows * kT + lane] = expf(lane == 0 ? tot[0] : (lane == 1 ? tot[1] : (lane == 2 ? tot[2] : tot[3])));
+            if (lane == 4) gt[L::gate_rows * kT + 4] = expf(all);
+            mbar_arrive(&bars[GF0 + (c & 1)]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        const bool got = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                         q == cudaDriverEntryPointSuccess;
+        return got ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// Rows of `width` bf16 elements, `stride` apart, in boxes of 128 rows and 64 columns; rows past the last read as zeros.
+bool map_rows(CUtensorMap* m, const void* base, long rows, long width, long stride) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, kT}, es[2] = {1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+cudaError_t launch(const SsmArgs& a, cudaStream_t s) {
+    CUtensorMap mX, mB, mC;
+    const long T = a.seqs.total_T;
+    if (!encoder() || !map_rows(&mX, a.x, T, (long)a.H * a.P, a.x_stride) || !map_rows(&mB, a.B, T, (long)a.G * N, a.B_stride) ||
+        !map_rows(&mC, a.C, T, (long)a.G * N, a.C_stride))
+        return cudaErrorInvalidValue;
+    const auto kernel = ssm_tc_kernel<N>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), kThreads, Lay<N>::bytes, s>>>(mX, mB, mC, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s) { return a.N == 128 ? launch<128>(a, s) : launch<64>(a, s); }
+
+}  // namespace ssm
+}  // namespace gdn

@@ -393,7 +393,7 @@ int gdn_short_conv_bwd(const void* dout, const void* x, long x_stride, const flo
 size_t gdn_short_conv_bwd_workspace_size(int num_seqs, int total_T, int dim);
 
 /*
- * gdn_ssm_chunk_fwd -- the selective state space scan over packed prompts, in chunks of 64 tokens.
+ * gdn_ssm_chunk_fwd -- the selective state space scan over packed prompts, in chunks of tokens.
  * Per head h, with dt_t = softplus(a_t + dt_bias) and a state S [d_head, d_state]:
  *   S_t = exp(-exp(A_log) dt_t) S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D x_t.
  *
@@ -404,8 +404,8 @@ size_t gdn_short_conv_bwd_workspace_size(int num_seqs, int total_T, int dim);
  *   out  [total_T, H, d_head] of dtype.
  *   d_head, d_state  each 64 or 128 (GDN_ERR_UNSUPPORTED otherwise); H at most 16384.
  *   workspace  gdn_ssm_chunk_fwd_workspace_size(...) bytes, 256-byte aligned; may be NULL when that is 0.
- * A NaN or an infinity in a token's inputs reaches the outputs of its chunk (64 tokens of its sequence) and of every
- * later token, and no other sequence.
+ * A NaN or an infinity in a token's inputs reaches the outputs of its chunk (up to 128 tokens of its sequence) and of
+ * every later token, and no other sequence.
  */
 int gdn_ssm_chunk_fwd(const void* x, long x_stride, const void* B, long B_stride, const void* C, long C_stride,
                       const float* a, const float* A_log, const float* dt_bias, const float* D,
