@@ -59,6 +59,15 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
+// 16 consecutive columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 // 16-byte chunk c of row r of a tile
 __device__ __forceinline__ uint32_t at16(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
 
@@ -127,81 +136,77 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             const float* gt = gates_of(c);
             if (!warp_wait(GF0 + (c & 1), c >> 1)) break;
             const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i], bi = gt[kB * kT + i];
-            // e^{sums from the end of run u to this token}, for the runs before this token's
-            float rf[3];
-            {
-                const float* et = gt + L::gate_rows * kT;
-                float f = exp2_hw(ph + pl);
-#pragma unroll
-                for (int u = 2; u >= 0; --u) {
-                    rf[u] = f;  // read for u < warp only
-                    if (u < warp) f *= et[u];
-                }
-                // rf[u] for u < warp: the factors of the runs between u and warp
-            }
             if (!warp_wait(CBD, c)) break;
             tc_fence_after();
+            // loops of small bodies throughout: eleven warps in six roles share the instruction caches
+            const auto put_planes = [&](int u, const float (&m)[32]) {
+                uint32_t o[32];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t r[32], o[32];
-                if (u > warp) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0;
-                } else {
-                    tmem_ld32(tCB + lanes + 32 * u, r);
-                    tmem_wait_ld();
-                    float m[32];
-                    if (u < warp) {
-                        const float f = u == 0 ? rf[0] : (u == 1 ? rf[1] : rf[2]);
-                        const float4* q = reinterpret_cast<const float4*>(gt + kQ * kT + 32 * u);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 t = q[j];
-                            m[4 * j] = __uint_as_float(r[4 * j]) * t.x * f;
-                            m[4 * j + 1] = __uint_as_float(r[4 * j + 1]) * t.y * f;
-                            m[4 * j + 2] = __uint_as_float(r[4 * j + 2]) * t.z * f;
-                            m[4 * j + 3] = __uint_as_float(r[4 * j + 3]) * t.w * f;
-                        }
-                    } else {
-                        const float4* qh = reinterpret_cast<const float4*>(gt + kPh * kT + 32 * u);
-                        const float4* ql = reinterpret_cast<const float4*>(gt + kPl * kT + 32 * u);
-                        const float4* qd = reinterpret_cast<const float4*>(gt + kDt * kT + 32 * u);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 th = qh[j], tl = ql[j], td = qd[j];
-                            const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int t = 4 * j + e;
-                                m[t] = t <= lane ? __uint_as_float(r[t]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])) : 0.f;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float x = m[2 * j], y = m[2 * j + 1];
-                        o[j] = bfp::peel(x, y);
-                        o[16 + j] = pack_bf16(x, y);
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    float x = m[2 * j], y = m[2 * j + 1];
+                    o[j] = bfp::peel(x, y);
+                    o[16 + j] = pack_bf16(x, y);
                 }
                 tmem_st32(tCB + lanes + 32 * u, o);
+            };
+            uint32_t r[32];
+            tmem_ld32(tCB + lanes + 32 * warp, r);
+            {
+                float m[32];
+                tmem_wait_ld();
+                const float4* qh = reinterpret_cast<const float4*>(gt + kPh * kT + 32 * warp);
+                const float4* ql = reinterpret_cast<const float4*>(gt + kPl * kT + 32 * warp);
+                const float4* qd = reinterpret_cast<const float4*>(gt + kDt * kT + 32 * warp);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 th = qh[j], tl = ql[j], td = qd[j];
+                    const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 4 * j + e;
+                        m[t] = t <= lane ? __uint_as_float(r[t]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])) : 0.f;
+                    }
+                }
+                put_planes(warp, m);
             }
+            float f = exp2_hw(ph + pl);  // e^{sums from the end of run u to this token}
+#pragma unroll 1
+            for (int u = warp - 1; u >= 0; --u) {
+                float m[32];
+                tmem_ld32(tCB + lanes + 32 * u, r);
+                tmem_wait_ld();
+                const float4* q = reinterpret_cast<const float4*>(gt + kQ * kT + 32 * u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 t = q[j];
+                    m[4 * j] = __uint_as_float(r[4 * j]) * t.x * f;
+                    m[4 * j + 1] = __uint_as_float(r[4 * j + 1]) * t.y * f;
+                    m[4 * j + 2] = __uint_as_float(r[4 * j + 2]) * t.z * f;
+                    m[4 * j + 3] = __uint_as_float(r[4 * j + 3]) * t.w * f;
+                }
+                put_planes(u, m);
+                f *= gt[L::gate_rows * kT + u];
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0;
+#pragma unroll 1
+            for (int u = warp + 1; u < 4; ++u) tmem_st32(tCB + lanes + 32 * u, r);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars[MR]);
             if (!warp_wait(YD, c)) break;
             tc_fence_after();
             const uint32_t xt = sm + L::x + (c & 1) * kBlock;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t hi[32], mid[32], mx[32];
-                tmem_ld32(tCS + lanes + 32 * half, hi);
-                tmem_ld32(tCS + lanes + 64 + 32 * half, mid);
-                tmem_ld32(tMX + lanes + 32 * half, mx);
+#pragma unroll 1
+            for (int half = 0; half < 4; ++half) {
+                uint32_t hi[16], mid[16], mx[16];
+                tmem_ld16(tCS + lanes + 16 * half, hi);
+                tmem_ld16(tCS + lanes + 64 + 16 * half, mid);
+                tmem_ld16(tMX + lanes + 16 * half, mx);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t at = at16(xt, i, half * 4 + k);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t at = at16(xt, i, half * 2 + k);
                     uint32_t u[4];
                     planes::lds128(at, u);
 #pragma unroll
@@ -219,7 +224,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             mbar_arrive(&bars[GE0 + (c & 1)]);
             __syncwarp();
             const int len = min(eos - bos - c * kT, kT);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < 8; ++k) {
                 const int r = warp * 32 + 4 * k + (lane >> 3), col = lane & 7;
                 if (r < len) {
@@ -241,27 +246,26 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
         for (int p = 0; p < 64; ++p) S[p] = holds && a.initial_state ? a.initial_state[row0 + (long)p * N + r] : 0.f;
         float decay = 0.f;
         bool ok = true;
-        const auto add_update = [&]() {
-            tc_fence_after();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t hi[32], mid[32], lo[32];
-                tmem_ld32(tU + lanes + 32 * half, hi);
-                tmem_ld32(tU + lanes + 64 + 32 * half, mid);
-                tmem_ld32(tU + lanes + 128 + 32 * half, lo);
-                tmem_wait_ld();
-#pragma unroll
-                for (int p = 0; p < 32; ++p)
-                    S[32 * half + p] = fmaf(decay, S[32 * half + p], __uint_as_float(hi[p]) + (__uint_as_float(mid[p]) + __uint_as_float(lo[p])));
-            }
-            tc_fence_before();
-        };
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c <= chunks; ++c) {
             if (c > 0) {
                 if (!(ok = warp_wait(UD, c - 1))) break;
-                add_update();
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t hi[16], mid[16], lo[16];
+                    tmem_ld16(tU + lanes + 16 * k, hi);
+                    tmem_ld16(tU + lanes + 64 + 16 * k, mid);
+                    tmem_ld16(tU + lanes + 128 + 16 * k, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int p = 0; p < 16; ++p)
+                        S[16 * k + p] = fmaf(decay, S[16 * k + p], __uint_as_float(hi[p]) + (__uint_as_float(mid[p]) + __uint_as_float(lo[p])));
+                }
+                tc_fence_before();
+                if (c == chunks) break;
                 if (!(ok = warp_wait(CSD, c - 1))) break;
             }
+            if (c == chunks) break;
             if (holds) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -287,7 +291,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             if (!(ok = warp_wait(FX0 + (c & 1), c >> 1))) break;
             const uint32_t xt = sm + L::x + (c & 1) * kBlock;
             if (r < eos - bos - c * kT) {
-#pragma unroll
+#pragma unroll 2
                 for (int k = 0; k < 8; ++k) {
                     uint32_t u[4], v[3][4];
                     planes::lds128(at16(xt, r, k), u);
@@ -307,7 +311,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 if (!(ok = warp_wait(FB0 + (c & 1), c >> 1))) break;
                 if (r >= eos - bos - c * kT) {
                     const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 8; ++k) {
                         planes::sts128(at16(xt, r, k), zero);
 #pragma unroll
@@ -319,10 +323,6 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             }
             fence_async_smem();
             mbar_arrive(&bars[VR]);
-        }
-        if (ok && chunks > 0) {
-            ok = warp_wait(UD, chunks - 1);
-            if (ok) add_update();
         }
         if (ok && holds && a.final_state) {
 #pragma unroll
