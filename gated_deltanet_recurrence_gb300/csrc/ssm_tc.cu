@@ -5,17 +5,19 @@
 // chunk four products, accumulated in TMEM:
 //   CB = C B^T                         [128 tokens x 128 tokens], exact inputs
 //   CS = C [S hi | S mid]              [128 tokens x 64 | 64], the state at the chunk's start in two bf16 planes
-//   U  = B^T [V hi | V mid | V lo]     [N x 64 | 64 | 64], V_j = e^{G_last - G_j} dt_j x_j in three planes
+//   U  = B^T [V hi | V mid + V lo]     [N x 64 | 64], V_j = e^{G_last - G_j} dt_j x_j in three planes
 //   MX = (CB o decays dt) X            [128 tokens x 64], its left side in two planes, from TMEM
 // The planes of a factor lie side by side, so that the other one is read once for all of them (an instruction with
-// N = 64 is bound by reading the left operand); their results are added in registers.  The state itself, in fp32,
-// is the registers of four warps, 64 a thread: S <- e^{G_last} S + U with rounded additions (the tensor cores cut
-// sums off, which a state carried through many chunks would keep).
+// N = 64 is bound by reading the left operand); their results are added in registers.  The state itself stays in TMEM in
+// fp32 and is taken through registers once a chunk: S <- e^{G_last} S + U with rounded additions (the tensor cores
+// cut sums off, which a state carried through many chunks would keep).
 //
-// Warps: 0 - 3 tokens (a thread is a token: masked decays, outputs), 4 - 7 state (a thread is a state column
-// [the N side], and a token where V is formed), 8 issues the MMAs, 9 the loads, 10 forms the gates.  Decays of pairs
-// of tokens in different runs of 32 are products of two factors that are at most 1; inside a run they are exponentials
-// of differences of sums in two floats.
+// Warps: 0 - 7 tokens (a thread is a token and half of what its row needs: masked decays, outputs), 8 - 15 state (a
+// thread is a state column [the N side] and half of its 64 rows, and half a token's row where V is formed), 16 issues the
+// MMAs, 17 the loads, 18 forms the gates.  Decays of pairs of tokens in different runs of 32 are products of two
+// factors that are at most 1; inside a run they are exponentials of differences of sums in two floats.
+// The bodies of all loops are a few dozen instructions: nineteen warps in five roles share the instruction caches,
+// and straight code was fetched no faster than an instruction in four cycles.
 //
 // Every mbarrier wait is bounded; when one runs out the kernel records GDN_ERR_TIMEOUT, every role leaves its loop,
 // copies and MMAs in flight are waited for (bounded), TMEM is freed.
@@ -33,7 +35,8 @@ using namespace ptx;
 constexpr int kT = 128;                    // tokens of a chunk
 constexpr int kBlock = kT * 128;           // bytes of a tile of 128 rows and 64 columns
 constexpr uint64_t kLimit = 2000000000ull;  // ns, bound on any wait
-constexpr int kThreads = 11 * 32;
+constexpr int kWorkers = 256;              // threads of a role's two sets of four warps
+constexpr int kThreads = 2 * kWorkers + 3 * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum Bar { FB0, FB1, EB0, EB1, FC, EC, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
@@ -49,24 +52,59 @@ struct Lay {
 // end} dt, dt, e^{sums to the chunk's end} dt, e^{sums from the chunk's start}; then e^{total} of the runs and of the chunk
 enum Gate { kPh, kPl, kQ, kDt, kW, kB };
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// MMAs issued by the elected thread of a warp that runs as one (its operands stay in uniform registers): left operand
+// from shared memory, or from TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
         : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar) {
+    if (on) mma_commit(bar);
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on;
 }
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
-// 16 consecutive columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
+// eight consecutive columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Polls until the phase completes; false when another role has given up, or the bound has passed (recorded).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, int* err) {
+    const long long limit = static_cast<long long>(kLimit) * 21 / 10, t0 = clock64();
+    while (!mbar_try_wait(bar, parity, 100000u)) {
+        if (*dead) return false;
+        if (clock64() - t0 > limit) {
+            record_error(err, GDN_ERR_TIMEOUT);
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
 }
 // 16-byte chunk c of row r of a tile
 __device__ __forceinline__ uint32_t at16(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
@@ -82,328 +120,323 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
     uint32_t* tbase = reinterpret_cast<uint32_t*>(smem + L::bars + kBars * 8);
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kBars * 8 + 4);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
-    const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kT - 1) / kT;
+    const int bos = __shfl_sync(0xffffffffu, a.seqs.bos(n), 0), eos = __shfl_sync(0xffffffffu, a.seqs.bos(n + 1), 0);
+    const int chunks = (eos - bos + kT - 1) / kT;
     const int g = h / (a.H / a.G);
     const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const bool all = i == VR || i == SR || i == MR || i == YE || i == EX0 || i == EX1;
-            mbar_init(&bars[i], all ? 128 : (i == GE0 || i == GE1 ? 256 : (i == GF0 || i == GF1 ? 32 : 1)));
+            mbar_init(&bars[i], all ? kWorkers : (i == GE0 || i == GE1 ? 2 * kWorkers : (i == GF0 || i == GF1 ? 32 : 1)));
         }
         *dead = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tmem_alloc(tbase, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = *tbase;
-    const uint32_t tU = tm, tCS = tm + 192, tMX = tm + 320, tCB = tm + 384;
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
+    const uint32_t tU = tm, tS = tm + 128, tCS = tm + 192, tMX = tm + 320, tCB = tm + 384;
 
-    // false once the wait has run out or another role has given up
+    // the completion number `index` of a barrier; false once a wait has run out here or elsewhere.  A whole warp goes on
+    // or none of it.
     const auto wait = [&](int bar, int index) -> bool {
-        if (mbar_try_wait(&bars[bar], index & 1, 100000u)) return true;
-        const long long limit = static_cast<long long>(kLimit) * 21 / 10, t0 = clock64();
-        while (!mbar_try_wait(&bars[bar], index & 1, 100000u)) {
-            if (*dead) return false;
-            if (clock64() - t0 > limit) {
-                record_error(a.err, GDN_ERR_TIMEOUT);
-                *dead = 1;
-                return false;
-            }
-        }
-        return true;
+        bool ok = mbar_try_wait(&bars[bar], index & 1, 100000u);
+        if (!ok) ok = wait_slow(&bars[bar], index & 1, dead, a.err);
+        return __all_sync(0xffffffffu, ok);
     };
-    // a whole warp's wait: all lanes go on or none
-    const auto warp_wait = [&](int bar, int index) -> bool { return __all_sync(0xffffffffu, wait(bar, index)); };
     const auto gates_of = [&](int c) { return reinterpret_cast<float*>(smem + L::gates + (c & 1) * L::gate_bytes); };
 
-    if (warp < 4) {
+    if (warp < 8) {
         // ================= tokens =================
-        const int i = tid;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const int q = warp & 3, half = warp >> 2, i = q * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        // which runs of columns this warp masks: of the rows' q + 1 and the zeros behind them, about half each
+        const uint32_t mine = half ? (q == 0 ? 14u : (q == 1 ? 10u : 12u)) : (q == 0 ? 1u : (q == 1 ? 5u : 3u));
         const float D = a.D ? a.D[h] : 0.f;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long)bos * a.H + h) * a.P + s * 64;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long)bos * a.H + h) * a.P + s * 64 + half * 32;
         const long out_stride = (long)a.H * a.P;
         for (int c = 0; c < chunks; ++c) {
             const float* gt = gates_of(c);
-            if (!warp_wait(GF0 + (c & 1), c >> 1)) break;
+            if (!wait(GF0 + (c & 1), c >> 1)) break;
             const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i], bi = gt[kB * kT + i];
-            if (!warp_wait(CBD, c)) break;
+            if (!wait(CBD, c)) break;
             tc_fence_after();
-            // loops of small bodies throughout: eleven warps in six roles share the instruction caches
-            const auto put_planes = [&](int u, const float (&m)[32]) {
-                uint32_t o[32];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float x = m[2 * j], y = m[2 * j + 1];
-                    o[j] = bfp::peel(x, y);
-                    o[16 + j] = pack_bf16(x, y);
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+                if (!(mine >> u & 1)) continue;
+                const uint32_t at = tCB + lanes + 32 * u;
+                if (u > q) {
+                    const uint32_t zero[8] = {};
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) tmem_st8(at + 8 * k, zero);
+                    continue;
                 }
-                tmem_st32(tCB + lanes + 32 * u, o);
-            };
-            uint32_t r[32];
-            tmem_ld32(tCB + lanes + 32 * warp, r);
-            {
-                float m[32];
-                tmem_wait_ld();
-                const float4* qh = reinterpret_cast<const float4*>(gt + kPh * kT + 32 * warp);
-                const float4* ql = reinterpret_cast<const float4*>(gt + kPl * kT + 32 * warp);
-                const float4* qd = reinterpret_cast<const float4*>(gt + kDt * kT + 32 * warp);
+                float f = exp2_hw(ph + pl);  // e^{sums from the end of run u to this token}
+                for (int v = u + 1; v < q; ++v) f *= gt[L::gate_rows * kT + v];
+                // the two planes of sixteen columns, eight words each, take those columns' place
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t r[2][8], hi[8], lo[8];
+                    tmem_ld8(at + 16 * k, r[0]);
+                    tmem_ld8(at + 16 * k + 8, r[1]);
+                    const float* base = gt + 32 * u + 16 * k;
+                    tmem_wait_ld();
+                    if (u == q) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 th = qh[j], tl = ql[j], td = qd[j];
-                    const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 th = *reinterpret_cast<const float4*>(base + kPh * kT + j);
+                            const float4 tl = *reinterpret_cast<const float4*>(base + kPl * kT + j);
+                            const float4 td = *reinterpret_cast<const float4*>(base + kDt * kT + j);
+                            const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = 4 * j + e;
-                        m[t] = t <= lane ? __uint_as_float(r[t]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])) : 0.f;
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t& x = r[j >> 3][(j & 7) + e];
+                                x = 16 * k + j + e <= lane
+                                        ? __float_as_uint(__uint_as_float(x) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])))
+                                        : 0u;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(base + kQ * kT + j);
+                            const float ts[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t& x = r[j >> 3][(j & 7) + e];
+                                x = __float_as_uint(__uint_as_float(x) * ts[e] * f);
+                            }
+                        }
                     }
-                }
-                put_planes(warp, m);
-            }
-            float f = exp2_hw(ph + pl);  // e^{sums from the end of run u to this token}
-#pragma unroll 1
-            for (int u = warp - 1; u >= 0; --u) {
-                float m[32];
-                tmem_ld32(tCB + lanes + 32 * u, r);
-                tmem_wait_ld();
-                const float4* q = reinterpret_cast<const float4*>(gt + kQ * kT + 32 * u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 t = q[j];
-                    m[4 * j] = __uint_as_float(r[4 * j]) * t.x * f;
-                    m[4 * j + 1] = __uint_as_float(r[4 * j + 1]) * t.y * f;
-                    m[4 * j + 2] = __uint_as_float(r[4 * j + 2]) * t.z * f;
-                    m[4 * j + 3] = __uint_as_float(r[4 * j + 3]) * t.w * f;
+                    for (int j = 0; j < 8; ++j) {
+                        float x = __uint_as_float(r[j >> 2][2 * (j & 3)]), y = __uint_as_float(r[j >> 2][2 * (j & 3) + 1]);
+                        hi[j] = bfp::peel(x, y);
+                        lo[j] = pack_bf16(x, y);
+                    }
+                    tmem_st8(at + 16 * k, hi);
+                    tmem_st8(at + 16 * k + 8, lo);
                 }
-                put_planes(u, m);
-                f *= gt[L::gate_rows * kT + u];
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0;
-#pragma unroll 1
-            for (int u = warp + 1; u < 4; ++u) tmem_st32(tCB + lanes + 32 * u, r);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars[MR]);
-            if (!warp_wait(YD, c)) break;
+            if (!wait(YD, c)) break;
             tc_fence_after();
             const uint32_t xt = sm + L::x + (c & 1) * kBlock;
 #pragma unroll 1
-            for (int half = 0; half < 4; ++half) {
-                uint32_t hi[16], mid[16], mx[16];
-                tmem_ld16(tCS + lanes + 16 * half, hi);
-                tmem_ld16(tCS + lanes + 64 + 16 * half, mid);
-                tmem_ld16(tMX + lanes + 16 * half, mx);
+            for (int k = 0; k < 4; ++k) {
+                uint32_t hi[8], mid[8], mx[8], u[4];
+                const int col = half * 32 + 8 * k;
+                tmem_ld8(tCS + lanes + col, hi);
+                tmem_ld8(tCS + lanes + 64 + col, mid);
+                tmem_ld8(tMX + lanes + col, mx);
+                const uint32_t at = at16(xt, i, half * 4 + k);
+                planes::lds128(at, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t at = at16(xt, i, half * 2 + k);
-                    uint32_t u[4];
-                    planes::lds128(at, u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = 8 * k + 2 * e;
-                        const float y0 = fmaf(bi, __uint_as_float(hi[j]) + __uint_as_float(mid[j]), __uint_as_float(mx[j]));
-                        const float y1 = fmaf(bi, __uint_as_float(hi[j + 1]) + __uint_as_float(mid[j + 1]), __uint_as_float(mx[j + 1]));
-                        u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
-                    }
-                    planes::sts128(at, u);  // y takes x's place
+                for (int e = 0; e < 4; ++e) {
+                    const float y0 = fmaf(bi, __uint_as_float(hi[2 * e]) + __uint_as_float(mid[2 * e]), __uint_as_float(mx[2 * e]));
+                    const float y1 = fmaf(bi, __uint_as_float(hi[2 * e + 1]) + __uint_as_float(mid[2 * e + 1]), __uint_as_float(mx[2 * e + 1]));
+                    u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
                 }
+                planes::sts128(at, u);  // y takes x's place
             }
             tc_fence_before();
             mbar_arrive(&bars[YE]);
             mbar_arrive(&bars[GE0 + (c & 1)]);
             __syncwarp();
             const int len = min(eos - bos - c * kT, kT);
-#pragma unroll 2
-            for (int k = 0; k < 8; ++k) {
-                const int r = warp * 32 + 4 * k + (lane >> 3), col = lane & 7;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {  // eight rows of 64 bytes at a time
+                const int r = q * 32 + 8 * k + (lane >> 2), col = lane & 3;
                 if (r < len) {
                     uint32_t u[4];
-                    planes::lds128(at16(xt, r, col), u);
+                    planes::lds128(at16(xt, r, half * 4 + col), u);
                     *reinterpret_cast<uint4*>(out + ((long)c * kT + r) * out_stride + col * 8) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
             }
             fence_async_smem();
             mbar_arrive(&bars[EX0 + (c & 1)]);
         }
-    } else if (warp < 8) {
+    } else if (warp < 16) {
         // ================= state =================
-        const int r = tid - 128;
-        const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+        const int q = warp & 3, half = (warp >> 2) & 1, r = q * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const bool holds = r < N;
-        float S[64];
-#pragma unroll
-        for (int p = 0; p < 64; ++p) S[p] = holds && a.initial_state ? a.initial_state[row0 + (long)p * N + r] : 0.f;
         float decay = 0.f;
-        bool ok = true;
         for (int c = 0; c <= chunks; ++c) {
             if (c > 0) {
-                if (!(ok = warp_wait(UD, c - 1))) break;
+                if (!wait(UD, c - 1)) break;
+                if (c < chunks && !wait(CSD, c - 1)) break;
                 tc_fence_after();
+            }
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int col = half * 32 + 8 * k;
+                float S[8];
+                if (c == 0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t hi[16], mid[16], lo[16];
-                    tmem_ld16(tU + lanes + 16 * k, hi);
-                    tmem_ld16(tU + lanes + 64 + 16 * k, mid);
-                    tmem_ld16(tU + lanes + 128 + 16 * k, lo);
+                    for (int p = 0; p < 8; ++p) S[p] = holds && a.initial_state ? a.initial_state[row0 + (long)(col + p) * N + r] : 0.f;
+                } else {
+                    uint32_t old[8], hi[8], mid[8];
+                    tmem_ld8(tS + lanes + col, old);
+                    tmem_ld8(tU + lanes + col, hi);
+                    tmem_ld8(tU + lanes + 64 + col, mid);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int p = 0; p < 16; ++p)
-                        S[16 * k + p] = fmaf(decay, S[16 * k + p], __uint_as_float(hi[p]) + (__uint_as_float(mid[p]) + __uint_as_float(lo[p])));
+                    for (int p = 0; p < 8; ++p)
+                        S[p] = fmaf(decay, __uint_as_float(old[p]), __uint_as_float(hi[p]) + __uint_as_float(mid[p]));
                 }
-                tc_fence_before();
-                if (c == chunks) break;
-                if (!(ok = warp_wait(CSD, c - 1))) break;
-            }
-            if (c == chunks) break;
-            if (holds) {
+                if (c == chunks) {
+                    if (holds && a.final_state) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t hi[4], mid[4];
+                        for (int p = 0; p < 8; ++p) a.final_state[row0 + (long)(col + p) * N + r] = S[p];
+                    }
+                    continue;
+                }
+                uint32_t v[8], hi[4], mid[4];
+#pragma unroll
+                for (int p = 0; p < 8; ++p) v[p] = __float_as_uint(S[p]);
+                tmem_st8(tS + lanes + col, v);
+                if (holds) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = S[8 * k + 2 * e], y = S[8 * k + 2 * e + 1];
-                        hi[e] = bfp::peel(x, y);
-                        mid[e] = pack_bf16(x, y);
+                        hi[e] = bfp::peel(S[2 * e], S[2 * e + 1]);
+                        mid[e] = pack_bf16(S[2 * e], S[2 * e + 1]);
                     }
-                    planes::sts128(at16(sm + L::s, r, k), hi);
-                    planes::sts128(at16(sm + L::s + kBlock, r, k), mid);
+                    planes::sts128(at16(sm + L::s, r, half * 4 + k), hi);
+                    planes::sts128(at16(sm + L::s + kBlock, r, half * 4 + k), mid);
                 }
             }
+            if (c == chunks) break;
+            tmem_wait_st();
             fence_async_smem();
+            tc_fence_before();
             mbar_arrive(&bars[SR]);
             // V of token r; rows past the sequence's end become zeros wherever they are summed over
-            if (!(ok = warp_wait(GF0 + (c & 1), c >> 1))) break;
+            if (!wait(GF0 + (c & 1), c >> 1)) break;
             const float* gt = gates_of(c);
             const float w = gt[kW * kT + r];
             decay = gt[L::gate_rows * kT + 4];
             mbar_arrive(&bars[GE0 + (c & 1)]);
-            if (!(ok = warp_wait(FX0 + (c & 1), c >> 1))) break;
+            if (!wait(FX0 + (c & 1), c >> 1)) break;
             const uint32_t xt = sm + L::x + (c & 1) * kBlock;
-            if (r < eos - bos - c * kT) {
-#pragma unroll 2
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t u[4], v[3][4];
-                    planes::lds128(at16(xt, r, k), u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t t[3];
-                        bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
-                        v[0][e] = t[0];
-                        v[1][e] = t[1];
-                        v[2][e] = t[2];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 3; ++q) planes::sts128(at16(sm + L::v + q * kBlock, r, k), v[q]);
-                }
-            }
-            if (c + 1 == chunks) {
-                if (!(ok = warp_wait(FB0 + (c & 1), c >> 1))) break;
-                if (r >= eos - bos - c * kT) {
-                    const uint32_t zero[4] = {0, 0, 0, 0};
+            const bool last = c + 1 == chunks;
+            if (last && !wait(FB0 + (c & 1), c >> 1)) break;
+            const bool live = r < eos - bos - c * kT;
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        planes::sts128(at16(xt, r, k), zero);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q) planes::sts128(at16(sm + L::v + q * kBlock, r, k), zero);
-#pragma unroll
-                        for (int q = 0; q < NB; ++q) planes::sts128(at16(sm + L::b + ((c & 1) * NB + q) * kBlock, r, k), zero);
-                    }
+            for (int k = half * 4; k < half * 4 + 4; ++k) {
+                uint32_t u[4] = {0, 0, 0, 0}, v[3][4];
+                if (live) planes::lds128(at16(xt, r, k), u);
+                else {
+                    planes::sts128(at16(xt, r, k), u);
+                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::b + ((c & 1) * NB + b) * kBlock, r, k), u);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t t[3];
+                    bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
+                    v[0][e] = t[0];
+                    v[1][e] = t[1];
+                    v[2][e] = t[2];
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::v + p * kBlock, r, k), v[p]);
             }
             fence_async_smem();
             mbar_arrive(&bars[VR]);
         }
-        if (ok && holds && a.final_state) {
-#pragma unroll
-            for (int p = 0; p < 64; ++p) a.final_state[row0 + (long)p * N + r] = S[p];
-        }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ================= MMAs =================
-        if (lane == 0) {
-            constexpr uint32_t idCB = idesc_bf16(128, 128, 0, 0), idCS = idesc_bf16(128, 128, 0, 1), idU = idesc_bf16(128, 192, 1, 1),
-                               idMX = idesc_bf16(128, 64, 0, 1);
-            const uint64_t dCk = sdesc_sw128(sm + L::c, 16, 1024), dS = sdesc_sw128(sm + L::s, kBlock, 1024),
-                           dV = sdesc_sw128(sm + L::v, kBlock, 1024);
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1;
-                const uint32_t bt = sm + L::b + st * NB * kBlock;
-                const uint64_t dBk = sdesc_sw128(bt, 16, 1024), dBm = sdesc_sw128(bt, kBlock, 1024),
-                               dX = sdesc_sw128(sm + L::x + st * kBlock, kBlock, 1024);
-                if (!wait(FB0 + st, c >> 1) || !wait(FC, c)) break;
-                if (c > 0 && !wait(YD, c - 1)) break;  // MX has read the masked products that CB overwrites
-                tc_fence_after();
+        constexpr uint32_t idCB = idesc_bf16(128, 128, 0, 0), idCS = idesc_bf16(128, 128, 0, 1), idU = idesc_bf16(128, 128, 1, 1),
+                           idUl = idesc_bf16(128, 64, 1, 1), idMX = idesc_bf16(128, 64, 0, 1);
+        const uint32_t on = elect();
+        const uint64_t dCk = sdesc_sw128(sm + L::c, 16, 1024), dS = sdesc_sw128(sm + L::s, kBlock, 1024),
+                       dV = sdesc_sw128(sm + L::v, kBlock, 1024);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            const uint32_t bt = sm + L::b + st * NB * kBlock;
+            const uint64_t dBk = sdesc_sw128(bt, 16, 1024), dBm = sdesc_sw128(bt, kBlock, 1024),
+                           dX = sdesc_sw128(sm + L::x + st * kBlock, kBlock, 1024);
+            if (!wait(FB0 + st, c >> 1) || !wait(FC, c)) break;
+            if (c > 0 && !wait(YD, c - 1)) break;  // MX has read the masked products that CB overwrites
+            tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < N / 16; ++k) {
-                    const uint64_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
-                    mma_bf16_ss(tCB, dCk + off, dBk + off, idCB, k > 0);
-                }
-                mma_commit(&bars[CBD]);
-                if (!wait(SR, c)) break;
-                if (c > 0 && !wait(YE, c - 1)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < N / 16; ++k)
-                    mma_bf16_ss(tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
-                mma_commit(&bars[CSD]);
-                mma_commit(&bars[EC]);
-                if (!wait(VR, c)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kT / 16; ++k) mma_bf16_ss(tU, dBm + k * 128, dV + k * 128, idU, k > 0);
-                mma_commit(&bars[UD]);
-                mma_commit(&bars[EB0 + st]);
-                if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int q = 1; q >= 0; --q)
-#pragma unroll
-                    for (int k = 0; k < kT / 16; ++k)
-                        mma_bf16_ts(tMX, tCB + 32 * (k >> 1) + 16 * q + 8 * (k & 1), dX + k * 128, idMX, q == 0 || k > 0);
-                mma_commit(&bars[YD]);
+            for (int k = 0; k < N / 16; ++k) {
+                const uint64_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                mma_ss(on, tCB, dCk + off, dBk + off, idCB, k > 0);
             }
-            if (chunks > 0) {  // MMAs in flight, after a wait that ran out, end before TMEM is freed
-                mma_commit(&bars[DR]);
-                mbar_wait(&bars[DR], 0, kLimit);
-            }
+            commit(on, &bars[CBD]);
+            if (!wait(SR, c)) break;
+            if (c > 0 && !wait(YE, c - 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k)
+                mma_ss(on, tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
+            commit(on, &bars[CSD]);
+            commit(on, &bars[EC]);
+            if (!wait(VR, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU, dBm + k * 128, dV + k * 128, idU, k > 0);
+#pragma unroll
+            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dBm + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
+            commit(on, &bars[UD]);
+            commit(on, &bars[EB0 + st]);
+            if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < kT / 16; ++k) mma_ts(on, tMX, tCB + 16 * k + 8 * p, dX + k * 128, idMX, p == 0 || k > 0);
+            commit(on, &bars[YD]);
         }
-    } else if (warp == 9) {
+        if (chunks > 0) {  // MMAs in flight, after a wait that ran out, end before TMEM is freed
+            commit(on, &bars[DR]);
+            mbar_wait(&bars[DR], 0, kLimit);
+        }
+    } else if (warp == 17) {
         // ================= loads =================
-        if (lane == 0) {
-            int nb = 0, nc = 0, nx = 0;  // loads issued
-            const int xc = h * a.P + s * 64, gc = g * N;
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1, t0 = bos + c * kT;
-                if (c >= 2 && !wait(EB0 + st, (c >> 1) - 1)) break;
+        const uint32_t on = elect();
+        int nb = 0, nc = 0, nx = 0;  // loads issued
+        const int xc = h * a.P + s * 64, gc = g * N;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1, t0 = bos + c * kT;
+            if (c >= 2 && !wait(EB0 + st, (c >> 1) - 1)) break;
+            if (on) {
                 mbar_arrive_expect_tx(&bars[FB0 + st], NB * kBlock);
                 for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::b + (st * NB + q) * kBlock, &mB, &bars[FB0 + st], gc + 64 * q, t0);
-                ++nb;
-                if (c >= 2 && !wait(EX0 + st, (c >> 1) - 1)) break;
+            }
+            ++nb;
+            if (c >= 2 && !wait(EX0 + st, (c >> 1) - 1)) break;
+            if (on) {
                 mbar_arrive_expect_tx(&bars[FX0 + st], kBlock);
                 tma_load_2d(smem + L::x + st * kBlock, &mX, &bars[FX0 + st], xc, t0);
-                ++nx;
-                if (c >= 1 && !wait(EC, c - 1)) break;
+            }
+            ++nx;
+            if (c >= 1 && !wait(EC, c - 1)) break;
+            if (on) {
                 mbar_arrive_expect_tx(&bars[FC], NB * kBlock);
                 for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::c + q * kBlock, &mC, &bars[FC], gc + 64 * q, t0);
-                ++nc;
                 if (c + 1 < chunks)
                     for (int q = 0; q < NB; ++q) prefetch_2d(&mC, gc + 64 * q, t0 + kT);
             }
-            // the last loads have landed before the block may leave
-            for (int k = max(0, nb - 2); k < nb; ++k) mbar_wait(&bars[FB0 + (k & 1)], (k >> 1) & 1, kLimit);
-            for (int k = max(0, nx - 2); k < nx; ++k) mbar_wait(&bars[FX0 + (k & 1)], (k >> 1) & 1, kLimit);
-            if (nc > 0) mbar_wait(&bars[FC], (nc - 1) & 1, kLimit);
+            ++nc;
         }
+        // the last loads have landed before the block may leave
+        for (int k = max(0, nb - 2); k < nb; ++k) mbar_wait(&bars[FB0 + (k & 1)], (k >> 1) & 1, kLimit);
+        for (int k = max(0, nx - 2); k < nx; ++k) mbar_wait(&bars[FX0 + (k & 1)], (k >> 1) & 1, kLimit);
+        if (nc > 0) mbar_wait(&bars[FC], (nc - 1) & 1, kLimit);
     } else {
         // ================= gates =================
         const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -451,7 +484,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 if (u > lane >> 3) tail += tot[u];
                 all += tot[u];
             }
-            if (c >= 2 && !warp_wait(GE0 + (c & 1), (c >> 1) - 1)) break;
+            if (c >= 2 && !wait(GE0 + (c & 1), (c >> 1) - 1)) break;
             float* gt = gates_of(c);
             float ph[4], pl[4], q[4], w[4], b[4];
 #pragma unroll
@@ -481,7 +514,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
