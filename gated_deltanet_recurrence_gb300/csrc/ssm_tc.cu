@@ -12,10 +12,11 @@
 // fp32 and is taken through registers once a chunk: S <- e^{G_last} S + U with rounded additions (the tensor cores
 // cut sums off, which a state carried through many chunks would keep).
 //
-// Warps: 0 - 7 tokens (a thread is a token and half of what its row needs: masked decays, outputs), 8 - 15 state (a
-// thread is a state column [the N side] and half of its 64 rows, and half a token's row where V is formed), 16 issues the
-// MMAs, 17 the loads, 18 forms the gates.  Decays of pairs of tokens in different runs of 32 are products of two
-// factors that are at most 1; inside a run they are exponentials of differences of sums in two floats.
+// Warps: 0 - 7 form the masked products M of a chunk and, while M X and the next C B^T run, the V of the next chunk (a
+// thread is a token and half of what its row needs); 8 - 15 take the state on (a thread is a state column [the N side]
+// and half of its 64 rows) and the outputs out (a token and half its row); 16 issues the MMAs, 17 the loads, 18 forms
+// the gates.  Decays of pairs of tokens in different runs of 32 are products of two factors that are at most 1; inside a
+// run they are exponentials of differences of sums in two floats.
 // The bodies of all loops are a few dozen instructions: nineteen warps in five roles share the instruction caches,
 // and straight code was fetched no faster than an instruction in four cycles.
 //
@@ -81,7 +82,14 @@ __device__ __forceinline__ uint32_t elect() {
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
-// eight consecutive columns of this thread's TMEM lane
+// 16 and eight consecutive columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -156,18 +164,47 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     const auto gates_of = [&](int c) { return reinterpret_cast<float*>(smem + L::gates + (c & 1) * L::gate_bytes); };
 
     if (warp < 8) {
-        // ================= tokens =================
+        // ================= masked products and V =================
         const int q = warp & 3, half = warp >> 2, i = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         // which runs of columns this warp masks: of the rows' q + 1 and the zeros behind them, about half each
         const uint32_t mine = half ? (q == 0 ? 14u : (q == 1 ? 10u : 12u)) : (q == 0 ? 1u : (q == 1 ? 5u : 3u));
-        const float D = a.D ? a.D[h] : 0.f;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long)bos * a.H + h) * a.P + s * 64 + half * 32;
-        const long out_stride = (long)a.H * a.P;
+        // V of this token; rows past the sequence's end become zeros wherever they are summed over
+        const auto form_v = [&](int c) -> bool {
+            if (!wait(GF0 + (c & 1), c >> 1)) return false;
+            const float w = gates_of(c)[kW * kT + i];
+            if (!wait(FX0 + (c & 1), c >> 1)) return false;
+            if (c + 1 == chunks && !wait(FB0 + (c & 1), c >> 1)) return false;
+            if (c > 0 && !wait(UD, c - 1)) return false;
+            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
+            const bool live = i < eos - bos - c * kT;
+#pragma unroll 1
+            for (int k = half * 4; k < half * 4 + 4; ++k) {
+                uint32_t u[4] = {0, 0, 0, 0}, v[3][4];
+                if (live) planes::lds128(at16(xt, i, k), u);
+                else {
+                    planes::sts128(at16(xt, i, k), u);
+                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::b + ((c & 1) * NB + b) * kBlock, i, k), u);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t t[3];
+                    bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
+                    v[0][e] = t[0];
+                    v[1][e] = t[1];
+                    v[2][e] = t[2];
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::v + p * kBlock, i, k), v[p]);
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[VR]);
+            return true;
+        };
         for (int c = 0; c < chunks; ++c) {
+            if (c == 0 && !form_v(0)) break;
             const float* gt = gates_of(c);
-            if (!wait(GF0 + (c & 1), c >> 1)) break;
-            const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i], bi = gt[kB * kT + i];
+            const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i];
             if (!wait(CBD, c)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -183,13 +220,16 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 float f = exp2_hw(ph + pl);  // e^{sums from the end of run u to this token}
                 for (int v = u + 1; v < q; ++v) f *= gt[L::gate_rows * kT + v];
                 // the two planes of sixteen columns, eight words each, take those columns' place
+                uint32_t next[16];
+                tmem_ld16(at, next);
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t r[2][8], hi[8], lo[8];
-                    tmem_ld8(at + 16 * k, r[0]);
-                    tmem_ld8(at + 16 * k + 8, r[1]);
-                    const float* base = gt + 32 * u + 16 * k;
+                    uint32_t r[16], hi[8], lo[8];
                     tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = next[j];
+                    if (k == 0) tmem_ld16(at + 16, next);
+                    const float* base = gt + 32 * u + 16 * k;
                     if (u == q) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
@@ -198,12 +238,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                             const float4 td = *reinterpret_cast<const float4*>(base + kDt * kT + j);
                             const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t& x = r[j >> 3][(j & 7) + e];
-                                x = 16 * k + j + e <= lane
-                                        ? __float_as_uint(__uint_as_float(x) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])))
-                                        : 0u;
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                r[j + e] = 16 * k + j + e <= lane
+                                               ? __float_as_uint(__uint_as_float(r[j + e]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])))
+                                               : 0u;
                         }
                     } else {
 #pragma unroll
@@ -211,15 +249,12 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                             const float4 t = *reinterpret_cast<const float4*>(base + kQ * kT + j);
                             const float ts[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t& x = r[j >> 3][(j & 7) + e];
-                                x = __float_as_uint(__uint_as_float(x) * ts[e] * f);
-                            }
+                            for (int e = 0; e < 4; ++e) r[j + e] = __float_as_uint(__uint_as_float(r[j + e]) * ts[e] * f);
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float x = __uint_as_float(r[j >> 2][2 * (j & 3)]), y = __uint_as_float(r[j >> 2][2 * (j & 3) + 1]);
+                        float x = __uint_as_float(r[2 * j]), y = __uint_as_float(r[2 * j + 1]);
                         hi[j] = bfp::peel(x, y);
                         lo[j] = pack_bf16(x, y);
                     }
@@ -230,51 +265,20 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars[MR]);
-            if (!wait(YD, c)) break;
-            tc_fence_after();
-            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                uint32_t hi[8], mid[8], mx[8], u[4];
-                const int col = half * 32 + 8 * k;
-                tmem_ld8(tCS + lanes + col, hi);
-                tmem_ld8(tCS + lanes + 64 + col, mid);
-                tmem_ld8(tMX + lanes + col, mx);
-                const uint32_t at = at16(xt, i, half * 4 + k);
-                planes::lds128(at, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y0 = fmaf(bi, __uint_as_float(hi[2 * e]) + __uint_as_float(mid[2 * e]), __uint_as_float(mx[2 * e]));
-                    const float y1 = fmaf(bi, __uint_as_float(hi[2 * e + 1]) + __uint_as_float(mid[2 * e + 1]), __uint_as_float(mx[2 * e + 1]));
-                    u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
-                }
-                planes::sts128(at, u);  // y takes x's place
-            }
-            tc_fence_before();
-            mbar_arrive(&bars[YE]);
             mbar_arrive(&bars[GE0 + (c & 1)]);
-            __syncwarp();
-            const int len = min(eos - bos - c * kT, kT);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {  // eight rows of 64 bytes at a time
-                const int r = q * 32 + 8 * k + (lane >> 2), col = lane & 3;
-                if (r < len) {
-                    uint32_t u[4];
-                    planes::lds128(at16(xt, r, half * 4 + col), u);
-                    *reinterpret_cast<uint4*>(out + ((long)c * kT + r) * out_stride + col * 8) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-            }
-            fence_async_smem();
-            mbar_arrive(&bars[EX0 + (c & 1)]);
+            if (c + 1 < chunks && !form_v(c + 1)) break;
         }
     } else if (warp < 16) {
-        // ================= state =================
+        // ================= state and outputs =================
         const int q = warp & 3, half = (warp >> 2) & 1, r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const bool holds = r < N;
+        const float D = a.D ? a.D[h] : 0.f;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long)bos * a.H + h) * a.P + s * 64 + half * 32;
+        const long out_stride = (long)a.H * a.P;
         float decay = 0.f;
         for (int c = 0; c <= chunks; ++c) {
+            // the state at the start of chunk c
             if (c > 0) {
                 if (!wait(UD, c - 1)) break;
                 if (c < chunks && !wait(CSD, c - 1)) break;
@@ -318,43 +322,55 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                     planes::sts128(at16(sm + L::s + kBlock, r, half * 4 + k), mid);
                 }
             }
-            if (c == chunks) break;
-            tmem_wait_st();
-            fence_async_smem();
-            tc_fence_before();
-            mbar_arrive(&bars[SR]);
-            // V of token r; rows past the sequence's end become zeros wherever they are summed over
-            if (!wait(GF0 + (c & 1), c >> 1)) break;
-            const float* gt = gates_of(c);
-            const float w = gt[kW * kT + r];
-            decay = gt[L::gate_rows * kT + 4];
-            mbar_arrive(&bars[GE0 + (c & 1)]);
-            if (!wait(FX0 + (c & 1), c >> 1)) break;
-            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
-            const bool last = c + 1 == chunks;
-            if (last && !wait(FB0 + (c & 1), c >> 1)) break;
-            const bool live = r < eos - bos - c * kT;
+            if (c < chunks) {
+                tmem_wait_st();
+                fence_async_smem();
+                tc_fence_before();
+                mbar_arrive(&bars[SR]);
+                if (!wait(GF0 + (c & 1), c >> 1)) break;
+                decay = gates_of(c)[L::gate_rows * kT + 4];
+            }
+            if (c == 0) continue;
+            // the outputs of chunk c - 1: token r
+            const int d = c - 1;
+            const float bi = gates_of(d)[kB * kT + r];
+            if (!wait(YD, d)) break;
+            tc_fence_after();
+            const uint32_t xt = sm + L::x + (d & 1) * kBlock;
 #pragma unroll 1
-            for (int k = half * 4; k < half * 4 + 4; ++k) {
-                uint32_t u[4] = {0, 0, 0, 0}, v[3][4];
-                if (live) planes::lds128(at16(xt, r, k), u);
-                else {
-                    planes::sts128(at16(xt, r, k), u);
-                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::b + ((c & 1) * NB + b) * kBlock, r, k), u);
-                }
+            for (int k = 0; k < 4; ++k) {
+                uint32_t hi[8], mid[8], mx[8], u[4];
+                const int col = half * 32 + 8 * k;
+                tmem_ld8(tCS + lanes + col, hi);
+                tmem_ld8(tCS + lanes + 64 + col, mid);
+                tmem_ld8(tMX + lanes + col, mx);
+                const uint32_t at = at16(xt, r, half * 4 + k);
+                planes::lds128(at, u);
+                tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint32_t t[3];
-                    bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
-                    v[0][e] = t[0];
-                    v[1][e] = t[1];
-                    v[2][e] = t[2];
+                    const float y0 = fmaf(bi, __uint_as_float(hi[2 * e]) + __uint_as_float(mid[2 * e]), __uint_as_float(mx[2 * e]));
+                    const float y1 = fmaf(bi, __uint_as_float(hi[2 * e + 1]) + __uint_as_float(mid[2 * e + 1]), __uint_as_float(mx[2 * e + 1]));
+                    u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
                 }
-#pragma unroll
-                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::v + p * kBlock, r, k), v[p]);
+                planes::sts128(at, u);  // y takes x's place
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[YE]);
+            mbar_arrive(&bars[GE0 + (d & 1)]);
+            __syncwarp();
+            const int len = min(eos - bos - d * kT, kT);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {  // eight rows of 64 bytes at a time
+                const int t = q * 32 + 8 * k + (lane >> 2), col = lane & 3;
+                if (t < len) {
+                    uint32_t u[4];
+                    planes::lds128(at16(xt, t, half * 4 + col), u);
+                    *reinterpret_cast<uint4*>(out + ((long)d * kT + t) * out_stride + col * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
             }
             fence_async_smem();
-            mbar_arrive(&bars[VR]);
+            mbar_arrive(&bars[EX0 + (d & 1)]);
         }
     } else if (warp == 16) {
         // ================= MMAs =================
@@ -377,15 +393,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 mma_ss(on, tCB, dCk + off, dBk + off, idCB, k > 0);
             }
             commit(on, &bars[CBD]);
-            if (!wait(SR, c)) break;
-            if (c > 0 && !wait(YE, c - 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < N / 16; ++k)
-                mma_ss(on, tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
-            commit(on, &bars[CSD]);
-            commit(on, &bars[EC]);
-            if (!wait(VR, c)) break;
+            if (!wait(SR, c) || !wait(VR, c)) break;  // (SR: the state has taken the former U in)
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU, dBm + k * 128, dV + k * 128, idU, k > 0);
@@ -393,6 +401,13 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dBm + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
             commit(on, &bars[UD]);
             commit(on, &bars[EB0 + st]);
+            if (c > 0 && !wait(YE, c - 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k)
+                mma_ss(on, tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
+            commit(on, &bars[CSD]);
+            commit(on, &bars[EC]);
             if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
             tc_fence_after();
 #pragma unroll
