@@ -40,18 +40,19 @@ constexpr int kWorkers = 256;              // threads of a role's two sets of fo
 constexpr int kThreads = 2 * kWorkers + 3 * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Bar { FB0, FB1, EB0, EB1, FC, EC, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
+enum Bar { FB, EB, FC0, FC1, EC0, EC1, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
 
 template <int N>
 struct Lay {
     static constexpr int nb = N / 64;  // tiles of B and of C
-    static constexpr int b = 0, c = b + 2 * nb * kBlock, x = c + nb * kBlock, v = x + 2 * kBlock, s = v + 3 * kBlock,
+    static constexpr int b = 0, c = b + nb * kBlock, x = c + 2 * nb * kBlock, v = x + 2 * kBlock, s = v + 3 * kBlock,
                          gates = s + 2 * kBlock, gate_rows = 6, gate_bytes = (gate_rows * kT + 8) * 4,
                          bars = gates + 2 * gate_bytes, bytes = bars + kBars * 8 + 16;
 };
-// rows of the gates of a chunk: sums from the start of the token's run of 32 in two floats (log2), e^{sums to the run's
-// end} dt, dt, e^{sums to the chunk's end} dt, e^{sums from the chunk's start}; then e^{total} of the runs and of the chunk
-enum Gate { kPh, kPl, kQ, kDt, kW, kB };
+// rows of the gates of a chunk: sums from the start of the token's run of 32 in two floats (log2), the second less log2 dt,
+// e^{sums to the run's end} dt, e^{sums to the chunk's end} dt, e^{sums from the chunk's start}; then e^{total} of the runs
+// and of the chunk
+enum Gate { kPh, kPl, kPd, kQ, kW, kB };
 
 // MMAs issued by the elected thread of a warp that runs as one (its operands stay in uniform registers): left operand
 // from shared memory, or from TMEM.
@@ -174,25 +175,24 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             if (!wait(GF0 + (c & 1), c >> 1)) return false;
             const float w = gates_of(c)[kW * kT + i];
             if (!wait(FX0 + (c & 1), c >> 1)) return false;
-            if (c + 1 == chunks && !wait(FB0 + (c & 1), c >> 1)) return false;
+            if (c + 1 == chunks && !wait(FB, c)) return false;
             if (c > 0 && !wait(UD, c - 1)) return false;
             const uint32_t xt = sm + L::x + (c & 1) * kBlock;
             const bool live = i < eos - bos - c * kT;
-#pragma unroll 1
+#pragma unroll 2
             for (int k = half * 4; k < half * 4 + 4; ++k) {
                 uint32_t u[4] = {0, 0, 0, 0}, v[3][4];
                 if (live) planes::lds128(at16(xt, i, k), u);
                 else {
                     planes::sts128(at16(xt, i, k), u);
-                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::b + ((c & 1) * NB + b) * kBlock, i, k), u);
+                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::b + b * kBlock, i, k), u);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint32_t t[3];
-                    bfp::split<3>(w * __uint_as_float(u[e] << 16), w * __uint_as_float(u[e] & 0xffff0000u), t);
-                    v[0][e] = t[0];
-                    v[1][e] = t[1];
-                    v[2][e] = t[2];
+                    bfp::F2 t = bfp::widen(u[e]) * bfp::F2(w, w);
+                    v[0][e] = bfp::peel(t);
+                    v[1][e] = bfp::peel(t);
+                    v[2][e] = bfp::pack(t);
                 }
 #pragma unroll
                 for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::v + p * kBlock, i, k), v[p]);
@@ -205,6 +205,14 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             if (c == 0 && !form_v(0)) break;
             const float* gt = gates_of(c);
             const float ph = gt[kPh * kT + i], pl = gt[kPl * kT + i];
+            // e^{sums from the end of run u to this token} for this warp's runs before the token's
+            float f0 = exp2_hw(ph + pl), f1 = f0;
+            if (q == 3 && half == 0) {
+                f1 = f0 * gt[L::gate_rows * kT + 2];
+                f0 = f1 * gt[L::gate_rows * kT + 1];
+            } else if (q == 2 && half == 0) {
+                f0 *= gt[L::gate_rows * kT + 1];
+            }
             if (!wait(CBD, c)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -217,14 +225,14 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                     for (int k = 0; k < 4; ++k) tmem_st8(at + 8 * k, zero);
                     continue;
                 }
-                float f = exp2_hw(ph + pl);  // e^{sums from the end of run u to this token}
-                for (int v = u + 1; v < q; ++v) f *= gt[L::gate_rows * kT + v];
+                const float f = u & 1 ? f1 : f0;
                 // the two planes of sixteen columns, eight words each, take those columns' place
                 uint32_t next[16];
                 tmem_ld16(at, next);
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     uint32_t r[16], hi[8], lo[8];
+                    bfp::F2 m[8];
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = next[j];
@@ -234,29 +242,33 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 th = *reinterpret_cast<const float4*>(base + kPh * kT + j);
-                            const float4 tl = *reinterpret_cast<const float4*>(base + kPl * kT + j);
-                            const float4 td = *reinterpret_cast<const float4*>(base + kDt * kT + j);
-                            const float hs[4] = {th.x, th.y, th.z, th.w}, ls[4] = {tl.x, tl.y, tl.z, tl.w}, ds[4] = {td.x, td.y, td.z, td.w};
+                            const float4 td = *reinterpret_cast<const float4*>(base + kPd * kT + j);
+                            const bfp::F2 one(-1.f, -1.f);
+                            bfp::F2 d[2] = {bfp::fma2(bfp::F2(th.x, th.y), one, bfp::F2(ph, ph)) + bfp::fma2(bfp::F2(td.x, td.y), one, bfp::F2(pl, pl)),
+                                            bfp::fma2(bfp::F2(th.z, th.w), one, bfp::F2(ph, ph)) + bfp::fma2(bfp::F2(td.z, td.w), one, bfp::F2(pl, pl))};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                r[j + e] = 16 * k + j + e <= lane
-                                               ? __float_as_uint(__uint_as_float(r[j + e]) * ds[e] * exp2_hw((ph - hs[e]) + (pl - ls[e])))
-                                               : 0u;
+                            for (int e = 0; e < 2; ++e) {
+                                float x, y;
+                                d[e].get(x, y);
+                                (bfp::F2::of(r[j + 2 * e], r[j + 2 * e + 1]) * bfp::F2(exp2_hw(x), exp2_hw(y))).get(x, y);
+                                // what lies behind the token is selected away
+                                x = 16 * k + j + 2 * e <= lane ? x : 0.f;
+                                y = 16 * k + j + 2 * e + 1 <= lane ? y : 0.f;
+                                m[j / 2 + e] = bfp::F2(x, y);
+                            }
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 t = *reinterpret_cast<const float4*>(base + kQ * kT + j);
-                            const float ts[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) r[j + e] = __float_as_uint(__uint_as_float(r[j + e]) * ts[e] * f);
+                            m[j / 2] = bfp::F2::of(r[j], r[j + 1]) * bfp::F2(t.x, t.y) * bfp::F2(f, f);
+                            m[j / 2 + 1] = bfp::F2::of(r[j + 2], r[j + 3]) * bfp::F2(t.z, t.w) * bfp::F2(f, f);
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float x = __uint_as_float(r[2 * j]), y = __uint_as_float(r[2 * j + 1]);
-                        hi[j] = bfp::peel(x, y);
-                        lo[j] = pack_bf16(x, y);
+                        hi[j] = bfp::peel(m[j]);
+                        lo[j] = bfp::pack(m[j]);
                     }
                     tmem_st8(at + 16 * k, hi);
                     tmem_st8(at + 16 * k + 8, lo);
@@ -284,13 +296,16 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 if (c < chunks && !wait(CSD, c - 1)) break;
                 tc_fence_after();
             }
-#pragma unroll 1
+#pragma unroll 2
             for (int k = 0; k < 4; ++k) {
                 const int col = half * 32 + 8 * k;
-                float S[8];
+                bfp::F2 S[4];
                 if (c == 0) {
 #pragma unroll
-                    for (int p = 0; p < 8; ++p) S[p] = holds && a.initial_state ? a.initial_state[row0 + (long)(col + p) * N + r] : 0.f;
+                    for (int p = 0; p < 8; p += 2) {
+                        const float* from = a.initial_state + row0 + (long)(col + p) * N + r;
+                        S[p / 2] = holds && a.initial_state ? bfp::F2(from[0], from[N]) : bfp::F2(0.f, 0.f);
+                    }
                 } else {
                     uint32_t old[8], hi[8], mid[8];
                     tmem_ld8(tS + lanes + col, old);
@@ -298,25 +313,29 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                     tmem_ld8(tU + lanes + 64 + col, mid);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        S[p] = fmaf(decay, __uint_as_float(old[p]), __uint_as_float(hi[p]) + __uint_as_float(mid[p]));
+                    for (int p = 0; p < 8; p += 2)
+                        S[p / 2] = bfp::fma2(bfp::F2(decay, decay), bfp::F2::of(old[p], old[p + 1]),
+                                             bfp::F2::of(hi[p], hi[p + 1]) + bfp::F2::of(mid[p], mid[p + 1]));
                 }
+                float v[8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) S[p].get(v[2 * p], v[2 * p + 1]);
                 if (c == chunks) {
                     if (holds && a.final_state) {
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) a.final_state[row0 + (long)(col + p) * N + r] = S[p];
+                        for (int p = 0; p < 8; ++p) a.final_state[row0 + (long)(col + p) * N + r] = v[p];
                     }
                     continue;
                 }
-                uint32_t v[8], hi[4], mid[4];
+                uint32_t w[8], hi[4], mid[4];
 #pragma unroll
-                for (int p = 0; p < 8; ++p) v[p] = __float_as_uint(S[p]);
-                tmem_st8(tS + lanes + col, v);
+                for (int p = 0; p < 8; ++p) w[p] = __float_as_uint(v[p]);
+                tmem_st8(tS + lanes + col, w);
                 if (holds) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        hi[e] = bfp::peel(S[2 * e], S[2 * e + 1]);
-                        mid[e] = pack_bf16(S[2 * e], S[2 * e + 1]);
+                        hi[e] = bfp::peel(S[e]);
+                        mid[e] = bfp::pack(S[e]);
                     }
                     planes::sts128(at16(sm + L::s, r, half * 4 + k), hi);
                     planes::sts128(at16(sm + L::s + kBlock, r, half * 4 + k), mid);
@@ -337,7 +356,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             if (!wait(YD, d)) break;
             tc_fence_after();
             const uint32_t xt = sm + L::x + (d & 1) * kBlock;
-#pragma unroll 1
+#pragma unroll 2
             for (int k = 0; k < 4; ++k) {
                 uint32_t hi[8], mid[8], mx[8], u[4];
                 const int col = half * 32 + 8 * k;
@@ -349,9 +368,9 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float y0 = fmaf(bi, __uint_as_float(hi[2 * e]) + __uint_as_float(mid[2 * e]), __uint_as_float(mx[2 * e]));
-                    const float y1 = fmaf(bi, __uint_as_float(hi[2 * e + 1]) + __uint_as_float(mid[2 * e + 1]), __uint_as_float(mx[2 * e + 1]));
-                    u[e] = pack_bf16(fmaf(D, __uint_as_float(u[e] << 16), y0), fmaf(D, __uint_as_float(u[e] & 0xffff0000u), y1));
+                    const bfp::F2 y = bfp::fma2(bfp::F2(bi, bi), bfp::F2::of(hi[2 * e], hi[2 * e + 1]) + bfp::F2::of(mid[2 * e], mid[2 * e + 1]),
+                                                bfp::F2::of(mx[2 * e], mx[2 * e + 1]));
+                    u[e] = bfp::pack(bfp::fma2(bfp::F2(D, D), bfp::widen(u[e]), y));
                 }
                 planes::sts128(at, u);  // y takes x's place
             }
@@ -360,15 +379,15 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             mbar_arrive(&bars[GE0 + (d & 1)]);
             __syncwarp();
             const int len = min(eos - bos - d * kT, kT);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {  // eight rows of 64 bytes at a time
-                const int t = q * 32 + 8 * k + (lane >> 2), col = lane & 3;
-                if (t < len) {
-                    uint32_t u[4];
-                    planes::lds128(at16(xt, t, half * 4 + col), u);
-                    *reinterpret_cast<uint4*>(out + ((long)d * kT + t) * out_stride + col * 8) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-            }
+            // eight rows of 64 bytes at a time
+            uint32_t u[4][4];
+            const int t = q * 32 + (lane >> 2), col = lane & 3;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) planes::lds128(at16(xt, t + 8 * k, half * 4 + col), u[k]);
+            __nv_bfloat16* to = out + ((long)d * kT + t) * out_stride + col * 8;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (t + 8 * k < len) *reinterpret_cast<uint4*>(to + 8 * k * out_stride) = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
             fence_async_smem();
             mbar_arrive(&bars[EX0 + (d & 1)]);
         }
@@ -377,14 +396,13 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
         constexpr uint32_t idCB = idesc_bf16(128, 128, 0, 0), idCS = idesc_bf16(128, 128, 0, 1), idU = idesc_bf16(128, 128, 1, 1),
                            idUl = idesc_bf16(128, 64, 1, 1), idMX = idesc_bf16(128, 64, 0, 1);
         const uint32_t on = elect();
-        const uint64_t dCk = sdesc_sw128(sm + L::c, 16, 1024), dS = sdesc_sw128(sm + L::s, kBlock, 1024),
-                       dV = sdesc_sw128(sm + L::v, kBlock, 1024);
+        const uint64_t dBk = sdesc_sw128(sm + L::b, 16, 1024), dBm = sdesc_sw128(sm + L::b, kBlock, 1024),
+                       dS = sdesc_sw128(sm + L::s, kBlock, 1024), dV = sdesc_sw128(sm + L::v, kBlock, 1024);
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
-            const uint32_t bt = sm + L::b + st * NB * kBlock;
-            const uint64_t dBk = sdesc_sw128(bt, 16, 1024), dBm = sdesc_sw128(bt, kBlock, 1024),
+            const uint64_t dCk = sdesc_sw128(sm + L::c + st * NB * kBlock, 16, 1024),
                            dX = sdesc_sw128(sm + L::x + st * kBlock, kBlock, 1024);
-            if (!wait(FB0 + st, c >> 1) || !wait(FC, c)) break;
+            if (!wait(FB, c) || !wait(FC0 + st, c >> 1)) break;
             if (c > 0 && !wait(YD, c - 1)) break;  // MX has read the masked products that CB overwrites
             tc_fence_after();
 #pragma unroll
@@ -400,14 +418,14 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
 #pragma unroll
             for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dBm + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
             commit(on, &bars[UD]);
-            commit(on, &bars[EB0 + st]);
+            commit(on, &bars[EB]);
             if (c > 0 && !wait(YE, c - 1)) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < N / 16; ++k)
                 mma_ss(on, tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
             commit(on, &bars[CSD]);
-            commit(on, &bars[EC]);
+            commit(on, &bars[EC0 + st]);
             if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
             tc_fence_after();
 #pragma unroll
@@ -427,31 +445,33 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
         const int xc = h * a.P + s * 64, gc = g * N;
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1, t0 = bos + c * kT;
-            if (c >= 2 && !wait(EB0 + st, (c >> 1) - 1)) break;
-            if (on) {
-                mbar_arrive_expect_tx(&bars[FB0 + st], NB * kBlock);
-                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::b + (st * NB + q) * kBlock, &mB, &bars[FB0 + st], gc + 64 * q, t0);
-            }
-            ++nb;
             if (c >= 2 && !wait(EX0 + st, (c >> 1) - 1)) break;
             if (on) {
                 mbar_arrive_expect_tx(&bars[FX0 + st], kBlock);
                 tma_load_2d(smem + L::x + st * kBlock, &mX, &bars[FX0 + st], xc, t0);
+                if (c + 1 < chunks) prefetch_2d(&mX, xc, t0 + kT);
             }
             ++nx;
-            if (c >= 1 && !wait(EC, c - 1)) break;
+            if (c >= 2 && !wait(EC0 + st, (c >> 1) - 1)) break;
             if (on) {
-                mbar_arrive_expect_tx(&bars[FC], NB * kBlock);
-                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::c + q * kBlock, &mC, &bars[FC], gc + 64 * q, t0);
+                mbar_arrive_expect_tx(&bars[FC0 + st], NB * kBlock);
+                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::c + (st * NB + q) * kBlock, &mC, &bars[FC0 + st], gc + 64 * q, t0);
+                // B has one place only: its next tile waits in L2
                 if (c + 1 < chunks)
-                    for (int q = 0; q < NB; ++q) prefetch_2d(&mC, gc + 64 * q, t0 + kT);
+                    for (int q = 0; q < NB; ++q) prefetch_2d(&mB, gc + 64 * q, t0 + kT);
             }
             ++nc;
+            if (c >= 1 && !wait(EB, c - 1)) break;
+            if (on) {
+                mbar_arrive_expect_tx(&bars[FB], NB * kBlock);
+                for (int q = 0; q < NB; ++q) tma_load_2d(smem + L::b + q * kBlock, &mB, &bars[FB], gc + 64 * q, t0);
+            }
+            ++nb;
         }
         // the last loads have landed before the block may leave
-        for (int k = max(0, nb - 2); k < nb; ++k) mbar_wait(&bars[FB0 + (k & 1)], (k >> 1) & 1, kLimit);
+        for (int k = max(0, nc - 2); k < nc; ++k) mbar_wait(&bars[FC0 + (k & 1)], (k >> 1) & 1, kLimit);
         for (int k = max(0, nx - 2); k < nx; ++k) mbar_wait(&bars[FX0 + (k & 1)], (k >> 1) & 1, kLimit);
-        if (nc > 0) mbar_wait(&bars[FC], (nc - 1) & 1, kLimit);
+        if (nb > 0) mbar_wait(&bars[FB], (nb - 1) & 1, kLimit);
     } else {
         // ================= gates =================
         const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -501,13 +521,14 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             }
             if (c >= 2 && !wait(GE0 + (c & 1), (c >> 1) - 1)) break;
             float* gt = gates_of(c);
-            float ph[4], pl[4], q[4], w[4], b[4];
+            float ph[4], pl[4], pd[4], q[4], w[4], b[4];
 #pragma unroll
             for (int e = 3; e >= 0; --e) {
                 const Two p = two_add(before, pre[e]);
                 ph[e] = p.h * kLog2e;
                 // the product's rounding, and the low part
                 pl[e] = fmaf(p.h, kLog2e, -ph[e]) + p.l * kLog2e + p.h * 1.9259629911266175e-8f;
+                pd[e] = pl[e] - log2f(dt[e]);  // no step: an exponential of -inf
                 q[e] = expf(behind) * dt[e];
                 w[e] = expf(behind + tail) * dt[e];
                 b[e] = expf(head + p.h);
@@ -519,7 +540,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             put(kPh, ph);
             put(kPl, pl);
             put(kQ, q);
-            put(kDt, dt);
+            put(kPd, pd);
             put(kW, w);
             put(kB, b);
             if (lane < 4) gt[L::gate_rows * kT + lane] = expf(lane == 0 ? tot[0] : (lane == 1 ? tot[1] : (lane == 2 ? tot[2] : tot[3])));
