@@ -420,7 +420,6 @@ cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
     ssm::Work w{};
     ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
     cudaError_t e = ssm::launch_gates(a, w, s);
-    if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
     if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
     if (e != cudaSuccess) return e;
     const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);

@@ -61,9 +61,9 @@ struct Work {
     int subsets;
 };
 
-// Launches gates and states; `reverse`: the gradients' states too.
+// Launches the gates, and the states at the chunks' starts; `both`: also their gradients at the chunks' ends.
 cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s);
-cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool reverse, cudaStream_t s);
+cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s);
 // The whole forward pass of bf16 prompts (ssm_tc.cu), for total_T > 0.
 cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s);
 

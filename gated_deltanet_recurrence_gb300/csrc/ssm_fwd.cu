@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, f
 
 // ---- states --------------------------------------------------------------------------------------
 
-// Block: 8 warps; warp w holds rows 16 (w % 4) .. of the 64 and half of the N columns.  REV: the states' gradients,
-// from the last chunk to the first.
+// Block: 8 warps; warp w holds rows 16 (w % 4) .. of the 64 and half of the N columns.  Blocks with blockIdx.y = 1: the
+// states' gradients, from the last chunk to the first.
 constexpr int kScanThreads = 256;
-template <typename T, int N, bool REV>
+template <typename T, int N>
 __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work w) {
     constexpr int PX = bfp::kPlanes<T>, NT = N / 16, KV = N / 32;  // KV: vectors of B a thread loads
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
     const bfp::Tile<kC, N, PX> Kt{base};
     const bfp::Tile<kC, 64, 3> Vt{base + bfp::kTileBytes<kC, N, PX>};
     __shared__ float fac[kC];
+    const bool REV = blockIdx.y;
     if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
     const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kC - 1) / kC;
@@ -144,13 +145,13 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
         });
 }
 
-template <typename T, int N, bool REV>
-cudaError_t scan_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
+template <typename T, int N>
+cudaError_t scan_one(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
     constexpr int smem = bfp::kTileBytes<kC, N, bfp::kPlanes<T>> + bfp::kTileBytes<kC, 64, 3>;
-    const auto kernel = ssm_scan_kernel<T, N, REV>;
+    const auto kernel = ssm_scan_kernel<T, N>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), kScanThreads, smem, s>>>(a, w);
+    kernel<<<dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), both ? 2 : 1), kScanThreads, smem, s>>>(a, w);
     return cudaGetLastError();
 }
 
@@ -275,13 +276,9 @@ cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool reverse, cudaStream_t s) {
-    if (a.dtype == GDN_BF16) {
-        if (a.N == 128) return reverse ? scan_one<__nv_bfloat16, 128, true>(a, w, s) : scan_one<__nv_bfloat16, 128, false>(a, w, s);
-        return reverse ? scan_one<__nv_bfloat16, 64, true>(a, w, s) : scan_one<__nv_bfloat16, 64, false>(a, w, s);
-    }
-    if (a.N == 128) return reverse ? scan_one<float, 128, true>(a, w, s) : scan_one<float, 128, false>(a, w, s);
-    return reverse ? scan_one<float, 64, true>(a, w, s) : scan_one<float, 64, false>(a, w, s);
+cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
+    if (a.dtype == GDN_BF16) return a.N == 128 ? scan_one<__nv_bfloat16, 128>(a, w, both, s) : scan_one<__nv_bfloat16, 64>(a, w, both, s);
+    return a.N == 128 ? scan_one<float, 128>(a, w, both, s) : scan_one<float, 64>(a, w, both, s);
 }
 
 }  // namespace ssm
