@@ -410,28 +410,15 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, un
 }
 
 }  // namespace
-}  // namespace ssm
 
-size_t ssm_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype) {
-    return ssm::layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
-}
-
-cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
-    ssm::Work w{};
-    ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
-    cudaError_t e = ssm::launch_gates(a, w, s);
-    if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
-    if (e != cudaSuccess) return e;
-    const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
-    if (a.dtype == GDN_BF16) e = a.N == 128 ? ssm::grad_one<__nv_bfloat16, 128>(a, w, s) : ssm::grad_one<__nv_bfloat16, 64>(a, w, s);
-    else e = a.N == 128 ? ssm::grad_one<float, 128>(a, w, s) : ssm::grad_one<float, 64>(a, w, s);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_finish(const SsmArgs& a, const Work& w, long slots, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const bool zeros = a.zero_outside && a.seqs.cu;
     if (a.seqs.total_T > 0 && (w.subsets > 1 || zeros)) {
         const long elems = (long)a.seqs.total_T * a.G * a.N;
         const dim3 grid((unsigned)((elems / 8 + 255) / 256), zeros ? 3 : 2);
-        if (a.dtype == GDN_BF16) ssm::ssm_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, w, elems);
-        else ssm::ssm_finish_kernel<float><<<grid, 256, 0, s>>>(a, w, elems);
+        if (a.dtype == GDN_BF16) ssm_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, w, elems);
+        else ssm_finish_kernel<float><<<grid, 256, 0, s>>>(a, w, elems);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -439,6 +426,26 @@ cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
     if (a.dA_log || a.ddt_bias) e = launch_column_sum(w.sums, slots, a.H, a.dA_log, a.ddt_bias, s);
     if (e == cudaSuccess && a.dD) e = launch_column_sum(w.sums + 2 * all, slots, a.H, a.dD, nullptr, s);
     return e;
+}
+
+}  // namespace ssm
+
+size_t ssm_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
+    if (dtype == GDN_BF16 && total_T > 0) return ssm::tc_bwd_workspace_bytes(num_seqs, total_T, H, G, P, N);
+    return ssm::layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
+}
+
+cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
+    if (a.dtype == GDN_BF16 && a.seqs.total_T > 0) return ssm::launch_tc_bwd(a, s);
+    ssm::Work w{};
+    ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
+    cudaError_t e = ssm::launch_gates(a, w, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
+    if (e != cudaSuccess) return e;
+    const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
+    e = a.N == 128 ? ssm::grad_one<float, 128>(a, w, s) : ssm::grad_one<float, 64>(a, w, s);
+    if (e != cudaSuccess) return e;
+    return ssm::launch_finish(a, w, slots, s);
 }
 
 }  // namespace gdn

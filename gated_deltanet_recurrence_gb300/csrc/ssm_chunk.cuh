@@ -66,6 +66,11 @@ cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s);
 cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s);
 // The whole forward pass of bf16 prompts (ssm_tc.cu), for total_T > 0.
 cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s);
+// The gradients of bf16 prompts (ssm_tc_bwd.cu), for total_T > 0, and what every backward pass ends with: dB and dC added
+// up, zeros outside the sequences, sums over the slots.
+size_t tc_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N);
+cudaError_t launch_tc_bwd(const SsmArgs& a, cudaStream_t s);
+cudaError_t launch_finish(const SsmArgs& a, const Work& w, long slots, cudaStream_t s);
 
 }  // namespace ssm
 }  // namespace gdn

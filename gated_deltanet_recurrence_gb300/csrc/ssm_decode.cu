@@ -14,23 +14,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 64;
 
-// Sums of R values over groups of L lanes; value r's sum ends in the lanes with (lane % L) % R == r (R <= L).
-template <int R, int L>
-__device__ __forceinline__ float sum_rows(float (&y)[R], int lane) {
-#pragma unroll
-    for (int o = R / 2; o > 0; o >>= 1) {
-#pragma unroll
-        for (int r = 0; r < o; ++r) {
-            const bool up = lane & o;
-            const float give = up ? y[r] : y[r + o], keep = up ? y[r + o] : y[r];
-            y[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-        }
-    }
-#pragma unroll
-    for (int o = R; o < L; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
-    return y[0];
-}
-
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs a) {
     constexpr int L = N / 4;             // lanes of a row

@@ -277,7 +277,6 @@ cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
 }
 
 cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
-    if (a.dtype == GDN_BF16) return a.N == 128 ? scan_one<__nv_bfloat16, 128>(a, w, both, s) : scan_one<__nv_bfloat16, 64>(a, w, both, s);
     return a.N == 128 ? scan_one<float, 128>(a, w, both, s) : scan_one<float, 64>(a, w, both, s);
 }
 
@@ -298,7 +297,6 @@ cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
     cudaError_t e = ssm::launch_gates(a, w, s);
     if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
     if (e != cudaSuccess || a.seqs.total_T == 0) return e;
-    if (a.dtype == GDN_BF16) return a.N == 128 ? ssm::out_one<__nv_bfloat16, 128>(a, w, s) : ssm::out_one<__nv_bfloat16, 64>(a, w, s);
     return a.N == 128 ? ssm::out_one<float, 128>(a, w, s) : ssm::out_one<float, 64>(a, w, s);
 }
 

@@ -189,6 +189,23 @@ __device__ __forceinline__ float sigmoid_hw(float x) {
     return y;
 }
 
+// Sums of R values over groups of L lanes; value r's sum ends in the lanes with (lane % L) % R == r (R <= L).
+template <int R, int L>
+__device__ __forceinline__ float sum_rows(float (&y)[R], int lane) {
+#pragma unroll
+    for (int o = R / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int r = 0; r < o; ++r) {
+            const bool up = lane & o;
+            const float give = up ? y[r] : y[r + o], keep = up ? y[r + o] : y[r];
+            y[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+#pragma unroll
+    for (int o = R; o < L; o <<= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+    return y[0];
+}
+
 // The step and the log decay of one token: dt = softplus(a + bias), g = -rate dt with rate = exp(A_log).
 __device__ __forceinline__ float ssm_softplus(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 

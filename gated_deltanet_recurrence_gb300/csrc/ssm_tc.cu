@@ -22,23 +22,17 @@
 //
 // Every mbarrier wait is bounded; when one runs out the kernel records GDN_ERR_TIMEOUT, every role leaves its loop,
 // copies and MMAs in flight are waited for (bounded), TMEM is freed.
-#include <cudaTypedefs.h>
-
-#include "sm100_ptx.cuh"
-#include "ssm_chunk.cuh"
+#include "ssm_tc.cuh"
 
 namespace gdn {
 namespace ssm {
 namespace {
 
 using namespace ptx;
+using namespace tc;
 
-constexpr int kT = 128;                    // tokens of a chunk
-constexpr int kBlock = kT * 128;           // bytes of a tile of 128 rows and 64 columns
-constexpr uint64_t kLimit = 2000000000ull;  // ns, bound on any wait
 constexpr int kWorkers = 256;              // threads of a role's two sets of four warps
 constexpr int kThreads = 2 * kWorkers + 3 * 32;
-constexpr float kLog2e = 1.4426950408889634f;
 
 enum Bar { FB, EB, FC0, FC1, EC0, EC1, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
 
@@ -53,70 +47,6 @@ struct Lay {
 // e^{sums to the run's end} dt, e^{sums to the chunk's end} dt, e^{sums from the chunk's start}; then e^{total} of the runs
 // and of the chunk
 enum Gate { kPh, kPl, kPd, kQ, kW, kB };
-
-// MMAs issued by the elected thread of a warp that runs as one (its operands stay in uniform registers): left operand
-// from shared memory, or from TMEM.
-__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar) {
-    if (on) mma_commit(bar);
-}
-__device__ __forceinline__ uint32_t elect() {
-    uint32_t on;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
-    return on;
-}
-__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
-}
-// 16 and eight consecutive columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-// Polls until the phase completes; false when another role has given up, or the bound has passed (recorded).
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead, int* err) {
-    const long long limit = static_cast<long long>(kLimit) * 21 / 10, t0 = clock64();
-    while (!mbar_try_wait(bar, parity, 100000u)) {
-        if (*dead) return false;
-        if (clock64() - t0 > limit) {
-            record_error(err, GDN_ERR_TIMEOUT);
-            *dead = 1;
-            return false;
-        }
-    }
-    return true;
-}
-// 16-byte chunk c of row r of a tile
-__device__ __forceinline__ uint32_t at16(uint32_t tile, int r, int c) { return tile + r * 128 + ((c ^ (r & 7)) << 4); }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -485,66 +415,32 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
         };
         if (chunks > 0) fetch(0);
         for (int c = 0; c < chunks; ++c) {
-            const int left = eos - bos - c * kT - 4 * lane;  // this lane's tokens inside the sequence
-            float dt[4], gl[4];
+            LaneGates o;
+            float zb[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                dt[e] = e < left ? ssm_softplus(z[e] + bias) : 0.f;
-                gl[e] = e < left ? fmaxf(-rate * dt[e], kMinLog) : 0.f;
-            }
+            for (int e = 0; e < 4; ++e) zb[e] = z[e] + bias;
+            lane_gates(zb, eos - bos - c * kT - 4 * lane, rate, lane, o);
             if (c + 1 < chunks) fetch(c + 1);
-            // sums inside the run of 32 (eight lanes): from its start, in two floats, and to its end
-            Two pre[4];
-            pre[0] = Two{gl[0], 0.f};
-#pragma unroll
-            for (int e = 1; e < 4; ++e) pre[e] = two_add(pre[e - 1], Two{gl[e], 0.f});
-            Two run = pre[3];
-            float suf = (gl[0] + gl[1]) + (gl[2] + gl[3]);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                const Two up{__shfl_up_sync(0xffffffffu, run.h, o, 8), __shfl_up_sync(0xffffffffu, run.l, o, 8)};
-                const float down = __shfl_down_sync(0xffffffffu, suf, o, 8);
-                if ((lane & 7) >= o) run = two_add(up, run);
-                if ((lane & 7) + o < 8) suf += down;
-            }
-            Two before{__shfl_up_sync(0xffffffffu, run.h, 1, 8), __shfl_up_sync(0xffffffffu, run.l, 1, 8)};
-            if ((lane & 7) == 0) before = Two{0.f, 0.f};
-            float behind = __shfl_down_sync(0xffffffffu, suf, 1, 8);
-            if ((lane & 7) == 7) behind = 0.f;
-            float tot[4], head = 0.f, tail = 0.f, all = 0.f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                tot[u] = __shfl_sync(0xffffffffu, run.h, 8 * u + 7);
-                if (u < lane >> 3) head += tot[u];
-                if (u > lane >> 3) tail += tot[u];
-                all += tot[u];
-            }
             if (c >= 2 && !wait(GE0 + (c & 1), (c >> 1) - 1)) break;
             float* gt = gates_of(c);
-            float ph[4], pl[4], pd[4], q[4], w[4], b[4];
+            float pd[4], q[4], w[4];
 #pragma unroll
-            for (int e = 3; e >= 0; --e) {
-                const Two p = two_add(before, pre[e]);
-                ph[e] = p.h * kLog2e;
-                // the product's rounding, and the low part
-                pl[e] = fmaf(p.h, kLog2e, -ph[e]) + p.l * kLog2e + p.h * 1.9259629911266175e-8f;
-                pd[e] = pl[e] - log2f(dt[e]);  // no step: an exponential of -inf
-                q[e] = expf(behind) * dt[e];
-                w[e] = expf(behind + tail) * dt[e];
-                b[e] = expf(head + p.h);
-                behind += gl[e];
+            for (int e = 0; e < 4; ++e) {
+                pd[e] = o.pl[e] - log2f(o.dt[e]);  // no step: an exponential of -inf
+                q[e] = o.to_run[e] * o.dt[e];
+                w[e] = o.to_end[e] * o.dt[e];
             }
             const auto put = [&](int row, const float (&x)[4]) {
                 *reinterpret_cast<float4*>(gt + row * kT + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
             };
-            put(kPh, ph);
-            put(kPl, pl);
-            put(kQ, q);
+            put(kPh, o.ph);
+            put(kPl, o.pl);
             put(kPd, pd);
+            put(kQ, q);
             put(kW, w);
-            put(kB, b);
-            if (lane < 4) gt[L::gate_rows * kT + lane] = expf(lane == 0 ? tot[0] : (lane == 1 ? tot[1] : (lane == 2 ? tot[2] : tot[3])));
-            if (lane == 4) gt[L::gate_rows * kT + 4] = expf(all);
+            put(kB, o.from_start);
+            if (lane < 4) gt[L::gate_rows * kT + lane] = expf(lane == 0 ? o.tot[0] : (lane == 1 ? o.tot[1] : (lane == 2 ? o.tot[2] : o.tot[3])));
+            if (lane == 4) gt[L::gate_rows * kT + 4] = expf(o.all);
             mbar_arrive(&bars[GF0 + (c & 1)]);
         }
     }
@@ -554,26 +450,6 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        const bool got = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                         q == cudaDriverEntryPointSuccess;
-        return got ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-    }();
-    return fn;
-}
-
-// Rows of `width` bf16 elements, `stride` apart, in boxes of 128 rows and 64 columns; rows past the last read as zeros.
-bool map_rows(CUtensorMap* m, const void* base, long rows, long width, long stride) {
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, kT}, es[2] = {1, 1};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int N>

@@ -1,0 +1,929 @@
+// ssm_tc_bwd.cu -- the gradients of the selective scan of bf16 prompts on the tensor cores (tcgen05).
+//
+// The formulas are those of ssm_bwd.cu, with chunks of 128 tokens.  Three kernels: the gates of all chunks; the states
+// at the chunks' starts and their gradients at the chunks' ends (one block per sequence, head, 64 rows and direction
+// walks along the chunks); the gradients, one block per chunk and subset of a group's heads.
+//
+// Every fp32 factor is three bf16 planes, exact beside the bf16 inputs; where a factor's planes lie side by side, the
+// input is read once for all of them.  All matrices of pairs of tokens are held with row j (the earlier token) and
+// column i >= j, as they are needed: (C B^T)^T once a block; per head dy . x; the masked decays' products M^T as the left
+// operand of M^T dy from TMEM; E^T summed over the heads in registers.
+//   dg_t = sum over pairs i >= t > j of T_ij + sum_{i >= t} b_i dy_i . S_0 C_i + b_last <dS_1, S_0>
+//          + sum_{j < t} r_j v_j . dS_1 B_j
+// is taken as it stands, without subtractions: suffix sums of T along a row, added over the rows before t.
+#include "ssm_tc.cuh"
+
+namespace gdn {
+namespace ssm {
+namespace {
+
+using namespace ptx;
+using namespace tc;
+
+// ---- gates ---------------------------------------------------------------------------------------
+
+// Rows of the gates of a chunk and head, and behind them e^{total} of the four runs and of the chunk.
+enum Row { rPh, rPl, rFromRun, rToRun, rDt, rToEnd, rFromStart, kRows };
+constexpr int kGates = kRows * kT + 8;
+
+long slots128(int num_seqs, int total_T) { return (long)total_T / kT + num_seqs; }
+
+struct TcWork {
+    float* gates;    // [slots][H][kGates]
+    float* states;   // [slots][H][P / 64] images of N x 64: row n, 16-byte chunk c at place c ^ (n & 7)
+    float* dstates;
+    float* sums;
+    float* parts;
+    int subsets;
+};
+
+// The chunk of a slot; false where the slot holds none.  The whole block takes part.
+__device__ __forceinline__ bool find_chunk128(const Packed& s, int slot, int* err, Chunk& c) {
+    c.n = packed_find(s, slot, kT, 1, err);
+    if (c.n < 0 || c.n >= s.num_seqs) return false;
+    c.bos = s.bos(c.n);
+    c.eos = s.bos(c.n + 1);
+    c.k = slot - (c.bos / kT + c.n);
+    c.t0 = c.bos + c.k * kT;
+    c.len = min(c.eos - c.t0, kT);
+    return c.len > 0;
+}
+
+constexpr int kGateWarps = 8;
+__global__ void __launch_bounds__(kGateWarps * 32) ssm_gates128_kernel(SsmArgs a, float* gates) {
+    Chunk c;
+    if (!find_chunk128(a.seqs, blockIdx.x, a.err, c)) return;
+    const int lane = threadIdx.x & 31, h = blockIdx.y * kGateWarps + (threadIdx.x >> 5);
+    if (h >= a.H) return;
+    const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    float z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = 4 * lane + e;
+        z[e] = t < c.len ? a.a[(long)(c.t0 + t) * a.H + h] + bias : 0.f;
+    }
+    LaneGates o;
+    lane_gates(z, c.len - 4 * lane, rate, lane, o);
+    float* gt = gates + ((long)blockIdx.x * a.H + h) * kGates;
+    const auto put = [&](int row, const float (&x)[4]) {
+        *reinterpret_cast<float4*>(gt + row * kT + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+    };
+    put(rPh, o.ph);
+    put(rPl, o.pl);
+    put(rFromRun, o.from_run);
+    put(rToRun, o.to_run);
+    put(rDt, o.dt);
+    put(rToEnd, o.to_end);
+    put(rFromStart, o.from_start);
+    if (lane < 4) gt[kRows * kT + lane] = expf(lane == 0 ? o.tot[0] : (lane == 1 ? o.tot[1] : (lane == 2 ? o.tot[2] : o.tot[3])));
+    if (lane == 4) gt[kRows * kT + 4] = expf(o.all);
+}
+
+// ---- states --------------------------------------------------------------------------------------
+
+// Warps 0 - 7 form the factors (V, or b dy: three planes), 8 - 15 take the state on and lay its image out, 16 issues the
+// MMAs, 17 the loads, 18 brings the gates.  Blocks with blockIdx.y = 1 go backwards, from dfinal_state.
+constexpr int kWorkers = 256, kScanThreads = 2 * kWorkers + 96;
+enum ScanBar { KF0, KF1, KE0, KE1, XF0, XF1, XE0, XE1, GF0, GF1, GE0, GE1, VR, UD, SR, DR, kScanBars };
+template <int N>
+struct ScanLay {
+    static constexpr int nb = N / 64, image = N * 256;
+    static constexpr int k = 0, x = k + 2 * nb * kBlock, v = x + 2 * kBlock, st = v + 3 * kBlock, gates = st + 2 * image,
+                         gate_bytes = (kT + 8) * 4, bars = gates + 2 * gate_bytes, bytes = bars + kScanBars * 8 + 16;
+};
+
+template <int N>
+__global__ void __launch_bounds__(kScanThreads, 1)
+ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mY, const __grid_constant__ CUtensorMap mB,
+                   const __grid_constant__ CUtensorMap mC, SsmArgs a, TcWork w) {
+    using L = ScanLay<N>;
+    constexpr int NB = L::nb;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sm = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint32_t* tbase = reinterpret_cast<uint32_t*>(smem + L::bars + kScanBars * 8);
+    volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kScanBars * 8 + 4);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const bool back = blockIdx.y;
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
+    const int bos = __shfl_sync(0xffffffffu, a.seqs.bos(n), 0), eos = __shfl_sync(0xffffffffu, a.seqs.bos(n + 1), 0);
+    const int chunks = (eos - bos + kT - 1) / kT;
+    const int g = h / (a.H / a.G);
+    const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
+    const long slot0 = bos / kT + n;
+    const auto chunk_of = [&](int c) { return back ? chunks - 1 - c : c; };
+
+    if (tid == 0) {
+        for (int i = 0; i < kScanBars; ++i)
+            mbar_init(&bars[i], i == VR || i == SR || i == XE0 || i == XE1 ? kWorkers : (i == GE0 || i == GE1 ? 2 * kWorkers : (i == GF0 || i == GF1 ? 32 : 1)));
+        *dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 16) {
+        tmem_alloc(tbase, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
+    const uint32_t tU = tm, tS = tm + 128;
+    const auto wait = [&](int bar, int index) -> bool {
+        bool ok = mbar_try_wait(&bars[bar], index & 1, 100000u);
+        if (!ok) ok = wait_slow(&bars[bar], index & 1, dead, a.err);
+        return __all_sync(0xffffffffu, ok);
+    };
+    const auto gates_of = [&](int c) { return reinterpret_cast<float*>(smem + L::gates + (c & 1) * L::gate_bytes); };
+
+    if (warp < 8) {
+        // ================= factors =================
+        const int q = warp & 3, half = warp >> 2, i = q * 32 + lane;
+        for (int c = 0; c < chunks; ++c) {
+            if (!wait(GF0 + (c & 1), c >> 1)) break;
+            const float f = gates_of(c)[i];
+            mbar_arrive(&bars[GE0 + (c & 1)]);
+            const int left = eos - bos - chunk_of(c) * kT;
+            if (!wait(XF0 + (c & 1), c >> 1)) break;
+            if (left < kT && !wait(KF0 + (c & 1), c >> 1)) break;
+            if (c > 0 && !wait(UD, c - 1)) break;
+            const uint32_t xt = sm + L::x + (c & 1) * kBlock;
+            const bool live = i < left;
+#pragma unroll 2
+            for (int k = half * 4; k < half * 4 + 4; ++k) {
+                uint32_t u[4] = {0, 0, 0, 0}, v[3][4];
+                if (live) planes::lds128(at16(xt, i, k), u);
+                else
+                    for (int b = 0; b < NB; ++b) planes::sts128(at16(sm + L::k + ((c & 1) * NB + b) * kBlock, i, k), u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    bfp::F2 t = bfp::widen(u[e]) * bfp::F2(f, f);
+                    v[0][e] = bfp::peel(t);
+                    v[1][e] = bfp::peel(t);
+                    v[2][e] = bfp::pack(t);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::v + p * kBlock, i, k), v[p]);
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[XE0 + (c & 1)]);
+            mbar_arrive(&bars[VR]);
+        }
+    } else if (warp < 16) {
+        // ================= state =================
+        const int q = warp & 3, half = (warp >> 2) & 1, r = q * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const bool holds = r < N, leader = tid == kWorkers;
+        const float* init = back ? a.dfinal_state : a.initial_state;
+        float* last = back ? a.dinitial_state : nullptr;
+        float decay = 0.f;
+        for (int c = 0; c <= chunks; ++c) {
+            bool ok = c == 0 || wait(UD, c - 1);
+            tc_fence_after();
+            if (c < chunks) {  // the image before the last one has been read by its copy
+                if (leader) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                if (bar_sync_or(1, kWorkers, !ok)) break;
+            } else if (!ok) {
+                break;
+            }
+            const uint32_t st = sm + L::st + (c & 1) * L::image;
+#pragma unroll 2
+            for (int k = 0; k < 4; ++k) {
+                const int col = half * 32 + 8 * k;
+                bfp::F2 S[4];
+                if (c == 0) {
+#pragma unroll
+                    for (int p = 0; p < 8; p += 2) {
+                        const float* from = init + row0 + (long)(col + p) * N + r;
+                        S[p / 2] = holds && init ? bfp::F2(from[0], from[N]) : bfp::F2(0.f, 0.f);
+                    }
+                } else {
+                    uint32_t old[8], hi[8], mid[8];
+                    tmem_ld8(tS + lanes + col, old);
+                    tmem_ld8(tU + lanes + col, hi);
+                    tmem_ld8(tU + lanes + 64 + col, mid);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int p = 0; p < 8; p += 2)
+                        S[p / 2] = bfp::fma2(bfp::F2(decay, decay), bfp::F2::of(old[p], old[p + 1]),
+                                             bfp::F2::of(hi[p], hi[p + 1]) + bfp::F2::of(mid[p], mid[p + 1]));
+                }
+                float v[8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) S[p].get(v[2 * p], v[2 * p + 1]);
+                if (c == chunks) {
+                    if (holds && last) {
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) last[row0 + (long)(col + p) * N + r] = v[p];
+                    }
+                    continue;
+                }
+                uint32_t u[8];
+#pragma unroll
+                for (int p = 0; p < 8; ++p) u[p] = __float_as_uint(v[p]);
+                tmem_st8(tS + lanes + col, u);
+                if (holds) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t part[4] = {u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]};
+                        planes::sts128(st + r * 256 + (((half * 8 + 2 * k + e) ^ (r & 7)) << 4), part);
+                    }
+                }
+            }
+            if (c == chunks) break;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars[SR]);
+            fence_async_smem();
+            ok = wait(GF0 + (c & 1), c >> 1);
+            decay = gates_of(c)[kT];
+            mbar_arrive(&bars[GE0 + (c & 1)]);
+            if (bar_sync_or(1, kWorkers, !ok)) break;
+            if (leader) {
+                float* to = (back ? w.dstates : w.states) + (((slot0 + chunk_of(c)) * a.H + h) * slices + s) * (long)(N * 64);
+                bulk_store(to, smem + L::st + (c & 1) * L::image, L::image);
+                bulk_commit();
+            }
+        }
+        if (leader) bulk_wait_all();
+    } else if (warp == 16) {
+        // ================= MMAs =================
+        constexpr uint32_t idU = idesc_bf16(128, 128, 1, 1), idUl = idesc_bf16(128, 64, 1, 1);
+        const uint32_t on = elect();
+        const uint64_t dV = sdesc_sw128(sm + L::v, kBlock, 1024);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            const uint64_t dK = sdesc_sw128(sm + L::k + st * NB * kBlock, kBlock, 1024);
+            if (!wait(KF0 + st, c >> 1) || !wait(SR, c) || !wait(VR, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU, dK + k * 128, dV + k * 128, idU, k > 0);
+#pragma unroll
+            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dK + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
+            commit(on, &bars[UD]);
+            commit(on, &bars[KE0 + st]);
+        }
+        if (chunks > 0) {
+            commit(on, &bars[DR]);
+            mbar_wait(&bars[DR], 0, kLimit);
+        }
+    } else if (warp == 17) {
+        // ================= loads =================
+        const uint32_t on = elect();
+        int nk = 0, nx = 0;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1, t0 = bos + chunk_of(c) * kT;
+            if (c >= 2 && !wait(XE0 + st, (c >> 1) - 1)) break;
+            if (on) {
+                mbar_arrive_expect_tx(&bars[XF0 + st], kBlock);
+                tma_load_2d(smem + L::x + st * kBlock, back ? &mY : &mX, &bars[XF0 + st], h * a.P + s * 64, t0);
+            }
+            ++nx;
+            if (c >= 2 && !wait(KE0 + st, (c >> 1) - 1)) break;
+            if (on) {
+                mbar_arrive_expect_tx(&bars[KF0 + st], NB * kBlock);
+                for (int q = 0; q < NB; ++q)
+                    tma_load_2d(smem + L::k + (st * NB + q) * kBlock, back ? &mC : &mB, &bars[KF0 + st], g * N + 64 * q, t0);
+            }
+            ++nk;
+        }
+        for (int k = max(0, nk - 2); k < nk; ++k) mbar_wait(&bars[KF0 + (k & 1)], (k >> 1) & 1, kLimit);
+        for (int k = max(0, nx - 2); k < nx; ++k) mbar_wait(&bars[XF0 + (k & 1)], (k >> 1) & 1, kLimit);
+    } else {
+        // ================= gates =================
+        for (int c = 0; c < chunks; ++c) {
+            const float* gt = w.gates + ((slot0 + chunk_of(c)) * a.H + h) * (long)kGates;
+            float4 f = *reinterpret_cast<const float4*>(gt + (back ? rFromStart : rToEnd) * kT + 4 * lane);
+            if (!back) {
+                const float4 d = *reinterpret_cast<const float4*>(gt + rDt * kT + 4 * lane);
+                f = make_float4(f.x * d.x, f.y * d.y, f.z * d.z, f.w * d.w);
+            }
+            const float all = gt[kRows * kT + 4];
+            if (c >= 2 && !wait(GE0 + (c & 1), (c >> 1) - 1)) break;
+            float* to = gates_of(c);
+            *reinterpret_cast<float4*>(to + 4 * lane) = f;
+            if (lane == 0) to[kT] = all;
+            mbar_arrive(&bars[GF0 + (c & 1)]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after();
+        tmem_dealloc(tm, 256);
+    }
+}
+
+// ---- gradients -----------------------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
+enum GradBar { LB, LX0, LX1, LS, MM, kGradBars };
+template <int N>
+struct GradLay {
+    static constexpr int nb = N / 64, image = N * 256;
+    static constexpr int b = 0, c = b + nb * kBlock, x = c + nb * kBlock, y = x + 2 * kBlock, sp = y + 2 * kBlock, st = sp + 3 * kBlock,
+                         gates = st + image, sums = gates + 2 * kGates * 4, bars = sums + (5 * 4 * kT + 2 * kGradWarps) * 4,
+                         bytes = bars + kGradBars * 8 + 16;
+};
+
+// TMEM: (C B^T)^T | results of 128 columns in turn | results with three planes, then M^T | M^T dy
+constexpr uint32_t kCB = 0, kRes = 128, kPlane = 256, kDv = 448;
+
+// Thread: token (row) 32 q + lane of the warp's quarter q, and its quarter cg of a result's columns.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads, 1)
+ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mY, const __grid_constant__ CUtensorMap mB,
+                   const __grid_constant__ CUtensorMap mC, SsmArgs a, TcWork w) {
+    using L = GradLay<N>;
+    constexpr int NB = L::nb, NV = N * 8 / kGradThreads;  // NV: vectors of eight of a state that a thread converts
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sm = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint32_t* tbase = reinterpret_cast<uint32_t*>(smem + L::bars + kGradBars * 8);
+    volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kGradBars * 8 + 4);
+    float* sums = reinterpret_cast<float*>(smem + L::sums);
+    // by quarter of the rows (colS) or of the columns: [4][128] each
+    float *colS = sums, *rowT = sums + 4 * kT, *in1 = sums + 8 * kT, *in2 = sums + 12 * kT, *ddt = sums + 16 * kT, *part = sums + 20 * kT;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, cg = warp >> 2;
+    const int g = blockIdx.y % a.G, subset = blockIdx.y / a.G, per = a.H / a.G;
+    const int h0 = g * per + per * subset / w.subsets, h1 = g * per + per * (subset + 1) / w.subsets;
+    Chunk c;
+    if (!find_chunk128(a.seqs, blockIdx.x, a.err, c)) {
+        const long all = (long)gridDim.x * a.H;
+        for (int i = tid; i < h1 - h0; i += kGradThreads) {
+            const long at = (long)blockIdx.x * a.H + h0 + i;
+            w.sums[at] = w.sums[all + at] = w.sums[2 * all + at] = 0.f;
+        }
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kGradBars; ++i) mbar_init(&bars[i], 1);
+        *dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tbase, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0), lanes = (uint32_t)(q * 32) << 16, on = elect();
+    const auto wait = [&](int bar, int index) -> bool {
+        bool there = mbar_try_wait(&bars[bar], index & 1, 100000u);
+        if (!there) there = wait_slow(&bars[bar], index & 1, dead, a.err);
+        return __all_sync(0xffffffffu, there);
+    };
+    const int slices = a.P / 64, steps = (h1 - h0) * slices, j = q * 32 + lane;
+    const auto image = [&](const float* all, int step) {
+        return all + (((long)blockIdx.x * a.H + h0) * slices + step) * (long)(N * 64);
+    };
+    const auto load_xy = [&](int step) {  // one thread
+        const int pl = step & 1, col = (h0 + step / slices) * a.P + step % slices * 64;
+        mbar_arrive_expect_tx(&bars[LX0 + pl], 2 * kBlock);
+        tma_load_2d(smem + L::x + pl * kBlock, &mX, &bars[LX0 + pl], col, c.t0);
+        tma_load_2d(smem + L::y + pl * kBlock, &mY, &bars[LX0 + pl], col, c.t0);
+    };
+    const auto load_image = [&](const float* from) {
+        mbar_arrive_expect_tx(&bars[LS], L::image);
+        bulk_load(smem + L::st, from, L::image, &bars[LS]);
+    };
+    const auto gates_of = [&](int h) { return reinterpret_cast<float*>(smem + L::gates) + ((h - h0) & 1) * kGates; };
+    const auto ask_gates = [&](int h) {  // asynchronous copies of each thread's own
+        if (tid < kGates / 4)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(gates_of(h) + 4 * tid)),
+                         "l"(w.gates + ((long)blockIdx.x * a.H + h) * kGates + 4 * tid)
+                         : "memory");
+        ring_commit();
+    };
+    if (warp == 0 && on) {
+        mbar_arrive_expect_tx(&bars[LB], 2 * NB * kBlock);
+        for (int k = 0; k < NB; ++k) {
+            tma_load_2d(smem + L::b + k * kBlock, &mB, &bars[LB], g * N + 64 * k, c.t0);
+            tma_load_2d(smem + L::c + k * kBlock, &mC, &bars[LB], g * N + 64 * k, c.t0);
+        }
+        if (steps > 0) {
+            load_xy(0);
+            load_image(image(w.dstates, 0));
+        }
+    }
+    int images = steps > 0 ? 1 : 0, tiles = images, seen = 0, mm = 0;  // loads asked for; images waited for; MMAs waited for
+    if (steps > 0) ask_gates(h0);
+    // rows past the chunk's end, which other sequences may have filled, are zeros in every tile
+    const auto zero_rows = [&](uint32_t tile) {
+        const uint32_t zero[4] = {0, 0, 0, 0};
+        const int r = tid >> 2;
+        if (r >= c.len) {
+            planes::sts128(at16(tile, r, (tid & 3) * 2), zero);
+            planes::sts128(at16(tile, r, (tid & 3) * 2 + 1), zero);
+        }
+    };
+    bool ok = wait(LB, 0);
+    if (ok && c.len < kT)
+        for (int k = 0; k < 2 * NB; ++k) zero_rows(sm + L::b + k * kBlock);
+    fence_async_smem();
+    const uint64_t dBk = sdesc_sw128(sm + L::b, 16, 1024), dBm = sdesc_sw128(sm + L::b, kBlock, 1024),
+                   dCk = sdesc_sw128(sm + L::c, 16, 1024), dCm = sdesc_sw128(sm + L::c, kBlock, 1024),
+                   dSk = sdesc_sw128(sm + L::sp, 16, 1024), dSm = sdesc_sw128(sm + L::sp, kBlock, 1024);
+    constexpr uint32_t id128 = idesc_bf16(128, 128, 0, 0), idN = idesc_bf16(128, N, 0, 0), id192 = idesc_bf16(128, 192, 0, 1),
+                       id64 = idesc_bf16(128, 64, 0, 1);
+    const auto kstep = [](int k) { return (uint64_t)(((k >> 2) * kBlock + (k & 3) * 32) >> 4); };  // of a K-major tile
+    float Es[32], dB[32], dC[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) Es[i] = dB[i] = dC[i] = 0.f;
+    float ss = 0.f, sd = 0.f;
+
+    // dg, da and the sums of a head whose parts are all there: one warp, four tokens a lane
+    const auto finish_head = [&](int h) {
+        const float* gt = gates_of(h);
+        float dot = lane < kGradWarps ? part[lane] : 0.f, dD = lane < kGradWarps ? part[kGradWarps + lane] : 0.f;
+        dot = warp_sum(dot) * gt[kRows * kT + 4];
+        dD = warp_sum(dD);
+        float u1[4], u2[4], dt_[4], dg[4];
+        const int u = lane >> 3;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = 4 * lane + e;
+            u1[e] = u2[e] = dt_[e] = dg[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                u1[e] += in1[k * kT + t];
+                u2[e] += in2[k * kT + t];
+                dt_[e] += ddt[k * kT + t];
+                if (k <= u) dg[e] += colS[k * kT + t];
+            }
+        }
+        // what the rows before t have in the runs behind t's own: for each run, sums over the rows before
+#pragma unroll
+        for (int run = 0; run < 3; ++run) {
+            float own[4], sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = 0.f;
+#pragma unroll
+                for (int k = run + 1; k < 4; ++k) x += u <= run ? rowT[k * kT + 4 * lane + e] : 0.f;
+                own[e] = x;
+                sum += x;
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += up;
+            }
+            float before = __shfl_up_sync(0xffffffffu, sum, 1);
+            if (lane == 0) before = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (u == run) dg[e] += before;
+                before += own[e];
+            }
+        }
+        float suf = (u1[0] + u1[1]) + (u1[2] + u1[3]), pre = (u2[0] + u2[1]) + (u2[2] + u2[3]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const float down = __shfl_down_sync(0xffffffffu, suf, d), up = __shfl_up_sync(0xffffffffu, pre, d);
+            if (lane + d < 32) suf += down;
+            if (lane >= d) pre += up;
+        }
+        float behind = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+        if (lane == 31) behind = 0.f;
+        if (lane == 0) before = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dg[e] += before + dot;
+            before += u2[e];
+        }
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+            behind += u1[e];
+            dg[e] += behind;
+        }
+        const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        float sA = 0.f, sb = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = 4 * lane + e;
+            if (t >= c.len) continue;
+            const long at = (long)(c.t0 + t) * a.H + h;
+            const float da = fmaf(-rate, dg[e], dt_[e]) * sigmoidf_(a.a[at] + bias);
+            a.da[at] = da;
+            sA = fmaf(dg[e], -rate * gt[rDt * kT + t], sA);
+            sb += da;
+        }
+        sA = warp_sum(sA);
+        sb = warp_sum(sb);
+        if (lane == 0) {
+            const long all = (long)gridDim.x * a.H, sh = (long)blockIdx.x * a.H + h;
+            w.sums[sh] = sA;
+            w.sums[all + sh] = sb;
+            w.sums[2 * all + sh] = dD;
+        }
+    };
+
+    bool failed = __syncthreads_or(!ok);
+    if (!failed && warp == 0) {  // (C B^T)^T: row j of B, column i of C
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k) mma_ss(on, tm + kCB, dBk + kstep(k), dCk + kstep(k), id128, k > 0);
+        commit(on, &bars[MM]);
+    }
+    if (!failed) failed = __syncthreads_or(!wait(MM, mm++));
+    for (int step = 0; step < steps && !failed; ++step) {
+        const int h = h0 + step / slices, s = step % slices, place = step & 1;
+        const uint32_t xt = sm + L::x + place * kBlock, yt = sm + L::y + place * kBlock;
+        const uint64_t dX = sdesc_sw128(xt, 16, 1024), dYk = sdesc_sw128(yt, 16, 1024), dYm = sdesc_sw128(yt, kBlock, 1024);
+        const float* gt = gates_of(h);
+        // ---- dS into its planes
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (s == 0 && step > 0 && warp == 15) finish_head(h - 1);
+        ok = wait(LX0 + place, step >> 1) && wait(LS, seen++);
+        if (ok && c.len < kT) {
+            zero_rows(xt);
+            zero_rows(yt);
+        }
+        float keep[NV][8];
+        const auto convert = [&](bool second) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = i * kGradThreads + tid, n = v >> 3, k = v & 7;
+                uint32_t u[2][4], pl[3][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) planes::lds128(sm + L::st + n * 256 + (((2 * k + e) ^ (n & 7)) << 4), u[e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = __uint_as_float(u[e >> 2][e & 3]);
+                    if (second) ss = fmaf(keep[i][e], x, ss);
+                    else keep[i][e] = x;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    bfp::F2 t = bfp::F2::of(u[e >> 1][2 * (e & 1)], u[e >> 1][2 * (e & 1) + 1]);
+                    pl[0][e] = bfp::peel(t);
+                    pl[1][e] = bfp::peel(t);
+                    pl[2][e] = bfp::pack(t);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::sp + p * kBlock, n, k), pl[p]);
+            }
+        };
+        convert(false);
+        fence_async_smem();
+        if ((failed = __syncthreads_or(!ok))) break;
+        if (s == slices - 1 && h + 1 < h1) ask_gates(h + 1);
+        if (warp == 0) {
+            if (on) {
+                load_image(image(w.states, step));
+                if (step + 1 < steps) load_xy(step + 1);
+            }
+            tc_fence_after();
+            // X dS: [token, n], the smallest plane first; B dS^T: [token, p] of the three planes
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_ss(on, tm + kRes, dX + 2 * k, dSk + p * (kBlock >> 4) + 2 * k, idN, p < 2 || k > 0);
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) mma_ss(on, tm + kPlane, dBk + kstep(k), dSm + k * 128, id192, k > 0);
+            commit(on, &bars[MM]);
+        }
+        ++images;
+        if (step + 1 < steps) ++tiles;
+        ok = wait(MM, mm++);
+        tc_fence_after();
+        const float dt = gt[rDt * kT + j], r_end = gt[rToEnd * kT + j];
+        float cR[16];
+        {
+            const float f = dt * r_end;
+            if (cg * 32 < N) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t r[8];
+                    tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dB[8 * p + e] = fmaf(f, __uint_as_float(r[e]), dB[8 * p + e]);
+                }
+            }
+            float q2 = 0.f;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t hi[8], mid[8], lo[8], x[4];
+                tmem_ld8(tm + kPlane + lanes + cg * 16 + 8 * p, hi);
+                tmem_ld8(tm + kPlane + lanes + 64 + cg * 16 + 8 * p, mid);
+                tmem_ld8(tm + kPlane + lanes + 128 + cg * 16 + 8 * p, lo);
+                planes::lds128(at16(xt, j, cg * 2 + p), x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = r_end * (__uint_as_float(hi[e]) + (__uint_as_float(mid[e]) + __uint_as_float(lo[e])));
+                    cR[8 * p + e] = v;
+                    q2 = fmaf(v, __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16), q2);
+                }
+            }
+            float* to = in2 + cg * kT + j;
+            *to = (s ? *to : 0.f) + dt * q2;
+        }
+        tc_fence_before();
+        if ((failed = __syncthreads_or(!ok))) break;
+        if (warp == 0) {  // x_j . dy_i
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(on, tm + kRes, dX + 2 * k, dYk + 2 * k, id128, k > 0);
+            commit(on, &bars[MM]);
+        }
+        // ---- S0 into the planes' place
+        ok = wait(LS, seen++);
+        convert(true);
+        fence_async_smem();
+        ok = wait(MM, mm++) && ok;
+        tc_fence_after();
+        // ---- E, T and M^T of this thread's row and run of columns
+        {
+            const int u = cg;
+            float acc = 0.f;
+            if (u < q) {
+                const uint32_t zero[8] = {};
+#pragma unroll
+                for (int p = 0; p < 6; ++p) tmem_st8(tm + kPlane + lanes + 48 * u + 8 * p, zero);
+            } else {
+                float f = gt[rToRun * kT + j];
+                for (int v = q + 1; v < u; ++v) f *= gt[kRows * kT + v];
+                const float ph = gt[rPh * kT + j], pl = gt[rPl * kT + j];
+#pragma unroll
+                for (int p = 3; p >= 0; --p) {
+                    uint32_t re[8], rc[8], hi[4], mid[4], lo[4];
+                    tmem_ld8(tm + kRes + lanes + 32 * u + 8 * p, re);
+                    tmem_ld8(tm + kCB + lanes + 32 * u + 8 * p, rc);
+                    float d[8], m[8], t[8];
+                    const float* at = gt + 32 * u + 8 * p;
+                    if (u == q) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d[e] = exp2_hw((at[rPh * kT + e] - ph) + (at[rPl * kT + e] - pl));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d[e] = at[rFromRun * kT + e] * f;
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 7; e >= 0; --e) {
+                        const bool in = u > q || 8 * p + e >= lane, below = u > q || 8 * p + e > lane;
+                        const float cb = __uint_as_float(rc[e]);
+                        m[e] = in ? d[e] * cb : 0.f;
+                        const float E = in ? d[e] * dt * __uint_as_float(re[e]) : 0.f;
+                        Es[8 * p + e] += E;
+                        acc += below ? E * cb : 0.f;
+                        t[e] = below ? acc : 0.f;  // sum over i >= t of row j < t
+                    }
+                    const float col = sum_rows<8, 32>(t, lane);
+                    if (lane < 8) {
+                        float* to = colS + q * kT + 32 * u + 8 * p + lane;
+                        *to = (s ? *to : 0.f) + col;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        bfp::F2 x(m[2 * e], m[2 * e + 1]);
+                        hi[e] = bfp::peel(x);
+                        mid[e] = bfp::peel(x);
+                        lo[e] = bfp::pack(x);
+                    }
+                    const uint32_t to = tm + kPlane + lanes + 24 * (2 * u + (p >> 1)) + 4 * (p & 1);
+                    tmem_st4(to, hi);
+                    tmem_st4(to + 8, mid);
+                    tmem_st4(to + 16, lo);
+                }
+            }
+            float* to = rowT + u * kT + j;
+            *to = (s ? *to : 0.f) + acc;
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        if ((failed = __syncthreads_or(!ok))) break;
+        if (warp == 0) {
+            if (on && step + 1 < steps) load_image(image(w.dstates, step + 1));
+            tc_fence_after();
+            // M^T dy, and dy S0
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_ts(on, tm + kDv, tm + kPlane + 24 * k + 8 * p, dYm + k * 128, id64, p < 2 || k > 0);
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_ss(on, tm + kRes, dYk + 2 * k, dSk + p * (kBlock >> 4) + 2 * k, idN, p < 2 || k > 0);
+            commit(on, &bars[MM]);
+        }
+        if (step + 1 < steps) ++images;
+        ok = wait(MM, mm++);
+        tc_fence_after();
+        {
+            const float D = a.D ? a.D[h] : 0.f, b = gt[rFromStart * kT + j];
+            float qd = 0.f, q1 = 0.f;
+            __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(a.dx) + ((long)(c.t0 + j) * a.H + h) * a.P + s * 64 + cg * 16;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t r[8], x[4], y[4], o[4];
+                tmem_ld8(tm + kDv + lanes + cg * 16 + 8 * p, r);
+                planes::lds128(at16(xt, j, cg * 2 + p), x);
+                planes::lds128(at16(yt, j, cg * 2 + p), y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = cR[8 * p + 2 * e] + __uint_as_float(r[2 * e]), v1 = cR[8 * p + 2 * e + 1] + __uint_as_float(r[2 * e + 1]);
+                    const float x0 = __uint_as_float(x[e] << 16), x1 = __uint_as_float(x[e] & 0xffff0000u);
+                    const float y0 = __uint_as_float(y[e] << 16), y1 = __uint_as_float(y[e] & 0xffff0000u);
+                    qd = fmaf(v0, x0, fmaf(v1, x1, qd));
+                    sd = fmaf(y0, x0, fmaf(y1, x1, sd));
+                    o[e] = pack_bf16(fmaf(dt, v0, D * y0), fmaf(dt, v1, D * y1));
+                }
+                if (j < c.len) reinterpret_cast<uint4*>(dx)[p] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (cg * 32 < N) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t r[8], cc[4];
+                    tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, r);
+                    planes::lds128(at16(sm + L::c + (cg >> 1) * kBlock, j, (cg & 1) * 4 + p), cc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = b * __uint_as_float(r[e]);
+                        q1 = fmaf(v, __uint_as_float(e & 1 ? cc[e >> 1] & 0xffff0000u : cc[e >> 1] << 16), q1);
+                        dC[8 * p + e] += v;
+                    }
+                }
+            }
+            float* to = in1 + cg * kT + j;
+            *to = (s ? *to : 0.f) + q1;
+            to = ddt + cg * kT + j;
+            *to = (s ? *to : 0.f) + qd;
+            if (s == slices - 1) {
+                ss = warp_sum(ss);
+                sd = warp_sum(sd);
+                if (lane == 0) {
+                    part[warp] = ss;
+                    part[kGradWarps + warp] = sd;
+                }
+                ss = sd = 0.f;
+            }
+        }
+        tc_fence_before();
+        failed = __syncthreads_or(!ok);
+    }
+    if (!failed && steps > 0 && warp == 15) finish_head(h1 - 1);
+    if (!failed) {
+        // dB += E^T C, dC += E B with the heads' sum of E in two planes (the outputs are bf16): rows j, columns i
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t hi[4], mid[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bfp::F2 x(Es[8 * p + 2 * e], Es[8 * p + 2 * e + 1]);
+                hi[e] = bfp::peel(x);
+                mid[e] = bfp::pack(x);
+            }
+            const uint32_t tile = sm + L::sp + (cg >> 1) * kBlock;
+            planes::sts128(at16(tile, j, (cg & 1) * 4 + p), hi);
+            planes::sts128(at16(tile + 2 * kBlock, j, (cg & 1) * 4 + p), mid);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            tc_fence_after();
+            constexpr uint32_t idB = idesc_bf16(128, N, 0, 1), idC = idesc_bf16(128, N, 1, 1);
+            const uint64_t dEk = sdesc_sw128(sm + L::sp, 16, 1024), dEm = sdesc_sw128(sm + L::sp, kBlock, 1024);
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mma_ss(on, tm + kRes, dEk + p * (kBlock >> 3) + kstep(k), dCm + k * 128, idB, p == 0 || k > 0);
+                    mma_ss(on, tm + kPlane, dEm + p * (kBlock >> 3) + k * 128, dBm + k * 128, idC, p == 0 || k > 0);
+                }
+            commit(on, &bars[MM]);
+        }
+        ok = wait(MM, mm++);
+        failed = __syncthreads_or(!ok);
+        tc_fence_after();
+        if (!failed && cg * 32 < N) {
+            const long at = ((long)(c.t0 + j) * a.G + g) * N + cg * 32, all = (long)a.seqs.total_T * a.G * N;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint32_t rb[8], rc[8];
+                tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, rb);
+                tmem_ld8(tm + kPlane + lanes + cg * 32 + 8 * p, rc);
+                tmem_wait_ld();
+                float vb[8], vc[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    vb[e] = dB[8 * p + e] + __uint_as_float(rb[e]);
+                    vc[e] = dC[8 * p + e] + __uint_as_float(rc[e]);
+                }
+                if (j >= c.len) continue;
+                if (w.subsets > 1) {
+                    store_row<8>(w.parts + subset * all + at + 8 * p, vb);
+                    store_row<8>(w.parts + (w.subsets + subset) * all + at + 8 * p, vc);
+                } else {
+                    store_row<8>(static_cast<__nv_bfloat16*>(a.dB) + at + 8 * p, vb);
+                    store_row<8>(static_cast<__nv_bfloat16*>(a.dC) + at + 8 * p, vc);
+                }
+            }
+        }
+    }
+    // loads and MMAs in flight, after a wait that ran out, end before the block leaves
+    if (failed && warp == 0 && on) {
+        mbar_wait(&bars[LB], 0, kLimit);
+        for (int k = max(0, tiles - 2); k < tiles; ++k) mbar_wait(&bars[LX0 + (k & 1)], (k >> 1) & 1, kLimit);
+        if (images > 0) mbar_wait(&bars[LS], (images - 1) & 1, kLimit);
+        mbar_wait(&bars[MM], (mm - 1) & 1, kLimit);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// Subsets of a group's heads: more blocks fill more SMs, but each loads B and C, ends with two products of its own, and
+// writes dB and dC in fp32 for another kernel to add.  In head steps of about 5 us.
+int subsets_of(int num_seqs, int total_T, int H, int G, int N) {
+    const long blocks = slots128(num_seqs, total_T) * G, per = H / G;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= per && s <= 16; ++s) {
+        const double rounds = (double)((blocks * s + 151) / 152), heads = (double)((per + s - 1) / s) + 0.7;
+        const double parts = s > 1 ? 0.8 + (2.0 * s + 1) * 2 * total_T * G * N * 4 / 5e12 / 5e-6 : 0.0;
+        if (rounds * heads + parts < least) {
+            least = rounds * heads + parts;
+            best = s;
+        }
+    }
+    return best;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, TcWork* w, unsigned char* at) {
+    const size_t slots = (size_t)slots128(num_seqs, total_T);
+    const size_t gates = up256(slots * H * kGates * sizeof(float)), states = slots * H * P * N * sizeof(float),
+                 sums = up256(slots * H * 3 * sizeof(float));
+    const int subsets = subsets_of(num_seqs, total_T, H, G, N);
+    const size_t parts = subsets > 1 ? (size_t)subsets * 2 * total_T * G * N * sizeof(float) : 0;
+    if (w) {
+        w->gates = reinterpret_cast<float*>(at);
+        w->states = reinterpret_cast<float*>(at + gates);
+        w->dstates = reinterpret_cast<float*>(at + gates + states);
+        w->sums = reinterpret_cast<float*>(at + gates + 2 * states);
+        w->parts = reinterpret_cast<float*>(at + gates + 2 * states + sums);
+        w->subsets = subsets;
+    }
+    return gates + 2 * states + sums + parts;
+}
+
+template <int N>
+cudaError_t launch(const SsmArgs& a, const TcWork& w, cudaStream_t s) {
+    CUtensorMap mX, mY, mB, mC;
+    const long T = a.seqs.total_T;
+    if (!map_rows(&mX, a.x, T, (long)a.H * a.P, a.x_stride) || !map_rows(&mY, a.dout, T, (long)a.H * a.P, (long)a.H * a.P) ||
+        !map_rows(&mB, a.B, T, (long)a.G * N, a.B_stride) || !map_rows(&mC, a.C, T, (long)a.G * N, a.C_stride))
+        return cudaErrorInvalidValue;
+    const unsigned slots = (unsigned)slots128(a.seqs.num_seqs, a.seqs.total_T);
+    ssm_gates128_kernel<<<dim3(slots, (unsigned)((a.H + kGateWarps - 1) / kGateWarps)), kGateWarps * 32, 0, s>>>(a, w.gates);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(ssm_scan_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanLay<N>::bytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(ssm_grad_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradLay<N>::bytes);
+    if (e != cudaSuccess) return e;
+    ssm_scan_tc_kernel<N><<<dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), 2), kScanThreads, ScanLay<N>::bytes, s>>>(mX, mY, mB, mC, a, w);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ssm_grad_tc_kernel<N><<<dim3(slots, (unsigned)(a.G * w.subsets)), kGradThreads, GradLay<N>::bytes, s>>>(mX, mY, mB, mC, a, w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t tc_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N) {
+    return layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
+}
+
+cudaError_t launch_tc_bwd(const SsmArgs& a, cudaStream_t s) {
+    TcWork w{};
+    layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
+    const cudaError_t e = a.N == 128 ? launch<128>(a, w, s) : launch<64>(a, w, s);
+    if (e != cudaSuccess) return e;
+    Work f{};
+    f.sums = w.sums;
+    f.parts = w.parts;
+    f.subsets = w.subsets;
+    return launch_finish(a, f, slots128(a.seqs.num_seqs, a.seqs.total_T), s);
+}
+
+}  // namespace ssm
+}  // namespace gdn
