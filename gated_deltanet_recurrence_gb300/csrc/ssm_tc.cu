@@ -34,7 +34,7 @@ using namespace tc;
 constexpr int kWorkers = 256;              // threads of a role's two sets of four warps
 constexpr int kThreads = 2 * kWorkers + 3 * 32;
 
-enum Bar { FB, EB, FC0, FC1, EC0, EC1, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
+enum Bar { FB, EB, FC0, FC1, EC0, EC1, FX0, FX1, EX0, EX1, GF0, GF1, GE0, GE1, VR, UA, UD, SR, CSD, CBD, MR, YD, YE, DR, kBars };
 
 template <int N>
 struct Lay {
@@ -345,10 +345,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU, dBm + k * 128, dV + k * 128, idU, k > 0);
-#pragma unroll
-            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dBm + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
-            commit(on, &bars[UD]);
-            commit(on, &bars[EB]);
+            commit(on, &bars[UA]);
             if (c > 0 && !wait(YE, c - 1)) break;
             tc_fence_after();
 #pragma unroll
@@ -356,6 +353,14 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 mma_ss(on, tCS, dCk + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), dS + k * 128, idCS, k > 0);
             commit(on, &bars[CSD]);
             commit(on, &bars[EC0 + st]);
+            // the low plane's sums go into the middle one's columns; MMAs of two shapes on the same columns are not ordered
+            // by themselves
+            if (!wait(UA, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dBm + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
+            commit(on, &bars[UD]);
+            commit(on, &bars[EB]);
             if (!wait(FX0 + st, c >> 1) || !wait(MR, c)) break;
             tc_fence_after();
 #pragma unroll

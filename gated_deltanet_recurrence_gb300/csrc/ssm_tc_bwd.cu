@@ -11,6 +11,8 @@
 //   dg_t = sum over pairs i >= t > j of T_ij + sum_{i >= t} b_i dy_i . S_0 C_i + b_last <dS_1, S_0>
 //          + sum_{j < t} r_j v_j . dS_1 B_j
 // is taken as it stands, without subtractions: suffix sums of T along a row, added over the rows before t.
+#include <type_traits>
+
 #include "ssm_tc.cuh"
 
 namespace gdn {
@@ -128,7 +130,7 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
-    const uint32_t tU = tm, tS = tm + 128;
+    const uint32_t tU = tm, tS = tm + 192;  // U: the three planes' sums
     const auto wait = [&](int bar, int index) -> bool {
         bool ok = mbar_try_wait(&bars[bar], index & 1, 100000u);
         if (!ok) ok = wait_slow(&bars[bar], index & 1, dead, a.err);
@@ -198,15 +200,16 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                         S[p / 2] = holds && init ? bfp::F2(from[0], from[N]) : bfp::F2(0.f, 0.f);
                     }
                 } else {
-                    uint32_t old[8], hi[8], mid[8];
+                    uint32_t old[8], hi[8], mid[8], lo[8];
                     tmem_ld8(tS + lanes + col, old);
                     tmem_ld8(tU + lanes + col, hi);
                     tmem_ld8(tU + lanes + 64 + col, mid);
+                    tmem_ld8(tU + lanes + 128 + col, lo);
                     tmem_wait_ld();
 #pragma unroll
                     for (int p = 0; p < 8; p += 2)
                         S[p / 2] = bfp::fma2(bfp::F2(decay, decay), bfp::F2::of(old[p], old[p + 1]),
-                                             bfp::F2::of(hi[p], hi[p + 1]) + bfp::F2::of(mid[p], mid[p + 1]));
+                                             bfp::F2::of(hi[p], hi[p + 1]) + (bfp::F2::of(mid[p], mid[p + 1]) + bfp::F2::of(lo[p], lo[p + 1])));
                 }
                 float v[8];
 #pragma unroll
@@ -248,7 +251,7 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         if (leader) bulk_wait_all();
     } else if (warp == 16) {
         // ================= MMAs =================
-        constexpr uint32_t idU = idesc_bf16(128, 128, 1, 1), idUl = idesc_bf16(128, 64, 1, 1);
+        constexpr uint32_t idU = idesc_bf16(128, 192, 1, 1);
         const uint32_t on = elect();
         const uint64_t dV = sdesc_sw128(sm + L::v, kBlock, 1024);
         for (int c = 0; c < chunks; ++c) {
@@ -258,8 +261,6 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU, dK + k * 128, dV + k * 128, idU, k > 0);
-#pragma unroll
-            for (int k = 0; k < kT / 16; ++k) mma_ss(on, tU + 64, dK + k * 128, dV + 2 * (kBlock >> 4) + k * 128, idUl, 1);
             commit(on, &bars[UD]);
             commit(on, &bars[KE0 + st]);
         }
@@ -433,85 +434,84 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     constexpr uint32_t id128 = idesc_bf16(128, 128, 0, 0), idN = idesc_bf16(128, N, 0, 0), id192 = idesc_bf16(128, 192, 0, 1),
                        id64 = idesc_bf16(128, 64, 0, 1);
     const auto kstep = [](int k) { return (uint64_t)(((k >> 2) * kBlock + (k & 3) * 32) >> 4); };  // of a K-major tile
-    float Es[32], dB[32], dC[32];
+    bfp::F2 Es[16], dB[16], dC[16];  // pairs of columns
 #pragma unroll
-    for (int i = 0; i < 32; ++i) Es[i] = dB[i] = dC[i] = 0.f;
-    float ss = 0.f, sd = 0.f;
+    for (int i = 0; i < 16; ++i) Es[i] = dB[i] = dC[i] = bfp::F2(0.f, 0.f);
+    bfp::F2 ss2(0.f, 0.f), sd2(0.f, 0.f);
 
     // dg, da and the sums of a head whose parts are all there: one warp, four tokens a lane
     const auto finish_head = [&](int h) {
         const float* gt = gates_of(h);
-        float dot = lane < kGradWarps ? part[lane] : 0.f, dD = lane < kGradWarps ? part[kGradWarps + lane] : 0.f;
-        dot = warp_sum(dot) * gt[kRows * kT + 4];
-        dD = warp_sum(dD);
-        float u1[4], u2[4], dt_[4], dg[4];
+        const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        float z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = 4 * lane + e < c.len ? a.a[(long)(c.t0 + 4 * lane + e) * a.H + h] + bias : 0.f;
         const int u = lane >> 3;
+        const auto four = [&](const float* from, float (&x)[4]) { load_row<4>(from + 4 * lane, x); };
+        float u1[4] = {}, u2[4] = {}, dd[4] = {}, dg[4] = {}, own[3][4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = 4 * lane + e;
-            u1[e] = u2[e] = dt_[e] = dg[e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                u1[e] += in1[k * kT + t];
-                u2[e] += in2[k * kT + t];
-                dt_[e] += ddt[k * kT + t];
-                if (k <= u) dg[e] += colS[k * kT + t];
-            }
-        }
-        // what the rows before t have in the runs behind t's own: for each run, sums over the rows before
-#pragma unroll
-        for (int run = 0; run < 3; ++run) {
-            float own[4], sum = 0.f;
+        for (int k = 0; k < 4; ++k) {
+            float x[5][4];
+            four(in1 + k * kT, x[0]);
+            four(in2 + k * kT, x[1]);
+            four(ddt + k * kT, x[2]);
+            four(colS + k * kT, x[3]);
+            four(rowT + k * kT, x[4]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = 0.f;
+                u1[e] += x[0][e];
+                u2[e] += x[1][e];
+                dd[e] += x[2][e];
+                if (k <= u) dg[e] += x[3][e];
 #pragma unroll
-                for (int k = run + 1; k < 4; ++k) x += u <= run ? rowT[k * kT + 4 * lane + e] : 0.f;
-                own[e] = x;
-                sum += x;
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float up = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += up;
-            }
-            float before = __shfl_up_sync(0xffffffffu, sum, 1);
-            if (lane == 0) before = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (u == run) dg[e] += before;
-                before += own[e];
+                for (int run = 0; run < 3; ++run)  // what a row in run `run` or before has in the runs behind it
+                    if (run < k && u <= run) own[run][e] += x[4][e];
             }
         }
-        float suf = (u1[0] + u1[1]) + (u1[2] + u1[3]), pre = (u2[0] + u2[1]) + (u2[2] + u2[3]);
+        float dot = lane < kGradWarps ? part[lane] : 0.f, dD = lane < kGradWarps ? part[kGradWarps + lane] : 0.f;
+        // sums over the rows before t of those, and of u2; over the rows from t on of u1
+        float pre[4], suf = (u1[0] + u1[1]) + (u1[2] + u1[3]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) pre[k] = (own[k][0] + own[k][1]) + (own[k][2] + own[k][3]);
+        pre[3] = (u2[0] + u2[1]) + (u2[2] + u2[3]);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const float down = __shfl_down_sync(0xffffffffu, suf, d), up = __shfl_up_sync(0xffffffffu, pre, d);
+            float up[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) up[k] = __shfl_up_sync(0xffffffffu, pre[k], d);
+            const float down = __shfl_down_sync(0xffffffffu, suf, d);
+            dot += __shfl_xor_sync(0xffffffffu, dot, d);
+            dD += __shfl_xor_sync(0xffffffffu, dD, d);
+            if (lane >= d) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pre[k] += up[k];
+            }
             if (lane + d < 32) suf += down;
-            if (lane >= d) pre += up;
         }
-        float behind = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-        if (lane == 31) behind = 0.f;
-        if (lane == 0) before = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            pre[k] = __shfl_up_sync(0xffffffffu, pre[k], 1);
+            if (lane == 0) pre[k] = 0.f;
+        }
+        suf = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 31) suf = 0.f;
+        dot *= gt[kRows * kT + 4];
+        float before = u == 0 ? pre[0] : (u == 1 ? pre[1] : (u == 2 ? pre[2] : 0.f));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            dg[e] += before + dot;
-            before += u2[e];
+            dg[e] += (before + pre[3]) + dot;
+            before += u == 0 ? own[0][e] : (u == 1 ? own[1][e] : (u == 2 ? own[2][e] : 0.f));
+            pre[3] += u2[e];
         }
-#pragma unroll
-        for (int e = 3; e >= 0; --e) {
-            behind += u1[e];
-            dg[e] += behind;
-        }
-        const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         float sA = 0.f, sb = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 3; e >= 0; --e) {
+            suf += u1[e];
+            dg[e] += suf;
             const int t = 4 * lane + e;
             if (t >= c.len) continue;
-            const long at = (long)(c.t0 + t) * a.H + h;
-            const float da = fmaf(-rate, dg[e], dt_[e]) * sigmoidf_(a.a[at] + bias);
-            a.da[at] = da;
+            const float da = fmaf(-rate, dg[e], dd[e]) * sigmoidf_(z[e]);
+            a.da[(long)(c.t0 + t) * a.H + h] = da;
             sA = fmaf(dg[e], -rate * gt[rDt * kT + t], sA);
             sb += da;
         }
@@ -522,6 +522,17 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
             w.sums[sh] = sA;
             w.sums[all + sh] = sb;
             w.sums[2 * all + sh] = dD;
+        }
+    };
+    // dx of a step lies in its x's place until the next step, when whole rows are written
+    const auto store_dx = [&](int step) {
+        __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(a.dx) + ((long)c.t0 * a.H + h0 + step / slices) * a.P + step % slices * 64;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 64 + (tid >> 3), k = tid & 7;
+            uint32_t u[4];
+            planes::lds128(at16(sm + L::x + (step & 1) * kBlock, r, k), u);
+            if (r < c.len) reinterpret_cast<uint4*>(dx + (long)r * a.H * a.P)[k] = make_uint4(u[0], u[1], u[2], u[3]);
         }
     };
 
@@ -541,24 +552,27 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         // ---- dS into its planes
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (s == 0 && step > 0 && warp == 15) finish_head(h - 1);
+        if (step > 0) store_dx(step - 1);
         ok = wait(LX0 + place, step >> 1) && wait(LS, seen++);
         if (ok && c.len < kT) {
             zero_rows(xt);
             zero_rows(yt);
         }
-        float keep[NV][8];
         const auto convert = [&](bool second) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int v = i * kGradThreads + tid, n = v >> 3, k = v & 7;
+                const uint32_t at = at16(sm + L::sp, n, k);
                 uint32_t u[2][4], pl[3][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) planes::lds128(sm + L::st + n * 256 + (((2 * k + e) ^ (n & 7)) << 4), u[e]);
+                if (second) {  // dS is the sum of the planes that S0 replaces
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = __uint_as_float(u[e >> 2][e & 3]);
-                    if (second) ss = fmaf(keep[i][e], x, ss);
-                    else keep[i][e] = x;
+                    for (int p = 0; p < 3; ++p) planes::lds128(at + p * kBlock, pl[p]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        ss2 = bfp::fma2(bfp::F2::of(u[e >> 1][2 * (e & 1)], u[e >> 1][2 * (e & 1) + 1]),
+                                        bfp::widen(pl[0][e]) + (bfp::widen(pl[1][e]) + bfp::widen(pl[2][e])), ss2);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -568,7 +582,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                     pl[2][e] = bfp::pack(t);
                 }
 #pragma unroll
-                for (int p = 0; p < 3; ++p) planes::sts128(at16(sm + L::sp + p * kBlock, n, k), pl[p]);
+                for (int p = 0; p < 3; ++p) planes::sts128(at + p * kBlock, pl[p]);
             }
         };
         convert(false);
@@ -595,20 +609,9 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         ok = wait(MM, mm++);
         tc_fence_after();
         const float dt = gt[rDt * kT + j], r_end = gt[rToEnd * kT + j];
-        float cR[16];
         {
-            const float f = dt * r_end;
-            if (cg * 32 < N) {
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t r[8];
-                    tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dB[8 * p + e] = fmaf(f, __uint_as_float(r[e]), dB[8 * p + e]);
-                }
-            }
-            float q2 = 0.f;
+            const bfp::F2 f(dt * r_end, dt * r_end), re(r_end, r_end);
+            bfp::F2 sum(0.f, 0.f);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 uint32_t hi[8], mid[8], lo[8], x[4];
@@ -618,14 +621,32 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 planes::lds128(at16(xt, j, cg * 2 + p), x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = r_end * (__uint_as_float(hi[e]) + (__uint_as_float(mid[e]) + __uint_as_float(lo[e])));
-                    cR[8 * p + e] = v;
-                    q2 = fmaf(v, __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16), q2);
+                for (int e = 0; e < 4; ++e) {
+                    const bfp::F2 v = re * (bfp::F2::of(hi[2 * e], hi[2 * e + 1]) + (bfp::F2::of(mid[2 * e], mid[2 * e + 1]) + bfp::F2::of(lo[2 * e], lo[2 * e + 1])));
+                    sum = bfp::fma2(v, bfp::widen(x[e]), sum);
+                    float v0, v1;
+                    v.get(v0, v1);
+                    hi[2 * e] = __float_as_uint(v0);
+                    hi[2 * e + 1] = __float_as_uint(v1);
+                }
+                tmem_st8(tm + kDv + lanes + cg * 16 + 8 * p, hi);  // M^T dy is added to it there
+            }
+            float q2, odd;
+            sum.get(q2, odd);
+            q2 += odd;
+            if (cg * 32 < N) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t r[8];
+                    tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dB[4 * p + e] = bfp::fma2(f, bfp::F2::of(r[2 * e], r[2 * e + 1]), dB[4 * p + e]);
                 }
             }
             float* to = in2 + cg * kT + j;
             *to = (s ? *to : 0.f) + dt * q2;
+            tmem_wait_st();
         }
         tc_fence_before();
         if ((failed = __syncthreads_or(!ok))) break;
@@ -653,48 +674,67 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 float f = gt[rToRun * kT + j];
                 for (int v = q + 1; v < u; ++v) f *= gt[kRows * kT + v];
                 const float ph = gt[rPh * kT + j], pl = gt[rPl * kT + j];
+                const bfp::F2 f2(f, f), dt2(dt, dt);
+                // eight columns at a time, from the last; the run on the diagonal keeps its upper triangle
+                const auto columns = [&](auto diagonal) {
+                    constexpr bool kDiagonal = decltype(diagonal)::value;
 #pragma unroll
-                for (int p = 3; p >= 0; --p) {
-                    uint32_t re[8], rc[8], hi[4], mid[4], lo[4];
-                    tmem_ld8(tm + kRes + lanes + 32 * u + 8 * p, re);
-                    tmem_ld8(tm + kCB + lanes + 32 * u + 8 * p, rc);
-                    float d[8], m[8], t[8];
-                    const float* at = gt + 32 * u + 8 * p;
-                    if (u == q) {
+                    for (int p = 3; p >= 0; --p) {
+                        uint32_t re[8], rc[8], hi[4], mid[4], lo[4];
+                        tmem_ld8(tm + kRes + lanes + 32 * u + 8 * p, re);
+                        tmem_ld8(tm + kCB + lanes + 32 * u + 8 * p, rc);
+                        bfp::F2 d[4];
+                        float x[8], y[8];
+                        if constexpr (kDiagonal) {
+                            load_row<8>(gt + rPh * kT + 32 * u + 8 * p, x);
+                            load_row<8>(gt + rPl * kT + 32 * u + 8 * p, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = exp2_hw((at[rPh * kT + e] - ph) + (at[rPl * kT + e] - pl));
-                    } else {
+                            for (int e = 0; e < 8; ++e) x[e] = exp2_hw((x[e] - ph) + (y[e] - pl));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d[e] = at[rFromRun * kT + e] * f;
+                            for (int e = 0; e < 4; ++e) d[e] = bfp::F2(x[2 * e], x[2 * e + 1]);
+                        } else {
+                            load_row<8>(gt + rFromRun * kT + 32 * u + 8 * p, x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) d[e] = bfp::F2(x[2 * e], x[2 * e + 1]) * f2;
+                        }
+                        tmem_wait_ld();
+                        float t[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bfp::F2 cb = bfp::F2::of(rc[2 * e], rc[2 * e + 1]);
+                            bfp::F2 E = d[e] * dt2 * bfp::F2::of(re[2 * e], re[2 * e + 1]), M = d[e] * cb;
+                            if constexpr (kDiagonal) {
+                                float v0, v1;
+                                E.get(v0, v1);
+                                E = bfp::F2(8 * p + 2 * e >= lane ? v0 : 0.f, 8 * p + 2 * e + 1 >= lane ? v1 : 0.f);
+                                M.get(v0, v1);
+                                M = bfp::F2(8 * p + 2 * e >= lane ? v0 : 0.f, 8 * p + 2 * e + 1 >= lane ? v1 : 0.f);
+                            }
+                            Es[4 * p + e] = Es[4 * p + e] + E;
+                            (E * cb).get(t[2 * e], t[2 * e + 1]);
+                            hi[e] = bfp::peel(M);
+                            mid[e] = bfp::peel(M);
+                            lo[e] = bfp::pack(M);
+                        }
+                        const uint32_t at = tm + kPlane + lanes + 24 * (2 * u + (p >> 1)) + 4 * (p & 1);
+                        tmem_st4(at, hi);
+                        tmem_st4(at + 8, mid);
+                        tmem_st4(at + 16, lo);
+#pragma unroll
+                        for (int e = 7; e >= 0; --e) {  // sum over i >= t of row j < t
+                            const bool below = !kDiagonal || 8 * p + e > lane;
+                            acc += below ? t[e] : 0.f;
+                            t[e] = below ? acc : 0.f;
+                        }
+                        const float col = sum_rows<8, 32>(t, lane);
+                        if (lane < 8) {
+                            float* to = colS + q * kT + 32 * u + 8 * p + lane;
+                            *to = (s ? *to : 0.f) + col;
+                        }
                     }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 7; e >= 0; --e) {
-                        const bool in = u > q || 8 * p + e >= lane, below = u > q || 8 * p + e > lane;
-                        const float cb = __uint_as_float(rc[e]);
-                        m[e] = in ? d[e] * cb : 0.f;
-                        const float E = in ? d[e] * dt * __uint_as_float(re[e]) : 0.f;
-                        Es[8 * p + e] += E;
-                        acc += below ? E * cb : 0.f;
-                        t[e] = below ? acc : 0.f;  // sum over i >= t of row j < t
-                    }
-                    const float col = sum_rows<8, 32>(t, lane);
-                    if (lane < 8) {
-                        float* to = colS + q * kT + 32 * u + 8 * p + lane;
-                        *to = (s ? *to : 0.f) + col;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        bfp::F2 x(m[2 * e], m[2 * e + 1]);
-                        hi[e] = bfp::peel(x);
-                        mid[e] = bfp::peel(x);
-                        lo[e] = bfp::pack(x);
-                    }
-                    const uint32_t to = tm + kPlane + lanes + 24 * (2 * u + (p >> 1)) + 4 * (p & 1);
-                    tmem_st4(to, hi);
-                    tmem_st4(to + 8, mid);
-                    tmem_st4(to + 16, lo);
-                }
+                };
+                if (u == q) columns(std::true_type{});
+                else columns(std::false_type{});
             }
             float* to = rowT + u * kT + j;
             *to = (s ? *to : 0.f) + acc;
@@ -709,7 +749,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
 #pragma unroll
             for (int p = 2; p >= 0; --p)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ts(on, tm + kDv, tm + kPlane + 24 * k + 8 * p, dYm + k * 128, id64, p < 2 || k > 0);
+                for (int k = 0; k < 8; ++k) mma_ts(on, tm + kDv, tm + kPlane + 24 * k + 8 * p, dYm + k * 128, id64, 1);
 #pragma unroll
             for (int p = 2; p >= 0; --p)
 #pragma unroll
@@ -721,69 +761,75 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         tc_fence_after();
         {
             const float D = a.D ? a.D[h] : 0.f, b = gt[rFromStart * kT + j];
-            float qd = 0.f, q1 = 0.f;
-            __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(a.dx) + ((long)(c.t0 + j) * a.H + h) * a.P + s * 64 + cg * 16;
+            const bfp::F2 dt2(dt, dt), D2(D, D), b2(b, b);
+            bfp::F2 qd2(0.f, 0.f), q12(0.f, 0.f);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                uint32_t r[8], x[4], y[4], o[4];
+                uint32_t r[8], x[4], y[4];
                 tmem_ld8(tm + kDv + lanes + cg * 16 + 8 * p, r);
                 planes::lds128(at16(xt, j, cg * 2 + p), x);
                 planes::lds128(at16(yt, j, cg * 2 + p), y);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v0 = cR[8 * p + 2 * e] + __uint_as_float(r[2 * e]), v1 = cR[8 * p + 2 * e + 1] + __uint_as_float(r[2 * e + 1]);
-                    const float x0 = __uint_as_float(x[e] << 16), x1 = __uint_as_float(x[e] & 0xffff0000u);
-                    const float y0 = __uint_as_float(y[e] << 16), y1 = __uint_as_float(y[e] & 0xffff0000u);
-                    qd = fmaf(v0, x0, fmaf(v1, x1, qd));
-                    sd = fmaf(y0, x0, fmaf(y1, x1, sd));
-                    o[e] = pack_bf16(fmaf(dt, v0, D * y0), fmaf(dt, v1, D * y1));
+                    const bfp::F2 v = bfp::F2::of(r[2 * e], r[2 * e + 1]), xe = bfp::widen(x[e]), ye = bfp::widen(y[e]);
+                    qd2 = bfp::fma2(v, xe, qd2);
+                    sd2 = bfp::fma2(ye, xe, sd2);
+                    x[e] = bfp::pack(bfp::fma2(dt2, v, D2 * ye));
                 }
-                if (j < c.len) reinterpret_cast<uint4*>(dx)[p] = make_uint4(o[0], o[1], o[2], o[3]);
+                planes::sts128(at16(xt, j, cg * 2 + p), x);  // dx takes x's place
             }
             if (cg * 32 < N) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    uint32_t r[8], cc[4];
+                    uint32_t r[8], x[4];
                     tmem_ld8(tm + kRes + lanes + cg * 32 + 8 * p, r);
-                    planes::lds128(at16(sm + L::c + (cg >> 1) * kBlock, j, (cg & 1) * 4 + p), cc);
+                    planes::lds128(at16(sm + L::c + (cg >> 1) * kBlock, j, (cg & 1) * 4 + p), x);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = b * __uint_as_float(r[e]);
-                        q1 = fmaf(v, __uint_as_float(e & 1 ? cc[e >> 1] & 0xffff0000u : cc[e >> 1] << 16), q1);
-                        dC[8 * p + e] += v;
+                    for (int e = 0; e < 4; ++e) {
+                        const bfp::F2 v = b2 * bfp::F2::of(r[2 * e], r[2 * e + 1]);
+                        q12 = bfp::fma2(v, bfp::widen(x[e]), q12);
+                        dC[4 * p + e] = dC[4 * p + e] + v;
                     }
                 }
             }
+            float qd, q1, odd;
+            qd2.get(qd, odd);
+            qd += odd;
+            q12.get(q1, odd);
+            q1 += odd;
             float* to = in1 + cg * kT + j;
             *to = (s ? *to : 0.f) + q1;
             to = ddt + cg * kT + j;
             *to = (s ? *to : 0.f) + qd;
             if (s == slices - 1) {
-                ss = warp_sum(ss);
-                sd = warp_sum(sd);
+                float x0, x1, y0, y1;
+                ss2.get(x0, x1);
+                sd2.get(y0, y1);
+                x0 = warp_sum(x0 + x1);
+                y0 = warp_sum(y0 + y1);
                 if (lane == 0) {
-                    part[warp] = ss;
-                    part[kGradWarps + warp] = sd;
+                    part[warp] = x0;
+                    part[kGradWarps + warp] = y0;
                 }
-                ss = sd = 0.f;
+                ss2 = sd2 = bfp::F2(0.f, 0.f);
             }
         }
         tc_fence_before();
         failed = __syncthreads_or(!ok);
     }
-    if (!failed && steps > 0 && warp == 15) finish_head(h1 - 1);
+    if (!failed && warp == 15) finish_head(h1 - 1);
     if (!failed) {
+        store_dx(steps - 1);
         // dB += E^T C, dC += E B with the heads' sum of E in two planes (the outputs are bf16): rows j, columns i
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             uint32_t hi[4], mid[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                bfp::F2 x(Es[8 * p + 2 * e], Es[8 * p + 2 * e + 1]);
-                hi[e] = bfp::peel(x);
-                mid[e] = bfp::pack(x);
+                hi[e] = bfp::peel(Es[4 * p + e]);
+                mid[e] = bfp::pack(Es[4 * p + e]);
             }
             const uint32_t tile = sm + L::sp + (cg >> 1) * kBlock;
             planes::sts128(at16(tile, j, (cg & 1) * 4 + p), hi);
@@ -818,9 +864,9 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 tmem_wait_ld();
                 float vb[8], vc[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    vb[e] = dB[8 * p + e] + __uint_as_float(rb[e]);
-                    vc[e] = dC[8 * p + e] + __uint_as_float(rc[e]);
+                for (int e = 0; e < 4; ++e) {
+                    (dB[4 * p + e] + bfp::F2::of(rb[2 * e], rb[2 * e + 1])).get(vb[2 * e], vb[2 * e + 1]);
+                    (dC[4 * p + e] + bfp::F2::of(rc[2 * e], rc[2 * e + 1])).get(vc[2 * e], vc[2 * e + 1]);
                 }
                 if (j >= c.len) continue;
                 if (w.subsets > 1) {
