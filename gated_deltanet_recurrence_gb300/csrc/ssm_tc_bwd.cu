@@ -323,12 +323,13 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 }
 
 constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
+constexpr int kSums = 5 * 4 * kT + 2 * kGradWarps;  // numbers that the steps of a head leave for its dg
 enum GradBar { LB, LX0, LX1, LS, MM, kGradBars };
 template <int N>
 struct GradLay {
     static constexpr int nb = N / 64, image = N * 256;
     static constexpr int b = 0, c = b + nb * kBlock, x = c + nb * kBlock, y = x + 2 * kBlock, sp = y + 2 * kBlock, st = sp + 3 * kBlock,
-                         gates = st + image, sums = gates + 2 * kGates * 4, bars = sums + (5 * 4 * kT + 2 * kGradWarps) * 4,
+                         gates = st + image, sums = gates + 2 * kGates * 4, bars = sums + kSums * 4,
                          bytes = bars + kGradBars * 8 + 16;
 };
 
@@ -439,16 +440,18 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     for (int i = 0; i < 16; ++i) Es[i] = dB[i] = dC[i] = bfp::F2(0.f, 0.f);
     bfp::F2 ss2(0.f, 0.f), sd2(0.f, 0.f);
 
-    // dg, da and the sums of a head whose parts are all there: one warp, four tokens a lane
-    const auto finish_head = [&](int h) {
+    // dg, da and the sums of a head whose parts are all there, in `from`: one warp, four tokens a lane
+    const auto finish_head = [&](int h, const float* from) {
         const float* gt = gates_of(h);
+        const float *colS = from, *rowT = from + 4 * kT, *in1 = from + 8 * kT, *in2 = from + 12 * kT, *ddt = from + 16 * kT,
+                    *part = from + 20 * kT;
         const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         float z[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] = 4 * lane + e < c.len ? a.a[(long)(c.t0 + 4 * lane + e) * a.H + h] + bias : 0.f;
         const int u = lane >> 3;
         const auto four = [&](const float* from, float (&x)[4]) { load_row<4>(from + 4 * lane, x); };
-        float u1[4] = {}, u2[4] = {}, dd[4] = {}, dg[4] = {}, own[3][4] = {};
+        float u1[4] = {}, u2[4] = {}, dd[4] = {}, dg[4] = {}, cols[4] = {}, own[3][4] = {};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float x[5][4];
@@ -462,7 +465,8 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 u1[e] += x[0][e];
                 u2[e] += x[1][e];
                 dd[e] += x[2][e];
-                if (k <= u) dg[e] += x[3][e];
+                if (k == u) dg[e] += x[3][e];
+                if (k < u) cols[e] += x[3][e];
 #pragma unroll
                 for (int run = 0; run < 3; ++run)  // what a row in run `run` or before has in the runs behind it
                     if (run < k && u <= run) own[run][e] += x[4][e];
@@ -495,6 +499,14 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         }
         suf = __shfl_down_sync(0xffffffffu, suf, 1);
         if (lane == 31) suf = 0.f;
+        float run = (cols[0] + cols[1]) + (cols[2] + cols[3]);  // over the columns from t on of t's run
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+            const float down = __shfl_down_sync(0xffffffffu, run, d, 8);
+            if ((lane & 7) + d < 8) run += down;
+        }
+        run = __shfl_down_sync(0xffffffffu, run, 1, 8);
+        if ((lane & 7) == 7) run = 0.f;
         dot *= gt[kRows * kT + 4];
         float before = u == 0 ? pre[0] : (u == 1 ? pre[1] : (u == 2 ? pre[2] : 0.f));
 #pragma unroll
@@ -507,7 +519,8 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
 #pragma unroll
         for (int e = 3; e >= 0; --e) {
             suf += u1[e];
-            dg[e] += suf;
+            run += cols[e];
+            dg[e] += suf + run;
             const int t = 4 * lane + e;
             if (t >= c.len) continue;
             const float da = fmaf(-rate, dg[e], dd[e]) * sigmoidf_(z[e]);
@@ -551,8 +564,10 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         const float* gt = gates_of(h);
         // ---- dS into its planes
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (s == 0 && step > 0 && warp == 15) finish_head(h - 1);
-        if (step > 0) store_dx(step - 1);
+        // a finished head's parts wait in the former dy's place for a warp that has nothing to mask
+        float* parts = reinterpret_cast<float*>(smem + L::y + (place ^ 1) * kBlock);
+        if (s == 0 && step > 0)
+            for (int i = tid; i < kSums; i += kGradThreads) parts[i] = sums[i];
         ok = wait(LX0 + place, step >> 1) && wait(LS, seen++);
         if (ok && c.len < kT) {
             zero_rows(xt);
@@ -588,11 +603,9 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         convert(false);
         fence_async_smem();
         if ((failed = __syncthreads_or(!ok))) break;
-        if (s == slices - 1 && h + 1 < h1) ask_gates(h + 1);
         if (warp == 0) {
             if (on) {
                 load_image(image(w.states, step));
-                if (step + 1 < steps) load_xy(step + 1);
             }
             tc_fence_after();
             // X dS: [token, n], the smallest plane first; B dS^T: [token, p] of the three planes
@@ -605,7 +618,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
             commit(on, &bars[MM]);
         }
         ++images;
-        if (step + 1 < steps) ++tiles;
+        if (step > 0) store_dx(step - 1);
         ok = wait(MM, mm++);
         tc_fence_after();
         const float dt = gt[rDt * kT + j], r_end = gt[rToEnd * kT + j];
@@ -670,6 +683,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 const uint32_t zero[8] = {};
 #pragma unroll
                 for (int p = 0; p < 6; ++p) tmem_st8(tm + kPlane + lanes + 48 * u + 8 * p, zero);
+                if (s == 0 && step > 0 && warp == 3) finish_head(h - 1, parts);
             } else {
                 float f = gt[rToRun * kT + j];
                 for (int v = q + 1; v < u; ++v) f *= gt[kRows * kT + v];
@@ -721,10 +735,14 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                         tmem_st4(at + 8, mid);
                         tmem_st4(at + 16, lo);
 #pragma unroll
-                        for (int e = 7; e >= 0; --e) {  // sum over i >= t of row j < t
-                            const bool below = !kDiagonal || 8 * p + e > lane;
-                            acc += below ? t[e] : 0.f;
-                            t[e] = below ? acc : 0.f;
+                        for (int e = 7; e >= 0; --e) {
+                            if constexpr (kDiagonal) {  // sum over i >= t of row j < t
+                                const bool below = 8 * p + e > lane;
+                                acc += below ? t[e] : 0.f;
+                                t[e] = below ? acc : 0.f;
+                            } else {  // all rows lie before t: the sums over i >= t are taken of the columns' sums
+                                acc += t[e];
+                            }
                         }
                         const float col = sum_rows<8, 32>(t, lane);
                         if (lane < 8) {
@@ -740,10 +758,14 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
             *to = (s ? *to : 0.f) + acc;
             tmem_wait_st();
         }
+        fence_async_smem();  // the finished head's parts have been read: the next dy may come
         tc_fence_before();
         if ((failed = __syncthreads_or(!ok))) break;
         if (warp == 0) {
-            if (on && step + 1 < steps) load_image(image(w.dstates, step + 1));
+            if (on && step + 1 < steps) {
+                load_image(image(w.dstates, step + 1));
+                load_xy(step + 1);
+            }
             tc_fence_after();
             // M^T dy, and dy S0
 #pragma unroll
@@ -756,7 +778,11 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
                 for (int k = 0; k < 4; ++k) mma_ss(on, tm + kRes, dYk + 2 * k, dSk + p * (kBlock >> 4) + 2 * k, idN, p < 2 || k > 0);
             commit(on, &bars[MM]);
         }
-        if (step + 1 < steps) ++images;
+        if (step + 1 < steps) {
+            ++images;
+            ++tiles;
+            if (s == slices - 1) ask_gates(h + 1);
+        }
         ok = wait(MM, mm++);
         tc_fence_after();
         {
@@ -819,7 +845,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
         tc_fence_before();
         failed = __syncthreads_or(!ok);
     }
-    if (!failed && warp == 15) finish_head(h1 - 1);
+    if (!failed && warp == 3) finish_head(h1 - 1, sums);
     if (!failed) {
         store_dx(steps - 1);
         // dB += E^T C, dC += E B with the heads' sum of E in two planes (the outputs are bf16): rows j, columns i
