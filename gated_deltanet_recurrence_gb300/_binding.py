@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 
@@ -636,26 +637,26 @@ def gdn_decay_from_logits_bwd(a, A_log, dt_bias, b, dg, dbeta, da=None, dA_log=N
 def _rows(ref, name, t, shape, lead=1):
     """Pointer and stride of a token tensor that may be a slice of a wider one: `shape` (its first `lead` dimensions
     the tokens), each token's row contiguous, tokens one stride apart."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {tuple(shape)}")
     if t.get_device() != ref.get_device() or (not ref.is_cuda and t.device != ref.device):
         raise ValueError(f"{name} is on {t.device}, the call runs on {ref.device}")
-    width, strides = 1, t.stride()
+    tokens, width = math.prod(shape[:lead]), math.prod(shape[lead:])
+    stride = width if tokens > 1 else -(-width // 8) * 8  # one row has no stride
+    if t.is_contiguous():
+        return t.data_ptr(), stride
+    strides, width = t.stride(), 1
     for n, st in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         if n != 1 and st != width:
             raise ValueError(f"{name}: the rows of a token must be contiguous")
         width *= n
-    stride = strides[lead - 1]
-    if lead == 2:
-        if shape[1] == 1:
-            stride = strides[0]
-        elif shape[0] > 1 and strides[0] != shape[1] * stride:
-            raise ValueError(f"{name}: tokens must be one stride apart over all sequences")
-    tokens = 1
-    for n in shape[:lead]:
-        tokens *= n
-    if tokens <= 1:  # one row has no stride
-        stride = -(-width // 8) * 8
+    if tokens > 1:
+        stride = strides[lead - 1]
+        if lead == 2:
+            if shape[1] == 1:
+                stride = strides[0]
+            elif shape[0] > 1 and strides[0] != shape[1] * stride:
+                raise ValueError(f"{name}: tokens must be one stride apart over all sequences")
     return t.data_ptr(), stride
 
 
@@ -668,8 +669,9 @@ def _seqs(cu_seqlens, num_seqs):
 
 
 def _same_dtype(dt, **tensors):
+    dtype = _torch_dt(dt)
     for name, t in tensors.items():
-        if t is not None and _dt(t) != dt:
+        if t is not None and t.dtype is not dtype:
             raise TypeError(f"{name} must have the dtype of the inputs")
 
 
