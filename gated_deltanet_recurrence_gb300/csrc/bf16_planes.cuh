@@ -193,37 +193,8 @@ __device__ __forceinline__ void put2(Mat<COLS, P, LO, HS> m, int row, int col, f
     for (int p = 0; p < P; ++p) planes::sts32(at + p * LO, u[p]);
 }
 
-// Planes an input of type T takes.
-template <typename T>
-constexpr int kPlanes = 3;
-template <>
-constexpr int kPlanes<__nv_bfloat16> = 1;
-
-// Eight consecutive inputs of type T as they are loaded; zeros where `on` is false.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool on) {
-        u = on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(v[i] << 16);
-            x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-        }
-    }
-    template <int COLS, int LO, int HS>
-    __device__ __forceinline__ void put(Mat<COLS, 1, LO, HS> m, int row, int col) const {
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-        planes::sts128(m(row, col), v);
-    }
-};
-template <>
-struct Raw8<float> {
+// Eight consecutive inputs as they are loaded; zeros where `on` is false.
+struct Raw8 {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p, bool on) {
         a = b = make_float4(0.f, 0.f, 0.f, 0.f);

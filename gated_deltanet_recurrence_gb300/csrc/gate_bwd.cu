@@ -402,18 +402,18 @@ __global__ void __launch_bounds__(kThreads, VEC == 8 && NV == 1 ? 2 : 1) norm_bw
     }
 }
 
-// out[c] = sum over r of table[r][c] for both tables (the second may be absent): 32 columns and 32
+// The sums of both tables (the second may be absent): 32 columns and 32
 // interleaved row ranges per block, each range added in order, the ranges then in order.
 constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) column_sum_kernel(const float* table, long rows, long cols, float* out0,
-                                                                 float* out1) {
+__global__ void __launch_bounds__(kSumThreads) column_sum_kernel(ColumnSum sum0, ColumnSum sum1, long rows) {
     dependency_wait();
     __shared__ float part[32][33];
     const int x = threadIdx.x & 31, k = threadIdx.x >> 5;
     const long c = (long)blockIdx.x * 32 + x;
-    const float* t = table + (blockIdx.y ? rows * cols : 0);
-    float* out = blockIdx.y ? out1 : out0;
-    if (!out) return;
+    const float* t = blockIdx.y ? sum1.table : sum0.table;
+    float* out = blockIdx.y ? sum1.out : sum0.out;
+    const long cols = blockIdx.y ? sum1.cols : sum0.cols;
+    if (!out || (long)blockIdx.x * 32 >= cols) return;
     float s = 0.f;
     if (c < cols) {
         long r = k;
@@ -576,9 +576,14 @@ __global__ void __launch_bounds__(kThreads) gate_prep_bwd_kernel(GatePrepBwdArgs
 
 }  // namespace
 
+cudaError_t launch_column_sums(const ColumnSum& sum0, const ColumnSum& sum1, long rows, cudaStream_t s) {
+    const long cols = sum1.out && sum1.cols > sum0.cols ? sum1.cols : sum0.cols;
+    return launch_after(column_sum_kernel, dim3((unsigned)((cols + 31) / 32), sum1.out ? 2 : 1), kSumThreads, 0, s, sum0,
+                        sum1, rows);
+}
+
 cudaError_t launch_column_sum(const float* table, long rows, long cols, float* out0, float* out1, cudaStream_t s) {
-    return launch_after(column_sum_kernel, dim3((unsigned)((cols + 31) / 32), out1 ? 2 : 1), kSumThreads, 0, s, table,
-                        rows, cols, out0, out1);
+    return launch_column_sums(ColumnSum{table, cols, out0}, ColumnSum{table + rows * cols, cols, out1}, rows, s);
 }
 
 size_t norm_bwd_workspace_bytes(long rows, int groups, int size) {
@@ -611,8 +616,7 @@ cudaError_t launch_gate_prep_bwd(const GatePrepBwdArgs& a, cudaStream_t s) {
     kernel<<<p.blocks, kThreads, 0, s>>>(a, p.cols, p.stride, p.prows);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !sums) return e;
-    return launch_after(column_sum_kernel, dim3((unsigned)((a.H + 31) / 32), a.ddt ? 2 : 1), kSumThreads, 0, s,
-                        a.partial, p.prows, a.H, a.dA_log, a.ddt);
+    return launch_column_sum(a.partial, p.prows, a.H, a.dA_log, a.ddt, s);
 }
 
 }  // namespace gdn

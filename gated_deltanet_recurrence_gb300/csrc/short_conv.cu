@@ -489,11 +489,9 @@ cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = cudaSuccess;
-    if (a.dw) e = launch_column_sum(a.partial, rows, (long)a.dim * kTaps, a.dw, nullptr, s);
-    if (e == cudaSuccess && a.dbias)
-        e = launch_column_sum(a.partial + (long)rows * a.dim * kTaps, rows, a.dim, a.dbias, nullptr, s);
-    return e;
+    if (!a.dw && !a.dbias) return cudaSuccess;
+    const long cols = (long)a.dim * kTaps;
+    return launch_column_sums(ColumnSum{a.partial, cols, a.dw}, ColumnSum{a.partial + rows * cols, a.dim, a.dbias}, rows, s);
 }
 
 }  // namespace gdn

@@ -25,11 +25,10 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
 // 16 warps: warp w holds rows 16 (w % 4) .. and a quarter of the columns.
-template <typename T, int N>
+template <int N>
 struct Smem {
-    static constexpr int PX = bfp::kPlanes<T>;
-    static constexpr int k = 0, c = k + bfp::kTileBytes<kC, N, PX>, x = c + bfp::kTileBytes<kC, N, PX>,
-                         y = x + bfp::kTileBytes<kC, 64, PX>, s = y + bfp::kTileBytes<kC, 64, PX>,
+    static constexpr int k = 0, c = k + bfp::kTileBytes<kC, N, 3>, x = c + bfp::kTileBytes<kC, N, 3>,
+                         y = x + bfp::kTileBytes<kC, 64, 3>, s = y + bfp::kTileBytes<kC, 64, 3>,
                          m = s + bfp::kTileBytes<64, N, 3>, bytes = m + bfp::kTileBytes<kC, 64, 3>;
 };
 
@@ -39,15 +38,15 @@ __device__ __forceinline__ float quad_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
-    using L = Smem<T, N>;
-    constexpr int PX = L::PX, NT = N / 32;  // NT: 8-column tiles of a warp in a 64 x N result
+    using L = Smem<N>;
+    constexpr int NT = N / 32;  // NT: 8-column tiles of a warp in a 64 x N result
     constexpr int KV = kC * N / 8 / kThreads;  // vectors of a 64 x N tile a thread loads
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const bfp::Tile<kC, N, PX> Kt{base + L::k}, Ct{base + L::c};
-    const bfp::Tile<kC, 64, PX> Xt{base + L::x}, Yt{base + L::y};
+    const bfp::Tile<kC, N, 3> Kt{base + L::k}, Ct{base + L::c};
+    const bfp::Tile<kC, 64, 3> Xt{base + L::x}, Yt{base + L::y};
     const bfp::Tile<64, N, 3> St{base + L::s};
     const bfp::Tile<kC, 64, 3> Mt{base + L::m};
     __shared__ float gate[kGateRows][kC];
@@ -58,7 +57,9 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
     const int g = blockIdx.y % a.G, subset = blockIdx.y / a.G, per = a.H / a.G;
     const int lo = per * subset / w.subsets, hi = per * (subset + 1) / w.subsets;
     Chunk c;
-    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) {
+    const bool found = find_chunk(a.seqs, blockIdx.x, a.err, c);
+    dependency_wait();
+    if (!found) {
         const long all = (long)gridDim.x * a.H;
         for (int i = tid; i < hi - lo; i += kThreads) {
             const long at = (long)blockIdx.x * a.H + g * per + lo + i;
@@ -68,12 +69,12 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
     }
     const int m = (warp & 3) * 16, cw = warp >> 2, n0 = cw * (N / 4), p0 = cw * 16;
     {
-        const T* B = static_cast<const T*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
-        const T* C = static_cast<const T*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
+        const float* B = static_cast<const float*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
+        const float* C = static_cast<const float*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
 #pragma unroll
         for (int i = 0; i < KV; ++i) {
             const int v = i * kThreads + tid, r = v / (N / 8), col = v % (N / 8) * 8;
-            bfp::Raw8<T> k, q;
+            bfp::Raw8 k, q;
             k.load(B + (long)r * a.B_stride + col, r < c.len);
             q.load(C + (long)r * a.C_stride + col, r < c.len);
             k.put(Kt, r, col);
@@ -103,9 +104,9 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
             {
                 const int r = tid / 8, col = tid % 8 * 8;
                 const long ch = (long)h * a.P + s * 64 + col;
-                bfp::Raw8<T> x, y;
-                x.load(static_cast<const T*>(a.x) + (long)(c.t0 + r) * a.x_stride + ch, r < c.len);
-                y.load(static_cast<const T*>(a.dout) + (long)(c.t0 + r) * a.H * a.P + ch, r < c.len);
+                bfp::Raw8 x, y;
+                x.load(static_cast<const float*>(a.x) + (long)(c.t0 + r) * a.x_stride + ch, r < c.len);
+                y.load(static_cast<const float*>(a.dout) + (long)(c.t0 + r) * a.H * a.P + ch, r < c.len);
                 x.put(Xt, r, col);
                 y.put(Yt, r, col);
             }
@@ -158,18 +159,14 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
                     q2[hh] = fmaf(acc[j][2 * hh], x.x, fmaf(acc[j][2 * hh + 1], x.y, q2[hh]));
                 });
                 bfp::product<kC, true, true, bfp::kUpper>(acc, Mt, m, Yt, p0, lane);
-                T* dx = static_cast<T*>(a.dx) + ((long)c.t0 * a.H + h) * a.P + s * 64;
+                float* dx = static_cast<float*>(a.dx) + ((long)c.t0 * a.H + h) * a.P + s * 64;
                 bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int p) {
                     const float2 x = bfp::get2(Xt, i, p), y = bfp::get2(Yt, i, p);
                     const float v0 = acc[j][2 * hh], v1 = acc[j][2 * hh + 1];
                     qd[hh] = fmaf(v0, x.x, fmaf(v1, x.y, qd[hh]));
                     sd = fmaf(y.x, x.x, fmaf(y.y, x.y, sd));
                     const float o0 = fmaf(gate[0][i], v0, D * y.x), o1 = fmaf(gate[0][i], v1, D * y.y);
-                    if (i < c.len) {
-                        T* o = dx + (long)i * a.H * a.P + p;
-                        if constexpr (PX == 1) *reinterpret_cast<uint32_t*>(o) = pack_bf16(o0, o1);
-                        else *reinterpret_cast<float2*>(o) = make_float2(o0, o1);
-                    }
+                    if (i < c.len) *reinterpret_cast<float2*>(dx + (long)i * a.H * a.P + p) = make_float2(o0, o1);
                 });
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
@@ -318,34 +315,53 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
             const long all = (long)a.seqs.total_T * a.G * N;
             *reinterpret_cast<float2*>(w.parts + subset * all + at) = vb;
             *reinterpret_cast<float2*>(w.parts + (w.subsets + subset) * all + at) = vc;
-        } else if constexpr (PX == 1) {
-            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.dB) + at) = pack_bf16(vb.x, vb.y);
-            *reinterpret_cast<uint32_t*>(static_cast<T*>(a.dC) + at) = pack_bf16(vc.x, vc.y);
         } else {
-            *reinterpret_cast<float2*>(static_cast<T*>(a.dB) + at) = vb;
-            *reinterpret_cast<float2*>(static_cast<T*>(a.dC) + at) = vc;
+            *reinterpret_cast<float2*>(static_cast<float*>(a.dB) + at) = vb;
+            *reinterpret_cast<float2*>(static_cast<float*>(a.dC) + at) = vc;
         }
     });
 }
 
-// What is left: the subsets' dB and dC added up in order, zeros for tokens outside every sequence where they are
-// asked for.  One thread: eight elements of dB or dC (y = 0, 1), or of dx and da (y = 2).
+// What is left, in one launch of three kinds of blocks: the sums over the slots of dA_log, ddt_bias and dD, 32 heads a
+// block; the subsets' dB and dC added up in order, eight elements a thread; zeros for the tokens outside every sequence.
+constexpr int kZeroBlocks = 152;
 template <typename T>
-__global__ void __launch_bounds__(256) ssm_finish_kernel(SsmArgs a, Work w, long elems) {
+__global__ void __launch_bounds__(256) ssm_finish_kernel(SsmArgs a, Work w, long slots, int sum_blocks, int part_blocks) {
+    dependency_wait();
+    const int per = (a.H + 31) / 32;
+    if ((int)blockIdx.x < sum_blocks) {
+        __shared__ Two part[8][32];
+        const int which = blockIdx.x / per, lane = threadIdx.x & 31, h = blockIdx.x % per * 32 + lane, k = threadIdx.x >> 5;
+        float* out = which == 0 ? a.dA_log : (which == 1 ? a.ddt_bias : a.dD);
+        if (!out) return;
+        const float* t = w.sums + (long)which * slots * a.H;
+        Two sum{0.f, 0.f};
+        if (h < a.H) {
+            long r = k;
+            for (; r + 24 < slots; r += 32) {
+                const float x[4] = {t[r * a.H + h], t[(r + 8) * a.H + h], t[(r + 16) * a.H + h], t[(r + 24) * a.H + h]};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) two_add(sum, x[i]);
+            }
+            for (; r < slots; r += 8) two_add(sum, t[r * a.H + h]);
+        }
+        part[k][lane] = sum;
+        __syncthreads();
+        if (k == 0 && h < a.H) {
+            for (int i = 1; i < 8; ++i) sum = two_add(sum, part[i][lane]);
+            out[h] = sum.h + sum.l;
+        }
+        return;
+    }
     if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
     const long first = a.seqs.cu ? a.seqs.bos(0) : 0, end = a.seqs.cu ? a.seqs.bos(a.seqs.num_seqs) : a.seqs.total_T;
-    const long at = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
-    const float zero[8] = {};
-    if (blockIdx.y < 2) {
-        if (at >= elems) return;
-        T* out = static_cast<T*>(blockIdx.y ? a.dC : a.dB) + at;
-        const long t = at / ((long)a.G * a.N);
-        if (t < first || t >= end) {
-            if (a.zero_outside) store_row<8>(out, zero);
-            return;
-        }
-        if (w.subsets == 1) return;
-        const float* p = w.parts + (blockIdx.y ? w.subsets * elems : 0) + at;
+    const int b = blockIdx.x - sum_blocks;
+    const long elems = (long)a.seqs.total_T * a.G * a.N;
+    if (b < part_blocks) {
+        const bool second = 2 * b >= part_blocks;
+        const long at = ((long)(b - (second ? part_blocks / 2 : 0)) * 256 + threadIdx.x) * 8, t = at / ((long)a.G * a.N);
+        if (at >= elems || t < first || t >= end) return;
+        const float* p = w.parts + (second ? w.subsets * elems : 0) + at;
         float x[8] = {};
         for (int s = 0; s < w.subsets; ++s) {
             float y[8];
@@ -353,31 +369,34 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(SsmArgs a, Work w, long
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += y[e];
         }
-        store_row<8>(out, x);
+        store_row<8>(static_cast<T*>(second ? a.dC : a.dB) + at, x);
         return;
     }
-    if (!a.zero_outside) return;
-    // dx, da: few rows as a rule, walked by all threads
-    const long rows = first + (a.seqs.total_T - end), width = (long)a.H * a.P / 8;
-    const long stride = (long)gridDim.x * 256, q0 = (long)blockIdx.x * 256 + threadIdx.x;
-    for (long q = q0; q < rows * width; q += stride) {
-        const long r = q / width, t = r < first ? r : end + (r - first);
-        store_row<8>(static_cast<T*>(a.dx) + (t * width + q % width) * 8, zero);
-    }
+    // few rows as a rule, walked by all threads
+    const float zero[8] = {};
+    const long rows = first + (a.seqs.total_T - end), stride = (long)kZeroBlocks * 256;
+    const long q0 = (long)(b - part_blocks) * 256 + threadIdx.x;
+    const auto clear = [&](void* out, long width) {
+        for (long q = q0; q < rows * width; q += stride) {
+            const long r = q / width, t = r < first ? r : end + (r - first);
+            store_row<8>(static_cast<T*>(out) + (t * width + q % width) * 8, zero);
+        }
+    };
+    clear(a.dx, (long)a.H * a.P / 8);
+    clear(a.dB, (long)a.G * a.N / 8);
+    clear(a.dC, (long)a.G * a.N / 8);
     for (long q = q0; q < rows * a.H; q += stride) {
         const long r = q / a.H, t = r < first ? r : end + (r - first);
         a.da[t * a.H + q % a.H] = 0.f;
     }
 }
 
-template <typename T, int N>
+template <int N>
 cudaError_t grad_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
-    const auto kernel = ssm_grad_kernel<T, N>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<T, N>::bytes);
+    const cudaError_t e = cudaFuncSetAttribute(ssm_grad_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<N>::bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)(a.G * w.subsets));
-    kernel<<<grid, kThreads, Smem<T, N>::bytes, s>>>(a, w);
-    return cudaGetLastError();
+    return launch_after(ssm_grad_kernel<N>, grid, kThreads, Smem<N>::bytes, s, a, w);
 }
 
 // Subsets of a group's heads: as many blocks as the SMs take in a few rounds, at least two heads a block where the
@@ -412,20 +431,13 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, un
 }  // namespace
 
 cudaError_t launch_finish(const SsmArgs& a, const Work& w, long slots, cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
-    const bool zeros = a.zero_outside && a.seqs.cu;
-    if (a.seqs.total_T > 0 && (w.subsets > 1 || zeros)) {
-        const long elems = (long)a.seqs.total_T * a.G * a.N;
-        const dim3 grid((unsigned)((elems / 8 + 255) / 256), zeros ? 3 : 2);
-        if (a.dtype == GDN_BF16) ssm_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, w, elems);
-        else ssm_finish_kernel<float><<<grid, 256, 0, s>>>(a, w, elems);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    const long all = slots * a.H;
-    if (a.dA_log || a.ddt_bias) e = launch_column_sum(w.sums, slots, a.H, a.dA_log, a.ddt_bias, s);
-    if (e == cudaSuccess && a.dD) e = launch_column_sum(w.sums + 2 * all, slots, a.H, a.dD, nullptr, s);
-    return e;
+    const int sums = a.dA_log || a.ddt_bias || a.dD ? 3 * ((a.H + 31) / 32) : 0;
+    const int parts = w.subsets > 1 ? 2 * (int)(((long)a.seqs.total_T * a.G * a.N / 8 + 255) / 256) : 0;
+    const int zeros = a.zero_outside && a.seqs.cu && a.seqs.total_T > 0 ? kZeroBlocks : 0;
+    if (sums + parts + zeros == 0) return cudaSuccess;
+    const dim3 grid((unsigned)(sums + parts + zeros));
+    return a.dtype == GDN_BF16 ? launch_after(ssm_finish_kernel<__nv_bfloat16>, grid, 256, 0, s, a, w, slots, sums, parts)
+                               : launch_after(ssm_finish_kernel<float>, grid, 256, 0, s, a, w, slots, sums, parts);
 }
 
 }  // namespace ssm
@@ -443,7 +455,7 @@ cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
     if (e != cudaSuccess) return e;
     const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
-    e = a.N == 128 ? ssm::grad_one<float, 128>(a, w, s) : ssm::grad_one<float, 64>(a, w, s);
+    e = a.N == 128 ? ssm::grad_one<128>(a, w, s) : ssm::grad_one<64>(a, w, s);
     if (e != cudaSuccess) return e;
     return ssm::launch_finish(a, w, slots, s);
 }

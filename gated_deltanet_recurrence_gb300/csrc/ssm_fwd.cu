@@ -16,6 +16,7 @@ namespace {
 // One warp per (slot, head): lane l holds tokens 2 l and 2 l + 1.
 constexpr int kGateWarps = 8;
 __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, float* gates) {
+    dependency_start();
     Chunk c;
     if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) return;
     const int lane = threadIdx.x & 31;
@@ -57,24 +58,28 @@ __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, f
 // Block: 8 warps; warp w holds rows 16 (w % 4) .. of the 64 and half of the N columns.  Blocks with blockIdx.y = 1: the
 // states' gradients, from the last chunk to the first.
 constexpr int kScanThreads = 256;
-template <typename T, int N>
+template <int N>
 __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work w) {
-    constexpr int PX = bfp::kPlanes<T>, NT = N / 16, KV = N / 32;  // KV: vectors of B a thread loads
+    constexpr int NT = N / 16, KV = N / 32;  // KV: vectors of B a thread loads
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const bfp::Tile<kC, N, PX> Kt{base};
-    const bfp::Tile<kC, 64, 3> Vt{base + bfp::kTileBytes<kC, N, PX>};
+    const bfp::Tile<kC, N, 3> Kt{base};
+    const bfp::Tile<kC, 64, 3> Vt{base + bfp::kTileBytes<kC, N, 3>};
     __shared__ float fac[kC];
     const bool REV = blockIdx.y;
-    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    dependency_start();
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) {
+        dependency_wait();
+        return;
+    }
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
     const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kC - 1) / kC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m0 = (warp & 3) * 16, n0 = (warp >> 2) * (N / 2);
     const int g = h / (a.H / a.G);
-    const T* K = static_cast<const T*>(REV ? a.C : a.B) + (long)g * N;
+    const float* K = static_cast<const float*>(REV ? a.C : a.B) + (long)g * N;
     const long k_stride = REV ? a.C_stride : a.B_stride;
-    const T* X = static_cast<const T*>(REV ? a.dout : a.x) + (long)h * a.P + s * 64;
+    const float* X = static_cast<const float*>(REV ? a.dout : a.x) + (long)h * a.P + s * 64;
     const long x_stride = REV ? (long)a.H * a.P : a.x_stride;
     const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
     const float* init = REV ? a.dfinal_state : a.initial_state;
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
         S[j][2 * hh] = v.x;
         S[j][2 * hh + 1] = v.y;
     });
-    bfp::Raw8<T> kr[KV], xr[2];
+    bfp::Raw8 kr[KV], xr[2];
     float gd = 0.f, gb = 0.f, gl = 0.f;  // this thread's token: dt, the chunk factor; the whole chunk's decay
     const auto fetch = [&](int k) {
         const int t0 = bos + k * kC, len = min(eos - t0, kC);
@@ -108,6 +113,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
         }
         gl = gt[3 * kC + kC - 1];
     };
+    dependency_wait();
     if (chunks > 0) fetch(REV ? chunks - 1 : 0);
     for (int q = 0; q < chunks; ++q) {
         const int k = REV ? chunks - 1 - q : q;
@@ -145,46 +151,44 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
         });
 }
 
-template <typename T, int N>
+template <int N>
 cudaError_t scan_one(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
-    constexpr int smem = bfp::kTileBytes<kC, N, bfp::kPlanes<T>> + bfp::kTileBytes<kC, 64, 3>;
-    const auto kernel = ssm_scan_kernel<T, N>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3>;
+    const cudaError_t e = cudaFuncSetAttribute(ssm_scan_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), both ? 2 : 1), kScanThreads, smem, s>>>(a, w);
-    return cudaGetLastError();
+    return launch_after(ssm_scan_kernel<N>, dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), both ? 2 : 1), kScanThreads, smem, s, a, w);
 }
 
 // ---- outputs -------------------------------------------------------------------------------------
 
-// Block: 4 warps of 16 tokens each.  PS: planes of the state and of the masked products (the output's accuracy).
+// Block: 4 warps of 16 tokens each.
 constexpr int kOutThreads = 128;
-template <typename T, int N>
-constexpr int kOutSmem = 2 * bfp::kTileBytes<kC, N, bfp::kPlanes<T>> + bfp::kTileBytes<kC, 64, bfp::kPlanes<T>> +
-                         bfp::kTileBytes<64, N, (bfp::kPlanes<T> == 1 ? 2 : 3)>;
-template <typename T, int N>
+template <int N>
+constexpr int kOutSmem = 2 * bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3> + bfp::kTileBytes<64, N, 3>;
+template <int N>
 __global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w) {
-    constexpr int PX = bfp::kPlanes<T>, PS = PX == 1 ? 2 : 3;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const bfp::Tile<kC, N, PX> Kt{base}, Ct{base + bfp::kTileBytes<kC, N, PX>};
-    const bfp::Tile<kC, 64, PX> Xt{base + 2 * bfp::kTileBytes<kC, N, PX>};
-    const bfp::Tile<64, N, PS> St{base + 2 * bfp::kTileBytes<kC, N, PX> + bfp::kTileBytes<kC, 64, PX>};
+    const bfp::Tile<kC, N, 3> Kt{base}, Ct{base + bfp::kTileBytes<kC, N, 3>};
+    const bfp::Tile<kC, 64, 3> Xt{base + 2 * bfp::kTileBytes<kC, N, 3>};
+    const bfp::Tile<64, N, 3> St{base + 2 * bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3>};
     __shared__ float gate[kGateRows][kC];
     Chunk c;
-    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) return;
+    if (!find_chunk(a.seqs, blockIdx.x, a.err, c)) {
+        dependency_wait();
+        return;
+    }
     const int slices = a.P / 64, s = blockIdx.y % slices, h = blockIdx.y / slices, g = h / (a.H / a.G);
     const int tid = threadIdx.x, lane = tid & 31, m = (tid >> 5) * 16;
-    const T* X = static_cast<const T*>(a.x) + (long)c.t0 * a.x_stride + (long)h * a.P + s * 64;
-    const T* B = static_cast<const T*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
-    const T* C = static_cast<const T*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
+    const float* X = static_cast<const float*>(a.x) + (long)c.t0 * a.x_stride + (long)h * a.P + s * 64;
+    const float* B = static_cast<const float*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
+    const float* C = static_cast<const float*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
     const float* S0 = w.states + (((long)blockIdx.x * a.H + h) * a.P + s * 64) * N;
     const float* gt = w.gates + ((long)blockIdx.x * a.H + h) * (kGateRows * kC);
-    for (int i = tid; i < kGateRows * kC; i += kOutThreads) (&gate[0][0])[i] = gt[i];
 #pragma unroll 4
     for (int v = tid; v < kC * N / 8; v += kOutThreads) {
         const int r = v / (N / 8), col = v % (N / 8) * 8;
-        bfp::Raw8<T> k, q;
+        bfp::Raw8 k, q;
         k.load(B + (long)r * a.B_stride + col, r < c.len);
         q.load(C + (long)r * a.C_stride + col, r < c.len);
         k.put(Kt, r, col);
@@ -192,10 +196,12 @@ __global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w)
     }
 #pragma unroll 4
     for (int v = tid; v < kC * 8; v += kOutThreads) {
-        bfp::Raw8<T> x;
+        bfp::Raw8 x;
         x.load(X + (long)(v / 8) * a.x_stride + v % 8 * 8, v / 8 < c.len);
         x.put(Xt, v / 8, v % 8 * 8);
     }
+    dependency_wait();  // gates and states
+    for (int i = tid; i < kGateRows * kC; i += kOutThreads) (&gate[0][0])[i] = gt[i];
 #pragma unroll 4
     for (int v = tid; v < 64 * N / 8; v += kOutThreads) {
         const int r = v / (N / 8), col = v % (N / 8) * 8;
@@ -224,46 +230,40 @@ __global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if (16 * k > m) continue;
-        uint32_t f[PS][4];
+        uint32_t f[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            uint32_t u[PS];
-            bfp::split<PS>(M[2 * k + (e >> 1)][2 * (e & 1)], M[2 * k + (e >> 1)][2 * (e & 1) + 1], u);
+            uint32_t u[3];
+            bfp::split<3>(M[2 * k + (e >> 1)][2 * (e & 1)], M[2 * k + (e >> 1)][2 * (e & 1) + 1], u);
 #pragma unroll
-            for (int p = 0; p < PS; ++p) f[p][e] = u[p];
+            for (int p = 0; p < 3; ++p) f[p][e] = u[p];
         }
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            uint32_t b[PX][4];
+            uint32_t b[3][4];
             bfp::load_b<true, 0, kC * 128>(b[0], lb, 8 * j, 16 * k);
-            if constexpr (PX > 1) {
-                bfp::load_b<true, kC * 128, kC * 128>(b[1], lb, 8 * j, 16 * k);
-                bfp::load_b<true, 2 * kC * 128, kC * 128>(b[2], lb, 8 * j, 16 * k);
-            }
-            bfp::terms<PS, PX>(Y[j], f, b, 0);
-            bfp::terms<PS, PX>(Y[j + 1], f, b, 1);
+            bfp::load_b<true, kC * 128, kC * 128>(b[1], lb, 8 * j, 16 * k);
+            bfp::load_b<true, 2 * kC * 128, kC * 128>(b[2], lb, 8 * j, 16 * k);
+            bfp::terms<3, 3>(Y[j], f, b, 0);
+            bfp::terms<3, 3>(Y[j + 1], f, b, 1);
         }
     }
     const float D = a.D ? a.D[h] : 0.f;
-    T* out = static_cast<T*>(a.out) + ((long)c.t0 * a.H + h) * a.P + s * 64;
+    float* out = static_cast<float*>(a.out) + ((long)c.t0 * a.H + h) * a.P + s * 64;
     bfp::pairs<8>(m, 0, lane, [&](int j, int hh, int i, int col) {
         if (i >= c.len) return;
         const float2 x = bfp::get2(Xt, i, col);
         const float y0 = fmaf(D, x.x, Y[j][2 * hh]), y1 = fmaf(D, x.y, Y[j][2 * hh + 1]);
-        T* o = out + (long)i * a.H * a.P + col;
-        if constexpr (PX == 1) *reinterpret_cast<uint32_t*>(o) = pack_bf16(y0, y1);
-        else *reinterpret_cast<float2*>(o) = make_float2(y0, y1);
+        *reinterpret_cast<float2*>(out + (long)i * a.H * a.P + col) = make_float2(y0, y1);
     });
 }
 
-template <typename T, int N>
+template <int N>
 cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
-    const auto kernel = ssm_out_kernel<T, N>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem<T, N>);
+    const cudaError_t e = cudaFuncSetAttribute(ssm_out_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem<N>);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)(a.H * (a.P / 64)));
-    kernel<<<grid, kOutThreads, kOutSmem<T, N>, s>>>(a, w);
-    return cudaGetLastError();
+    return launch_after(ssm_out_kernel<N>, grid, kOutThreads, kOutSmem<N>, s, a, w);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -277,7 +277,7 @@ cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
 }
 
 cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
-    return a.N == 128 ? scan_one<float, 128>(a, w, both, s) : scan_one<float, 64>(a, w, both, s);
+    return a.N == 128 ? scan_one<128>(a, w, both, s) : scan_one<64>(a, w, both, s);
 }
 
 }  // namespace ssm
@@ -297,7 +297,7 @@ cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
     cudaError_t e = ssm::launch_gates(a, w, s);
     if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
     if (e != cudaSuccess || a.seqs.total_T == 0) return e;
-    return a.N == 128 ? ssm::out_one<float, 128>(a, w, s) : ssm::out_one<float, 64>(a, w, s);
+    return a.N == 128 ? ssm::out_one<128>(a, w, s) : ssm::out_one<64>(a, w, s);
 }
 
 }  // namespace gdn

@@ -221,8 +221,9 @@ cudaError_t allow_smem(K kernel, int smem) {
 // Device error word of the current device, or null (abi.cu).
 int* device_error_word();
 
-// out0[c] (out1[c]) = sum over rows of table[r][c] (of the second table behind it), in a fixed order; a kernel that
-// begins behind the one before it on the stream.
+// The column sums of two tables of as many rows, in a fixed order, by a kernel that begins behind the one before it on
+// the stream; and those of a table and of the one that lies behind it.
+cudaError_t launch_column_sums(const ColumnSum& sum0, const ColumnSum& sum1, long rows, cudaStream_t s);
 cudaError_t launch_column_sum(const float* table, long rows, long cols, float* out0, float* out1, cudaStream_t s);
 
 struct ShortConvArgs {

@@ -53,6 +53,7 @@ __device__ __forceinline__ bool find_chunk128(const Packed& s, int slot, int* er
 
 constexpr int kGateWarps = 8;
 __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates128_kernel(SsmArgs a, float* gates) {
+    dependency_start();
     Chunk c;
     if (!find_chunk128(a.seqs, blockIdx.x, a.err, c)) return;
     const int lane = threadIdx.x & 31, h = blockIdx.y * kGateWarps + (threadIdx.x >> 5);
@@ -107,7 +108,10 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kScanBars * 8 + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const bool back = blockIdx.y;
-    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
+    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) {
+        dependency_wait();
+        return;
+    }
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
     const int bos = __shfl_sync(0xffffffffu, a.seqs.bos(n), 0), eos = __shfl_sync(0xffffffffu, a.seqs.bos(n + 1), 0);
     const int chunks = (eos - bos + kT - 1) / kT;
@@ -129,6 +133,7 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    dependency_wait();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
     const uint32_t tU = tm, tS = tm + 192;  // U: the three planes' sums
     const auto wait = [&](int bar, int index) -> bool {
@@ -361,6 +366,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
             const long at = (long)blockIdx.x * a.H + h0 + i;
             w.sums[at] = w.sums[all + at] = w.sums[2 * all + at] = 0.f;
         }
+        dependency_wait();
         return;
     }
     if (tid == 0) {
@@ -375,6 +381,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    dependency_wait();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0), lanes = (uint32_t)(q * 32) << 16, on = elect();
     const auto wait = [&](int bar, int index) -> bool {
         bool there = mbar_try_wait(&bars[bar], index & 1, 100000u);
@@ -965,18 +972,17 @@ cudaError_t launch(const SsmArgs& a, const TcWork& w, cudaStream_t s) {
         !map_rows(&mB, a.B, T, (long)a.G * N, a.B_stride) || !map_rows(&mC, a.C, T, (long)a.G * N, a.C_stride))
         return cudaErrorInvalidValue;
     const unsigned slots = (unsigned)slots128(a.seqs.num_seqs, a.seqs.total_T);
-    ssm_gates128_kernel<<<dim3(slots, (unsigned)((a.H + kGateWarps - 1) / kGateWarps)), kGateWarps * 32, 0, s>>>(a, w.gates);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(ssm_scan_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanLay<N>::bytes);
+    cudaError_t e = cudaFuncSetAttribute(ssm_scan_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanLay<N>::bytes);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(ssm_grad_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradLay<N>::bytes);
     if (e != cudaSuccess) return e;
-    ssm_scan_tc_kernel<N><<<dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), 2), kScanThreads, ScanLay<N>::bytes, s>>>(mX, mY, mB, mC, a, w);
+    ssm_gates128_kernel<<<dim3(slots, (unsigned)((a.H + kGateWarps - 1) / kGateWarps)), kGateWarps * 32, 0, s>>>(a, w.gates);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    ssm_grad_tc_kernel<N><<<dim3(slots, (unsigned)(a.G * w.subsets)), kGradThreads, GradLay<N>::bytes, s>>>(mX, mY, mB, mC, a, w);
-    return cudaGetLastError();
+    const dim3 scan((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), 2), grad(slots, (unsigned)(a.G * w.subsets));
+    e = launch_after(ssm_scan_tc_kernel<N>, scan, kScanThreads, ScanLay<N>::bytes, s, mX, mY, mB, mC, a, w);
+    if (e != cudaSuccess) return e;
+    return launch_after(ssm_grad_tc_kernel<N>, grad, kGradThreads, GradLay<N>::bytes, s, mX, mY, mB, mC, a, w);
 }
 
 }  // namespace

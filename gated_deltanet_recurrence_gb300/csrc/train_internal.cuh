@@ -31,8 +31,15 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t
     return launch_config(cfg, kernel, args...);
 }
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel behind this one start, up to its dependency_wait(), once every block has come here.
+__device__ __forceinline__ void dependency_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- launchers (called from abi.cu after argument checks) -----------------------------------
+
+// out[c] = the sum over the rows of table[r][c], where out is given.
+struct ColumnSum {
+    const float* table; long cols; float* out;
+};
 
 // Gradients of the output norms: RMS norm (rms = 1, groups = 1, bias null) and group norm.
 struct NormArgs {

@@ -84,7 +84,8 @@ def test_refusals(name, status, kw):
 
 def test_workspace_sizes():
     L = gdn.lib()
-    assert L.gdn_ssm_chunk_fwd_workspace_size(1, 64, 2, 1, 64, 64, 1) > 0
+    assert L.gdn_ssm_chunk_fwd_workspace_size(1, 64, 2, 1, 64, 64, 0) > 0
+    assert L.gdn_ssm_chunk_fwd_workspace_size(1, 64, 2, 1, 64, 64, 1) == 0  # one kernel, nothing between kernels
     for bad in ((0, 64, 2, 1, 64, 64, 1), (1, -1, 2, 1, 64, 64, 1), (1, 64, 3, 2, 64, 64, 1), (1, 64, 2, 1, 32, 64, 1),
                 (1, 64, 2, 1, 64, 64, 5)):
         assert L.gdn_ssm_chunk_fwd_workspace_size(*bad) == 0
