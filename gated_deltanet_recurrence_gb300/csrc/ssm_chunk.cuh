@@ -65,6 +65,7 @@ struct Work {
 cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s);
 cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s);
 // The whole forward pass of bf16 prompts (ssm_tc.cu), for total_T > 0.
+size_t tc_workspace_bytes(int num_seqs, int total_T, int H, int P, int N);
 cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s);
 // The gradients of bf16 prompts (ssm_tc_bwd.cu), for total_T > 0, and what every backward pass ends with: dB and dC added
 // up, zeros outside the sequences, sums over the slots.

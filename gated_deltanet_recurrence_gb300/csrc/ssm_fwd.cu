@@ -283,7 +283,7 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t
 }  // namespace ssm
 
 size_t ssm_fwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
-    if (dtype == GDN_BF16) return 0;
+    if (dtype == GDN_BF16) return total_T > 0 ? ssm::tc_workspace_bytes(num_seqs, total_T, H, P, N) : 0;
     const size_t slots = (size_t)ssm::slots_of(num_seqs, total_T);
     return ssm::align256(slots * H * ssm::kGateRows * ssm::kC * sizeof(float)) + slots * H * P * N * sizeof(float);
 }

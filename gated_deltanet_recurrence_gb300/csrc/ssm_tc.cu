@@ -51,7 +51,7 @@ enum Gate { kPh, kPl, kPd, kQ, kW, kB };
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
 ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mC,
-              SsmArgs a) {
+              SsmArgs a, Segments w) {
     using L = Lay<N>;
     constexpr int NB = L::nb;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -60,12 +60,19 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     uint32_t* tbase = reinterpret_cast<uint32_t*>(smem + L::bars + kBars * 8);
     volatile int* dead = reinterpret_cast<volatile int*>(smem + L::bars + kBars * 8 + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
-    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
-    const int bos = __shfl_sync(0xffffffffu, a.seqs.bos(n), 0), eos = __shfl_sync(0xffffffffu, a.seqs.bos(n + 1), 0);
+    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, index = blockIdx.x / slices / a.H;
+    Run run;
+    if (!find_run(a.seqs, w.each, index, a.err, run)) {
+        dependency_wait();
+        return;
+    }
+    const int bos = __shfl_sync(0xffffffffu, run.t0, 0), eos = __shfl_sync(0xffffffffu, run.end, 0);
     const int chunks = (eos - bos + kT - 1) / kT;
     const int g = h / (a.H / a.G);
-    const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
+    const long row0 = (((long)run.n * a.H + h) * a.P + s * 64) * N;
+    const float* init = a.initial_state ? a.initial_state + row0 : nullptr;
+    if (w.each) init = w.start[0] + (((long)index * a.H + h) * a.P + s * 64) * N;
+    float* last = run.last && a.final_state ? a.final_state + row0 : nullptr;
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
@@ -82,6 +89,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    dependency_wait();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tbase, 0);
     const uint32_t tU = tm, tS = tm + 128, tCS = tm + 192, tMX = tm + 320, tCB = tm + 384;
 
@@ -233,8 +241,8 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
                 if (c == 0) {
 #pragma unroll
                     for (int p = 0; p < 8; p += 2) {
-                        const float* from = a.initial_state + row0 + (long)(col + p) * N + r;
-                        S[p / 2] = holds && a.initial_state ? bfp::F2(from[0], from[N]) : bfp::F2(0.f, 0.f);
+                        const float* from = init + (long)(col + p) * N + r;
+                        S[p / 2] = holds && init ? bfp::F2(from[0], from[N]) : bfp::F2(0.f, 0.f);
                     }
                 } else {
                     uint32_t old[8], hi[8], mid[8];
@@ -251,9 +259,9 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
 #pragma unroll
                 for (int p = 0; p < 4; ++p) S[p].get(v[2 * p], v[2 * p + 1]);
                 if (c == chunks) {
-                    if (holds && a.final_state) {
+                    if (holds && last) {
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) a.final_state[row0 + (long)(col + p) * N + r] = v[p];
+                        for (int p = 0; p < 8; ++p) last[(long)(col + p) * N + r] = v[p];
                     }
                     continue;
                 }
@@ -458,22 +466,42 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
 }
 
 template <int N>
-cudaError_t launch(const SsmArgs& a, cudaStream_t s) {
+cudaError_t launch(const SsmArgs& a, const Segments& w, cudaStream_t s) {
     CUtensorMap mX, mB, mC;
     const long T = a.seqs.total_T;
     if (!encoder() || !map_rows(&mX, a.x, T, (long)a.H * a.P, a.x_stride) || !map_rows(&mB, a.B, T, (long)a.G * N, a.B_stride) ||
         !map_rows(&mC, a.C, T, (long)a.G * N, a.C_stride))
         return cudaErrorInvalidValue;
-    const auto kernel = ssm_tc_kernel<N>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::bytes);
+    const cudaError_t e = cudaFuncSetAttribute(ssm_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), kThreads, Lay<N>::bytes, s>>>(mX, mB, mC, a);
+    const long runs = w.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w.each) : a.seqs.num_seqs;
+    const dim3 grid((unsigned)(runs * a.H * (a.P / 64)));
+    if (w.each) return launch_after(ssm_tc_kernel<N>, grid, kThreads, Lay<N>::bytes, s, mX, mB, mC, a, w);
+    ssm_tc_kernel<N><<<grid, kThreads, Lay<N>::bytes, s>>>(mX, mB, mC, a, w);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s) { return a.N == 128 ? launch<128>(a, s) : launch<64>(a, s); }
+size_t tc_workspace_bytes(int num_seqs, int total_T, int H, int P, int N) {
+    size_t most = 0;
+    for (int varied = 0; varied < 2; ++varied) {
+        const size_t segments = segments_layout(num_seqs, total_T, H, P, N, 1, varied, nullptr, nullptr);
+        if (segments > most) most = segments;
+    }
+    return most;
+}
+
+cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s) {
+    Segments w{};
+    const Packed& q = a.seqs;
+    segments_layout(q.num_seqs, q.total_T, a.H, a.P, a.N, 1, q.cu && q.num_seqs > 1, &w, static_cast<unsigned char*>(a.workspace));
+    if (w.each) {
+        const cudaError_t e = launch_starts(a, nullptr, w, 1, s);
+        if (e != cudaSuccess) return e;
+    }
+    return a.N == 128 ? launch<128>(a, w, s) : launch<64>(a, w, s);
+}
 
 }  // namespace ssm
 }  // namespace gdn

@@ -207,6 +207,38 @@ def test_scan(lengths, tail, H, G, P, N, dtype, carried, extra):
     assert torch.equal(again, got) and torch.equal(last2, last)
 
 
+SEGMENT_CASES = [  # long sequences of few heads, which are walked along in segments
+    ([1700], 0, 1, 1, 64, 64, BF, True, True), ([0, 5200, 1], 9, 2, 2, 64, 64, BF, True, False),
+    ([1600], 0, 2, 1, 128, 128, BF, True, True), ([2048], 0, 3, 3, 64, 128, BF, False, True),
+]
+
+
+@pytest.mark.parametrize("first", [0, 77])
+@pytest.mark.parametrize("lengths,tail,H,G,P,N,dtype,carried,extra", SEGMENT_CASES)
+def test_scan_in_segments(lengths, tail, H, G, P, N, dtype, carried, extra, first):
+    offs, T, s, S0, r = scan_inputs(lengths, tail, H, G, P, N, dtype, carried, extra, seed=H + sum(lengths), first=first)
+    assert gdn.lib().gdn_ssm_chunk_fwd_workspace_size(len(lengths), T, H, G, P, N, 1) > 0
+    out = torch.full((T, H, P), 7.0, dtype=dtype, device="cuda")
+    got, last = gdn.gdn_ssm_chunk_fwd(**s, cu_seqlens=cu(offs), initial_state=S0, out=out)
+    (ref, ref_last), (terms, terms_last) = scan_reference(s, offs, S0)
+    check("out", got[first:offs[-1]], ref[first:offs[-1]], terms[first:offs[-1]])
+    check("state", last, ref_last, terms_last)
+    assert bool((got[:first] == 7.0).all()) and bool((got[offs[-1]:] == 7.0).all())
+    if carried:  # the final states in the initial ones' place
+        keep = S0.clone()
+        again, same = gdn.gdn_ssm_chunk_fwd(**s, cu_seqlens=cu(offs), initial_state=keep, final_state=keep, out=out.clone())
+        assert torch.equal(again, got) and torch.equal(keep, last) and same is keep
+    dout = dev(r(T, H, P), dtype)
+    dlast = dev(r(len(lengths), H, P, N)) if carried else None
+    args = dict(cu_seqlens=cu(offs), initial_state=S0)
+    grads = gdn.gdn_ssm_chunk_bwd(dout, **s, **args, dfinal_state=dlast)
+    check_grads(grads, dout, s, offs, S0, dlast, dtype)
+    if carried:
+        keep = dlast.clone()
+        for a, b in zip(grads, gdn.gdn_ssm_chunk_bwd(dout, **s, **args, dfinal_state=keep, dinitial_state=keep)):
+            assert a is None or torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_scan_of_many_sequences_without_offsets_and_states_in_place(dtype):
     offs, T, s, S0, _ = scan_inputs([70] * 5, 0, 2, 1, 64, 64, dtype, True, True, seed=9)
