@@ -895,6 +895,17 @@ def _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight, dq_weight=None, dk_
     return T, H, H_k, d, rot, dt, max_positions, p, rows
 
 
+def _qk_output(q, name, out, T, heads, d):
+    """An output of the norm and rotation, its pointer and stride; allocated unless given."""
+    if heads == 0:
+        return None, None, 0
+    if out is None:
+        out = q.new_empty((T, heads, d))
+        return out, out.data_ptr(), heads * d
+    _same_dtype(_dt(q), **{name: out})
+    return out, *_rows(q, name, out, (T, heads, d))
+
+
 @_on_stream
 def gdn_qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, norm=GDN_NORM_RMS, eps=1e-6,
                      interleaved=False, q_out=None, k_out=None):
@@ -904,15 +915,11 @@ def gdn_qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None
     positions int32 [T] or None (row t has position t), weights [d] fp32 or None.  Pairs are channels i and
     d_rot / 2 + i, or neighbours when interleaved.  Returns (q_out, k_out), allocated unless given (they may be q and k)."""
     T, H, H_k, d, rot, dt, most, p, rows = _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight)
-    if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty((T, H_k, d), dtype=q.dtype, device=q.device)
-    _same_dtype(dt, q_out=q_out, k_out=k_out)
-    outs = (*_rows(q, "q_out", q_out, (T, H, d)), *((None, 0) if k is None else _rows(q, "k_out", k_out, (T, H_k, d))))
+    q_out, pq, sq = _qk_output(q, "q_out", q_out, T, H, d)
+    k_out, pk, sk = _qk_output(q, "k_out", k_out, T, H_k, d)
     _check("gdn_qk_norm_rope",
            _run(q, lib().gdn_qk_norm_rope, *rows, p[0], p[1], most, p[2], p[3], int(norm), float(eps),
-                int(bool(interleaved)), T, H, H_k, d, rot, dt, *outs, _stream(None, q)))
+                int(bool(interleaved)), T, H, H_k, d, rot, dt, pq, sq, pk, sk, _stream(None, q)))
     return q_out, k_out
 
 
@@ -926,19 +933,16 @@ def gdn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin, positions=None, q_weight
     if k_weight is not None and dk_weight is None and k is not None:
         dk_weight = torch.empty_like(k_weight)
     T, H, H_k, d, rot, dt, most, p, rows = _qk_inputs(q, k, cos_sin, positions, q_weight, k_weight, dq_weight, dk_weight)
-    if dq is None:
-        dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    if dk is None and k is not None:
-        dk = torch.empty((T, H_k, d), dtype=q.dtype, device=q.device)
-    _same_dtype(dt, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
+    dq, pq, sq = _qk_output(q, "dq", dq, T, H, d)
+    dk, pk, sk = _qk_output(q, "dk", dk, T, H_k, d)
+    _same_dtype(dt, dq_out=dq_out, dk_out=dk_out)
     g = _pointers(q, ("dq_out", "dk_out"), (dq_out, dk_out), (T * H * d, T * H_k * d), (False, False))
-    outs = (*_rows(q, "dq", dq, (T, H, d)), *((None, 0) if k is None else _rows(q, "dk", dk, (T, H_k, d))))
     L = lib()
     need = L.gdn_qk_norm_rope_bwd_workspace_size(T, H, H_k, d) if dq_weight is not None or dk_weight is not None else 0
     workspace, ws, ws_bytes = _workspace(workspace, need, q)
     _check("gdn_qk_norm_rope_bwd",
            _run(q, L.gdn_qk_norm_rope_bwd, *g, *rows, p[0], p[1], most, p[2], p[3], int(norm), float(eps),
-                int(bool(interleaved)), T, H, H_k, d, rot, dt, *outs, p[4], p[5], ws, ws_bytes, _stream(None, q)))
+                int(bool(interleaved)), T, H, H_k, d, rot, dt, pq, sq, pk, sk, p[4], p[5], ws, ws_bytes, _stream(None, q)))
     return dq, dk, dq_weight, dk_weight
 
 
