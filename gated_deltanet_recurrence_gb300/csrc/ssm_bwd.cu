@@ -409,12 +409,10 @@ int subsets_of(int num_seqs, int total_T, int H, int G) {
     return (int)(n < 1 ? 1 : n);
 }
 
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, unsigned char* at) {
     const size_t slots = (size_t)slots_of(num_seqs, total_T);
-    const size_t gates = align256(slots * H * kGateRows * kC * sizeof(float));
-    const size_t states = align256(slots * H * P * N * sizeof(float)), sums = align256(slots * H * 3 * sizeof(float));
+    const size_t gates = up256(slots * H * kGateRows * kC * sizeof(float));
+    const size_t states = up256(slots * H * P * N * sizeof(float)), sums = up256(slots * H * 3 * sizeof(float));
     const int subsets = subsets_of(num_seqs, total_T, H, G);
     const size_t parts = subsets > 1 ? (size_t)subsets * 2 * total_T * G * N * sizeof(float) : 0;
     if (w) {
@@ -425,7 +423,8 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, un
         w->parts = reinterpret_cast<float*>(at + gates + 2 * states + sums);
         w->subsets = subsets;
     }
-    return gates + 2 * states + sums + parts;
+    const size_t used = gates + 2 * states + sums + up256(parts);
+    return used + segments64(num_seqs, total_T, H, P, N, 2, false, w ? &w->g : nullptr, w ? at + used : nullptr);
 }
 
 }  // namespace
@@ -452,7 +451,7 @@ cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
     ssm::Work w{};
     ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
     cudaError_t e = ssm::launch_gates(a, w, s);
-    if (e == cudaSuccess) e = ssm::launch_scan(a, w, true, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, 2, s);
     if (e != cudaSuccess) return e;
     const long slots = ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
     e = a.N == 128 ? ssm::grad_one<128>(a, w, s) : ssm::grad_one<64>(a, w, s);

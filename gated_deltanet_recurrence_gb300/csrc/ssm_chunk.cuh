@@ -52,6 +52,46 @@ __device__ __forceinline__ bool find_chunk(const Packed& s, int slot, int* err, 
 }
 inline long slots_of(int num_seqs, int total_T) { return (long)total_T / kC + num_seqs; }
 
+// Sequences are walked along whole, or, where that leaves SMs idle, in segments of `each` chunks at once: first every
+// segment's own end state (from zero), then those joined into the states that the segments begin with.  Segments have
+// slots as chunks have; an empty sequence has one segment.  Index 1 of a pair: backwards, gradients of states.
+struct Segments {
+    int each, unit;   // chunks of a segment (0: whole sequences), tokens of a chunk
+    float* decay[2];  // [slots][H]: e^{sum of the segment's log decays}
+    float* own[2];    // [slots][H][P][N]
+    float* start[2];
+};
+struct Run {
+    int n, t0, end;     // sequence, tokens
+    bool first, last;   // of its sequence
+    long slot0;         // of its first chunk
+};
+// The segment of slot `index`, or sequence `index`; false where there is none.  The whole block takes part.
+__device__ __forceinline__ bool find_run(const Packed& s, int each, int chunk, int index, int* err, Run& r) {
+    const int unit = each * chunk, found = each ? packed_find(s, index, unit, 1, err) : packed_find(s, 0, 1, 0, err);
+    if (each ? found < 0 || found >= s.num_seqs : found == -2) return false;
+    r.n = each ? found : index;
+    const int bos = s.bos(r.n), eos = s.bos(r.n + 1), k = each ? index - (bos / unit + r.n) : 0;
+    r.t0 = bos + k * unit;
+    r.first = k == 0;
+    if (!r.first && r.t0 >= eos) return false;
+    r.last = !each || eos - r.t0 <= unit;
+    r.end = r.last ? eos : r.t0 + unit;
+    r.slot0 = bos / chunk + r.n + (long)k * each;
+    return true;
+}
+inline long segment_slots(int num_seqs, int total_T, const Segments& g) { return (long)total_T / (g.each * g.unit) + num_seqs; }
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// ssm_fwd.cu: the segments of a call and the workspace that they need, laid out from `at` (`varied`: the lengths may
+// differ).  The cost of a chunk, in us: along whole sequences, for a segment's own state; of what segments need besides.
+struct SegmentCost {
+    double whole, own, more;
+};
+size_t segments_layout(int num_seqs, int total_T, int H, int P, int N, int unit, int directions, bool varied, SegmentCost cost,
+                       Segments* g, unsigned char* at);
+cudaError_t launch_join(const SsmArgs& a, const Segments& g, int directions, cudaStream_t s);
+
 struct Work {
     float* gates;     // [slots][H][kGateRows][64]
     float* states;    // [slots][H][P][N], at the chunks' starts
@@ -59,11 +99,17 @@ struct Work {
     float* sums;      // [3][slots][H]: dA_log, ddt_bias, dD of each chunk
     float* parts;     // [subsets][total_T][G][N] twice (dB, dC), with more than one subset of a group's heads
     int subsets;
+    Segments g;
 };
 
-// Launches the gates, and the states at the chunks' starts; `both`: also their gradients at the chunks' ends.
+// The segments of a fp32 call.  Launches the gates, and the states at the chunks' starts; with two directions also their
+// gradients at the chunks' ends.
+inline size_t segments64(int num_seqs, int total_T, int H, int P, int N, int directions, bool varied, Segments* g, unsigned char* at) {
+    const double chunk = N == 128 ? 3.3 : 2.1;
+    return segments_layout(num_seqs, total_T, H, P, N, kC, directions, varied, SegmentCost{chunk, chunk, 8.}, g, at);
+}
 cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s);
-cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s);
+cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStream_t s);
 // The whole forward pass of bf16 prompts (ssm_tc.cu), for total_T > 0.
 size_t tc_workspace_bytes(int num_seqs, int total_T, int H, int P, int N);
 cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s);

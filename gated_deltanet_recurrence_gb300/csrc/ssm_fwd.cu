@@ -56,10 +56,11 @@ __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, f
 // ---- states --------------------------------------------------------------------------------------
 
 // Block: 8 warps; warp w holds rows 16 (w % 4) .. of the 64 and half of the N columns.  Blocks with blockIdx.y = 1: the
-// states' gradients, from the last chunk to the first.
+// states' gradients, from the last chunk to the first.  With `own` the blocks leave their segments' states from zero, and
+// nothing of the way.
 constexpr int kScanThreads = 256;
 template <int N>
-__global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work w) {
+__global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work w, bool own) {
     constexpr int NT = N / 16, KV = N / 32;  // KV: vectors of B a thread loads
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
@@ -68,12 +69,14 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
     __shared__ float fac[kC];
     const bool REV = blockIdx.y;
     dependency_start();
-    if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) {
+    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, index = blockIdx.x / slices / a.H;
+    Run run;
+    // what a segment leaves goes to the next one: the last of a sequence has none
+    if (!find_run(a.seqs, w.g.each, kC, index, a.err, run) || (own && (REV ? run.first : run.last))) {
         dependency_wait();
         return;
     }
-    const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, n = blockIdx.x / slices / a.H;
-    const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1), chunks = (eos - bos + kC - 1) / kC;
+    const int bos = run.t0, eos = run.end, chunks = (eos - bos + kC - 1) / kC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m0 = (warp & 3) * 16, n0 = (warp >> 2) * (N / 2);
     const int g = h / (a.H / a.G);
@@ -81,14 +84,23 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
     const long k_stride = REV ? a.C_stride : a.B_stride;
     const float* X = static_cast<const float*>(REV ? a.dout : a.x) + (long)h * a.P + s * 64;
     const long x_stride = REV ? (long)a.H * a.P : a.x_stride;
-    const long row0 = (((long)n * a.H + h) * a.P + s * 64) * N;
-    const float* init = REV ? a.dfinal_state : a.initial_state;
-    float* last = REV ? a.dinitial_state : a.final_state;
+    const long row0 = (((long)run.n * a.H + h) * a.P + s * 64) * N, own0 = (((long)index * a.H + h) * a.P + s * 64) * N;
+    const float* init = nullptr;
+    float* last = nullptr;
+    if (own) {
+        last = (REV ? w.g.own[1] : w.g.own[0]) + own0;
+    } else {
+        const float* given = REV ? a.dfinal_state : a.initial_state;
+        init = w.g.each ? (REV ? w.g.start[1] : w.g.start[0]) + own0 : (given ? given + row0 : nullptr);
+        float* end = REV ? a.dinitial_state : a.final_state;
+        if (end && (REV ? run.first : run.last)) last = end + row0;
+    }
     float* keep = REV ? w.dstates : w.states;
 
+    dependency_wait();
     float S[NT][4];
     bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
-        const float2 v = init ? *reinterpret_cast<const float2*>(init + row0 + (long)p * N + c) : make_float2(0.f, 0.f);
+        const float2 v = init ? *reinterpret_cast<const float2*>(init + (long)p * N + c) : make_float2(0.f, 0.f);
         S[j][2 * hh] = v.x;
         S[j][2 * hh + 1] = v.y;
     });
@@ -106,18 +118,19 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
             const int v = i * kScanThreads + tid, r = v / 8, c = v % 8 * 8;
             xr[i].load(X + (long)(t0 + r) * x_stride + c, r < len);
         }
-        const float* gt = w.gates + ((long)(bos / kC + n + k) * a.H + h) * (kGateRows * kC);
+        const float* gt = w.gates + ((run.slot0 + k) * a.H + h) * (kGateRows * kC);
         if (tid < kC) {
             gd = REV ? 1.f : gt[tid];
             gb = gt[(REV ? 3 : 4) * kC + tid];
         }
         gl = gt[3 * kC + kC - 1];
     };
-    dependency_wait();
+    float total = 1.f;
     if (chunks > 0) fetch(REV ? chunks - 1 : 0);
     for (int q = 0; q < chunks; ++q) {
         const int k = REV ? chunks - 1 - q : q;
         const float decay = gl;
+        total *= decay;
         if (tid < kC) fac[tid] = gd * gb;
 #pragma unroll
         for (int i = 0; i < KV; ++i) {
@@ -134,9 +147,9 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
             for (int e = 0; e < 8; ++e) x[e] *= fac[r];
             bfp::put8(Vt, r, v % 8 * 8, x);
         }
-        float* to = keep + (((long)(bos / kC + n + k) * a.H + h) * a.P + s * 64) * N;
+        float* to = keep + (((run.slot0 + k) * a.H + h) * a.P + s * 64) * N;
         bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
-            *reinterpret_cast<float2*>(to + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
+            if (!own) *reinterpret_cast<float2*>(to + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
             S[j][2 * hh] *= decay;
             S[j][2 * hh + 1] *= decay;
         });
@@ -147,16 +160,58 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, Work 
     }
     if (last)
         bfp::pairs<NT>(m0, n0, lane, [&](int j, int hh, int p, int c) {
-            *reinterpret_cast<float2*>(last + row0 + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
+            *reinterpret_cast<float2*>(last + (long)p * N + c) = make_float2(S[j][2 * hh], S[j][2 * hh + 1]);
         });
+    if (own && s == 0 && tid == 0) (REV ? w.g.decay[1] : w.g.decay[0])[(long)index * a.H + h] = total;
 }
 
 template <int N>
-cudaError_t scan_one(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
+cudaError_t scan_one(const SsmArgs& a, const Work& w, bool own, int directions, cudaStream_t s) {
     constexpr int smem = bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3>;
     const cudaError_t e = cudaFuncSetAttribute(ssm_scan_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(ssm_scan_kernel<N>, dim3((unsigned)((long)a.seqs.num_seqs * a.H * (a.P / 64)), both ? 2 : 1), kScanThreads, smem, s, a, w);
+    const long runs = w.g.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w.g) : a.seqs.num_seqs;
+    return launch_after(ssm_scan_kernel<N>, dim3((unsigned)(runs * a.H * (a.P / 64)), directions), kScanThreads, smem, s, a, w, own);
+}
+
+// ---- segments ------------------------------------------------------------------------------------
+
+// One thread: four numbers of the states of a (sequence, head), in one direction, along its segments.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, Segments g) {
+    const int n = blockIdx.z, back = blockIdx.y / a.H, h = blockIdx.y % a.H, unit = g.each * g.unit;
+    dependency_start();
+    const bool bad = packed_find(a.seqs, 0, 1, 0, a.err) == -2;
+    dependency_wait();
+    if (bad) return;
+    const int bos = a.seqs.bos(n), count = max((a.seqs.bos(n + 1) - bos + unit - 1) / unit, 1);
+    const long size = (long)a.P * a.N, at = ((long)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+    if (at >= size) return;
+    const float* given = back ? a.dfinal_state : a.initial_state;
+    float4 S = given ? *reinterpret_cast<const float4*>(given + ((long)n * a.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const long first = bos / unit + n;
+    const auto row = [&](int k) { return (first + (back ? count - 1 - k : k)) * a.H + h; };  // of the k-th segment on the way
+    // the first one's too: the given states may be overwritten by the last segment's block
+    *reinterpret_cast<float4*>((back ? g.start[1] : g.start[0]) + row(0) * size + at) = S;
+    for (int k0 = 0; k0 + 1 < count; k0 += 4) {
+        float4 own[4];
+        float decay[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k0 + e + 1 >= count) continue;
+            own[e] = *reinterpret_cast<const float4*>((back ? g.own[1] : g.own[0]) + row(k0 + e) * size + at);
+            decay[e] = (back ? g.decay[1] : g.decay[0])[row(k0 + e)];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k0 + e + 1 >= count) continue;
+            S.x = fmaf(decay[e], S.x, own[e].x);
+            S.y = fmaf(decay[e], S.y, own[e].y);
+            S.z = fmaf(decay[e], S.z, own[e].z);
+            S.w = fmaf(decay[e], S.w, own[e].w);
+            *reinterpret_cast<float4*>((back ? g.start[1] : g.start[0]) + row(k0 + e + 1) * size + at) = S;
+        }
+    }
 }
 
 // ---- outputs -------------------------------------------------------------------------------------
@@ -266,8 +321,6 @@ cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
     return launch_after(ssm_out_kernel<N>, grid, kOutThreads, kOutSmem<N>, s, a, w);
 }
 
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 }  // namespace
 
 cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
@@ -276,8 +329,59 @@ cudaError_t launch_gates(const SsmArgs& a, const Work& w, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t s) {
-    return a.N == 128 ? scan_one<128>(a, w, both, s) : scan_one<64>(a, w, both, s);
+cudaError_t launch_join(const SsmArgs& a, const Segments& g, int directions, cudaStream_t s) {
+    const dim3 grid((unsigned)(a.P * a.N / (4 * kJoinThreads)), (unsigned)(a.H * directions), (unsigned)a.seqs.num_seqs);
+    return launch_after(ssm_join_kernel, grid, kJoinThreads, 0, s, a, g);
+}
+
+cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStream_t s) {
+    const auto scan = [&](bool own) {
+        return a.N == 128 ? scan_one<128>(a, w, own, directions, s) : scan_one<64>(a, w, own, directions, s);
+    };
+    if (w.g.each) {
+        cudaError_t e = scan(true);
+        if (e == cudaSuccess) e = launch_join(a, w.g, directions, s);
+        if (e != cudaSuccess) return e;
+    }
+    return scan(false);
+}
+
+// Chunks of a segment, or 0.  Blocks are counted against 152 SMs.  Few rows: as many segments as fill the SMs, where that
+// pays for sequences of one length.  A packed batch of up to two rounds of blocks, forwards: segments a little longer
+// than the average, where it pays if the longest of n sequences is 1 + 1/2 + ... + 1/n times the average.
+static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int directions, bool varied, SegmentCost cost) {
+    const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
+               avg = (chunks + num_seqs - 1) / num_seqs;
+    const auto split = [&](long each) { return each * (cost.whole + cost.own) + cost.more; };
+    if (rows <= 152) {
+        const long count = 152 / rows, fill = (avg + count - 1) / count, each = fill < 4 ? 4 : fill;
+        if (avg * cost.whole > split(each)) return (int)each;
+    }
+    if (directions > 1 || !varied || rows > 304) return 0;
+    const long each = avg + avg / 4 < 8 ? 8 : avg + avg / 4;
+    double longest = 0.;
+    for (int n = 1; n <= num_seqs; ++n) longest += (double)avg / n;
+    return longest * cost.whole > split(each) ? (int)each : 0;
+}
+
+size_t segments_layout(int num_seqs, int total_T, int H, int P, int N, int unit, int directions, bool varied, SegmentCost cost,
+                       Segments* g, unsigned char* at) {
+    Segments w{};
+    w.unit = unit;
+    w.each = segment_chunks(num_seqs, total_T, H, P, unit, directions, varied, cost);
+    size_t bytes = 0;
+    if (w.each) {
+        const size_t slots = (size_t)segment_slots(num_seqs, total_T, w), states = slots * H * P * N * sizeof(float),
+                     decays = up256(slots * H * sizeof(float));
+        for (int i = 0; i < directions && g; ++i) {
+            w.own[i] = reinterpret_cast<float*>(at + 2 * i * states);
+            w.start[i] = reinterpret_cast<float*>(at + (2 * i + 1) * states);
+            w.decay[i] = reinterpret_cast<float*>(at + 2 * directions * states + i * decays);
+        }
+        bytes = directions * (2 * states + decays);
+    }
+    if (g) *g = w;
+    return bytes;
 }
 
 }  // namespace ssm
@@ -285,7 +389,10 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, bool both, cudaStream_t
 size_t ssm_fwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
     if (dtype == GDN_BF16) return total_T > 0 ? ssm::tc_workspace_bytes(num_seqs, total_T, H, P, N) : 0;
     const size_t slots = (size_t)ssm::slots_of(num_seqs, total_T);
-    return ssm::align256(slots * H * ssm::kGateRows * ssm::kC * sizeof(float)) + slots * H * P * N * sizeof(float);
+    const size_t used = ssm::up256(slots * H * ssm::kGateRows * ssm::kC * sizeof(float)) + slots * H * P * N * sizeof(float);
+    const size_t equal = ssm::segments64(num_seqs, total_T, H, P, N, 1, false, nullptr, nullptr),
+                 varied = ssm::segments64(num_seqs, total_T, H, P, N, 1, true, nullptr, nullptr);
+    return used + (equal > varied ? equal : varied);
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
@@ -293,9 +400,11 @@ cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t s) {
     ssm::Work w{};
     const size_t slots = (size_t)ssm::slots_of(a.seqs.num_seqs, a.seqs.total_T);
     w.gates = static_cast<float*>(a.workspace);
-    w.states = w.gates + ssm::align256(slots * a.H * ssm::kGateRows * ssm::kC * sizeof(float)) / sizeof(float);
+    w.states = w.gates + ssm::up256(slots * a.H * ssm::kGateRows * ssm::kC * sizeof(float)) / sizeof(float);
+    ssm::segments64(a.seqs.num_seqs, a.seqs.total_T, a.H, a.P, a.N, 1, a.seqs.cu && a.seqs.num_seqs > 1, &w.g,
+                    reinterpret_cast<unsigned char*>(w.states + slots * a.H * a.P * a.N));
     cudaError_t e = ssm::launch_gates(a, w, s);
-    if (e == cudaSuccess) e = ssm::launch_scan(a, w, false, s);
+    if (e == cudaSuccess) e = ssm::launch_scan(a, w, 1, s);
     if (e != cudaSuccess || a.seqs.total_T == 0) return e;
     return a.N == 128 ? ssm::out_one<128>(a, w, s) : ssm::out_one<64>(a, w, s);
 }

@@ -62,7 +62,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CU
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, index = blockIdx.x / slices / a.H;
     Run run;
-    if (!find_run(a.seqs, w.each, index, a.err, run)) {
+    if (!find_run(a.seqs, w.each, kT, index, a.err, run)) {
         dependency_wait();
         return;
     }
@@ -474,7 +474,7 @@ cudaError_t launch(const SsmArgs& a, const Segments& w, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(ssm_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::bytes);
     if (e != cudaSuccess) return e;
-    const long runs = w.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w.each) : a.seqs.num_seqs;
+    const long runs = w.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w) : a.seqs.num_seqs;
     const dim3 grid((unsigned)(runs * a.H * (a.P / 64)));
     if (w.each) return launch_after(ssm_tc_kernel<N>, grid, kThreads, Lay<N>::bytes, s, mX, mB, mC, a, w);
     ssm_tc_kernel<N><<<grid, kThreads, Lay<N>::bytes, s>>>(mX, mB, mC, a, w);
@@ -486,7 +486,7 @@ cudaError_t launch(const SsmArgs& a, const Segments& w, cudaStream_t s) {
 size_t tc_workspace_bytes(int num_seqs, int total_T, int H, int P, int N) {
     size_t most = 0;
     for (int varied = 0; varied < 2; ++varied) {
-        const size_t segments = segments_layout(num_seqs, total_T, H, P, N, 1, varied, nullptr, nullptr);
+        const size_t segments = segments128(num_seqs, total_T, H, P, N, 1, varied, nullptr, nullptr);
         if (segments > most) most = segments;
     }
     return most;
@@ -495,7 +495,7 @@ size_t tc_workspace_bytes(int num_seqs, int total_T, int H, int P, int N) {
 cudaError_t launch_tc(const SsmArgs& a, cudaStream_t s) {
     Segments w{};
     const Packed& q = a.seqs;
-    segments_layout(q.num_seqs, q.total_T, a.H, a.P, a.N, 1, q.cu && q.num_seqs > 1, &w, static_cast<unsigned char*>(a.workspace));
+    segments128(q.num_seqs, q.total_T, a.H, a.P, a.N, 1, q.cu && q.num_seqs > 1, &w, static_cast<unsigned char*>(a.workspace));
     if (w.each) {
         const cudaError_t e = launch_starts(a, nullptr, w, 1, s);
         if (e != cudaSuccess) return e;

@@ -152,45 +152,16 @@ __device__ __forceinline__ bool find_chunk128(const Packed& s, int slot, int* er
     return c.len > 0;
 }
 
-// Sequences are walked along whole, or, where that leaves SMs idle, in segments of `each` chunks at once: first every
-// segment's own end state (from zero), then those joined into the states that the segments begin with.  Segments have
-// slots as chunks have; an empty sequence has one segment.  Index 1 of a pair: backwards, gradients of states.
-struct Segments {
-    int each;         // chunks of a segment; 0: whole sequences
-    float* decay[2];  // [slots][H]: e^{sum of the segment's log decays}
-    float* own[2];    // [slots][H][P][N]
-    float* start[2];
-};
-struct Run {
-    int n, t0, end;     // sequence, tokens
-    bool first, last;   // of its sequence
-    long slot0;         // of its first chunk
-};
-// The segment of slot `index`, or sequence `index`; false where there is none.  The whole block takes part.
-__device__ __forceinline__ bool find_run(const Packed& s, int each, int index, int* err, Run& r) {
-    const int unit = each * kT, found = each ? packed_find(s, index, unit, 1, err) : packed_find(s, 0, 1, 0, err);
-    if (each ? found < 0 || found >= s.num_seqs : found == -2) return false;
-    r.n = each ? found : index;
-    const int bos = s.bos(r.n), eos = s.bos(r.n + 1), k = each ? index - (bos / unit + r.n) : 0;
-    r.t0 = bos + k * unit;
-    r.first = k == 0;
-    if (!r.first && r.t0 >= eos) return false;
-    r.last = !each || eos - r.t0 <= unit;
-    r.end = r.last ? eos : r.t0 + unit;
-    r.slot0 = bos / kT + r.n + (long)k * each;
-    return true;
-}
-
 // ---- host ------------------------------------------------------------------------------------------
 
 inline long slots128(int num_seqs, int total_T) { return (long)total_T / kT + num_seqs; }
-inline long segment_slots(int num_seqs, int total_T, int each) { return (long)total_T / (each * kT) + num_seqs; }
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// ssm_tc_scan.cu: chunks of a segment, or 0 (`varied`: the lengths may differ); the workspace that `directions` of segments
-// need, laid out from `at`; the gates of all chunks; the states that the segments begin with (no gates given: forwards).
-int segment_chunks(int num_seqs, int total_T, int H, int P, int directions, bool varied);
-size_t segments_layout(int num_seqs, int total_T, int H, int P, int N, int directions, bool varied, Segments* g, unsigned char* at);
+// ssm_tc_scan.cu: the segments of a bf16 call; the gates of all chunks; the states that the segments begin with (no gates
+// given: forwards).
+inline size_t segments128(int num_seqs, int total_T, int H, int P, int N, int directions, bool varied, Segments* g, unsigned char* at) {
+    const SegmentCost cost = directions == 1 ? SegmentCost{2.7, 1.7, 10.} : SegmentCost{1.8, 1.7, 8.};
+    return segments_layout(num_seqs, total_T, H, P, N, kT, directions, varied, cost, g, at);
+}
 cudaError_t launch_gates128(const SsmArgs& a, float* gates, cudaStream_t s);
 cudaError_t launch_starts(const SsmArgs& a, const float* gates, const Segments& g, int directions, cudaStream_t s);
 // The images of the states at the chunks' starts and of their gradients at the chunks' ends: [slots][H][P / 64] of N x 64

@@ -670,7 +670,7 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, TcWork* w, 
         w->subsets = subsets;
     }
     const size_t used = gates + 2 * states + sums + up256(parts);
-    return used + segments_layout(num_seqs, total_T, H, P, N, 2, false, w ? &w->g : nullptr, w ? at + used : nullptr);
+    return used + segments128(num_seqs, total_T, H, P, N, 2, false, w ? &w->g : nullptr, w ? at + used : nullptr);
 }
 
 template <int N>

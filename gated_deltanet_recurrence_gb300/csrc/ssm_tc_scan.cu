@@ -86,7 +86,7 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     const int slices = a.P / 64, s = blockIdx.x % slices, h = blockIdx.x / slices % a.H, index = blockIdx.x / slices / a.H;
     Run run;
     // what a segment leaves goes to the next one: the last of a sequence has none
-    if (!find_run(a.seqs, w.g.each, index, a.err, run) || (w.own && (back ? run.first : run.last))) {
+    if (!find_run(a.seqs, w.g.each, kT, index, a.err, run) || (w.own && (back ? run.first : run.last))) {
         dependency_wait();
         return;
     }
@@ -324,46 +324,6 @@ ssm_scan_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     }
 }
 
-// ---- segments ------------------------------------------------------------------------------------
-
-// One thread: four numbers of the states of a (sequence, head), in one direction, along its segments.
-constexpr int kJoinThreads = 128;
-__global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, Segments g) {
-    const int n = blockIdx.z, back = blockIdx.y / a.H, h = blockIdx.y % a.H, unit = g.each * kT;
-    dependency_start();
-    const bool bad = packed_find(a.seqs, 0, 1, 0, a.err) == -2;
-    dependency_wait();
-    if (bad) return;
-    const int bos = a.seqs.bos(n), count = max((a.seqs.bos(n + 1) - bos + unit - 1) / unit, 1);
-    const long size = (long)a.P * a.N, at = ((long)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
-    if (at >= size) return;
-    const float* given = back ? a.dfinal_state : a.initial_state;
-    float4 S = given ? *reinterpret_cast<const float4*>(given + ((long)n * a.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const long first = bos / unit + n;
-    const auto row = [&](int k) { return (first + (back ? count - 1 - k : k)) * a.H + h; };  // of the k-th segment on the way
-    // the first one's too: the given states may be overwritten by the last segment's block
-    *reinterpret_cast<float4*>((back ? g.start[1] : g.start[0]) + row(0) * size + at) = S;
-    for (int k0 = 0; k0 + 1 < count; k0 += 4) {
-        float4 own[4];
-        float decay[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (k0 + e + 1 >= count) continue;
-            own[e] = *reinterpret_cast<const float4*>((back ? g.own[1] : g.own[0]) + row(k0 + e) * size + at);
-            decay[e] = (back ? g.decay[1] : g.decay[0])[row(k0 + e)];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (k0 + e + 1 >= count) continue;
-            S.x = fmaf(decay[e], S.x, own[e].x);
-            S.y = fmaf(decay[e], S.y, own[e].y);
-            S.z = fmaf(decay[e], S.z, own[e].z);
-            S.w = fmaf(decay[e], S.w, own[e].w);
-            *reinterpret_cast<float4*>((back ? g.start[1] : g.start[0]) + row(k0 + e + 1) * size + at) = S;
-        }
-    }
-}
-
 template <int N>
 cudaError_t launch_scan128(const SsmArgs& a, const ScanOut& w, int directions, cudaStream_t s) {
     CUtensorMap mX, mY{}, mB, mC{};
@@ -373,7 +333,7 @@ cudaError_t launch_scan128(const SsmArgs& a, const ScanOut& w, int directions, c
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(ssm_scan_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanLay<N>::bytes);
     if (e != cudaSuccess) return e;
-    const long runs = w.g.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w.g.each) : a.seqs.num_seqs;
+    const long runs = w.g.each ? segment_slots(a.seqs.num_seqs, a.seqs.total_T, w.g) : a.seqs.num_seqs;
     const dim3 grid((unsigned)(runs * a.H * (a.P / 64)), directions);
     if (w.gates) return launch_after(ssm_scan_tc_kernel<N>, grid, kScanThreads, ScanLay<N>::bytes, s, mX, mY, mB, mC, a, w);
     // the call's first kernel
@@ -385,35 +345,6 @@ cudaError_t launch_scan128(const SsmArgs& a, const ScanOut& w, int directions, c
 
 namespace tc {
 
-int segment_chunks(int num_seqs, int total_T, int H, int P, int directions, bool varied) {
-    const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = (total_T + kT - 1) / kT, avg = (chunks + num_seqs - 1) / num_seqs;
-    const double whole = directions == 1 ? 2.7 : 1.8, own = 1.7, more = directions == 1 ? 10. : 8.;
-    if (rows <= 152) {
-        const long count = 152 / rows, fill = (avg + count - 1) / count, each = fill < 4 ? 4 : fill;
-        if (avg * whole > each * (whole + own) + more) return (int)each;
-    }
-    if (directions > 1 || !varied || rows > 304) return 0;
-    const long each = avg + avg / 4 < 8 ? 8 : avg + avg / 4;
-    double longest = 0.;
-    for (int n = 1; n <= num_seqs; ++n) longest += (double)avg / n;
-    return longest * whole > each * (whole + own) + more ? (int)each : 0;
-}
-
-size_t segments_layout(int num_seqs, int total_T, int H, int P, int N, int directions, bool varied, Segments* g, unsigned char* at) {
-    const int each = segment_chunks(num_seqs, total_T, H, P, directions, varied);
-    if (g) g->each = each;
-    if (!each) return 0;
-    const size_t slots = (size_t)segment_slots(num_seqs, total_T, each), states = slots * H * P * N * sizeof(float),
-                 decays = up256(slots * H * sizeof(float));
-    if (g)
-        for (int i = 0; i < directions; ++i) {
-            g->own[i] = reinterpret_cast<float*>(at + 2 * i * states);
-            g->start[i] = reinterpret_cast<float*>(at + (2 * i + 1) * states);
-            g->decay[i] = reinterpret_cast<float*>(at + 2 * directions * states + i * decays);
-        }
-    return directions * (2 * states + decays);
-}
-
 cudaError_t launch_gates128(const SsmArgs& a, float* gates, cudaStream_t s) {
     const dim3 grid((unsigned)slots128(a.seqs.num_seqs, a.seqs.total_T), (unsigned)((a.H + kGateWarps - 1) / kGateWarps));
     ssm_gates128_kernel<<<grid, kGateWarps * 32, 0, s>>>(a, gates);
@@ -424,8 +355,7 @@ cudaError_t launch_starts(const SsmArgs& a, const float* gates, const Segments& 
     const ScanOut w{gates, g, true, {nullptr, nullptr}};
     const cudaError_t e = a.N == 128 ? launch_scan128<128>(a, w, directions, s) : launch_scan128<64>(a, w, directions, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.P * a.N / (4 * kJoinThreads)), (unsigned)(a.H * directions), (unsigned)a.seqs.num_seqs);
-    return launch_after(ssm_join_kernel, grid, kJoinThreads, 0, s, a, g);
+    return launch_join(a, g, directions, s);
 }
 
 cudaError_t launch_states(const SsmArgs& a, const float* gates, const Segments& g, float* states, float* dstates, cudaStream_t s) {

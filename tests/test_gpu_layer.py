@@ -210,6 +210,7 @@ def test_scan(lengths, tail, H, G, P, N, dtype, carried, extra):
 SEGMENT_CASES = [  # long sequences of few heads, which are walked along in segments
     ([1700], 0, 1, 1, 64, 64, BF, True, True), ([0, 5200, 1], 9, 2, 2, 64, 64, BF, True, False),
     ([1600], 0, 2, 1, 128, 128, BF, True, True), ([2048], 0, 3, 3, 64, 128, BF, False, True),
+    ([900], 0, 2, 1, 64, 128, F32, True, True), ([0, 2500, 1], 9, 2, 2, 64, 64, F32, True, False), ([1024], 0, 1, 1, 128, 128, F32, False, True),
 ]
 
 
@@ -217,7 +218,7 @@ SEGMENT_CASES = [  # long sequences of few heads, which are walked along in segm
 @pytest.mark.parametrize("lengths,tail,H,G,P,N,dtype,carried,extra", SEGMENT_CASES)
 def test_scan_in_segments(lengths, tail, H, G, P, N, dtype, carried, extra, first):
     offs, T, s, S0, r = scan_inputs(lengths, tail, H, G, P, N, dtype, carried, extra, seed=H + sum(lengths), first=first)
-    assert gdn.lib().gdn_ssm_chunk_fwd_workspace_size(len(lengths), T, H, G, P, N, 1) > 0
+    assert dtype == F32 or gdn.lib().gdn_ssm_chunk_fwd_workspace_size(len(lengths), T, H, G, P, N, 1) > 0
     out = torch.full((T, H, P), 7.0, dtype=dtype, device="cuda")
     got, last = gdn.gdn_ssm_chunk_fwd(**s, cu_seqlens=cu(offs), initial_state=S0, out=out)
     (ref, ref_last), (terms, terms_last) = scan_reference(s, offs, S0)
@@ -237,6 +238,17 @@ def test_scan_in_segments(lengths, tail, H, G, P, N, dtype, carried, extra, firs
         keep = dlast.clone()
         for a, b in zip(grads, gdn.gdn_ssm_chunk_bwd(dout, **s, **args, dfinal_state=keep, dinitial_state=keep)):
             assert a is None or torch.equal(a, b)
+
+
+def test_scan_in_segments_of_packed_prompts_that_differ():
+    """More blocks than SMs, and one sequence that outlasts the others."""
+    lengths, H, P, N = [1, 37, 513, 2901, 0, 1333, 700], 24, 64, 64
+    assert gdn.lib().gdn_ssm_chunk_fwd_workspace_size(len(lengths), sum(lengths), H, 1, P, N, 1) > 0
+    offs, T, s, S0, _ = scan_inputs(lengths, 0, H, 1, P, N, BF, True, True, seed=57)
+    got, last = gdn.gdn_ssm_chunk_fwd(**s, cu_seqlens=cu(offs), initial_state=S0)
+    (ref, ref_last), (terms, terms_last) = scan_reference(s, offs, S0)
+    check("out", got, ref, terms)
+    check("state", last, ref_last, terms_last)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
