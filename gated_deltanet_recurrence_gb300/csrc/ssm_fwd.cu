@@ -216,16 +216,17 @@ __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, Segme
 
 // ---- outputs -------------------------------------------------------------------------------------
 
-// Block: 4 warps of 16 tokens each.
-constexpr int kOutThreads = 128;
+// Block: a chunk and a share of one group's (head, 64 rows of its state); C B^T is formed once for them.  16 warps of 16
+// tokens and 16 columns each.  What the next head brings is loaded beside the products of this one.
+constexpr int kOutThreads = 512;
 template <int N>
 constexpr int kOutSmem = 2 * bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3> + bfp::kTileBytes<64, N, 3>;
 template <int N>
-__global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w) {
+__global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w, int shares) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const bfp::Tile<kC, N, 3> Kt{base}, Ct{base + bfp::kTileBytes<kC, N, 3>};
-    const bfp::Tile<kC, 64, 3> Xt{base + 2 * bfp::kTileBytes<kC, N, 3>};
+    const bfp::Tile<kC, 64, 3> Xt{base + 2 * bfp::kTileBytes<kC, N, 3>}, Mt{base};  // the masked products take B's place
     const bfp::Tile<64, N, 3> St{base + 2 * bfp::kTileBytes<kC, N, 3> + bfp::kTileBytes<kC, 64, 3>};
     __shared__ float gate[kGateRows][kC];
     Chunk c;
@@ -233,92 +234,91 @@ __global__ void __launch_bounds__(kOutThreads) ssm_out_kernel(SsmArgs a, Work w)
         dependency_wait();
         return;
     }
-    const int slices = a.P / 64, s = blockIdx.y % slices, h = blockIdx.y / slices, g = h / (a.H / a.G);
-    const int tid = threadIdx.x, lane = tid & 31, m = (tid >> 5) * 16;
-    const float* X = static_cast<const float*>(a.x) + (long)c.t0 * a.x_stride + (long)h * a.P + s * 64;
-    const float* B = static_cast<const float*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
-    const float* C = static_cast<const float*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
-    const float* S0 = w.states + (((long)blockIdx.x * a.H + h) * a.P + s * 64) * N;
-    const float* gt = w.gates + ((long)blockIdx.x * a.H + h) * (kGateRows * kC);
-#pragma unroll 4
-    for (int v = tid; v < kC * N / 8; v += kOutThreads) {
-        const int r = v / (N / 8), col = v % (N / 8) * 8;
-        bfp::Raw8 k, q;
-        k.load(B + (long)r * a.B_stride + col, r < c.len);
-        q.load(C + (long)r * a.C_stride + col, r < c.len);
-        k.put(Kt, r, col);
-        q.put(Ct, r, col);
-    }
-#pragma unroll 4
-    for (int v = tid; v < kC * 8; v += kOutThreads) {
-        bfp::Raw8 x;
-        x.load(X + (long)(v / 8) * a.x_stride + v % 8 * 8, v / 8 < c.len);
-        x.put(Xt, v / 8, v % 8 * 8);
-    }
-    dependency_wait();  // gates and states
-    for (int i = tid; i < kGateRows * kC; i += kOutThreads) (&gate[0][0])[i] = gt[i];
-#pragma unroll 4
-    for (int v = tid; v < 64 * N / 8; v += kOutThreads) {
-        const int r = v / (N / 8), col = v % (N / 8) * 8;
-        float x[8];
-        load_row<8>(S0 + (long)r * N + col, x);
-        bfp::put8(St, r, col, x);
+    const int tid = threadIdx.x, lane = tid & 31, m = (tid >> 5 & 3) * 16, p0 = (tid >> 7) * 16;
+    const int slices = a.P / 64, g = blockIdx.y % a.G, share = blockIdx.y / a.G, units = a.H / a.G * slices;
+    const int u0 = (int)((long)units * share / shares), u1 = (int)((long)units * (share + 1) / shares);
+    {
+        const float* B = static_cast<const float*>(a.B) + (long)c.t0 * a.B_stride + (long)g * N;
+        const float* C = static_cast<const float*>(a.C) + (long)c.t0 * a.C_stride + (long)g * N;
+#pragma unroll
+        for (int v = tid; v < kC * N / 8; v += kOutThreads) {
+            const int r = v / (N / 8), col = v % (N / 8) * 8;
+            bfp::Raw8 k, q;
+            k.load(B + (long)r * a.B_stride + col, r < c.len);
+            q.load(C + (long)r * a.C_stride + col, r < c.len);
+            k.put(Kt, r, col);
+            q.put(Ct, r, col);
+        }
     }
     __syncthreads();
-    float M[8][4], Y[8][4];
-    bfp::clear(M);
-    bfp::clear(Y);
-    bfp::product<N, false, false>(M, Ct, m, Kt, 0, lane);
-    bfp::product<N, false, false>(Y, Ct, m, St, 0, lane);
-    bfp::pairs<8>(m, 0, lane, [&](int j, int hh, int i, int col) {
-        Y[j][2 * hh] *= gate[3][i];
-        Y[j][2 * hh + 1] *= gate[3][i];
+    float CB[2][4];
+    bfp::clear(CB);
+    if (p0 <= m) bfp::product<N, false, false>(CB, Ct, m, Kt, p0, lane);
+    constexpr int NV = N / 64;  // vectors of a state that a thread loads
+    bfp::Raw8 xr, sr[NV];
+    float gr = 0.f;
+    const auto fetch = [&](int u) {
+        const int h = g * (a.H / a.G) + u / slices, s = u % slices;
+        const float* X = static_cast<const float*>(a.x) + (long)c.t0 * a.x_stride + (long)h * a.P + s * 64;
+        xr.load(X + (long)(tid / 8) * a.x_stride + tid % 8 * 8, tid / 8 < c.len);
+        const float* S0 = w.states + (((long)blockIdx.x * a.H + h) * a.P + s * 64) * N;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = col + e;
-            const float d = (gate[1][i] - gate[1][t]) + (gate[2][i] - gate[2][t]);
-            M[j][2 * hh + e] = t <= i ? M[j][2 * hh + e] * gate[0][t] * expf(d) : 0.f;
+        for (int i = 0; i < NV; ++i) sr[i].load(S0 + (long)(i * kOutThreads + tid) * 8, true);
+        if (tid < kGateRows * kC) gr = w.gates[((long)blockIdx.x * a.H + h) * (kGateRows * kC) + tid];
+    };
+    dependency_wait();  // gates and states
+    if (u0 < u1) fetch(u0);
+    for (int u = u0; u < u1; ++u) {
+        __syncthreads();  // what was in the tiles has been read
+        xr.put(Xt, tid / 8, tid % 8 * 8);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * kOutThreads + tid;
+            sr[i].put(St, v / (N / 8), v % (N / 8) * 8);
         }
-    });
-    // the masked products are the left operand of the product with x, from the registers they are in
-    const uint32_t lb = bfp::lane_b<true>(Xt, lane);
+        if (tid < kGateRows * kC) (&gate[0][0])[tid] = gr;
+        __syncthreads();
+        const int h = g * (a.H / a.G) + u / slices, s = u % slices;
+        if (p0 <= m)
+            bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int col) {
+                float v[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (16 * k > m) continue;
-        uint32_t f[3][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t u[3];
-            bfp::split<3>(M[2 * k + (e >> 1)][2 * (e & 1)], M[2 * k + (e >> 1)][2 * (e & 1) + 1], u);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) f[p][e] = u[p];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint32_t b[3][4];
-            bfp::load_b<true, 0, kC * 128>(b[0], lb, 8 * j, 16 * k);
-            bfp::load_b<true, kC * 128, kC * 128>(b[1], lb, 8 * j, 16 * k);
-            bfp::load_b<true, 2 * kC * 128, kC * 128>(b[2], lb, 8 * j, 16 * k);
-            bfp::terms<3, 3>(Y[j], f, b, 0);
-            bfp::terms<3, 3>(Y[j + 1], f, b, 1);
-        }
+                for (int e = 0; e < 2; ++e) {
+                    const int t = col + e;
+                    const float d = (gate[1][i] - gate[1][t]) + (gate[2][i] - gate[2][t]);
+                    v[e] = t <= i ? CB[j][2 * hh + e] * gate[0][t] * expf(d) : 0.f;
+                }
+                bfp::put2(Mt, i, col, v[0], v[1]);
+            });
+        if (u + 1 < u1) fetch(u + 1);
+        float Y[2][4];
+        bfp::clear(Y);
+        bfp::product<N, false, false>(Y, Ct, m, St, p0, lane);
+        bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int) {
+            Y[j][2 * hh] *= gate[3][i];
+            Y[j][2 * hh + 1] *= gate[3][i];
+        });
+        __syncthreads();
+        bfp::product<kC, false, true, bfp::kLower>(Y, Mt, m, Xt, p0, lane);
+        const float D = a.D ? a.D[h] : 0.f;
+        float* out = static_cast<float*>(a.out) + ((long)c.t0 * a.H + h) * a.P + s * 64;
+        bfp::pairs<2>(m, p0, lane, [&](int j, int hh, int i, int col) {
+            if (i >= c.len) return;
+            const float2 x = bfp::get2(Xt, i, col);
+            const float y0 = fmaf(D, x.x, Y[j][2 * hh]), y1 = fmaf(D, x.y, Y[j][2 * hh + 1]);
+            *reinterpret_cast<float2*>(out + (long)i * a.H * a.P + col) = make_float2(y0, y1);
+        });
     }
-    const float D = a.D ? a.D[h] : 0.f;
-    float* out = static_cast<float*>(a.out) + ((long)c.t0 * a.H + h) * a.P + s * 64;
-    bfp::pairs<8>(m, 0, lane, [&](int j, int hh, int i, int col) {
-        if (i >= c.len) return;
-        const float2 x = bfp::get2(Xt, i, col);
-        const float y0 = fmaf(D, x.x, Y[j][2 * hh]), y1 = fmaf(D, x.y, Y[j][2 * hh + 1]);
-        *reinterpret_cast<float2*>(out + (long)i * a.H * a.P + col) = make_float2(y0, y1);
-    });
 }
 
 template <int N>
 cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(ssm_out_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem<N>);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)slots_of(a.seqs.num_seqs, a.seqs.total_T), (unsigned)(a.H * (a.P / 64)));
-    return launch_after(ssm_out_kernel<N>, grid, kOutThreads, kOutSmem<N>, s, a, w);
+    // enough shares for a few rounds of blocks: each brings B and C again
+    const long slots = slots_of(a.seqs.num_seqs, a.seqs.total_T), blocks = slots * a.G, units = (long)(a.H / a.G) * (a.P / 64);
+    const long fill = (3 * 152 + blocks - 1) / blocks, shares = fill < units ? fill : units;
+    return launch_after(ssm_out_kernel<N>, dim3((unsigned)slots, (unsigned)(a.G * shares)), kOutThreads, kOutSmem<N>, s, a, w, (int)shares);
 }
 
 }  // namespace
