@@ -7,10 +7,12 @@
 // with cos_i, sin_i of the token's position from a table; the other channels pass.  Gradients: the rotation
 // backwards, then dw = sum dm n, dn = dm w, dx = r (dn - n mean(dn n)) (or the sum's, for length one).
 //
-// Bound by memory.  A row (one head of one token) is d / 8 lanes of 8 channels; a set of lanes takes one token
-// and several heads, so that the token's cosines and sines and the weights are loaded once.  Pairs of channels
-// m = d_rot / 2 apart are exchanged by shuffles where they lie in the same place of another lane (m a multiple
-// of 8), through shared memory otherwise.
+// Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 17.5 us, 4.9 TB/s (72% of a copy's rate), with
+// 58% of the issue slots taken and three blocks an SM for their registers; gradients of 3001 tokens of 16 + 16 heads of
+// 64 9.3 us with the launch behind.  Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one
+// head of one token) is d / 8 lanes of 8 channels; a set of lanes takes one token and several heads, so that the token's
+// cosines and sines and the weights are loaded once.  Pairs of channels m = d_rot / 2 apart are exchanged by shuffles
+// where they lie in the same place of another lane (m a multiple of 8), through shared memory otherwise.
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -28,9 +30,10 @@ int lanes_of(int d) {
     return l;
 }
 
-// Heads a set of lanes takes: all of a token's when there are tokens enough for a block an SM, fewer in small calls.  In us,
-// with sets for half a block, one, two, four and eight blocks an SM: 8192 tokens of 16 + 4 heads of 128 (bf16) 18.2, 18.3, 18.3,
-// 19.6, 23.8; 3001 of 16 + 16 of 64: 9.6, 7.6, 6.8, 8.4, 11.7; 1000 of 8 + 8 of 256: 8.0, 6.7, 8.4, 11.3, 16.6.
+// Heads a set of lanes takes: all of a token's when there are tokens enough for a block an SM, fewer in small calls.  In
+// us, with sets for half a block, one, two, four and eight blocks an SM: 8192 tokens of 16 + 4 heads of 128 (bf16) 18.2,
+// 18.3, 18.3, 19.6, 23.8; 3001 of 16 + 16 of 64: 9.6, 7.6, 6.8, 8.4, 11.7; 1000 of 8 + 8 of 256: 8.0, 6.7, 8.4, 11.3,
+// 16.6.
 int heads_per_set(int T, int heads, int L) {
     const long sets = (long)kSMs * (kThreads / L);
     int per = heads;

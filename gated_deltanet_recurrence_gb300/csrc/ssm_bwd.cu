@@ -14,7 +14,10 @@
 //   dA_log = sum dg g,  ddt_bias = sum da,  dD = sum dy . x.
 // The states and their gradients come from the scan kernels of the forward pass, run in both directions.  The
 // gradient kernel's block takes one chunk and a subset of the heads of one group, so that C B^T is formed once and
-// dB, dC of the group's heads are summed before they are written.
+// dB, dC of the group's heads are summed before they are written.  This is the fp32 form (bf16: ssm_tc_bwd.cu), on three
+// planes a factor; a head's step is a chain of seven products with barriers between them, and its latency bounds short
+// batches (493 tokens of six heads: 58 us, the gradients 36 of them), the tensor instructions and the splits long ones
+// (6144 tokens of 24 heads, d_state 128, in three sequences: 485 us).
 #include "ssm_chunk.cuh"
 
 namespace gdn {
@@ -400,8 +403,8 @@ cudaError_t grad_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
 }
 
 // Subsets of a group's heads: blocks for two rounds, at least two heads a block where the group has them (each subset
-// writes its dB and dC in fp32 for another kernel to add).  For one, two, three rounds: 2048 tokens of 16 heads 202, 155, 155
-// us; 6144 of 24 in three sequences 583, 485, 509.
+// writes its dB and dC in fp32 for another kernel to add).  For one, two, three rounds: 2048 tokens of 16 heads 202, 155,
+// 155 us; 6144 of 24 in three sequences 583, 485, 509.
 int subsets_of(int num_seqs, int total_T, int H, int G) {
     const long blocks = slots_of(num_seqs, total_T) * G, per = H / G;
     long n = (2 * 152 + blocks - 1) / blocks;

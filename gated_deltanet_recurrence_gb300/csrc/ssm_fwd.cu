@@ -3,8 +3,17 @@
 // Per head, with v_t = dt_t x_t and G the running sums of the log decays g_t = -exp(A_log) dt_t inside a chunk,
 //   y_i = e^{G_i} S_0 C_i + sum_{j <= i} e^{G_i - G_j} (B_j . C_i) v_j + D x_i,
 //   S_1 = e^{G_last} S_0 + sum_j e^{G_last - G_j} v_j B_j^T.
-// Three kernels: the gates of all chunks; the states at the chunk starts, one block per (sequence, head, 64 rows)
-// that walks along its chunks with the state in registers; the outputs, one block per (chunk, head, 64 rows).
+// Fp32 inputs (bf16: ssm_tc.cu).  Three kernels: the gates of all chunks; the states at the chunk starts, one block per
+// (sequence or segment of it, head, 64 rows) that walks along its chunks with the state in registers; the outputs, one
+// block per chunk and share of a group's heads.  All products are fp32 matrices in three bf16 planes, six terms each: the
+// tensor instructions and the splits into planes bound the outputs (6144 tokens of 24 heads of 128, d_state 128: 431 us),
+// a chunk's latency the walk (3.3 us, d_state 64: 2.1).  A block of four warps for each (chunk, head) took 629 us.
+// Smallest calls: 200 tokens of two heads 16 us, three launches that start behind one another.
+//
+// Long sequences of few heads are cut into segments of `each` chunks: all segments' own states (from zero) at once, then
+//   start_{k + 1} = e^{sum of segment k} start_k + own_k
+// for all numbers of a state at once, then the walk itself from the segments' starts: the walk's work twice, spread over
+// all SMs.  6144 tokens of 8 heads, d_state 128: 403 us whole, 103 in segments.
 #include "ssm_chunk.cuh"
 
 namespace gdn {
@@ -176,7 +185,8 @@ cudaError_t scan_one(const SsmArgs& a, const Work& w, bool own, int directions, 
 
 // ---- segments ------------------------------------------------------------------------------------
 
-// One thread: four numbers of the states of a (sequence, head), in one direction, along its segments.
+// One thread: four numbers of the states of a (sequence, head), in one direction, along its segments; loads of four
+// segments at a time.  About 3 us.
 constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads) ssm_join_kernel(SsmArgs a, Segments g) {
     const int n = blockIdx.z, back = blockIdx.y / a.H, h = blockIdx.y % a.H, unit = g.each * g.unit;
@@ -315,8 +325,8 @@ template <int N>
 cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(ssm_out_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOutSmem<N>);
     if (e != cudaSuccess) return e;
-    // shares for two rounds of blocks: each brings B and C again (for one, two, three rounds: 2048 tokens of 16 heads 80, 70,
-    // 78 us; 6144 of 24 in three sequences 251, 224, 232)
+    // shares for two rounds of blocks: each brings B and C again (for one, two, three rounds: 2048 tokens of 16 heads 80,
+    // 70, 78 us; 6144 of 24 in three sequences 251, 224, 232)
     const long slots = slots_of(a.seqs.num_seqs, a.seqs.total_T), blocks = slots * a.G, units = (long)(a.H / a.G) * (a.P / 64);
     const long fill = (2 * 152 + blocks - 1) / blocks, shares = fill < units ? fill : units;
     return launch_after(ssm_out_kernel<N>, dim3((unsigned)slots, (unsigned)(a.G * shares)), kOutThreads, kOutSmem<N>, s, a, w, (int)shares);
@@ -349,7 +359,10 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStr
 
 // Chunks of a segment, or 0.  Blocks are counted against 152 SMs.  Few rows: as many segments as fill the SMs, where that
 // pays for sequences of one length.  A packed batch of up to two rounds of blocks, forwards: segments a little longer
-// than the average, where it pays if the longest of n sequences is 1 + 1/2 + ... + 1/n times the average.
+// than the average, where it pays if the longest of n sequences is 1 + 1/2 + ... + 1/n times the average. In us, whole
+// and in segments, bf16, d_state 128, 64 rows a head: 1536 tokens of 8 heads 36, 27; 6144 of 8 128, 30; 6144 of 24 129,
+// 48; 32768 of 16 657, 136; 8192 in 4 sequences of 16 heads 47, 56 (stays whole).  Packed: lengths 1, 37, 513, 3001, 64,
+// 1333, 700 of 24 rows 71, 60 (seven of 807: 47, 52); 8000, 3 x 2000, 4 x 500 of 24 170, 118 (eight of 2048: 95, 105).
 static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int directions, bool varied, SegmentCost cost) {
     const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
                avg = (chunks + num_seqs - 1) / num_seqs;

@@ -1,8 +1,16 @@
 // ssm_tc_bwd.cu -- the gradients of the selective scan of bf16 prompts on the tensor cores (tcgen05).
 //
-// The formulas are those of ssm_bwd.cu, with chunks of 128 tokens.  Three kernels: the gates of all chunks; the states
-// at the chunks' starts and their gradients at the chunks' ends (one block per sequence, head, 64 rows and direction
-// walks along the chunks); the gradients, one block per chunk and subset of a group's heads.
+// The formulas are those of ssm_bwd.cu, with chunks of 128 tokens.  The gates of all chunks and the states at the chunks'
+// starts, with their gradients at the chunks' ends, come from ssm_tc_scan.cu; here the gradients, one block per chunk and
+// subset of a group's heads.
+//
+// A head's step is a chain of phases, about 19000 cycles, one block an SM for its tiles: planes of dS (2100), products
+// with it (2200), their results (1000 - 2400), planes of S_0 and dy . x (1500), masks and planes of M (4000), products
+// with those (2100), dx and dC (2500); the tensor pipe is busy 13% of it.  All of a chunk is on the way through
+// registers, whose 64,000 the accumulators of dB, dC and E fill, so that steps do not overlap.  Tried, and no faster: 256
+// threads, rolled loops for the masks (260 us for 255 of the call below), tiles of both states at once with their
+// conversion beside the products (254). Two sequences of 4096 tokens, 32 heads of 64 in two groups, d_state 128: 170 us
+// of the call's 235 (with states 54, gates 4, sums 4; kernels on mma.sync took 735).
 //
 // Every fp32 factor is three bf16 planes, exact beside the bf16 inputs; where a factor's planes lie side by side, the
 // input is read once for all of them.  All matrices of pairs of tokens are held with row j (the earlier token) and
@@ -639,8 +647,8 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
 }
 
 // Subsets of a group's heads: more blocks fill more SMs, but each loads B and C, ends with two products of its own, and
-// writes dB and dC in fp32 for another kernel to add.  Counted in steps of a head.  In us, for 1, 2, 4 and 8 subsets
-// and the choice made here: 8192 tokens of 32 heads in two groups 233, 262, 302, 348, 233; 2048 of 32 in one 341, 197, 126,
+// writes dB and dC in fp32 for another kernel to add.  Counted in steps of a head.  In us, for 1, 2, 4 and 8 subsets and
+// the choice made here: 8192 tokens of 32 heads in two groups 233, 262, 302, 348, 233; 2048 of 32 in one 341, 197, 126,
 // 94, 94; 1024 of 16 180, 111, 74, 56, 50; 4096 of 64 684, 387, 237, 260, 237.
 int subsets_of(int num_seqs, int total_T, int H, int G, int N) {
     const long blocks = slots128(num_seqs, total_T) * G, per = H / G;

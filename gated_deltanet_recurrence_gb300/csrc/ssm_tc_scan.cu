@@ -1,12 +1,11 @@
-// ssm_tc_scan.cu -- what lies between the chunks of 128 tokens of a bf16 scan: gates, states, and segments of long sequences.
+// ssm_tc_scan.cu -- what lies between the chunks of 128 tokens of a bf16 scan: gates, states, and segments of long
+// sequences.
 //
 // The states along a sequence, and their gradients backwards, are one product a chunk (U = B^T V, or C^T (b dy)) and
 //   S <- e^{G_last} S + U.
-// A walk along a sequence takes a block about 1.8 us a chunk (3.1 us with the outputs), whatever else is idle, so a long
-// sequence of few heads is cut into segments of `each` chunks: all segments' own states S_own (from zero) at once, then
-//   start_{k + 1} = e^{sum of segment k} start_k + own_k
-// for all numbers of a state at once, then the walk itself from the segments' starts.  That is 1.6 times the work of the
-// forward pass (twice that of the states), spread over all SMs.
+// A walk along a sequence takes a block 1.7 us a chunk, the latency of its phases (tensor pipe 20%, issue slots 44%); two
+// sequences of 4096 tokens, 32 heads of 64, d_state 128, in both directions: 54 us with 134 MB of images written, 2.5
+// TB/s.  Both directions in one launch take as long as one.  Segments: see ssm_fwd.cu.
 #include "ssm_tc.cuh"
 
 namespace gdn {

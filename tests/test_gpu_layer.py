@@ -238,6 +238,17 @@ def test_scan_in_segments(lengths, tail, H, G, P, N, dtype, carried, extra, firs
         keep = dlast.clone()
         for a, b in zip(grads, gdn.gdn_ssm_chunk_bwd(dout, **s, **args, dfinal_state=keep, dinitial_state=keep)):
             assert a is None or torch.equal(a, b)
+    # a workspace of just the size, of NaN, with a guard behind it
+    L, sizes = gdn.lib(), (len(lengths), T, H, G, P, N, int(dtype == BF))
+    for need, call in ((L.gdn_ssm_chunk_fwd_workspace_size(*sizes), lambda ws: gdn.gdn_ssm_chunk_fwd(**s, **args, workspace=ws)),
+                       (L.gdn_ssm_chunk_bwd_workspace_size(*sizes),
+                        lambda ws: gdn.gdn_ssm_chunk_bwd(dout, **s, **args, dfinal_state=dlast, workspace=ws))):
+        ws = torch.full((need + 1024,), 255, dtype=torch.uint8, device="cuda")
+        results = call(ws[:need])
+        assert bool((ws[need:] == 255).all())
+        for a, b in zip(results, (got, last) if len(results) == 2 else grads):
+            rows = slice(first, offs[-1]) if a is not None and a.shape[0] == T else slice(None)
+            assert a is None or torch.equal(a[rows], b[rows])
 
 
 def test_scan_in_segments_of_packed_prompts_that_differ():
