@@ -22,9 +22,8 @@
 //
 // What bounds it is a chunk's chain of phases: 2.7 us whatever the number of blocks (shared memory about 3900 of a
 // chunk's 5200 cycles, the tensor pipe 34%, issue slots 54%).  Two sequences of 4096 tokens, 64 heads of 64, d_state 128:
-// 90 us, 1.6 TB/s, 190 TFLOP/s of the recurrence in chunks; 32768 tokens of 16 heads in segments (ssm_fwd.cu) 136 us.  As
-// three kernels with chunks of 64 on mma.sync, as the fp32 form, the first of these took 360 us; chunks of 64 on tcgen05
-// 202.
+// 90 us, 1.6 TB/s, 190 TFLOP/s of the recurrence in chunks; 32768 tokens of 16 heads in segments (ssm_fwd.cu) 136 us.  Three
+// kernels on mma.sync with chunks of 64, as for fp32, took 360 us.
 //
 // Every mbarrier wait is bounded; when one runs out the kernel records GDN_ERR_TIMEOUT, every role leaves its loop,
 // copies and MMAs in flight are waited for (bounded), TMEM is freed.
