@@ -26,6 +26,9 @@ using planes::lane_b;
 using planes::load_a;
 using planes::load_b;
 using planes::Mat;
+using gdn::F2;
+using gdn::fma2;
+using gdn::widen;
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -34,36 +37,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two floats in one 64-bit register: additions, products and sums of both at once.
-struct F2 {
-    unsigned long long v;
-    __device__ __forceinline__ F2() {}
-    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-    __device__ __forceinline__ static F2 of(uint32_t x, uint32_t y) { return F2(__uint_as_float(x), __uint_as_float(y)); }
-    __device__ __forceinline__ void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-};
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ uint32_t pack(F2 a) {
     float x, y;
     a.get(x, y);
     return pack_bf16(x, y);
 }
-// The two values of a bf16 pair.
-__device__ __forceinline__ F2 widen(uint32_t u) { return F2::of(u << 16, u & 0xffff0000u); }
 // The next plane of a pair, and what is left of the pair.
 __device__ __forceinline__ uint32_t peel(F2& a) {
     const uint32_t u = pack(a);

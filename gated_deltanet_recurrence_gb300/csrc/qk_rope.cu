@@ -7,12 +7,13 @@
 // with cos_i, sin_i of the token's position from a table; the other channels pass.  Gradients: the rotation
 // backwards, then dw = sum dm n, dn = dm w, dx = r (dn - n mean(dn n)) (or the sum's, for length one).
 //
-// Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 17.5 us, 4.9 TB/s (72% of a copy's rate), with
-// 58% of the issue slots taken and three blocks an SM for their registers; gradients of 3001 tokens of 16 + 16 heads of
-// 64 9.3 us with the launch behind.  Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one
-// head of one token) is d / 8 lanes of 8 channels; a set of lanes takes one token and several heads, so that the token's
-// cosines and sines and the weights are loaded once.  Pairs of channels m = d_rot / 2 apart are exchanged by shuffles
-// where they lie in the same place of another lane (m a multiple of 8), through shared memory otherwise.
+// Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 17.0 us, 5.1 TB/s (75% of a copy's rate),
+// gradients of 3001 tokens of 16 + 16 heads of 64 9.3 us with the launch behind.  What is left are instructions: 58% of
+// the issue slots before arithmetic went in pairs of channels (17.5 us).  Two blocks an SM with all values in registers;
+// three, with spills, 17.8. Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one head of one
+// token) is d / 8 lanes of 8 channels; a set of lanes takes one token and several heads, so that the token's cosines and
+// sines and the weights are loaded once.  Pairs of channels m = d_rot / 2 apart are exchanged by shuffles where they lie
+// in the same place of another lane (m a multiple of 8), through shared memory otherwise.
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -22,6 +23,13 @@ constexpr int kThreads = 256;
 constexpr int kSMs = 152;
 constexpr int kV = 8;
 enum Pairs { kNeighbours, kLanes, kShared };
+// Rows worked on together, and groups of them on their way; the rings that hold them (of x; backwards of the gradient
+// too).
+template <bool BWD>
+constexpr int kTogether = BWD ? 2 : 4;
+constexpr int kAhead = 2;
+template <typename T, bool BWD>
+using Rows = Ring<T, kV, kTogether<BWD> * kAhead, kThreads>;
 
 // Lanes of a row: the power of two that holds d / 8 vectors.
 int lanes_of(int d) {
@@ -49,12 +57,17 @@ __device__ __forceinline__ float set_sum(float x) {
 }
 
 // One lane's eight channels x and their partners y, as they lie in memory (so that bf16 pairs move in one exchange).
+constexpr int kPairsOf = kV / 2;
 template <typename T, int L, Pairs PAIRS>
-__device__ __forceinline__ void partners(const RawRow<T, kV>& r, const float (&x)[kV], float (&y)[kV], int lane, int from, int m,
+__device__ __forceinline__ void partners(const RawRow<T, kV>& r, const F2 (&x)[kPairsOf], F2 (&y)[kPairsOf], int lane, int from, int m,
                                          float* row) {
     if constexpr (PAIRS == kNeighbours) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) y[j] = x[j ^ 1];
+        for (int j = 0; j < kPairsOf; ++j) {
+            float u, v;
+            x[j].get(u, v);
+            y[j] = F2(v, u);
+        }
     } else if constexpr (PAIRS == kLanes) {
         RawRow<T, kV> p;
 #pragma unroll
@@ -63,24 +76,30 @@ __device__ __forceinline__ void partners(const RawRow<T, kV>& r, const float (&x
     } else {
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kV; ++j) row[lane * kV + j] = x[j];
+        for (int j = 0; j < kPairsOf; ++j) x[j].get(row[lane * kV + 2 * j], row[lane * kV + 2 * j + 1]);
         __syncwarp();
+        float o[kV];
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = lane * kV + j;
-            y[j] = row[c < m ? c + m : (c < 2 * m ? c - m : c)];
+            o[j] = row[c < m ? c + m : (c < 2 * m ? c - m : c)];
         }
+        pair_up<kV>(o, y);
     }
+}
+__device__ __forceinline__ float sum_of(F2 x) {
+    float u, v;
+    x.get(u, v);
+    return u + v;
 }
 
 // One block: kThreads / L sets; a set: one token, `per` heads of the q and k heads taken together.  Sets are numbered
 // part by part, each part's tokens rounded up to whole warps, so that all sets of a warp have the same heads.
 template <typename T, int L, Pairs PAIRS, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int per, long tokens, long sets) {
-    constexpr int U = BWD ? 2 : 4, kGroups = 2;  // rows worked on together; groups of them on their way
-    using Rows = Ring<T, kV, U * kGroups, kThreads>;
+__global__ void __launch_bounds__(kThreads, 2) qk_kernel(QkArgs a, int per, long tokens, long sets) {
+    constexpr int U = kTogether<BWD>;
     extern __shared__ __align__(16) unsigned char smem[];
-    Rows rx(smem), rg(smem + (BWD ? Rows::kSmem : 0));
+    Rows<T, BWD> rx(smem), rg(smem + (BWD ? Rows<T, BWD>::kSmem : 0));
     __shared__ float stage[PAIRS == kShared ? kThreads * kV : 1];
     const int lane = threadIdx.x % L;
     const int c0 = lane * kV, d = a.d, m = a.rot / 2;
@@ -88,9 +107,9 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int
     const float inv = a.l2 ? 1.0f : 1.0f / (float)d;
     float* row = stage + (PAIRS == kShared ? threadIdx.x / L * L * kV : 0);
     const int off = m / kV, from = lane >= 2 * off ? lane : (lane < off ? lane + off : lane - off);
-    float dw[2][kV];
+    F2 dw[2][kPairsOf];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) dw[0][j] = dw[1][j] = 0.f;
+    for (int j = 0; j < kPairsOf; ++j) dw[0][j] = dw[1][j] = F2(0.f, 0.f);
     const long stride = (long)gridDim.x * (kThreads / L);
     for (long base = (long)blockIdx.x * (kThreads / L); base < sets; base += stride) {
         const long set = base + threadIdx.x / L;
@@ -131,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int
         }
         const bool on = live && in;
         if (!on) {  // a set without a row reads zeros, whatever an earlier one has left
-            for (int i = 0; i < U * kGroups; ++i) {
+            for (int i = 0; i < U * kAhead; ++i) {
                 rx.clear(i);
                 if (BWD) rg.clear(i);
             }
@@ -143,20 +162,22 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int
             const int h0 = i ? max(lo - a.heads[0], 0) : lo, h1 = i ? hi - a.heads[0] : min(hi, a.heads[0]);
             if (h0 >= h1) continue;
             // forward: the weights go into the rotation's factors, w of the channel and of its partner
-            float w[kV], wc[kV], ws[kV];
+            F2 w[kPairsOf], fc[kPairsOf], fs[kPairsOf];
             {
+                float own[kV], wc[kV], ws[kV];
 #pragma unroll
-                for (int j = 0; j < kV; ++j) w[j] = 1.f;
-                if (in && a.w[i]) load_row<kV>(a.w[i] + c0, w);
-                if constexpr (!BWD) {
+                for (int j = 0; j < kV; ++j) own[j] = 1.f;
+                if (in && a.w[i]) load_row<kV>(a.w[i] + c0, own);
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) {
-                        const int c = c0 + j;
-                        const int other = PAIRS == kNeighbours ? c ^ 1 : (c < m ? c + m : (c < 2 * m ? c - m : c));
-                        wc[j] = w[j] * cs[j];
-                        ws[j] = in && a.w[i] ? a.w[i][other] * sn[j] : sn[j];
-                    }
+                for (int j = 0; j < kV; ++j) {
+                    const int c = c0 + j;
+                    const int other = PAIRS == kNeighbours ? c ^ 1 : (c < m ? c + m : (c < 2 * m ? c - m : c));
+                    wc[j] = BWD ? cs[j] : own[j] * cs[j];
+                    ws[j] = !BWD && in && a.w[i] ? a.w[i][other] * sn[j] : sn[j];
                 }
+                pair_up<kV>(own, w);
+                pair_up<kV>(wc, fc);
+                pair_up<kV>(ws, fs);
             }
             const T* src = static_cast<const T*>(a.x[i]) + t * a.x_stride[i] + h0 * d + c0;
             const T* grad = BWD ? static_cast<const T*>(a.dout[i]) + (t * a.heads[i] + h0) * d + c0 : nullptr;
@@ -177,49 +198,48 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int
                 if (BWD) grad += U * d;
             };
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) ask(q);
+            for (int q = 0; q < kAhead; ++q) ask(q);
             int group = 0;
             for (int h = h0; h < h1; h += U) {
                 RawRow<T, kV> xr[U], gr[BWD ? U : 1];
-                ring_wait<kGroups - 1>();
+                ring_wait<kAhead - 1>();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     rx.read(U * group + u, xr[u]);
                     if constexpr (BWD) rg.read(U * group + u, gr[u]);
                 }
                 ask(group);
-                group ^= 1;
+                group = group + 1 == kAhead ? 0 : group + 1;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h + u >= h1) break;
-                    float x[kV], y[kV];
+                    F2 x[kPairsOf], y[kPairsOf], s2(0.f, 0.f);
                     xr[u].get(x);
-                    float ss = 0.f;
 #pragma unroll
-                    for (int j = 0; j < kV; ++j) ss = fmaf(x[j], x[j], ss);
-                    const float r = rsqrtf(set_sum<L>(ss) * inv + a.eps);
+                    for (int j = 0; j < kPairsOf; ++j) s2 = fma2(x[j], x[j], s2);
+                    const float r = rsqrtf(set_sum<L>(sum_of(s2)) * inv + a.eps);
+                    const F2 r2(r, r);
                     if constexpr (!BWD) {
                         partners<T, L, PAIRS>(xr[u], x, y, lane, from, m, row);
 #pragma unroll
-                        for (int j = 0; j < kV; ++j) x[j] = r * fmaf(y[j], ws[j], x[j] * wc[j]);
-                        if (on) store_row<kV>(out + u * d, x);
+                        for (int j = 0; j < kPairsOf; ++j) x[j] = r2 * fma2(y[j], fs[j], x[j] * fc[j]);
+                        if (on) store_pairs<kV>(out + u * d, x);
                     } else {
-                        float g[kV];
+                        F2 g[kPairsOf], d2(0.f, 0.f);
                         gr[u].get(g);
                         partners<T, L, PAIRS>(gr[u], g, y, lane, from, m, row);
-                        float dot = 0.f;
 #pragma unroll
-                        for (int j = 0; j < kV; ++j) {
-                            g[j] = fmaf(y[j], sn[j], g[j] * cs[j]);
-                            x[j] *= r;
-                            dw[i][j] = fmaf(g[j], x[j], dw[i][j]);
-                            g[j] *= w[j];
-                            dot = fmaf(g[j], x[j], dot);
+                        for (int j = 0; j < kPairsOf; ++j) {
+                            g[j] = fma2(y[j], fs[j], g[j] * fc[j]);
+                            x[j] = x[j] * r2;
+                            dw[i][j] = fma2(g[j], x[j], dw[i][j]);
+                            g[j] = g[j] * w[j];
+                            d2 = fma2(g[j], x[j], d2);
                         }
-                        dot = set_sum<L>(dot) * inv;
+                        const float dot = -set_sum<L>(sum_of(d2)) * inv;
 #pragma unroll
-                        for (int j = 0; j < kV; ++j) g[j] = r * fmaf(-x[j], dot, g[j]);
-                        if (on) store_row<kV>(out + u * d, g);
+                        for (int j = 0; j < kPairsOf; ++j) g[j] = r2 * fma2(x[j], F2(dot, dot), g[j]);
+                        if (on) store_pairs<kV>(out + u * d, g);
                     }
                 }
                 out += U * d;
@@ -234,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3) qk_kernel(QkArgs a, int
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < kV; ++j) sums[threadIdx.x / L][i][c0 + j] = dw[i][j];
+            for (int j = 0; j < kPairsOf; ++j) dw[i][j].get(sums[threadIdx.x / L][i][c0 + 2 * j], sums[threadIdx.x / L][i][c0 + 2 * j + 1]);
         __syncthreads();
         for (int e = threadIdx.x; e < 2 * d; e += kThreads) {
             const int i = e >= d, c = i ? e - d : e;
@@ -267,7 +287,7 @@ cudaError_t launch_pairs(const QkArgs& a, const Plan& p, cudaStream_t s) {
     const auto kernel = a.interleaved ? qk_kernel<T, L, kNeighbours, BWD>
                         : (a.rot / 2) % kV == 0 ? qk_kernel<T, L, kLanes, BWD>
                                                 : qk_kernel<T, L, kShared, BWD>;
-    constexpr int smem = 8 * kV * (int)sizeof(T) * kThreads;  // the rings
+    constexpr int smem = (BWD ? 2 : 1) * Rows<T, BWD>::kSmem;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)p.blocks, kThreads, smem, s>>>(a, p.per, p.tokens, p.sets);

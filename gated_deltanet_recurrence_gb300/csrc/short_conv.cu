@@ -11,9 +11,10 @@
 // (64% and 61% of the slots, with the three blocks an SM that the registers leave room for).  So a thread asks for its
 // rows by asynchronous copies into a ring of its own in shared memory, four groups of four rows ahead, which takes
 // neither registers nor waits, has few channels (four forward, two backward: eight and four were slower, for their
-// registers), and takes its sigmoid from the hardware's exponential and reciprocal.  Measured, bf16: 8192 tokens of 4352
-// channels 32.5 us, 4.4 TB/s (65% of a copy's rate); gradients of 4132 tokens of 2304 channels 25 us, four of them the
-// sums behind, 2.3 TB/s; a token of five sequences of 384 channels 1.9 us.
+// registers), and takes its sigmoid from the hardware's exponential and reciprocal.  Gradients' arithmetic goes in pairs
+// of channels (8192 x 4352: 69 -> 66 us; forward that spilled, 33 -> 36).  Measured, bf16: 8192 tokens of 4352 channels
+// 32.5 us, 4.4 TB/s (65% of a copy's rate); gradients of 4132 tokens of 2304 channels 25 us, four of them the sums
+// behind, 2.4 TB/s; a token of five sequences of 384 channels 1.9 us.
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -26,8 +27,8 @@ constexpr int kVecB = 2;    // and in the backward pass, whose taps, windows and
 constexpr int kSMs = 152;
 constexpr int kGroups = 4;  // groups of four rows that a thread has on their way
 
-template <bool SILU>
-__device__ __forceinline__ float silu_or(float c) {
+template <bool SILU, class V>
+__device__ __forceinline__ V silu_or(V c) {
     return SILU ? c * sigmoid_hw(c) : c;
 }
 
@@ -51,6 +52,28 @@ __device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c0, float 
         load_vec<4>(a.w + (long)(c0 + j) * kTaps, w[j]);
         b[j] = a.bias ? a.bias[c0 + j] : 0.f;
     }
+}
+
+// A vector's taps and bias in pairs of channels.
+template <int VEC>
+__device__ __forceinline__ void load_taps(const ShortConvArgs& a, int c0, F2 (&w)[kTaps][VEC / 2], F2 (&b)[VEC / 2]) {
+    float x[VEC][kTaps], y[VEC];
+    load_taps<VEC>(a, c0, x, y);
+    pair_up<VEC>(y, b);
+#pragma unroll
+    for (int i = 0; i < kTaps; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) w[i][j] = F2(x[2 * j][i], x[2 * j + 1][i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void input_at(const ShortConvArgs& a, int n, int bos, int p, int c0, F2 (&x)[VEC / 2]) {
+    float y[VEC];
+    input_at<T, VEC>(a, n, bos, p, c0, y);
+    pair_up<VEC>(y, x);
+}
+// The sum of the taps' products with the inputs of four tokens, the newest first.
+__device__ __forceinline__ F2 taps(const F2& w0, const F2& w1, const F2& w2, const F2& w3, F2 b, F2 x, F2 h2, F2 h1, F2 h0) {
+    return fma2(w3, x, fma2(w2, h2, fma2(w1, h1, fma2(w0, h0, b))));
 }
 
 // The last three inputs of sequence n, for one vector of channels.
@@ -197,10 +220,10 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ShortConvArgs a) {
 
 // dc of one token: the slope of the SiLU at c, times dout.
 template <bool SILU>
-__device__ __forceinline__ float dc_of(float c, float d) {
+__device__ __forceinline__ F2 dc_of(F2 c, F2 d) {
     if (!SILU) return d;
-    const float sg = sigmoid_hw(c);
-    return d * sg * fmaf(c, 1.0f - sg, 1.0f);
+    const F2 sg = sigmoid_hw(c), one(1.f, 1.f);
+    return d * sg * fma2(c, fma2(sg, F2(-1.f, -1.f), one), one);
 }
 
 // A block is 32 channel vectors (of two) x 8 runs of tokens; the sums over its runs are added in order and go to
@@ -219,13 +242,14 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
     T* dx = static_cast<T*>(a.dx) + c0;
     const bool state_block = (int)blockIdx.x == rows;
     const int first = state_block ? 0 : (int)blockIdx.x * 8 * run;
-    float w[kVecB][kTaps], b[kVecB];
-    float dw[kVecB][kTaps], db[kVecB];
+    constexpr int kPairs = kVecB / 2;
+    F2 w[kTaps][kPairs], b[kPairs], dw[kTaps][kPairs], db[kPairs];
+    const F2 zero2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < kVecB; ++j) {
-        db[j] = 0.f;
+    for (int j = 0; j < kPairs; ++j) {
+        db[j] = zero2;
 #pragma unroll
-        for (int i = 0; i < kTaps; ++i) dw[j][i] = 0.f;
+        for (int i = 0; i < kTaps; ++i) dw[i][j] = zero2;
     }
     if (on) load_taps<kVecB>(a, c0, w, b);
     int n = packed_find(a.seqs, first, 1, 0, a.err);
@@ -233,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
         if (n == -2 || !on) return;
         for (int m = k; m < N; m += 8) {
             const int bos = a.seqs.bos(m), len = a.seqs.bos(m + 1) - bos;
-            float x[6][kVecB], g[3][kVecB];
+            F2 x[6][kPairs], g[3][kPairs];
 #pragma unroll
             for (int p = 0; p < 6; ++p) {
                 if (p - 3 < len) input_at<T, kVecB>(a, m, bos, p - 3, c0, x[p]);
@@ -241,24 +265,28 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
 #pragma unroll
             for (int p = 0; p < 3; ++p) {  // dc of the first three tokens
 #pragma unroll
-                for (int j = 0; j < kVecB; ++j) g[p][j] = 0.f;
+                for (int j = 0; j < kPairs; ++j) g[p][j] = zero2;
                 if (p >= len) continue;
-                float d[kVecB];
-                load_row<kVecB>(dout + (long)(bos + p) * a.dim, d);
+                float y[kVecB];
+                load_row<kVecB>(dout + (long)(bos + p) * a.dim, y);
+                F2 d[kPairs];
+                pair_up<kVecB>(y, d);
 #pragma unroll
-                for (int j = 0; j < kVecB; ++j) {
-                    const float c = fmaf(w[j][3], x[p + 3][j], fmaf(w[j][2], x[p + 2][j], fmaf(w[j][1], x[p + 1][j], fmaf(w[j][0], x[p][j], b[j]))));
-                    g[p][j] = dc_of<SILU>(c, d[j]);
-                }
+                for (int j = 0; j < kPairs; ++j)
+                    g[p][j] = dc_of<SILU>(taps(w[0][j], w[1][j], w[2][j], w[3][j], b[j], x[p + 3][j], x[p + 2][j], x[p + 1][j], x[p][j]), d[j]);
+            }
+            float two[3][kVecB];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                // position p - 3 meets token q through tap p - q (of the taps 0 .. 2)
+                (w[0][j] * g[0][j]).get(two[0][2 * j], two[0][2 * j + 1]);
+                fma2(w[0][j], g[1][j], w[1][j] * g[0][j]).get(two[1][2 * j], two[1][2 * j + 1]);
+                fma2(w[0][j], g[2][j], fma2(w[1][j], g[1][j], w[2][j] * g[0][j])).get(two[2][2 * j], two[2][2 * j + 1]);
             }
 #pragma unroll
             for (int j = 0; j < kVecB; ++j) {
                 const long at = ((long)m * a.dim + c0 + j) * 3;
-                float o[3];
-                // position p - 3 meets token q through tap p - q (of the taps 0 .. 2)
-                o[0] = w[j][0] * g[0][j];
-                o[1] = fmaf(w[j][0], g[1][j], w[j][1] * g[0][j]);
-                o[2] = fmaf(w[j][0], g[2][j], fmaf(w[j][1], g[1][j], w[j][2] * g[0][j]));
+                float o[3] = {two[0][j], two[1][j], two[2][j]};
                 float s[3] = {0.f, 0.f, 0.f};
                 if (a.dstate_out) {
 #pragma unroll
@@ -291,38 +319,38 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
         const int bos = a.seqs.bos(n), eos = a.seqs.bos(n + 1);
         if (t >= eos) { ++n; continue; }
         const int stop = min(end, eos);
-        float h[3][kVecB], g[3][kVecB];  // the inputs and the dc of the three tokens before
+        F2 h[3][kPairs], g[3][kPairs];  // the inputs and the dc of the three tokens before
         const int from = t;
         const long xs = a.x_stride, os = a.dim;
         const T* px = src + (long)t * xs;
         const T* pd = dout + (long)t * os;
         T* po = dx + (long)(t - 3) * os;
         // dc of a token of the run (its sums too, where `sums`), from its input and the three before it
-        const auto dc = [&](const float (&x)[kVecB], const float (&h2)[kVecB], const float (&h1)[kVecB], const float (&h0)[kVecB],
-                            const float (&d)[kVecB], bool sums, float (&gc)[kVecB]) {
+        const auto dc = [&](const F2 (&x)[kPairs], const F2 (&h2)[kPairs], const F2 (&h1)[kPairs], const F2 (&h0)[kPairs],
+                            const F2 (&d)[kPairs], bool sums, F2 (&gc)[kPairs]) {
 #pragma unroll
-            for (int j = 0; j < kVecB; ++j) {
-                const float c = fmaf(w[j][3], x[j], fmaf(w[j][2], h2[j], fmaf(w[j][1], h1[j], fmaf(w[j][0], h0[j], b[j]))));
-                gc[j] = dc_of<SILU>(c, d[j]);
+            for (int j = 0; j < kPairs; ++j) {
+                gc[j] = dc_of<SILU>(taps(w[0][j], w[1][j], w[2][j], w[3][j], b[j], x[j], h2[j], h1[j], h0[j]), d[j]);
                 if (sums) {
-                    dw[j][0] = fmaf(gc[j], h0[j], dw[j][0]);
-                    dw[j][1] = fmaf(gc[j], h1[j], dw[j][1]);
-                    dw[j][2] = fmaf(gc[j], h2[j], dw[j][2]);
-                    dw[j][3] = fmaf(gc[j], x[j], dw[j][3]);
-                    db[j] += gc[j];
+                    dw[0][j] = fma2(gc[j], h0[j], dw[0][j]);
+                    dw[1][j] = fma2(gc[j], h1[j], dw[1][j]);
+                    dw[2][j] = fma2(gc[j], h2[j], dw[2][j]);
+                    dw[3][j] = fma2(gc[j], x[j], dw[3][j]);
+                    db[j] = db[j] + gc[j];
                 }
             }
         };
         // the gradient that is complete with g3, the dc of three tokens later
-        const auto gradient = [&](const float (&g3)[kVecB], const float (&g2)[kVecB], const float (&g1)[kVecB], const float (&g0)[kVecB],
-                                  const float (&more)[kVecB], T* to) {
-            float o[kVecB];
+        const auto gradient = [&](const F2 (&g3)[kPairs], const F2 (&g2)[kPairs], const F2 (&g1)[kPairs], const F2 (&g0)[kPairs],
+                                  const F2 (&more)[kPairs], T* to) {
+            F2 o[kPairs];
 #pragma unroll
-            for (int j = 0; j < kVecB; ++j)
-                o[j] = fmaf(w[j][0], g3[j], fmaf(w[j][1], g2[j], fmaf(w[j][2], g1[j], fmaf(w[j][3], g0[j], more[j]))));
-            store_row<kVecB>(to, o);
+            for (int j = 0; j < kPairs; ++j) o[j] = taps(w[3][j], w[2][j], w[1][j], w[0][j], more[j], g3[j], g2[j], g1[j], g0[j]);
+            store_pairs<kVecB>(to, o);
         };
-        const float none[kVecB] = {};
+        F2 none[kPairs];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) none[j] = zero2;
         const int last = min(stop + 3, eos);
         int asked = t, group = 0;
         const auto ask = [&](int q) {
@@ -343,10 +371,10 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
         for (int j = 0; j < 3; ++j) {
             input_at<T, kVecB>(a, n, bos, t - bos - 3 + j, c0, h[j]);
 #pragma unroll
-            for (int i = 0; i < kVecB; ++i) g[j][i] = 0.f;
+            for (int i = 0; i < kPairs; ++i) g[j][i] = zero2;
         }
         for (; t + 4 <= stop; t += 4) {
-            float x[4][kVecB], d[4][kVecB], n4[4][kVecB];
+            F2 x[4][kPairs], d[4][kPairs], n4[4][kPairs];
             ring_wait<kGroups - 1>();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -367,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
             gradient(n4[3], n4[2], n4[1], n4[0], none, po + 3 * os);
             po += 4 * os;
 #pragma unroll
-            for (int j = 0; j < kVecB; ++j) {
+            for (int j = 0; j < kPairs; ++j) {
                 h[0][j] = x[1][j]; h[1][j] = x[2][j]; h[2][j] = x[3][j];
                 g[0][j] = n4[1][j]; g[1][j] = n4[2][j]; g[2][j] = n4[3][j];
             }
@@ -379,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
         for (int i = 0; i < 6; ++i) {
             if (i >= rest) break;
             const int u = t + i - 3;
-            float x[kVecB] = {}, d[kVecB], gc[kVecB] = {}, more[kVecB] = {};
+            F2 x[kPairs], d[kPairs], gc[kPairs], more[kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) x[j] = gc[j] = more[j] = zero2;
             if (i < live) {
                 const int slot = 4 * (i < 4 ? group : (group + 1 == kGroups ? 0 : group + 1)) + (i & 3);
                 rx.read(slot, x);
@@ -387,12 +417,14 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
                 dc(x, h[2], h[1], h[0], d, t + i < stop, gc);
             }
             if (a.dstate_out && u >= eos - 3 && u < eos) {
+                float y[kVecB];
 #pragma unroll
-                for (int j = 0; j < kVecB; ++j) more[j] = a.dstate_out[((long)n * a.dim + c0 + j) * 3 + u - (eos - 3)];
+                for (int j = 0; j < kVecB; ++j) y[j] = a.dstate_out[((long)n * a.dim + c0 + j) * 3 + u - (eos - 3)];
+                pair_up<kVecB>(y, more);
             }
             if (u >= from) gradient(gc, g[2], g[1], g[0], more, dx + (long)u * os);
 #pragma unroll
-            for (int j = 0; j < kVecB; ++j) {
+            for (int j = 0; j < kPairs; ++j) {
                 h[0][j] = h[1][j]; h[1][j] = h[2][j]; h[2][j] = x[j];
                 g[0][j] = g[1][j]; g[1][j] = g[2][j]; g[2][j] = gc[j];
             }
@@ -402,10 +434,11 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
     if (!a.partial) return;
     __shared__ float sh[8][32][kVecB * 5 + 1];
 #pragma unroll
-    for (int j = 0; j < kVecB; ++j) {
+    for (int j = 0; j < kPairs; ++j) {
+        float* to = sh[k][threadIdx.x & 31];
 #pragma unroll
-        for (int i = 0; i < kTaps; ++i) sh[k][threadIdx.x & 31][j * kTaps + i] = dw[j][i];
-        sh[k][threadIdx.x & 31][kVecB * kTaps + j] = db[j];
+        for (int i = 0; i < kTaps; ++i) dw[i][j].get(to[2 * j * kTaps + i], to[(2 * j + 1) * kTaps + i]);
+        db[j].get(to[kVecB * kTaps + 2 * j], to[kVecB * kTaps + 2 * j + 1]);
     }
     __syncthreads();
     float* pw = a.partial + (long)blockIdx.x * a.dim * kTaps;

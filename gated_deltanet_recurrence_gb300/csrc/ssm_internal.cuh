@@ -88,6 +88,44 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&x)[VEC
     else *reinterpret_cast<uint32_t*>(p) = u[0];
 }
 
+// Two floats in one 64-bit register: additions, products and sums of both at once.
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ static F2 of(uint32_t x, uint32_t y) { return F2(__uint_as_float(x), __uint_as_float(y)); }
+    __device__ __forceinline__ void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+// The two values of a bf16 pair.
+__device__ __forceinline__ F2 widen(uint32_t u) { return F2::of(u << 16, u & 0xffff0000u); }
+template <int VEC>
+__device__ __forceinline__ void pair_up(const float (&x)[VEC], F2 (&y)[VEC / 2]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) y[i] = F2(x[2 * i], x[2 * i + 1]);
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void store_pairs(T* p, const F2 (&y)[VEC / 2]) {
+    float x[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) y[i].get(x[2 * i], x[2 * i + 1]);
+    store_row<VEC>(p, x);
+}
+
 // VEC consecutive elements as they lie in memory, fetched ahead of their use.
 template <typename T, int VEC>
 struct RawRow {
@@ -110,6 +148,13 @@ struct RawRow {
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < W; ++i) u[i] = 0;
+    }
+    __device__ __forceinline__ void get(F2 (&x)[VEC / 2]) const {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            if constexpr (sizeof(T) == 4) x[i] = F2::of(u[2 * i], u[2 * i + 1]);
+            else x[i] = widen(u[i]);
+        }
     }
     __device__ __forceinline__ void get(float (&x)[VEC]) const {
         if constexpr (sizeof(T) == 4) {
@@ -153,7 +198,8 @@ struct Ring {
         for (int i = 0; i < BYTES / 4; ++i)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (i / 4) * 16 * THREADS + (i % 4) * 4), "r"(0) : "memory");
     }
-    __device__ __forceinline__ void read(int slot, float (&x)[VEC]) const {
+    template <class V, int C>  // floats, or pairs
+    __device__ __forceinline__ void read(int slot, V (&x)[C]) const {
         RawRow<T, VEC> r;
         read(slot, r);
         r.get(x);
@@ -187,6 +233,15 @@ __device__ __forceinline__ float sigmoid_hw(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + exp2_hw(x * -1.4426950408889634f)));
     return y;
+}
+
+__device__ __forceinline__ F2 sigmoid_hw(F2 x) {
+    float u, v, y, z;
+    (x * F2(-1.4426950408889634f, -1.4426950408889634f)).get(u, v);
+    (F2(exp2_hw(u), exp2_hw(v)) + F2(1.f, 1.f)).get(u, v);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(u));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(v));
+    return F2(y, z);
 }
 
 // Sums of R values over groups of L lanes; value r's sum ends in the lanes with (lane % L) % R == r (R <= L).
