@@ -16,7 +16,7 @@
 // gradient kernel's block takes one chunk and a subset of the heads of one group, so that C B^T is formed once and
 // dB, dC of the group's heads are summed before they are written.  This is the fp32 form (bf16: ssm_tc_bwd.cu), on three
 // planes a factor; a head's step is a chain of seven products with barriers between them, and its latency bounds short
-// batches (493 tokens of six heads: 58 us, the gradients 36 of them), the tensor instructions and the splits long ones
+// batches (493 tokens of six heads: 36 us), the tensor instructions and the splits long ones
 // (6144 tokens of 24 heads, d_state 128, in three sequences: 485 us).
 #include "ssm_chunk.cuh"
 
@@ -402,18 +402,19 @@ cudaError_t grad_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
     return launch_after(ssm_grad_kernel<N>, grid, kThreads, Smem<N>::bytes, s, a, w);
 }
 
-// Subsets of a group's heads: blocks for two rounds, at least two heads a block where the group has them (each subset
-// writes its dB and dC in fp32 for another kernel to add).  For one, two, three rounds: 2048 tokens of 16 heads 202, 155,
-// 155 us; 6144 of 24 in three sequences 583, 485, 509.
+// Subsets of a group's heads: blocks for two rounds, at least two heads a block unless that leaves SMs without one (each
+// subset writes its dB and dC in fp32 for another kernel to add).  For one, two, three rounds: 2048 tokens of 16 heads
+// 202, 155, 155 us; 6144 of 24 in three sequences 583, 485, 509.  One head a block against all three, 493 tokens of six
+// heads in two groups: 36 us for 59; one against two, 23 tokens of 15 in three: 36 for 68.
 int subsets_of(int num_seqs, int total_T, int H, int G) {
     const long blocks = slots_of(num_seqs, total_T) * G, per = H / G;
     long n = (2 * 152 + blocks - 1) / blocks;
-    const long most = per > 1 ? per / 2 : 1;
+    const long most = per == 1 || blocks * per <= 152 ? per : per / 2;
     n = n > most ? most : n;
     return (int)(n < 1 ? 1 : n);
 }
 
-size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, unsigned char* at) {
+size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, bool varied, Work* w, unsigned char* at) {
     const size_t slots = (size_t)slots_of(num_seqs, total_T);
     const size_t gates = up256(slots * H * kGateRows * kC * sizeof(float));
     const size_t states = up256(slots * H * P * N * sizeof(float)), sums = up256(slots * H * 3 * sizeof(float));
@@ -428,7 +429,7 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, Work* w, un
         w->subsets = subsets;
     }
     const size_t used = gates + 2 * states + sums + up256(parts);
-    return used + segments64(num_seqs, total_T, H, P, N, 2, false, w ? &w->g : nullptr, w ? at + used : nullptr);
+    return used + segments64(num_seqs, total_T, H, P, N, 2, varied, w ? &w->g : nullptr, w ? at + used : nullptr);
 }
 
 }  // namespace
@@ -447,13 +448,15 @@ cudaError_t launch_finish(const SsmArgs& a, const Work& w, long slots, cudaStrea
 
 size_t ssm_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N, gdn_dtype dtype) {
     if (dtype == GDN_BF16 && total_T > 0) return ssm::tc_bwd_workspace_bytes(num_seqs, total_T, H, G, P, N);
-    return ssm::layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
+    const size_t equal = ssm::layout(num_seqs, total_T, H, G, P, N, false, nullptr, nullptr),
+                 varied = ssm::layout(num_seqs, total_T, H, G, P, N, true, nullptr, nullptr);
+    return equal > varied ? equal : varied;
 }
 
 cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t s) {
     if (a.dtype == GDN_BF16 && a.seqs.total_T > 0) return ssm::launch_tc_bwd(a, s);
     ssm::Work w{};
-    ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
+    ssm::layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, a.seqs.cu && a.seqs.num_seqs > 1, &w, static_cast<unsigned char*>(a.workspace));
     cudaError_t e = ssm::launch_gates(a, w, s);
     if (e == cudaSuccess) e = ssm::launch_scan(a, w, 2, s);
     if (e != cudaSuccess) return e;

@@ -358,23 +358,25 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStr
 }
 
 // Chunks of a segment, or 0.  Blocks are counted against 152 SMs.  Few rows: as many segments as fill the SMs, where that
-// pays for sequences of one length.  A packed batch of up to two rounds of blocks, forwards: segments a little longer
-// than the average, where it pays if the longest of n sequences is 1 + 1/2 + ... + 1/n times the average. In us, whole
-// and in segments, bf16, d_state 128, 64 rows a head: 1536 tokens of 8 heads 36, 27; 6144 of 8 128, 30; 6144 of 24 129,
-// 48; 32768 of 16 657, 136; 8192 in 4 sequences of 16 heads 47, 56 (stays whole).  Packed: lengths 1, 37, 513, 3001, 64,
-// 1333, 700 of 24 rows 71, 60 (seven of 807: 47, 52); 8000, 3 x 2000, 4 x 500 of 24 170, 118 (eight of 2048: 95, 105).
+// pays for sequences of one length, or, where the lengths may differ, for the longest of n, taken as 1 + 1/2 + ... + 1/n
+// times the average.  A packed batch of up to two rounds of blocks, forwards: segments a little longer than the average,
+// where they pay for that longest one. In us, whole and in segments, bf16, d_state 128, 64 rows a head: 1536 tokens of 8
+// heads 36, 27; 6144 of 8 128, 30; 6144 of 24 129, 48; 32768 of 16 657, 136; 8192 in 4 sequences of 16 heads 47, 56
+// (stays whole).  Packed: lengths 1, 37, 513, 3001, 64, 1333, 700 of 24 rows 71, 60 (seven of 807: 47, 52); 8000, 3 x
+// 2000, 4 x 500 of 24 170, 118 (eight of 2048: 95, 105).
 static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int directions, bool varied, SegmentCost cost) {
     const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
                avg = (chunks + num_seqs - 1) / num_seqs;
     const auto split = [&](long each) { return each * (cost.whole + cost.own) + cost.more; };
+    if (rows > 304) return 0;
+    double longest = (double)avg;
+    for (int n = 2; varied && n <= num_seqs; ++n) longest += (double)avg / n;
     if (rows <= 152) {
         const long count = 152 / rows, fill = (avg + count - 1) / count, each = fill < 4 ? 4 : fill;
-        if (avg * cost.whole > split(each)) return (int)each;
+        if (longest * cost.whole > split(each)) return (int)each;
     }
-    if (directions > 1 || !varied || rows > 304) return 0;
+    if (directions > 1 || !varied) return 0;
     const long each = avg + avg / 4 < 8 ? 8 : avg + avg / 4;
-    double longest = 0.;
-    for (int n = 1; n <= num_seqs; ++n) longest += (double)avg / n;
     return longest * cost.whole > split(each) ? (int)each : 0;
 }
 

@@ -665,7 +665,7 @@ int subsets_of(int num_seqs, int total_T, int H, int G, int N) {
     return best;
 }
 
-size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, TcWork* w, unsigned char* at) {
+size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, bool varied, TcWork* w, unsigned char* at) {
     const size_t slots = (size_t)slots128(num_seqs, total_T);
     const size_t gates = up256(slots * H * kGates * sizeof(float)), states = slots * H * P * N * sizeof(float),
                  sums = up256(slots * H * 3 * sizeof(float));
@@ -680,7 +680,7 @@ size_t layout(int num_seqs, int total_T, int H, int G, int P, int N, TcWork* w, 
         w->subsets = subsets;
     }
     const size_t used = gates + 2 * states + sums + up256(parts);
-    return used + segments128(num_seqs, total_T, H, P, N, 2, false, w ? &w->g : nullptr, w ? at + used : nullptr);
+    return used + segments128(num_seqs, total_T, H, P, N, 2, varied, w ? &w->g : nullptr, w ? at + used : nullptr);
 }
 
 template <int N>
@@ -702,12 +702,14 @@ cudaError_t launch(const SsmArgs& a, const TcWork& w, cudaStream_t s) {
 }  // namespace
 
 size_t tc_bwd_workspace_bytes(int num_seqs, int total_T, int H, int G, int P, int N) {
-    return layout(num_seqs, total_T, H, G, P, N, nullptr, nullptr);
+    const size_t equal = layout(num_seqs, total_T, H, G, P, N, false, nullptr, nullptr),
+                 varied = layout(num_seqs, total_T, H, G, P, N, true, nullptr, nullptr);
+    return equal > varied ? equal : varied;
 }
 
 cudaError_t launch_tc_bwd(const SsmArgs& a, cudaStream_t s) {
     TcWork w{};
-    layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, &w, static_cast<unsigned char*>(a.workspace));
+    layout(a.seqs.num_seqs, a.seqs.total_T, a.H, a.G, a.P, a.N, a.seqs.cu && a.seqs.num_seqs > 1, &w, static_cast<unsigned char*>(a.workspace));
     const cudaError_t e = a.N == 128 ? launch<128>(a, w, s) : launch<64>(a, w, s);
     if (e != cudaSuccess) return e;
     Work f{};
