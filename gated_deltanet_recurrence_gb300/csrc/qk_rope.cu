@@ -7,10 +7,12 @@
 // with cos_i, sin_i of the token's position from a table; the other channels pass.  Gradients: the rotation
 // backwards, then dw = sum dm n, dn = dm w, dx = r (dn - n mean(dn n)) (or the sum's, for length one).
 //
-// Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 17.0 us, 5.1 TB/s (75% of a copy's rate),
-// gradients of 3001 tokens of 16 + 16 heads of 64 9.3 us with the launch behind.  What is left are instructions: 58% of
-// the issue slots before arithmetic went in pairs of channels (17.5 us).  Two blocks an SM with all values in registers;
-// three, with spills, 17.8. Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one head of one
+// Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 16.4 us, 5.2 TB/s (77% of a copy's rate),
+// gradients of 3001 tokens of 16 + 16 heads of 64 8.7 us with the launch behind.  What is left are instructions (58% of the
+// issue slots before arithmetic went in pairs of channels, 17.5 us).  Two blocks an SM with all values in registers; three,
+// with spills, 17.8 for 17.0 on another machine.
+//
+// Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one head of one
 // token) is d / 8 lanes of 8 channels; a set of lanes takes one token and several heads, so that the token's cosines and
 // sines and the weights are loaded once.  Pairs of channels m = d_rot / 2 apart are exchanged by shuffles where they lie
 // in the same place of another lane (m a multiple of 8), through shared memory otherwise.

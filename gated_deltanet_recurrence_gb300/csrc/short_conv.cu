@@ -27,8 +27,8 @@ constexpr int kVecB = 2;    // and in the backward pass, whose taps, windows and
 constexpr int kSMs = 152;
 constexpr int kGroups = 4;  // groups of four rows that a thread has on their way
 
-template <bool SILU, class V>
-__device__ __forceinline__ V silu_or(V c) {
+template <bool SILU>
+__device__ __forceinline__ float silu_or(float c) {
     return SILU ? c * sigmoid_hw(c) : c;
 }
 

@@ -368,7 +368,7 @@ static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int
     const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
                avg = (chunks + num_seqs - 1) / num_seqs;
     const auto split = [&](long each) { return each * (cost.whole + cost.own) + cost.more; };
-    if (rows > 304) return 0;
+    if (rows > 304 || total_T > 1 << 29) return 0;  // a segment's tokens are an int
     double longest = (double)avg;
     for (int n = 2; varied && n <= num_seqs; ++n) longest += (double)avg / n;
     if (rows <= 152) {

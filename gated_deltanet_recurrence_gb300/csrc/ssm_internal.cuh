@@ -126,29 +126,11 @@ __device__ __forceinline__ void store_pairs(T* p, const F2 (&y)[VEC / 2]) {
     store_row<VEC>(p, x);
 }
 
-// VEC consecutive elements as they lie in memory, fetched ahead of their use.
+// VEC consecutive elements as they lie in memory.
 template <typename T, int VEC>
 struct RawRow {
     static constexpr int W = VEC * (int)sizeof(T) / 4;
     uint32_t u[W];
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (W == 1) {
-            u[0] = *reinterpret_cast<const uint32_t*>(p);
-        } else if constexpr (W == 2) {
-            const uint2 t = *reinterpret_cast<const uint2*>(p);
-            u[0] = t.x; u[1] = t.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; i += 4) {
-                const uint4 t = reinterpret_cast<const uint4*>(p)[i / 4];
-                u[i] = t.x; u[i + 1] = t.y; u[i + 2] = t.z; u[i + 3] = t.w;
-            }
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < W; ++i) u[i] = 0;
-    }
     __device__ __forceinline__ void get(F2 (&x)[VEC / 2]) const {
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i) {

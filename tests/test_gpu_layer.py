@@ -251,6 +251,19 @@ def test_scan_in_segments(lengths, tail, H, G, P, N, dtype, carried, extra, firs
             assert a is None or torch.equal(a[rows], b[rows])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scale,shift,a_log", [(30.0, 0.0, 0.0), (1.0, 60.0, 3.0), (1.0, -40.0, 0.0), (1.0, 0.0, -20.0)])
+def test_scan_in_segments_with_extreme_steps_and_decays(dtype, scale, shift, a_log):
+    offs, T, s, S0, r = scan_inputs([1600], 0, 1, 1, 64, 64, dtype, True, True, seed=58, a_scale=scale, a_shift=shift)
+    s["A_log"] = torch.full_like(s["A_log"], a_log)
+    got, last = gdn.gdn_ssm_chunk_fwd(**s, cu_seqlens=cu(offs), initial_state=S0)
+    (ref, ref_last), (terms, terms_last) = scan_reference(s, offs, S0)
+    check("out", got, ref, terms)
+    check("state", last, ref_last, terms_last)
+    dout = dev(r(*s["x"].shape), dtype)
+    check_grads(gdn.gdn_ssm_chunk_bwd(dout, **s, cu_seqlens=cu(offs), initial_state=S0), dout, s, offs, S0, None, dtype)
+
+
 def test_scan_in_segments_of_packed_prompts_that_differ():
     """More blocks than SMs, and one sequence that outlasts the others."""
     lengths, H, P, N = [1, 37, 513, 2901, 0, 1333, 700], 24, 64, 64
