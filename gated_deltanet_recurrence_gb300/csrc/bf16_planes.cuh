@@ -4,8 +4,8 @@
 // is one plane as it lies in memory.  A product takes the terms of planes i and j with i + j <= 2, each an m16n8k16
 // instruction with fp32 accumulation: three for an input times a fp32 matrix, six for two fp32 matrices; what is
 // left out is below 2^-24 of a term.  Two planes (2^-17) are enough in front of an output that is rounded to bf16.
-// The alternative, two fp16 planes with scales (mma_planes.cuh), takes a third fewer instructions and scales by
-// rows that have to follow every operand; inputs that are exact in one plane without conversion make up for it.
+// The alternative, two fp16 planes with scales (mma_planes.cuh), takes three instructions for six and scales by rows
+// that have to follow every operand; bf16 inputs, exact in one plane without conversion, make up for it on tcgen05.
 //
 // Tiles, addresses and fragments are those of mma_planes.cuh: blocks of 64 columns, rows of 128 bytes, 16-byte chunks
 // XORed by the row.

@@ -12,9 +12,9 @@
 // rows by asynchronous copies into a ring of its own in shared memory, four groups of four rows ahead, which takes
 // neither registers nor waits, has few channels (four forward, two backward: eight and four were slower, for their
 // registers), and takes its sigmoid from the hardware's exponential and reciprocal.  Gradients' arithmetic goes in pairs
-// of channels (8192 x 4352: 69 -> 66 us; forward that spilled, 33 -> 36).  Measured, bf16: 8192 tokens of 4352 channels
-// 32.5 us, 4.4 TB/s (65% of a copy's rate); gradients of 4132 tokens of 2304 channels 25 us, four of them the sums
-// behind, 2.4 TB/s; a token of five sequences of 384 channels 1.9 us.
+// of channels (8192 x 4352: 69 -> 66 us; forward that spilled, 33 -> 36 us).  Measured, bf16: 8192 tokens of 4352
+// channels 27.5 us, 5.2 TB/s (77% of a copy's rate; 32768 tokens 93 us, 6.1 TB/s); gradients of 4132 tokens of 2304
+// channels 22 us, four of them the sums behind, 2.6 TB/s; a token of five sequences of 384 channels 1.9 us.
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -88,34 +88,33 @@ __device__ void final_history(const ShortConvArgs& a, int n, int bos, int len, i
         for (int k = 0; k < 3; ++k) a.state_out[((long)n * a.dim + c0 + j) * 3 + k] = h[k][j];
 }
 
-// Blocks [0, runs * cols): one run of `run` tokens of kThreads channel vectors each; the blocks behind them write
-// the final histories (num_seqs * vectors threads).
+// A thread: one channel vector along one run of `run` tokens; threads are numbered through the vectors of a run, then
+// through the runs.  The blocks behind `blocks` write the final histories (num_seqs * vectors threads).
 template <typename T, bool SILU>
-__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ShortConvArgs a, int run, int cols, int runs) {
+__global__ void __launch_bounds__(kThreads, 3) conv_fwd_kernel(ShortConvArgs a, int run, unsigned blocks) {
     extern __shared__ __align__(16) unsigned char smem[];
     Ring<T, kVec, 4 * kGroups, kThreads> ring(smem);
     const int vecs = a.dim / kVec;
-    if (blockIdx.x >= (unsigned)(runs * cols)) {
+    if (blockIdx.x >= blocks) {
         if (packed_find(a.seqs, 0, 1, 0, a.err) == -2) return;
-        const long q = (long)(blockIdx.x - runs * cols) * kThreads + threadIdx.x;
+        const long q = (long)(blockIdx.x - blocks) * kThreads + threadIdx.x;
         if (q >= (long)a.seqs.num_seqs * vecs) return;
         const int n = (int)(q / vecs), bos = a.seqs.bos(n);
         final_history<T, kVec>(a, n, bos, a.seqs.bos(n + 1) - bos, (int)(q % vecs) * kVec);
         return;
     }
-    const int col = blockIdx.x % cols;
-    // `cols` blocks cover the channel vectors, or, with few channels, one block covers several runs
-    const int per = cols > 1 ? 1 : kThreads / vecs;
-    const int v = cols > 1 ? col * kThreads + (int)threadIdx.x : (int)threadIdx.x % vecs;
-    const int first = (int)(blockIdx.x / cols) * per * run;
+    const long q = (long)blockIdx.x * kThreads;
+    const int skip = (int)(q % vecs) + (int)threadIdx.x, v = skip % vecs;
+    const long first = q / vecs * run;  // of the block's first thread
+    const long start = first + (long)(skip / vecs) * run;
+    const bool on = start < a.seqs.total_T;
     const int c0 = v * kVec;
     float w[kVec][kTaps], b[kVec], h[3][kVec];
-    if (v < vecs) load_taps<kVec>(a, c0, w, b);
-    int n = packed_find(a.seqs, first, 1, 0, a.err);
-    if (n == -2) return;
-    int t = first + (cols > 1 ? 0 : (int)threadIdx.x / vecs * run);
-    if (v >= vecs || (cols == 1 && (int)threadIdx.x / vecs >= per)) return;
-    const int end = min(t + run, a.seqs.total_T), N = a.seqs.num_seqs;
+    if (on) load_taps<kVec>(a, c0, w, b);
+    int n = packed_find(a.seqs, (int)first, 1, 0, a.err);
+    if (n == -2 || !on) return;
+    int t = (int)start;
+    const int end = (int)min(start + run, (long)a.seqs.total_T), N = a.seqs.num_seqs;
     if (n < 0) {  // tokens before the first sequence stay as they are
         n = 0;
         t = max(t, a.seqs.bos(0));
@@ -454,24 +453,23 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
     }
 }
 
-// Tokens a thread walks: long runs re-read few rows, short ones give enough threads to a small call, here two blocks an
-// SM. In us, forward of 8192 tokens x 4352 channels (bf16) with runs of 8, 16, 32, 64, 128: 48, 38, 33, 34, 39; 4132 x
-// 2304: 15.3, 12.8, 12.1, 15.0, 16.4; 500 x 2304: 5.5 (runs of 4), 5.5, 5.1, 10, 17.  Gradients with runs of 2, 8, 16,
-// 32: 4132 x 2304: 89, 24, 26, 23; 500 x 2304: 17, 9.3, 8.9, 10; 100 x 384: 6.3, 6.3, 7.2, 7.9.
-int run_length(long total_T, long vecs, int least, int most) {
-    long run = total_T * vecs / (kSMs * 2L * kThreads);
-    run = run < least ? least : (run > most ? most : run);
-    return (int)run;
+// Tokens a thread walks, of a call whose runs find room `at_once` by three blocks an SM: whole rounds of those, few and
+// long runs, which start and end seldom.  In us, forward, 8192 tokens x 4352 channels (bf16) with runs of 21, 26, 32, 39,
+// 77 (a round): 36, 33, 33, 30, 28; 4132 x 2304 with 21 (a round), 26, 32, 39: 10.1, 11.3, 12.0, 10.9; 500 x 2304 with 2,
+// 4, 16: 5.6, 5.1, 5.5; 32768 x 4352 with runs of at most 64, 96, 128, 192: 95, 95, 93, 92.  Gradients, 8192 x 4352 with
+// 19, 27, 36, 77: 79, 69, 64, 60; 500 x 2304 with 4, 8, 16: 11.8, 9.3, 8.8; 100 x 384: 6.4, 6.6, 7.4.
+int run_length(long total_T, long at_once, int least) {
+    const long longest = 128, most = at_once > 0 ? at_once : 1, whole = (total_T + most - 1) / most;
+    const long rounds = whole > longest ? (whole + longest - 1) / longest : 1, run = (total_T + most * rounds - 1) / (most * rounds);
+    return (int)(run < least ? least : run);
 }
 
 }  // namespace
 
 cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
     const int vecs = a.dim / kVec;
-    const int cols = vecs > kThreads ? (vecs + kThreads - 1) / kThreads : 1;
-    const int per = cols > 1 ? 1 : kThreads / vecs;
-    const int run = run_length(a.seqs.total_T, vecs, 4, 32);
-    const int runs = (int)(((long)a.seqs.total_T + (long)per * run - 1) / ((long)per * run));
+    const int run = run_length(a.seqs.total_T, 3L * kSMs * kThreads / vecs, 4);
+    const long runs = ((long)a.seqs.total_T + run - 1) / run, blocks = (runs * vecs + kThreads - 1) / kThreads;
     const long tail = a.state_out ? ((long)a.seqs.num_seqs * vecs + kThreads - 1) / kThreads : 0;
     using B = __nv_bfloat16;
     const auto kernel = a.dtype == GDN_BF16 ? (a.silu ? conv_fwd_kernel<B, true> : conv_fwd_kernel<B, false>)
@@ -481,14 +479,14 @@ cudaError_t launch_short_conv_fwd(const ShortConvArgs& a, cudaStream_t s) {
     if (set != cudaSuccess) return set;
     // histories that are carried in place are written behind everything that reads them
     const bool apart = a.state_out && a.state_out == a.state_in;
-    if ((long)runs * cols + tail > 0x7fffffffL) return cudaErrorInvalidValue;
-    if (runs > 0 || (tail > 0 && !apart)) {
-        kernel<<<(unsigned)((long)runs * cols + (apart ? 0 : tail)), kThreads, smem, s>>>(a, run, cols, runs);
+    if (blocks + tail > 0x7fffffffL) return cudaErrorInvalidValue;
+    if (blocks > 0 || (tail > 0 && !apart)) {
+        kernel<<<(unsigned)(blocks + (apart ? 0 : tail)), kThreads, smem, s>>>(a, run, (unsigned)blocks);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (apart) {
-        kernel<<<(unsigned)tail, kThreads, smem, s>>>(a, run, cols, 0);
+        kernel<<<(unsigned)tail, kThreads, smem, s>>>(a, run, 0);
         return cudaGetLastError();
     }
     return cudaSuccess;
@@ -505,7 +503,7 @@ cudaError_t launch_short_conv_step(const ShortConvArgs& a, cudaStream_t s) {
 }
 
 static void bwd_plan(int total_T, int dim, int& run, int& rows) {
-    run = run_length(total_T, dim / kVecB, 8, 32);
+    run = run_length(total_T, 3 * kSMs / ((dim / kVecB + 31) / 32) * 8, 8);
     rows = (int)(((long)total_T + 8L * run - 1) / (8L * run));
 }
 
