@@ -363,7 +363,8 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStr
 // where they pay for that longest one. In us, whole and in segments, bf16, d_state 128, 64 rows a head: 1536 tokens of 8
 // heads 36, 27; 6144 of 8 128, 30; 6144 of 24 129, 48; 32768 of 16 657, 136; 8192 in 4 sequences of 16 heads 47, 56
 // (stays whole).  Packed: lengths 1, 37, 513, 3001, 64, 1333, 700 of 24 rows 71, 60 (seven of 807: 47, 52); 8000, 3 x
-// 2000, 4 x 500 of 24 170, 118 (eight of 2048: 95, 105).
+// 2000, 4 x 500 of 24 170, 118 (eight of 2048: 95, 105).  Segments of 0.75, 1, 1.25 times the average:
+// the first of these 65, 61, 60, the third 129, 129, 118.
 static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int directions, bool varied, SegmentCost cost) {
     const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
                avg = (chunks + num_seqs - 1) / num_seqs;
