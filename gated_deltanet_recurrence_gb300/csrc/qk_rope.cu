@@ -219,7 +219,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_kernel(QkArgs a, int per, long
                     xr[u].get(x);
 #pragma unroll
                     for (int j = 0; j < kPairsOf; ++j) s2 = fma2(x[j], x[j], s2);
-                    const float r = rsqrtf(set_sum<L>(sum_of(s2)) * inv + a.eps);
+                    const float ms = set_sum<L>(sum_of(s2)) * inv + a.eps;
+                    // a set without a row has a sum of zero, whose factor with eps = 0 is infinite, and adds to dw
+                    const float r = BWD && !live ? 0.f : rsqrtf(ms);
                     const F2 r2(r, r);
                     if constexpr (!BWD) {
                         partners<T, L, PAIRS>(xr[u], x, y, lane, from, m, row);

@@ -460,7 +460,8 @@ typedef enum { GDN_NORM_RMS = 0, GDN_NORM_L2 = 1 } gdn_norm;
  *   positions int32 [T] (4-byte aligned), or NULL: row t has position t.  A position outside the table is recorded as
  *   GDN_ERR_ARG in the device error word and its row is left as it was.
  *   q_out, k_out  like q and k, rows by their own strides; may be q and k themselves.
- *   d a multiple of 8, at most 256 (GDN_ERR_UNSUPPORTED otherwise); d_rot even, 0 <= d_rot <= d.
+ *   d a multiple of 8, at most 256 (GDN_ERR_UNSUPPORTED otherwise); d_rot even, 0 <= d_rot <= d; eps >= 0 (with 0 a
+ *   head of zeros is 0 / 0, NaN).
  */
 int gdn_qk_norm_rope(const void* q, long q_stride, const void* k, long k_stride, const float* cos_sin,
                      const int32_t* positions, long max_positions, const float* q_weight, const float* k_weight,

@@ -1,0 +1,41 @@
+"""Ends of the state space layer's calls: eps = 0, and parameters that are no numbers."""
+import pytest
+import torch
+
+import gated_deltanet_recurrence_gb300 as gdn
+from tests import _layer
+from tests._layer import check, wide
+from tests.test_gpu_layer import ARG_ERROR, BF, F32, angles, clean_error_word, dev, qk_inputs  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("l2", [False, True])
+@pytest.mark.parametrize("T,H,H_k,d,rot,interleaved,dtype", [
+    (1, 1, 1, 64, 32, False, F32), (7, 3, 1, 64, 64, True, BF), (33, 2, 2, 128, 64, False, BF), (5, 2, 1, 96, 24, False, F32),
+    (6, 1, 2, 8, 4, False, F32), (9, 2, 0, 256, 256, False, F32), (2501, 4, 1, 64, 64, False, BF)])
+def test_rotation_gradients_without_eps(T, H, H_k, d, rot, interleaved, l2, dtype):
+    """No head of a row is zero; places without a row (tokens rounded up to whole warps, a position outside the table)
+    add nothing to the weights' gradients."""
+    for outside in (None, T // 2):
+        q, k, table, pos, w, r = qk_inputs(T, H, H_k, d, rot, True, dtype, seed=T + d)
+        if outside is not None:
+            pos[outside] = 300
+        kw = dict(positions=pos, q_weight=w[0], k_weight=w[1] if H_k else None, eps=0.0, interleaved=interleaved,
+                  norm=gdn.GDN_NORM_L2 if l2 else gdn.GDN_NORM_RMS)
+        douts = dev(r(T, H, d), dtype), dev(r(T, H_k, d), dtype) if H_k else None
+        outs = gdn.gdn_qk_norm_rope(q, k, table, **kw)
+        grads = gdn.gdn_qk_norm_rope_bwd(*douts, q, k, table, **kw)
+        torch.cuda.synchronize()
+        assert gdn.gdn_get_device_error() == (0 if outside is None else ARG_ERROR)
+        rows = torch.tensor([t for t in range(T) if t != outside], dtype=torch.long)
+        cos, sin = angles(table, pos[rows.cuda()], rot, len(rows))
+        for i, x in enumerate((q, k)):
+            if x is None:
+                continue
+            X, DO, wt = wide(x)[rows], wide(douts[i])[rows], wide(w[i])
+            ref, terms = _layer.qk(X, wt, cos, sin, l2, 0.0, interleaved)
+            check("rotated", outs[i][rows.cuda()], ref, terms)
+            ref = _layer.qk_bwd(DO, X, wt, cos, sin, l2, 0.0, interleaved)
+            check("dx", grads[i][rows.cuda()], ref[0], ref[2])
+            check("dw", grads[2 + i], ref[1], 2 * ref[3])  # up to 128 additions one by one, as rows are many
