@@ -32,6 +32,10 @@ bool packed_ok(const int32_t* cu, int num_seqs, int total_T) {
 }
 bool elements_ok(long rows, long width) { return width <= 0 || rows <= kMaxElements / width; }
 
+// Tokens of a packed convolution: its kernels count in 32 bits up to eight runs of 128 tokens past the last one, and
+// the rows that they ask for ahead.
+constexpr int kMaxConvTokens = 0x7fffffff - 2048;
+
 // The sizes of a convolution call; GDN_ERR_UNSUPPORTED for channels that are no whole vectors.
 int conv_sizes(long tokens, int dim) {
     if (dim <= 0 || !elements_ok(tokens, dim)) return GDN_ERR_ARG;
@@ -80,7 +84,7 @@ int gdn_short_conv_fwd(const void* x, long x_stride, const float* weight, const 
                        int num_seqs, int total_T, int dim, gdn_dtype dtype, int silu, const float* conv_state_in,
                        float* conv_state_out, void* out, void* stream) {
     if (!valid_dtype(dtype)) return GDN_ERR_DTYPE;
-    if (!packed_ok(cu_seqlens, num_seqs, total_T)) return GDN_ERR_ARG;
+    if (!packed_ok(cu_seqlens, num_seqs, total_T) || total_T > kMaxConvTokens) return GDN_ERR_ARG;
     const int rc = conv_sizes((long)total_T + 3L * num_seqs, dim);
     if (rc != GDN_OK) return rc;
     if (!rows_ok(x_stride, dim)) return GDN_ERR_ARG;
@@ -118,7 +122,7 @@ int gdn_short_conv_step(const void* x, long x_stride, const float* weight, const
 }
 
 size_t gdn_short_conv_bwd_workspace_size(int num_seqs, int total_T, int dim) {
-    if (num_seqs <= 0 || total_T < 0 || conv_sizes((long)total_T + 3L * num_seqs, dim) != GDN_OK) return 0;
+    if (num_seqs <= 0 || total_T < 0 || total_T > kMaxConvTokens || conv_sizes((long)total_T + 3L * num_seqs, dim) != GDN_OK) return 0;
     return gdn::short_conv_bwd_workspace_bytes(total_T, dim);
 }
 
@@ -127,7 +131,7 @@ int gdn_short_conv_bwd(const void* dout, const void* x, long x_stride, const flo
                        const float* conv_state_in, const float* dconv_state_out, void* dx, float* dweight, float* dbias,
                        float* dconv_state_in, int zero_outside, void* workspace, size_t workspace_bytes, void* stream) {
     if (!valid_dtype(dtype)) return GDN_ERR_DTYPE;
-    if (!packed_ok(cu_seqlens, num_seqs, total_T)) return GDN_ERR_ARG;
+    if (!packed_ok(cu_seqlens, num_seqs, total_T) || total_T > kMaxConvTokens) return GDN_ERR_ARG;
     const int rc = conv_sizes((long)total_T + 3L * num_seqs, dim);
     if (rc != GDN_OK) return rc;
     if (!rows_ok(x_stride, dim)) return GDN_ERR_ARG;

@@ -361,7 +361,7 @@ size_t gdn_decay_bwd_workspace_size(long total_T, int H);
  *   conv_state_in, conv_state_out  [num_seqs, dim, 3]: the three inputs before each sequence's first token, oldest
  *           first (NULL: zeros), and the last three of it (NULL: not written).  They may be the same array.
  *   out     [total_T, dim] of dtype.
- *   dim     a multiple of 8 (GDN_ERR_UNSUPPORTED otherwise), at most 2^20.
+ *   dim     a multiple of 8 (GDN_ERR_UNSUPPORTED otherwise), at most 2^20; total_T at most 2^31 - 2049.
  */
 int gdn_short_conv_fwd(const void* x, long x_stride, const float* weight, const float* bias,
                        const int32_t* cu_seqlens, int num_seqs, int total_T, int dim, gdn_dtype dtype, int silu,
