@@ -14,6 +14,11 @@ namespace ssm {
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kGateRows = 5;    // dt, G hi, G lo, b, r
 constexpr float kMinLog = -128.f;  // a log decay below it is a decay to zero
+// fmaxf would make a decay to zero of a NaN.
+__device__ __forceinline__ float log_decay(float rate, float dt) {
+    const float g = -rate * dt;
+    return g < kMinLog ? kMinLog : g;
+}
 
 // A sum in two floats, h + l.
 struct Two {

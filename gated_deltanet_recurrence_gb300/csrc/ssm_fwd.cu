@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates_kernel(SsmArgs a, f
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
         dt[i] = t < c.len ? ssm_softplus(a.a[(long)(c.t0 + t) * a.H + h] + bias) : 0.f;
-        g[i] = t < c.len ? fmaxf(-rate * dt[i], kMinLog) : 0.f;
+        g[i] = t < c.len ? log_decay(rate, dt[i]) : 0.f;
     }
     Two pair = two_add(Two{g[0], 0.f}, Two{g[1], 0.f}), sum = pair;
     float suf = g[0] + g[1];

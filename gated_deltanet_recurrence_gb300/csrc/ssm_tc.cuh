@@ -94,7 +94,7 @@ __device__ __forceinline__ void lane_gates(const float (&z)[4], int left, float 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         o.dt[e] = e < left ? ssm_softplus(z[e]) : 0.f;
-        gl[e] = e < left ? fmaxf(-rate * o.dt[e], kMinLog) : 0.f;
+        gl[e] = e < left ? log_decay(rate, o.dt[e]) : 0.f;
     }
     Two pre[4];
     pre[0] = Two{gl[0], 0.f};

@@ -5,7 +5,7 @@ import torch
 import gated_deltanet_recurrence_gb300 as gdn
 from tests import _layer
 from tests._layer import check, wide
-from tests.test_gpu_layer import ARG_ERROR, BF, F32, angles, clean_error_word, dev, qk_inputs  # noqa: F401
+from tests.test_gpu_layer import ARG_ERROR, BF, F32, angles, clean_error_word, dev, qk_inputs, scan_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,33 @@ def test_rotation_gradients_without_eps(T, H, H_k, d, rot, interleaved, l2, dtyp
             ref = _layer.qk_bwd(DO, X, wt, cos, sin, l2, 0.0, interleaved)
             check("dx", grads[i][rows.cuda()], ref[0], ref[2])
             check("dw", grads[2 + i], ref[1], 2 * ref[3])  # up to 128 additions one by one, as rows are many
+
+
+@pytest.mark.parametrize("name", ["A_log", "dt_bias", "D"])
+@pytest.mark.parametrize("dtype,T", [(F32, 150), (BF, 150), (F32, 2000), (BF, 2000)])  # 2000: in segments
+def test_a_parameter_that_is_no_number_reaches_its_heads_outputs_and_no_others(name, dtype, T):
+    """As in the definition, and as token by token: exp(NaN) S is no number, whatever S."""
+    H = 2
+    offs, _, s, S0, r = scan_inputs([T], 0, H, 1, 64, 64, dtype, True, True, seed=T)
+    dout = dev(r(T, H, 64), dtype)
+    good = *gdn.gdn_ssm_chunk_fwd(**s, initial_state=S0), *gdn.gdn_ssm_chunk_bwd(dout, **s, initial_state=S0)
+    s[name] = s[name].clone()
+    s[name][1] = float("nan")
+    out, last, dx, dB, dC, da, *sums, dS0 = *gdn.gdn_ssm_chunk_fwd(**s, initial_state=S0), \
+        *gdn.gdn_ssm_chunk_bwd(dout, **s, initial_state=S0)
+    pool = S0.clone()
+    n = 70
+    step = gdn.gdn_ssm_step(*(s[k][:n][None].contiguous() for k in ("x", "B", "C", "a")), s["A_log"], pool,
+                            dt_bias=s["dt_bias"], D=s["D"])[0]
+    assert bool(torch.isnan(step[:, 1]).all()) and bool(torch.isnan(out[:, 1]).all())
+    assert bool(torch.isnan(dx[:, 1]).all())
+    if name != "D":
+        assert bool(torch.isnan(pool[0, 1]).all()) and bool(torch.isnan(last[0, 1]).all())
+        assert bool(torch.isnan(da[:, 1]).all()) and bool(torch.isnan(dS0[0, 1]).all())
+        assert bool(torch.isnan(sums[0][1])) and bool(torch.isnan(dB).all()) and bool(torch.isnan(dC).all())
+    for a, b in zip((out, dx, da), (good[0], good[2], good[5])):
+        assert torch.equal(a[:, 0], b[:, 0])
+    for a, b in zip((last, dS0), (good[1], good[9])):
+        assert torch.equal(a[:, 0], b[:, 0])
+    for a, b in zip(sums, good[6:9]):
+        assert torch.equal(a[0], b[0])
