@@ -15,7 +15,8 @@
 // registers), and takes its sigmoid from the hardware's exponential and reciprocal.  Gradients' arithmetic goes in pairs
 // of channels (8192 x 4352: 69 -> 66 us; forward that spilled, 33 -> 36 us).  Measured, bf16: 8192 tokens of 4352
 // channels 27.5 us, 5.2 TB/s (77% of a copy's rate; 32768 tokens 93 us, 6.1 TB/s); gradients of 4132 tokens of 2304
-// channels 22 us, four of them the sums behind, 2.6 TB/s; a token of five sequences of 384 channels 1.9 us.
+// channels 22 us, four of them the sums behind, 2.6 TB/s; a token of five sequences of 384 channels 1.9 us.  Fp32: gradients
+// of 8192 tokens of 4352 channels 81 us, 5.3 TB/s; of 4132 of 2304 25.8 (with two blocks an SM 29.8).
 #include "ssm_internal.cuh"
 
 namespace gdn {
@@ -27,6 +28,11 @@ constexpr int kVec = 4;     // channels of a thread, forward
 constexpr int kVecB = 2;    // and in the backward pass, whose taps, windows and sums take 30 registers a channel
 constexpr int kSMs = 152;
 constexpr int kGroups = 4;  // groups of four rows that a thread has on their way
+constexpr int kSums = kVecB * 5 + 1;  // sums of a thread of the backward pass, and a word between them
+template <typename T>
+constexpr int kRingsB = 2 * Ring<T, kVecB, 4 * kGroups, kThreads>::kSmem;
+static_assert(kRingsB<__nv_bfloat16> >= 8 * 32 * kSums * 4, "the sums take the rings' place");
+static_assert(3 * (kRingsB<float> + 1024 + 256) <= 228 * 1024, "three blocks an SM, with what the system and packed_find keep");
 
 template <bool SILU>
 __device__ __forceinline__ float silu_or(float c) {
@@ -432,7 +438,10 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
         t = stop;
     }
     if (!a.partial) return;
-    __shared__ float sh[8][32][kVecB * 5 + 1];
+    // in the rings' place, once every thread has read its rows
+    ring_wait<0>();
+    __syncthreads();
+    float(*sh)[32][kSums] = reinterpret_cast<float(*)[32][kSums]>(smem);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
         float* to = sh[k][threadIdx.x & 31];
@@ -523,7 +532,7 @@ cudaError_t launch_short_conv_bwd(const ShortConvArgs& a, cudaStream_t s) {
         using B = __nv_bfloat16;
         const auto kernel = bf ? (a.silu ? conv_bwd_kernel<B, true> : conv_bwd_kernel<B, false>)
                                : (a.silu ? conv_bwd_kernel<float, true> : conv_bwd_kernel<float, false>);
-        const int smem = 2 * (bf ? Ring<__nv_bfloat16, kVecB, 4 * kGroups, kThreads>::kSmem : Ring<float, kVecB, 4 * kGroups, kThreads>::kSmem);
+        const int smem = bf ? kRingsB<B> : kRingsB<float>;
         cudaError_t e = allow_smem(kernel, smem);
         if (e != cudaSuccess) return e;
         kernel<<<grid, kThreads, smem, s>>>(a, run, rows);
