@@ -467,7 +467,9 @@ __global__ void __launch_bounds__(kThreads, 3) conv_bwd_kernel(ShortConvArgs a, 
 // long runs, which start and end seldom.  In us, forward, 8192 tokens x 4352 channels (bf16) with runs of 21, 26, 32, 39,
 // 77 (a round): 36, 33, 33, 30, 28; 4132 x 2304 with 21 (a round), 26, 32, 39: 10.1, 11.3, 12.0, 10.9; 500 x 2304 with 2,
 // 4, 16: 5.6, 5.1, 5.5; 32768 x 4352 with runs of at most 64, 96, 128, 192: 95, 95, 93, 92.  Gradients, 8192 x 4352 with
-// 19, 27, 36, 77: 79, 69, 64, 60; 500 x 2304 with 4, 8, 16: 11.8, 9.3, 8.8; 100 x 384: 6.4, 6.6, 7.4.
+// 19, 27, 36: 79, 69, 64, with 58, 72, 86 (two rounds), 103, 128: 63, 61.5, 62, 61, 59; 500 x 2304 with 4, 8, 16: 11.8, 9.3,
+// 8.8; 100 x 384: 6.4, 6.6, 7.4.  Their places are whole blocks for each 32 vectors: with the fractions counted too,
+// 4132 x 2304 takes 23.2 for 19.8 (a second round), 32768 x 4352 197 for 200.
 int run_length(long total_T, long at_once, int least) {
     const long longest = 128, most = at_once > 0 ? at_once : 1, whole = (total_T + most - 1) / most;
     const long rounds = whole > longest ? (whole + longest - 1) / longest : 1, run = (total_T + most * rounds - 1) / (most * rounds);
