@@ -69,3 +69,24 @@ def test_a_parameter_that_is_no_number_reaches_its_heads_outputs_and_no_others(n
         assert torch.equal(a[:, 0], b[:, 0])
     for a, b in zip(sums, good[6:9]):
         assert torch.equal(a[0], b[0])
+
+
+@pytest.mark.parametrize("P,N,H,G", [(64, 128, 2, 1), (128, 64, 4, 2), (64, 64, 1, 1)])
+def test_gradients_of_B_and_C_are_rounded_once(P, N, H, G):
+    """Sequences of one token whose x and dout have one channel each: dC = sum over heads of E B with E = dt dout x, dB =
+    sum of E C, whose few roundings (the step's six, two products', one addition a head, three planes' sum, a cut of the
+    tensor cores counted twice: at most 32 of 2^-24) move a bf16 output only next to a border of two values."""
+    n = 300
+    gen = torch.Generator().manual_seed(P + N + H)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x, dout = torch.zeros(n, H, P), torch.zeros(n, H, P)
+    x[:, :, 5], dout[:, :, 5] = r(n, H).abs() + 0.5, r(n, H).abs() + 0.5  # no cancellation between heads
+    x, dout, B, C, a, A_log = x.to(BF), dout.to(BF), r(n, G, N).to(BF), r(n, G, N).to(BF), r(n, H), r(H)
+    grads = gdn.gdn_ssm_chunk_bwd(*(dev(t) for t in (dout, x, B, C, a, A_log)), num_seqs=n)
+    dt = torch.log1p(a.double().exp())
+    E = (dt * dout[:, :, 5].double() * x[:, :, 5].double()).unflatten(1, (G, H // G)).sum(-1)[..., None]
+    for got, ref in ((grads[1], E * C.double()), (grads[2], E * B.double())):
+        # half the distance of two bf16 values at ref
+        half = torch.exp2(torch.floor(torch.log2(ref.abs())) - 8)
+        over = (got.cpu().double() - ref).abs() - half
+        assert (over / ref.abs()).max().item() <= 32 * 2.0 ** -24
