@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_kernel(SsmArgs a, Work w) {
 
 // What is left, in one launch of three kinds of blocks: the sums over the slots of dA_log, ddt_bias and dD, 32 heads a
 // block; the subsets' dB and dC added up in order, eight elements a thread; zeros for the tokens outside every sequence.
-constexpr int kZeroBlocks = 152;
+constexpr int kZeroBlocks = kSMs;
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_finish_kernel(SsmArgs a, Work w, long slots, int sum_blocks, int part_blocks) {
     dependency_wait();
@@ -408,8 +408,8 @@ cudaError_t grad_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
 // heads in two groups: 36 us for 59; one against two, 23 tokens of 15 in three: 36 for 68.
 int subsets_of(int num_seqs, int total_T, int H, int G) {
     const long blocks = slots_of(num_seqs, total_T) * G, per = H / G;
-    long n = (2 * 152 + blocks - 1) / blocks;
-    const long most = per == 1 || blocks * per <= 152 ? per : per / 2;
+    long n = (2 * kSMs + blocks - 1) / blocks;
+    const long most = per == 1 || blocks * per <= kSMs ? per : per / 2;
     n = n > most ? most : n;
     return (int)(n < 1 ? 1 : n);
 }

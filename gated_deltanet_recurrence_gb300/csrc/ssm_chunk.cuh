@@ -11,6 +11,7 @@
 namespace gdn {
 namespace ssm {
 
+constexpr int kSMs = 152;
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kGateRows = 5;    // dt, G hi, G lo, b, r
 constexpr float kMinLog = -128.f;  // a log decay below it is a decay to zero
@@ -44,15 +45,16 @@ __device__ __forceinline__ Two two_shfl(Two a, int mask) {
 struct Chunk {
     int n, k, bos, eos, t0, len;  // sequence, chunk of it, its tokens, the chunk's first token, tokens in it
 };
-// The chunk of a slot; false where the slot holds none.  The whole block takes part.
+// The chunk (of TOKENS) of a slot; false where the slot holds none.  The whole block takes part.
+template <int TOKENS = kC>
 __device__ __forceinline__ bool find_chunk(const Packed& s, int slot, int* err, Chunk& c) {
-    c.n = packed_find(s, slot, kC, 1, err);
+    c.n = packed_find(s, slot, TOKENS, 1, err);
     if (c.n < 0 || c.n >= s.num_seqs) return false;
     c.bos = s.bos(c.n);
     c.eos = s.bos(c.n + 1);
-    c.k = slot - (c.bos / kC + c.n);
-    c.t0 = c.bos + c.k * kC;
-    c.len = min(c.eos - c.t0, kC);
+    c.k = slot - (c.bos / TOKENS + c.n);
+    c.t0 = c.bos + c.k * TOKENS;
+    c.len = min(c.eos - c.t0, TOKENS);
     return c.len > 0;
 }
 inline long slots_of(int num_seqs, int total_T) { return (long)total_T / kC + num_seqs; }

@@ -328,7 +328,7 @@ cudaError_t out_one(const SsmArgs& a, const Work& w, cudaStream_t s) {
     // shares for two rounds of blocks: each brings B and C again (for one, two, three rounds: 2048 tokens of 16 heads 80,
     // 70, 78 us; 6144 of 24 in three sequences 251, 224, 232)
     const long slots = slots_of(a.seqs.num_seqs, a.seqs.total_T), blocks = slots * a.G, units = (long)(a.H / a.G) * (a.P / 64);
-    const long fill = (2 * 152 + blocks - 1) / blocks, shares = fill < units ? fill : units;
+    const long fill = (2 * kSMs + blocks - 1) / blocks, shares = fill < units ? fill : units;
     return launch_after(ssm_out_kernel<N>, dim3((unsigned)slots, (unsigned)(a.G * shares)), kOutThreads, kOutSmem<N>, s, a, w, (int)shares);
 }
 
@@ -357,7 +357,7 @@ cudaError_t launch_scan(const SsmArgs& a, const Work& w, int directions, cudaStr
     return scan(false);
 }
 
-// Chunks of a segment, or 0.  Blocks are counted against 152 SMs.  Few rows: as many segments as fill the SMs, where that
+// Chunks of a segment, or 0.  Blocks are counted against the SMs.  Few rows: as many segments as fill the SMs, where that
 // pays for sequences of one length, or, where the lengths may differ, for the longest of n, taken as 1 + 1/2 + ... + 1/n
 // times the average.  A packed batch of up to two rounds of blocks, forwards: segments a little longer than the average,
 // where they pay for that longest one. In us, whole and in segments, bf16, d_state 128, 64 rows a head: 1536 tokens of 8
@@ -369,11 +369,11 @@ static int segment_chunks(int num_seqs, int total_T, int H, int P, int unit, int
     const long rows = (long)H * (P / 64) * directions * num_seqs, chunks = ((long)total_T + unit - 1) / unit,
                avg = (chunks + num_seqs - 1) / num_seqs;
     const auto split = [&](long each) { return each * (cost.whole + cost.own) + cost.more; };
-    if (rows > 304 || total_T > 1 << 29) return 0;  // a segment's tokens are an int
+    if (rows > 2 * kSMs || total_T > 1 << 29) return 0;  // a segment's tokens are an int
     double longest = (double)avg;
     for (int n = 2; varied && n <= num_seqs; ++n) longest += (double)avg / n;
-    if (rows <= 152) {
-        const long count = 152 / rows, fill = (avg + count - 1) / count, each = fill < 4 ? 4 : fill;
+    if (rows <= kSMs) {
+        const long count = kSMs / rows, fill = (avg + count - 1) / count, each = fill < 4 ? 4 : fill;
         if (longest * cost.whole > split(each)) return (int)each;
     }
     if (directions > 1 || !varied) return 0;

@@ -140,18 +140,6 @@ __device__ __forceinline__ void lane_gates(const float (&z)[4], int left, float 
 enum Row { rPh, rPl, rFromRun, rToRun, rDt, rToEnd, rFromStart, kRows };
 constexpr int kGates = kRows * kT + 8;
 
-// The chunk of a slot; false where the slot holds none.  The whole block takes part.
-__device__ __forceinline__ bool find_chunk128(const Packed& s, int slot, int* err, Chunk& c) {
-    c.n = packed_find(s, slot, kT, 1, err);
-    if (c.n < 0 || c.n >= s.num_seqs) return false;
-    c.bos = s.bos(c.n);
-    c.eos = s.bos(c.n + 1);
-    c.k = slot - (c.bos / kT + c.n);
-    c.t0 = c.bos + c.k * kT;
-    c.len = min(c.eos - c.t0, kT);
-    return c.len > 0;
-}
-
 // ---- host ------------------------------------------------------------------------------------------
 
 inline long slots128(int num_seqs, int total_T) { return (long)total_T / kT + num_seqs; }

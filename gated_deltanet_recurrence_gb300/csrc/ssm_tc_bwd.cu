@@ -78,7 +78,7 @@ ssm_grad_tc_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant
     const int g = blockIdx.y % a.G, subset = blockIdx.y / a.G, per = a.H / a.G;
     const int h0 = g * per + per * subset / w.subsets, h1 = g * per + per * (subset + 1) / w.subsets;
     Chunk c;
-    if (!find_chunk128(a.seqs, blockIdx.x, a.err, c)) {
+    if (!find_chunk<kT>(a.seqs, blockIdx.x, a.err, c)) {
         const long all = (long)gridDim.x * a.H;
         for (int i = tid; i < h1 - h0; i += kGradThreads) {
             const long at = (long)blockIdx.x * a.H + h0 + i;
@@ -660,7 +660,7 @@ int subsets_of(int num_seqs, int total_T, int H, int G, int N) {
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= per && s <= 16; ++s) {
-        const double rounds = (double)((blocks * s + 151) / 152), heads = (double)((per + s - 1) / s) + 0.7;
+        const double rounds = (double)((blocks * s + kSMs - 1) / kSMs), heads = (double)((per + s - 1) / s) + 0.7;
         const double parts = s > 1 ? 0.8 + (2.0 * s + 1) * 2 * total_T * G * N * 4 / 5e12 / 5e-6 : 0.0;
         if (rounds * heads + parts < least) {
             least = rounds * heads + parts;

@@ -21,7 +21,7 @@ constexpr int kGateWarps = 8;
 __global__ void __launch_bounds__(kGateWarps * 32) ssm_gates128_kernel(SsmArgs a, float* gates) {
     dependency_start();
     Chunk c;
-    if (!find_chunk128(a.seqs, blockIdx.x, a.err, c)) return;
+    if (!find_chunk<kT>(a.seqs, blockIdx.x, a.err, c)) return;
     const int lane = threadIdx.x & 31, h = blockIdx.y * kGateWarps + (threadIdx.x >> 5);
     if (h >= a.H) return;
     const float rate = expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f;
