@@ -8,9 +8,9 @@
 // backwards, then dw = sum dm n, dn = dm w, dx = r (dn - n mean(dn n)) (or the sum's, for length one).
 //
 // Memory would bound it; 8192 tokens of 16 + 4 heads of 128 (bf16) take 16.4 us, 5.2 TB/s (77% of a copy's rate),
-// gradients of 3001 tokens of 16 + 16 heads of 64 8.7 us with the launch behind.  What is left are instructions (58% of the
-// issue slots before arithmetic went in pairs of channels, 17.5 us).  Two blocks an SM with all values in registers; three,
-// with spills, 17.8 for 17.0 on another machine.
+// gradients of 3001 tokens of 16 + 16 heads of 64 8.9 us with the launch behind.  What is left are instructions (43% of the
+// issue slots; 58% and 17.5 us before arithmetic went in pairs of channels) and, at two blocks an SM, their latency.  Two
+// blocks with all values in registers; three, with spills, 17.8 for 17.0 on another machine.
 //
 // Rows come through rings of asynchronous copies, as in short_conv.cu.  A row (one head of one
 // token) is d / 8 lanes of 8 channels; a set of lanes takes one token and several heads, so that the token's cosines and

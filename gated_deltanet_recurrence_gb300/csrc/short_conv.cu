@@ -8,10 +8,9 @@
 // Every input is read once and every output written once but for the three rows in front of (and, for gradients, behind)
 // the run of tokens that a thread walks along with the window of four inputs in registers.  Arithmetic and sums are fp32;
 // an output is rounded once, at its store. Memory would bound all three calls; what does is the issue of instructions
-// (with runs of 32 tokens 64% and 61% of the slots, at the three blocks an SM that the registers leave room for) and
-// the start and end of a run.  So a thread asks for its
-// rows by asynchronous copies into a ring of its own in shared memory, four groups of four rows ahead, which takes
-// neither registers nor waits, has few channels (four forward, two backward: eight and four were slower, for their
+// (65% and 53% of the slots, at the three blocks an SM that the registers leave room for) and the start and end of a run.
+// So a thread asks for its rows by asynchronous copies into a ring of its own in shared memory, four groups of four rows
+// ahead, which takes neither registers nor waits, has few channels (four forward, two backward: eight and four were slower, for their
 // registers), and takes its sigmoid from the hardware's exponential and reciprocal.  Gradients' arithmetic goes in pairs
 // of channels (8192 x 4352: 69 -> 66 us; forward that spilled, 33 -> 36 us).  Measured, bf16: 8192 tokens of 4352
 // channels 27.5 us, 5.2 TB/s (77% of a copy's rate; 32768 tokens 93 us, 6.1 TB/s); gradients of 4132 tokens of 2304

@@ -9,8 +9,8 @@
 // with those (2100), dx and dC (2500); the tensor pipe is busy 13% of it.  All of a chunk is on the way through
 // registers, whose 64,000 the accumulators of dB, dC and E fill, so that steps do not overlap.  Tried, and no faster: 256
 // threads, rolled loops for the masks (260 us for 255 of the call below), tiles of both states at once with their
-// conversion beside the products (254). Two sequences of 4096 tokens, 32 heads of 64 in two groups, d_state 128: 170 us
-// of the call's 235 (with states 54, gates 4, sums 4; kernels on mma.sync took 735).
+// conversion beside the products (254). Two sequences of 4096 tokens, 32 heads of 64 in two groups, d_state 128: 171 us
+// of the call's 236 (with states 54, gates 4, sums 4; kernels on mma.sync took 735).
 //
 // Every fp32 factor is three bf16 planes, exact beside the bf16 inputs; where a factor's planes lie side by side, the
 // input is read once for all of them.  All matrices of pairs of tokens are held with row j (the earlier token) and

@@ -405,7 +405,7 @@ size_t gdn_short_conv_bwd_workspace_size(int num_seqs, int total_T, int dim);
  *   d_head, d_state  each 64 or 128 (GDN_ERR_UNSUPPORTED otherwise); H at most 16384.
  *   workspace  gdn_ssm_chunk_fwd_workspace_size(...) bytes, 256-byte aligned; may be NULL when that is 0.
  * A NaN or an infinity in a token's inputs reaches the outputs of its chunk (up to 128 tokens of its sequence) and of
- * every later token, and no other sequence.
+ * every later token, and no other sequence; one in a head's parameters reaches the whole head.
  */
 int gdn_ssm_chunk_fwd(const void* x, long x_stride, const void* B, long B_stride, const void* C, long C_stride,
                       const float* a, const float* A_log, const float* dt_bias, const float* D,
